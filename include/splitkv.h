@@ -120,7 +120,8 @@ int skv_scratch_info(const skv_handle *h, size_t *workspace_bytes, size_t *ring_
  * status word.  SKV_ETIMEOUT: a bounded device-side wait (tensor-core
  * pipeline barriers) gave up; the affected outputs are not valid.  SKV_EDEVICE:
  * another bit is set (bit 1 = an append named a position outside its cache;
- * that row was not written).  The word is stored in *dev_code when dev_code
+ * that row was not written; bit 2 = a call over 8-bit pages met a page id
+ * outside the pool or a length beyond its list).  The word is stored in *dev_code when dev_code
  * is not NULL. */
 int skv_status(skv_handle *h, int32_t *dev_code);
 
@@ -443,6 +444,104 @@ int skv_bcache_ring_attn(skv_bcache *c, const skv_shape *shape, const void *q, i
 /* Device pointers of the page pool and of the last resolve's page ids. */
 int skv_bcache_pool(const skv_bcache *c, const void **k_pages, const void **v_pages, int64_t *n_pool_pages,
                     const int32_t **last_page_ids);
+
+/* ---- the 8-bit page cache ---------------------------------------------------
+ *
+ * K and V in 8 bits with one scale for each block of tokens and KV head.  A
+ * page holds SKV_Q8_PAGE consecutive tokens of ONE KV head: int8 codes
+ * [SKV_Q8_PAGE][D] and one fp32 scale for K, the same for V (value = scale *
+ * code, codes in [-127, 127]), and for every channel the smallest and the
+ * largest K code over the tokens held, from which skv_q8_select bounds a
+ * page's scores.  A pool is an array of such pages; the caller owns its
+ * tensors.
+ *
+ * Lists.  page_ids int32 [S][Hk][pages_per_list] (device): key j of sequence
+ * s, KV head k is token j % SKV_Q8_PAGE of page page_ids[(s*Hk + k) *
+ * pages_per_list + j / SKV_Q8_PAGE].  kv_len int32 [S] (device): keys held
+ * (all heads of a sequence hold the same number).  A negative page id is
+ * absent: nothing is read and its keys do not exist.  A page id outside the
+ * pool reads as absent and sets bit 2 of the device status word; a kv_len
+ * beyond the list is cut to it and sets the same bit; a negative one is 0.  Entries
+ * behind a sequence's last token are not read by attention and selection.
+ * One page may stand in several lists as long as no append writes it.
+ * A token the page does not hold yet may keep any bytes.
+ *
+ * The calls below take their sizes from skv_shape (S, nq, H, Hk, D, scale);
+ * its k_type, v_type and row strides are not looked at.  D is 64 or 128.  They
+ * run on the handle's device, whichever device is current. */
+#define SKV_Q8_PAGE 64
+#define SKV_F32 3            /* element type of o and of rows to append        */
+
+typedef struct skv_q8_pool {
+    int64_t n_pages;
+    int32_t D;
+    int8_t *k;               /* [n_pages][SKV_Q8_PAGE][D], 16-byte aligned      */
+    int8_t *v;
+    float *k_scale;          /* [n_pages]                                       */
+    float *v_scale;
+    int8_t *k_min;           /* [n_pages][D], 16-byte aligned                   */
+    int8_t *k_max;
+} skv_q8_pool;
+
+/* Write the tokens kv_len[s] .. kv_len[s] + n - 1 of every sequence (n =
+ * n_new[s] when n_new is given, at most n_max; negative counts as 0).  k_new,
+ * v_new: x_type (SKV_F32 or SKV_F16) [S][n_max][Hk][D], 16-byte aligned; kv_len
+ * itself is left to the caller.  For each page touched
+ *   d' = max(d, fp32(amax / 127)), amax = largest finite magnitude written,
+ * d = its present scale when it holds earlier tokens (below kv_len[s]), else 0;
+ * earlier codes c become the integer nearest c*d/d' when d' > d, new codes are
+ * the integer nearest x/d' within [-127, 127] (ties to even, decided by the
+ * exact quotient; d' = 0 gives codes 0; NaN gives 0, an infinity +-127), and the
+ * smallest and largest K codes follow.  Nothing else of the page changes, so
+ * writing the same tokens again gives the same bytes.  A token whose page is
+ * absent or outside the list or the pool is not written and sets bit 1 of the device
+ * status word.  Two lists of one call must not write one page. */
+int skv_q8_append(skv_handle *h, const skv_q8_pool *pool, int32_t S, int32_t Hk, int32_t n_max, int32_t x_type,
+                  const void *k_new, const void *v_new, const int32_t *page_ids, int64_t pages_per_list,
+                  const int32_t *kv_len, const int32_t *n_new, void *stream);
+
+/* Attention of q (fp16 [S][nq][H][D]) over the lists.  q_pos int32 [S][nq] or
+ * NULL: token t sees key j iff j <= q_pos[s][t] (and j < kv_len[s]).  sel NULL:
+ * every page of the list.  sel int32 [S][nq][Hk][n_sel]: only the pages with
+ * these indices in the list, chosen for each query and KV head (entries below
+ * 0 or behind the last token are skipped; an index given twice counts twice).
+ * mass NULL, or fp32 [S][Hk][pages_per_list]: for every page that is read, the
+ * attention probabilities of its keys, summed over the tokens and the query
+ * heads of the KV head, are added to it (in an order that does not change from
+ * run to run).  o: o_type [S][nq][H][D] (SKV_F32 or SKV_F16), lse fp32
+ * [S][nq][H]; a row that sees no key gets o = 0, lse = -inf.  fp32 results are
+ * good to about 1e-6 (probabilities enter the value product in two fp16
+ * parts) and can be merged with those of other partitions
+ * (skv_attn_combine). */
+int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,
+                const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
+                const int32_t *sel, int32_t n_sel, float *mass, int32_t o_type, void *o, float *lse, void *stream);
+
+/* Pick n_sel pages for every query and KV head: sel int32 [S][nq][Hk][n_sel]
+ * receives list indices in ascending order, padded with -1.  Candidates are
+ * the pages that hold a key the token sees and are present.  Those among the
+ * list's first n_first pages and among the last n_last that hold a visible key
+ * are always picked; the others by the largest bound, ties to the lowest index:
+ *   bound = k_scale * max over the KV head's query heads of
+ *           fp32(dq * sum_d max(cq_d * k_min_d, cq_d * k_max_d)),
+ * dq = fp32(max|q| / 127) and cq_d the integer nearest q_d / dq, both
+ * products rounded to fp32: an upper bound of the coded query's scores over
+ * the page.  n_first + n_last <= n_sel. */
+int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,
+                  const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
+                  int32_t n_sel, int32_t n_first, int32_t n_last, int32_t *sel, void *stream);
+
+/* Cut every list to n_keep pages: the first n_first, the last n_last (>= 1, so
+ * that a partly filled page stays the last one), and the others of largest
+ * mass (ties to the lowest index; absent pages go first; a NaN counts as
+ * +inf).  A list of at most n_keep pages stays as it is.  The kept pages move
+ * together in their order, entries behind the last token follow them, the
+ * rest is -1; mass_out moves alike, 0 elsewhere; kv_len_out = kv_len less the
+ * tokens of the pages taken out; freed_out [S][Hk][pages_per_list]: the page
+ * ids taken out, in list order, then -1.  Outputs must not overlap inputs. */
+int skv_q8_evict(skv_handle *h, int32_t S, int32_t Hk, int64_t pages_per_list, const int32_t *page_ids,
+                 const float *mass, const int32_t *kv_len, int32_t n_keep, int32_t n_first, int32_t n_last,
+                 int32_t *page_ids_out, float *mass_out, int32_t *kv_len_out, int32_t *freed_out, void *stream);
 
 #ifdef __cplusplus
 }

@@ -11,6 +11,13 @@ streams.
     o, lse = attn_window_tail(h, q, k_win, v_win, k_tail, v_tail, Hk=8, ...)
     o, lse = attn_combine(h, o_parts, lse_parts)
     x = kv_dequant_q8_0(h, blocks, n_values)
+
+    pool = Q8Pool.empty(n_pages, D=128)                          # 8-bit pages of 64 tokens of one KV head
+    q8_append(h, pool, k_new, v_new, page_ids, kv_len)           # write tokens (kv_len is the caller's to advance)
+    o, lse = q8_attn(h, pool, q, page_ids, kv_len, mass=mass)    # attend; mass += each page's attention weight
+    sel = q8_select(h, pool, q, page_ids, kv_len, n_sel=64)      # the pages of the largest score bounds ...
+    o, lse = q8_attn(h, pool, q, page_ids, kv_len, sel=sel)      # ... and attention over those alone
+    page_ids, mass, kv_len, freed = q8_evict(h, page_ids, mass, kv_len, n_keep=512)
 """
 from __future__ import annotations
 
@@ -18,11 +25,11 @@ import ctypes
 import math
 
 from . import _lib
-from ._lib import F16, Q4_0, Q8_0, SkvShape
+from ._lib import F16, F32, Q4_0, Q8_0, Q8_PAGE, SkvQ8Pool, SkvShape
 
 __all__ = ["Handle", "SplitKVError", "F16", "Q8_0", "Q4_0", "attn_partial", "attn_combine", "attn_window_tail",
            "attn_paged", "BlockCache", "kv_dequant_q8_0", "kv_dequant_q4_0", "gather_rows", "kv_append", "plan_splits", "plan_prefill_splits",
-           "segment_bytes"]
+           "segment_bytes", "Q8_PAGE", "Q8Pool", "q8_append", "q8_attn", "q8_select", "q8_evict"]
 
 
 class SplitKVError(RuntimeError):
@@ -365,3 +372,150 @@ def kv_append(h: Handle, x, positions, dst0, dst1=None, *, type_=F16, n_rows0=No
         n_rows1 = 0 if dst1 is None else dst1.numel() * dst1.element_size() // row_bytes
     h.check(_lib.lib().skv_kv_append(h.ptr, int(type_), Hk, D, int(row_bytes), _ptr(x), _ptr(positions), n,
                                      _ptr(dst0), int(n_rows0), _ptr(dst1), int(n_rows1), _stream(stream)))
+
+
+class Q8Pool:
+    """8-bit pages (see include/splitkv.h): k, v int8 [n_pages][64][D], k_scale,
+    v_scale fp32 [n_pages], k_min, k_max int8 [n_pages][D].  The tensors stay
+    the caller's; the pool keeps references to them."""
+
+    def __init__(self, k, v, k_scale, v_scale, k_min, k_max):
+        torch = _torch()
+        n, rows, D = (int(x) for x in k.shape)
+        want = [("k", k, torch.int8, (n, Q8_PAGE, D)), ("v", v, torch.int8, (n, Q8_PAGE, D)),
+                ("k_scale", k_scale, torch.float32, (n,)), ("v_scale", v_scale, torch.float32, (n,)),
+                ("k_min", k_min, torch.int8, (n, D)), ("k_max", k_max, torch.int8, (n, D))]
+        for name, x, dtype, shape in want:
+            _need(name, x, dtype, shape, k.device)
+        self.n_pages, self.D, self.device = n, D, k.device
+        self.k, self.v, self.k_scale, self.v_scale, self.k_min, self.k_max = k, v, k_scale, v_scale, k_min, k_max
+        self._c = SkvQ8Pool(n, D, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                            k_min.data_ptr(), k_max.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages, D, device="cuda"):
+        """A pool of unwritten pages (appends need nothing cleared)."""
+        torch = _torch()
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+        n, D = int(n_pages), int(D)
+        return cls(new((n, Q8_PAGE, D), torch.int8), new((n, Q8_PAGE, D), torch.int8), new((n,), torch.float32),
+                   new((n,), torch.float32), new((n, D), torch.int8), new((n, D), torch.int8))
+
+
+def _need(name, x, dtype, shape, device):
+    """Raise SKV_EINVAL unless x is a contiguous tensor of this type, shape and device."""
+    if x.dtype != dtype or tuple(x.shape) != shape or x.device != device or not x.is_contiguous():
+        raise SplitKVError(1, f"{name}: want contiguous {dtype} {list(shape)} on {device}, got "
+                              f"{'' if x.is_contiguous() else 'non-contiguous '}{x.dtype} {list(x.shape)} on {x.device}")
+
+
+def _q8_stream(h, stream, device):
+    """The raw stream of a call over 8-bit pages (default: the pool's device's current one)."""
+    if device.type != "cuda" or device.index != h.device:
+        raise SplitKVError(1, f"tensors on {device}, handle on cuda:{h.device}")
+    if stream is None:
+        return _torch().cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def _q8_lists(page_ids, kv_len, device):
+    torch = _torch()
+    if page_ids.dim() != 3:
+        raise SplitKVError(1, f"page_ids: want int32 [S, Hk, pages_per_list], got {list(page_ids.shape)}")
+    S, Hk, cap = page_ids.shape
+    _need("page_ids", page_ids, torch.int32, (S, Hk, cap), device)
+    _need("kv_len", kv_len, torch.int32, (S,), device)
+    return S, Hk, cap
+
+
+def _q8_query(pool, q, page_ids, kv_len, q_pos, scale):
+    torch = _torch()
+    S, Hk, cap = _q8_lists(page_ids, kv_len, pool.device)
+    if q.dim() != 4:
+        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(q.shape)}")
+    nq, H = q.shape[1], q.shape[2]
+    _need("q", q, torch.float16, (S, nq, H, pool.D), pool.device)
+    if q_pos is not None:
+        _need("q_pos", q_pos, torch.int32, (S, nq), pool.device)
+    sc = 1.0 / math.sqrt(pool.D) if scale is None else float(scale)
+    return SkvShape(S, nq, H, Hk, pool.D, sc, 0, 0, 0, 0), S, nq, H, Hk, cap
+
+
+def q8_append(h: Handle, pool: Q8Pool, k_new, v_new, page_ids, kv_len, *, n_new=None, stream=None):
+    """skv_q8_append: write k_new, v_new (fp32 or fp16 [S, n, Hk, D]) as tokens
+    kv_len[s] .. of each sequence; n_new int32 [S]: how many of the n rows."""
+    torch = _torch()
+    S, Hk, cap = _q8_lists(page_ids, kv_len, pool.device)
+    st = _q8_stream(h, stream, pool.device)
+    if k_new.dim() != 4 or k_new.dtype not in (torch.float32, torch.float16):
+        raise SplitKVError(1, f"k_new: want fp32 or fp16 [S, n, Hk, D], got {k_new.dtype} {list(k_new.shape)}")
+    n = k_new.shape[1]
+    _need("k_new", k_new, k_new.dtype, (S, n, Hk, pool.D), pool.device)
+    _need("v_new", v_new, k_new.dtype, (S, n, Hk, pool.D), pool.device)
+    if n_new is not None:
+        _need("n_new", n_new, torch.int32, (S,), pool.device)
+    h.check(_lib.lib().skv_q8_append(h.ptr, pool._ref, S, Hk, n, F32 if k_new.dtype == torch.float32 else F16,
+                                     k_new.data_ptr(), v_new.data_ptr(), page_ids.data_ptr(), cap,
+                                     kv_len.data_ptr(), _ptr(n_new), st))
+
+
+def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=None, sel=None, mass=None,
+            o_dtype=None, o=None, lse=None, stream=None):
+    """skv_q8_attn: attention of q over the lists (sel: over those pages of
+    them); mass fp32 [S, Hk, pages_per_list] is added to.  o is fp32 unless
+    o_dtype (or a given o) is torch.float16."""
+    torch = _torch()
+    sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, scale)
+    st = _q8_stream(h, stream, pool.device)
+    if o is None:
+        o = torch.empty(q.shape, dtype=torch.float32 if o_dtype is None else o_dtype, device=q.device)
+    if o.dtype not in (torch.float32, torch.float16) or (o_dtype is not None and o.dtype != o_dtype):
+        raise SplitKVError(1, f"o: fp32 or fp16 is wanted, got {o.dtype} (o_dtype {o_dtype})")
+    _need("o", o, o.dtype, tuple(q.shape), pool.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _need("lse", lse, torch.float32, (S, nq, H), pool.device)
+    n_sel = 0
+    if sel is not None:
+        n_sel = sel.shape[-1]
+        _need("sel", sel, torch.int32, (S, nq, Hk, n_sel), pool.device)
+    if mass is not None:
+        _need("mass", mass, torch.float32, (S, Hk, cap), pool.device)
+    h.check(_lib.lib().skv_q8_attn(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
+                                   kv_len.data_ptr(), _ptr(q_pos), _ptr(sel), n_sel, _ptr(mass),
+                                   F32 if o.dtype == torch.float32 else F16, o.data_ptr(), lse.data_ptr(), st))
+    return o, lse
+
+
+def q8_select(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, n_sel, n_first=1, n_last=1, q_pos=None, sel=None,
+              stream=None):
+    """skv_q8_select: the n_sel list indices int32 [S, nq, Hk, n_sel] (ascending,
+    -1 padded) of the pages with the largest score bounds for each query and
+    KV head, the first n_first and last n_last among them."""
+    torch = _torch()
+    sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, None)
+    st = _q8_stream(h, stream, pool.device)
+    if sel is None:
+        sel = torch.empty((S, nq, Hk, max(0, int(n_sel))), dtype=torch.int32, device=q.device)
+    _need("sel", sel, torch.int32, (S, nq, Hk, int(n_sel)), pool.device)
+    h.check(_lib.lib().skv_q8_select(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
+                                     kv_len.data_ptr(), _ptr(q_pos), int(n_sel), int(n_first), int(n_last),
+                                     sel.data_ptr(), st))
+    return sel
+
+
+def q8_evict(h: Handle, page_ids, mass, kv_len, *, n_keep, n_first=1, n_last=1, stream=None):
+    """skv_q8_evict: lists cut to n_keep pages (the first n_first, the last
+    n_last, the others of largest mass): (page_ids, mass, kv_len, freed)."""
+    torch = _torch()
+    S, Hk, cap = _q8_lists(page_ids, kv_len, page_ids.device)
+    st = _q8_stream(h, stream, page_ids.device)
+    _need("mass", mass, torch.float32, (S, Hk, cap), page_ids.device)
+    ids_out, freed = torch.empty_like(page_ids), torch.empty_like(page_ids)
+    mass_out, len_out = torch.empty_like(mass), torch.empty_like(kv_len)
+    h.check(_lib.lib().skv_q8_evict(h.ptr, S, Hk, cap, page_ids.data_ptr(), mass.data_ptr(), kv_len.data_ptr(),
+                                    int(n_keep), int(n_first), int(n_last), ids_out.data_ptr(), mass_out.data_ptr(),
+                                    len_out.data_ptr(), freed.data_ptr(), st))
+    return ids_out, mass_out, len_out, freed

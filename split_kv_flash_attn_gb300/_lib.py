@@ -15,7 +15,8 @@ LIB_PATH = os.path.join(PKG, "libsplitkv.so")
 SKV_OK = 0
 STATUS = {0: "SKV_OK", 1: "SKV_EINVAL", 2: "SKV_EUNSUPPORTED", 3: "SKV_ENOTPINNED", 4: "SKV_ENOMEM",
           5: "SKV_ECAPTURE", 6: "SKV_ECUDA", 7: "SKV_ETIMEOUT", 8: "SKV_EDEVICE"}
-F16, Q8_0, Q4_0 = 0, 1, 2
+F16, Q8_0, Q4_0, F32 = 0, 1, 2, 3
+Q8_PAGE = 64
 
 # Every entry point that include/splitkv.h declares.
 EXPORTS = [
@@ -26,6 +27,7 @@ EXPORTS = [
     "skv_bcache_append", "skv_bcache_attn", "skv_bcache_stats", "skv_bcache_check", "skv_bcache_pool",
     "skv_bcache_create_ring", "skv_bcache_ring_restore", "skv_bcache_ring_attn",
     "skv_attn_partial_static", "skv_plan_window", "skv_plan_tail_tile", "skv_selftest_wait_timeout",
+    "skv_q8_append", "skv_q8_attn", "skv_q8_select", "skv_q8_evict",
 ]
 
 
@@ -41,9 +43,16 @@ class SkvShape(ctypes.Structure):
                 ("v_type", ctypes.c_int32), ("k_row_bytes", ctypes.c_int64), ("v_row_bytes", ctypes.c_int64)]
 
 
+class SkvQ8Pool(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int64), ("D", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("k_min", ctypes.c_void_p),
+                ("k_max", ctypes.c_void_p)]
+
+
 def _declare(lib):
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     SH = ctypes.POINTER(SkvShape)
+    QP = ctypes.POINTER(SkvQ8Pool)
     sig = {
         "skv_create": ([ctypes.c_int, ctypes.POINTER(P)], ctypes.c_int),
         "skv_destroy": ([P], ctypes.c_int),
@@ -81,6 +90,10 @@ def _declare(lib):
         "skv_bcache_attn": ([P, SH, P, P, I32, P, P, P], ctypes.c_int),
         "skv_bcache_stats": ([P, ctypes.POINTER(SkvBcacheCounters)], ctypes.c_int),
         "skv_bcache_check": ([P, ctypes.POINTER(I32)], ctypes.c_int),
+        "skv_q8_append": ([P, QP, I32, I32, I32, I32, P, P, P, I64, P, P, P], ctypes.c_int),
+        "skv_q8_attn": ([P, QP, SH, P, P, I64, P, P, P, I32, P, I32, P, P, P], ctypes.c_int),
+        "skv_q8_select": ([P, QP, SH, P, P, I64, P, P, I32, I32, I32, P, P], ctypes.c_int),
+        "skv_q8_evict": ([P, I32, I32, I64, P, P, P, I32, I32, I32, P, P, P, P, P], ctypes.c_int),
         "skv_bcache_pool": ([P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(I64), ctypes.POINTER(P)],
                             ctypes.c_int),
     }

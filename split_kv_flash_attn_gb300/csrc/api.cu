@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <new>
 
 #include "internal.h"
 
@@ -39,15 +40,26 @@ static size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 
 int ensure_workspace(skv_handle *h, size_t bytes, cudaStream_t stream)
 {
-    if (bytes <= h->ws_cap) return SKV_OK;
+    if (bytes <= h->ws_cap) {
+        if (!h->ws_in_graph && capturing(stream)) h->ws_in_graph = true;
+        return SKV_OK;
+    }
     if (capturing(stream))
         return fail(h, SKV_ECAPTURE, "workspace must grow to %zu bytes during graph capture; call skv_reserve first",
                     bytes);
     const size_t cap = round_up(bytes, size_t(1) << 20);
     if (h->workspace) {
-        cudaError_t e = cudaFree(h->workspace);   // waits for work still using it
+        cudaError_t e = cudaSuccess;
+        if (h->ws_in_graph) {                     // a graph's replays go on using it
+            auto *r = new (std::nothrow) skv_handle::Retired{h->workspace, h->ws_retired};
+            if (!r) return fail(h, SKV_ENOMEM, "out of host memory");
+            h->ws_retired = r;
+        } else {
+            e = cudaFree(h->workspace);           // waits for work still using it
+        }
         h->workspace = nullptr;
         h->ws_cap = 0;
+        h->ws_in_graph = false;
         if (e != cudaSuccess) return cuda_fail(h, e, "cudaFree(workspace)");
     }
     cudaError_t e = cudaMalloc(&h->workspace, cap);
@@ -325,6 +337,12 @@ int skv_destroy(skv_handle *h)
     if (!h) return SKV_OK;
     if (h->copy_stream) cudaStreamSynchronize(h->copy_stream);
     cudaFree(h->workspace);
+    while (h->ws_retired) {
+        skv_handle::Retired *r = h->ws_retired;
+        h->ws_retired = r->next;
+        cudaFree(r->p);
+        delete r;
+    }
     cudaFree(h->counters);
     cudaFree(h->status);
     for (int s = 0; s < SKV_MAX_SLOTS; ++s) cudaFree(h->ring[s]);

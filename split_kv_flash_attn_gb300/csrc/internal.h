@@ -24,6 +24,11 @@ struct skv_handle {
     int *counters = nullptr;                           // per-unit arrival counters of the fused split merge
     void *workspace = nullptr;                         // partial outputs (grow-only)
     size_t ws_cap = 0;
+    bool ws_in_graph = false;                          // a captured graph may name the workspace
+    struct Retired {
+        void *p;
+        Retired *next;
+    } *ws_retired = nullptr;                           // outgrown workspaces that captured graphs may name
     void *ring[SKV_MAX_SLOTS] = {};                    // tail-tile slots: [K bytes | V bytes]
     size_t ring_cap = 0;                               // bytes per slot
     int n_ring = 0;

@@ -1,0 +1,219 @@
+// q8_api.cu -- host side of the calls over 8-bit pages: checks, scratch and the
+// choice of kernel.
+#include <algorithm>
+
+#include "q8.cuh"
+
+namespace skv {
+namespace q8 {
+
+// Makes the handle's device current for a call.
+struct OnDevice {
+    int prev = -1;
+    bool moved = false;
+    explicit OnDevice(int want)
+    {
+        if (cudaGetDevice(&prev) == cudaSuccess && prev != want) moved = cudaSetDevice(want) == cudaSuccess;
+    }
+    ~OnDevice()
+    {
+        if (moved) cudaSetDevice(prev);
+    }
+};
+
+static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+static int check_pool(skv_handle *h, const skv_q8_pool *p)
+{
+    if (!p) return fail(h, SKV_EINVAL, "pool is NULL");
+    if (p->D != 64 && p->D != 128) return fail(h, SKV_EUNSUPPORTED, "head dim %d (supported: 64, 128)", p->D);
+    if (p->n_pages < 1 || p->n_pages > INT32_MAX) return fail(h, SKV_EINVAL, "pool of %lld pages", (long long)p->n_pages);
+    if (!p->k || !p->v || !p->k_scale || !p->v_scale || !p->k_min || !p->k_max)
+        return fail(h, SKV_EINVAL, "a pool pointer is NULL");
+    if (misaligned(p->k, 16) || misaligned(p->v, 16) || misaligned(p->k_min, 16) || misaligned(p->k_max, 16) ||
+        misaligned(p->k_scale, 4) || misaligned(p->v_scale, 4))
+        return fail(h, SKV_EUNSUPPORTED, "pool codes must be 16-byte and scales 4-byte aligned");
+    return SKV_OK;
+}
+
+static int check_lists(skv_handle *h, int32_t S, int32_t Hk, const int32_t *ids, int64_t cap, const int32_t *kv_len)
+{
+    if (S < 1 || Hk < 1) return fail(h, SKV_EINVAL, "bad sizes S=%d Hk=%d", S, Hk);
+    if (S > 65535 || Hk > 65535) return fail(h, SKV_EUNSUPPORTED, "S and Hk are limited to 65535");
+    // lengths and list indices are int32
+    if (cap < 1 || cap > INT32_MAX / kPage) return fail(h, SKV_EINVAL, "pages_per_list = %lld", (long long)cap);
+    if (!ids || !kv_len) return fail(h, SKV_EINVAL, "page_ids or kv_len is NULL");
+    return SKV_OK;
+}
+
+static int check_query(skv_handle *h, const skv_q8_pool *pool, const skv_shape *sh, const void *q)
+{
+    if (!sh) return fail(h, SKV_EINVAL, "shape is NULL");
+    if (sh->nq < 1 || sh->H < 1 || sh->Hk < 1 || sh->S < 1 || sh->H % sh->Hk)
+        return fail(h, SKV_EINVAL, "bad shape S=%d nq=%d H=%d Hk=%d", sh->S, sh->nq, sh->H, sh->Hk);
+    if (sh->D != pool->D) return fail(h, SKV_EINVAL, "head dim %d over pages of head dim %d", sh->D, pool->D);
+    if (!q) return fail(h, SKV_EINVAL, "q is NULL");
+    if (misaligned(q, 16)) return fail(h, SKV_EUNSUPPORTED, "q must be 16-byte aligned");
+    if (static_cast<int64_t>(sh->S) * sh->nq > INT32_MAX || static_cast<int64_t>(sh->nq) * (sh->H / sh->Hk) > INT32_MAX)
+        return fail(h, SKV_EUNSUPPORTED, "S*nq or nq*H/Hk exceeds 2^31 - 1");
+    return SKV_OK;
+}
+
+static Lists lists_of(skv_handle *h, int64_t n_pages, int32_t S, int32_t Hk, const int32_t *ids, int64_t cap,
+                      const int32_t *kv_len)
+{
+    return Lists{ids, kv_len, cap, n_pages, S, Hk, h->status};
+}
+
+static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace q8
+}  // namespace skv
+
+using namespace skv;
+using namespace skv::q8;
+
+extern "C" {
+
+int skv_q8_append(skv_handle *h, const skv_q8_pool *pool, int32_t S, int32_t Hk, int32_t n_max, int32_t x_type,
+                  const void *k_new, const void *v_new, const int32_t *page_ids, int64_t pages_per_list,
+                  const int32_t *kv_len, const int32_t *n_new, void *stream)
+{
+    if (!h) return SKV_EINVAL;
+    h->err[0] = 0;
+    int rc = check_pool(h, pool);
+    if (rc || (rc = check_lists(h, S, Hk, page_ids, pages_per_list, kv_len))) return rc;
+    if (n_max < 0) return fail(h, SKV_EINVAL, "n_max = %d", n_max);
+    if (x_type != SKV_F32 && x_type != SKV_F16) return fail(h, SKV_EINVAL, "rows to append are SKV_F32 or SKV_F16");
+    if (n_max == 0) return SKV_OK;
+    if (!k_new || !v_new) return fail(h, SKV_EINVAL, "k_new or v_new is NULL");
+    if (misaligned(k_new, 16) || misaligned(v_new, 16))
+        return fail(h, SKV_EUNSUPPORTED, "k_new and v_new must be 16-byte aligned");
+    OnDevice on(h->device);
+    return launch_append(h, *pool, lists_of(h, pool->n_pages, S, Hk, page_ids, pages_per_list, kv_len), n_max, x_type,
+                         k_new, v_new, n_new, static_cast<cudaStream_t>(stream));
+}
+
+int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,
+                const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
+                const int32_t *sel, int32_t n_sel, float *mass, int32_t o_type, void *o, float *lse, void *stream)
+{
+    if (!h) return SKV_EINVAL;
+    h->err[0] = 0;
+    int rc = check_pool(h, pool);
+    if (rc || (rc = check_query(h, pool, shape, q)) ||
+        (rc = check_lists(h, shape->S, shape->Hk, page_ids, pages_per_list, kv_len)))
+        return rc;
+    if (sel && n_sel < 1) return fail(h, SKV_EINVAL, "n_sel = %d", n_sel);
+    if (o_type != SKV_F32 && o_type != SKV_F16) return fail(h, SKV_EINVAL, "o_type is SKV_F32 or SKV_F16");
+    if (!o || !lse) return fail(h, SKV_EINVAL, "o or lse is NULL");
+    if (misaligned(o, 16) || misaligned(lse, 4)) return fail(h, SKV_EUNSUPPORTED, "o must be 16-byte aligned");
+    OnDevice on(h->device);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int D = shape->D;
+    AttnArgs a = {};
+    a.L = lists_of(h, pool->n_pages, shape->S, shape->Hk, page_ids, pages_per_list, kv_len);
+    a.k = pool->k;
+    a.v = pool->v;
+    a.k_scale = pool->k_scale;
+    a.v_scale = pool->v_scale;
+    a.q = static_cast<const __half *>(q);
+    a.q_pos = q_pos;
+    a.sel = sel;
+    a.n_sel = sel ? n_sel : 0;
+    a.nq = shape->nq;
+    a.H = shape->H;
+    a.G = shape->H / shape->Hk;
+    a.scale_log2 = shape->scale * 1.4426950408889634f;
+    a.o = o;
+    a.lse = lse;
+    a.counters = h->counters;
+    const int64_t n_lists = sel ? static_cast<int64_t>(shape->S) * shape->nq : shape->S;
+    a.rows = sel ? a.G : shape->nq * a.G;
+    const int nc = a.rows <= 8 ? 1 : 2;
+    a.row_groups = (a.rows + 8 * nc - 1) / (8 * nc);
+    const int64_t units = n_lists * shape->Hk * a.row_groups;
+    if (units > kMaxUnits)
+        return fail(h, SKV_EUNSUPPORTED, "%lld (list, KV head, row group) units exceed %d", (long long)units, kMaxUnits);
+    // every CTA that can be resident, but no more than pieces of one page a warp
+    const int64_t most = units * (sel ? n_sel : pages_per_list);
+    const int grid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(h->sm_count) * (nc == 1 ? kDecodeCtas : 2),
+                                                        (most + kDecodeWarps - 1) / kDecodeWarps));
+    const size_t po = round256(static_cast<size_t>(2) * grid * 8 * nc * D * sizeof(float));
+    const size_t pm = round256(static_cast<size_t>(2) * grid * 8 * nc * 2 * sizeof(float));
+    a.page_ld = sel ? n_sel : pages_per_list;
+    const size_t pl = mass ? static_cast<size_t>(shape->S) * shape->nq * shape->H * a.page_ld * sizeof(float) : 0;
+    if ((rc = ensure_workspace(h, po + pm + pl, st))) return rc;
+    uint8_t *ws = static_cast<uint8_t *>(h->workspace);
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float *>(ws + po);
+    a.page_lse = mass ? reinterpret_cast<float *>(ws + po + pm) : nullptr;
+    if ((rc = launch_decode(h, a, D, o_type == SKV_F16, grid, nc, st))) return rc;
+    return mass ? launch_mass(h, a, mass, st) : SKV_OK;
+}
+
+int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,
+                  const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
+                  int32_t n_sel, int32_t n_first, int32_t n_last, int32_t *sel, void *stream)
+{
+    if (!h) return SKV_EINVAL;
+    h->err[0] = 0;
+    int rc = check_pool(h, pool);
+    if (rc || (rc = check_query(h, pool, shape, q)) ||
+        (rc = check_lists(h, shape->S, shape->Hk, page_ids, pages_per_list, kv_len)))
+        return rc;
+    if (n_sel < 1 || n_first < 0 || n_last < 0 || static_cast<int64_t>(n_first) + n_last > n_sel)
+        return fail(h, SKV_EINVAL, "n_sel = %d with n_first = %d, n_last = %d", n_sel, n_first, n_last);
+    if (!sel) return fail(h, SKV_EINVAL, "sel is NULL");
+    const int64_t rows = static_cast<int64_t>(shape->S) * shape->nq * shape->Hk;
+    if (rows > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "S*nq*Hk exceeds 2^31 - 1");
+    OnDevice on(h->device);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    SelectArgs a = {};
+    a.L = lists_of(h, pool->n_pages, shape->S, shape->Hk, page_ids, pages_per_list, kv_len);
+    a.k_min = pool->k_min;
+    a.k_max = pool->k_max;
+    a.k_scale = pool->k_scale;
+    a.q = static_cast<const __half *>(q);
+    a.q_pos = q_pos;
+    a.nq = shape->nq;
+    a.H = shape->H;
+    a.G = shape->H / shape->Hk;
+    a.n_sel = n_sel;
+    a.n_first = n_first;
+    a.n_last = n_last;
+    a.sel = sel;
+    if ((rc = ensure_workspace(h, static_cast<size_t>(rows) * pages_per_list * sizeof(uint32_t), st))) return rc;
+    a.keys = static_cast<uint32_t *>(h->workspace);
+    return launch_select(h, a, shape->D, st);
+}
+
+int skv_q8_evict(skv_handle *h, int32_t S, int32_t Hk, int64_t pages_per_list, const int32_t *page_ids,
+                 const float *mass, const int32_t *kv_len, int32_t n_keep, int32_t n_first, int32_t n_last,
+                 int32_t *page_ids_out, float *mass_out, int32_t *kv_len_out, int32_t *freed_out, void *stream)
+{
+    if (!h) return SKV_EINVAL;
+    h->err[0] = 0;
+    int rc = check_lists(h, S, Hk, page_ids, pages_per_list, kv_len);
+    if (rc) return rc;
+    if (n_keep < 1 || n_first < 0 || n_last < 1 || static_cast<int64_t>(n_first) + n_last > n_keep)
+        return fail(h, SKV_EINVAL, "n_keep = %d with n_first = %d, n_last = %d (at least 1)", n_keep, n_first, n_last);
+    if (!mass || !page_ids_out || !mass_out || !kv_len_out || !freed_out) return fail(h, SKV_EINVAL, "NULL pointer");
+    struct Span {
+        uintptr_t at, bytes;
+    };
+    const uintptr_t lists = static_cast<uintptr_t>(S) * Hk * pages_per_list * 4, lens = static_cast<uintptr_t>(S) * 4;
+    const Span spans[7] = {{reinterpret_cast<uintptr_t>(page_ids_out), lists}, {reinterpret_cast<uintptr_t>(mass_out), lists},
+                           {reinterpret_cast<uintptr_t>(freed_out), lists},    {reinterpret_cast<uintptr_t>(kv_len_out), lens},
+                           {reinterpret_cast<uintptr_t>(page_ids), lists},     {reinterpret_cast<uintptr_t>(mass), lists},
+                           {reinterpret_cast<uintptr_t>(kv_len), lens}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (spans[i].at < spans[j].at + spans[j].bytes && spans[j].at < spans[i].at + spans[i].bytes)
+                return fail(h, SKV_EINVAL, "an output overlaps an input or another output");
+    OnDevice on(h->device);
+    return launch_evict(h, lists_of(h, INT32_MAX, S, Hk, page_ids, pages_per_list, kv_len), mass, n_keep, n_first,
+                        n_last, page_ids_out, mass_out, kv_len_out, freed_out, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

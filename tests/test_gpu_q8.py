@@ -1,0 +1,480 @@
+"""The calls over 8-bit pages on the GPU against their definitions in 64 bits:
+appends code for code, attention within the arithmetic's bounds, selections and
+evictions index for index, and the calls together as a server makes them."""
+import numpy as np
+import pytest
+
+import q8_util as u
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def h():
+    import split_kv_flash_attn_gb300 as skv
+    x = skv.Handle(0)
+    yield x
+    x.close()
+
+
+def _dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _q(rng, S, nq, H, D):
+    return rng.standard_normal((S, nq, H, D)).astype(np.float16)
+
+
+def _causal(c, nq):
+    return (c.lens[:, None] - nq + np.arange(nq)[None]).astype(np.int32)
+
+
+# --------------------------------------------------------------------- appends
+
+@pytest.mark.parametrize("D,Hk,n,lens,f16", [
+    (128, 2, 1, [0, 1, 63, 64, 65, 127], False), (64, 3, 1, [5, 62, 128], True),
+    (128, 1, 64, [0, 1, 64, 100], True), (64, 2, 130, [0, 37, 63], False),
+    (128, 2, 200, [3], False), (128, 8, 7, [60, 61, 0, 200], True)])
+def test_append_codes(h, D, Hk, n, lens, f16):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(D + Hk * 10 + n)
+    c = u.Cache(rng, lens, Hk, D, extra=n)
+    pool, ids, kv_len = c.on_gpu()
+    x = rng.standard_normal((2, len(lens), n, Hk, D)) * rng.choice([0.1, 1.0, 6.0], (2, len(lens), n, Hk, 1))
+    x = x.astype(np.float16 if f16 else np.float32)
+    for _ in range(2):                                # again: the same bytes
+        skv.q8_append(h, pool, _dev(x[0]), _dev(x[1]), ids, kv_len)
+        u.append(c, x[0], x[1])
+        for name, want in (("k", c.k), ("v", c.v), ("k_scale", c.ks), ("v_scale", c.vs), ("k_min", c.lo), ("k_max", c.hi)):
+            got = getattr(pool, name).cpu().numpy()
+            assert np.array_equal(got, want), f"{name} differs in {np.count_nonzero(got != want)} places"
+    assert h.status() == 0
+
+
+def test_append_special_values_and_ragged_counts(h):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(5)
+    D, Hk, lens = 64, 1, [10, 64, 0, 3, 70, 1]
+    c = u.Cache(rng, lens, Hk, D, extra=20)
+    c.vs[c.ids[3, 0, 0]] = np.float32(1e-41)          # a subnormal scale already there
+    pool, ids, kv_len = c.on_gpu()
+    x = rng.standard_normal((2, 6, 20, Hk, D)).astype(np.float32)
+    x[0, 0, 3, 0, 5], x[0, 0, 4, 0, 6], x[0, 0, 5, 0, 7] = np.inf, -np.inf, np.nan
+    x[1, 1] = 0.0                                     # nothing but zeros: scale 0
+    x[:, 2] *= np.float32(2e-43)                      # subnormal values, scale of a few units
+    x[1, 3] *= np.float32(1e-40)
+    x[0, 4] *= np.float32(1e37)
+    x[0, 5] = (np.arange(D) + 0.5).astype(np.float32) # exact ties against a scale of 1
+    x[0, 5, :, 0, 0] = 127.0
+    c.ks[c.ids[5, 0, 0]] = 1.0
+    pool.k_scale[int(c.ids[5, 0, 0])] = 1.0
+    n_new = np.array([20, 7, 20, 5, -3, 20], np.int32)
+    skv.q8_append(h, pool, _dev(x[0]), _dev(x[1]), ids, kv_len, n_new=_dev(n_new))
+    u.append(c, x[0], x[1], n_new)
+    for name, want in (("k", c.k), ("v", c.v), ("k_scale", c.ks), ("v_scale", c.vs), ("k_min", c.lo), ("k_max", c.hi)):
+        assert np.array_equal(getattr(pool, name).cpu().numpy(), want), name
+    assert h.status() == 0
+
+
+def test_append_without_a_page_is_reported(h):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(6)
+    c = u.Cache(rng, [60, 5], 1, 64, cap=2)           # the first list has no second page
+    pool, ids, kv_len = c.on_gpu()
+    before = pool.k.clone()
+    x = rng.standard_normal((2, 10, 1, 64)).astype(np.float32)
+    skv.q8_append(h, pool, _dev(x), _dev(x), ids, kv_len)
+    with pytest.raises(skv.SplitKVError, match="0x2"):
+        h.status()
+    u.append(c, x, x)
+    assert np.array_equal(pool.k.cpu().numpy(), c.k) and not np.array_equal(before.cpu().numpy(), c.k)
+    ids[0, 0, 1] = c.n_pages                          # outside the pool: not written either
+    skv.q8_append(h, pool, _dev(x), _dev(x), ids, kv_len)
+    with pytest.raises(skv.SplitKVError, match="0x2"):
+        h.status()
+    assert np.array_equal(pool.k.cpu().numpy(), c.k)
+
+
+# ------------------------------------------------------------------- attention
+
+ATTN = [
+    # S lens, nq, H, Hk, D, causal
+    ([1], 1, 1, 1, 64, False), ([256], 1, 4, 1, 64, False), ([63, 64, 65, 0, 1], 1, 8, 2, 128, False),
+    ([1000, 3, 517], 1, 10, 2, 128, False), ([300], 1, 16, 1, 128, False), ([777, 0, 12], 3, 8, 2, 64, True),
+    ([130, 40], 5, 6, 2, 128, True), ([4097], 1, 40, 8, 128, False), ([2000, 64], 2, 24, 8, 64, True),
+    ([90], 40, 2, 2, 128, True), ([5, 200], 9, 20, 4, 128, True), ([321], 1, 71, 1, 64, False),
+]
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("lens,nq,H,Hk,D,causal", ATTN)
+def test_attention(h, lens, nq, H, Hk, D, causal, f16):
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(sum(lens) + H + D)
+    c = u.Cache(rng, lens, Hk, D)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, len(lens), nq, H, D)
+    q_pos = _causal(c, nq) if causal else None
+    ref = u.attention(c, q, q_pos=q_pos)
+    mass = torch.ones((len(lens), Hk, c.cap), device="cuda")
+    for m in (None, mass):
+        o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=None if q_pos is None else _dev(q_pos), mass=m,
+                             o_dtype=torch.float16 if f16 else torch.float32)
+        u.check(o, lse, ref, f16=f16)
+    # a page's weight: at most nq*H/Hk probabilities, each off by e = tol_o / (2 vmax) relative, and fp32 sums
+    tol = (ref[3] / (2 * ref[5]) if ref[5] else 0) * nq * H / Hk + nq * H / Hk * 2.0 ** -20 + 2.0 ** -22
+    assert np.abs(mass.double().cpu().numpy() - 1.0 - ref[2]).max() <= tol
+    assert h.status() == 0
+
+
+def test_attention_absent_pages_and_far_scales(h):
+    """Padding inside a list, scales that differ by 2^40 and zero scales, large scores."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(11)
+    c = u.Cache(rng, [700, 640, 128], 2, 128)
+    c.ids[0, 0, 3] = -1
+    c.ids[0, 1, 0] = -5
+    c.ids[2, 1, :2] = -1                              # nothing left for this head
+    c.vs *= (2.0 ** rng.integers(-40, 1, c.n_pages)).astype(np.float32)
+    c.vs[c.ids[1, 0, 0]] = 0.0
+    c.ks[c.ids[1, 1, 4]] = 0.0
+    c.ks[c.ids[1, 0, 2]] *= 20
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 3, 1, 8, 128)
+    mass = torch.zeros((3, 2, c.cap), device="cuda")
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, mass=mass)
+    ref = u.attention(c, q)
+    u.check(o, lse, ref)
+    assert np.array_equal(mass.cpu().numpy() == 0, ref[2] == 0)
+    assert h.status() == 0
+
+
+def test_attention_reports_bad_lists(h):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(12)
+    c = u.Cache(rng, [200, 100], 1, 64, cap=4)
+    c.ids[0, 0, 1] = c.n_pages + 7                    # outside the pool: reads as absent
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 2, 1, 4, 64)
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len)
+    u.check(o, lse, u.attention(c, q))
+    with pytest.raises(skv.SplitKVError, match="0x4"):
+        h.status()
+    c.ids[0, 0, 1] = -1
+    c.lens[:] = [200, -3]
+    o, lse = skv.q8_attn(h, pool, _dev(q), _dev(c.ids), _dev(c.lens))
+    c.lens[1] = 0
+    u.check(o, lse, u.attention(c, q))
+    assert h.status() == 0
+    long = c.lens.copy()
+    long[0] = 4 * u.PAGE + 1                          # longer than its list: cut to it
+    c.lens[0] = 4 * u.PAGE
+    o, lse = skv.q8_attn(h, pool, _dev(q), _dev(c.ids), _dev(long))
+    u.check(o, lse, u.attention(c, q))
+    with pytest.raises(skv.SplitKVError, match="0x4"):
+        h.status()
+
+
+@pytest.mark.parametrize("lens,nq,H,Hk,D,n", [([1000, 64, 0], 1, 8, 2, 128, 5), ([640, 333], 4, 8, 1, 64, 3), ([2000], 2, 40, 2, 128, 40)])
+def test_attention_over_a_selection(h, lens, nq, H, Hk, D, n):
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(n)
+    c = u.Cache(rng, lens, Hk, D)
+    c.ids[0, 0, 2] = -1
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, len(lens), nq, H, D)
+    q_pos = _causal(c, nq)
+    sel = rng.integers(-1, max(lens) // u.PAGE + 3, (len(lens), nq, Hk, n)).astype(np.int32)
+    sel[0, 0, 0, 0] = sel[0, 0, 0, -1] = 1            # the same page twice counts twice
+    sel[0, -1, 0, :2] = 2 ** 30                       # far behind the list
+    ref = u.attention(c, q, q_pos=q_pos, sel=sel)
+    mass = torch.zeros((len(lens), Hk, c.cap), device="cuda")
+    runs = []
+    for _ in range(2):
+        mass.zero_()
+        o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(q_pos), sel=_dev(sel), mass=mass)
+        u.check(o, lse, ref)
+        runs.append(mass.clone())
+    assert torch.equal(runs[0], runs[1])
+    tol = (ref[3] / (2 * ref[5]) + 2.0 ** -20) * nq * H / Hk
+    assert np.abs(mass.double().cpu().numpy() - ref[2]).max() <= tol
+    assert h.status() == 0
+
+
+# --------------------------------------------------------------- the selection
+
+@pytest.mark.parametrize("lens,nq,H,Hk,D,n,first,last,causal", [
+    ([1000], 1, 4, 1, 128, 4, 1, 1, False), ([5000, 64, 0, 1], 1, 8, 2, 64, 16, 0, 0, False),
+    ([777, 2500], 3, 10, 2, 128, 7, 2, 2, True), ([300], 20, 4, 4, 64, 3, 1, 2, True),
+    ([4096], 1, 80, 1, 64, 10, 0, 1, False), ([130], 2, 8, 8, 128, 8, 1, 1, True), ([9000], 1, 2, 2, 128, 1, 0, 1, False)])
+def test_selection(h, lens, nq, H, Hk, D, n, first, last, causal):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(sum(lens) + n)
+    c = u.Cache(rng, lens, Hk, D)
+    if c.cap > 8:
+        c.ids[0, 0, 3] = -1                           # absent
+        c.ids[0, 0, 6] = c.ids[0, 0, 4]               # the same page twice: the same score
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, len(lens), nq, H, D)
+    q[0, 0, 0] = 0                                    # a query of zeros: all its bounds are 0
+    if H // Hk == 1:
+        q[0, 0] = 0                                   # ... for every head: all ties
+    q_pos = _causal(c, nq) if causal else None
+    got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=n, n_first=first, n_last=last,
+                        q_pos=None if q_pos is None else _dev(q_pos))
+    want = u.select(c, q, n, first, last, q_pos)
+    assert np.array_equal(got.cpu().numpy(), want)
+    assert h.status() == 0
+
+
+def test_selection_bounds_every_score(h):
+    """The bound is one: the page of the best key under the coded query is always picked."""
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(3)
+    c = u.Cache(rng, [64 * 40], 1, 128)
+    c.ks[:] = 0.03
+    best = 17
+    q = _q(rng, 1, 1, 1, 128)
+    cq = u.code(q[0, 0, 0], np.float32(np.abs(q).astype(np.float64).max() / 127))
+    c.k[c.ids[0, 0, best], 9] = np.clip(cq.astype(int) * 2, -127, 127)   # one key along the query
+    c.extremes()
+    pool, ids, kv_len = c.on_gpu()
+    got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=8, n_first=0, n_last=0).cpu().numpy()[0, 0, 0]
+    scores = np.array([(c.k[p].astype(int) @ cq.astype(int)).max() for p in c.ids[0, 0, :40]])
+    bounds = np.array([np.maximum(cq.astype(int) * c.lo[p].astype(int), cq.astype(int) * c.hi[p].astype(int)).sum()
+                       for p in c.ids[0, 0, :40]])
+    assert np.all(bounds >= scores)
+    assert np.all(np.sort(bounds)[::-1][:8] == np.sort(bounds[got])[::-1])
+
+
+# ------------------------------------------------------------------- evictions
+
+@pytest.mark.parametrize("lens,Hk,cap,keep,first,last", [
+    ([64 * 20], 1, 25, 5, 1, 1), ([1000, 64, 0, 63, 5000], 2, 90, 8, 2, 3), ([700], 3, 11, 1, 0, 1), ([700], 3, 11, 11, 0, 2),
+    ([64 * 3000 - 5, 64 * 1500], 2, 3000, 700, 1, 4), ([64 * 49000, 64 * 10], 1, 49500, 200, 1, 1)])
+def test_eviction(h, lens, Hk, cap, keep, first, last):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(keep + cap)
+    S = len(lens)
+    ids = rng.permutation(S * Hk * cap).astype(np.int32).reshape(S, Hk, cap)
+    ids[rng.random(ids.shape) < 0.1] = -1
+    mass = rng.choice(np.array([0.0, -0.0, 0.25, 1.0, np.inf, np.nan, 3.5], np.float32), ids.shape)
+    mass = np.where(rng.random(ids.shape) < 0.5, mass, rng.random(ids.shape)).astype(np.float32)
+    got = skv.q8_evict(h, _dev(ids), _dev(mass), _dev(np.array(lens, np.int32)), n_keep=keep, n_first=first, n_last=last)
+    want = u.evict(ids, mass, lens, keep, first, last)
+    for name, a, b in zip(("page_ids", "mass", "kv_len", "freed"), got, want):
+        assert np.array_equal(a.cpu().numpy(), b, equal_nan=name == "mass"), name
+    assert h.status() == 0
+
+
+# ------------------------------------------------------------- the calls together
+
+def test_a_server_s_steps(h):
+    """Prompt, decode steps with accumulated weight, sparse steps, eviction, reuse of the freed pages."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(77)
+    Hk, H, D, S = 2, 8, 128, 2
+    c = u.Cache(rng, [0, 0], Hk, D, extra=1400, spare=0)
+    pool, ids, kv_len = c.on_gpu()
+    pool.k.fill_(99)                                  # pages need not be cleared
+    pool.k_scale.fill_(7.0)
+    c.k[:], c.ks[:] = 99, 7.0
+    mass = torch.zeros((S, Hk, c.cap), device="cuda")
+    ref_mass = np.zeros((S, Hk, c.cap))
+
+    def append(n, n_new=None):
+        x = rng.standard_normal((2, S, n, Hk, D)).astype(np.float16)
+        skv.q8_append(h, pool, _dev(x[0]), _dev(x[1]), ids, kv_len, n_new=None if n_new is None else _dev(n_new))
+        u.append(c, x[0], x[1], n_new)
+        kv_len.add_(n if n_new is None else _dev(n_new))
+        c.lens += n if n_new is None else n_new
+
+    append(700, np.array([700, 333], np.int32))
+    q = _q(rng, S, 30, H, D)                          # the prompt's last tokens
+    pos = _causal(c, 30)
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(pos), mass=mass)
+    ref = u.attention(c, q, q_pos=pos)
+    u.check(o, lse, ref)
+    ref_mass += ref[2]
+    for step in range(4):
+        append(1)
+        q = _q(rng, S, 1, H, D)
+        sel = None
+        if step % 2:
+            sel = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=4)
+            assert np.array_equal(sel.cpu().numpy(), u.select(c, q, 4, 1, 1))
+        o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, sel=sel, mass=mass)
+        ref = u.attention(c, q, sel=None if sel is None else sel.cpu().numpy())
+        u.check(o, lse, ref)
+        ref_mass += ref[2]
+    assert np.allclose(mass.cpu().numpy(), ref_mass, rtol=1e-4, atol=1e-4)
+    m = mass.cpu().numpy()
+    ids2, mass2, len2, freed = skv.q8_evict(h, ids, mass, kv_len, n_keep=6, n_first=1, n_last=2)
+    w = u.evict(c.ids, m, c.lens, 6, 1, 2)
+    for a, b in zip((ids2, mass2, len2, freed), w):
+        assert np.array_equal(a.cpu().numpy(), b)
+    c.ids, c.lens = w[0], w[2]
+    ids, kv_len = ids2, len2
+    # the freed pages go behind what each list still holds
+    for s in range(S):
+        for k in range(Hk):
+            free = w[3][s, k][w[3][s, k] >= 0]
+            row = c.ids[s, k]
+            n = int((row >= 0).sum())
+            assert np.all(row[:n] >= 0)
+            row[n:n + len(free)] = free
+    ids.copy_(_dev(c.ids))
+    append(200)
+    q = _q(rng, S, 2, H, D)
+    pos = _causal(c, 2)
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(pos))
+    u.check(o, lse, u.attention(c, q, q_pos=pos))
+    assert h.status() == 0
+
+
+def test_partitions_merge(h):
+    """8-bit pages for old tokens and fp16 rows for recent ones: two partials, one combine."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(8)
+    Hk, H, D = 2, 8, 128
+    c = u.Cache(rng, [500], Hk, D)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 1, 1, H, D)
+    K = rng.standard_normal((100, Hk, D)).astype(np.float16)
+    V = rng.standard_normal((100, Hk, D)).astype(np.float16)
+    o1, l1 = skv.q8_attn(h, pool, _dev(q), ids, kv_len)
+    o2, l2 = skv.attn_partial(h, _dev(q), _dev(K.reshape(100, -1)), _dev(V.reshape(100, -1)), Hk=Hk)
+    o, lse = skv.attn_combine(h, torch.stack([o1.view(H, D), o2.view(H, D)]), torch.stack([l1.view(H), l2.view(H)]))
+    ro, rl, _, tol, tol_l, vmax = u.attention(c, q)
+    for x in range(H):
+        k = x // (H // Hk)
+        w = K[:, k].astype(np.float64) @ q[0, 0, x].astype(np.float64) / np.sqrt(D)
+        z = np.logaddexp(rl[0, 0, x], np.logaddexp.reduce(w))
+        want = np.exp(rl[0, 0, x] - z) * ro[0, 0, x] + np.exp(w - z) @ V[:, k].astype(np.float64)
+        assert np.abs(o[x].double().cpu().numpy() - want).max() <= tol + 2e-3 * max(vmax, np.abs(V).max())
+        assert abs(lse[x].item() - z) <= tol_l + 1e-4
+
+
+# ----------------------------------------------------------- streams and graphs
+
+def test_graph_replays_follow_the_inputs(h):
+    """A captured step replayed on other lengths, queries and lists, with a graph
+    captured before and one after the workspace grew."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(21)
+    hh = skv.Handle(0)
+    Hk, H, D = 2, 8, 128
+    c = u.Cache(rng, [400, 900], Hk, D)
+    pool, ids, kv_len = c.on_gpu()
+    q = _dev(_q(rng, 2, 1, H, D))
+    mass = torch.zeros((2, Hk, c.cap), device="cuda")
+
+    def step():
+        sel = skv.q8_select(hh, pool, q, ids, kv_len, n_sel=5)
+        return skv.q8_attn(hh, pool, q, ids, kv_len, sel=sel) + skv.q8_attn(hh, pool, q, ids, kv_len, mass=mass) + (sel,)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    hh.reserve(64 << 20)                              # the workspace moves; the graph keeps its own
+    junk = torch.full((32 << 20,), 1.0, device="cuda")
+    for lens in ([400, 900], [1, 0], [833, 64]):
+        c.lens[:] = lens
+        c.extremes()
+        pool.k_min.copy_(_dev(c.lo))
+        pool.k_max.copy_(_dev(c.hi))
+        kv_len.copy_(_dev(c.lens))
+        qq = _q(rng, 2, 1, H, D)
+        q.copy_(_dev(qq))
+        g.replay()
+        torch.cuda.synchronize()
+        want = u.select(c, qq, 5, 1, 1)
+        assert np.array_equal(out[4].cpu().numpy(), want)
+        u.check(out[0], out[1], u.attention(c, qq, sel=want))
+        u.check(out[2], out[3], u.attention(c, qq))
+        eager = step()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))
+    del junk
+    assert hh.status() == 0
+    hh.close()
+
+
+def test_capture_does_not_grow_scratch():
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(22)
+    hh = skv.Handle(0)
+    c = u.Cache(rng, [400], 1, 64)
+    pool, ids, kv_len = c.on_gpu()
+    q = _dev(_q(rng, 1, 1, 4, 64))
+    g = torch.cuda.CUDAGraph()
+    o = torch.empty((1, 1, 4, 64), device="cuda")
+    lse = torch.empty((1, 1, 4), device="cuda")
+    err = None
+    with torch.cuda.graph(g):
+        o.zero_()
+        try:
+            skv.q8_attn(hh, pool, q, ids, kv_len, o=o, lse=lse)
+        except skv.SplitKVError as e:
+            err = e
+    assert err is not None and "SKV_ECAPTURE" in str(err)
+    hh.close()
+
+
+def test_runs_on_the_stream_it_is_given(h):
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(23)
+    c = u.Cache(rng, [1500], 2, 128)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 1, 1, 8, 128)
+    qd, zero = _dev(q), torch.zeros((1, 1, 8, 128), dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        big = torch.zeros(64 << 20, device="cuda")
+        for _ in range(10):
+            big.add_(1.0)                             # holds the stream for a while
+        zero.copy_(qd)
+        o, lse = skv.q8_attn(h, pool, zero, ids, kv_len)
+    s.synchronize()
+    u.check(o, lse, u.attention(c, q))
+
+
+def test_offsets_beyond_32_bits(h):
+    """A pool whose codes pass 2^31 bytes, read and written at its end."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(31)
+    n = (1 << 31) // (64 * 128) + 40
+    small = u.Cache(rng, [500], 1, 128, extra=70, shuffle=False, spare=0)
+    pool = skv.Q8Pool.empty(n, 128)
+    off = n - small.n_pages
+    for name, x in (("k", small.k), ("v", small.v), ("k_scale", small.ks), ("v_scale", small.vs), ("k_min", small.lo), ("k_max", small.hi)):
+        getattr(pool, name)[off:] = _dev(x)
+    ids = small.ids.copy()
+    ids[ids >= 0] += off
+    x = rng.standard_normal((2, 1, 70, 1, 128)).astype(np.float32)
+    kv_len = _dev(small.lens)
+    skv.q8_append(h, pool, _dev(x[0]), _dev(x[1]), _dev(ids), kv_len)
+    u.append(small, x[0], x[1])
+    small.lens += 70
+    kv_len += 70
+    assert np.array_equal(pool.k[off:].cpu().numpy(), small.k)
+    q = _q(rng, 1, 1, 4, 128)
+    sel = skv.q8_select(h, pool, _dev(q), _dev(ids), kv_len, n_sel=3)
+    assert np.array_equal(sel.cpu().numpy(), u.select(small, q, 3, 1, 1))
+    o, lse = skv.q8_attn(h, pool, _dev(q), _dev(ids), kv_len)
+    u.check(o, lse, u.attention(small, q))
+    assert h.status() == 0
+    del pool
+    torch.cuda.empty_cache()
