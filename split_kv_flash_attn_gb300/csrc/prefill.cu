@@ -12,13 +12,9 @@ using namespace pf;
 
 // ---- host side ------------------------------------------------------------
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // The driver entry point is process-wide (not per device); it is looked up
 // once, under C++'s thread-safe initialisation of a local static.
-static EncodeTiledFn encode_fn()
+tc::EncodeTiledFn tc::encode_fn()
 {
     static const EncodeTiledFn fn = []() -> EncodeTiledFn {
         void *p = nullptr;
@@ -37,7 +33,7 @@ static EncodeTiledFn encode_fn()
 // (Hk*D wide), y = row; box 64 x 128 with the 128-byte swizzle.
 static int make_map(skv_handle *h, CUtensorMap *map, const void *base, int64_t n_rows, int Hk, int64_t row_bytes)
 {
-    EncodeTiledFn fn = encode_fn();
+    tc::EncodeTiledFn fn = tc::encode_fn();
     if (!fn) return fail(h, SKV_ECUDA, "cuTensorMapEncodeTiled is not available");
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(Hk) * kPD, static_cast<cuuint64_t>(n_rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};

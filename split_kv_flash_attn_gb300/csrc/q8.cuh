@@ -5,6 +5,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tc.cuh"
 
 namespace skv {
 namespace q8 {
@@ -41,8 +42,8 @@ struct AttnArgs {
     float *part_o;                 // [2 * grid][columns][D] unnormalised partials
     float *part_ml;                // [2 * grid][columns][2] reference (log2) and sum
     int *counters;                 // arrivals, zero between launches
-    float *page_lse;               // mass: [S][Hk][nq * G][page_ld] log2 sums, or null
-    int64_t page_ld;               // cap, or n_sel with sel
+    float *page_lse;               // mass: [S][Hk][nq * G][page_ld] log2 sums of half pages, or null
+    int64_t page_ld;               // 2 cap, or 2 n_sel with sel
 };
 
 // Tokens of sequence s that its list can hold.
@@ -113,10 +114,14 @@ __device__ __forceinline__ int nearest_code(float x, float d)
     return static_cast<int>(fminf(fmaxf(r, -127.f), 127.f));
 }
 
-int launch_decode(skv_handle *h, const AttnArgs &a, int D, bool out_f16, int grid, int nc, cudaStream_t st);
-// CTAs of the decode kernel that one SM holds, and its pages per step of a CTA.
-constexpr int kDecodeCtas = 3;
-constexpr int kDecodeWarps = 4;
+// Pages as a tensor [n_pages][64][D] of bytes, `rows` rows of a page a box, its
+// 16-byte pieces swizzled (128 bytes a row for D = 128, 64 for D = 64).
+int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pages, int D, int rows);
+// Fewest pages of a CTA's piece in the decode kernel: with fewer, putting the
+// pieces together costs more than it gains.
+constexpr int kPieceMin = 8;
+int launch_decode(skv_handle *h, const AttnArgs &a, int64_t n_pages, int D, bool out_f16, int grid, int nc,
+                  cudaStream_t st);
 int launch_mass(skv_handle *h, const AttnArgs &a, float *mass, cudaStream_t st);
 int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_max, int x_type, const void *k_new,
                   const void *v_new, const int32_t *n_new, cudaStream_t st);

@@ -135,20 +135,19 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     const int64_t units = n_lists * shape->Hk * a.row_groups;
     if (units > kMaxUnits)
         return fail(h, SKV_EUNSUPPORTED, "%lld (list, KV head, row group) units exceed %d", (long long)units, kMaxUnits);
-    // every CTA that can be resident, but no more than pieces of one page a warp
+    // one CTA a SM, but no more than pieces of kPieceMin pages
     const int64_t most = units * (sel ? n_sel : pages_per_list);
-    const int grid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(h->sm_count) * (nc == 1 ? kDecodeCtas : 2),
-                                                        (most + kDecodeWarps - 1) / kDecodeWarps));
+    const int grid = static_cast<int>(std::min<int64_t>(h->sm_count, (most + kPieceMin - 1) / kPieceMin));
     const size_t po = round256(static_cast<size_t>(2) * grid * 8 * nc * D * sizeof(float));
     const size_t pm = round256(static_cast<size_t>(2) * grid * 8 * nc * 2 * sizeof(float));
-    a.page_ld = sel ? n_sel : pages_per_list;
+    a.page_ld = 2 * (sel ? static_cast<int64_t>(n_sel) : pages_per_list);
     const size_t pl = mass ? static_cast<size_t>(shape->S) * shape->nq * shape->H * a.page_ld * sizeof(float) : 0;
     if ((rc = ensure_workspace(h, po + pm + pl, st))) return rc;
     uint8_t *ws = static_cast<uint8_t *>(h->workspace);
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_ml = reinterpret_cast<float *>(ws + po);
     a.page_lse = mass ? reinterpret_cast<float *>(ws + po + pm) : nullptr;
-    if ((rc = launch_decode(h, a, D, o_type == SKV_F16, grid, nc, st))) return rc;
+    if ((rc = launch_decode(h, a, pool->n_pages, D, o_type == SKV_F16, grid, nc, st))) return rc;
     return mass ? launch_mass(h, a, mass, st) : SKV_OK;
 }
 

@@ -3,11 +3,14 @@
 // The mathematics.  Over a page the score of key j is (scale * d_k) * (q . c_j)
 // and its value d_v * c_vj, so the codes go into the products as they are
 // (int8 is exact in fp16) and the page's scales multiply fp32 numbers.  With m
-// the running reference of a query row and r the largest |d_v| so far,
-//   p_j = 2^(s_j - m + 10),  l = sum p_j,  O = sum (p_j * d_v / r) c_vj,
-// and o = r O / l.  The weights p_j d_v / r stay below 2^15, and each enters the
-// product as two fp16 numbers (itself rounded, and what the rounding left), which
-// keeps it to 2^-22 of its value down to 2^-24: results are good to fp32.
+// the running reference of a query row,
+//   p_j = 2^(s_j - m + 10),  l = sum p_j,  O = sum over pages d_v sum p_j c_vj,
+// and o = O / l.  The weights p_j stay below 2^14, and each enters the product as
+// two fp16 numbers (itself rounded, and what the rounding left), which keeps it
+// to 2^-22 of its value down to 2^-24.  The tensor core adds to its accumulator
+// with truncation, so products of 32 keys are summed from zero and joined to O
+// by an fp32 FMA, which also applies d_v (one accumulator over all pages was
+// off by 1.5e-6 after 11 pages a warp, growing with them).
 //
 // Work split.  All pages of all (sequence, KV head, row group) units form one
 // line, of which every CTA takes an equal piece; a piece that covers several
@@ -16,15 +19,21 @@
 // depend on timing).  Lengths are read on the device: a call costs its keys, not
 // its lists' capacity, and ragged batches stay balanced.
 //
-// A CTA's four warps take its pages in turn, each on its own: K and V bytes go
-// from global memory into registers as mma fragments without shared memory.  A
-// thread (g, t) of the fragment layout reads 16-byte pieces: of key rows g and
-// g + 8 the channels 16t .. (the order of the channels inside the product is
-// free, the queries follow it), and of value rows 2t, 2t+1, 2t+8, 2t+9 the
-// channels 16g .. (pairs of rows are interleaved by byte permutes).  Keys are
-// the M side of S = K Q^T and channels that of O^T = V^T P^T, so that the eight
-// query columns of a product carry a KV head's query heads.  32 keys at a time: V
-// is requested before S is computed, the next 32 keys' K after it.
+// A CTA is one warp that fetches and W that compute.  The first walks the CTA's
+// pages, looks their ids and scales up 32 at a time and keeps a ring of pages (K
+// and V, one TMA box each) in flight.  The others take half pages (32 keys) in
+// turn, each on its own with a state of its own; twice the slots are a
+// multiple of W, so that the same two warps own every turn of a slot (a
+// barrier's parity tells a warp only whether the turn after its last one has
+// come).  A ring of half pages was bound by the fetching warp (300 ns a slot).
+//
+// Fragments.  The order of channels inside q . c and of keys inside p . c is free,
+// so a thread (g, t) of the mma layout takes 16-byte pieces: of key rows r(g), r(g) + 8
+// the channels 16t .. and 64 + 16t .., of four value rows the channels 16 p(g) ..
+// (pairs of rows are interleaved by byte permutes).  r and p swap the low bit of g
+// to the top, which with the 128-byte swizzle makes these reads free of bank conflicts.
+// Keys are the M side of S = K Q^T and channels that of O^T = V^T P^T, so
+// the eight query columns of a product carry a KV head's query heads.
 //
 // Bound: the pages' bytes at long lengths (see the table in the design notes);
 // launch, plan and merge at short ones.
@@ -35,7 +44,21 @@ namespace q8 {
 
 constexpr float kShift = 10.f;      // weights are kept times 2^10 ...
 constexpr float kGrow = 4.f;        // ... and their reference moves when a score passes it by 2^4
-constexpr int kThreads = kDecodeWarps * 32;
+constexpr int kStep = 32;           // keys a warp takes at a time
+
+// Computing warps and ring slots.  One column group: 8 sequences x 32768 keys take
+// 64 us with 11 and 11, 65 with 7 and 7 or 8 and 8, 70 with 6 and 12; two groups
+// need the registers of 7 warps.
+__host__ __device__ constexpr int warps_of(int nc) { return nc == 1 ? 11 : 7; }
+__host__ __device__ constexpr int slots_of(int nc) { return nc == 1 ? 11 : 7; }
+template <int D, int NC>
+__host__ __device__ constexpr int decode_smem()
+{
+    return 1024 + slots_of(NC) * 2 * kPage * D               // the ring, aligned for the swizzle
+           + warps_of(NC) * 8 * (D + 4) * 4                  // the warps' results
+           + NC * (D / 16) * 32 * 8;                         // query fragments
+}
+static_assert(decode_smem<128, 1>() < 226 * 1024 && decode_smem<128, 2>() < 226 * 1024, "shared memory per CTA");
 
 // Where a piece of the line of pages lies.
 struct Place {
@@ -56,21 +79,40 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i)
 }
 
 template <int D, int NC, bool HILO, bool F16>
-__global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a)
 {
     constexpr int KS = D / 16;                      // k-steps of S
     constexpr int CH = D / 64;                      // 16-byte chunks of a key row per thread
     constexpr int MT = D / 16;                      // m-tiles of O^T
     constexpr int VW = D / 32;                      // words of a value row per thread
     constexpr int LDO = D + 4;
-    __shared__ float s_o[kDecodeWarps][8][LDO];
-    __shared__ float s_ml[kDecodeWarps][8][2];
-    __shared__ uint2 s_q[NC * KS * 32];
-    __shared__ int s_last;
+    constexpr int W = warps_of(NC);                 // computing warps; the last warp fetches
+    constexpr int kConsumers = W * 32, kThreads = kConsumers + 32;
+    constexpr int NS = slots_of(NC);
+    static_assert(2 * NS % W == 0, "the same warps own a slot's halves at every turn");
+    constexpr int BYTES = kPage * D;                // of a slot's K or V
+    struct Meta {
+        int id, blk;
+        float ks, vs;
+    };
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ alignas(8) uint64_t s_bar[2 * NS];   // full, empty
+    __shared__ Meta s_meta[64];                     // of page n of the CTA: s_meta[n % 64]
+    __shared__ float s_ml[W][8][2];
+    __shared__ int s_last, s_abort;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float(*s_o)[8][LDO] = reinterpret_cast<float(*)[8][LDO]>(ring + NS * 2 * BYTES);
+    uint2 *s_q = reinterpret_cast<uint2 *>(ring + NS * 2 * BYTES + W * 8 * LDO * 4);
+    const uint32_t bar0 = smem_addr(s_bar);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
     const int n_lists = a.sel ? a.L.S * a.nq : a.L.S;
     const int64_t mult = static_cast<int64_t>(a.L.Hk) * a.row_groups;   // units per list
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2 * NS; ++i) tc::mbar_init(bar0 + 8 * i, i < NS ? 1 : 2);
+        tc::fence_barrier_init();
+    }
 
     // ---- the plan: total pages, this CTA's piece, the list that it starts in --
     int64_t total;
@@ -87,11 +129,9 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
     total *= mult;
-    int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
-    chunk = max(int64_t(kDecodeWarps), (chunk + kDecodeWarps - 1) / kDecodeWarps * kDecodeWarps);
-    int64_t pos = blockIdx.x * chunk;
-    const int64_t pos_end = min(total, pos + chunk);
-    const int64_t pos0 = pos;
+    const int64_t chunk = max(int64_t(kPieceMin), (total + gridDim.x - 1) / gridDim.x);
+    const int64_t pos0 = blockIdx.x * chunk;
+    const int64_t pos_end = min(total, pos0 + chunk);
 
     // lists without a page: their rows are written here
     if (!a.sel) {
@@ -105,12 +145,13 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
             for (int64_t e = tid; e < nr; e += kThreads) a.lse[r0 + e] = -INFINITY;
         }
     }
-    if (pos >= pos_end) return;
+    __syncthreads();                                // the barriers are ready
+    if (pos0 >= pos_end) return;
 
     Place at = {0, 0, 0};
     if (a.sel) {
         at.np = a.n_sel;
-        at.list = static_cast<int>(pos / (at.np * mult));
+        at.list = static_cast<int>(pos0 / (at.np * mult));
         at.base = at.list * (at.np * mult);
     } else {
         int64_t before = 0;
@@ -122,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
                 const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += x;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, (before + inc) * mult > pos);
+            const unsigned hit = __ballot_sync(0xffffffffu, (before + inc) * mult > pos0);
             if (hit) {
                 const int f = __ffs(hit) - 1;
                 at.list = c0 + f;
@@ -134,64 +175,168 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
         }
     }
 
-    while (pos < pos_end) {
-        // ---- the next unit: its pages [pg0, pg1) are this CTA's ---------------
+    // The units of the piece in turn, for both roles: pages [pg0, pg1) of one unit.
+    struct Unit {
+        int64_t u_in, unit0;                        // its number within the list; the line's position of its page 0
+        int pg0, pg1, kh, rg, seq;
+        int64_t tok0;                               // token of its row 0
+    };
+    auto unit_at = [&](int64_t pos) {
         while (pos >= at.base + at.np * mult) {     // the next list with pages
             at.base += at.np * mult;
             ++at.list;
             at.np = pages_of(a, at.list);
         }
-        const int64_t u_in = (pos - at.base) / at.np;
-        const int64_t unit0 = at.base + u_in * at.np;              // the line's position of the unit's first page
-        const int pg0 = static_cast<int>(pos - unit0);
-        const int pg1 = static_cast<int>(min(at.np, pos_end - unit0));
-        const int kh = static_cast<int>(u_in / a.row_groups);
-        const int rg = static_cast<int>(u_in - static_cast<int64_t>(kh) * a.row_groups);
-        const int seq = a.sel ? at.list / a.nq : at.list;
-        const int64_t tok0 = a.sel ? at.list : static_cast<int64_t>(at.list) * a.nq;   // token of row 0
-        const int row0 = rg * 8 * NC;
-        const int len = static_cast<int>(list_len(a.L, seq));
-        const int32_t *ids = a.L.ids + (static_cast<int64_t>(seq) * a.L.Hk + kh) * a.L.cap;
-        const int32_t *sel = a.sel ? a.sel + (static_cast<int64_t>(at.list) * a.L.Hk + kh) * a.n_sel : nullptr;
-        auto out_row = [&](int row) { return (tok0 + row / a.G) * a.H + kh * a.G + row % a.G; };
+        Unit x;
+        x.u_in = (pos - at.base) / at.np;
+        x.unit0 = at.base + x.u_in * at.np;
+        x.pg0 = static_cast<int>(pos - x.unit0);
+        x.pg1 = static_cast<int>(min(at.np, pos_end - x.unit0));
+        x.kh = static_cast<int>(x.u_in / a.row_groups);
+        x.rg = static_cast<int>(x.u_in - static_cast<int64_t>(x.kh) * a.row_groups);
+        x.seq = a.sel ? at.list / a.nq : at.list;
+        x.tok0 = a.sel ? at.list : static_cast<int64_t>(at.list) * a.nq;
+        return x;
+    };
+    // A phase already complete is taken at once; the abort flag is read only
+    // when the barrier is not ready.
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&s_abort)) return false;
+        if (tc::mbar_wait(bar, parity, &s_abort)) return true;
+        s_abort = 1;
+        atomicOr(a.L.status, 1);
+        return false;
+    };
+    // keys that a row sees
+    auto seen_by = [&](const Unit &x, int row, int len) {
+        if (!a.q_pos) return len;
+        const int qp = a.q_pos[x.tok0 + row / a.G];
+        return qp < 0 ? 0 : (qp < len ? qp + 1 : len);
+    };
 
+    if (warp == W) {
+        // ---------------- the fetching warp -----------------------------------
+        uint32_t n_put = 0;                         // pages put into the ring so far
+        bool ok = true;
+        for (int64_t pos = pos0; ok && pos < pos_end;) {
+            const Unit x = unit_at(pos);
+            const int len = static_cast<int>(list_len(a.L, x.seq));
+            const int32_t *ids = a.L.ids + (static_cast<int64_t>(x.seq) * a.L.Hk + x.kh) * a.L.cap;
+            const int32_t *sel = a.sel ? a.sel + (static_cast<int64_t>(at.list) * a.L.Hk + x.kh) * a.n_sel : nullptr;
+            int lim = len;                          // keys that any row of the unit sees
+            if (a.q_pos) {
+                const int row = x.rg * 8 * NC + lane;
+                lim = lane < 8 * NC && row < a.rows ? seen_by(x, row, len) : 0;
+                lim = __reduce_max_sync(0xffffffffu, lim);
+            }
+            auto load_meta = [&](int first) {
+                Meta m = {-1, 0, 0.f, 0.f};
+                const int p = first + lane;
+                if (p < x.pg1) {
+                    const int64_t blk = sel ? __ldg(sel + p) : p;
+                    if (blk >= 0 && blk * kPage < lim) m.id = max(-1, checked_page(a.L, __ldg(ids + blk)));
+                    m.blk = static_cast<int>(blk);
+                    if (m.id >= 0) {
+                        m.ks = __ldg(a.k_scale + m.id) * a.scale_log2;
+                        m.vs = __ldg(a.v_scale + m.id);
+                    }
+                }
+                return m;
+            };
+            Meta nxt = load_meta(x.pg0);
+            for (int first = x.pg0; ok && first < x.pg1; first += 32) {
+                const Meta cur = nxt;
+                if (first + 32 < x.pg1) nxt = load_meta(first + 32);
+                const int n = min(32, x.pg1 - first);
+                // (64 entries: those of the 32 pages before are still in use, at
+                // most NS of them not taken yet)
+                if (lane < n) s_meta[(n_put + lane) % 64] = cur;
+                __syncwarp();
+                if (lane == 0) {
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t m = n_put + i, slot = m % NS, turn = m / NS;
+                        const uint32_t full = bar0 + 8 * slot, empty = bar0 + 8 * (NS + slot);
+                        if (turn > 0 && !wait(empty, (turn - 1) & 1)) {
+                            ok = false;
+                            n_put = m - n;          // (+ n below)
+                            break;
+                        }
+                        const int id = s_meta[m % 64].id;
+                        if (id >= 0) {
+                            const uint32_t dst = smem_addr(ring + slot * 2 * BYTES);
+                            tc::mbar_expect_tx(full, 2 * BYTES);
+                            tc::tma_load_3d(dst, &map_k, 0, 0, id, full);
+                            tc::tma_load_3d(dst + BYTES, &map_v, 0, 0, id, full);
+                        } else {
+                            tc::mbar_arrive(full);
+                        }
+                    }
+                }
+                n_put += n;
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            pos = x.unit0 + x.pg1;
+        }
+        if (!ok && lane == 0) {
+            // copies in flight land before the CTA ends (bounded)
+            for (uint32_t i = n_put > NS ? n_put - NS : 0; i < n_put; ++i)
+                tc::mbar_wait(bar0 + 8 * (i % NS), (i / NS) & 1, nullptr, 100000000ull);
+        }
+        return;
+    }
+
+    // ---------------- the computing warps --------------------------------------
+    const int g = lane >> 2, t = lane & 3;
+    const int rg_ = D == 128 ? (g >> 1) | ((g & 1) << 2) : g;       // r(g), p(g)
+    auto sync_all = [] { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); };
+    // byte offsets of the thread's pieces in a page (see the header)
+    uint32_t k_off[CH], v_off[2];
+    if constexpr (D == 128) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) k_off[c] = rg_ * 128 + (((t + 4 * c) ^ rg_) << 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v_off[e] = (t + 4 * e) * 128 + ((rg_ ^ (t + 4 * e)) << 4);
+    } else {
+        k_off[0] = g * 64 + ((t ^ (g >> 1)) << 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v_off[e] = (2 * t + e) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+    }
+    uint32_t n_taken = 0;                           // half pages of the CTA's earlier units
+    for (int64_t pos = pos0; pos < pos_end;) {
+        const Unit x = unit_at(pos);
+        const int row0 = x.rg * 8 * NC;
+        const int len = static_cast<int>(list_len(a.L, x.seq));
+        auto out_row = [&](int row) { return (x.tok0 + row / a.G) * a.H + x.kh * a.G + row % a.G; };
+        auto page_lse = [&](int row) {              // log sums of a row's pages
+            const int64_t r = a.sel ? (at.list % a.nq) * static_cast<int64_t>(a.G) + row : row;
+            return a.page_lse + ((static_cast<int64_t>(x.seq) * a.L.Hk + x.kh) * a.nq * a.G + r) * a.page_ld;
+        };
         // query fragments into shared memory: lane (g, t) of k-step (c, w) holds
         // channels 64c + 16t + 4w .. + 3 of column g
-        for (int x = tid; x < NC * KS * 32; x += kThreads) {
-            const int row = row0 + x / (KS * 32) * 8 + ((x & 31) >> 2);
-            const int ks = x / 32 % KS;
+        for (int i = tid; i < NC * KS * 32; i += kConsumers) {
+            const int row = row0 + i / (KS * 32) * 8 + ((i & 31) >> 2);
+            const int ks = i / 32 % KS;
             uint2 v = make_uint2(0, 0);
             if (row < a.rows)
-                v = __ldg(reinterpret_cast<const uint2 *>(a.q + out_row(row) * D + 64 * (ks >> 2) + 16 * (x & 3) + 4 * (ks & 3)));
-            s_q[x] = v;
+                v = __ldg(reinterpret_cast<const uint2 *>(a.q + out_row(row) * D + 64 * (ks >> 2) + 16 * (i & 3) + 4 * (ks & 3)));
+            s_q[i] = v;
         }
         int lim[NC][2];                             // keys that columns 2t, 2t+1 see
-        int lim_min = len, lim_max = a.q_pos ? 0 : len;
+        int lim_min = len;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = row0 + j * 8 + 2 * t + e;
-                lim[j][e] = len;
-                if (a.q_pos && r < a.rows) {
-                    const int qp = a.q_pos[tok0 + r / a.G];
-                    lim[j][e] = qp < 0 ? 0 : (qp < len ? qp + 1 : len);
-                    lim_min = min(lim_min, lim[j][e]);
-                    lim_max = max(lim_max, lim[j][e]);
-                }
+                lim[j][e] = r < a.rows ? seen_by(x, r, len) : len;
+                lim_min = min(lim_min, lim[j][e]);
             }
-        }
-        if (a.q_pos) {
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
-                lim_max = max(lim_max, __shfl_xor_sync(0xffffffffu, lim_max, o));
-            }
-        }
+        for (int o = 1; o < 4; o <<= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+        sync_all();                                 // s_q is written
 
-        __syncthreads();                            // s_q is written
         float m_ref[NC][2], l_sum[NC][2], acc[NC][MT][4];
-        float r_ref = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             m_ref[j][0] = m_ref[j][1] = -INFINITY;
@@ -202,264 +347,211 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
                 for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
         }
 
-        // ---- pages, 32 at a time: lane i holds what is known of the i-th -------
-        struct Meta {
-            int id, blk;
-            float ks, vs;
-        };
-        auto load_meta = [&](int first) {
-            Meta x = {-1, 0, 0.f, 0.f};
-            const int p = first + kDecodeWarps * lane;
-            if (p < pg1) {
-                const int64_t blk = sel ? __ldg(sel + p) : p;
-                if (blk >= 0 && blk * kPage < lim_max) x.id = checked_page(a.L, __ldg(ids + blk));
-                x.blk = static_cast<int>(blk);
-                if (x.id >= 0) {
-                    x.ks = __ldg(a.k_scale + x.id) * a.scale_log2;
-                    x.vs = __ldg(a.v_scale + x.id);
-                } else if (a.page_lse) {
-                    for (int c = 0; c < 8 * NC; ++c) {
-                        const int row = row0 + c;
-                        if (row >= a.rows) break;
-                        const int64_t rr = a.sel ? (at.list % a.nq) * a.G + row : row;
-                        a.page_lse[((static_cast<int64_t>(seq) * a.L.Hk + kh) * a.nq * a.G + rr) * a.page_ld + p] = -INFINITY;
-                    }
-                }
+        const uint32_t n_end = n_taken + 2 * (x.pg1 - x.pg0);
+        for (uint32_t n = n_taken + (warp + W - n_taken % W) % W; n < n_end; n += W) {
+            const uint32_t m = n >> 1, slot = m % NS;   // (units begin at even n)
+            const int p = x.pg0 + static_cast<int>((n - n_taken) >> 1), h = n & 1;
+            const bool there = wait(bar0 + 8 * slot, (m / NS) & 1);
+            const Meta meta = s_meta[m % 64];
+            if (!there || meta.id < 0) {
+                if (a.page_lse && lane < 8 * NC && row0 + lane < a.rows) page_lse(row0 + lane)[2 * p + h] = -INFINITY;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar0 + 8 * (NS + slot));
+                continue;
             }
-            return x;
-        };
-        uint4 kr[2][2][CH];
-        auto load_k = [&](int id, int h) {
-            const int8_t *base = a.k + static_cast<int64_t>(id) * (kPage * D) + (32 * h + g) * D + 16 * t;
+            const uint8_t *pk = ring + slot * 2 * BYTES + h * (kStep * D), *pv = pk + BYTES;
+            const int key0 = meta.blk * kPage + h * kStep;   // (blk * 64 is below len)
+            // (a zero scale as a tiny one, so that its product with a masked -inf stays one)
+            const float ks = fmaxf(fabsf(meta.ks), 1e-30f), vs = meta.vs;
+            const bool masked = lim_min - key0 < kStep;
+            {
+                // S = K Q^T of 32 keys
+                float s[NC][2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int c = 0; c < CH; ++c) {
+                    uint4 kr[2][2];
 #pragma unroll
-                for (int rr = 0; rr < 2; ++rr)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) kr[i][rr][c] = ld_stream16(base + (16 * i + 8 * rr) * D + 64 * c);
-        };
-        int first = pg0 + warp;
-        Meta cur = load_meta(first);
-        while (first < pg1) {
-            const int next_first = first + 32 * kDecodeWarps;
-            unsigned todo = __ballot_sync(0xffffffffu, cur.id >= 0);
-            const Meta nxt = next_first < pg1 ? load_meta(next_first) : Meta{-1, 0, 0.f, 0.f};
-            if (todo) load_k(__shfl_sync(0xffffffffu, cur.id, __ffs(todo) - 1), 0);
-            while (todo) {
-                const int src = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int id = __shfl_sync(0xffffffffu, cur.id, src);
-                // (blk * 64 < lim_max <= 2^31 - 1)
-                const int key0 = __shfl_sync(0xffffffffu, cur.blk, src) * kPage;
-                const float ks = __shfl_sync(0xffffffffu, cur.ks, src);
-                const float vs = __shfl_sync(0xffffffffu, cur.vs, src);
-                const int id_next = todo ? __shfl_sync(0xffffffffu, cur.id, __ffs(todo) - 1) : -1;
-                const bool masked = lim_min - key0 < kPage;
-                if (fabsf(vs) > 2.f * r_ref) {
-                    const float b = r_ref / fabsf(vs);
-                    r_ref = fabsf(vs);
+                        for (int rr = 0; rr < 2; ++rr)
+                            kr[i][rr] = *reinterpret_cast<const uint4 *>(pk + (16 * i + 8 * rr) * D + k_off[c]);
 #pragma unroll
-                    for (int j = 0; j < NC; ++j)
+                    for (int w = 0; w < 4; ++w) {
+                        uint2 qf[NC];
 #pragma unroll
-                        for (int i = 0; i < MT; ++i)
+                        for (int j = 0; j < NC; ++j) qf[j] = s_q[(j * KS + c * 4 + w) * 32 + lane];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[j][i][e] *= b;
-                }
-                const float f = r_ref > 0.f ? vs / r_ref : 0.f;
-                float l_page[NC][2];
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t lo = word(kr[i][0], w) ^ 0x80808080u, hi = word(kr[i][1], w) ^ 0x80808080u;
+                            const uint32_t a0 = codes_lo(lo), a1 = codes_lo(hi), a2 = codes_hi(lo), a3 = codes_hi(hi);
 #pragma unroll
-                for (int j = 0; j < NC; ++j) l_page[j][0] = l_page[j][1] = 0.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // V of these 32 keys: rows 16i + 2t + {0, 1, 8, 9}
-                    uint32_t vr[2][4][VW];
-                    {
-                        const int8_t *base =
-                            a.v + static_cast<int64_t>(id) * (kPage * D) + (32 * h + 2 * t) * D + (D / 8) * g;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int rr = 0; rr < 4; ++rr) {
-                                const int8_t *p = base + (16 * i + (rr & 1) + 8 * (rr >> 1)) * D;
-                                if constexpr (VW == 4) {
-                                    const uint4 x = ld_stream16(p);
-                                    vr[i][rr][0] = x.x;
-                                    vr[i][rr][1] = x.y;
-                                    vr[i][rr][2] = x.z;
-                                    vr[i][rr][3] = x.w;
-                                } else {
-                                    const uint2 x = ld_stream8(p);
-                                    vr[i][rr][0] = x.x;
-                                    vr[i][rr][1] = x.y;
-                                }
-                            }
-                    }
-                    // S = K Q^T
-                    float s[NC][2][4];
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[j][i][e] = 0.f;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint2 qf[NC];
-#pragma unroll
-                            for (int j = 0; j < NC; ++j) qf[j] = s_q[(j * KS + c * 4 + w) * 32 + lane];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t x = word(kr[i][0][c], w) ^ 0x80808080u;
-                                const uint32_t y = word(kr[i][1][c], w) ^ 0x80808080u;
-                                const uint32_t a0 = codes_lo(x), a1 = codes_lo(y), a2 = codes_hi(x), a3 = codes_hi(y);
-#pragma unroll
-                                for (int j = 0; j < NC; ++j) mma_16816(s[j][i], a0, a1, a2, a3, qf[j].x, qf[j].y);
+                            for (int j = 0; j < NC; ++j) {
+                                if (c == 0 && w == 0) mma_16816_from0(s[j][i], a0, a1, a2, a3, qf[j].x, qf[j].y);
+                                else mma_16816(s[j][i], a0, a1, a2, a3, qf[j].x, qf[j].y);
                             }
                         }
-                    // the next 32 keys' K
-                    if (h == 0) load_k(id, 1);
-                    else if (id_next >= 0) load_k(id_next, 0);
-
-                    uint32_t bh[NC][2][2], bl[NC][2][2];
+                    }
+                }
+                if (meta.ks < 0.f || masked) {
 #pragma unroll
-                    for (int j = 0; j < NC; ++j) {
+                    for (int j = 0; j < NC; ++j)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                s[j][i][e] *= ks;
-                                if (masked && 32 * h + 16 * i + 8 * (e >> 1) + g >= lim[j][e & 1] - key0)
-                                    s[j][i][e] = -INFINITY;
+                                if (meta.ks < 0.f) s[j][i][e] = -s[j][i][e];
+                                if (16 * i + 8 * (e >> 1) + rg_ >= lim[j][e & 1] - key0) s[j][i][e] = -INFINITY;
                             }
-                        float top[2];
+                }
+                float l_step[NC][2];
+                uint32_t bh[NC][2][2], bl[NC][2][2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            top[e] = fmaxf(fmaxf(s[j][0][e], s[j][0][e + 2]), fmaxf(s[j][1][e], s[j][1][e + 2]));
-                        // m_ref + kGrow is -inf at first, and then any score moves it
-                        if (__any_sync(0xffffffffu, top[0] > m_ref[j][0] + kGrow || top[1] > m_ref[j][1] + kGrow)) {
+                for (int j = 0; j < NC; ++j) {
+                    // largest scores, in log2 units
+                    float top[2];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float x = top[e];
+                    for (int e = 0; e < 2; ++e)
+                        top[e] = fmaxf(fmaxf(s[j][0][e], s[j][0][e + 2]), fmaxf(s[j][1][e], s[j][1][e + 2])) * ks;
+                    // m_ref + kGrow is -inf at first, and then any score moves it
+                    if (__any_sync(0xffffffffu, top[0] > m_ref[j][0] + kGrow || top[1] > m_ref[j][1] + kGrow)) {
 #pragma unroll
-                                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                                if (x > m_ref[j][e] + kGrow) {
-                                    const float b = fast_exp2(m_ref[j][e] - x);
-                                    m_ref[j][e] = x;
-                                    l_sum[j][e] *= b;
-                                    l_page[j][e] *= b;
+                        for (int e = 0; e < 2; ++e) {
+                            float y = top[e];
 #pragma unroll
-                                    for (int i = 0; i < MT; ++i) {
-                                        acc[j][i][e] *= b;
-                                        acc[j][i][e + 2] *= b;
-                                    }
+                            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+                            if (y > m_ref[j][e] + kGrow) {
+                                const float b = fast_exp2(m_ref[j][e] - y);
+                                m_ref[j][e] = y;
+                                l_sum[j][e] *= b;
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) {
+                                    acc[j][i][e] *= b;
+                                    acc[j][i][e + 2] *= b;
                                 }
                             }
                         }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                float w[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float off = m_ref[j][e] == -INFINITY ? 0.f : kShift - m_ref[j][e];
-                                    const float p = fast_exp2(s[j][i][half * 2 + e] + off);
-                                    l_page[j][e] += p;
-                                    w[e] = p * f;
-                                }
-                                const uint32_t hw = pack_half2(w[0], w[1]);
-                                bh[j][i][half] = movmatrix_trans(hw);
-                                if (HILO) {
-                                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
-                                    bl[j][i][half] = movmatrix_trans(pack_half2(w[0] - back.x, w[1] - back.y));
-                                }
-                            }
                     }
-                    // O^T += V^T P^T
+                    float off[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        off[e] = m_ref[j][e] == -INFINITY ? 0.f : kShift - m_ref[j][e];
+                        l_step[j][e] = 0.f;
+                    }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int rr = 0; rr < 4; ++rr) x[rr] = vr[i][rr][w] ^ 0x80808080u;
+                        for (int half = 0; half < 2; ++half) {
+                            float w[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                // channels (D/8) g + 4w + 2e (m = g) and + 1 (m = g + 8)
-                                const uint32_t p01 = __byte_perm(x[0], x[1], e ? 0x7362 : 0x5140);
-                                const uint32_t p89 = __byte_perm(x[2], x[3], e ? 0x7362 : 0x5140);
-                                const uint32_t a0 = codes_lo(p01), a1 = codes_hi(p01);
-                                const uint32_t a2 = codes_lo(p89), a3 = codes_hi(p89);
-#pragma unroll
-                                for (int j = 0; j < NC; ++j) {
-                                    mma_16816(acc[j][2 * w + e], a0, a1, a2, a3, bh[j][i][0], bh[j][i][1]);
-                                    if (HILO) mma_16816(acc[j][2 * w + e], a0, a1, a2, a3, bl[j][i][0], bl[j][i][1]);
-                                }
+                                w[e] = fast_exp2(fmaf(s[j][i][half * 2 + e], ks, off[e]));
+                                l_step[j][e] += w[e];
+                            }
+                            const uint32_t hw = pack_half2(w[0], w[1]);
+                            bh[j][i][half] = movmatrix_trans(hw);
+                            if (HILO) {
+                                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
+                                bl[j][i][half] = movmatrix_trans(pack_half2(w[0] - back.x, w[1] - back.y));
                             }
                         }
-                }
-#pragma unroll
-                for (int j = 0; j < NC; ++j) {
-                    l_sum[j][0] += l_page[j][0];
-                    l_sum[j][1] += l_page[j][1];
+                    l_sum[j][0] += l_step[j][0];
+                    l_sum[j][1] += l_step[j][1];
                 }
                 if (a.page_lse) {
-                    const int p = first + kDecodeWarps * src;
 #pragma unroll
                     for (int j = 0; j < NC; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float x = l_page[j][e];
+                            float y = l_step[j][e];
 #pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                            for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
                             const int row = row0 + j * 8 + 2 * t + e;
-                            if (g == 0 && row < a.rows) {
-                                const int64_t rr = a.sel ? (at.list % a.nq) * a.G + row : row;
-                                a.page_lse[((static_cast<int64_t>(seq) * a.L.Hk + kh) * a.nq * a.G + rr) * a.page_ld + p] =
-                                    x > 0.f ? m_ref[j][e] - kShift + log2f(x) : -INFINITY;
-                            }
+                            if (g == 0 && row < a.rows)
+                                page_lse(row)[2 * p + h] = y > 0.f ? m_ref[j][e] - kShift + log2f(y) : -INFINITY;
                         }
                 }
+                // O^T += d_v V^T P^T: 32 keys' sums from zero, then one fp32 addition.
+                // B's rows 2t, 2t+1 (+ 8) are keys r(2t), r(2t+1) (+ 8).
+                uint32_t vr[2][4][VW];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int rr = 0; rr < 4; ++rr) {
+                        const uint8_t *src = pv + (16 * i + 8 * (rr >> 1)) * D + v_off[rr & 1];
+                        if constexpr (VW == 4) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(src);
+                            vr[i][rr][0] = y.x;
+                            vr[i][rr][1] = y.y;
+                            vr[i][rr][2] = y.z;
+                            vr[i][rr][3] = y.w;
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2 *>(src);
+                            vr[i][rr][0] = y.x;
+                            vr[i][rr][1] = y.y;
+                        }
+                    }
+                __syncwarp();                       // the slot is read
+                if (lane == 0) tc::mbar_arrive(bar0 + 8 * (NS + slot));
+#pragma unroll
+                for (int w = 0; w < VW; ++w)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // channels (D/8) p(g) + 4w + 2e (m = g) and + 1 (m = g + 8)
+                        float y[NC][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t p01 = __byte_perm(vr[i][0][w], vr[i][1][w], e ? 0x7362 : 0x5140) ^ 0x80808080u;
+                            const uint32_t p89 = __byte_perm(vr[i][2][w], vr[i][3][w], e ? 0x7362 : 0x5140) ^ 0x80808080u;
+                            const uint32_t a0 = codes_lo(p01), a1 = codes_hi(p01);
+                            const uint32_t a2 = codes_lo(p89), a3 = codes_hi(p89);
+#pragma unroll
+                            for (int j = 0; j < NC; ++j) {
+                                if (i == 0) mma_16816_from0(y[j], a0, a1, a2, a3, bh[j][i][0], bh[j][i][1]);
+                                else mma_16816(y[j], a0, a1, a2, a3, bh[j][i][0], bh[j][i][1]);
+                                if (HILO) mma_16816(y[j], a0, a1, a2, a3, bl[j][i][0], bl[j][i][1]);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < NC; ++j)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) acc[j][2 * w + e][c] = fmaf(vs, y[j][c], acc[j][2 * w + e][c]);
+                    }
             }
-            cur = nxt;
-            first = next_first;
         }
+        n_taken = n_end;
 
         // ---- the warps' results together, eight columns at a time ---------------
-        const bool whole = pg0 == 0 && pg1 == at.np;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (pos == pos0 ? 0 : 1);
+        const bool whole = x.pg0 == 0 && x.pg1 == at.np;
+        const int64_t slot_out = 2 * static_cast<int64_t>(blockIdx.x) + (pos == pos0 ? 0 : 1);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            __syncthreads();                        // the buffers of the last round are read
+            if (j > 0) sync_all();                  // the buffers of the last round are read
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float x = l_sum[j][e];
+                float y = l_sum[j][e];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
                 if (g == 0) {
                     s_ml[warp][2 * t + e][0] = m_ref[j][e];
-                    s_ml[warp][2 * t + e][1] = x;
+                    s_ml[warp][2 * t + e][1] = y;
                 }
 #pragma unroll
-                for (int i = 0; i < MT; ++i)        // channels (D/8) g + 2i, + 1
-                    *reinterpret_cast<float2 *>(&s_o[warp][2 * t + e][(D / 8) * g + 2 * i]) =
-                        make_float2(acc[j][i][e] * r_ref, acc[j][i][e + 2] * r_ref);
+                for (int i = 0; i < MT; ++i)        // channels (D/8) p(g) + 2i, + 1
+                    *reinterpret_cast<float2 *>(&s_o[warp][2 * t + e][(D / 8) * rg_ + 2 * i]) =
+                        make_float2(acc[j][i][e], acc[j][i][e + 2]);
             }
-            __syncthreads();
-#pragma unroll
-            for (int it = 0; it < 8 * D / kThreads; ++it) {
-                const int c = (it * kThreads + tid) / D, d = (it * kThreads + tid) % D;
+            sync_all();
+            for (int i = tid; i < 8 * D; i += kConsumers) {
+                const int c = i / D, d = i % D;
                 const int row = row0 + j * 8 + c;
                 if (row >= a.rows) continue;
                 float M = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, s_ml[w][c][0]);
+                for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][c][0]);
                 float Lw = 0.f, O = 0.f;
                 if (M != -INFINITY) {
 #pragma unroll
-                    for (int w = 0; w < kDecodeWarps; ++w) {
+                    for (int w = 0; w < W; ++w) {
                         const float b = fast_exp2(s_ml[w][c][0] - M);
                         Lw = fmaf(b, s_ml[w][c][1], Lw);
                         O = fmaf(b, s_o[w][c][d], O);
@@ -472,38 +564,38 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
                     else static_cast<float *>(a.o)[r * D + d] = v;
                     if (d == 0) a.lse[r] = Lw > 0.f ? (M - kShift + log2f(Lw)) * 0.6931471805599453f : -INFINITY;
                 } else {
-                    a.part_o[(slot * (8 * NC) + j * 8 + c) * D + d] = O;
+                    a.part_o[(slot_out * (8 * NC) + j * 8 + c) * D + d] = O;
                     if (d == 0) {
-                        a.part_ml[(slot * (8 * NC) + j * 8 + c) * 2] = M;
-                        a.part_ml[(slot * (8 * NC) + j * 8 + c) * 2 + 1] = Lw;
+                        a.part_ml[(slot_out * (8 * NC) + j * 8 + c) * 2] = M;
+                        a.part_ml[(slot_out * (8 * NC) + j * 8 + c) * 2 + 1] = Lw;
                     }
                 }
             }
         }
         if (!whole) {
             // ---- the last CTA of the unit puts the pieces together, in order -----
-            const int64_t u = at.list * mult + u_in;
-            const int64_t c_lo = unit0 / chunk, c_hi = (unit0 + at.np - 1) / chunk;
+            const int64_t u = at.list * mult + x.u_in;
+            const int64_t c_lo = x.unit0 / chunk, c_hi = (x.unit0 + at.np - 1) / chunk;
             __threadfence();
-            __syncthreads();
+            sync_all();
             if (tid == 0) s_last = atomicAdd(a.counters + u, 1) == static_cast<int>(c_hi - c_lo);
-            __syncthreads();
+            sync_all();
             if (s_last) {
                 __threadfence();
-                auto slot_of = [&](int64_t c) { return 2 * c + (c == c_lo && unit0 > c * chunk ? 1 : 0); };
-                for (int e = tid; e < 8 * NC * (D / 4); e += kThreads) {
+                auto slot_of = [&](int64_t c) { return 2 * c + (c == c_lo && x.unit0 > c * chunk ? 1 : 0); };
+                for (int e = tid; e < 8 * NC * (D / 4); e += kConsumers) {
                     const int c = e / (D / 4), d4 = e % (D / 4);
                     const int row = row0 + c;
                     if (row >= a.rows) continue;
                     float M = -INFINITY;
-                    for (int64_t x = c_lo; x <= c_hi; ++x)
-                        M = fmaxf(M, __ldcg(a.part_ml + (slot_of(x) * (8 * NC) + c) * 2));
+                    for (int64_t y = c_lo; y <= c_hi; ++y)
+                        M = fmaxf(M, __ldcg(a.part_ml + (slot_of(y) * (8 * NC) + c) * 2));
                     float Ls = 0.f;
                     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (M != -INFINITY) {
 #pragma unroll 8
-                        for (int64_t x = c_lo; x <= c_hi; ++x) {
-                            const int64_t sl = slot_of(x) * (8 * NC) + c;
+                        for (int64_t y = c_lo; y <= c_hi; ++y) {
+                            const int64_t sl = slot_of(y) * (8 * NC) + c;
                             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + sl);
                             const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + sl * D) + d4);
                             const float b = fast_exp2(ml.x - M);
@@ -531,12 +623,12 @@ __global__ void __launch_bounds__(kThreads, NC == 2 ? 2 : kDecodeCtas) decode_ke
                 if (tid == 0) a.counters[u] = 0;
             }
         }
-        pos = unit0 + pg1;
+        pos = x.unit0 + x.pg1;
     }
 }
 
-// Attention weight of each page from its log sums: mass += sum over rows of
-// 2^(page - row).  Rows are added in their order.
+// Attention weight of each page from its halves' log sums: mass += sum over rows
+// of 2^(half page - row).  Rows are added in their order.
 __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass)
 {
     const int kh = blockIdx.y, s = blockIdx.z;
@@ -555,8 +647,8 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass
 #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
             const float z = lse2(r);
-            const float x = __ldcg(pl + r * a.page_ld + p);
-            sum += z == -INFINITY ? 0.f : fast_exp2(x - z);
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(pl + r * a.page_ld) + p);
+            sum += z == -INFINITY ? 0.f : fast_exp2(x.x - z) + fast_exp2(x.y - z);
         }
         out[p] += sum;
         return;
@@ -571,8 +663,8 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass
             float sum = 0.f;
             for (int g = 0; g < a.G; ++g) {
                 const float z = lse2(t * a.G + g);
-                const float x = __ldcg(pl + (t * a.G + g) * a.page_ld + i);
-                sum += z == -INFINITY ? 0.f : fast_exp2(x - z);
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(pl + (t * a.G + g) * a.page_ld) + i);
+                sum += z == -INFINITY ? 0.f : fast_exp2(x.x - z) + fast_exp2(x.y - z);
             }
             if (sum > 0.f) atomicAdd(out + blk, sum);
         }
@@ -587,28 +679,56 @@ int launch_mass(skv_handle *h, const AttnArgs &a, float *mass, cudaStream_t st)
     return cuda_fail(h, cudaGetLastError(), "page weight launch");
 }
 
-template <int D>
-static void launch_decode_d(const AttnArgs &a, bool f16, int grid, int nc, cudaStream_t st)
+int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pages, int D, int rows)
 {
-    // One column group always takes both parts of the weights (its products are
-    // a small part of a page's time); more of them only when o is fp32.
-    if (nc == 1) {
-        if (f16) decode_kernel<D, 1, true, true><<<grid, kThreads, 0, st>>>(a);
-        else decode_kernel<D, 1, true, false><<<grid, kThreads, 0, st>>>(a);
-    } else {
-        if (f16) decode_kernel<D, 2, false, true><<<grid, kThreads, 0, st>>>(a);
-        else decode_kernel<D, 2, true, false><<<grid, kThreads, 0, st>>>(a);
-    }
+    tc::EncodeTiledFn fn = tc::encode_fn();
+    if (!fn) return fail(h, SKV_ECUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), kPage, static_cast<cuuint64_t>(n_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(D) * kPage};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(pages), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(h, SKV_EUNSUPPORTED, "tensor map encoding failed (%d)", static_cast<int>(r));
+    return SKV_OK;
 }
 
-int launch_decode(skv_handle *h, const AttnArgs &a, int D, bool f16, int grid, int nc, cudaStream_t st)
+template <int D, int NC, bool HILO, bool F16>
+static int launch_one(skv_handle *h, const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int grid,
+                      cudaStream_t st)
 {
+    static KernelAttrCache cache;
+    constexpr int smem = decode_smem<D, NC>();
+    const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(decode_kernel<D, NC, HILO, F16>), smem,
+                                            warps_of(NC) * 32 + 32, nullptr);
+    if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(8-bit decode)");
     if (h->prof_before) cudaEventRecord(h->prof_before, st);
-    if (D == 128) launch_decode_d<128>(a, f16, grid, nc, st);
-    else launch_decode_d<64>(a, f16, grid, nc, st);
-    const cudaError_t e = cudaGetLastError();
+    decode_kernel<D, NC, HILO, F16><<<grid, warps_of(NC) * 32 + 32, smem, st>>>(mk, mv, a);
+    const cudaError_t l = cudaGetLastError();
     if (h->prof_after) cudaEventRecord(h->prof_after, st);
-    return cuda_fail(h, e, "8-bit decode launch");
+    return cuda_fail(h, l, "8-bit decode launch");
+}
+
+template <int D>
+static int launch_d(skv_handle *h, const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, bool f16, int grid,
+                    int nc, cudaStream_t st)
+{
+    // One column group always takes both parts of the weights (its products are
+    // a small part of a page's time); two of them only when o is fp32.
+    if (nc == 1)
+        return f16 ? launch_one<D, 1, true, true>(h, mk, mv, a, grid, st)
+                   : launch_one<D, 1, true, false>(h, mk, mv, a, grid, st);
+    return f16 ? launch_one<D, 2, false, true>(h, mk, mv, a, grid, st)
+               : launch_one<D, 2, true, false>(h, mk, mv, a, grid, st);
+}
+
+int launch_decode(skv_handle *h, const AttnArgs &a, int64_t n_pages, int D, bool f16, int grid, int nc, cudaStream_t st)
+{
+    CUtensorMap mk, mv;
+    int rc = page_map(h, &mk, a.k, n_pages, D, kPage);
+    if (rc || (rc = page_map(h, &mv, a.v, n_pages, D, kPage))) return rc;
+    return D == 128 ? launch_d<128>(h, mk, mv, a, f16, grid, nc, st) : launch_d<64>(h, mk, mv, a, f16, grid, nc, st);
 }
 
 }  // namespace q8
