@@ -32,7 +32,8 @@ struct AttnArgs {
     const int32_t *q_pos;          // [S][nq] or null
     const int32_t *sel;            // [S][nq][Hk][n_sel] or null
     int n_sel;
-    int nq, H, G;
+    int nq, H, G;                  // nq: tokens of this launch
+    int nq_ld, tok0;               // tokens a sequence in q, q_pos, sel, o and lse; the first of this launch
     int rows;                      // query rows of one unit: nq * G, or G with sel
     int row_groups;                // units per (list, KV head)
     float scale_log2;              // scale * log2(e)
@@ -44,6 +45,9 @@ struct AttnArgs {
     int *counters;                 // arrivals, zero between launches
     float *page_lse;               // mass: [S][Hk][nq * G][page_ld] log2 sums of half pages, or null
     int64_t page_ld;               // 2 cap, or 2 n_sel with sel
+
+    // Index of token t of sequence s in q, q_pos, o and lse.
+    __host__ __device__ int64_t token(int s, int t) const { return static_cast<int64_t>(s) * nq_ld + tok0 + t; }
 };
 
 // Tokens of sequence s that its list can hold.
@@ -122,6 +126,8 @@ int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pag
 constexpr int kPieceMin = 8;
 int launch_decode(skv_handle *h, const AttnArgs &a, int64_t n_pages, int D, bool out_f16, int grid, int nc,
                   cudaStream_t st);
+int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool out_f16, int64_t *plan, int n_pairs, float *mass,
+                   int grid, cudaStream_t st);
 int launch_mass(skv_handle *h, const AttnArgs &a, float *mass, cudaStream_t st);
 int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_max, int x_type, const void *k_new,
                   const void *v_new, const int32_t *n_new, cudaStream_t st);

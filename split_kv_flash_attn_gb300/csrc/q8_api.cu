@@ -21,6 +21,14 @@ struct OnDevice {
     }
 };
 
+// Query rows of a KV head from which the tensor-core kernel serves.
+#ifndef VTC
+#define VTC 33
+#endif
+constexpr int kTcRows = VTC;
+// Scratch for the pages' log sums of one launch.
+constexpr int64_t kMassScratch = int64_t(256) << 20;
+
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 static int check_pool(skv_handle *h, const skv_q8_pool *p)
@@ -121,34 +129,61 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     a.q_pos = q_pos;
     a.sel = sel;
     a.n_sel = sel ? n_sel : 0;
-    a.nq = shape->nq;
+    a.nq_ld = shape->nq;
     a.H = shape->H;
     a.G = shape->H / shape->Hk;
     a.scale_log2 = shape->scale * 1.4426950408889634f;
     a.o = o;
     a.lse = lse;
     a.counters = h->counters;
-    const int64_t n_lists = sel ? static_cast<int64_t>(shape->S) * shape->nq : shape->S;
-    a.rows = sel ? a.G : shape->nq * a.G;
-    const int nc = a.rows <= 8 ? 1 : 2;
-    a.row_groups = (a.rows + 8 * nc - 1) / (8 * nc);
-    const int64_t units = n_lists * shape->Hk * a.row_groups;
-    if (units > kMaxUnits)
-        return fail(h, SKV_EUNSUPPORTED, "%lld (list, KV head, row group) units exceed %d", (long long)units, kMaxUnits);
+    const bool f16 = o_type == SKV_F16;
+    // Rows of a KV head: the tensor-core kernel takes 256 at a time, the decode
+    // kernel 8 or 16.
+    const bool tc = !sel && static_cast<int64_t>(shape->nq) * a.G >= kTcRows;
+    // Tokens of one launch: as many as the kernels' counters have units for, and as
+    // keep the pages' log sums within kMassScratch (at least one).
+    const int64_t heads = static_cast<int64_t>(shape->S) * shape->Hk;
+    int64_t nq_max = shape->nq;
+    const int rows1 = sel ? a.G : 0;                      // rows of a unit that do not grow with the tokens
+    const int nc = (sel ? a.G : static_cast<int64_t>(shape->nq) * a.G) <= 8 ? 1 : 2;
+    const int64_t unit_rows = tc ? 256 : 8 * nc;
+    if (sel) nq_max = std::min(nq_max, kMaxUnits / std::max<int64_t>(1, heads * ((a.G + unit_rows - 1) / unit_rows)));
+    else nq_max = std::min(nq_max, (kMaxUnits / heads) * unit_rows / a.G);
+    const int64_t per_list = sel ? n_sel : pages_per_list;
+    if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kMassScratch / (heads * a.G * per_list * 8)));
+    if (nq_max < 1)
+        return fail(h, SKV_EUNSUPPORTED, "S*Hk = %lld lists with %d query heads each exceed %d units", (long long)heads, a.G, kMaxUnits);
+    a.nq = static_cast<int>(nq_max);
+    a.rows = sel ? rows1 : a.nq * a.G;
+    a.row_groups = static_cast<int>((a.rows + unit_rows - 1) / unit_rows);
+    const int64_t units = (sel ? heads * a.nq : heads) * a.row_groups;
     // one CTA a SM, but no more than pieces of kPieceMin pages
-    const int64_t most = units * (sel ? n_sel : pages_per_list);
-    const int grid = static_cast<int>(std::min<int64_t>(h->sm_count, (most + kPieceMin - 1) / kPieceMin));
-    const size_t po = round256(static_cast<size_t>(2) * grid * 8 * nc * D * sizeof(float));
-    const size_t pm = round256(static_cast<size_t>(2) * grid * 8 * nc * 2 * sizeof(float));
-    a.page_ld = 2 * (sel ? static_cast<int64_t>(n_sel) : pages_per_list);
-    const size_t pl = mass ? static_cast<size_t>(shape->S) * shape->nq * shape->H * a.page_ld * sizeof(float) : 0;
-    if ((rc = ensure_workspace(h, po + pm + pl, st))) return rc;
+    const int64_t pieces = tc ? (units * per_list + 1) / 2 : (units * per_list + kPieceMin - 1) / kPieceMin;
+    const int grid = static_cast<int>(std::min<int64_t>(h->sm_count, pieces));
+    const size_t po = round256(static_cast<size_t>(2) * grid * unit_rows * D * sizeof(float));
+    const size_t pm = round256(static_cast<size_t>(2) * grid * unit_rows * 2 * sizeof(float));
+    const size_t pp = tc ? round256((static_cast<size_t>(shape->S) * a.row_groups + 1) * sizeof(int64_t)) : 0;
+    const size_t pl = mass ? static_cast<size_t>(heads) * a.nq * a.G * per_list * (tc ? 4 : 8) : 0;
+    if ((rc = ensure_workspace(h, po + pm + pp + pl, st))) return rc;
     uint8_t *ws = static_cast<uint8_t *>(h->workspace);
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_ml = reinterpret_cast<float *>(ws + po);
-    a.page_lse = mass ? reinterpret_cast<float *>(ws + po + pm) : nullptr;
-    if ((rc = launch_decode(h, a, pool->n_pages, D, o_type == SKV_F16, grid, nc, st))) return rc;
-    return mass ? launch_mass(h, a, mass, st) : SKV_OK;
+    a.page_ld = 2 * per_list;
+    a.page_lse = mass ? reinterpret_cast<float *>(ws + po + pm + pp) : nullptr;
+    for (int t = 0; t < shape->nq; t += static_cast<int>(nq_max)) {
+        a.tok0 = t;
+        a.nq = static_cast<int>(std::min<int64_t>(nq_max, shape->nq - t));
+        if (!sel) a.rows = a.nq * a.G;
+        a.row_groups = static_cast<int>((a.rows + unit_rows - 1) / unit_rows);
+        if (tc) {
+            rc = launch_prefill(h, a, D, f16, reinterpret_cast<int64_t *>(ws + po + pm), a.row_groups, mass, grid, st);
+        } else {
+            rc = launch_decode(h, a, pool->n_pages, D, f16, grid, nc, st);
+            if (!rc && mass) rc = launch_mass(h, a, mass, st);
+        }
+        if (rc) return rc;
+    }
+    return SKV_OK;
 }
 
 int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,

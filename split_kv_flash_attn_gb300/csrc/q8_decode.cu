@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     if (!a.sel) {
         for (int i = blockIdx.x; i < n_lists; i += gridDim.x) {
             if (pages_of(a, i) != 0) continue;
-            const int64_t r0 = static_cast<int64_t>(i) * a.nq * a.H, nr = static_cast<int64_t>(a.nq) * a.H;
+            const int64_t r0 = a.token(i, 0) * a.H, nr = static_cast<int64_t>(a.nq) * a.H;
             for (int64_t e = tid; e < nr * D; e += kThreads) {
                 if (F16) static_cast<__half *>(a.o)[r0 * D + e] = __float2half(0.f);
                 else static_cast<float *>(a.o)[r0 * D + e] = 0.f;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         x.kh = static_cast<int>(x.u_in / a.row_groups);
         x.rg = static_cast<int>(x.u_in - static_cast<int64_t>(x.kh) * a.row_groups);
         x.seq = a.sel ? at.list / a.nq : at.list;
-        x.tok0 = a.sel ? at.list : static_cast<int64_t>(at.list) * a.nq;
+        x.tok0 = a.sel ? a.token(x.seq, at.list % a.nq) : a.token(at.list, 0);
         return x;
     };
     // A phase already complete is taken at once; the abort flag is read only
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
             const Unit x = unit_at(pos);
             const int len = static_cast<int>(list_len(a.L, x.seq));
             const int32_t *ids = a.L.ids + (static_cast<int64_t>(x.seq) * a.L.Hk + x.kh) * a.L.cap;
-            const int32_t *sel = a.sel ? a.sel + (static_cast<int64_t>(at.list) * a.L.Hk + x.kh) * a.n_sel : nullptr;
+            const int32_t *sel = a.sel ? a.sel + (x.tok0 * a.L.Hk + x.kh) * a.n_sel : nullptr;
             int lim = len;                          // keys that any row of the unit sees
             if (a.q_pos) {
                 const int row = x.rg * 8 * NC + lane;
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass
     const float *pl = a.page_lse + unit * rows * a.page_ld;
     float *out = mass + unit * a.L.cap;
     auto lse2 = [&](int r) {
-        return a.lse[(static_cast<int64_t>(s) * a.nq + r / a.G) * a.H + kh * a.G + r % a.G] * 1.4426950408889634f;
+        return a.lse[a.token(s, r / a.G) * a.H + kh * a.G + r % a.G] * 1.4426950408889634f;
     };
     if (!a.sel) {
         const int64_t p = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass
     // with a selection: token by token (a token's pages are different ones, or
     // the same page with the same weight: the order of their additions is free)
     for (int t = 0; t < a.nq; ++t) {
-        const int32_t *sel = a.sel + ((static_cast<int64_t>(s) * a.nq + t) * a.L.Hk + kh) * a.n_sel;
+        const int32_t *sel = a.sel + (a.token(s, t) * a.L.Hk + kh) * a.n_sel;
         for (int i = threadIdx.x; i < a.n_sel; i += 128) {
             const int64_t blk = sel[i];
             if (blk < 0 || blk * kPage >= len) continue;

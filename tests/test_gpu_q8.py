@@ -129,7 +129,44 @@ def test_attention(h, lens, nq, H, Hk, D, causal, f16):
     assert h.status() == 0
 
 
-def test_attention_absent_pages_and_far_scales(h):
+# many rows a KV head: tiles of 128 rows in pairs, the last pair of some with one
+PREFILL = [
+    ([64], 33, 1, 1, 128, False), ([300], 64, 8, 2, 64, True), ([1000, 0, 300], 150, 8, 2, 128, True),
+    ([700, 20], 33, 16, 1, 128, False), ([2000], 70, 40, 8, 64, True), ([5000, 129], 64, 8, 4, 128, True),
+    ([40], 100, 6, 2, 128, True), ([260] * 9, 72, 4, 1, 64, False),
+]
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("lens,nq,H,Hk,D,causal", PREFILL)
+def test_attention_many_rows(h, lens, nq, H, Hk, D, causal, f16):
+    test_attention(h, lens, nq, H, Hk, D, causal, f16)
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_many_rows_any_positions(h, f16):
+    """Query positions in no order, beyond the keys and before them; absent pages."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(41)
+    c = u.Cache(rng, [900, 130], 2, 128)
+    c.ids[0, 0, 5] = -1
+    c.ids[0, 1, 0] = c.ids[0, 1, 1] = -1
+    c.ids[1, 0, :3] = -1                              # nothing at all for this head
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 2, 90, 8, 128)
+    q_pos = rng.integers(-50, 1100, (2, 90)).astype(np.int32)
+    ref = u.attention(c, q, q_pos=q_pos)
+    mass = torch.zeros((2, 2, c.cap), device="cuda")
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(q_pos), mass=mass, o_dtype=torch.float16 if f16 else None)
+    u.check(o, lse, ref, f16=f16)
+    tol = (ref[3] / (2 * ref[5]) + 2.0 ** -20) * 90 * 4
+    assert np.abs(mass.double().cpu().numpy() - ref[2]).max() <= tol
+    assert h.status() == 0
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_absent_pages_and_far_scales(h, nq):
     """Padding inside a list, scales that differ by 2^40 and zero scales, large scores."""
     import torch
     import split_kv_flash_attn_gb300 as skv
@@ -142,13 +179,15 @@ def test_attention_absent_pages_and_far_scales(h):
     c.vs[c.ids[1, 0, 0]] = 0.0
     c.ks[c.ids[1, 1, 4]] = 0.0
     c.ks[c.ids[1, 0, 2]] *= 20
+    c.ks[c.ids[0, 0, 1]] *= -1                        # the pool's scales may have either sign
+    c.vs[c.ids[0, 1, 2]] *= -1
     pool, ids, kv_len = c.on_gpu()
-    q = _q(rng, 3, 1, 8, 128)
+    q = _q(rng, 3, nq, 8, 128)
     mass = torch.zeros((3, 2, c.cap), device="cuda")
     o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, mass=mass)
     ref = u.attention(c, q)
     u.check(o, lse, ref)
-    assert np.array_equal(mass.cpu().numpy() == 0, ref[2] == 0)
+    assert np.array_equal(mass.cpu().numpy() == 0, ref[2] < 2.0 ** -100)
     assert h.status() == 0
 
 
