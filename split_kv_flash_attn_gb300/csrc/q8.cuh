@@ -126,7 +126,7 @@ int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pag
 constexpr int kPieceMin = 8;
 int launch_decode(skv_handle *h, const AttnArgs &a, int64_t n_pages, int D, bool out_f16, int grid, int nc,
                   cudaStream_t st);
-int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool out_f16, int64_t *plan, int n_pairs, float *mass,
+int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool out_f16, uint32_t *plan, int n_pairs, float *mass,
                    int grid, cudaStream_t st);
 int launch_mass(skv_handle *h, const AttnArgs &a, float *mass, cudaStream_t st);
 int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_max, int x_type, const void *k_new,

@@ -150,9 +150,15 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     if (sel) nq_max = std::min(nq_max, kMaxUnits / std::max<int64_t>(1, heads * ((a.G + unit_rows - 1) / unit_rows)));
     else nq_max = std::min(nq_max, (kMaxUnits / heads) * unit_rows / a.G);
     const int64_t per_list = sel ? n_sel : pages_per_list;
+    if (tc) {
+        // the tensor-core kernel counts key tiles of a launch in 32 bits
+        const int64_t pairs = std::min<int64_t>(INT32_MAX, (int64_t(1) << 31) / (heads * ((pages_per_list + 1) / 2)));
+        nq_max = std::min(nq_max, pairs * unit_rows / a.G);
+    }
     if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kMassScratch / (heads * a.G * per_list * 8)));
     if (nq_max < 1)
-        return fail(h, SKV_EUNSUPPORTED, "S*Hk = %lld lists with %d query heads each exceed %d units", (long long)heads, a.G, kMaxUnits);
+        return fail(h, SKV_EUNSUPPORTED, "S*Hk = %lld lists of %lld pages with %d query heads each are too many for one launch",
+                    (long long)heads, (long long)pages_per_list, a.G);
     a.nq = static_cast<int>(nq_max);
     a.rows = sel ? rows1 : a.nq * a.G;
     a.row_groups = static_cast<int>((a.rows + unit_rows - 1) / unit_rows);
@@ -162,7 +168,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     const int grid = static_cast<int>(std::min<int64_t>(h->sm_count, pieces));
     const size_t po = round256(static_cast<size_t>(2) * grid * unit_rows * D * sizeof(float));
     const size_t pm = round256(static_cast<size_t>(2) * grid * unit_rows * 2 * sizeof(float));
-    const size_t pp = tc ? round256((static_cast<size_t>(shape->S) * a.row_groups + 1) * sizeof(int64_t)) : 0;
+    const size_t pp = tc ? round256((static_cast<size_t>(shape->S) * a.row_groups + 1) * sizeof(uint32_t)) : 0;
     const size_t pl = mass ? static_cast<size_t>(heads) * a.nq * a.G * per_list * (tc ? 4 : 8) : 0;
     if ((rc = ensure_workspace(h, po + pm + pp + pl, st))) return rc;
     uint8_t *ws = static_cast<uint8_t *>(h->workspace);
@@ -176,7 +182,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
         if (!sel) a.rows = a.nq * a.G;
         a.row_groups = static_cast<int>((a.rows + unit_rows - 1) / unit_rows);
         if (tc) {
-            rc = launch_prefill(h, a, D, f16, reinterpret_cast<int64_t *>(ws + po + pm), a.row_groups, mass, grid, st);
+            rc = launch_prefill(h, a, D, f16, reinterpret_cast<uint32_t *>(ws + po + pm), a.row_groups, mass, grid, st);
         } else {
             rc = launch_decode(h, a, pool->n_pages, D, f16, grid, nc, st);
             if (!rc && mass) rc = launch_mass(h, a, mass, st);

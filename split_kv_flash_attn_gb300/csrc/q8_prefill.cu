@@ -16,8 +16,9 @@
 // the head's query heads), so each decoded tile serves both:
 //   producers  : four warps, 32 key rows of every tile each; a row's 128 code
 //                bytes lie 16 to a lane and are held in registers a tile ahead.
-//   MMA thread : for tile g = 0, 1 in turn, O_g += W_g(j-1) V(j-1), then
-//                S_g(j) = Q_g K(j)^T into the same tensor-memory columns.
+//   MMA warps  : one issues S_g(j) = Q_g K(j)^T for tile g = 0, 1 in turn, the
+//                other O_g += W_g(j) V(j), W_g in the columns of S_g (one warp for
+//                both was bound by its issue, 130 cycles a product).
 //   softmax g  : four warps, one thread per query row, 64 keys (a page) at a time;
 //                a half's weights are stored over its own consumed scores.
 // While one tile's softmax runs, the tensor core works for the other.
@@ -25,7 +26,8 @@
 // Work split.  All key tiles of all (sequence, KV head, tile pair) units form one
 // line (its prefix sums come from a one-CTA plan kernel, which reads lengths and
 // query positions on the device), cut into one equal piece for each CTA; units that several
-// pieces share are merged by the last CTA to finish, in piece order.
+// pieces share are merged by a kernel of a warp a row, in piece order (by the last
+// CTA of each unit that took 60 to 100 us).
 //
 // Tensor memory: S_0/W_0 in columns 0-127, S_1/W_1 128-255, O_0 256-383, O_1
 // 384-511.  Every mbarrier wait is bounded; one that gives up sets the handle's
@@ -39,10 +41,36 @@ constexpr int kPM = 128;                        // query rows of a tile
 constexpr int kPN = 128;                        // keys of a tile
 constexpr int kSoftWarps = 8;                   // warps 0-3: tile 0, warps 4-7: tile 1
 constexpr int kProdWarps = 4;                   // warps 8-11
-constexpr int kMmaWarp = kSoftWarps + kProdWarps;
-constexpr int kPfThreads = (kMmaWarp + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps + kProdWarps;   // S; the next warp O; two more fill their warpgroup
+constexpr int kPfThreads = (kMmaWarp + 4) * 32;
+// Registers of a thread by role: 16 warps launch with 128 each, the softmax groups
+// take what the others can spare (spilled, they would go to an L1 of 20 KB:
+// 396 us against PFTIME at 512 tokens over 32768 keys).
+#ifndef VRS
+#define VRS 168
+#define VRP 104
+#define VRM 72
+#endif
+constexpr int kRegSoft = VRS, kRegProd = VRP, kRegMma = VRM;
+static_assert(2 * kRegSoft + kRegProd + kRegMma <= 4 * 128, "no more than the launch has");
+static_assert(kRegSoft >= 128 && kRegProd <= 128 && kRegMma <= 128, "the first is an increase, the others decreases");
+template <int N>
+__device__ __forceinline__ void more_regs()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+#ifndef VPT
+#define VPT 3
+#endif
+constexpr uint32_t kPieceTiles = VPT;                // fewest key tiles of a piece: each costs set-up and merge
 constexpr int kPlanSmem = 1024;                 // plan entries kept in shared memory
 constexpr float kPfShift = 8.f, kPfGrow = 5.f, kPfScaleGrow = 2.f;
+constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a wait gives up (tens of ms at least)
 constexpr float kNoScale = -100.f;              // log2 d_v - r of a zero scale (fp16 0, while l stays right)
 
 template <int D>
@@ -52,8 +80,10 @@ struct PfSmem {
     static constexpr int kQ = 0;                // two query tiles
     static constexpr int kK = kQ + 2 * kTile;   // two stages
     static constexpr int kV = kK + 2 * kTile;   // two stages
-    static constexpr int kPlan = kV + 2 * kTile;
-    static constexpr int kTotal = kPlan + (kPlanSmem + 1) * 8 + 1024;   // + alignment slack
+    static constexpr int kStage = kV + 2 * kTile;               // results on their way out: 32 rows of 16 for each softmax warp
+    static constexpr int kStageLd = 20;                         // (floats a row: free of bank conflicts)
+    static constexpr int kPlan = kStage + kSoftWarps * 32 * kStageLd * 4;
+    static constexpr int kTotal = kPlan + (kPlanSmem + 1) * 4 + 1024;   // + alignment slack
 };
 static_assert(PfSmem<128>::kTotal <= 226 * 1024, "shared memory per CTA");
 
@@ -69,56 +99,130 @@ enum { PB_KFULL = 0, PB_KEMPTY = 2, PB_VFULL = 4, PB_VEMPTY = 6, PB_QFULL = 8, P
 
 struct PrefillArgs {
     AttnArgs a;
-    const int64_t *plan;                        // [S * n_pairs + 1] tiles before each (sequence, pair)
+    const uint32_t *plan;                       // [S * n_pairs + 1] tiles before each (sequence, pair)
     int n_pairs;
     int out_f16;
 };
 
+// Tiles of a CTA's piece.
+__host__ __device__ inline uint32_t piece_tiles(uint32_t total, uint32_t ctas)
+{
+    const uint32_t c = (total + ctas - 1) / ctas;
+    return c < kPieceTiles ? kPieceTiles : c;
+}
+
 // Tiles of each (sequence, pair of query tiles): up to its last visible key; prefix
 // sums over all of them.
-__global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, int n_pairs, int64_t *plan)
+__global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, int n_pairs, uint32_t *plan)
 {
-    __shared__ int64_t s_sum[32];
+    __shared__ uint32_t s_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t n = static_cast<int64_t>(a.L.S) * n_pairs;
-    const int64_t share = (n + 1023) / 1024, lo = min(n, tid * share), hi = min(n, lo + share);
-    auto tiles = [&](int64_t e) {
+    for (int64_t e = warp; e < n; e += 32) {            // one warp an entry
         const int s = static_cast<int>(e / n_pairs), pr = static_cast<int>(e % n_pairs);
         int64_t keys = list_len(a.L, s);
         if (a.q_pos) {
-            const int t0 = 2 * kPM * static_cast<int64_t>(pr) / a.G;
+            const int t0 = static_cast<int>(2 * kPM * static_cast<int64_t>(pr) / a.G);
             const int t1 = static_cast<int>(min(int64_t(a.nq - 1), (2 * kPM * (static_cast<int64_t>(pr) + 1) - 1) / a.G));
             int top = -1;
-            for (int t = t0; t <= t1; ++t) top = max(top, __ldg(a.q_pos + a.token(s, t)));
+            for (int t = t0 + lane; t <= t1; t += 32) top = max(top, __ldg(a.q_pos + a.token(s, t)));
+            top = __reduce_max_sync(0xffffffffu, top);
             keys = max(int64_t(0), min(keys, static_cast<int64_t>(top) + 1));
         }
-        return (keys + kPN - 1) / kPN;
-    };
-    int64_t sum = 0;
-    for (int64_t e = lo; e < hi; ++e) {
-        const int64_t x = tiles(e);
-        plan[e] = x;                            // (made a prefix sum below, by the same thread)
-        sum += x;
+        if (lane == 0) {
+            plan[e] = static_cast<uint32_t>((keys + kPN - 1) / kPN);
+            if (pr == 0 && list_len(a.L, s) < max(0, a.L.kv_len[s])) atomicOr(a.L.status, kStatusList);
+        }
     }
-    for (int s = tid; s < a.L.S; s += 1024)
-        if (list_len(a.L, s) < max(0, a.L.kv_len[s])) atomicOr(a.L.status, kStatusList);
-    int64_t inc = sum;
+    __syncthreads();
+    const int64_t share = (n + 1023) / 1024, lo = min(n, tid * share), hi = min(n, lo + share);
+    uint32_t sum = 0;
+    for (int64_t e = lo; e < hi; ++e) sum += plan[e];
+    uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
     if (lane == 31) s_sum[warp] = inc;
     __syncthreads();
-    int64_t before = inc - sum;
+    uint32_t before = inc - sum;
     for (int w = 0; w < warp; ++w) before += s_sum[w];
     for (int64_t e = lo; e < hi; ++e) {
-        const int64_t x = plan[e];
+        const uint32_t x = plan[e];
         plan[e] = before;
         before += x;
     }
     if (tid == 1023) plan[n] = before;
 }
+
+// The units of a CTA's piece of the line in turn, as every role walks them.
+struct Unit {
+    int s, kh, pr;
+    uint32_t unit0;                             // the line's position of its tile 0
+    int t0, t1, n;                              // its tiles [t0, t1) are this CTA's, of n
+};
+struct Walk {
+    const uint32_t *plan;                       // shared or global memory
+    int np, S, Hk;
+    uint32_t end;                               // of the piece
+
+    __device__ void cut(Unit &x, uint32_t pos) const
+    {
+        x.t0 = static_cast<int>(pos - x.unit0);
+        x.t1 = static_cast<int>(min(static_cast<uint32_t>(x.n), end - x.unit0));
+    }
+    __device__ int tiles(const Unit &x) const
+    {
+        const int64_t e = static_cast<int64_t>(x.s) * np + x.pr;
+        return static_cast<int>(plan[e + 1] - plan[e]);
+    }
+    __device__ Unit first(uint32_t pos) const
+    {
+        Unit x;
+        int lo = 0, hi = S;                     // the last sequence that begins at or before pos
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (plan[static_cast<int64_t>(mid) * np] * Hk <= pos) lo = mid;
+            else hi = mid;
+        }
+        x.s = lo;
+        const int64_t e0 = static_cast<int64_t>(lo) * np;
+        const uint32_t p0 = plan[e0], T = plan[e0 + np] - p0, r = pos - p0 * Hk;
+        x.kh = static_cast<int>(r / T);
+        const uint32_t rr = r - x.kh * T + p0;  // within one head's pairs
+        int el = 0, eh = np;
+        while (eh - el > 1) {
+            const int mid = (el + eh) >> 1;
+            if (plan[e0 + mid] <= rr) el = mid;
+            else eh = mid;
+        }
+        x.pr = el;
+        x.n = tiles(x);
+        x.unit0 = pos - (rr - plan[e0 + el]);
+        cut(x, pos);
+        return x;
+    }
+    __device__ bool next(Unit &x) const         // false at the end of the piece
+    {
+        const uint32_t pos = x.unit0 + x.t1;
+        if (pos >= end) return false;
+        do {
+            if (++x.pr == np) {
+                x.pr = 0;
+                const int64_t e0 = static_cast<int64_t>(x.s) * np;
+                if (++x.kh == Hk || plan[e0 + np] == plan[e0]) {
+                    x.kh = 0;
+                    ++x.s;
+                }
+            }
+            x.n = tiles(x);
+        } while (x.n == 0);
+        x.unit0 = pos;
+        cut(x, pos);
+        return true;
+    }
+};
 
 template <int D, bool HILO>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArgs pa)
@@ -135,21 +239,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     __shared__ alignas(8) uint64_t s_bar[PB_COUNT];
     __shared__ Meta s_meta[4][2];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_last;
-    int64_t *s_plan = reinterpret_cast<int64_t *>(sm + SM::kPlan);
+    __shared__ int s_abort;
     const uint32_t bar0 = smem_addr(s_bar);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     constexpr uint32_t kIdescS = tc::idesc_f16(kPM, kPN, false);
     constexpr uint32_t kIdescPV = tc::idesc_f16(kPM, D, true);
     constexpr int kOCol = 2 * kPN;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int np = pa.n_pairs;
     const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
-    const bool plan_here = n_entries <= kPlanSmem;
-    if (plan_here)
+    Walk walk{pa.plan, np, a.L.S, a.L.Hk, 0};
+    if (n_entries <= kPlanSmem) {
+        uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
         for (int i = tid; i <= n_entries; i += kPfThreads) s_plan[i] = __ldcg(pa.plan + i);
-    auto plan = [&](int64_t e) { return plan_here ? s_plan[e] : __ldcg(pa.plan + e); };
+        walk.plan = s_plan;
+    }
     if (tid == 0) s_abort = 0;
     if (warp == 0) {
         tc::tmem_alloc<512>(smem_addr(&s_tmem));
@@ -174,369 +280,379 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    const int64_t total = plan(n_entries) * a.L.Hk;
-    const int64_t chunk = max(int64_t(1), (total + gridDim.x - 1) / gridDim.x);
-    const int64_t pos0 = min(total, blockIdx.x * chunk), pos_end = min(total, pos0 + chunk);
+    const uint32_t total = walk.plan[n_entries] * a.L.Hk;
+    const uint32_t chunk = piece_tiles(total, gridDim.x);
+    const uint32_t pos0 = min(total, blockIdx.x * chunk);
+    walk.end = min(total, pos0 + chunk);
+    const bool any = pos0 < walk.end;
+    auto two_tiles = [&](const Unit &x) { return (2 * x.pr + 1) * kPM < a.rows; };
 
-    // The units of the piece in turn, for every role.
-    struct Unit {
-        int s, kh, pr;
-        int64_t unit0;                          // the line's position of its tile 0
-        int t0, t1, n;                          // its tiles [t0, t1) are this CTA's, of n
-    };
-    auto unit_at = [&](int64_t pos) {
-        Unit x;
-        int lo = 0, hi = a.L.S;                 // the last sequence that begins at or before pos
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (plan(static_cast<int64_t>(mid) * np) * a.L.Hk <= pos) lo = mid;
-            else hi = mid;
-        }
-        x.s = lo;
-        const int64_t e0 = static_cast<int64_t>(lo) * np, p0 = plan(e0), T = plan(e0 + np) - p0;
-        const int64_t r = pos - p0 * a.L.Hk;
-        x.kh = static_cast<int>(r / T);
-        const int64_t rr = r - x.kh * T + p0;   // within one head's pairs
-        int64_t el = e0, eh = e0 + np;
-        while (eh - el > 1) {
-            const int64_t mid = (el + eh) >> 1;
-            if (plan(mid) <= rr) el = mid;
-            else eh = mid;
-        }
-        x.pr = static_cast<int>(el - e0);
-        x.n = static_cast<int>(plan(el + 1) - plan(el));
-        x.unit0 = pos - (rr - plan(el));
-        x.t0 = static_cast<int>(pos - x.unit0);
-        x.t1 = static_cast<int>(min(int64_t(x.n), pos_end - x.unit0));
-        return x;
-    };
-    auto two_tiles = [&](const Unit &x) { return (2 * static_cast<int64_t>(x.pr) + 1) * kPM < a.rows; };
-
-    // A phase already complete is taken at once; the abort flag is read only
-    // when the barrier is not ready.
+    // Bounded: gives up after kSpins polls, or when another role has.
     auto wait = [&](int b, uint32_t parity) -> bool {
-        if (tc::mbar_try_wait(bar(b), parity)) return true;
-        if (*reinterpret_cast<volatile int *>(&s_abort)) return false;
-        if (tc::mbar_wait(bar(b), parity, &s_abort)) return true;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kSpins; ++i) {
+            if (tc::mbar_try_wait(bar(b), parity)) return true;
+            if (*reinterpret_cast<volatile int *>(&s_abort)) return false;
+        }
         s_abort = 1;
         atomicOr(a.L.status, 1);
         return false;
     };
-    auto store_o = [&](int64_t r, int c, const float (&v)[4]) {
-        if (pa.out_f16)
-            *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + c) =
-                make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + c) = make_float4(v[0], v[1], v[2], v[3]);
-    };
-
-    // rows of pairs without a visible key: written here
-    for (int64_t e = blockIdx.x; e < n_entries; e += gridDim.x) {
-        if (plan(e + 1) != plan(e)) continue;
-        const int s = static_cast<int>(e / np), pr = static_cast<int>(e % np);
-        const int64_t r0 = 2 * kPM * static_cast<int64_t>(pr), nr = min(int64_t(2 * kPM), a.rows - r0);
-        for (int64_t i = tid; i < nr * a.L.Hk; i += kPfThreads) {
-            const int kh = static_cast<int>(i / nr), row = static_cast<int>(r0 + i % nr);
-            const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
-            const float z[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int c = 0; c < D; c += 4) store_o(r, c, z);
-            a.lse[r] = -INFINITY;
-        }
-    }
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ---------------- producers ----------------------------------------------
+        fewer_regs<kRegProd>();
         const int pw = warp - kSoftWarps;       // rows 32 pw .. of every tile: page pw / 2 of it
-        constexpr int LPR = D / 16;             // lanes a row
-        constexpr int RPI = 32 / LPR;           // rows an instruction
-        constexpr int NI = 32 / RPI;            // instructions a warp's 32 rows
-        const int c16 = lane % LPR, r0 = pw * 32 + lane / LPR;
-        int64_t j = 0;                          // key tiles so far
-        bool ok = true;
-        auto convert = [&](const uint4 (&w)[NI], bool on, uint32_t neg, uint8_t *tile) {
+        // 16 code bytes a lane.  Eight lanes that write together cover the same 64
+        // channels of two rows, whose swizzled pieces fall on different banks.
+        constexpr int NI = D / 16;              // loads for a warp's 32 rows
+        constexpr int RPI = 32 / NI;            // rows of one
+        const int c16 = (lane & 3) | (D == 128 ? (lane >> 4) << 2 : 0);
+        const int r0 = pw * 32 + ((lane >> 2) & (RPI - 1));
+        const int ch = 2 * (c16 & 3);
+        auto convert = [&](const uint4 (&w)[NI], bool on, bool neg, uint8_t *tile) {
+            uint8_t *dst = tile + (c16 >> 2) * SM::kHalf + r0 * 128;
+            if (!on) {
+#pragma unroll 1
+                for (int i = 0; i < NI; ++i) {
+                    const int x7 = (r0 + i * RPI) & 7;
+                    *reinterpret_cast<uint4 *>(dst + i * RPI * 128 + ((ch ^ x7) << 4)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(dst + i * RPI * 128 + (((ch + 1) ^ x7) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+                return;
+            }
+            // 1024 + u in fp16, then +-(that - 1152)
+            const __half2 sg = neg ? __half2half2(__ushort_as_half(0xbc00)) : __half2half2(__ushort_as_half(0x3c00));
+            const __half2 bias = neg ? __half2half2(__ushort_as_half(0x6480)) : __half2half2(__ushort_as_half(0xe480));
+            auto pair = [&](uint32_t x, uint32_t sel) -> uint32_t {
+                const uint32_t h = __byte_perm(x, 0x64646464u, sel);
+                const __half2 v = __hfma2(*reinterpret_cast<const __half2 *>(&h), sg, bias);
+                return *reinterpret_cast<const uint32_t *>(&v);
+            };
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int r = r0 + i * RPI;
-                const uint32_t in[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u,
-                                        w[i].w ^ 0x80808080u};
-                uint32_t v[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[2 * e] = on ? codes_lo(in[e]) ^ neg : 0u;
-                    v[2 * e + 1] = on ? codes_hi(in[e]) ^ neg : 0u;
-                }
-                // 16-byte chunks 2 c16 and 2 c16 + 1 of the row; lanes of the two
-                // 64-channel halves write them in opposite order, so that a row's
-                // writes spread over all banks
-                uint8_t *dst = tile + (c16 >> 2) * SM::kHalf + r * 128;
-                const int ch = 2 * (c16 & 3);
-                const int a0 = ((ch + (c16 >> 2)) ^ (r & 7)) << 4, a1 = ((ch + 1 - (c16 >> 2)) ^ (r & 7)) << 4;
-                const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-                *reinterpret_cast<uint4 *>(dst + a0) = (c16 >> 2) ? hi : lo;
-                *reinterpret_cast<uint4 *>(dst + a1) = (c16 >> 2) ? lo : hi;
+                const int x7 = (r0 + i * RPI) & 7;
+                const uint32_t a0 = w[i].x ^ 0x80808080u, a1 = w[i].y ^ 0x80808080u;
+                const uint32_t a2 = w[i].z ^ 0x80808080u, a3 = w[i].w ^ 0x80808080u;
+                *reinterpret_cast<uint4 *>(dst + i * RPI * 128 + ((ch ^ x7) << 4)) =
+                    make_uint4(pair(a0, 0x4140), pair(a0, 0x4342), pair(a1, 0x4140), pair(a1, 0x4342));
+                *reinterpret_cast<uint4 *>(dst + i * RPI * 128 + (((ch + 1) ^ x7) << 4)) =
+                    make_uint4(pair(a2, 0x4140), pair(a2, 0x4342), pair(a3, 0x4140), pair(a3, 0x4342));
             }
         };
-        for (int64_t pos = pos0; ok && pos < pos_end;) {
-            const Unit x = unit_at(pos);
-            const int64_t len = list_len(a.L, x.s);
-            const int32_t *ids = a.L.ids + (static_cast<int64_t>(x.s) * a.L.Hk + x.kh) * a.L.cap;
-            auto page_id = [&](int tile) {
-                const int64_t b = 2 * static_cast<int64_t>(tile) + (pw >> 1);
-                return tile < x.t1 && b * kPage < len ? max(-1, checked_page(a.L, __ldg(ids + b))) : -1;
-            };
-            uint4 kr[NI], vr[NI];
-            auto load = [&](uint4 (&w)[NI], const int8_t *codes, int id) {
-                if (id < 0) return;
-                const int8_t *p = codes + (static_cast<int64_t>(id) * kPage + (r0 & 63)) * D + c16 * 16;
+        uint4 kr[NI], vr[NI];
+        auto load = [&](uint4 (&w)[NI], const int8_t *codes, int id) {
+            if (id < 0) return;
+            const int8_t *p = codes + (static_cast<int64_t>(id) * kPage + (r0 & 63)) * D + c16 * 16;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) w[i] = ld_stream16(p + i * RPI * D);
-            };
-            int id = page_id(x.t0), id1 = page_id(x.t0 + 1);
-            float dk = id >= 0 ? __ldg(a.k_scale + id) : 0.f, dv = id >= 0 ? __ldg(a.v_scale + id) : 0.f;
-            load(kr, a.k, id);
-            load(vr, a.v, id);
-            for (int tl = x.t0; tl < x.t1; ++tl, ++j) {
-                const int b = static_cast<int>(j & 1);
-                const uint32_t ph = static_cast<uint32_t>(j >> 1);
-                const int id2 = page_id(tl + 2);
-                const float dk1 = id1 >= 0 ? __ldg(a.k_scale + id1) : 0.f, dv1 = id1 >= 0 ? __ldg(a.v_scale + id1) : 0.f;
-                const float ks = dk * a.scale_log2;
-                if (!__all_sync(0xffffffffu, j < 2 || wait(PB_KEMPTY + b, (ph - 1) & 1))) { ok = false; break; }
-                // (the slot's last reader is four tiles back: see the barriers)
-                if ((pw & 1) == 0 && lane == 0) {
-                    s_meta[j & 3][pw >> 1] = Meta{fmaxf(fabsf(ks), 1e-30f), dv != 0.f ? log2f(fabsf(dv)) : -INFINITY, id >= 0};
-                    tc::mbar_arrive(bar(PB_META + static_cast<int>(j & 3)));
+            for (int i = 0; i < NI; ++i) w[i] = ld_stream16(p + i * RPI * D);
+        };
+        uint32_t j = 0;                         // key tiles so far
+        bool ok = any;
+        if (any) {
+            Unit x = walk.first(pos0);
+            do {
+                const int pages = static_cast<int>((list_len(a.L, x.s) + kPage - 1) / kPage);
+                const int32_t *ids = a.L.ids + (static_cast<int64_t>(x.s) * a.L.Hk + x.kh) * a.L.cap;
+                auto page_id = [&](int tile) {
+                    const int b = 2 * tile + (pw >> 1);
+                    return tile < x.t1 && b < pages ? max(-1, checked_page(a.L, __ldg(ids + b))) : -1;
+                };
+                int id = page_id(x.t0), id1 = page_id(x.t0 + 1);
+                load(kr, a.k, id);
+                load(vr, a.v, id);
+                float dk = id >= 0 ? __ldg(a.k_scale + id) : 0.f, dv = id >= 0 ? __ldg(a.v_scale + id) : 0.f;
+#pragma unroll 1
+                for (int tl = x.t0; tl < x.t1; ++tl, ++j) {
+                    const int b = static_cast<int>(j & 1);
+                    const uint32_t before = ((j >> 1) - 1) & 1;
+                    const int id2 = page_id(tl + 2);
+                    const float dk1 = id1 >= 0 ? __ldg(a.k_scale + id1) : 0.f, dv1 = id1 >= 0 ? __ldg(a.v_scale + id1) : 0.f;
+                    const float ks = dk * a.scale_log2;
+                    if (!__all_sync(0xffffffffu, j < 2 || wait(PB_KEMPTY + b, before))) { ok = false; break; }
+                    if ((pw & 1) == 0 && lane == 0) {
+                        s_meta[j & 3][pw >> 1] = Meta{fmaxf(fabsf(ks), 1e-30f), dv != 0.f ? log2f(fabsf(dv)) : -INFINITY, id >= 0};
+                        tc::mbar_arrive(bar(PB_META + static_cast<int>(j & 3)));
+                    }
+                    convert(kr, id >= 0, ks < 0.f, sm + SM::kK + b * SM::kTile);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(bar(PB_KFULL + b));
+                    load(kr, a.k, id1);
+                    if (!__all_sync(0xffffffffu, j < 2 || wait(PB_VEMPTY + b, before))) { ok = false; break; }
+                    convert(vr, id >= 0, dv < 0.f, sm + SM::kV + b * SM::kTile);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(bar(PB_VFULL + b));
+                    load(vr, a.v, id1);
+                    id = id1;
+                    id1 = id2;
+                    dk = dk1;
+                    dv = dv1;
                 }
-                convert(kr, id >= 0, ks < 0.f ? 0x80008000u : 0u, sm + SM::kK + b * SM::kTile);
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(bar(PB_KFULL + b));
-                load(kr, a.k, id1);
-                if (!__all_sync(0xffffffffu, j < 2 || wait(PB_VEMPTY + b, (ph - 1) & 1))) { ok = false; break; }
-                convert(vr, id >= 0, dv < 0.f ? 0x80008000u : 0u, sm + SM::kV + b * SM::kTile);
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(bar(PB_VFULL + b));
-                load(vr, a.v, id1);
-                id = id1;
-                id1 = id2;
-                dk = dk1;
-                dv = dv1;
-            }
-            pos = x.unit0 + x.t1;
+            } while (ok && walk.next(x));
         }
-    } else if (warp == kMmaWarp) {
-        // ---------------- MMA issuer ---------------------------------------------
-        if (lane == 0) {
-            bool ok = true;
-            int64_t j0 = 0;                     // the CTA's tiles before this unit
-            uint32_t units[2] = {0, 0}, tiles[2] = {0, 0};   // of each query tile g so far
-            int last_bar = -1;
-            uint32_t last_par = 0;
+    } else if (warp >= kMmaWarp) {
+        // ---------------- MMA issuers --------------------------------------------
+        fewer_regs<kRegMma>();
+        auto all = [](bool p) { return __all_sync(0xffffffffu, p) != 0; };
+        uint32_t j = 0, units0 = 0, units1 = 0, tiles0 = 0, tiles1 = 0;   // key tiles, and of each query tile, so far
+        bool ok = any;
+        if (warp == kMmaWarp && any) {
+            // S_g = Q_g K^T, once PV_g of the tile before has read W_g
             const uint64_t dq0 = tc::smem_desc(sbase + SM::kQ, 16, 1024);
             const uint64_t dk0 = tc::smem_desc(sbase + SM::kK, 16, 1024);
-            const uint64_t dv0 = tc::smem_desc(sbase + SM::kV, SM::kHalf, 1024);
-            for (int64_t pos = pos0; ok && pos < pos_end;) {
-                const Unit x = unit_at(pos);
-                const int ng = two_tiles(x) ? 2 : 1;
-                const int n = x.t1 - x.t0;
-                for (int g = 0; g < ng && ok; ++g) ok = wait(PB_QFULL + g, units[g]++ & 1);
-                tc::tc_fence_after();
-                for (int jj = 0; ok && jj <= n; ++jj) {
-                    for (int g = 0; g < ng; ++g) {
+            Unit x = walk.first(pos0);
+            do {
+                const bool two = two_tiles(x);
+                ok = all(wait(PB_QFULL, units0++ & 1)) && (!two || all(wait(PB_QFULL + 1, units1++ & 1)));
+#pragma unroll 1
+                for (int tl = x.t0; ok && tl < x.t1; ++tl, ++j) {
+                    const int b = static_cast<int>(j & 1);
+                    if (!(ok = all(wait(PB_KFULL + b, (j >> 1) & 1)))) break;
+#pragma unroll 1
+                    for (int g = 0; g < (two ? 2 : 1); ++g) {
+                        const uint32_t t = g ? tiles1++ : tiles0++;
+                        if (!(ok = t == 0 || all(wait(PB_PDONE + g, (t - 1) & 1)))) break;
+                        tc::tc_fence_after();
+                        const uint64_t ad = tc::desc_add(dq0, g * SM::kTile), bd = tc::desc_add(dk0, b * SM::kTile);
                         const uint32_t d_s = tmem + static_cast<uint32_t>(g * kPN);
-                        if (jj >= 1) {
-                            // O_g += W_g V
-                            const int64_t j = j0 + jj - 1;
-                            const int b = static_cast<int>(j & 1);
-                            const uint32_t par = (tiles[g] - 1) & 1;
-                            if (!wait(PB_PFULL + g, par)) { ok = false; break; }
-                            if (g == 0 && !wait(PB_VFULL + b, (j >> 1) & 1)) { ok = false; break; }
-                            tc::tc_fence_after();
-                            const uint32_t d_o = tmem + static_cast<uint32_t>(kOCol + g * D);
-#pragma unroll
-                            for (int kk = 0; kk < kPN / 16; ++kk) {
-                                const uint64_t bd = tc::desc_add(dv0, b * SM::kTile + kk * 2048);
-                                const uint32_t at = d_s + static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8);
-                                tc::mma_f16_ts(d_o, at, bd, kIdescPV, (jj > 1 || kk > 0) ? 1u : 0u);
-                                if (HILO) tc::mma_f16_ts(d_o, at + 32, bd, kIdescPV, 1u);
-                            }
-                            tc::mma_commit(bar(PB_PDONE + g));
-                            last_bar = PB_PDONE + g;
-                            last_par = par;
-                            if (g == ng - 1) tc::mma_commit(bar(PB_VEMPTY + b));
-                        }
-                        if (jj < n) {
-                            // S_g = Q_g K^T, once PV_g of the tile before has read W_g
-                            const int64_t j = j0 + jj;
-                            const int b = static_cast<int>(j & 1);
-                            if (g == 0 && !wait(PB_KFULL + b, (j >> 1) & 1)) { ok = false; break; }
-                            if (tiles[g] >= 1 && !wait(PB_PDONE + g, (tiles[g] - 1) & 1)) { ok = false; break; }
-                            tc::tc_fence_after();
+                        if (tc::elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t off = (kk >> 2) * SM::kHalf + (kk & 3) * 32;
-                                tc::mma_f16_ss(d_s, tc::desc_add(dq0, g * SM::kTile + off),
-                                               tc::desc_add(dk0, b * SM::kTile + off), kIdescS, kk > 0 ? 1u : 0u);
+                                tc::mma_f16_ss(d_s, tc::desc_add(ad, off), tc::desc_add(bd, off), kIdescS, kk > 0 ? 1u : 0u);
                             }
                             tc::mma_commit(bar(PB_SFULL + g));
-                            last_bar = PB_SFULL + g;
-                            last_par = tiles[g]++ & 1;
-                            if (g == ng - 1) tc::mma_commit(bar(PB_KEMPTY + b));
+                            if (g == 1 || !two) tc::mma_commit(bar(PB_KEMPTY + b));
                         }
+                        __syncwarp();
                     }
                 }
-                j0 += n;
-                pos = x.unit0 + x.t1;
+            } while (ok && walk.next(x));
+            // nobody waits for the last commits on the stages' free barriers: they
+            // are awaited here, so that none is in flight at exit (after a wait gave
+            // up: with a limit, as for all that was issued)
+            for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) tc::mbar_wait(bar(PB_KEMPTY + static_cast<int>(i & 1)), (i >> 1) & 1, nullptr, 100000000ull);
+            if (!ok) {
+                if (tiles0) tc::mbar_wait(bar(PB_SFULL), (tiles0 - 1) & 1, nullptr, 100000000ull);
+                if (tiles1) tc::mbar_wait(bar(PB_SFULL + 1), (tiles1 - 1) & 1, nullptr, 100000000ull);
             }
-            if (*reinterpret_cast<volatile int *>(&s_abort)) {
-                // drain issued MMAs: the last commit covers every MMA issued before it
-                if (last_bar >= 0) tc::mbar_wait(bar(last_bar), last_par, nullptr, 100000000ull);
-            } else {
-                // nobody waits for the last commits on the stages' free barriers;
-                // they are awaited here, so that none is in flight at exit
-                for (int64_t j = max(int64_t(0), j0 - 2); j < j0; ++j) {
-                    wait(PB_KEMPTY + static_cast<int>(j & 1), (j >> 1) & 1);
-                    wait(PB_VEMPTY + static_cast<int>(j & 1), (j >> 1) & 1);
+        } else if (warp == kMmaWarp + 1 && any) {
+            // O_g += W_g V
+            const uint64_t dv0 = tc::smem_desc(sbase + SM::kV, SM::kHalf, 1024);
+            Unit x = walk.first(pos0);
+            do {
+                const bool two = two_tiles(x);
+#pragma unroll 1
+                for (int tl = x.t0; ok && tl < x.t1; ++tl, ++j) {
+                    const int b = static_cast<int>(j & 1);
+                    if (!(ok = all(wait(PB_VFULL + b, (j >> 1) & 1)))) break;
+#pragma unroll 1
+                    for (int g = 0; g < (two ? 2 : 1); ++g) {
+                        const uint32_t t = g ? tiles1++ : tiles0++;
+                        if (!(ok = all(wait(PB_PFULL + g, t & 1)))) break;
+                        tc::tc_fence_after();
+                        const uint64_t bd = tc::desc_add(dv0, b * SM::kTile);
+                        const uint32_t d_w = tmem + static_cast<uint32_t>(g * kPN);
+                        const uint32_t d_o = tmem + static_cast<uint32_t>(kOCol + g * D);
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < kPN / 16; ++kk) {
+                                const uint32_t at = d_w + static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8);
+                                tc::mma_f16_ts(d_o, at, tc::desc_add(bd, kk * 2048), kIdescPV, (tl > x.t0 || kk > 0) ? 1u : 0u);
+                                if (HILO) tc::mma_f16_ts(d_o, at + 16, tc::desc_add(bd, kk * 2048), kIdescPV, 1u);
+                            }
+                            tc::mma_commit(bar(PB_PDONE + g));
+                            if (g == 1 || !two) tc::mma_commit(bar(PB_VEMPTY + b));
+                        }
+                        __syncwarp();
+                    }
+                }
+            } while (ok && walk.next(x));
+            for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) tc::mbar_wait(bar(PB_VEMPTY + static_cast<int>(i & 1)), (i >> 1) & 1, nullptr, 100000000ull);
+            if (!ok) {
+                if (tiles0) tc::mbar_wait(bar(PB_PDONE), (tiles0 - 1) & 1, nullptr, 100000000ull);
+                if (tiles1) tc::mbar_wait(bar(PB_PDONE + 1), (tiles1 - 1) & 1, nullptr, 100000000ull);
+            }
+        } else if (warp == kMmaWarp + 2) {
+            // rows of pairs without a visible key: written here, by all CTAs' spare warps
+            for (int64_t e = 0; e < n_entries; ++e) {
+                if (walk.plan[e + 1] != walk.plan[e]) continue;
+                const int s = static_cast<int>(e / np), pr = static_cast<int>(e % np);
+                const int r0 = 2 * kPM * pr;
+                const int64_t nr = min(2 * kPM, a.rows - r0), n = nr * a.L.Hk * (D / 4);
+                for (int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane; i < n; i += static_cast<int64_t>(gridDim.x) * 32) {
+                    const int c = static_cast<int>(i % (D / 4)), kh = static_cast<int>(i / (D / 4) / nr);
+                    const int row = r0 + static_cast<int>(i / (D / 4) % nr);
+                    const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
+                    if (pa.out_f16) *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + 4 * c) = make_uint2(0, 0);
+                    else *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + 4 * c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c == 0) a.lse[r] = -INFINITY;
                 }
             }
         }
     } else {
         // ---------------- softmax: one thread per query row -----------------------
+        more_regs<kRegSoft>();
         const int g = warp >> 2;
         const int m = (warp & 3) * 32 + lane;   // row of the tile = lane of tensor memory
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_col = lane_base + static_cast<uint32_t>(g * kPN);
         const uint32_t o_col = lane_base + static_cast<uint32_t>(kOCol + g * D);
-        auto put_q = [&](const Unit &x) {       // this thread's query row into shared memory
-            const int64_t row = (2 * static_cast<int64_t>(x.pr) + g) * kPM + m;
-            const bool on = row < a.rows;
-            const int64_t r = on ? a.token(x.s, static_cast<int>(row / a.G)) * a.H + x.kh * a.G + row % a.G : 0;
-            const __half *qp = a.q + r * D;
-            uint8_t *qt = sm + SM::kQ + g * SM::kTile + m * 128;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = on ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(qt + (c >> 3) * SM::kHalf + (((c & 7) ^ (m & 7)) << 4)) = v;
+        auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); };
+        auto active = [&](const Unit &y) { return g == 0 || two_tiles(y); };
+        // index of this thread's row in q and o (-1: past the last)
+        auto row_index = [&](const Unit &x) -> int64_t {
+            const int row = (2 * x.pr + g) * kPM + m;
+            return row < a.rows ? a.token(x.s, row / a.G) * a.H + x.kh * a.G + row % a.G : -1;
+        };
+        // the warp's 32 query rows into shared memory, D / 8 lanes a row
+        auto put_q = [&](int64_t index) {
+            constexpr int LPR = D / 8;
+            const int c = lane % LPR;
+            uint8_t *qt = sm + SM::kQ + g * SM::kTile + (c >> 3) * SM::kHalf;
+#pragma unroll 4
+            for (int i = 0; i < LPR; ++i) {
+                const int rl = i * (32 / LPR) + lane / LPR;         // row of the warp
+                const int64_t r = __shfl_sync(0xffffffffu, index, rl);
+                const uint4 v = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.q + r * D) + c) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(qt + ((warp & 3) * 32 + rl) * 128 + (((c & 7) ^ (rl & 7)) << 4)) = v;
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(bar(PB_QFULL + g));
         };
-        int64_t j = 0;                          // key tiles so far
-        uint32_t tiles = 0;                     // of them with this group's query tile
-        auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); };
-        auto active = [&](const Unit &y) { return g == 0 || two_tiles(y); };
+        uint32_t j = 0, tiles = 0;              // key tiles so far, and those with this query tile
         Unit x = {};
-        if (pos0 < pos_end) {
-            x = unit_at(pos0);
-            if (active(x)) put_q(x);
+        int64_t index = -1;
+        if (any) {
+            x = walk.first(pos0);
+            index = row_index(x);
+            if (active(x)) put_q(index);
         }
-        for (int64_t pos = pos0; pos < pos_end;) {
+        for (bool more = any; more;) {
             meet();
-            const int64_t row = (2 * static_cast<int64_t>(x.pr) + g) * kPM + m;
-            const bool row_on = row < a.rows;
             const bool tile_on = active(x);
-            const int64_t len = list_len(a.L, x.s);
-            int64_t lim = len;                  // keys that this row sees
-            const int64_t tok = a.token(x.s, row_on ? static_cast<int>(row / a.G) : 0);
-            if (a.q_pos) lim = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + tok)) + 1));
-            float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
             const int n = x.t1 - x.t0;
+            const int64_t out = index;
+            const bool whole = n == x.n;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x.unit0 + x.t0 == pos0 ? 0 : 1);
+            float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
             if (tile_on) {
+                const int row = (2 * x.pr + g) * kPM + m;
+                const int len = static_cast<int>(list_len(a.L, x.s));
+                int lim = len;                  // keys that this row sees
+                if (a.q_pos) {
+                    const int qp = __ldg(a.q_pos + a.token(x.s, min(row / a.G, a.nq - 1)));
+                    lim = qp < 0 ? 0 : (qp < len ? qp + 1 : len);
+                }
+                lim -= x.t0 * kPN;              // counted from the tile at hand
+                int pages = (len + kPage - 1) / kPage - 2 * x.t0;
+                float *pl = nullptr;
+                if (a.page_lse && row < a.rows)
+                    pl = a.page_lse + ((static_cast<int64_t>(x.s) * a.L.Hk + x.kh) * a.L.cap + 2 * x.t0) * a.rows + row;
                 // No early exit from this loop: after a wait gives up, every later
                 // wait returns at once and the warp runs through (the outputs are
                 // then invalid and the status word says so).
-                for (int jj = 0; jj < n; ++jj, ++j, ++tiles) {
-                    const int64_t key0 = static_cast<int64_t>(x.t0 + jj) * kPN;
+#pragma unroll 1
+                for (int jj = 0; jj < n; ++jj, ++j, ++tiles, lim -= kPN, pages -= 2) {
                     __all_sync(0xffffffffu, wait(PB_SFULL + g, tiles & 1));
-                    __all_sync(0xffffffffu, wait(PB_META + static_cast<int>(j & 3), (j >> 2) & 1));
                     tc::tc_fence_after();
-                    const Meta m0 = s_meta[j & 3][0], m1 = s_meta[j & 3][1];
+                    // 32 columns at a time, the next ones on their way: their largest score,
+                    // their weights against the reference as it stands then, and these
+                    // stored over their own scores (keys 32c .. in columns 32c .., what
+                    // rounding left 16 further on).
+                    uint32_t xr[2][32];
+                    tc::tmem_ld32(s_col, xr[0]);
+                    __all_sync(0xffffffffu, wait(PB_META + static_cast<int>(j & 3), (j >> 2) & 1));
+                    const Meta *mt2 = s_meta[j & 3];
                     // the pages' reference
                     const float r_old = r_ref;
-                    const float lv_max = fmaxf(m0.on ? m0.lv : -INFINITY, m1.on ? m1.lv : -INFINITY);
+                    const float lv_max = fmaxf(mt2[0].lv, mt2[1].lv);       // (-inf where there is no page)
                     if (lv_max > r_ref + kPfScaleGrow) r_ref = ceilf(lv_max);
-                    float ref = m_ref, beta = 1.f, ls0 = 0.f, ls1 = 0.f;
-                    const int64_t lim_t = lim - key0;               // columns at or past it are masked
-                    const bool masked = __any_sync(0xffffffffu, lim_t < kPN);
-#pragma unroll
+                    float ref = m_ref, ls = 0.f, lh = 0.f;
+                    const bool masked = __any_sync(0xffffffffu, lim < kPN);
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
-                        const Meta mt = h == 0 ? m0 : m1;
-                        uint32_t xr[2][32];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) tc::tmem_ld32(s_col + h * 64 + c * 32, xr[c]);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) tc::tmem_wait_ld(xr[c]);
-                        auto X = [&](int i) -> uint32_t & { return xr[i >> 5][i & 31]; };
-                        if (masked || !mt.on) {
-                            const int64_t lh = mt.on ? lim_t - h * 64 : 0;
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (i >= lh) X(i) = 0xff800000u;
-                        }
-                        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) mq[i & 3] = fmaxf(mq[i & 3], __uint_as_float(X(i)));
-                        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * mt.ks;
-                        const float prev = ref;
-                        if (mx > ref + kPfGrow) ref = ceilf(mx);    // true on the first finite maximum
+                        const Meta mt = mt2[h];
                         const float dl = mt.lv == -INFINITY ? kNoScale : fmaxf(mt.lv - r_ref, kNoScale);
-                        const float off = ref == -INFINITY ? 0.f : kPfShift + dl - ref;
-                        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                        const float un = fast_exp2(-dl);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            // 32 keys: weights over their own consumed scores
+                        for (int cc = 0; cc < 2; ++cc) {
+                            const int c = 2 * h + cc;
+                            uint32_t(&xc)[32] = xr[cc];
+                            tc::tmem_wait_ld(xc);
+                            if (c < 3) tc::tmem_ld32(s_col + (c + 1) * 32, xr[cc ^ 1]);
+                            if (masked || !mt.on) {
+                                const int lc = mt.on ? lim - c * 32 : 0;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i >= lc) xc[i] = 0xff800000u;
+                            }
+                            auto X = [&](int i) { return __uint_as_float(xc[i]); };
+                            float mq[4] = {X(0), X(1), X(2), X(3)};
+#pragma unroll
+                            for (int i = 4; i < 28; i += 8)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) mq[e] = max3(mq[e], X(i + e), X(i + e + 4));
+                            const float mx = fmaxf(max3(max3(mq[0], X(28), X(29)), max3(mq[1], X(30), X(31)), mq[2]), mq[3]) * mt.ks;
+                            const float prev = ref;
+                            if (mx > ref + kPfGrow) ref = ceilf(mx);  // true on the first finite maximum
+                            const float off = ref == -INFINITY ? 0.f : kPfShift + dl - ref;
+                            if (c > 0 && __any_sync(0xffffffffu, ref != prev)) {
+                                // the weights stored above to the moved reference, by two exact
+                                // factors, as fp16 has none below 2^-24
+                                const float e = ref == prev ? 0.f : prev == -INFINITY ? -28.f : fmaxf(prev - ref, -28.f);
+                                const float beta = ref == prev ? 1.f : prev == -INFINITY ? 0.f : fast_exp2(prev - ref);
+                                const __half2 b0 = __float2half2_rn(fast_exp2(fmaxf(e, -14.f)));
+                                const __half2 b1 = __float2half2_rn(fast_exp2(fminf(e + 14.f, 0.f)));
+                                ls *= beta;
+                                lh *= beta;
+                                tc::tmem_wait_st();
+#pragma unroll 1
+                                for (int d = 0; d < (HILO ? 2 * c : c); ++d) {
+                                    const uint32_t at = s_col + d * (HILO ? 16 : 32);
+                                    uint32_t pr[16];
+                                    tc::tmem_ld16(at, pr);
+                                    tc::tmem_wait_ld16(pr);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&pr[i]), b0), b1);
+                                        pr[i] = *reinterpret_cast<const uint32_t *>(&v);
+                                    }
+                                    tc::tmem_st16u(at, pr);
+                                }
+                            }
+                            float lq[4] = {0.f, 0.f, 0.f, 0.f};
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                const float w0 = fast_exp2(fmaf(__uint_as_float(xr[c][i]), mt.ks, off));
-                                const float w1 = fast_exp2(fmaf(__uint_as_float(xr[c][i + 1]), mt.ks, off));
-                                ls[i & 2] += w0;
-                                ls[(i & 2) + 1] += w1;
+                                float w0, w1;
+                                fma2(w0, w1, X(i), X(i + 1), mt.ks, off);
+                                w0 = fast_exp2(w0);
+                                w1 = fast_exp2(w1);
+                                add2(lq[i & 2], lq[(i & 2) + 1], w0, w1);
                                 hi[i >> 1] = pack_half2(w0, w1);
                                 if (HILO) {
                                     const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i >> 1]));
                                     lo[i >> 1] = pack_half2(w0 - back.x, w1 - back.y);
                                 }
                             }
-                            tc::tmem_st16u(s_col + h * 64 + c * 16, hi);
-                            if (HILO) tc::tmem_st16u(s_col + h * 64 + 32 + c * 16, lo);
+                            tc::tmem_st16u(s_col + c * 32, hi);
+                            if (HILO) tc::tmem_st16u(s_col + c * 32 + 16, lo);
+                            lh += ((lq[0] + lq[1]) + (lq[2] + lq[3])) * un;
                         }
-                        const float lh = ((ls[0] + ls[1]) + (ls[2] + ls[3])) * fast_exp2(-dl);
-                        if (a.page_lse && row_on && key0 + h * 64 < len)
-                            a.page_lse[((static_cast<int64_t>(x.s) * a.L.Hk + x.kh) * a.L.cap + 2 * (x.t0 + jj) + h) * a.rows + row] =
-                                lh > 0.f ? ref - kPfShift + log2f(lh) : -INFINITY;
-                        if (h == 0) {
-                            ls0 = lh;
-                        } else {
-                            ls1 = lh;
-                            if (ref != prev) beta = prev == -INFINITY ? 0.f : fast_exp2(prev - ref);
-                            if (__any_sync(0xffffffffu, beta != 1.f)) {
-                                // the first half's weights, stored above, to the moved reference
-                                tc::tmem_wait_st();
-                                // (two exact factors, as fp16 has none below 2^-24)
-                                const float e = prev == -INFINITY ? -28.f : fmaxf(prev - ref, -28.f);
-                                const __half2 b0 = __float2half2_rn(fast_exp2(fmaxf(e, -14.f)));
-                                const __half2 b1 = __float2half2_rn(fast_exp2(fminf(e + 14.f, 0.f)));
-#pragma unroll
-                                for (int c = 0; c < (HILO ? 2 : 1); ++c) {
-                                    uint32_t pr[32];
-                                    tc::tmem_ld32(s_col + c * 32, pr);
-                                    tc::tmem_wait_ld(pr);
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) {
-                                        const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&pr[i]), b0), b1);
-                                        pr[i] = *reinterpret_cast<const uint32_t *>(&v);
-                                    }
-                                    tc::tmem_st32u(s_col + c * 32, pr);
-                                }
-                            }
+                        if (pl) {
+                            if (h < pages) *pl = lh > 0.f ? ref - kPfShift + log2f(lh) : -INFINITY;
+                            pl += a.rows;
                         }
+                        ls += lh;
+                        lh = 0.f;
                     }
                     const float alpha = ref == m_ref ? 1.f : (m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref));
                     const float alpha_o = r_ref == r_old ? alpha : (r_old == -INFINITY ? 0.f : alpha * fast_exp2(r_old - r_ref));
                     // O_g holds every PV up to the last tile (S_g was issued after
                     // it was done) and none of this tile before W_g is full
                     if (jj > 0 && __any_sync(0xffffffffu, alpha_o != 1.f)) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t rr[32];
                             tc::tmem_ld32(o_col + c * 32, rr);
@@ -547,103 +663,69 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                             tc::tmem_st32(o_col + c * 32, v);
                         }
                     }
-                    l_run = l_run * alpha + (ls0 * beta + ls1);
+                    l_run = l_run * alpha + ls;
                     m_ref = ref;
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     tc::mbar_arrive(bar(PB_PFULL + g));
                 }
+            } else {
+                j += n;
             }
             // the next unit's queries go in while this one's last product runs: S_g of
             // the last tile is done, and nothing else reads Q_g
-            const Unit cur = x;
-            const int64_t here = pos;
-            pos = x.unit0 + x.t1;
-            if (!tile_on) j += n;
-            if (pos < pos_end) {
-                x = unit_at(pos);
-                if (active(x)) put_q(x);
+            more = walk.next(x);
+            if (more) {
+                index = row_index(x);
+                if (active(x)) put_q(index);
             }
+            if (!tile_on) continue;
             // ---------------- O / l, lse: result or piece ------------------------------
-            const bool whole = cur.t0 == 0 && cur.t1 == cur.n;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (here == pos0 ? 0 : 1);
-            if (tile_on) {
-                bool have = !*reinterpret_cast<volatile int *>(&s_abort) && wait(PB_PDONE + g, (tiles - 1) & 1);
-                have = __all_sync(0xffffffffu, have);
-                if (have) tc::tc_fence_after();
-                const bool empty = !have || !(l_run > 0.f);
-                const float inv = empty ? 0.f : fast_exp2(r_ref == -INFINITY ? 0.f : r_ref) / l_run;
-                const int64_t r = tok * a.H + cur.kh * a.G + row % a.G;
-                const float lse2 = empty ? -INFINITY : m_ref - kPfShift + log2f(l_run);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t orr[32];
-                    if (have) {
-                        tc::tmem_ld32(o_col + c * 32, orr);         // warp-wide: every lane takes part
-                        tc::tmem_wait_ld(orr);
-                    }
-                    if (row_on) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = empty ? 0.f : __uint_as_float(orr[i + e]) * inv;
-                            if (whole)
-                                store_o(r, c * 32 + i, v);
-                            else
-                                *reinterpret_cast<float4 *>(a.part_o + ((slot * 2 + g) * kPM + m) * D + c * 32 + i) =
-                                    make_float4(v[0], v[1], v[2], v[3]);
-                        }
-                    }
+            bool have = wait(PB_PDONE + g, (tiles - 1) & 1) && !*reinterpret_cast<volatile int *>(&s_abort);
+            have = __all_sync(0xffffffffu, have);
+            if (have) tc::tc_fence_after();
+            const bool empty = !have || !(l_run > 0.f);
+            const float inv = empty ? 0.f : fast_exp2(r_ref == -INFINITY ? 0.f : r_ref) / l_run;
+            const float lse2 = empty ? -INFINITY : m_ref - kPfShift + log2f(l_run);
+            // 16 columns of the warp's rows through shared memory, so that four lanes
+            // write 64 (fp16: 32) bytes of a row
+            float *stage = reinterpret_cast<float *>(sm + SM::kStage) + warp * 32 * SM::kStageLd;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t orr[16];
+                if (have) {
+                    tc::tmem_ld16(o_col + c * 16, orr);             // warp-wide: every lane takes part
+                    tc::tmem_wait_ld16(orr);
                 }
-                if (row_on) {
-                    if (whole) a.lse[r] = lse2 * 0.6931471805599453f;
-                    else a.part_ml[(slot * 2 + g) * kPM + m] = lse2;
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = empty ? 0.f : __uint_as_float(orr[i + e]) * inv;
+                    *reinterpret_cast<float4 *>(stage + lane * SM::kStageLd + i) = make_float4(v[0], v[1], v[2], v[3]);
                 }
-                tc::tc_fence_before();          // O_g is read before W_g of the next unit is announced
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rl = i * 8 + (lane >> 2), col = c * 16 + (lane & 3) * 4;
+                    const float4 v = *reinterpret_cast<const float4 *>(stage + rl * SM::kStageLd + (lane & 3) * 4);
+                    const int64_t r = __shfl_sync(0xffffffffu, out, rl);
+                    if (r < 0) continue;
+                    if (!whole)
+                        *reinterpret_cast<float4 *>(a.part_o + ((slot * 2 + g) * kPM + (warp & 3) * 32 + rl) * D + col) = v;
+                    else if (pa.out_f16)
+                        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + col) =
+                            make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + col) = v;
+                }
+                __syncwarp();
             }
-            if (!whole) {
-                // the last CTA of the unit puts the pieces together, in order
-                const int64_t unit = (static_cast<int64_t>(cur.s) * a.L.Hk + cur.kh) * np + cur.pr;
-                const int64_t c_lo = cur.unit0 / chunk, c_hi = (cur.unit0 + cur.n - 1) / chunk;
-                __threadfence();
-                meet();
-                if (tid == 0) s_last = atomicAdd(a.counters + unit, 1) == static_cast<int>(c_hi - c_lo);
-                meet();
-                if (s_last) {
-                    __threadfence();
-                    const int64_t first = 2 * kPM * static_cast<int64_t>(cur.pr);
-                    const int nr = static_cast<int>(min(int64_t(2 * kPM), a.rows - first));
-                    auto slot_of = [&](int64_t c) { return 2 * c + (c == c_lo && cur.unit0 > c * chunk ? 1 : 0); };
-                    constexpr int V = D / 4;    // float4 of a row
-                    for (int i = tid; i < nr * V; i += kSoftWarps * 32) {
-                        const int rr = i / V, c4 = i % V;
-                        float M = -INFINITY;
-                        for (int64_t c = c_lo; c <= c_hi; ++c) M = fmaxf(M, __ldcg(a.part_ml + slot_of(c) * 2 * kPM + rr));
-                        float W = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (M != -INFINITY) {
-#pragma unroll 4
-                            for (int64_t c = c_lo; c <= c_hi; ++c) {
-                                const int64_t at = slot_of(c) * 2 * kPM + rr;
-                                const float w = fast_exp2(__ldcg(a.part_ml + at) - M);
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + c4);
-                                W += w;
-                                v[0] = fmaf(w, y.x, v[0]);
-                                v[1] = fmaf(w, y.y, v[1]);
-                                v[2] = fmaf(w, y.z, v[2]);
-                                v[3] = fmaf(w, y.w, v[3]);
-                            }
-                            const float q = 1.f / W;
-                            for (int e = 0; e < 4; ++e) v[e] *= q;
-                        }
-                        const int64_t prow = first + rr;
-                        const int64_t r = a.token(cur.s, static_cast<int>(prow / a.G)) * a.H + cur.kh * a.G + prow % a.G;
-                        store_o(r, c4 * 4, v);
-                        if (c4 == 0) a.lse[r] = M == -INFINITY ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
-                    }
-                    if (tid == 0) a.counters[unit] = 0;
-                }
+            if (out >= 0) {
+                if (whole) a.lse[out] = lse2 * 0.6931471805599453f;
+                else a.part_ml[(slot * 2 + g) * kPM + m] = lse2;
             }
+            tc::tc_fence_before();              // O_g is read before W_g of the next unit is announced
         }
     }
     tc::tc_fence_before();
@@ -652,6 +734,61 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         tc::tc_fence_after();
         tc::tmem_dealloc<512>(tmem);
     }
+}
+
+// Rows of units that several CTAs share: their pieces together, in order.  One warp
+// a row (D / 4 lanes of it), so that the whole machine merges.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa, int pieces)
+{
+    const AttnArgs &a = pa.a;
+    const int np = pa.n_pairs;
+    constexpr int LPR = D / 4;
+    const int lane = threadIdx.x % LPR;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;   // row of the unit line
+    const int64_t per_head = static_cast<int64_t>(np) * 2 * kPM;
+    const int64_t list = i / per_head;
+    if (list >= static_cast<int64_t>(a.L.S) * a.L.Hk) return;
+    const int s = static_cast<int>(list / a.L.Hk), kh = static_cast<int>(list % a.L.Hk);
+    const int row = static_cast<int>(i % per_head);
+    const int pr = row / (2 * kPM);
+    if (row >= a.rows) return;
+    const int64_t e0 = static_cast<int64_t>(s) * np, e = e0 + pr;
+    const uint32_t total = __ldcg(pa.plan + static_cast<int64_t>(a.L.S) * np) * a.L.Hk;
+    const uint32_t p0 = __ldcg(pa.plan + e0), pe = __ldcg(pa.plan + e), pe1 = __ldcg(pa.plan + e + 1);
+    const uint32_t T = __ldcg(pa.plan + e0 + np) - p0;
+    if (pe1 == pe) return;
+    const uint32_t chunk = piece_tiles(total, pieces);
+    const uint32_t unit0 = p0 * a.L.Hk + kh * T + (pe - p0);
+    const uint32_t c_lo = unit0 / chunk, c_hi = (unit0 + (pe1 - pe) - 1) / chunk;
+    if (c_lo == c_hi) return;
+    auto at_of = [&](uint32_t c) {
+        return (2 * static_cast<int64_t>(c) + (c == c_lo && unit0 > c * chunk ? 1 : 0)) * 2 * kPM + row % (2 * kPM);
+    };
+    float M = -INFINITY;
+    for (uint32_t c = c_lo; c <= c_hi; ++c) M = fmaxf(M, __ldcg(a.part_ml + at_of(c)));
+    float W = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (M != -INFINITY) {
+#pragma unroll 4
+        for (uint32_t c = c_lo; c <= c_hi; ++c) {
+            const float w = fast_exp2(__ldcg(a.part_ml + at_of(c)) - M);
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at_of(c) * D) + lane);
+            W += w;
+            v[0] = fmaf(w, y.x, v[0]);
+            v[1] = fmaf(w, y.y, v[1]);
+            v[2] = fmaf(w, y.z, v[2]);
+            v[3] = fmaf(w, y.w, v[3]);
+        }
+        const float q = 1.f / W;
+        for (int e4 = 0; e4 < 4; ++e4) v[e4] *= q;
+    }
+    const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
+    if (pa.out_f16)
+        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + lane * 4) =
+            make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + lane * 4) = make_float4(v[0], v[1], v[2], v[3]);
+    if (lane == 0) a.lse[r] = M == -INFINITY ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
 }
 
 // Attention weight of each page from the log sums of its rows: one warp a page,
@@ -686,12 +823,15 @@ static int launch_one(skv_handle *h, const PrefillArgs &pa, int grid, cudaStream
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(8-bit prefill)");
     if (h->prof_before) cudaEventRecord(h->prof_before, st);
     prefill_kernel<D, HILO><<<grid, kPfThreads, smem, st>>>(pa);
-    const cudaError_t l = cudaGetLastError();
+    cudaError_t l = cudaGetLastError();
     if (h->prof_after) cudaEventRecord(h->prof_after, st);
-    return cuda_fail(h, l, "8-bit prefill launch");
+    if (l != cudaSuccess) return cuda_fail(h, l, "8-bit prefill launch");
+    const int64_t rows = static_cast<int64_t>(pa.a.L.S) * pa.a.L.Hk * pa.n_pairs * 2 * kPM;
+    prefill_merge_kernel<D><<<static_cast<unsigned>((rows * (D / 4) + 255) / 256), 256, 0, st>>>(pa, grid);
+    return cuda_fail(h, cudaGetLastError(), "8-bit prefill merge launch");
 }
 
-int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, int64_t *plan, int n_pairs, float *mass, int grid,
+int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, uint32_t *plan, int n_pairs, float *mass, int grid,
                    cudaStream_t st)
 {
     prefill_plan_kernel<<<1, 1024, 0, st>>>(a, n_pairs, plan);
