@@ -554,98 +554,85 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                 // then invalid and the status word says so).
 #pragma unroll 1
                 for (int jj = 0; jj < n; ++jj, ++j, ++tiles, lim -= kPN, pages -= 2) {
+                    // what does not depend on the scores first: the pages' factors and reference
+                    __all_sync(0xffffffffu, wait(PB_META + static_cast<int>(j & 3), (j >> 2) & 1));
+                    const Meta mt0 = s_meta[j & 3][0], mt1 = s_meta[j & 3][1];
+                    const float r_old = r_ref;
+                    const float lv_max = fmaxf(mt0.lv, mt1.lv);             // (-inf where there is no page)
+                    if (lv_max > r_ref + kPfScaleGrow) r_ref = ceilf(lv_max);
+                    const float dl0 = mt0.lv == -INFINITY ? kNoScale : fmaxf(mt0.lv - r_ref, kNoScale);
+                    const float dl1 = mt1.lv == -INFINITY ? kNoScale : fmaxf(mt1.lv - r_ref, kNoScale);
+                    const float un0 = fast_exp2(-dl0), un1 = fast_exp2(-dl1);
+                    const int lim0 = mt0.on ? lim : 0, lim1 = mt1.on ? lim - kPage : 0;
+                    const bool masked = __any_sync(0xffffffffu, lim0 < kPage || lim1 < kPage);
                     __all_sync(0xffffffffu, wait(PB_SFULL + g, tiles & 1));
                     tc::tc_fence_after();
-                    // 32 columns at a time, the next ones on their way: their largest score,
-                    // their weights against the reference as it stands then, and these
-                    // stored over their own scores (keys 32c .. in columns 32c .., what
-                    // rounding left 16 further on).
+                    // The row's largest score, 32 columns at a time, the next ones on their way;
+                    // masked ones go back as -inf.
                     uint32_t xr[2][32];
+                    float top[2];
                     tc::tmem_ld32(s_col, xr[0]);
-                    __all_sync(0xffffffffu, wait(PB_META + static_cast<int>(j & 3), (j >> 2) & 1));
-                    const Meta *mt2 = s_meta[j & 3];
-                    // the pages' reference
-                    const float r_old = r_ref;
-                    const float lv_max = fmaxf(mt2[0].lv, mt2[1].lv);       // (-inf where there is no page)
-                    if (lv_max > r_ref + kPfScaleGrow) r_ref = ceilf(lv_max);
-                    float ref = m_ref, ls = 0.f, lh = 0.f;
-                    const bool masked = __any_sync(0xffffffffu, lim < kPN);
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const Meta mt = mt2[h];
-                        const float dl = mt.lv == -INFINITY ? kNoScale : fmaxf(mt.lv - r_ref, kNoScale);
-                        const float un = fast_exp2(-dl);
 #pragma unroll
-                        for (int cc = 0; cc < 2; ++cc) {
-                            const int c = 2 * h + cc;
-                            uint32_t(&xc)[32] = xr[cc];
-                            tc::tmem_wait_ld(xc);
-                            if (c < 3) tc::tmem_ld32(s_col + (c + 1) * 32, xr[cc ^ 1]);
-                            if (masked || !mt.on) {
-                                const int lc = mt.on ? lim - c * 32 : 0;
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t(&xc)[32] = xr[c & 1];
+                        tc::tmem_wait_ld(xc);
+                        if (c < 3) tc::tmem_ld32(s_col + (c + 1) * 32, xr[(c + 1) & 1]);
+                        if (masked) {
+                            const int lc = (c < 2 ? lim0 : lim1) - (c & 1) * 32;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i >= lc) xc[i] = 0xff800000u;
-                            }
-                            auto X = [&](int i) { return __uint_as_float(xc[i]); };
-                            float mq[4] = {X(0), X(1), X(2), X(3)};
-#pragma unroll
-                            for (int i = 4; i < 28; i += 8)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) mq[e] = max3(mq[e], X(i + e), X(i + e + 4));
-                            const float mx = fmaxf(max3(max3(mq[0], X(28), X(29)), max3(mq[1], X(30), X(31)), mq[2]), mq[3]) * mt.ks;
-                            const float prev = ref;
-                            if (mx > ref + kPfGrow) ref = ceilf(mx);  // true on the first finite maximum
-                            const float off = ref == -INFINITY ? 0.f : kPfShift + dl - ref;
-                            if (c > 0 && __any_sync(0xffffffffu, ref != prev)) {
-                                // the weights stored above to the moved reference, by two exact
-                                // factors, as fp16 has none below 2^-24
-                                const float e = ref == prev ? 0.f : prev == -INFINITY ? -28.f : fmaxf(prev - ref, -28.f);
-                                const float beta = ref == prev ? 1.f : prev == -INFINITY ? 0.f : fast_exp2(prev - ref);
-                                const __half2 b0 = __float2half2_rn(fast_exp2(fmaxf(e, -14.f)));
-                                const __half2 b1 = __float2half2_rn(fast_exp2(fminf(e + 14.f, 0.f)));
-                                ls *= beta;
-                                lh *= beta;
-                                tc::tmem_wait_st();
-#pragma unroll 1
-                                for (int d = 0; d < (HILO ? 2 * c : c); ++d) {
-                                    const uint32_t at = s_col + d * (HILO ? 16 : 32);
-                                    uint32_t pr[16];
-                                    tc::tmem_ld16(at, pr);
-                                    tc::tmem_wait_ld16(pr);
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) {
-                                        const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&pr[i]), b0), b1);
-                                        pr[i] = *reinterpret_cast<const uint32_t *>(&v);
-                                    }
-                                    tc::tmem_st16u(at, pr);
-                                }
-                            }
-                            float lq[4] = {0.f, 0.f, 0.f, 0.f};
-                            uint32_t hi[16], lo[16];
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float w0, w1;
-                                fma2(w0, w1, X(i), X(i + 1), mt.ks, off);
-                                w0 = fast_exp2(w0);
-                                w1 = fast_exp2(w1);
-                                add2(lq[i & 2], lq[(i & 2) + 1], w0, w1);
-                                hi[i >> 1] = pack_half2(w0, w1);
-                                if (HILO) {
-                                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i >> 1]));
-                                    lo[i >> 1] = pack_half2(w0 - back.x, w1 - back.y);
-                                }
-                            }
-                            tc::tmem_st16u(s_col + c * 32, hi);
-                            if (HILO) tc::tmem_st16u(s_col + c * 32 + 16, lo);
-                            lh += ((lq[0] + lq[1]) + (lq[2] + lq[3])) * un;
+                            for (int i = 0; i < 32; ++i)
+                                if (i >= lc) xc[i] = 0xff800000u;
+                            tc::tmem_st32u(s_col + c * 32, xc);
                         }
-                        if (pl) {
-                            if (h < pages) *pl = lh > 0.f ? ref - kPfShift + log2f(lh) : -INFINITY;
-                            pl += a.rows;
+                        auto X = [&](int i) { return __uint_as_float(xc[i]); };
+                        float mq[4] = {X(0), X(1), X(2), X(3)};
+#pragma unroll
+                        for (int i = 4; i < 28; i += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mq[e] = max3(mq[e], X(i + e), X(i + e + 4));
+                        const float mx = fmaxf(max3(max3(mq[0], X(28), X(29)), max3(mq[1], X(30), X(31)), mq[2]), mq[3]);
+                        top[c >> 1] = (c & 1) ? fmaxf(top[c >> 1], mx) : mx;
+                    }
+                    if (masked) tc::tmem_wait_st();
+                    tc::tmem_ld32(s_col, xr[0]);
+                    float ref = m_ref;
+                    const float mx = fmaxf(top[0] * mt0.ks, top[1] * mt1.ks);
+                    if (mx > ref + kPfGrow) ref = ceilf(mx);        // true on the first finite maximum
+                    const float off = ref == -INFINITY ? 0.f : kPfShift - ref;
+                    // The weights, stored over their own scores (keys 32c .. in columns 32c ..,
+                    // what rounding left 16 further on).
+                    float lq[2][4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t(&xc)[32] = xr[c & 1];
+                        const float ks = c < 2 ? mt0.ks : mt1.ks, of = off + (c < 2 ? dl0 : dl1);
+                        tc::tmem_wait_ld(xc);
+                        if (c < 3) tc::tmem_ld32(s_col + (c + 1) * 32, xr[(c + 1) & 1]);
+                        float(&l4)[4] = lq[c >> 1];
+                        if ((c & 1) == 0) l4[0] = l4[1] = l4[2] = l4[3] = 0.f;
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float w0, w1;
+                            fma2(w0, w1, __uint_as_float(xc[i]), __uint_as_float(xc[i + 1]), ks, of);
+                            w0 = fast_exp2(w0);
+                            w1 = fast_exp2(w1);
+                            add2(l4[i & 2], l4[(i & 2) + 1], w0, w1);
+                            hi[i >> 1] = pack_half2(w0, w1);
+                            if (HILO) {
+                                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i >> 1]));
+                                lo[i >> 1] = pack_half2(w0 - back.x, w1 - back.y);
+                            }
                         }
-                        ls += lh;
-                        lh = 0.f;
+                        tc::tmem_st16u(s_col + c * 32, hi);
+                        if (HILO) tc::tmem_st16u(s_col + c * 32 + 16, lo);
+                    }
+                    const float ls0 = ((lq[0][0] + lq[0][1]) + (lq[0][2] + lq[0][3])) * un0;
+                    const float ls1 = ((lq[1][0] + lq[1][1]) + (lq[1][2] + lq[1][3])) * un1;
+                    if (pl) {
+                        if (pages > 0) pl[0] = ls0 > 0.f ? ref - kPfShift + log2f(ls0) : -INFINITY;
+                        if (pages > 1) pl[a.rows] = ls1 > 0.f ? ref - kPfShift + log2f(ls1) : -INFINITY;
+                        pl += 2 * static_cast<int64_t>(a.rows);
                     }
                     const float alpha = ref == m_ref ? 1.f : (m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref));
                     const float alpha_o = r_ref == r_old ? alpha : (r_old == -INFINITY ? 0.f : alpha * fast_exp2(r_old - r_ref));
@@ -663,7 +650,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                             tc::tmem_st32(o_col + c * 32, v);
                         }
                     }
-                    l_run = l_run * alpha + ls;
+                    l_run = l_run * alpha + (ls0 + ls1);
                     m_ref = ref;
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
