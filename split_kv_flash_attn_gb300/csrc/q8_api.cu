@@ -143,12 +143,13 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     // Tokens of one launch: as many as the kernels' counters have units for, and as
     // keep the pages' log sums within kMassScratch (at least one).
     const int64_t heads = static_cast<int64_t>(shape->S) * shape->Hk;
+    constexpr int64_t max_units = kMaxUnits - 1;          // (a grid's y)
     int64_t nq_max = shape->nq;
     const int rows1 = sel ? a.G : 0;                      // rows of a unit that do not grow with the tokens
     const int nc = (sel ? a.G : static_cast<int64_t>(shape->nq) * a.G) <= 8 ? 1 : 2;
     const int64_t unit_rows = tc ? 256 : 8 * nc;
-    if (sel) nq_max = std::min(nq_max, kMaxUnits / std::max<int64_t>(1, heads * ((a.G + unit_rows - 1) / unit_rows)));
-    else nq_max = std::min(nq_max, (kMaxUnits / heads) * unit_rows / a.G);
+    if (sel) nq_max = std::min(nq_max, max_units / std::max<int64_t>(1, heads * ((a.G + unit_rows - 1) / unit_rows)));
+    else nq_max = std::min(nq_max, (max_units / heads) * unit_rows / a.G);
     const int64_t per_list = sel ? n_sel : pages_per_list;
     if (tc) {
         // the tensor-core kernel counts key tiles of a launch in 32 bits

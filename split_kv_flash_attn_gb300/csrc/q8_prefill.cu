@@ -24,14 +24,16 @@
 // While one tile's softmax runs, the tensor core works for the other.
 //
 // Work split.  All key tiles of all (sequence, KV head, tile pair) units form one
-// line (its prefix sums come from a one-CTA plan kernel, which reads lengths and
-// query positions on the device), cut into one equal piece for each CTA; units that several
+// line (its prefix sums are taken from the lengths and query positions on the
+// device, by a one-CTA kernel where they are many), cut into one equal piece for each CTA; units that several
 // pieces share are merged by a kernel of a warp a row, in piece order (by the last
 // CTA of each unit that took 60 to 100 us).
 //
 // Tensor memory: S_0/W_0 in columns 0-127, S_1/W_1 128-255, O_0 256-383, O_1
 // 384-511.  Every mbarrier wait is bounded; one that gives up sets the handle's
 // device status word, the CTA drains what it issued and frees its tensor memory.
+#include <algorithm>
+
 #include "q8.cuh"
 
 namespace skv {
@@ -47,9 +49,9 @@ constexpr int kPfThreads = (kMmaWarp + 4) * 32;
 // take what the others can spare (spilled, they would go to an L1 of 20 KB:
 // 396 us against PFTIME at 512 tokens over 32768 keys).
 #ifndef VRS
-#define VRS 168
+#define VRS 176
 #define VRP 104
-#define VRM 72
+#define VRM 56
 #endif
 constexpr int kRegSoft = VRS, kRegProd = VRP, kRegMma = VRM;
 static_assert(2 * kRegSoft + kRegProd + kRegMma <= 4 * 128, "no more than the launch has");
@@ -68,6 +70,7 @@ __device__ __forceinline__ void fewer_regs()
 #define VPT 3
 #endif
 constexpr uint32_t kPieceTiles = VPT;                // fewest key tiles of a piece: each costs set-up and merge
+constexpr int kPlanHere = 256;                  // plan entries that the prefill kernel counts itself
 constexpr int kPlanSmem = 1024;                 // plan entries kept in shared memory
 constexpr float kPfShift = 8.f, kPfGrow = 5.f, kPfScaleGrow = 2.f;
 constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a wait gives up (tens of ms at least)
@@ -90,16 +93,16 @@ static_assert(PfSmem<128>::kTotal <= 226 * 1024, "shared memory per CTA");
 // Barriers (+ stage or query tile g).  Key tile j of the CTA is phase j / 2 of its
 // K and V stages' barriers and j / 4 of its meta slot.  The t-th tile that query
 // tile g takes part in (not every unit has a second one) is phase t of its S full,
-// P full and PV done, the u-th such unit phase u of its Q full.  No waiter is ever
+// P half, P full and PV done, the u-th such unit phase u of its Q full.  No waiter is ever
 // two phases behind: each side needs the other's next step before it can complete
 // another phase, and the softmax groups enter every unit together, so that a
 // meta slot is rewritten (four tiles on) only after both have read it.
 enum { PB_KFULL = 0, PB_KEMPTY = 2, PB_VFULL = 4, PB_VEMPTY = 6, PB_QFULL = 8, PB_SFULL = 10, PB_PFULL = 12,
-       PB_PDONE = 14, PB_META = 16, PB_COUNT = 20 };
+       PB_PDONE = 14, PB_META = 16, PB_PHALF = 20, PB_COUNT = 22 };
 
 struct PrefillArgs {
     AttnArgs a;
-    const uint32_t *plan;                       // [S * n_pairs + 1] tiles before each (sequence, pair)
+    uint32_t *plan;                             // [S * n_pairs + 1] tiles before each (sequence, pair)
     int n_pairs;
     int out_f16;
 };
@@ -111,29 +114,42 @@ __host__ __device__ inline uint32_t piece_tiles(uint32_t total, uint32_t ctas)
     return c < kPieceTiles ? kPieceTiles : c;
 }
 
-// Tiles of each (sequence, pair of query tiles): up to its last visible key; prefix
-// sums over all of them.
+// Key tiles of (sequence, pair of query tiles) e: up to its last visible key.  For
+// a whole warp.
+__device__ __forceinline__ uint32_t entry_tiles(const AttnArgs &a, int n_pairs, int64_t e)
+{
+    const int lane = threadIdx.x & 31;
+    const int s = static_cast<int>(e / n_pairs), pr = static_cast<int>(e % n_pairs);
+    int keys = static_cast<int>(list_len(a.L, s));
+    if (a.q_pos) {
+        const int t0 = static_cast<int>(2 * kPM * static_cast<int64_t>(pr) / a.G);
+        const int t1 = static_cast<int>(min(int64_t(a.nq - 1), (2 * kPM * (static_cast<int64_t>(pr) + 1) - 1) / a.G));
+        int top = -1;
+        for (int t = t0 + lane; t <= t1; t += 32) top = max(top, __ldg(a.q_pos + a.token(s, t)));
+        top = __reduce_max_sync(0xffffffffu, top);
+        keys = top < 0 ? 0 : (top < keys ? top + 1 : keys);
+    }
+    return (static_cast<uint32_t>(keys) + kPN - 1) / kPN;
+}
+
+// Sets the status bit of lengths beyond their lists; `t` of `n` threads.
+__device__ __forceinline__ void check_lengths(const AttnArgs &a, int t, int n)
+{
+    for (int s = t; s < a.L.S; s += n)
+        if (list_len(a.L, s) < max(0, a.L.kv_len[s])) atomicOr(a.L.status, kStatusList);
+}
+
+// The plan of many entries: prefix sums of their tiles.
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, int n_pairs, uint32_t *plan)
 {
     __shared__ uint32_t s_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t n = static_cast<int64_t>(a.L.S) * n_pairs;
-    for (int64_t e = warp; e < n; e += 32) {            // one warp an entry
-        const int s = static_cast<int>(e / n_pairs), pr = static_cast<int>(e % n_pairs);
-        int64_t keys = list_len(a.L, s);
-        if (a.q_pos) {
-            const int t0 = static_cast<int>(2 * kPM * static_cast<int64_t>(pr) / a.G);
-            const int t1 = static_cast<int>(min(int64_t(a.nq - 1), (2 * kPM * (static_cast<int64_t>(pr) + 1) - 1) / a.G));
-            int top = -1;
-            for (int t = t0 + lane; t <= t1; t += 32) top = max(top, __ldg(a.q_pos + a.token(s, t)));
-            top = __reduce_max_sync(0xffffffffu, top);
-            keys = max(int64_t(0), min(keys, static_cast<int64_t>(top) + 1));
-        }
-        if (lane == 0) {
-            plan[e] = static_cast<uint32_t>((keys + kPN - 1) / kPN);
-            if (pr == 0 && list_len(a.L, s) < max(0, a.L.kv_len[s])) atomicOr(a.L.status, kStatusList);
-        }
+    for (int64_t e = warp; e < n; e += 32) {
+        const uint32_t x = entry_tiles(a, n_pairs, e);
+        if (lane == 0) plan[e] = x;
     }
+    check_lengths(a, tid, 1024);
     __syncthreads();
     const int64_t share = (n + 1023) / 1024, lo = min(n, tid * share), hi = min(n, lo + share);
     uint32_t sum = 0;
@@ -240,6 +256,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     __shared__ Meta s_meta[4][2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ Unit s_unit[kSoftWarps][2];      // the softmax warps' units: kept out of their registers
     const uint32_t bar0 = smem_addr(s_bar);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     constexpr uint32_t kIdescS = tc::idesc_f16(kPM, kPN, false);
@@ -251,8 +268,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     const int np = pa.n_pairs;
     const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
     Walk walk{pa.plan, np, a.L.S, a.L.Hk, 0};
-    if (n_entries <= kPlanSmem) {
-        uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
+    uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
+    if (n_entries <= kPlanHere) {               // few entries: every CTA counts them itself
+        for (int e = warp; e < n_entries; e += kPfThreads / 32) {
+            const uint32_t x = entry_tiles(a, np, e);
+            if (lane == 0) s_plan[e] = x;
+        }
+        if (blockIdx.x == 0) check_lengths(a, tid, kPfThreads);
+        walk.plan = s_plan;
+    } else if (n_entries <= kPlanSmem) {
         for (int i = tid; i <= n_entries; i += kPfThreads) s_plan[i] = __ldcg(pa.plan + i);
         walk.plan = s_plan;
     }
@@ -270,6 +294,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             tc::mbar_init(bar(PB_QFULL + i), kPM);
             tc::mbar_init(bar(PB_SFULL + i), 1);
             tc::mbar_init(bar(PB_PFULL + i), kPM);
+            tc::mbar_init(bar(PB_PHALF + i), kPM);
             tc::mbar_init(bar(PB_PDONE + i), 1);
         }
         for (int i = 0; i < 4; ++i) tc::mbar_init(bar(PB_META + i), 2);
@@ -279,6 +304,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
+    if (n_entries <= kPlanHere) {               // their prefix sums; the merge reads CTA 0's
+        if (warp == 0) {
+            uint32_t before = 0;
+            for (int b = 0; b < n_entries; b += 32) {
+                const uint32_t x = b + lane < n_entries ? s_plan[b + lane] : 0u;
+                uint32_t inc = x;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                if (b + lane < n_entries) s_plan[b + lane] = before + inc - x;
+                before += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0) s_plan[n_entries] = before;
+        }
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int i = tid; i <= n_entries; i += kPfThreads) pa.plan[i] = s_plan[i];
+    }
 
     const uint32_t total = walk.plan[n_entries] * a.L.Hk;
     const uint32_t chunk = piece_tiles(total, gridDim.x);
@@ -449,18 +494,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll 1
                     for (int g = 0; g < (two ? 2 : 1); ++g) {
                         const uint32_t t = g ? tiles1++ : tiles0++;
-                        if (!(ok = all(wait(PB_PFULL + g, t & 1)))) break;
+                        // the second 64 keys first, as the softmax does
+                        if (!(ok = all(wait(PB_PHALF + g, t & 1)))) break;
                         tc::tc_fence_after();
                         const uint64_t bd = tc::desc_add(dv0, b * SM::kTile);
                         const uint32_t d_w = tmem + static_cast<uint32_t>(g * kPN);
                         const uint32_t d_o = tmem + static_cast<uint32_t>(kOCol + g * D);
-                        if (tc::elect_one()) {
+                        auto products = [&](int k0, bool from0) {
 #pragma unroll
-                            for (int kk = 0; kk < kPN / 16; ++kk) {
+                            for (int i = 0; i < kPN / 32; ++i) {
+                                const int kk = k0 + i;
                                 const uint32_t at = d_w + static_cast<uint32_t>((kk >> 1) * 32 + (kk & 1) * 8);
-                                tc::mma_f16_ts(d_o, at, tc::desc_add(bd, kk * 2048), kIdescPV, (tl > x.t0 || kk > 0) ? 1u : 0u);
+                                tc::mma_f16_ts(d_o, at, tc::desc_add(bd, kk * 2048), kIdescPV, (from0 && i == 0) ? 0u : 1u);
                                 if (HILO) tc::mma_f16_ts(d_o, at + 16, tc::desc_add(bd, kk * 2048), kIdescPV, 1u);
                             }
+                        };
+                        if (tc::elect_one()) products(kPN / 32, tl == x.t0);
+                        __syncwarp();
+                        if (!(ok = all(wait(PB_PFULL + g, t & 1)))) break;
+                        tc::tc_fence_after();
+                        if (tc::elect_one()) {
+                            products(0, false);
                             tc::mma_commit(bar(PB_PDONE + g));
                             if (g == 1 || !two) tc::mma_commit(bar(PB_VEMPTY + b));
                         }
@@ -521,20 +575,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             tc::mbar_arrive(bar(PB_QFULL + g));
         };
         uint32_t j = 0, tiles = 0;              // key tiles so far, and those with this query tile
-        Unit x = {};
-        int64_t index = -1;
         if (any) {
-            x = walk.first(pos0);
-            index = row_index(x);
-            if (active(x)) put_q(index);
+            if (lane == 0) s_unit[warp][0] = walk.first(pos0);
+            __syncwarp();
+            if (active(s_unit[warp][0])) put_q(row_index(s_unit[warp][0]));
         }
-        for (bool more = any; more;) {
+        bool more = any;
+#pragma unroll 1
+        for (int u = 0; more; u ^= 1) {
             meet();
+            const Unit &x = s_unit[warp][u];
             const bool tile_on = active(x);
             const int n = x.t1 - x.t0;
-            const int64_t out = index;
-            const bool whole = n == x.n;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x.unit0 + x.t0 == pos0 ? 0 : 1);
             float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
             if (tile_on) {
                 const int row = (2 * x.pr + g) * kPM + m;
@@ -567,66 +619,86 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                     const bool masked = __any_sync(0xffffffffu, lim0 < kPage || lim1 < kPage);
                     __all_sync(0xffffffffu, wait(PB_SFULL + g, tiles & 1));
                     tc::tc_fence_after();
-                    // The row's largest score, 32 columns at a time, the next ones on their way;
-                    // masked ones go back as -inf.
+                    // The row's largest score, which the loads bring along; masked ones go
+                    // back as -inf first.
                     uint32_t xr[2][32];
-                    float top[2];
-                    tc::tmem_ld32(s_col, xr[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t(&xc)[32] = xr[c & 1];
-                        tc::tmem_wait_ld(xc);
-                        if (c < 3) tc::tmem_ld32(s_col + (c + 1) * 32, xr[(c + 1) & 1]);
-                        if (masked) {
+                    float top[4];
+                    if (masked) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
                             const int lc = (c < 2 ? lim0 : lim1) - (c & 1) * 32;
+                            tc::tmem_ld32(s_col + c * 32, xr[0]);
+                            tc::tmem_wait_ld(xr[0]);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (i >= lc) xc[i] = 0xff800000u;
-                            tc::tmem_st32u(s_col + c * 32, xc);
+                                if (i >= lc) xr[0][i] = 0xff800000u;
+                            tc::tmem_st32u(s_col + c * 32, xr[0]);
                         }
-                        auto X = [&](int i) { return __uint_as_float(xc[i]); };
-                        float mq[4] = {X(0), X(1), X(2), X(3)};
-#pragma unroll
-                        for (int i = 4; i < 28; i += 8)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) mq[e] = max3(mq[e], X(i + e), X(i + e + 4));
-                        const float mx = fmaxf(max3(max3(mq[0], X(28), X(29)), max3(mq[1], X(30), X(31)), mq[2]), mq[3]);
-                        top[c >> 1] = (c & 1) ? fmaxf(top[c >> 1], mx) : mx;
+                        tc::tmem_wait_st();
                     }
-                    if (masked) tc::tmem_wait_st();
-                    tc::tmem_ld32(s_col, xr[0]);
-                    float ref = m_ref;
-                    const float mx = fmaxf(top[0] * mt0.ks, top[1] * mt1.ks);
-                    if (mx > ref + kPfGrow) ref = ceilf(mx);        // true on the first finite maximum
-                    const float off = ref == -INFINITY ? 0.f : kPfShift - ref;
-                    // The weights, stored over their own scores (keys 32c .. in columns 32c ..,
-                    // what rounding left 16 further on).
-                    float lq[2][4];
+                    tc::tmem_ld32_max(s_col, xr[0], top[0]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
+                        tc::tmem_wait_ld_max(xr[c & 1], top[c]);
+                        if (c < 3) tc::tmem_ld32_max(s_col + (c + 1) * 32, xr[(c + 1) & 1], top[c + 1]);
+                    }
+                    float ref = m_ref;
+                    const float mx = fmaxf(fmaxf(top[0], top[1]) * mt0.ks, fmaxf(top[2], top[3]) * mt1.ks);
+                    if (mx > ref + kPfGrow) ref = ceilf(mx);        // true on the first finite maximum
+                    const float off = ref == -INFINITY ? 0.f : kPfShift - ref;
+                    const float alpha = ref == m_ref ? 1.f : (m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref));
+                    const float alpha_o = r_ref == r_old ? alpha : (r_old == -INFINITY ? 0.f : alpha * fast_exp2(r_old - r_ref));
+                    // O_g holds every PV up to the last tile (S_g was issued after
+                    // it was done) and none of this tile before its weights are announced
+                    if (jj > 0 && __any_sync(0xffffffffu, alpha_o != 1.f)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t rr[16];
+                            tc::tmem_ld16(o_col + c * 16, rr);
+                            tc::tmem_wait_ld16(rr);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha_o);
+                            tc::tmem_st16u(o_col + c * 16, rr);
+                        }
+                    }
+                    // The weights, stored over their own scores (keys 32c .. in columns 32c ..,
+                    // what rounding left 16 further on): the second page's, which are in
+                    // registers, then the first's; each half is announced by itself.
+                    float lq[2][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = i ^ 2;
                         uint32_t(&xc)[32] = xr[c & 1];
                         const float ks = c < 2 ? mt0.ks : mt1.ks, of = off + (c < 2 ? dl0 : dl1);
-                        tc::tmem_wait_ld(xc);
-                        if (c < 3) tc::tmem_ld32(s_col + (c + 1) * 32, xr[(c + 1) & 1]);
+                        if (i >= 2) tc::tmem_wait_ld(xc);
                         float(&l4)[4] = lq[c >> 1];
                         if ((c & 1) == 0) l4[0] = l4[1] = l4[2] = l4[3] = 0.f;
                         uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int e = 0; e < 32; e += 2) {
                             float w0, w1;
-                            fma2(w0, w1, __uint_as_float(xc[i]), __uint_as_float(xc[i + 1]), ks, of);
+                            fma2(w0, w1, __uint_as_float(xc[e]), __uint_as_float(xc[e + 1]), ks, of);
                             w0 = fast_exp2(w0);
                             w1 = fast_exp2(w1);
-                            add2(l4[i & 2], l4[(i & 2) + 1], w0, w1);
-                            hi[i >> 1] = pack_half2(w0, w1);
+                            add2(l4[e & 2], l4[(e & 2) + 1], w0, w1);
+                            hi[e >> 1] = pack_half2(w0, w1);
                             if (HILO) {
-                                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i >> 1]));
-                                lo[i >> 1] = pack_half2(w0 - back.x, w1 - back.y);
+                                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e >> 1]));
+                                lo[e >> 1] = pack_half2(w0 - back.x, w1 - back.y);
                             }
                         }
+                        if (i < 2) tc::tmem_ld32(s_col + i * 32, xc);
                         tc::tmem_st16u(s_col + c * 32, hi);
                         if (HILO) tc::tmem_st16u(s_col + c * 32 + 16, lo);
+                        if (i == 1) {
+                            tc::tmem_wait_st();
+                            tc::tc_fence_before();
+                            tc::mbar_arrive(bar(PB_PHALF + g));
+                        }
                     }
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(bar(PB_PFULL + g));
                     const float ls0 = ((lq[0][0] + lq[0][1]) + (lq[0][2] + lq[0][3])) * un0;
                     const float ls1 = ((lq[1][0] + lq[1][1]) + (lq[1][2] + lq[1][3])) * un1;
                     if (pl) {
@@ -634,39 +706,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                         if (pages > 1) pl[a.rows] = ls1 > 0.f ? ref - kPfShift + log2f(ls1) : -INFINITY;
                         pl += 2 * static_cast<int64_t>(a.rows);
                     }
-                    const float alpha = ref == m_ref ? 1.f : (m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref));
-                    const float alpha_o = r_ref == r_old ? alpha : (r_old == -INFINITY ? 0.f : alpha * fast_exp2(r_old - r_ref));
-                    // O_g holds every PV up to the last tile (S_g was issued after
-                    // it was done) and none of this tile before W_g is full
-                    if (jj > 0 && __any_sync(0xffffffffu, alpha_o != 1.f)) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t rr[32];
-                            tc::tmem_ld32(o_col + c * 32, rr);
-                            tc::tmem_wait_ld(rr);
-                            float v[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(rr[i]) * alpha_o;
-                            tc::tmem_st32(o_col + c * 32, v);
-                        }
-                    }
                     l_run = l_run * alpha + (ls0 + ls1);
                     m_ref = ref;
-                    tc::tmem_wait_st();
-                    tc::tc_fence_before();
-                    tc::mbar_arrive(bar(PB_PFULL + g));
                 }
             } else {
                 j += n;
             }
             // the next unit's queries go in while this one's last product runs: S_g of
             // the last tile is done, and nothing else reads Q_g
-            more = walk.next(x);
-            if (more) {
-                index = row_index(x);
-                if (active(x)) put_q(index);
+            {
+                int again = 0;
+                if (lane == 0) {
+                    Unit y = x;
+                    again = walk.next(y);
+                    s_unit[warp][u ^ 1] = y;
+                }
+                more = __shfl_sync(0xffffffffu, again, 0) != 0;
+                if (more && active(s_unit[warp][u ^ 1])) put_q(row_index(s_unit[warp][u ^ 1]));
             }
             if (!tile_on) continue;
+            const int64_t out = row_index(x);
+            const bool whole = n == x.n;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x.unit0 + x.t0 == pos0 ? 0 : 1);
             // ---------------- O / l, lse: result or piece ------------------------------
             bool have = wait(PB_PDONE + g, (tiles - 1) & 1) && !*reinterpret_cast<volatile int *>(&s_abort);
             have = __all_sync(0xffffffffu, have);
@@ -723,59 +784,67 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     }
 }
 
-// Rows of units that several CTAs share: their pieces together, in order.  One warp
-// a row (D / 4 lanes of it), so that the whole machine merges.
+// Rows of units that several CTAs share: their pieces together, in order.  One CTA
+// takes 32 rows of a unit, D / 4 lanes a row, so that the whole machine merges.
+constexpr int kMergeRows = 32;
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa, int pieces)
 {
     const AttnArgs &a = pa.a;
+    constexpr int LPR = D / 4, RPP = 256 / LPR;
     const int np = pa.n_pairs;
-    constexpr int LPR = D / 4;
-    const int lane = threadIdx.x % LPR;
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;   // row of the unit line
-    const int64_t per_head = static_cast<int64_t>(np) * 2 * kPM;
-    const int64_t list = i / per_head;
-    if (list >= static_cast<int64_t>(a.L.S) * a.L.Hk) return;
-    const int s = static_cast<int>(list / a.L.Hk), kh = static_cast<int>(list % a.L.Hk);
-    const int row = static_cast<int>(i % per_head);
-    const int pr = row / (2 * kPM);
-    if (row >= a.rows) return;
-    const int64_t e0 = static_cast<int64_t>(s) * np, e = e0 + pr;
+    const int unit = blockIdx.y, list = unit / np, pr = unit - list * np;
+    const int s = list / a.L.Hk, kh = list - s * a.L.Hk;
+    const int64_t e0 = static_cast<int64_t>(s) * np;
     const uint32_t total = __ldcg(pa.plan + static_cast<int64_t>(a.L.S) * np) * a.L.Hk;
-    const uint32_t p0 = __ldcg(pa.plan + e0), pe = __ldcg(pa.plan + e), pe1 = __ldcg(pa.plan + e + 1);
+    const uint32_t p0 = __ldcg(pa.plan + e0), pe = __ldcg(pa.plan + e0 + pr), pe1 = __ldcg(pa.plan + e0 + pr + 1);
     const uint32_t T = __ldcg(pa.plan + e0 + np) - p0;
     if (pe1 == pe) return;
     const uint32_t chunk = piece_tiles(total, pieces);
     const uint32_t unit0 = p0 * a.L.Hk + kh * T + (pe - p0);
     const uint32_t c_lo = unit0 / chunk, c_hi = (unit0 + (pe1 - pe) - 1) / chunk;
     if (c_lo == c_hi) return;
-    auto at_of = [&](uint32_t c) {
-        return (2 * static_cast<int64_t>(c) + (c == c_lo && unit0 > c * chunk ? 1 : 0)) * 2 * kPM + row % (2 * kPM);
-    };
-    float M = -INFINITY;
-    for (uint32_t c = c_lo; c <= c_hi; ++c) M = fmaxf(M, __ldcg(a.part_ml + at_of(c)));
-    float W = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (M != -INFINITY) {
+    const int lane = threadIdx.x % LPR;
+#pragma unroll 1
+    for (int i = 0; i < kMergeRows / RPP; ++i) {
+        const int rr = blockIdx.x * kMergeRows + i * RPP + threadIdx.x / LPR;   // row of the unit
+        const int row = pr * 2 * kPM + rr;
+        if (row >= a.rows) return;
+        // piece c of the unit is slot 2c, or 2c + 1 when an earlier unit begins CTA c's piece
+        auto at_of = [&](uint32_t c) {
+            return (2 * static_cast<int64_t>(c) + (c == c_lo && unit0 > c * chunk ? 1 : 0)) * 2 * kPM + rr;
+        };
+        float M = -INFINITY, W = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (uint32_t c = c_lo; c <= c_hi; ++c) {
-            const float w = fast_exp2(__ldcg(a.part_ml + at_of(c)) - M);
+            const float z = __ldcg(a.part_ml + at_of(c));
             const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at_of(c) * D) + lane);
+            if (z > M) {
+                const float b = fast_exp2(M - z);
+                M = z;
+                W *= b;
+                v[0] *= b;
+                v[1] *= b;
+                v[2] *= b;
+                v[3] *= b;
+            }
+            const float w = z == -INFINITY ? 0.f : fast_exp2(z - M);
             W += w;
             v[0] = fmaf(w, y.x, v[0]);
             v[1] = fmaf(w, y.y, v[1]);
             v[2] = fmaf(w, y.z, v[2]);
             v[3] = fmaf(w, y.w, v[3]);
         }
-        const float q = 1.f / W;
-        for (int e4 = 0; e4 < 4; ++e4) v[e4] *= q;
+        const float q = W > 0.f ? 1.f / W : 0.f;
+        const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
+        if (pa.out_f16)
+            *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + lane * 4) =
+                make_uint2(pack_half2(v[0] * q, v[1] * q), pack_half2(v[2] * q, v[3] * q));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + lane * 4) =
+                make_float4(v[0] * q, v[1] * q, v[2] * q, v[3] * q);
+        if (lane == 0) a.lse[r] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
     }
-    const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
-    if (pa.out_f16)
-        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + lane * 4) =
-            make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
-    else
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + lane * 4) = make_float4(v[0], v[1], v[2], v[3]);
-    if (lane == 0) a.lse[r] = M == -INFINITY ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
 }
 
 // Attention weight of each page from the log sums of its rows: one warp a page,
@@ -813,17 +882,20 @@ static int launch_one(skv_handle *h, const PrefillArgs &pa, int grid, cudaStream
     cudaError_t l = cudaGetLastError();
     if (h->prof_after) cudaEventRecord(h->prof_after, st);
     if (l != cudaSuccess) return cuda_fail(h, l, "8-bit prefill launch");
-    const int64_t rows = static_cast<int64_t>(pa.a.L.S) * pa.a.L.Hk * pa.n_pairs * 2 * kPM;
-    prefill_merge_kernel<D><<<static_cast<unsigned>((rows * (D / 4) + 255) / 256), 256, 0, st>>>(pa, grid);
+    const int units = pa.a.L.S * pa.a.L.Hk * pa.n_pairs;
+    const int rows = std::min(2 * kPM, pa.a.rows);
+    prefill_merge_kernel<D><<<dim3((rows + kMergeRows - 1) / kMergeRows, units), 256, 0, st>>>(pa, grid);
     return cuda_fail(h, cudaGetLastError(), "8-bit prefill merge launch");
 }
 
 int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, uint32_t *plan, int n_pairs, float *mass, int grid,
                    cudaStream_t st)
 {
-    prefill_plan_kernel<<<1, 1024, 0, st>>>(a, n_pairs, plan);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(h, e, "8-bit prefill plan launch");
+    if (static_cast<int64_t>(a.L.S) * n_pairs > kPlanHere) {
+        prefill_plan_kernel<<<1, 1024, 0, st>>>(a, n_pairs, plan);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(h, e, "8-bit prefill plan launch");
+    }
     const PrefillArgs pa{a, plan, n_pairs, f16};
     int rc;
     if (D == 128) rc = f16 ? launch_one<128, false>(h, pa, grid, st) : launch_one<128, true>(h, pa, grid, st);

@@ -133,7 +133,8 @@ def test_attention(h, lens, nq, H, Hk, D, causal, f16):
 PREFILL = [
     ([64], 33, 1, 1, 128, False), ([300], 64, 8, 2, 64, True), ([1000, 0, 300], 150, 8, 2, 128, True),
     ([700, 20], 33, 16, 1, 128, False), ([2000], 70, 40, 8, 64, True), ([5000, 129], 64, 8, 4, 128, True),
-    ([40], 100, 6, 2, 128, True), ([260] * 9, 72, 4, 1, 64, False),
+    ([40], 100, 6, 2, 128, True), ([260] * 9, 72, 4, 1, 64, False), ([70, 0, 131] * 100, 34, 1, 1, 64, True),
+    ([65] * 1100, 33, 1, 1, 64, False),
 ]
 
 
