@@ -381,13 +381,15 @@ class Q8Pool:
 
     def __init__(self, k, v, k_scale, v_scale, k_min, k_max):
         torch = _torch()
-        n, rows, D = (int(x) for x in k.shape)
+        if k.dim() != 3:
+            raise SplitKVError(1, f"k: want int8 [n_pages, {Q8_PAGE}, D], got {list(k.shape)}")
+        n, _, D = (int(x) for x in k.shape)
         want = [("k", k, torch.int8, (n, Q8_PAGE, D)), ("v", v, torch.int8, (n, Q8_PAGE, D)),
                 ("k_scale", k_scale, torch.float32, (n,)), ("v_scale", v_scale, torch.float32, (n,)),
                 ("k_min", k_min, torch.int8, (n, D)), ("k_max", k_max, torch.int8, (n, D))]
         for name, x, dtype, shape in want:
-            _need(name, x, dtype, shape, k.device)
-        self.n_pages, self.D, self.device = n, D, k.device
+            _need(name, x, dtype, shape, k.get_device())
+        self.n_pages, self.D, self.device, self.scale = n, D, k.get_device(), 1.0 / math.sqrt(max(1, D))
         self.k, self.v, self.k_scale, self.v_scale, self.k_min, self.k_max = k, v, k_scale, v_scale, k_min, k_max
         self._c = SkvQ8Pool(n, D, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                             k_min.data_ptr(), k_max.data_ptr())
@@ -405,29 +407,43 @@ class Q8Pool:
 
 
 def _need(name, x, dtype, shape, device):
-    """Raise SKV_EINVAL unless x is a contiguous tensor of this type, shape and device."""
-    if x.dtype != dtype or tuple(x.shape) != shape or x.device != device or not x.is_contiguous():
-        raise SplitKVError(1, f"{name}: want contiguous {dtype} {list(shape)} on {device}, got "
+    """Raise SKV_EINVAL unless x is a contiguous tensor of this type, shape and
+    device (an index, -1 for the CPU)."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
+        raise SplitKVError(1, f"{name}: want contiguous {dtype} {list(shape)} on device {device}, got "
                               f"{'' if x.is_contiguous() else 'non-contiguous '}{x.dtype} {list(x.shape)} on {x.device}")
 
 
 def _q8_stream(h, stream, device):
-    """The raw stream of a call over 8-bit pages (default: the pool's device's current one)."""
-    if device.type != "cuda" or device.index != h.device:
-        raise SplitKVError(1, f"tensors on {device}, handle on cuda:{h.device}")
+    """The raw stream of a call over 8-bit pages (default: the current one of the tensors' device)."""
+    if device != h.device:
+        raise SplitKVError(1, f"tensors on device {device}, handle on cuda:{h.device}")
     if stream is None:
-        return _torch().cuda.current_stream(device).cuda_stream
+        return _raw_stream()(device)
     return _stream(stream)
+
+
+_raw_stream_fn = None
+
+
+def _raw_stream():
+    global _raw_stream_fn
+    if _raw_stream_fn is None:
+        torch = _torch()
+        # the same number as torch.cuda.current_stream(device).cuda_stream, without the objects
+        _raw_stream_fn = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream_fn
 
 
 def _q8_lists(page_ids, kv_len, device):
     torch = _torch()
-    if page_ids.dim() != 3:
-        raise SplitKVError(1, f"page_ids: want int32 [S, Hk, pages_per_list], got {list(page_ids.shape)}")
-    S, Hk, cap = page_ids.shape
-    _need("page_ids", page_ids, torch.int32, (S, Hk, cap), device)
-    _need("kv_len", kv_len, torch.int32, (S,), device)
-    return S, Hk, cap
+    shape = page_ids.shape
+    if len(shape) != 3:
+        raise SplitKVError(1, f"page_ids: want int32 [S, Hk, pages_per_list], got {list(shape)}")
+    _need("page_ids", page_ids, torch.int32, shape, device)
+    _need("kv_len", kv_len, torch.int32, shape[:1], device)
+    return shape
 
 
 def _q8_query(pool, q, page_ids, kv_len, q_pos, scale):
@@ -435,12 +451,11 @@ def _q8_query(pool, q, page_ids, kv_len, q_pos, scale):
     S, Hk, cap = _q8_lists(page_ids, kv_len, pool.device)
     if q.dim() != 4:
         raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(q.shape)}")
-    nq, H = q.shape[1], q.shape[2]
+    _, nq, H, _ = q.shape
     _need("q", q, torch.float16, (S, nq, H, pool.D), pool.device)
     if q_pos is not None:
         _need("q_pos", q_pos, torch.int32, (S, nq), pool.device)
-    sc = 1.0 / math.sqrt(pool.D) if scale is None else float(scale)
-    return SkvShape(S, nq, H, Hk, pool.D, sc, 0, 0, 0, 0), S, nq, H, Hk, cap
+    return SkvShape(S, nq, H, Hk, pool.D, pool.scale if scale is None else float(scale), 0, 0, 0, 0), S, nq, H, Hk, cap
 
 
 def q8_append(h: Handle, pool: Q8Pool, k_new, v_new, page_ids, kv_len, *, n_new=None, stream=None):
@@ -467,25 +482,38 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     them); mass fp32 [S, Hk, pages_per_list] is added to.  o is fp32 unless
     o_dtype (or a given o) is torch.float16."""
     torch = _torch()
+    dev = pool.device
     sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, scale)
-    st = _q8_stream(h, stream, pool.device)
+    st = _q8_stream(h, stream, dev)
     if o is None:
-        o = torch.empty(q.shape, dtype=torch.float32 if o_dtype is None else o_dtype, device=q.device)
-    if o.dtype not in (torch.float32, torch.float16) or (o_dtype is not None and o.dtype != o_dtype):
-        raise SplitKVError(1, f"o: fp32 or fp16 is wanted, got {o.dtype} (o_dtype {o_dtype})")
-    _need("o", o, o.dtype, tuple(q.shape), pool.device)
+        o = torch.empty_like(q, dtype=torch.float32 if o_dtype is None else o_dtype)
+    else:
+        _need("o", o, o.dtype, q.shape, dev)
+    if o.dtype is torch.float32:
+        o_type = F32
+    elif o.dtype is torch.float16:
+        o_type = F16
+    else:
+        raise SplitKVError(1, f"o: fp32 or fp16 is wanted, got {o.dtype}")
+    if o_dtype is not None and o.dtype is not o_dtype:
+        raise SplitKVError(1, f"o is {o.dtype}, o_dtype {o_dtype}")
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _need("lse", lse, torch.float32, (S, nq, H), pool.device)
-    n_sel = 0
+        lse = torch.empty((S, nq, H), dtype=torch.float32, device=q.device)
+    else:
+        _need("lse", lse, torch.float32, (S, nq, H), dev)
+    n_sel, sel_ptr, mass_ptr = 0, None, None
     if sel is not None:
         n_sel = sel.shape[-1]
-        _need("sel", sel, torch.int32, (S, nq, Hk, n_sel), pool.device)
+        _need("sel", sel, torch.int32, (S, nq, Hk, n_sel), dev)
+        sel_ptr = sel.data_ptr()
     if mass is not None:
-        _need("mass", mass, torch.float32, (S, Hk, cap), pool.device)
-    h.check(_lib.lib().skv_q8_attn(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
-                                   kv_len.data_ptr(), _ptr(q_pos), _ptr(sel), n_sel, _ptr(mass),
-                                   F32 if o.dtype == torch.float32 else F16, o.data_ptr(), lse.data_ptr(), st))
+        _need("mass", mass, torch.float32, (S, Hk, cap), dev)
+        mass_ptr = mass.data_ptr()
+    rc = _lib.lib().skv_q8_attn(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
+                                kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(), sel_ptr, n_sel,
+                                mass_ptr, o_type, o.data_ptr(), lse.data_ptr(), st)
+    if rc:
+        h.check(rc)
     return o, lse
 
 
@@ -497,11 +525,13 @@ def q8_select(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, n_sel, n_first=1,
     torch = _torch()
     sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, None)
     st = _q8_stream(h, stream, pool.device)
+    n_sel = int(n_sel)
     if sel is None:
-        sel = torch.empty((S, nq, Hk, max(0, int(n_sel))), dtype=torch.int32, device=q.device)
-    _need("sel", sel, torch.int32, (S, nq, Hk, int(n_sel)), pool.device)
+        sel = torch.empty((S, nq, Hk, max(0, n_sel)), dtype=torch.int32, device=q.device)
+    else:
+        _need("sel", sel, torch.int32, (S, nq, Hk, n_sel), pool.device)
     h.check(_lib.lib().skv_q8_select(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
-                                     kv_len.data_ptr(), _ptr(q_pos), int(n_sel), int(n_first), int(n_last),
+                                     kv_len.data_ptr(), _ptr(q_pos), n_sel, int(n_first), int(n_last),
                                      sel.data_ptr(), st))
     return sel
 
@@ -510,9 +540,10 @@ def q8_evict(h: Handle, page_ids, mass, kv_len, *, n_keep, n_first=1, n_last=1, 
     """skv_q8_evict: lists cut to n_keep pages (the first n_first, the last
     n_last, the others of largest mass): (page_ids, mass, kv_len, freed)."""
     torch = _torch()
-    S, Hk, cap = _q8_lists(page_ids, kv_len, page_ids.device)
-    st = _q8_stream(h, stream, page_ids.device)
-    _need("mass", mass, torch.float32, (S, Hk, cap), page_ids.device)
+    dev = page_ids.get_device()
+    S, Hk, cap = _q8_lists(page_ids, kv_len, dev)
+    st = _q8_stream(h, stream, dev)
+    _need("mass", mass, torch.float32, (S, Hk, cap), dev)
     ids_out, freed = torch.empty_like(page_ids), torch.empty_like(page_ids)
     mass_out, len_out = torch.empty_like(mass), torch.empty_like(kv_len)
     h.check(_lib.lib().skv_q8_evict(h.ptr, S, Hk, cap, page_ids.data_ptr(), mass.data_ptr(), kv_len.data_ptr(),

@@ -9,6 +9,12 @@
 // c*d has 31 significant bits, so c*d/d' cannot be rounded onto a half-integer
 // that it is not); rounding is monotone, so the old extremes recode like codes.
 //
+// A code is rint(t), t = x (1/d') with an approximate reciprocal, when t is further
+// than 2^-13 from every half-integer: t is off by less than 2^-21.4 * 128 = 2^-14.4
+// and |x/d'| never exceeds 127 + 2^-16, so nothing is left to clamp.  Nearer ones (one
+// value in 4000), infinities and NaN are decided by the exact quotient, eight at a
+// time; with that division for every value a 4096-token prompt took 31 us.
+//
 // Bound: a token's append is two dependent reads (length, page id) and one
 // write deep, the prompt's by its bytes (x read once, codes written once).
 #include "q8.cuh"
@@ -109,14 +115,26 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     const bool recode = r_lo > 0 && d1 != d0;
     int8_t *page = a.codes[which] + id * (kPage * D);
     const float up = d1 < 0x1p-100f ? 0x1p40f : 1.f;                        // see nearest_code
+    float rd;                                                               // 1 / (d' up), off by 2^-22 at most
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d1 * up));
     uint32_t lo[2] = {0x7f7f7f7fu, 0x7f7f7f7fu}, hi[2] = {0x81818181u, 0x81818181u};
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = r0 + i * RPP;
         if (r < r_lo || r >= r_hi) continue;
         int q[8];
+        bool sure = d1 > 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = d1 > 0.f ? nearest_code(v[i][e] * up, d1 * up) : 0;
+        for (int e = 0; e < 8; ++e) {
+            const float t = v[i][e] * up * rd;
+            const float r = rintf(t);
+            sure = sure && fabsf(t - r) < 0.5f - 0x1p-13f;               // (false for what is not finite)
+            q[e] = static_cast<int>(r);
+        }
+        if (!sure) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = d1 > 0.f ? nearest_code(v[i][e] * up, d1 * up) : 0;
+        }
         const uint32_t w0 = pack4(q[0], q[1], q[2], q[3]), w1 = pack4(q[4], q[5], q[6], q[7]);
         *reinterpret_cast<uint2 *>(page + r * D + c8) = make_uint2(w0, w1);
         lo[0] = __vmins4(lo[0], w0);
