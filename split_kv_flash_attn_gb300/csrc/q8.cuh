@@ -40,8 +40,8 @@ struct AttnArgs {
     void *o;                       // [S][nq][H][D]
     float *lse;                    // [S][nq][H]
     // scratch
-    float *part_o;                 // [2 * grid][columns][D] unnormalised partials
-    float *part_ml;                // [2 * grid][columns][2] reference (log2) and sum
+    float *part_o;                 // [2 * grid][columns][D] partials
+    float *part_ml;                // [2 * grid][columns][2] reference (log2) and sum (prefill: one log sum)
     int *counters;                 // arrivals, zero between launches
     float *page_lse;               // mass: [S][Hk][nq * G][page_ld] log2 sums of half pages, or null
     int64_t page_ld;               // 2 cap, or 2 n_sel with sel

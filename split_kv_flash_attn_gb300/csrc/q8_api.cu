@@ -167,6 +167,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     // one CTA a SM, but no more than pieces of kPieceMin pages
     const int64_t pieces = tc ? (units * per_list + 1) / 2 : (units * per_list + kPieceMin - 1) / kPieceMin;
     const int grid = static_cast<int>(std::min<int64_t>(h->sm_count, pieces));
+    // two partials for each CTA's piece
     const size_t po = round256(static_cast<size_t>(2) * grid * unit_rows * D * sizeof(float));
     const size_t pm = round256(static_cast<size_t>(2) * grid * unit_rows * 2 * sizeof(float));
     const size_t pp = tc ? round256((static_cast<size_t>(shape->S) * a.row_groups + 1) * sizeof(uint32_t)) : 0;

@@ -16,7 +16,9 @@
 // line, of which every CTA takes an equal piece; a piece that covers several
 // units works through them, and a unit that several pieces share is put
 // together by the last CTA to finish with it, in piece order (so results do not
-// depend on timing).  Lengths are read on the device: a call costs its keys, not
+// depend on timing).  (Equal pieces end up to 15 % apart, as some SMs see less
+// bandwidth; short pieces handed out at the end cost more than that: each begins
+// with a chain of look-ups and ends with a join, 72 against 64 us.)  Lengths are read on the device: a call costs its keys, not
 // its lists' capacity, and ragged batches stay balanced.
 //
 // A CTA is one warp that fetches and W that compute.  The first walks the CTA's
@@ -60,17 +62,17 @@ __host__ __device__ constexpr int decode_smem()
 }
 static_assert(decode_smem<128, 1>() < 226 * 1024 && decode_smem<128, 2>() < 226 * 1024, "shared memory per CTA");
 
-// Where a piece of the line of pages lies.
+// A list on the line of pages.
 struct Place {
     int list;                       // sequence, or sequence x token with a selection
-    int64_t np;                     // its pages
-    int64_t base;                   // the line's position of its first page
+    uint32_t np;                    // its pages
+    uint32_t base;                  // the line's position of its first page
 };
 
-__device__ __forceinline__ int64_t pages_of(const AttnArgs &a, int list)
+__device__ __forceinline__ uint32_t pages_of(const AttnArgs &a, int list)
 {
     if (a.sel) return a.n_sel;
-    return (list_len(a.L, list) + kPage - 1) / kPage;
+    return static_cast<uint32_t>((list_len(a.L, list) + kPage - 1) / kPage);
 }
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i)
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     const uint32_t bar0 = smem_addr(s_bar);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_lists = a.sel ? a.L.S * a.nq : a.L.S;
-    const int64_t mult = static_cast<int64_t>(a.L.Hk) * a.row_groups;   // units per list
+    const uint32_t mult = a.L.Hk * a.row_groups;    // units per list
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < 2 * NS; ++i) tc::mbar_init(bar0 + 8 * i, i < NS ? 1 : 2);
@@ -115,28 +117,33 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     }
 
     // ---- the plan: total pages, this CTA's piece, the list that it starts in --
-    int64_t total;
+    uint64_t sum = 0;
+    uint32_t np_lane = 0;                           // pages of list `lane`
     if (a.sel) {
-        total = static_cast<int64_t>(n_lists) * a.n_sel;
+        sum = static_cast<uint64_t>(n_lists) * a.n_sel;
     } else {
-        total = 0;
         for (int i = lane; i < n_lists; i += 32) {
-            const int64_t n = pages_of(a, i);
-            total += n;
-            if (n * kPage < max(0, a.L.kv_len[i]) && blockIdx.x == 0) atomicOr(a.L.status, kStatusList);
+            const uint32_t n = pages_of(a, i);
+            if (i == lane) np_lane = n;
+            sum += n;
+            if (blockIdx.x == 0 && static_cast<int64_t>(n) * kPage < max(0, a.L.kv_len[i])) atomicOr(a.L.status, kStatusList);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    total *= mult;
-    const int64_t chunk = max(int64_t(kPieceMin), (total + gridDim.x - 1) / gridDim.x);
-    const int64_t pos0 = blockIdx.x * chunk;
-    const int64_t pos_end = min(total, pos0 + chunk);
+    sum *= mult;
+    if (sum > (1u << 30)) {                         // (16 TB of pages: lengths that are none)
+        if (blockIdx.x == 0 && tid == 0) atomicOr(a.L.status, kStatusList);
+        sum = 0;
+    }
+    const uint32_t total = static_cast<uint32_t>(sum);
+    const uint32_t chunk = max(static_cast<uint32_t>(kPieceMin), (total + gridDim.x - 1) / gridDim.x);
+    const uint32_t pos0 = blockIdx.x * chunk, pos_end = min(total, pos0 + chunk);
 
     // lists without a page: their rows are written here
     if (!a.sel) {
         for (int i = blockIdx.x; i < n_lists; i += gridDim.x) {
-            if (pages_of(a, i) != 0) continue;
+            if ((n_lists <= 32 ? __shfl_sync(0xffffffffu, np_lane, i) : pages_of(a, i)) != 0) continue;
             const int64_t r0 = a.token(i, 0) * a.H, nr = static_cast<int64_t>(a.nq) * a.H;
             for (int64_t e = tid; e < nr * D; e += kThreads) {
                 if (F16) static_cast<__half *>(a.o)[r0 * D + e] = __float2half(0.f);
@@ -154,13 +161,13 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         at.list = static_cast<int>(pos0 / (at.np * mult));
         at.base = at.list * (at.np * mult);
     } else {
-        int64_t before = 0;
+        uint32_t before = 0;
         for (int c0 = 0; c0 < n_lists; c0 += 32) {
-            const int64_t n = c0 + lane < n_lists ? pages_of(a, c0 + lane) : 0;
-            int64_t inc = n;
+            const uint32_t n = c0 == 0 ? np_lane : c0 + lane < n_lists ? pages_of(a, c0 + lane) : 0u;
+            uint32_t inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += x;
             }
             const unsigned hit = __ballot_sync(0xffffffffu, (before + inc) * mult > pos0);
@@ -177,11 +184,11 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
 
     // The units of the piece in turn, for both roles: pages [pg0, pg1) of one unit.
     struct Unit {
-        int64_t u_in, unit0;                        // its number within the list; the line's position of its page 0
+        uint32_t u_in, unit0;                       // its number within the list; the line's position of its page 0
         int pg0, pg1, kh, rg, seq;
         int64_t tok0;                               // token of its row 0
     };
-    auto unit_at = [&](int64_t pos) {
+    auto unit_at = [&](uint32_t pos) {
         while (pos >= at.base + at.np * mult) {     // the next list with pages
             at.base += at.np * mult;
             ++at.list;
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         x.pg0 = static_cast<int>(pos - x.unit0);
         x.pg1 = static_cast<int>(min(at.np, pos_end - x.unit0));
         x.kh = static_cast<int>(x.u_in / a.row_groups);
-        x.rg = static_cast<int>(x.u_in - static_cast<int64_t>(x.kh) * a.row_groups);
+        x.rg = static_cast<int>(x.u_in - x.kh * a.row_groups);
         x.seq = a.sel ? at.list / a.nq : at.list;
         x.tok0 = a.sel ? a.token(x.seq, at.list % a.nq) : a.token(at.list, 0);
         return x;
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         // ---------------- the fetching warp -----------------------------------
         uint32_t n_put = 0;                         // pages put into the ring so far
         bool ok = true;
-        for (int64_t pos = pos0; ok && pos < pos_end;) {
+        for (uint32_t pos = pos0; ok && pos < pos_end;) {
             const Unit x = unit_at(pos);
             const int len = static_cast<int>(list_len(a.L, x.seq));
             const int32_t *ids = a.L.ids + (static_cast<int64_t>(x.seq) * a.L.Hk + x.kh) * a.L.cap;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         for (int e = 0; e < 2; ++e) v_off[e] = (2 * t + e) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
     }
     uint32_t n_taken = 0;                           // half pages of the CTA's earlier units
-    for (int64_t pos = pos0; pos < pos_end;) {
+    for (uint32_t pos = pos0; pos < pos_end;) {
         const Unit x = unit_at(pos);
         const int row0 = x.rg * 8 * NC;
         const int len = static_cast<int>(list_len(a.L, x.seq));
@@ -520,8 +527,42 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         }
         n_taken = n_end;
 
+        // The warps' results for column group j, as they stand in shared memory, to the
+        // result or to a piece's slot.
+        auto join = [&](int j, bool final, int64_t slot) {
+            for (int i = tid; i < 8 * D; i += kConsumers) {
+                const int c = i / D, d = i % D;
+                const int row = row0 + j * 8 + c;
+                if (row >= a.rows) continue;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][c][0]);
+                float Lw = 0.f, O = 0.f;
+                if (M != -INFINITY) {
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float b = fast_exp2(s_ml[w][c][0] - M);
+                        Lw = fmaf(b, s_ml[w][c][1], Lw);
+                        O = fmaf(b, s_o[w][c][d], O);
+                    }
+                }
+                if (final) {
+                    const int64_t r = out_row(row);
+                    const float v = Lw > 0.f ? O / Lw : 0.f;
+                    if (F16) static_cast<__half *>(a.o)[r * D + d] = __float2half_rn(v);
+                    else static_cast<float *>(a.o)[r * D + d] = v;
+                    if (d == 0) a.lse[r] = Lw > 0.f ? (M - kShift + log2f(Lw)) * 0.6931471805599453f : -INFINITY;
+                } else {
+                    a.part_o[(slot * (8 * NC) + j * 8 + c) * D + d] = O;
+                    if (d == 0) {
+                        a.part_ml[(slot * (8 * NC) + j * 8 + c) * 2] = M;
+                        a.part_ml[(slot * (8 * NC) + j * 8 + c) * 2 + 1] = Lw;
+                    }
+                }
+            }
+        };
         // ---- the warps' results together, eight columns at a time ---------------
-        const bool whole = x.pg0 == 0 && x.pg1 == at.np;
+        const bool whole = x.pg0 == 0 && x.pg1 == static_cast<int>(at.np);
         const int64_t slot_out = 2 * static_cast<int64_t>(blockIdx.x) + (pos == pos0 ? 0 : 1);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
@@ -541,84 +582,66 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                         make_float2(acc[j][i][e], acc[j][i][e + 2]);
             }
             sync_all();
-            for (int i = tid; i < 8 * D; i += kConsumers) {
-                const int c = i / D, d = i % D;
-                const int row = row0 + j * 8 + c;
-                if (row >= a.rows) continue;
-                float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < W; ++w) M = fmaxf(M, s_ml[w][c][0]);
-                float Lw = 0.f, O = 0.f;
-                if (M != -INFINITY) {
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const float b = fast_exp2(s_ml[w][c][0] - M);
-                        Lw = fmaf(b, s_ml[w][c][1], Lw);
-                        O = fmaf(b, s_o[w][c][d], O);
-                    }
-                }
-                if (whole) {
-                    const int64_t r = out_row(row);
-                    const float v = Lw > 0.f ? O / Lw : 0.f;
-                    if (F16) static_cast<__half *>(a.o)[r * D + d] = __float2half_rn(v);
-                    else static_cast<float *>(a.o)[r * D + d] = v;
-                    if (d == 0) a.lse[r] = Lw > 0.f ? (M - kShift + log2f(Lw)) * 0.6931471805599453f : -INFINITY;
-                } else {
-                    a.part_o[(slot_out * (8 * NC) + j * 8 + c) * D + d] = O;
-                    if (d == 0) {
-                        a.part_ml[(slot_out * (8 * NC) + j * 8 + c) * 2] = M;
-                        a.part_ml[(slot_out * (8 * NC) + j * 8 + c) * 2 + 1] = Lw;
-                    }
-                }
-            }
+            join(j, whole, slot_out);
         }
         if (!whole) {
-            // ---- the last CTA of the unit puts the pieces together, in order -----
-            const int64_t u = at.list * mult + x.u_in;
-            const int64_t c_lo = x.unit0 / chunk, c_hi = (x.unit0 + at.np - 1) / chunk;
+            // ---- the last CTA of the unit puts the pieces together, in order: each
+            // warp some of them, then the warps' results as above
+            const uint32_t u = at.list * mult + x.u_in;
+            const uint32_t c_lo = x.unit0 / chunk, c_hi = (x.unit0 + at.np - 1) / chunk;
             __threadfence();
             sync_all();
             if (tid == 0) s_last = atomicAdd(a.counters + u, 1) == static_cast<int>(c_hi - c_lo);
             sync_all();
             if (s_last) {
                 __threadfence();
-                auto slot_of = [&](int64_t c) { return 2 * c + (c == c_lo && x.unit0 > c * chunk ? 1 : 0); };
-                for (int e = tid; e < 8 * NC * (D / 4); e += kConsumers) {
-                    const int c = e / (D / 4), d4 = e % (D / 4);
-                    const int row = row0 + c;
-                    if (row >= a.rows) continue;
-                    float M = -INFINITY;
-                    for (int64_t y = c_lo; y <= c_hi; ++y)
-                        M = fmaxf(M, __ldcg(a.part_ml + (slot_of(y) * (8 * NC) + c) * 2));
-                    float Ls = 0.f;
-                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (M != -INFINITY) {
-#pragma unroll 8
-                        for (int64_t y = c_lo; y <= c_hi; ++y) {
-                            const int64_t sl = slot_of(y) * (8 * NC) + c;
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + sl);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + sl * D) + d4);
-                            const float b = fast_exp2(ml.x - M);
-                            Ls = fmaf(b, ml.y, Ls);
-                            O.x = fmaf(b, v.x, O.x);
-                            O.y = fmaf(b, v.y, O.y);
-                            O.z = fmaf(b, v.z, O.z);
-                            O.w = fmaf(b, v.w, O.w);
+                constexpr int CPI = 128 / D;        // columns a warp reads at once
+                const int sub = lane / (D / 4), d4 = lane % (D / 4);
+#pragma unroll 1
+                for (int j = 0; j < NC; ++j) {
+                    float M[8 / CPI], L[8 / CPI], O[8 / CPI][4];
+#pragma unroll
+                    for (int c = 0; c < 8 / CPI; ++c) {
+                        M[c] = -INFINITY;
+                        L[c] = O[c][0] = O[c][1] = O[c][2] = O[c][3] = 0.f;
+                    }
+#pragma unroll 1
+                    for (uint32_t y = c_lo + warp; y <= c_hi; y += W) {
+                        const int64_t sl = 2 * static_cast<int64_t>(y) + (y == c_lo && x.unit0 > c_lo * chunk ? 1 : 0);
+                        float2 ml[8 / CPI];
+                        float4 v[8 / CPI];
+#pragma unroll
+                        for (int c = 0; c < 8 / CPI; ++c) {
+                            const int64_t at_c = sl * (8 * NC) + j * 8 + c * CPI + sub;
+                            const bool on = row0 + j * 8 + c * CPI + sub < a.rows;
+                            ml[c] = on ? __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at_c) : make_float2(-INFINITY, 0.f);
+                            v[c] = on ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + at_c * D) + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8 / CPI; ++c) {
+                            const float m = fmaxf(M[c], ml[c].x);
+                            const float bo = M[c] == -INFINITY ? 0.f : fast_exp2(M[c] - m);
+                            const float bn = ml[c].x == -INFINITY ? 0.f : fast_exp2(ml[c].x - m);
+                            M[c] = m;
+                            L[c] = L[c] * bo + bn * ml[c].y;
+                            O[c][0] = O[c][0] * bo + bn * v[c].x;
+                            O[c][1] = O[c][1] * bo + bn * v[c].y;
+                            O[c][2] = O[c][2] * bo + bn * v[c].z;
+                            O[c][3] = O[c][3] * bo + bn * v[c].w;
                         }
                     }
-                    const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-                    O.x *= inv;
-                    O.y *= inv;
-                    O.z *= inv;
-                    O.w *= inv;
-                    const int64_t r = out_row(row);
-                    if (F16)
-                        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + d4 * 4) =
-                            make_uint2(pack_half2(O.x, O.y), pack_half2(O.z, O.w));
-                    else
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + d4 * 4) = O;
-                    if (d4 == 0)
-                        a.lse[r] = Ls > 0.f ? (M - kShift + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+                    if (j > 0) sync_all();
+#pragma unroll
+                    for (int c = 0; c < 8 / CPI; ++c) {
+                        const int col = c * CPI + sub;
+                        if (d4 == 0) {
+                            s_ml[warp][col][0] = M[c];
+                            s_ml[warp][col][1] = L[c];
+                        }
+                        *reinterpret_cast<float4 *>(&s_o[warp][col][d4 * 4]) = make_float4(O[c][0], O[c][1], O[c][2], O[c][3]);
+                    }
+                    sync_all();
+                    join(j, true, 0);
                 }
                 if (tid == 0) a.counters[u] = 0;
             }

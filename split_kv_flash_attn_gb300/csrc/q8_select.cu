@@ -12,13 +12,18 @@
 // memory into fragments, as in the decode kernel) against the queries of a KV
 // head, 8 columns at a time.
 //
-// The choice.  Scores become 32-bit keys whose order as unsigned numbers is the scores'
-// order; one CTA for each list finds the n-th largest key two bits at a time,
-// counting keys in shared memory, and writes the picked indices in order by
-// prefix sums over the warps' equal shares.  Ties at the n-th key go to the lowest indices.
+// The choice.  Scores become 32-bit keys whose order as unsigned numbers is the
+// scores' order; one CTA for each list finds the n-th largest key two bits at a
+// time, counting keys in shared memory, and writes the picked indices in order by
+// prefix sums over the warps' equal shares.  Ties at the n-th key go to the lowest
+// indices.
 //
-// Bound: 2D + 8 bytes a page and head for the scores; the choice is latency
-// (about 15 counting rounds, each one pass over shared memory and one barrier).
+// Bound: the scores by latency (lengths, ids, extremes and queries are read one
+// after the other, 2D + 8 bytes a page and head in all); the choice by its
+// counting rounds, each one pass over shared memory and one barrier, about 12 for the
+// keys of one list.
+#include <algorithm>
+
 #include "q8.cuh"
 
 namespace skv {
@@ -37,9 +42,39 @@ __device__ __forceinline__ uint32_t order_key(float x)
 
 // ---------------------------------------------------------------- the bounds
 
-constexpr int kScoreWarps = 4;
+constexpr int kScoreWarps = 8;
 constexpr int kScoreCols = 64;                // query columns in shared memory at a time
 
+// The codes of 16 pages as fragments: rows g, g + 8; [largest | smallest].
+template <int D>
+struct Extremes {
+    static constexpr int CH = D / 64;
+    uint4 x[2][2][CH];
+    int id[2];
+
+    __device__ void ids_of(const SelectArgs &a, const int32_t *ids, int64_t first, int64_t nb, int g)
+    {
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+            const int64_t b = first + g + 8 * rr;
+            id[rr] = b < nb ? checked_page(a.L, __ldg(ids + b)) : -1;
+        }
+    }
+    __device__ void load(const SelectArgs &a, int t)
+    {
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int64_t off = static_cast<int64_t>(max(id[rr], 0)) * D + 64 * c + 16 * t;
+                x[0][rr][c] = id[rr] >= 0 ? ld_stream16(a.k_max + off) : make_uint4(0, 0, 0, 0);
+                x[1][rr][c] = id[rr] >= 0 ? ld_stream16(a.k_min + off) : make_uint4(0, 0, 0, 0);
+            }
+    }
+};
+
+// Grid: x pieces of a list's pages, y KV heads, z sequences.  The warps of a CTA
+// take groups of 16 of its pages in turn, a group's bytes a turn ahead.
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArgs a)
 {
@@ -52,32 +87,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
     const int kh = blockIdx.y, s = blockIdx.z;
     const int64_t len = list_len(a.L, s);
     const int64_t nb = (len + kPage - 1) / kPage;
-    const int64_t b0 = (static_cast<int64_t>(blockIdx.x) * kScoreWarps) * 16;      // the CTA's first page
-    if (b0 >= nb) return;
-    const int64_t bw = b0 + warp * 16;                                             // the warp's
+    const int64_t groups = (nb + 15) / 16, stride = static_cast<int64_t>(gridDim.x) * kScoreWarps;
+    const int64_t group0 = static_cast<int64_t>(blockIdx.x) * kScoreWarps + warp;
+    if (static_cast<int64_t>(blockIdx.x) * kScoreWarps >= groups) return;
     const int32_t *ids = a.L.ids + (static_cast<int64_t>(s) * a.L.Hk + kh) * a.L.cap;
 
-    // rows g, g + 8 of the warp's 16 pages: [largest | smallest] codes
-    int id[2];
-    uint4 kr[2][2][CH];
-#pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-        const int64_t b = bw + g + 8 * rr;
-        id[rr] = b < nb ? checked_page(a.L, __ldg(ids + b)) : -1;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int64_t off = static_cast<int64_t>(max(id[rr], 0)) * D + 64 * c + 16 * t;
-            kr[0][rr][c] = id[rr] >= 0 ? ld_stream16(a.k_max + off) : make_uint4(0, 0, 0, 0);
-            kr[1][rr][c] = id[rr] >= 0 ? ld_stream16(a.k_min + off) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    // lane l finishes page l % 16
-    const int id0 = __shfl_sync(0xffffffffu, id[0], (lane & 7) * 4);
-    const int id1 = __shfl_sync(0xffffffffu, id[1], (lane & 7) * 4);
-    const int page_id = (lane & 8) ? id1 : id0;
-    const float page_scale = page_id >= 0 ? __ldg(a.k_scale + page_id) : 0.f;
-
-    // tokens in groups whose columns fit; a token of more query heads than that
+    // tokens in rounds whose columns fit; a token of more query heads than that
     // takes several rounds
     const int tg = max(1, kScoreCols / a.G);              // tokens a round
     const int hg = min(a.G, kScoreCols);                  // heads a round
@@ -85,58 +100,86 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
         const int nt = min(tg, a.nq - t0);
         for (int h0 = 0; h0 < a.G; h0 += hg) {
             const int nh = min(hg, a.G - h0);
-            const int cols = nt * nh;
-            __syncthreads();
+            const int cols = nt * nh, ncg = (cols + 7) / 8;
+            Extremes<D> nxt;
+            nxt.ids_of(a, ids, group0 * 16, group0 < groups ? nb : 0, g);
+            __syncthreads();                              // the last round's columns are read
             // coded queries: one warp a column
-            for (int c = warp; c < (cols + 7) / 8 * 8; c += kScoreWarps) {
-                float v[D / 32];
+            for (int c = warp; c < ncg * 8; c += kScoreWarps) {
+                constexpr int N = D / 32;
+                float v[N];
                 float top = 0.f;
                 const int tok = t0 + c / nh, head = kh * a.G + h0 + c % nh;
-                const __half *qp = a.q + ((static_cast<int64_t>(s) * a.nq + tok) * a.H + head) * D + lane * (D / 32);
+                const __half *qp = a.q + ((static_cast<int64_t>(s) * a.nq + tok) * a.H + head) * D + lane * N;
+                __half raw[N];
+                if (c < cols) {
+                    if constexpr (N == 4) *reinterpret_cast<uint2 *>(raw) = __ldg(reinterpret_cast<const uint2 *>(qp));
+                    else *reinterpret_cast<uint32_t *>(raw) = __ldg(reinterpret_cast<const uint32_t *>(qp));
+                }
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    v[i] = c < cols ? __half2float(qp[i]) : 0.f;
+                for (int i = 0; i < N; ++i) {
+                    v[i] = c < cols ? __half2float(raw[i]) : 0.f;
                     const float m = fabsf(v[i]);
                     top = fmaxf(top, m <= 65504.f ? m : 0.f);
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // (magnitudes: their order is that of their bits)
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
                 const float dq = __fdiv_rn(top, 127.f);
                 if (lane == 0) s_dq[c] = dq;
-                __half hc[4];
+                __half hc[N];
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) hc[i] = __int2half_rn(dq > 0.f ? nearest_code(v[i], dq) : 0);
+                for (int i = 0; i < N; ++i) hc[i] = __int2half_rn(dq > 0.f ? nearest_code(v[i], dq) : 0);
                 // channel d of column c: chunk d/64, t = d/16 % 4, word d/4 % 4, place d % 4
-                const int d = lane * (D / 32);
+                const int d = lane * N;
                 __half *dst = reinterpret_cast<__half *>(&s_q[c >> 3][(d >> 6) * 4 + ((d >> 2) & 3)][(c & 7) * 4 + ((d >> 4) & 3)]) + (d & 3);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) dst[i] = hc[i];
+                for (int i = 0; i < N; ++i) dst[i] = hc[i];
             }
+            nxt.load(a, t);
             __syncthreads();
-            if (bw < nb) {
-                for (int j = 0; j < (cols + 7) / 8; ++j) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int64_t gr = group0; gr < groups; gr += stride) {
+                const Extremes<D> cur = nxt;
+                // lane l finishes page l % 16
+                const int id0 = __shfl_sync(0xffffffffu, cur.id[0], (lane & 7) * 4);
+                const int id1 = __shfl_sync(0xffffffffu, cur.id[1], (lane & 7) * 4);
+                const int page_id = (lane & 8) ? id1 : id0;
+                const float page_scale = page_id >= 0 ? __ldg(a.k_scale + page_id) : 0.f;
+                if (gr + stride < groups) {
+                    nxt.ids_of(a, ids, (gr + stride) * 16, nb, g);
+                    nxt.load(a, t);
+                }
+                float acc[kScoreCols / 8][4];
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                for (int j = 0; j < kScoreCols / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
-                        for (int c = 0; c < CH; ++c)
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const uint4 &lo = kr[part][0][c], &hi = kr[part][1][c];
-                                const uint32_t x = (w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w) ^ 0x80808080u;
-                                const uint32_t y = (w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w) ^ 0x80808080u;
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint4 &lo = cur.x[part][0][c], &hi = cur.x[part][1][c];
+                            const uint32_t x = (w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w) ^ 0x80808080u;
+                            const uint32_t y = (w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w) ^ 0x80808080u;
+                            const uint32_t a0 = codes_lo(x), a1 = codes_lo(y), a2 = codes_hi(x), a3 = codes_hi(y);
+                            const __half2 z = __half2half2(__ushort_as_half(0));
+#pragma unroll
+                            for (int j = 0; j < kScoreCols / 8; ++j) {
+                                if (j >= ncg) break;
                                 uint2 q = s_q[j][c * 4 + w][lane];
-                                const __half2 z = __half2half2(__ushort_as_half(0));
                                 __half2 q0 = *reinterpret_cast<__half2 *>(&q.x), q1 = *reinterpret_cast<__half2 *>(&q.y);
                                 q0 = part == 0 ? __hmax2(q0, z) : __hmin2(q0, z);
                                 q1 = part == 0 ? __hmax2(q1, z) : __hmin2(q1, z);
-                                mma_16816(acc, codes_lo(x), codes_lo(y), codes_hi(x), codes_hi(y),
-                                          *reinterpret_cast<uint32_t *>(&q0), *reinterpret_cast<uint32_t *>(&q1));
+                                mma_16816(acc[j], a0, a1, a2, a3, *reinterpret_cast<uint32_t *>(&q0),
+                                          *reinterpret_cast<uint32_t *>(&q1));
                             }
+                        }
+#pragma unroll
+                for (int j = 0; j < kScoreCols / 8; ++j) {
+                    if (j >= ncg) break;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int c = j * 8 + 2 * t + (e & 1);
-                        s_f[warp][g + 8 * (e >> 1)][c] = __fmul_rn(acc[e], s_dq[c]);
+                        s_f[warp][g + 8 * (e >> 1)][c] = __fmul_rn(acc[j][e], s_dq[c]);
                     }
                 }
                 __syncwarp();
@@ -145,12 +188,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                     const int b = x & 15, tok = x >> 4;   // b = lane & 15: the lane's own page
                     float m = -INFINITY;
                     for (int i = 0; i < nh; ++i) m = fmaxf(m, s_f[warp][b][tok * nh + i]);
-                    const int64_t blk = bw + b;
+                    const int64_t blk = gr * 16 + b;
                     if (blk >= nb) continue;
                     const int64_t row = (static_cast<int64_t>(s) * a.nq + t0 + tok) * a.L.Hk + kh;
                     uint32_t *out = a.keys + row * a.L.cap + blk;
                     int64_t seen = len;
-                    if (a.q_pos) seen = max(int64_t(0), min(len, static_cast<int64_t>(a.q_pos[static_cast<int64_t>(s) * a.nq + t0 + tok]) + 1));
+                    if (a.q_pos)
+                        seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + static_cast<int64_t>(s) * a.nq + t0 + tok)) + 1));
                     const int64_t nbq = (seen + kPage - 1) / kPage;
                     uint32_t key = kNever;
                     if (page_id >= 0 && blk < nbq) {
@@ -167,23 +211,23 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
 
 // ---------------------------------------------------------------- the choice
 
-constexpr int kPickThreads = 1024;
-constexpr int kPickWarps = kPickThreads / 32;
-
+template <int THREADS>
 struct PickScratch {
-    int cnt[2][kPickWarps][3];
-    uint32_t lo[kPickWarps], hi[kPickWarps];
-    int warp_n[kPickWarps];
-    int warp_m[kPickWarps];
+    static constexpr int W = THREADS / 32;
+    int cnt[2][W][3];
+    uint32_t lo[W], hi[W];
+    int n[3][W];
 };
 
 // The k-th largest of keys[0, n) (n >= k >= 1).
-__device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch &sc)
+template <int THREADS>
+__device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch<THREADS> &sc)
 {
+    constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // bits that all keys share need no rounds
     uint32_t both = 0xffffffffu, any = 0u;
-    for (int i = tid; i < n; i += kPickThreads) {
+    for (int i = tid; i < n; i += THREADS) {
         const uint32_t x = keys[i];
         both &= x;
         any |= x;
@@ -195,8 +239,8 @@ __device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch 
         sc.hi[warp] = any;
     }
     __syncthreads();
-    both = __reduce_and_sync(0xffffffffu, sc.lo[lane]);
-    any = __reduce_or_sync(0xffffffffu, sc.hi[lane]);
+    both = __reduce_and_sync(0xffffffffu, lane < W ? sc.lo[lane] : 0xffffffffu);
+    any = __reduce_or_sync(0xffffffffu, lane < W ? sc.hi[lane] : 0u);
     const uint32_t diff = both ^ any;
     uint32_t found = both;
     if (diff) {
@@ -207,7 +251,7 @@ __device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch 
             // how many keys reach found + 1, 2, 3 units of 2^b
             const uint32_t t1 = found | (1u << b), t2 = found | (2u << b), t3 = found | (3u << b);
             int c1 = 0, c2 = 0, c3 = 0;
-            for (int i = tid; i < n; i += kPickThreads) {
+            for (int i = tid; i < n; i += THREADS) {
                 const uint32_t x = keys[i];
                 c1 += x >= t1;
                 c2 += x >= t2;
@@ -222,53 +266,64 @@ __device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch 
                 sc.cnt[round][warp][2] = c3;
             }
             __syncthreads();
-            c1 = __reduce_add_sync(0xffffffffu, sc.cnt[round][lane][0]);
-            c2 = __reduce_add_sync(0xffffffffu, sc.cnt[round][lane][1]);
-            c3 = __reduce_add_sync(0xffffffffu, sc.cnt[round][lane][2]);
+            c1 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][lane][0] : 0);
+            c2 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][lane][1] : 0);
+            c3 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][lane][2] : 0);
             found = c3 >= k ? t3 : c2 >= k ? t2 : c1 >= k ? t1 : found;
         }
     }
     return found;
 }
 
-// Calls emit(i, rank) for the i in [0, n) for which pred(i) holds, rank counting
-// them from 0 in the order of i.  Each warp takes an equal run of indices.
-template <typename P, typename E>
-__device__ int ordered(int n, int *warp_n, P pred, E emit)
+// In the order of indices, calls emit(i, key, above, ties, nevers) for every i in [0, n):
+// how many earlier keys are above T, equal to it, and kNever.  Each warp takes an
+// equal run of indices.  `totals` receives the counts over all keys before any emit.
+template <int THREADS, typename B, typename E>
+__device__ void in_order(const uint32_t *keys, int n, uint32_t T, PickScratch<THREADS> &sc, B totals, E emit)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int share = (n + kPickThreads - 1) / kPickThreads * 32;
+    constexpr int W = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int share = (n + THREADS - 1) / THREADS * 32;
     const int lo = min(n, warp * share), hi = min(n, lo + share);
-    int c = 0;
-    for (int i = lo; i < hi; i += 32) c += __popc(__ballot_sync(0xffffffffu, i + lane < hi && pred(i + lane)));
-    __syncthreads();                                      // warp_n of an earlier call is read
-    if (lane == 0) warp_n[warp] = c;
-    __syncthreads();
-    const int x = warp_n[lane];
-    int inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    const int all = __shfl_sync(0xffffffffu, inc, 31);
-    int at = __shfl_sync(0xffffffffu, inc - x, warp);
+    int c[3] = {0, 0, 0};
     for (int i = lo; i < hi; i += 32) {
-        const bool on = i + lane < hi && pred(i + lane);
-        const unsigned m = __ballot_sync(0xffffffffu, on);
-        if (on) emit(i + lane, at + __popc(m & ((1u << lane) - 1u)));
-        at += __popc(m);
+        const bool in = i + lane < hi;
+        const uint32_t k = in ? keys[i + lane] : 0u;
+        c[0] += __popc(__ballot_sync(0xffffffffu, in && k > T));
+        c[1] += __popc(__ballot_sync(0xffffffffu, in && k == T));
+        c[2] += __popc(__ballot_sync(0xffffffffu, in && k == kNever));
     }
-    return all;
+    if (lane < 3) sc.n[lane][warp] = lane == 0 ? c[0] : lane == 1 ? c[1] : c[2];
+    __syncthreads();
+    int at[3], all[3];
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+        const int x = lane < W ? sc.n[e][lane] : 0;
+        at[e] = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+        all[e] = __reduce_add_sync(0xffffffffu, x);
+    }
+    totals(all[0], all[1], all[2]);
+    const unsigned before = (1u << lane) - 1u;
+    for (int i = lo; i < hi; i += 32) {
+        const bool in = i + lane < hi;
+        const uint32_t k = in ? keys[i + lane] : 0u;
+        const unsigned m0 = __ballot_sync(0xffffffffu, in && k > T), m1 = __ballot_sync(0xffffffffu, in && k == T),
+                       m2 = __ballot_sync(0xffffffffu, in && k == kNever);
+        if (in) emit(i + lane, k, at[0] + __popc(m0 & before), at[1] + __popc(m1 & before), at[2] + __popc(m2 & before));
+        at[0] += __popc(m0);
+        at[1] += __popc(m1);
+        at[2] += __popc(m2);
+    }
 }
 
 constexpr int kPickSmemKeys = 48 * 1024;                  // 192 KB of keys
 
 // One CTA a row (sequence, token, KV head).
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a, bool in_smem)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a, bool in_smem)
 {
     extern __shared__ uint32_t s_keys[];
-    __shared__ PickScratch sc;
+    __shared__ PickScratch<THREADS> sc;
     const int64_t row = blockIdx.x;
     const int64_t tok = row / a.L.Hk;
     const int s = static_cast<int>(tok / a.nq);
@@ -278,93 +333,70 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectArgs a, 
     const uint32_t *keys = a.keys + row * a.L.cap;
     int32_t *out = a.sel + row * a.n_sel;
     if (in_smem) {
-        for (int i = threadIdx.x; i < n; i += kPickThreads) s_keys[i] = __ldcg(keys + i);
+        for (int i = threadIdx.x; i < n; i += THREADS) s_keys[i] = __ldcg(keys + i);
         __syncthreads();
         keys = s_keys;
     }
-    // no more candidates than places: all of them
-    uint32_t T = kNever;
-    int need = 0;                                         // of the keys equal to T
-    if (n > a.n_sel) {
-        T = kth_largest(keys, n, a.n_sel, sc);
-        __syncthreads();
-        const int above = ordered(n, sc.warp_n, [&](int i) { return keys[i] > T; }, [](int, int) {});
-        need = T == kNever ? 0 : a.n_sel - above;
-    }
-    // keys above T, and the first `need` of those equal to it.  A key's place is
-    // the number of picked ones before it: those above plus at most `need` ties.
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int share = (n + kPickThreads - 1) / kPickThreads * 32;
-    const int lo = min(n, warp * share), hi = min(n, lo + share);
-    int ca = 0, ce = 0;
-    for (int i = lo; i < hi; i += 32) {
-        const uint32_t k = i + lane < hi ? keys[i + lane] : kNever;
-        ca += __popc(__ballot_sync(0xffffffffu, k > T));
-        ce += __popc(__ballot_sync(0xffffffffu, i + lane < hi && k == T && need > 0));
-    }
-    __syncthreads();
-    if (lane == 0) {
-        sc.warp_n[warp] = ca;
-        sc.warp_m[warp] = ce;
-    }
-    __syncthreads();
-    int ia = sc.warp_n[lane], ie = sc.warp_m[lane];
-    const int xa = ia, xe = ie;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, ia, o), z = __shfl_up_sync(0xffffffffu, ie, o);
-        if (lane >= o) {
-            ia += y;
-            ie += z;
-        }
-    }
-    const int total = __shfl_sync(0xffffffffu, ia, 31) + min(need, __shfl_sync(0xffffffffu, ie, 31));
-    int at_a = __shfl_sync(0xffffffffu, ia - xa, warp), at_e = __shfl_sync(0xffffffffu, ie - xe, warp);
-    for (int i = lo; i < hi; i += 32) {
-        const uint32_t k = i + lane < hi ? keys[i + lane] : kNever;
-        const bool above = k > T, tie = i + lane < hi && k == T && need > 0;
-        const unsigned ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, tie);
-        const unsigned before = (1u << lane) - 1u;
-        const int ra = at_a + __popc(ma & before), re = at_e + __popc(me & before);
-        if (above || (tie && re < need)) out[ra + min(re, need)] = i + lane;
-        at_a += __popc(ma);
-        at_e += __popc(me);
-    }
-    for (int i = total + threadIdx.x; i < a.n_sel; i += kPickThreads) out[i] = -1;
+    // no more pages than places: all candidates; else the keys above the n-th and the
+    // first ties with it
+    const uint32_t T = n > a.n_sel ? kth_largest<THREADS>(keys, n, a.n_sel, sc) : kNever;
+    int need = 0, picked = 0;
+    in_order<THREADS>(
+        keys, n, T, sc,
+        [&](int above, int, int) {
+            need = T == kNever ? 0 : a.n_sel - above;
+            picked = above + need;
+        },
+        [&](int i, uint32_t k, int above, int ties, int) {
+            if (k > T || (k == T && ties < need)) out[above + min(ties, need)] = i;
+        });
+    for (int i = picked + threadIdx.x; i < a.n_sel; i += THREADS) out[i] = -1;
 }
 
-int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
+template <int THREADS>
+static cudaError_t launch_pick(const SelectArgs &a, cudaStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>((a.L.cap + kScoreWarps * 16 - 1) / (kScoreWarps * 16)), a.L.Hk, a.L.S);
-    if (D == 128) score_kernel<128><<<grid, kScoreWarps * 32, 0, st>>>(a);
-    else score_kernel<64><<<grid, kScoreWarps * 32, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(h, e, "page score launch");
     static KernelAttrCache cache;
     const bool in_smem = a.L.cap <= kPickSmemKeys;
     const int smem = in_smem ? static_cast<int>(a.L.cap) * 4 : 0;
     if (smem > 32 * 1024) {
-        e = kernel_smem_optin(cache, reinterpret_cast<const void *>(pick_kernel), smem, kPickThreads, nullptr);
-        if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(page choice)");
+        const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(pick_kernel<THREADS>), smem, THREADS, nullptr);
+        if (e != cudaSuccess) return e;
     }
-    pick_kernel<<<static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk), kPickThreads, smem, st>>>(a, in_smem);
-    return cuda_fail(h, cudaGetLastError(), "page choice launch");
+    pick_kernel<THREADS><<<static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk), THREADS, smem, st>>>(a, in_smem);
+    return cudaGetLastError();
+}
+
+int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
+{
+    // two CTAs a SM in all, no more than groups of 16 pages for their warps
+    const int64_t lists = static_cast<int64_t>(a.L.S) * a.L.Hk;
+    const int64_t most = (a.L.cap + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
+    const int64_t want = std::max<int64_t>(1, (2 * h->sm_count + lists - 1) / lists);
+    const dim3 grid(static_cast<unsigned>(std::min(most, want)), a.L.Hk, a.L.S);
+    if (D == 128) score_kernel<128><<<grid, kScoreWarps * 32, 0, st>>>(a);
+    else score_kernel<64><<<grid, kScoreWarps * 32, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(h, e, "page score launch");
+    // fewer threads meet sooner: worth it while each has at most four keys
+    e = a.L.cap <= 1024 ? launch_pick<256>(a, st) : launch_pick<1024>(a, st);
+    return cuda_fail(h, e, "page choice launch");
 }
 
 // ------------------------------------------------------------------ eviction
 
 // One CTA a list.  `keys` is shared memory, or the list's part of mass_out, which
 // is written last and holds its keys until then.
-__global__ void __launch_bounds__(kPickThreads) evict_kernel(const Lists L, const float *mass, int n_keep, int n_first,
-                                                            int n_last, int32_t *ids_out, float *mass_out,
-                                                            int32_t *kv_len_out, int32_t *freed_out, bool in_smem)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_kernel(const Lists L, const float *mass, int n_keep, int n_first,
+                                                       int n_last, int32_t *ids_out, float *mass_out,
+                                                       int32_t *kv_len_out, int32_t *freed_out, bool in_smem)
 {
     extern __shared__ uint32_t s_keys[];
-    __shared__ PickScratch sc;
+    __shared__ PickScratch<THREADS> sc;
     const int kh = blockIdx.x, s = blockIdx.y;
     const int64_t list = static_cast<int64_t>(s) * L.Hk + kh;
     const int64_t len = list_len(L, s);
-    if (kh == 0 && threadIdx.x == 0 && len < max(0, L.kv_len[s])) atomicOr(L.status, kStatusList);
     const int cap = static_cast<int>(L.cap);
     const int n = static_cast<int>((len + kPage - 1) / kPage);
     const int32_t *ids = L.ids + list * L.cap;
@@ -373,9 +405,12 @@ __global__ void __launch_bounds__(kPickThreads) evict_kernel(const Lists L, cons
     float *om = mass_out + list * L.cap;
     int32_t *of = freed_out + list * L.cap;
     const int out_n = max(0, n - n_keep);                 // pages taken out
-    if (kh == 0 && threadIdx.x == 0) kv_len_out[s] = static_cast<int32_t>(len - static_cast<int64_t>(out_n) * kPage);
+    if (kh == 0 && threadIdx.x == 0) {
+        if (len < max(0, L.kv_len[s])) atomicOr(L.status, kStatusList);
+        kv_len_out[s] = static_cast<int32_t>(len - static_cast<int64_t>(out_n) * kPage);
+    }
     if (out_n == 0) {
-        for (int i = threadIdx.x; i < cap; i += kPickThreads) {
+        for (int i = threadIdx.x; i < cap; i += THREADS) {
             oi[i] = ids[i];
             om[i] = i < n ? m[i] : 0.f;
             of[i] = -1;
@@ -384,66 +419,78 @@ __global__ void __launch_bounds__(kPickThreads) evict_kernel(const Lists L, cons
     }
     // an absent page ranks below every weight, the kept ends above
     uint32_t *keys = in_smem ? s_keys : reinterpret_cast<uint32_t *>(om);
-    for (int i = threadIdx.x; i < n; i += kPickThreads)
+    for (int i = threadIdx.x; i < n; i += THREADS)
         keys[i] = i < n_first || i >= n - n_last ? kAlways : ids[i] < 0 ? kNever : order_key(m[i]);
+    // what lies behind the last token follows the kept pages
+    for (int i = n + threadIdx.x; i < cap; i += THREADS) oi[i - out_n] = ids[i];
+    for (int i = cap - out_n + threadIdx.x; i < cap; i += THREADS) oi[i] = -1;
     __syncthreads();
-    const uint32_t T = kth_largest(keys, n, n_keep, sc);
-    __syncthreads();
-    const int above = ordered(n, sc.warp_n, [&](int i) { return keys[i] > T; }, [](int, int) {});
-    const int need = n_keep - above;
-    // ties beyond the first `need` go: marked by key 0, the others by T + 1.  (T
-    // can be kNever: absent pages are then kept for want of others, lowest index first.)
-    const int ties = ordered(n, sc.warp_n, [&](int i) { return keys[i] == T; },
-                             [&](int i, int rank) { of[rank] = i; });
-    __syncthreads();
-    for (int r = threadIdx.x; r < ties; r += kPickThreads) keys[of[r]] = r < need ? 0xffffffffu : 0u;
-    __syncthreads();
-    auto kept = [&](int i) { return keys[i] > T; };
-    ordered(n, sc.warp_n, kept, [&](int i, int rank) { oi[rank] = ids[i]; });
-    const int freed = ordered(n, sc.warp_n, [&](int i) { return !kept(i) && ids[i] >= 0; },
-                              [&](int i, int rank) { of[rank] = ids[i]; });
-    for (int i = n + threadIdx.x; i < cap; i += kPickThreads) oi[i - out_n] = ids[i];
-    for (int i = cap - out_n + threadIdx.x; i < cap; i += kPickThreads) oi[i] = -1;
-    for (int i = freed + threadIdx.x; i < cap; i += kPickThreads) of[i] = -1;
-    if (in_smem) {
-        ordered(n, sc.warp_n, kept, [&](int i, int rank) { om[rank] = m[i]; });
-    } else {
-        // the keys lie in om: a kept page's weight moves to a lower place, whose key
-        // has been used by then, one run of kPickThreads indices at a time
-        int at = 0;
-        for (int b = 0; b < n; b += kPickThreads) {
-            const int i = b + static_cast<int>(threadIdx.x);
-            const bool on = i < n && kept(i);
-            const unsigned ball = __ballot_sync(0xffffffffu, on);
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) sc.warp_n[threadIdx.x >> 5] = __popc(ball);
-            __syncthreads();
-            int before = at, all = 0;
-            for (int w = 0; w < kPickWarps; ++w) {
-                if (w < static_cast<int>(threadIdx.x >> 5)) before += sc.warp_n[w];
-                all += sc.warp_n[w];
+    const uint32_t T = kth_largest<THREADS>(keys, n, n_keep, sc);
+    // (T can be kNever: absent pages are then kept for want of others, and none is freed)
+    int need = 0, freed = 0;
+    in_order<THREADS>(
+        keys, n, T, sc,
+        [&](int above, int, int nevers) {
+            need = n_keep - above;
+            freed = T == kNever ? 0 : out_n - nevers;
+        },
+        [&](int i, uint32_t k, int above, int ties, int nevers) {
+            const int at = above + min(ties, need);       // kept pages before i
+            if (k > T || (k == T && ties < need)) {
+                oi[at] = ids[i];
+                if (in_smem) om[at] = m[i];
+            } else if (k != kNever) {
+                of[i - at - nevers] = ids[i];             // taken out before i, absent ones apart
             }
-            if (on) om[before + __popc(ball & ((1u << (threadIdx.x & 31)) - 1u))] = m[i];
-            at += all;
+        });
+    for (int i = freed + threadIdx.x; i < cap; i += THREADS) of[i] = -1;
+    if (!in_smem) {
+        // the keys lie in om: a kept page's weight moves to a lower place, whose key
+        // has been used by then, one run of THREADS indices at a time
+        __syncthreads();
+        constexpr int W = THREADS / 32;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        int above = 0, ties = 0;
+        for (int b = 0; b < n; b += THREADS) {
+            const int i = b + static_cast<int>(threadIdx.x);
+            const uint32_t k = i < n ? keys[i] : 0u;
+            const unsigned m0 = __ballot_sync(0xffffffffu, i < n && k > T), m1 = __ballot_sync(0xffffffffu, i < n && k == T);
+            __syncthreads();
+            if (lane == 0) {
+                sc.n[0][warp] = __popc(m0);
+                sc.n[1][warp] = __popc(m1);
+            }
+            __syncthreads();
+            const int x0 = lane < W ? sc.n[0][lane] : 0, x1 = lane < W ? sc.n[1][lane] : 0;
+            const unsigned before = (1u << lane) - 1u;
+            const int a0 = above + __reduce_add_sync(0xffffffffu, lane < warp ? x0 : 0) + __popc(m0 & before);
+            const int a1 = ties + __reduce_add_sync(0xffffffffu, lane < warp ? x1 : 0) + __popc(m1 & before);
+            above += __reduce_add_sync(0xffffffffu, x0);
+            ties += __reduce_add_sync(0xffffffffu, x1);
+            if (i < n && (k > T || (k == T && a1 < need))) om[a0 + min(a1, need)] = m[i];
             __syncthreads();
         }
     }
-    __syncthreads();
-    for (int i = n_keep + threadIdx.x; i < cap; i += kPickThreads) om[i] = 0.f;
+    for (int i = n_keep + threadIdx.x; i < cap; i += THREADS) om[i] = 0.f;
 }
 
 int launch_evict(skv_handle *h, const Lists &L, const float *mass, int n_keep, int n_first, int n_last,
                  int32_t *ids_out, float *mass_out, int32_t *kv_len_out, int32_t *freed_out, cudaStream_t st)
 {
+    constexpr int kThreads = 1024;
     static KernelAttrCache cache;
     const bool in_smem = L.cap <= kPickSmemKeys;
     const int smem = in_smem ? static_cast<int>(L.cap) * 4 : 0;
     if (smem > 32 * 1024) {
-        const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(evict_kernel), smem, kPickThreads, nullptr);
+        const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(evict_kernel<kThreads>), smem, kThreads, nullptr);
         if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(eviction)");
     }
-    evict_kernel<<<dim3(L.Hk, L.S), kPickThreads, smem, st>>>(L, mass, n_keep, n_first, n_last, ids_out, mass_out,
-                                                             kv_len_out, freed_out, in_smem);
+    const dim3 grid(L.Hk, L.S);
+    if (L.cap <= 1024)
+        evict_kernel<256><<<grid, 256, smem, st>>>(L, mass, n_keep, n_first, n_last, ids_out, mass_out, kv_len_out, freed_out, true);
+    else
+        evict_kernel<kThreads><<<grid, kThreads, smem, st>>>(L, mass, n_keep, n_first, n_last, ids_out, mass_out, kv_len_out,
+                                                            freed_out, in_smem);
     return cuda_fail(h, cudaGetLastError(), "eviction launch");
 }
 
