@@ -50,6 +50,30 @@ struct AttnArgs {
     __host__ __device__ int64_t token(int s, int t) const { return static_cast<int64_t>(s) * nq_ld + tok0 + t; }
 };
 
+// Programmatic dependent launch.  Every kernel over 8-bit pages is launched while
+// the one before it on the stream ends; it reads and writes nothing of memory
+// before start(), which waits for the whole of that kernel (and so, as each one
+// waits, for all before it).  About 1 us a launch.  None lets its successor come
+// any earlier: CTAs that wait on an SM keep those that work from spreading (62
+// against 73 us for a selection with its attention).
+__device__ __forceinline__ void start() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 // Tokens of sequence s that its list can hold.
 __device__ __forceinline__ int64_t list_len(const Lists &L, int s)
 {

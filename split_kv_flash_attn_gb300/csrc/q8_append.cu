@@ -34,24 +34,41 @@ struct AppendArgs {
     int n_max;
 };
 
+// Eight values as they come, and as fp32 numbers.
 template <typename X>
-__device__ __forceinline__ void load8(const X *p, float (&v)[8])
-{
-    if constexpr (sizeof(X) == 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+    uint4 raw[sizeof(X) / 2];
+
+    __device__ __forceinline__ void load(const X *p)
+    {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+        for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i) raw[i] = ld_stream16(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+        if constexpr (sizeof(X) == 4) {
+            const uint32_t z[4] = {raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = __uint_as_float(w[i]);
+                v[4 + i] = __uint_as_float(z[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
         }
     }
-}
+};
 
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
 {
@@ -67,6 +84,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     __shared__ float s_max[kAppendThreads / 32];
     __shared__ int8_t s_lut[256];
     __shared__ uint32_t s_lo[kAppendThreads / 32][TPR][2], s_hi[kAppendThreads / 32][TPR][2];
+    start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int which = blockIdx.x & 1;
     const int kh = blockIdx.y, s = blockIdx.z;
@@ -76,37 +94,40 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     const int64_t blk = len / kPage + (blockIdx.x >> 1);
     const int64_t p0 = blk * kPage;                  // token of the page's row 0
     if (p0 >= len + n) return;
+    const int r_lo = static_cast<int>(max(int64_t(0), len - p0));            // first row written
+    const int r_hi = static_cast<int>(min(int64_t(kPage), len + n - p0));
+    const int c8 = (tid % TPR) * 8, r0 = tid / TPR;
+    const X *x = static_cast<const X *>(a.x[which]);
+    // the values and the page's id are on their way together
+    Eight<X> in[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = r0 + i * RPP;
+        if (r >= r_lo && r < r_hi)
+            in[i].load(x + ((static_cast<int64_t>(s) * a.n_max + (p0 + r - len)) * a.L.Hk + kh) * D + c8);
+        else
+            in[i].clear();
+    }
     const int64_t entry = (static_cast<int64_t>(s) * a.L.Hk + kh) * a.L.cap + blk;
     const int64_t id = blk < a.L.cap ? __ldg(a.L.ids + entry) : -1;
     if (id < 0 || id >= a.L.n_pages) {
         if (tid == 0) atomicOr(a.L.status, kStatusAppend);
         return;
     }
-    const int r_lo = static_cast<int>(max(int64_t(0), len - p0));            // first row written
-    const int r_hi = static_cast<int>(min(int64_t(kPage), len + n - p0));
-    const int c8 = (tid % TPR) * 8, r0 = tid / TPR;
-    const X *x = static_cast<const X *>(a.x[which]);
-    float v[PASSES][8];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = r0 + i * RPP;
-        if (r >= r_lo && r < r_hi)
-            load8(x + ((static_cast<int64_t>(s) * a.n_max + (p0 + r - len)) * a.L.Hk + kh) * D + c8, v[i]);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
     const float d0 = r_lo > 0 ? a.scale[which][id] : 0.f;
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i)
+    for (int i = 0; i < PASSES; ++i) {
+        float v[8];
+        in[i].values(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float m = fabsf(v[i][e]);
+            const float m = fabsf(v[e]);
             amax = fmaxf(amax, m <= 3.402823466e38f ? m : 0.f);             // finite values only
         }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    // (magnitudes: their order is that of their bits)
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
     if (lane == 0) s_max[warp] = amax;
     __syncthreads();
 #pragma unroll
@@ -122,18 +143,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     for (int i = 0; i < PASSES; ++i) {
         const int r = r0 + i * RPP;
         if (r < r_lo || r >= r_hi) continue;
+        float v[8];
+        in[i].values(v);
         int q[8];
         bool sure = d1 > 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float t = v[i][e] * up * rd;
+            const float t = v[e] * up * rd;
             const float r = rintf(t);
             sure = sure && fabsf(t - r) < 0.5f - 0x1p-13f;               // (false for what is not finite)
             q[e] = static_cast<int>(r);
         }
         if (!sure) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = d1 > 0.f ? nearest_code(v[i][e] * up, d1 * up) : 0;
+            for (int e = 0; e < 8; ++e) q[e] = d1 > 0.f ? nearest_code(v[e] * up, d1 * up) : 0;
         }
         const uint32_t w0 = pack4(q[0], q[1], q[2], q[3]), w1 = pack4(q[4], q[5], q[6], q[7]);
         *reinterpret_cast<uint2 *>(page + r * D + c8) = make_uint2(w0, w1);
@@ -219,14 +242,14 @@ int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_
     // a run of n tokens touches at most ceil((n + 63) / 64) pages
     const int64_t blocks = (static_cast<int64_t>(n_max) + 2 * kPage - 2) / kPage;
     const dim3 grid(static_cast<unsigned>(2 * blocks), L.Hk, L.S);
-    if (x_type == SKV_F32) {
-        if (pool.D == 128) append_kernel<128, float><<<grid, kAppendThreads, 0, st>>>(a);
-        else append_kernel<64, float><<<grid, kAppendThreads, 0, st>>>(a);
-    } else {
-        if (pool.D == 128) append_kernel<128, __half><<<grid, kAppendThreads, 0, st>>>(a);
-        else append_kernel<64, __half><<<grid, kAppendThreads, 0, st>>>(a);
-    }
-    return cuda_fail(h, cudaGetLastError(), "8-bit append launch");
+    cudaError_t e;
+    if (x_type == SKV_F32)
+        e = pool.D == 128 ? launch(append_kernel<128, float>, grid, kAppendThreads, 0, st, a)
+                          : launch(append_kernel<64, float>, grid, kAppendThreads, 0, st, a);
+    else
+        e = pool.D == 128 ? launch(append_kernel<128, __half>, grid, kAppendThreads, 0, st, a)
+                          : launch(append_kernel<64, __half>, grid, kAppendThreads, 0, st, a);
+    return cuda_fail(h, e, "8-bit append launch");
 }
 
 }  // namespace q8

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         for (int i = 0; i < 2 * NS; ++i) tc::mbar_init(bar0 + 8 * i, i < NS ? 1 : 2);
         tc::fence_barrier_init();
     }
+    start();
 
     // ---- the plan: total pages, this CTA's piece, the list that it starts in --
     uint64_t sum = 0;
@@ -654,6 +655,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
 // of 2^(half page - row).  Rows are added in their order.
 __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass)
 {
+    start();
     const int kh = blockIdx.y, s = blockIdx.z;
     const int64_t unit = static_cast<int64_t>(s) * a.L.Hk + kh;
     const int rows = a.nq * a.G;
@@ -698,8 +700,7 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass
 int launch_mass(skv_handle *h, const AttnArgs &a, float *mass, cudaStream_t st)
 {
     const unsigned bx = a.sel ? 1u : static_cast<unsigned>((a.L.cap + 127) / 128);
-    mass_kernel<<<dim3(bx, a.L.Hk, a.L.S), 128, 0, st>>>(a, mass);
-    return cuda_fail(h, cudaGetLastError(), "page weight launch");
+    return cuda_fail(h, launch(mass_kernel, dim3(bx, a.L.Hk, a.L.S), 128, 0, st, a, mass), "page weight launch");
 }
 
 int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pages, int D, int rows)
@@ -727,8 +728,7 @@ static int launch_one(skv_handle *h, const CUtensorMap &mk, const CUtensorMap &m
                                             warps_of(NC) * 32 + 32, nullptr);
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(8-bit decode)");
     if (h->prof_before) cudaEventRecord(h->prof_before, st);
-    decode_kernel<D, NC, HILO, F16><<<grid, warps_of(NC) * 32 + 32, smem, st>>>(mk, mv, a);
-    const cudaError_t l = cudaGetLastError();
+    const cudaError_t l = launch(decode_kernel<D, NC, HILO, F16>, dim3(grid), warps_of(NC) * 32 + 32, smem, st, mk, mv, a);
     if (h->prof_after) cudaEventRecord(h->prof_after, st);
     return cuda_fail(h, l, "8-bit decode launch");
 }

@@ -142,6 +142,7 @@ __device__ __forceinline__ void check_lengths(const AttnArgs &a, int t, int n)
 // The plan of many entries: prefix sums of their tiles.
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, int n_pairs, uint32_t *plan)
 {
+    start();
     __shared__ uint32_t s_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t n = static_cast<int64_t>(a.L.S) * n_pairs;
@@ -265,21 +266,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int np = pa.n_pairs;
-    const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
-    Walk walk{pa.plan, np, a.L.S, a.L.Hk, 0};
-    uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
-    if (n_entries <= kPlanHere) {               // few entries: every CTA counts them itself
-        for (int e = warp; e < n_entries; e += kPfThreads / 32) {
-            const uint32_t x = entry_tiles(a, np, e);
-            if (lane == 0) s_plan[e] = x;
-        }
-        if (blockIdx.x == 0) check_lengths(a, tid, kPfThreads);
-        walk.plan = s_plan;
-    } else if (n_entries <= kPlanSmem) {
-        for (int i = tid; i <= n_entries; i += kPfThreads) s_plan[i] = __ldcg(pa.plan + i);
-        walk.plan = s_plan;
-    }
     if (tid == 0) s_abort = 0;
     if (warp == 0) {
         tc::tmem_alloc<512>(smem_addr(&s_tmem));
@@ -299,6 +285,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         }
         for (int i = 0; i < 4; ++i) tc::mbar_init(bar(PB_META + i), 2);
         tc::fence_barrier_init();
+    }
+    start();
+    const int np = pa.n_pairs;
+    const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
+    Walk walk{pa.plan, np, a.L.S, a.L.Hk, 0};
+    uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
+    if (n_entries <= kPlanHere) {               // few entries: every CTA counts them itself
+        for (int e = warp; e < n_entries; e += kPfThreads / 32) {
+            const uint32_t x = entry_tiles(a, np, e);
+            if (lane == 0) s_plan[e] = x;
+        }
+        if (blockIdx.x == 0) check_lengths(a, tid, kPfThreads);
+        walk.plan = s_plan;
+    } else if (n_entries <= kPlanSmem) {
+        for (int i = tid; i <= n_entries; i += kPfThreads) s_plan[i] = __ldcg(pa.plan + i);
+        walk.plan = s_plan;
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -790,6 +792,7 @@ constexpr int kMergeRows = 32;
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa, int pieces)
 {
+    start();
     const AttnArgs &a = pa.a;
     constexpr int LPR = D / 4, RPP = 256 / LPR;
     const int np = pa.n_pairs;
@@ -851,6 +854,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa
 // rows in the lanes' order.
 __global__ void __launch_bounds__(256) prefill_mass_kernel(const AttnArgs a, float *mass)
 {
+    start();
     const int kh = blockIdx.y, s = blockIdx.z;
     const int64_t unit = static_cast<int64_t>(s) * a.L.Hk + kh;
     const int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -878,22 +882,20 @@ static int launch_one(skv_handle *h, const PrefillArgs &pa, int grid, cudaStream
     const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(prefill_kernel<D, HILO>), smem, kPfThreads, nullptr);
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(8-bit prefill)");
     if (h->prof_before) cudaEventRecord(h->prof_before, st);
-    prefill_kernel<D, HILO><<<grid, kPfThreads, smem, st>>>(pa);
-    cudaError_t l = cudaGetLastError();
+    const cudaError_t l = launch(prefill_kernel<D, HILO>, dim3(grid), kPfThreads, smem, st, pa);
     if (h->prof_after) cudaEventRecord(h->prof_after, st);
     if (l != cudaSuccess) return cuda_fail(h, l, "8-bit prefill launch");
     const int units = pa.a.L.S * pa.a.L.Hk * pa.n_pairs;
     const int rows = std::min(2 * kPM, pa.a.rows);
-    prefill_merge_kernel<D><<<dim3((rows + kMergeRows - 1) / kMergeRows, units), 256, 0, st>>>(pa, grid);
-    return cuda_fail(h, cudaGetLastError(), "8-bit prefill merge launch");
+    return cuda_fail(h, launch(prefill_merge_kernel<D>, dim3((rows + kMergeRows - 1) / kMergeRows, units), 256, 0, st, pa, grid),
+                     "8-bit prefill merge launch");
 }
 
 int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, uint32_t *plan, int n_pairs, float *mass, int grid,
                    cudaStream_t st)
 {
     if (static_cast<int64_t>(a.L.S) * n_pairs > kPlanHere) {
-        prefill_plan_kernel<<<1, 1024, 0, st>>>(a, n_pairs, plan);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch(prefill_plan_kernel, dim3(1), 1024, 0, st, a, n_pairs, plan);
         if (e != cudaSuccess) return cuda_fail(h, e, "8-bit prefill plan launch");
     }
     const PrefillArgs pa{a, plan, n_pairs, f16};
@@ -901,8 +903,8 @@ int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, uint32_t *
     if (D == 128) rc = f16 ? launch_one<128, false>(h, pa, grid, st) : launch_one<128, true>(h, pa, grid, st);
     else rc = f16 ? launch_one<64, false>(h, pa, grid, st) : launch_one<64, true>(h, pa, grid, st);
     if (rc || !mass) return rc;
-    prefill_mass_kernel<<<dim3(static_cast<unsigned>((a.L.cap + 7) / 8), a.L.Hk, a.L.S), 256, 0, st>>>(a, mass);
-    return cuda_fail(h, cudaGetLastError(), "page weight launch");
+    return cuda_fail(h, launch(prefill_mass_kernel, dim3(static_cast<unsigned>((a.L.cap + 7) / 8), a.L.Hk, a.L.S), 256, 0, st, a, mass),
+                     "page weight launch");
 }
 
 }  // namespace q8

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
     __shared__ uint2 s_q[kScoreCols / 8][KS][32];         // coded queries in fragment order
     __shared__ float s_dq[kScoreCols];
     __shared__ float s_f[kScoreWarps][16][kScoreCols + 1];
+    start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int kh = blockIdx.y, s = blockIdx.z;
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a, bool 
 {
     extern __shared__ uint32_t s_keys[];
     __shared__ PickScratch<THREADS> sc;
+    start();
     const int64_t row = blockIdx.x;
     const int64_t tok = row / a.L.Hk;
     const int s = static_cast<int>(tok / a.nq);
@@ -363,8 +365,8 @@ static cudaError_t launch_pick(const SelectArgs &a, cudaStream_t st)
         const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(pick_kernel<THREADS>), smem, THREADS, nullptr);
         if (e != cudaSuccess) return e;
     }
-    pick_kernel<THREADS><<<static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk), THREADS, smem, st>>>(a, in_smem);
-    return cudaGetLastError();
+    return launch(pick_kernel<THREADS>, dim3(static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk)), THREADS, smem, st,
+                  a, in_smem);
 }
 
 int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
@@ -374,9 +376,8 @@ int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
     const int64_t most = (a.L.cap + kScoreWarps * 16 - 1) / (kScoreWarps * 16);
     const int64_t want = std::max<int64_t>(1, (2 * h->sm_count + lists - 1) / lists);
     const dim3 grid(static_cast<unsigned>(std::min(most, want)), a.L.Hk, a.L.S);
-    if (D == 128) score_kernel<128><<<grid, kScoreWarps * 32, 0, st>>>(a);
-    else score_kernel<64><<<grid, kScoreWarps * 32, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = D == 128 ? launch(score_kernel<128>, grid, kScoreWarps * 32, 0, st, a)
+                             : launch(score_kernel<64>, grid, kScoreWarps * 32, 0, st, a);
     if (e != cudaSuccess) return cuda_fail(h, e, "page score launch");
     // fewer threads meet sooner: worth it while each has at most four keys
     e = a.L.cap <= 1024 ? launch_pick<256>(a, st) : launch_pick<1024>(a, st);
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(const Lists L, const flo
 {
     extern __shared__ uint32_t s_keys[];
     __shared__ PickScratch<THREADS> sc;
+    start();
     const int kh = blockIdx.x, s = blockIdx.y;
     const int64_t list = static_cast<int64_t>(s) * L.Hk + kh;
     const int64_t len = list_len(L, s);
@@ -486,12 +488,12 @@ int launch_evict(skv_handle *h, const Lists &L, const float *mass, int n_keep, i
         if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(eviction)");
     }
     const dim3 grid(L.Hk, L.S);
-    if (L.cap <= 1024)
-        evict_kernel<256><<<grid, 256, smem, st>>>(L, mass, n_keep, n_first, n_last, ids_out, mass_out, kv_len_out, freed_out, true);
-    else
-        evict_kernel<kThreads><<<grid, kThreads, smem, st>>>(L, mass, n_keep, n_first, n_last, ids_out, mass_out, kv_len_out,
-                                                            freed_out, in_smem);
-    return cuda_fail(h, cudaGetLastError(), "eviction launch");
+    const cudaError_t e =
+        L.cap <= 1024 ? launch(evict_kernel<256>, grid, 256, smem, st, L, mass, n_keep, n_first, n_last, ids_out, mass_out,
+                               kv_len_out, freed_out, true)
+                      : launch(evict_kernel<kThreads>, grid, kThreads, smem, st, L, mass, n_keep, n_first, n_last, ids_out,
+                               mass_out, kv_len_out, freed_out, in_smem);
+    return cuda_fail(h, e, "eviction launch");
 }
 
 }  // namespace q8
