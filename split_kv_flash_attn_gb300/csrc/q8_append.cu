@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
 }
 
 template <int D, typename X>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a)
 {
     constexpr int TPR = D / 8;                       // threads a row
     constexpr int RPP = kAppendThreads / TPR;        // rows a pass

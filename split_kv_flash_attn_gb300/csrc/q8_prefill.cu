@@ -48,12 +48,7 @@ constexpr int kPfThreads = (kMmaWarp + 4) * 32;
 // Registers of a thread by role: 16 warps launch with 128 each, the softmax groups
 // take what the others can spare (spilled, they would go to an L1 of 20 KB:
 // 396 us against PFTIME at 512 tokens over 32768 keys).
-#ifndef VRS
-#define VRS 176
-#define VRP 104
-#define VRM 56
-#endif
-constexpr int kRegSoft = VRS, kRegProd = VRP, kRegMma = VRM;
+constexpr int kRegSoft = 176, kRegProd = 104, kRegMma = 56;
 static_assert(2 * kRegSoft + kRegProd + kRegMma <= 4 * 128, "no more than the launch has");
 static_assert(kRegSoft >= 128 && kRegProd <= 128 && kRegMma <= 128, "the first is an increase, the others decreases");
 template <int N>
@@ -66,10 +61,7 @@ __device__ __forceinline__ void fewer_regs()
 {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-#ifndef VPT
-#define VPT 3
-#endif
-constexpr uint32_t kPieceTiles = VPT;                // fewest key tiles of a piece: each costs set-up and merge
+constexpr uint32_t kPieceTiles = 3;                // fewest key tiles of a piece: each costs set-up and merge
 constexpr int kPlanHere = 256;                  // plan entries that the prefill kernel counts itself
 constexpr int kPlanSmem = 1024;                 // plan entries kept in shared memory
 constexpr float kPfShift = 8.f, kPfGrow = 5.f, kPfScaleGrow = 2.f;
@@ -786,9 +778,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     }
 }
 
-// Rows of units that several CTAs share: their pieces together, in order.  One CTA
-// takes 32 rows of a unit, D / 4 lanes a row, so that the whole machine merges.
-constexpr int kMergeRows = 32;
+// Rows of units that several CTAs share: their pieces together, in order.  D / 4
+// lanes a row, kMergeRows rows a thread.
+constexpr int kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa, int pieces)
 {
@@ -808,45 +800,58 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa
     const uint32_t c_lo = unit0 / chunk, c_hi = (unit0 + (pe1 - pe) - 1) / chunk;
     if (c_lo == c_hi) return;
     const int lane = threadIdx.x % LPR;
+    float M[kMergeRows], W[kMergeRows], v[kMergeRows][4];
+    int rr[kMergeRows];                         // rows of the unit
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        rr[i] = (blockIdx.x * kMergeRows + i) * RPP + threadIdx.x / LPR;
+        M[i] = -INFINITY;
+        W[i] = v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+    }
+    // pieces four at a time, all their loads before any use
 #pragma unroll 1
-    for (int i = 0; i < kMergeRows / RPP; ++i) {
-        const int rr = blockIdx.x * kMergeRows + i * RPP + threadIdx.x / LPR;   // row of the unit
-        const int row = pr * 2 * kPM + rr;
-        if (row >= a.rows) return;
-        // piece c of the unit is slot 2c, or 2c + 1 when an earlier unit begins CTA c's piece
-        auto at_of = [&](uint32_t c) {
-            return (2 * static_cast<int64_t>(c) + (c == c_lo && unit0 > c * chunk ? 1 : 0)) * 2 * kPM + rr;
-        };
-        float M = -INFINITY, W = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (uint32_t c = c_lo; c <= c_hi; ++c) {
-            const float z = __ldcg(a.part_ml + at_of(c));
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at_of(c) * D) + lane);
-            if (z > M) {
-                const float b = fast_exp2(M - z);
-                M = z;
-                W *= b;
-                v[0] *= b;
-                v[1] *= b;
-                v[2] *= b;
-                v[3] *= b;
+    for (uint32_t c0 = c_lo; c0 <= c_hi; c0 += 4) {
+        float z[kMergeRows][4];
+        float4 y[kMergeRows][4];
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t c = c0 + e;
+                // piece c of the unit is slot 2c, or 2c + 1 when an earlier unit begins CTA c's piece
+                const int64_t at = (2 * static_cast<int64_t>(c) + (c == c_lo && unit0 > c * chunk ? 1 : 0)) * 2 * kPM + rr[i];
+                const bool on = c <= c_hi && pr * 2 * kPM + rr[i] < a.rows && rr[i] < 2 * kPM;
+                z[i][e] = on ? __ldcg(a.part_ml + at) : -INFINITY;
+                y[i][e] = on ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            const float w = z == -INFINITY ? 0.f : fast_exp2(z - M);
-            W += w;
-            v[0] = fmaf(w, y.x, v[0]);
-            v[1] = fmaf(w, y.y, v[1]);
-            v[2] = fmaf(w, y.z, v[2]);
-            v[3] = fmaf(w, y.w, v[3]);
-        }
-        const float q = W > 0.f ? 1.f / W : 0.f;
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float m = fmaxf(M[i], z[i][e]);
+                const float bo = M[i] == -INFINITY ? 0.f : fast_exp2(M[i] - m);
+                const float bn = z[i][e] == -INFINITY ? 0.f : fast_exp2(z[i][e] - m);
+                M[i] = m;
+                W[i] = fmaf(W[i], bo, bn);
+                v[i][0] = fmaf(v[i][0], bo, bn * y[i][e].x);
+                v[i][1] = fmaf(v[i][1], bo, bn * y[i][e].y);
+                v[i][2] = fmaf(v[i][2], bo, bn * y[i][e].z);
+                v[i][3] = fmaf(v[i][3], bo, bn * y[i][e].w);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        const int row = pr * 2 * kPM + rr[i];
+        if (row >= a.rows || rr[i] >= 2 * kPM) continue;
+        const float q = W[i] > 0.f ? 1.f / W[i] : 0.f;
         const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
         if (pa.out_f16)
             *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + lane * 4) =
-                make_uint2(pack_half2(v[0] * q, v[1] * q), pack_half2(v[2] * q, v[3] * q));
+                make_uint2(pack_half2(v[i][0] * q, v[i][1] * q), pack_half2(v[i][2] * q, v[i][3] * q));
         else
             *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + lane * 4) =
-                make_float4(v[0] * q, v[1] * q, v[2] * q, v[3] * q);
-        if (lane == 0) a.lse[r] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
+                make_float4(v[i][0] * q, v[i][1] * q, v[i][2] * q, v[i][3] * q);
+        if (lane == 0) a.lse[r] = W[i] > 0.f ? (M[i] + log2f(W[i])) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -887,7 +892,7 @@ static int launch_one(skv_handle *h, const PrefillArgs &pa, int grid, cudaStream
     if (l != cudaSuccess) return cuda_fail(h, l, "8-bit prefill launch");
     const int units = pa.a.L.S * pa.a.L.Hk * pa.n_pairs;
     const int rows = std::min(2 * kPM, pa.a.rows);
-    return cuda_fail(h, launch(prefill_merge_kernel<D>, dim3((rows + kMergeRows - 1) / kMergeRows, units), 256, 0, st, pa, grid),
+    return cuda_fail(h, launch(prefill_merge_kernel<D>, dim3((rows * (D / 4) + 256 * kMergeRows - 1) / (256 * kMergeRows), units), 256, 0, st, pa, grid),
                      "8-bit prefill merge launch");
 }
 

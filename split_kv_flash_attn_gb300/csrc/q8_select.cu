@@ -14,7 +14,7 @@
 //
 // The choice.  Scores become 32-bit keys whose order as unsigned numbers is the
 // scores' order; one CTA for each list finds the n-th largest key two bits at a
-// time, counting keys in shared memory, and writes the picked indices in order by
+// time, counting keys in registers, and writes the picked indices in order by
 // prefix sums over the warps' equal shares.  Ties at the n-th key go to the lowest
 // indices.
 //
@@ -23,6 +23,7 @@
 // counting rounds, each one pass over shared memory and one barrier, about 12 for the
 // keys of one list.
 #include <algorithm>
+#include <type_traits>
 
 #include "q8.cuh"
 
@@ -81,6 +82,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
     constexpr int KS = D / 16, CH = D / 64;
     __shared__ uint2 s_q[kScoreCols / 8][KS][32];         // coded queries in fragment order
     __shared__ float s_dq[kScoreCols];
+    __shared__ int s_nb[kScoreCols];
     __shared__ float s_f[kScoreWarps][16][kScoreCols + 1];
     start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -105,21 +107,42 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
             Extremes<D> nxt;
             nxt.ids_of(a, ids, group0 * 16, group0 < groups ? nb : 0, g);
             __syncthreads();                              // the last round's columns are read
-            // coded queries: one warp a column
-            for (int c = warp; c < ncg * 8; c += kScoreWarps) {
-                constexpr int N = D / 32;
+            // coded queries: a warp takes up to eight columns, their values requested together
+            constexpr int N = D / 32, CPW = kScoreCols / kScoreWarps;
+            uint2 raw[CPW];
+#pragma unroll
+            for (int e = 0; e < CPW; ++e) {
+                const int c = warp + e * kScoreWarps;
+                raw[e] = make_uint2(0, 0);
+                if (c < cols) {
+                    const int tok = t0 + c / nh, head = kh * a.G + h0 + c % nh;
+                    const __half *qp = a.q + ((static_cast<int64_t>(s) * a.nq + tok) * a.H + head) * D + lane * N;
+                    if constexpr (N == 4) raw[e] = __ldg(reinterpret_cast<const uint2 *>(qp));
+                    else raw[e].x = __ldg(reinterpret_cast<const uint32_t *>(qp));
+                }
+            }
+            if (tid < nt) {
+                // pages that hold a key the token sees
+                int64_t seen = len;
+                if (a.q_pos)
+                    seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + static_cast<int64_t>(s) * a.nq + t0 + tid)) + 1));
+                s_nb[tid] = static_cast<int>((seen + kPage - 1) / kPage);
+            }
+#pragma unroll
+            for (int e = 0; e < CPW; ++e) {
+                const int c = warp + e * kScoreWarps;
+                if (c >= ncg * 8) break;
                 float v[N];
                 float top = 0.f;
-                const int tok = t0 + c / nh, head = kh * a.G + h0 + c % nh;
-                const __half *qp = a.q + ((static_cast<int64_t>(s) * a.nq + tok) * a.H + head) * D + lane * N;
-                __half raw[N];
-                if (c < cols) {
-                    if constexpr (N == 4) *reinterpret_cast<uint2 *>(raw) = __ldg(reinterpret_cast<const uint2 *>(qp));
-                    else *reinterpret_cast<uint32_t *>(raw) = __ldg(reinterpret_cast<const uint32_t *>(qp));
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const uint32_t w = i == 0 ? raw[e].x : raw[e].y;
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                    v[i] = f.x;
+                    v[i + 1] = f.y;
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    v[i] = c < cols ? __half2float(raw[i]) : 0.f;
                     const float m = fabsf(v[i]);
                     top = fmaxf(top, m <= 65504.f ? m : 0.f);
                 }
@@ -127,9 +150,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                 top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
                 const float dq = __fdiv_rn(top, 127.f);
                 if (lane == 0) s_dq[c] = dq;
+                // the integer nearest v / dq: by the approximate reciprocal unless that
+                // comes within 2^-13 of a half-integer (its error is below 2^-14)
+                float rd;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(dq));
+                bool sure = dq > 0.f;
+                float r[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float x = v[i] * rd;
+                    r[i] = rintf(x);
+                    sure = sure && fabsf(x - r[i]) < 0.5f - 0x1p-13f;
+                }
+                if (!sure) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) r[i] = dq > 0.f ? static_cast<float>(nearest_code(v[i], dq)) : 0.f;
+                }
                 __half hc[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) hc[i] = __int2half_rn(dq > 0.f ? nearest_code(v[i], dq) : 0);
+                for (int i = 0; i < N; ++i) hc[i] = __float2half_rn(r[i]);
                 // channel d of column c: chunk d/64, t = d/16 % 4, word d/4 % 4, place d % 4
                 const int d = lane * N;
                 __half *dst = reinterpret_cast<__half *>(&s_q[c >> 3][(d >> 6) * 4 + ((d >> 2) & 3)][(c & 7) * 4 + ((d >> 4) & 3)]) + (d & 3);
@@ -193,10 +232,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                     if (blk >= nb) continue;
                     const int64_t row = (static_cast<int64_t>(s) * a.nq + t0 + tok) * a.L.Hk + kh;
                     uint32_t *out = a.keys + row * a.L.cap + blk;
-                    int64_t seen = len;
-                    if (a.q_pos)
-                        seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + static_cast<int64_t>(s) * a.nq + t0 + tok)) + 1));
-                    const int64_t nbq = (seen + kPage - 1) / kPage;
+                    const int nbq = s_nb[tok];
                     uint32_t key = kNever;
                     if (page_id >= 0 && blk < nbq) {
                         key = blk < a.n_first || blk >= nbq - a.n_last ? kAlways : order_key(__fmul_rn(m, page_scale));
@@ -212,27 +248,68 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
 
 // ---------------------------------------------------------------- the choice
 
+// The keys of one list for a CTA of THREADS: each warp takes an equal run of
+// indices, 32 at a time.  KPT > 0: in registers, KPT a thread; 0: where `at` says.
+template <int THREADS, int KPT>
+struct Keys {
+    static constexpr int W = THREADS / 32;
+    uint32_t k[KPT > 0 ? KPT : 1];
+    const uint32_t *at;
+    int n, lo, hi;                                        // the warp's run
+
+    __device__ Keys(int n_, const uint32_t *at_) : at(at_), n(n_)
+    {
+        const int share = (n + THREADS - 1) / THREADS * 32, warp = threadIdx.x >> 5;
+        lo = min(n, warp * share);
+        hi = min(n, lo + share);
+    }
+    // f(i, key of i or 0, whether there is an i) for the lane's index of every step
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        const int lane = threadIdx.x & 31;
+        if constexpr (KPT > 0) {
+#pragma unroll
+            for (int e = 0; e < KPT; ++e)
+                if (lo + 32 * e < hi) f(lo + 32 * e + lane, k[e], lo + 32 * e + lane < hi);
+        } else {
+            for (int i = lo; i < hi; i += 32) f(i + lane, i + lane < hi ? at[i + lane] : 0u, i + lane < hi);
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void fill(F f)             // k of index i = f(i), 0 past the end
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int e = 0; e < KPT; ++e) {
+            const int i = lo + 32 * e + lane;
+            k[e] = i < hi ? f(i) : 0u;
+        }
+    }
+};
+
 template <int THREADS>
 struct PickScratch {
     static constexpr int W = THREADS / 32;
-    int cnt[2][W][3];
+    int cnt[2][3][W];
     uint32_t lo[W], hi[W];
     int n[3][W];
 };
 
-// The k-th largest of keys[0, n) (n >= k >= 1).
-template <int THREADS>
-__device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch<THREADS> &sc)
+// A value T such that the `count` largest keys are those above T and some equal to
+// it (n > count >= 1): the count-th largest key, or, once a prefix of it tells the
+// largest `count` from the others, anything between the two.
+template <int THREADS, int KPT>
+__device__ uint32_t threshold(const Keys<THREADS, KPT> &keys, int count, PickScratch<THREADS> &sc)
 {
     constexpr int W = THREADS / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // bits that all keys share need no rounds
     uint32_t both = 0xffffffffu, any = 0u;
-    for (int i = tid; i < n; i += THREADS) {
-        const uint32_t x = keys[i];
-        both &= x;
+    keys.each([&](int, uint32_t x, bool in) {
+        both &= in ? x : 0xffffffffu;
         any |= x;
-    }
+    });
     both = __reduce_and_sync(0xffffffffu, both);
     any = __reduce_or_sync(0xffffffffu, any);
     if (lane == 0) {
@@ -243,58 +320,53 @@ __device__ uint32_t kth_largest(const uint32_t *keys, int n, int k, PickScratch<
     both = __reduce_and_sync(0xffffffffu, lane < W ? sc.lo[lane] : 0xffffffffu);
     any = __reduce_or_sync(0xffffffffu, lane < W ? sc.hi[lane] : 0u);
     const uint32_t diff = both ^ any;
-    uint32_t found = both;
-    if (diff) {
-        const int top = 31 - __clz(diff);                 // highest bit in which keys differ
-        found = top == 31 ? 0u : both & ~((2u << top) - 1u);
-        int round = 0;
-        for (int b = top & ~1; b >= 0; b -= 2, round ^= 1) {
-            // how many keys reach found + 1, 2, 3 units of 2^b
-            const uint32_t t1 = found | (1u << b), t2 = found | (2u << b), t3 = found | (3u << b);
-            int c1 = 0, c2 = 0, c3 = 0;
-            for (int i = tid; i < n; i += THREADS) {
-                const uint32_t x = keys[i];
-                c1 += x >= t1;
-                c2 += x >= t2;
-                c3 += x >= t3;
-            }
-            c1 = __reduce_add_sync(0xffffffffu, c1);
-            c2 = __reduce_add_sync(0xffffffffu, c2);
-            c3 = __reduce_add_sync(0xffffffffu, c3);
-            if (lane == 0) {
-                sc.cnt[round][warp][0] = c1;
-                sc.cnt[round][warp][1] = c2;
-                sc.cnt[round][warp][2] = c3;
-            }
-            __syncthreads();
-            c1 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][lane][0] : 0);
-            c2 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][lane][1] : 0);
-            c3 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][lane][2] : 0);
-            found = c3 >= k ? t3 : c2 >= k ? t2 : c1 >= k ? t1 : found;
-        }
+    if (diff == 0) return both;
+    const int top = 31 - __clz(diff);                     // highest bit in which keys differ
+    uint32_t found = top == 31 ? 0u : both & ~((2u << top) - 1u);
+    int round = 0;
+    for (int b = top & ~1; b >= 0; b -= 2, round ^= 1) {
+        // how many keys reach found + 1, 2, 3 units of 2^b
+        const uint32_t t1 = found | (1u << b), t2 = found | (2u << b), t3 = found | (3u << b);
+        int c1 = 0, c2 = 0, c3 = 0;
+        keys.each([&](int, uint32_t x, bool) {
+            c1 += x >= t1;
+            c2 += x >= t2;
+            c3 += x >= t3;
+        });
+        c1 = __reduce_add_sync(0xffffffffu, c1);
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        if (lane < 3) sc.cnt[round][lane][warp] = lane == 0 ? c1 : lane == 1 ? c2 : c3;
+        __syncthreads();
+        c1 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][0][lane] : 0);
+        c2 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][1][lane] : 0);
+        c3 = __reduce_add_sync(0xffffffffu, lane < W ? sc.cnt[round][2][lane] : 0);
+        if (c3 == count) return t3 - 1;
+        if (c2 == count) return t2 - 1;
+        if (c1 == count) return t1 - 1;
+        found = c3 > count ? t3 : c2 > count ? t2 : c1 > count ? t1 : found;
     }
     return found;
 }
 
 // In the order of indices, calls emit(i, key, above, ties, nevers) for every i in [0, n):
-// how many earlier keys are above T, equal to it, and kNever.  Each warp takes an
-// equal run of indices.  `totals` receives the counts over all keys before any emit.
-template <int THREADS, typename B, typename E>
-__device__ void in_order(const uint32_t *keys, int n, uint32_t T, PickScratch<THREADS> &sc, B totals, E emit)
+// how many earlier keys are above T, equal to it, and kNever.  `totals` receives the
+// counts over all keys before any emit.
+template <int THREADS, int KPT, typename B, typename E>
+__device__ void in_order(const Keys<THREADS, KPT> &keys, uint32_t T, PickScratch<THREADS> &sc, B totals, E emit)
 {
     constexpr int W = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int share = (n + THREADS - 1) / THREADS * 32;
-    const int lo = min(n, warp * share), hi = min(n, lo + share);
-    int c[3] = {0, 0, 0};
-    for (int i = lo; i < hi; i += 32) {
-        const bool in = i + lane < hi;
-        const uint32_t k = in ? keys[i + lane] : 0u;
-        c[0] += __popc(__ballot_sync(0xffffffffu, in && k > T));
-        c[1] += __popc(__ballot_sync(0xffffffffu, in && k == T));
-        c[2] += __popc(__ballot_sync(0xffffffffu, in && k == kNever));
-    }
-    if (lane < 3) sc.n[lane][warp] = lane == 0 ? c[0] : lane == 1 ? c[1] : c[2];
+    int c0 = 0, c1 = 0, c2 = 0;
+    keys.each([&](int, uint32_t k, bool in) {
+        c0 += in && k > T;
+        c1 += in && k == T;
+        c2 += in && k == kNever;
+    });
+    c0 = __reduce_add_sync(0xffffffffu, c0);
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    if (lane < 3) sc.n[lane][warp] = lane == 0 ? c0 : lane == 1 ? c1 : c2;
     __syncthreads();
     int at[3], all[3];
 #pragma unroll
@@ -305,46 +377,49 @@ __device__ void in_order(const uint32_t *keys, int n, uint32_t T, PickScratch<TH
     }
     totals(all[0], all[1], all[2]);
     const unsigned before = (1u << lane) - 1u;
-    for (int i = lo; i < hi; i += 32) {
-        const bool in = i + lane < hi;
-        const uint32_t k = in ? keys[i + lane] : 0u;
+    keys.each([&](int i, uint32_t k, bool in) {
         const unsigned m0 = __ballot_sync(0xffffffffu, in && k > T), m1 = __ballot_sync(0xffffffffu, in && k == T),
                        m2 = __ballot_sync(0xffffffffu, in && k == kNever);
-        if (in) emit(i + lane, k, at[0] + __popc(m0 & before), at[1] + __popc(m1 & before), at[2] + __popc(m2 & before));
+        if (in) emit(i, k, at[0] + __popc(m0 & before), at[1] + __popc(m1 & before), at[2] + __popc(m2 & before));
         at[0] += __popc(m0);
         at[1] += __popc(m1);
         at[2] += __popc(m2);
-    }
+    });
 }
 
-constexpr int kPickSmemKeys = 48 * 1024;                  // 192 KB of keys
+// Threads and keys a thread for lists of up to `cap` pages: few threads meet sooner
+// and count in registers (4096 pages: 14 us with 1024 threads over shared memory).
+template <typename F>
+auto for_cap(int64_t cap, F f)
+{
+    if (cap <= 1024) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
+    if (cap <= 6144) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 12>());
+    if (cap <= 16384) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 0>());
+}
 
 // One CTA a row (sequence, token, KV head).
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a, bool in_smem)
+template <int THREADS, int KPT>
+__global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a)
 {
-    extern __shared__ uint32_t s_keys[];
-    __shared__ PickScratch<THREADS> sc;
     start();
+    __shared__ PickScratch<THREADS> sc;
     const int64_t row = blockIdx.x;
     const int64_t tok = row / a.L.Hk;
     const int s = static_cast<int>(tok / a.nq);
     int64_t seen = list_len(a.L, s);
-    if (a.q_pos) seen = max(int64_t(0), min(seen, static_cast<int64_t>(a.q_pos[tok]) + 1));
+    if (a.q_pos) seen = max(int64_t(0), min(seen, static_cast<int64_t>(__ldg(a.q_pos + tok)) + 1));
     const int n = static_cast<int>((seen + kPage - 1) / kPage);
-    const uint32_t *keys = a.keys + row * a.L.cap;
+    const uint32_t *src = a.keys + row * a.L.cap;
     int32_t *out = a.sel + row * a.n_sel;
-    if (in_smem) {
-        for (int i = threadIdx.x; i < n; i += THREADS) s_keys[i] = __ldcg(keys + i);
-        __syncthreads();
-        keys = s_keys;
-    }
+    Keys<THREADS, KPT> keys(n, src);
+    if constexpr (KPT > 0) keys.fill([&](int i) { return __ldcg(src + i); });
     // no more pages than places: all candidates; else the keys above the n-th and the
     // first ties with it
-    const uint32_t T = n > a.n_sel ? kth_largest<THREADS>(keys, n, a.n_sel, sc) : kNever;
+    const uint32_t T = n > a.n_sel ? threshold(keys, a.n_sel, sc) : kNever;
     int need = 0, picked = 0;
-    in_order<THREADS>(
-        keys, n, T, sc,
+    in_order(
+        keys, T, sc,
         [&](int above, int, int) {
             need = T == kNever ? 0 : a.n_sel - above;
             picked = above + need;
@@ -353,20 +428,6 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a, bool 
             if (k > T || (k == T && ties < need)) out[above + min(ties, need)] = i;
         });
     for (int i = picked + threadIdx.x; i < a.n_sel; i += THREADS) out[i] = -1;
-}
-
-template <int THREADS>
-static cudaError_t launch_pick(const SelectArgs &a, cudaStream_t st)
-{
-    static KernelAttrCache cache;
-    const bool in_smem = a.L.cap <= kPickSmemKeys;
-    const int smem = in_smem ? static_cast<int>(a.L.cap) * 4 : 0;
-    if (smem > 32 * 1024) {
-        const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(pick_kernel<THREADS>), smem, THREADS, nullptr);
-        if (e != cudaSuccess) return e;
-    }
-    return launch(pick_kernel<THREADS>, dim3(static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk)), THREADS, smem, st,
-                  a, in_smem);
 }
 
 int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
@@ -379,23 +440,24 @@ int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
     cudaError_t e = D == 128 ? launch(score_kernel<128>, grid, kScoreWarps * 32, 0, st, a)
                              : launch(score_kernel<64>, grid, kScoreWarps * 32, 0, st, a);
     if (e != cudaSuccess) return cuda_fail(h, e, "page score launch");
-    // fewer threads meet sooner: worth it while each has at most four keys
-    e = a.L.cap <= 1024 ? launch_pick<256>(a, st) : launch_pick<1024>(a, st);
+    const dim3 rows(static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk));
+    e = for_cap(a.L.cap, [&](auto threads, auto kpt) {
+        return launch(pick_kernel<threads.value, kpt.value>, rows, threads.value, 0, st, a);
+    });
     return cuda_fail(h, e, "page choice launch");
 }
 
 // ------------------------------------------------------------------ eviction
 
-// One CTA a list.  `keys` is shared memory, or the list's part of mass_out, which
-// is written last and holds its keys until then.
-template <int THREADS>
+// One CTA a list.  With KPT = 0 the keys lie in the list's part of mass_out, which is
+// written last.
+template <int THREADS, int KPT>
 __global__ void __launch_bounds__(THREADS) evict_kernel(const Lists L, const float *mass, int n_keep, int n_first,
                                                        int n_last, int32_t *ids_out, float *mass_out,
-                                                       int32_t *kv_len_out, int32_t *freed_out, bool in_smem)
+                                                       int32_t *kv_len_out, int32_t *freed_out)
 {
-    extern __shared__ uint32_t s_keys[];
-    __shared__ PickScratch<THREADS> sc;
     start();
+    __shared__ PickScratch<THREADS> sc;
     const int kh = blockIdx.x, s = blockIdx.y;
     const int64_t list = static_cast<int64_t>(s) * L.Hk + kh;
     const int64_t len = list_len(L, s);
@@ -420,18 +482,27 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(const Lists L, const flo
         return;
     }
     // an absent page ranks below every weight, the kept ends above
-    uint32_t *keys = in_smem ? s_keys : reinterpret_cast<uint32_t *>(om);
-    for (int i = threadIdx.x; i < n; i += THREADS)
-        keys[i] = i < n_first || i >= n - n_last ? kAlways : ids[i] < 0 ? kNever : order_key(m[i]);
+    auto key_of = [&](int i) {
+        const int id = __ldg(ids + i);
+        const float x = __ldg(m + i);
+        return i < n_first || i >= n - n_last ? kAlways : id < 0 ? kNever : order_key(x);
+    };
+    uint32_t *in_om = reinterpret_cast<uint32_t *>(om);
+    Keys<THREADS, KPT> keys(n, in_om);
+    if constexpr (KPT > 0) {
+        keys.fill(key_of);
+    } else {
+        for (int i = threadIdx.x; i < n; i += THREADS) in_om[i] = key_of(i);
+        __syncthreads();
+    }
     // what lies behind the last token follows the kept pages
     for (int i = n + threadIdx.x; i < cap; i += THREADS) oi[i - out_n] = ids[i];
     for (int i = cap - out_n + threadIdx.x; i < cap; i += THREADS) oi[i] = -1;
-    __syncthreads();
-    const uint32_t T = kth_largest<THREADS>(keys, n, n_keep, sc);
+    const uint32_t T = threshold(keys, n_keep, sc);
     // (T can be kNever: absent pages are then kept for want of others, and none is freed)
     int need = 0, freed = 0;
-    in_order<THREADS>(
-        keys, n, T, sc,
+    in_order(
+        keys, T, sc,
         [&](int above, int, int nevers) {
             need = n_keep - above;
             freed = T == kNever ? 0 : out_n - nevers;
@@ -439,23 +510,23 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(const Lists L, const flo
         [&](int i, uint32_t k, int above, int ties, int nevers) {
             const int at = above + min(ties, need);       // kept pages before i
             if (k > T || (k == T && ties < need)) {
-                oi[at] = ids[i];
-                if (in_smem) om[at] = m[i];
+                oi[at] = __ldg(ids + i);
+                if constexpr (KPT > 0) om[at] = __ldg(m + i);
             } else if (k != kNever) {
-                of[i - at - nevers] = ids[i];             // taken out before i, absent ones apart
+                of[i - at - nevers] = __ldg(ids + i);     // taken out before i, absent ones apart
             }
         });
     for (int i = freed + threadIdx.x; i < cap; i += THREADS) of[i] = -1;
-    if (!in_smem) {
-        // the keys lie in om: a kept page's weight moves to a lower place, whose key
-        // has been used by then, one run of THREADS indices at a time
+    if constexpr (KPT == 0) {
+        // a kept page's weight moves to a lower place, whose key has been used by
+        // then, one run of THREADS indices at a time
         __syncthreads();
         constexpr int W = THREADS / 32;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         int above = 0, ties = 0;
         for (int b = 0; b < n; b += THREADS) {
             const int i = b + static_cast<int>(threadIdx.x);
-            const uint32_t k = i < n ? keys[i] : 0u;
+            const uint32_t k = i < n ? in_om[i] : 0u;
             const unsigned m0 = __ballot_sync(0xffffffffu, i < n && k > T), m1 = __ballot_sync(0xffffffffu, i < n && k == T);
             __syncthreads();
             if (lane == 0) {
@@ -479,20 +550,10 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(const Lists L, const flo
 int launch_evict(skv_handle *h, const Lists &L, const float *mass, int n_keep, int n_first, int n_last,
                  int32_t *ids_out, float *mass_out, int32_t *kv_len_out, int32_t *freed_out, cudaStream_t st)
 {
-    constexpr int kThreads = 1024;
-    static KernelAttrCache cache;
-    const bool in_smem = L.cap <= kPickSmemKeys;
-    const int smem = in_smem ? static_cast<int>(L.cap) * 4 : 0;
-    if (smem > 32 * 1024) {
-        const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(evict_kernel<kThreads>), smem, kThreads, nullptr);
-        if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(eviction)");
-    }
-    const dim3 grid(L.Hk, L.S);
-    const cudaError_t e =
-        L.cap <= 1024 ? launch(evict_kernel<256>, grid, 256, smem, st, L, mass, n_keep, n_first, n_last, ids_out, mass_out,
-                               kv_len_out, freed_out, true)
-                      : launch(evict_kernel<kThreads>, grid, kThreads, smem, st, L, mass, n_keep, n_first, n_last, ids_out,
-                               mass_out, kv_len_out, freed_out, in_smem);
+    const cudaError_t e = for_cap(L.cap, [&](auto threads, auto kpt) {
+        return launch(evict_kernel<threads.value, kpt.value>, dim3(L.Hk, L.S), threads.value, 0, st, L, mass, n_keep, n_first,
+                      n_last, ids_out, mass_out, kv_len_out, freed_out);
+    });
     return cuda_fail(h, e, "eviction launch");
 }
 

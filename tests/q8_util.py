@@ -197,6 +197,7 @@ def evict(ids, mass, lens, n_keep, n_first, n_last):
         for k in range(Hk):
             m = mass[s, k].astype(np.float64)
             m = np.where(np.isnan(m), np.inf, m)
+            m = np.where(ids[s, k] < 0, -np.inf, m)      # absent pages go first, all alike
             rank = sorted(range(n), key=lambda b: (not (b < n_first or b >= n - n_last), ids[s, k, b] < 0, -m[b], b))
             keep = sorted(rank[:n_keep])
             gone = [b for b in range(n) if b not in set(keep) and ids[s, k, b] >= 0]

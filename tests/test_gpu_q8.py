@@ -250,7 +250,8 @@ def test_attention_over_a_selection(h, lens, nq, H, Hk, D, n):
 @pytest.mark.parametrize("lens,nq,H,Hk,D,n,first,last,causal", [
     ([1000], 1, 4, 1, 128, 4, 1, 1, False), ([5000, 64, 0, 1], 1, 8, 2, 64, 16, 0, 0, False),
     ([777, 2500], 3, 10, 2, 128, 7, 2, 2, True), ([300], 20, 4, 4, 64, 3, 1, 2, True),
-    ([4096], 1, 80, 1, 64, 10, 0, 1, False), ([130], 2, 8, 8, 128, 8, 1, 1, True), ([9000], 1, 2, 2, 128, 1, 0, 1, False)])
+    ([4096], 1, 80, 1, 64, 10, 0, 1, False), ([64 * 2000], 1, 2, 1, 64, 300, 1, 1, False), ([64 * 7000 - 3], 1, 1, 1, 64, 77, 0, 1, False),
+    ([64 * 17000], 1, 1, 1, 64, 2000, 1, 2, False), ([130], 2, 8, 8, 128, 8, 1, 1, True), ([9000], 1, 2, 2, 128, 1, 0, 1, False)])
 def test_selection(h, lens, nq, H, Hk, D, n, first, last, causal):
     import split_kv_flash_attn_gb300 as skv
     rng = np.random.default_rng(sum(lens) + n)
@@ -295,7 +296,8 @@ def test_selection_bounds_every_score(h):
 
 @pytest.mark.parametrize("lens,Hk,cap,keep,first,last", [
     ([64 * 20], 1, 25, 5, 1, 1), ([1000, 64, 0, 63, 5000], 2, 90, 8, 2, 3), ([700], 3, 11, 1, 0, 1), ([700], 3, 11, 11, 0, 2),
-    ([64 * 3000 - 5, 64 * 1500], 2, 3000, 700, 1, 4), ([64 * 49000, 64 * 10], 1, 49500, 200, 1, 1)])
+    ([64 * 3000 - 5, 64 * 1500], 2, 3000, 700, 1, 4), ([64 * 49000, 64 * 10], 1, 49500, 200, 1, 1),
+    ([64 * 9000, 64 * 16000 - 1], 1, 16384, 5000, 3, 3), ([64 * 1024], 2, 1024, 1023, 1, 1), ([64 * 6000], 1, 6144, 2, 1, 1)])
 def test_eviction(h, lens, Hk, cap, keep, first, last):
     import split_kv_flash_attn_gb300 as skv
     rng = np.random.default_rng(keep + cap)
