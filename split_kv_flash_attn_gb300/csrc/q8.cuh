@@ -150,6 +150,11 @@ int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pag
 constexpr int kPieceMin = 8;
 int launch_decode(skv_handle *h, const AttnArgs &a, int64_t n_pages, int D, bool out_f16, int grid, int nc,
                   cudaStream_t st);
+// fp32(top / 127).  In 64 bits the product with 1/127 is within 2^-52 of the quotient,
+// and no quotient of an fp32 number by 127 comes nearer than 2^-32 to a number on
+// which fp32 rounding turns (127 m has a bit more than m, so none lies on one).
+__device__ __forceinline__ float over_127(float top) { return __double2float_rn(static_cast<double>(top) * (1.0 / 127.0)); }
+
 int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool out_f16, uint32_t *plan, int n_pairs, float *mass,
                    int grid, cudaStream_t st);
 int launch_mass(skv_handle *h, const AttnArgs &a, float *mass, cudaStream_t st);

@@ -12,8 +12,9 @@
 // A code is rint(t), t = x (1/d') with an approximate reciprocal, when t is further
 // than 2^-13 from every half-integer: t is off by less than 2^-21.4 * 128 = 2^-14.4
 // and |x/d'| never exceeds 127 + 2^-16, so nothing is left to clamp.  Nearer ones (one
-// value in 4000), infinities and NaN are decided by the exact quotient, eight at a
-// time; with that division for every value a 4096-token prompt took 31 us.
+// value in 4000) are decided by the sign of x - h d' at the half-integer h; tiny d',
+// infinities and NaN go by the exact quotient, which for every value took 31 us
+// with a 4096-token prompt.
 //
 // Bound: a token's append is two dependent reads (length, page id) and one
 // write deep, the prompt's by its bytes (x read once, codes written once).
@@ -34,6 +35,13 @@ struct AppendArgs {
     int n_max;
 };
 
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 // Eight values as they come, and as fp32 numbers.
 template <typename X>
 struct Eight {
@@ -48,6 +56,23 @@ struct Eight {
     {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    }
+    // the largest magnitude, or NaN
+    __device__ __forceinline__ float top() const
+    {
+        if constexpr (sizeof(X) == 4) {
+            float v[8];
+            values(v);
+            return max_nan(max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3]))),
+                           max_nan(max_nan(fabsf(v[4]), fabsf(v[5])), max_nan(fabsf(v[6]), fabsf(v[7]))));
+        } else {
+            const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+            __half2 m = __habs2(*reinterpret_cast<const __half2 *>(&w[0]));
+#pragma unroll
+            for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2 *>(&w[i])));
+            const float2 f = __half22float2(m);
+            return max_nan(f.x, f.y);
+        }
     }
     __device__ __forceinline__ void values(float (&v)[8]) const
     {
@@ -75,8 +100,14 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// Four codes through the table.
+__device__ __forceinline__ uint32_t recode4(const int8_t *lut, uint32_t w)
+{
+    return pack4(lut[w & 255u], lut[(w >> 8) & 255u], lut[(w >> 16) & 255u], lut[w >> 24]);
+}
+
 template <int D, typename X>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(kAppendThreads, sizeof(X) == 2 ? 4 : 3) append_kernel(const AppendArgs a)
 {
     constexpr int TPR = D / 8;                       // threads a row
     constexpr int RPP = kAppendThreads / TPR;        // rows a pass
@@ -86,25 +117,30 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
     __shared__ uint32_t s_lo[kAppendThreads / 32][TPR][2], s_hi[kAppendThreads / 32][TPR][2];
     start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int which = blockIdx.x & 1;
-    const int kh = blockIdx.y, s = blockIdx.z;
+    // (heads side by side: their rows of a token are neighbours in memory)
+    const int which = blockIdx.y & 1;
+    const int kh = blockIdx.x, s = blockIdx.z;
     const int64_t len = max(0, __ldg(a.L.kv_len + s));
     const int n = min(a.n_max, a.n_new ? max(0, __ldg(a.n_new + s)) : a.n_max);
     if (n == 0) return;
-    const int64_t blk = len / kPage + (blockIdx.x >> 1);
+    const int64_t blk = len / kPage + (blockIdx.y >> 1);
     const int64_t p0 = blk * kPage;                  // token of the page's row 0
     if (p0 >= len + n) return;
     const int r_lo = static_cast<int>(max(int64_t(0), len - p0));            // first row written
     const int r_hi = static_cast<int>(min(int64_t(kPage), len + n - p0));
     const int c8 = (tid % TPR) * 8, r0 = tid / TPR;
-    const X *x = static_cast<const X *>(a.x[which]);
+    // (not by index: that would copy the arguments to local memory)
+    const X *x = static_cast<const X *>(which ? a.x[1] : a.x[0]);
+    int8_t *const codes = which ? a.codes[1] : a.codes[0];
+    float *const scale = which ? a.scale[1] : a.scale[0];
+    auto at_of = [&](int r) { return ((static_cast<int64_t>(s) * a.n_max + (p0 + r - len)) * a.L.Hk + kh) * D + c8; };
     // the values and the page's id are on their way together
     Eight<X> in[PASSES];
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = r0 + i * RPP;
         if (r >= r_lo && r < r_hi)
-            in[i].load(x + ((static_cast<int64_t>(s) * a.n_max + (p0 + r - len)) * a.L.Hk + kh) * D + c8);
+            in[i].load(x + at_of(r));
         else
             in[i].clear();
     }
@@ -114,56 +150,98 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
         if (tid == 0) atomicOr(a.L.status, kStatusAppend);
         return;
     }
-    const float d0 = r_lo > 0 ? a.scale[which][id] : 0.f;
+    const float d0 = r_lo > 0 ? scale[id] : 0.f;
+    // the largest magnitude; NaN where there is one
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        float v[8];
-        in[i].values(v);
+    for (int i = 0; i < PASSES; ++i) amax = max_nan(amax, in[i].top());
+    const bool odd = !(amax <= 3.402823466e38f);                            // a NaN or an infinity among the values
+    if (odd) {                                                              // finite values only
+        amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float m = fabsf(v[e]);
-            amax = fmaxf(amax, m <= 3.402823466e38f ? m : 0.f);             // finite values only
+        for (int i = 0; i < PASSES; ++i) {
+            float v[8];
+            in[i].values(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]) <= 3.402823466e38f ? fabsf(v[e]) : 0.f);
         }
     }
     // (magnitudes: their order is that of their bits)
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
     if (lane == 0) s_max[warp] = amax;
-    __syncthreads();
+    const bool any_odd = __syncthreads_or(odd);
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
-    const float d1 = fmaxf(d0, __fdiv_rn(amax, 127.f));
+    const float d1 = fmaxf(d0, over_127(amax));
     const bool recode = r_lo > 0 && d1 != d0;
-    int8_t *page = a.codes[which] + id * (kPage * D);
+    const bool plain = !any_odd && d1 >= 0x1p-100f;                         // every value finite, d' not tiny
+    int8_t *page = codes + id * (kPage * D);
     const float up = d1 < 0x1p-100f ? 0x1p40f : 1.f;                        // see nearest_code
-    float rd;                                                               // 1 / (d' up), off by 2^-22 at most
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d1 * up));
-    uint32_t lo[2] = {0x7f7f7f7fu, 0x7f7f7f7fu}, hi[2] = {0x81818181u, 0x81818181u};
+    float rd;                                                               // 1 / d', off by 2^-22 at most
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d1));
+    float lo[8], hi[8];                                                     // of the thread's channels
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo[e] = 127.f;
+        hi[e] = -127.f;
+    }
+    if (plain) {
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = r0 + i * RPP;
         if (r < r_lo || r >= r_hi) continue;
-        float v[8];
+        // t + 1.5 2^23 rounds t to an integer, whose low byte is the sum's
+        constexpr float kMagic = 12582912.f;
+        float v[8], c[8];
+        uint32_t q[8];
         in[i].values(v);
-        int q[8];
-        bool sure = d1 > 0.f;
+        float off = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float t = v[e] * up * rd;
-            const float r = rintf(t);
-            sure = sure && fabsf(t - r) < 0.5f - 0x1p-13f;               // (false for what is not finite)
-            q[e] = static_cast<int>(r);
+            const float t = v[e] * rd;
+            const float m = t + kMagic;
+            q[e] = __float_as_uint(m);
+            c[e] = m - kMagic;
+            off = fmaxf(off, fabsf(t - c[e]));
         }
-        if (!sure) {
+        if (!(off < 0.5f - 0x1p-13f)) {
+            // next to a half-integer h, the sign of x - h d' decides (one rounding,
+            // so the sign is exact; d' is not tiny)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = d1 > 0.f ? nearest_code(v[e] * up, d1 * up) : 0;
+            for (int e = 0; e < 8; ++e) {
+                const float side = v[e] * rd - c[e];
+                const float rem = __fmaf_rn(-(c[e] + copysignf(0.5f, side)), d1, v[e]) * copysignf(1.f, side);
+                if (rem > 0.f || (rem == 0.f && fabsf(side) > 0.25f && (q[e] & 1u))) {
+                    c[e] += copysignf(1.f, side);
+                    q[e] = __float_as_uint(c[e] + kMagic);
+                }
+            }
         }
-        const uint32_t w0 = pack4(q[0], q[1], q[2], q[3]), w1 = pack4(q[4], q[5], q[6], q[7]);
-        *reinterpret_cast<uint2 *>(page + r * D + c8) = make_uint2(w0, w1);
-        lo[0] = __vmins4(lo[0], w0);
-        lo[1] = __vmins4(lo[1], w1);
-        hi[0] = __vmaxs4(hi[0], w0);
-        hi[1] = __vmaxs4(hi[1], w1);
+        *reinterpret_cast<uint2 *>(page + r * D + c8) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+        if (which == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                lo[e] = fminf(lo[e], c[e]);
+                hi[e] = fmaxf(hi[e], c[e]);
+            }
+        }
+    }
+    } else {
+        // the values once more, one by one
+        for (int r = r0; r < r_hi; r += RPP) {
+            if (r < r_lo) continue;
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                const float v = static_cast<float>(x[at_of(r) + e]);
+                const int q = d1 > 0.f ? nearest_code(v * up, d1 * up) : 0;
+                page[r * D + c8 + e] = static_cast<int8_t>(q);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    lo[k] = e == k ? fminf(lo[k], static_cast<float>(q)) : lo[k];
+                    hi[k] = e == k ? fmaxf(hi[k], static_cast<float>(q)) : hi[k];
+                }
+            }
+        }
     }
     if (recode) {
         const int c = static_cast<int8_t>(tid);
@@ -171,28 +249,31 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
         s_lut[tid] = static_cast<int8_t>(fmin(fmax(t, -127.0), 127.0));
         __syncthreads();
         for (int i = tid; i < r_lo * TPR; i += kAppendThreads) {
-            uint2 w = *reinterpret_cast<const uint2 *>(page + i * 8);
-            uint8_t *b = reinterpret_cast<uint8_t *>(&w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = static_cast<uint8_t>(s_lut[b[e]]);
-            *reinterpret_cast<uint2 *>(page + i * 8) = w;
+            const uint2 w = *reinterpret_cast<const uint2 *>(page + i * 8);
+            *reinterpret_cast<uint2 *>(page + i * 8) = make_uint2(recode4(s_lut, w.x), recode4(s_lut, w.y));
         }
     }
-    if (tid == 0) a.scale[which][id] = d1;
+    if (tid == 0) scale[id] = d1;
     if (which != 0) return;
     // the channels' extremes: over a thread's rows, the warp's, then the CTA's
+    uint32_t lo4[2], hi4[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        lo4[e] = pack4(static_cast<int>(lo[4 * e]), static_cast<int>(lo[4 * e + 1]), static_cast<int>(lo[4 * e + 2]), static_cast<int>(lo[4 * e + 3]));
+        hi4[e] = pack4(static_cast<int>(hi[4 * e]), static_cast<int>(hi[4 * e + 1]), static_cast<int>(hi[4 * e + 2]), static_cast<int>(hi[4 * e + 3]));
+    }
 #pragma unroll
     for (int o = TPR; o < 32; o <<= 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            lo[e] = __vmins4(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
-            hi[e] = __vmaxs4(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+            lo4[e] = __vmins4(lo4[e], __shfl_xor_sync(0xffffffffu, lo4[e], o));
+            hi4[e] = __vmaxs4(hi4[e], __shfl_xor_sync(0xffffffffu, hi4[e], o));
         }
     if (lane < TPR) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            s_lo[warp][lane][e] = lo[e];
-            s_hi[warp][lane][e] = hi[e];
+            s_lo[warp][lane][e] = lo4[e];
+            s_hi[warp][lane][e] = hi4[e];
         }
     }
     __syncthreads();
@@ -209,12 +290,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
         if (r_lo > 0) {
             uint32_t ol = *pl, om = *pm;
             if (recode) {
-                uint8_t *bl = reinterpret_cast<uint8_t *>(&ol), *bm = reinterpret_cast<uint8_t *>(&om);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bl[i] = static_cast<uint8_t>(s_lut[bl[i]]);
-                    bm[i] = static_cast<uint8_t>(s_lut[bm[i]]);
-                }
+                ol = recode4(s_lut, ol);
+                om = recode4(s_lut, om);
             }
             l = __vmins4(l, ol);
             m = __vmaxs4(m, om);
@@ -241,7 +318,7 @@ int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_
     a.n_max = n_max;
     // a run of n tokens touches at most ceil((n + 63) / 64) pages
     const int64_t blocks = (static_cast<int64_t>(n_max) + 2 * kPage - 2) / kPage;
-    const dim3 grid(static_cast<unsigned>(2 * blocks), L.Hk, L.S);
+    const dim3 grid(L.Hk, static_cast<unsigned>(2 * blocks), L.S);
     cudaError_t e;
     if (x_type == SKV_F32)
         e = pool.D == 128 ? launch(append_kernel<128, float>, grid, kAppendThreads, 0, st, a)

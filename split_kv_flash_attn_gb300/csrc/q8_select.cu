@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                 }
                 // (magnitudes: their order is that of their bits)
                 top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-                const float dq = __fdiv_rn(top, 127.f);
+                const float dq = over_127(top);
                 if (lane == 0) s_dq[c] = dq;
                 // the integer nearest v / dq: by the approximate reciprocal unless that
                 // comes within 2^-13 of a half-integer (its error is below 2^-14)
