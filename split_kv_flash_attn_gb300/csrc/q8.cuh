@@ -147,7 +147,7 @@ __device__ __forceinline__ int nearest_code(float x, float d)
 int page_map(skv_handle *h, CUtensorMap *map, const int8_t *pages, int64_t n_pages, int D, int rows);
 // Fewest pages of a CTA's piece in the decode kernel: with fewer, putting the
 // pieces together costs more than it gains.
-constexpr int kPieceMin = 8;
+constexpr int kPieceMin = 4;
 int launch_decode(skv_handle *h, const AttnArgs &a, int64_t n_pages, int D, bool out_f16, int grid, int nc,
                   cudaStream_t st);
 // fp32(top / 127).  In 64 bits the product with 1/127 is within 2^-52 of the quotient,

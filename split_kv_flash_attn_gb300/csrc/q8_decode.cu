@@ -47,6 +47,7 @@ namespace q8 {
 constexpr float kShift = 10.f;      // weights are kept times 2^10 ...
 constexpr float kGrow = 4.f;        // ... and their reference moves when a score passes it by 2^4
 constexpr int kStep = 32;           // keys a warp takes at a time
+constexpr uint32_t kStraddle = 8;   // pages that a second start and join of a CTA cost
 
 // Computing warps and ring slots.  One column group: 8 sequences x 32768 keys take
 // 64 us with 11 and 11, 65 with 7 and 7 or 8 and 8, 70 with 6 and 12; two groups
@@ -65,7 +66,7 @@ static_assert(decode_smem<128, 1>() < 226 * 1024 && decode_smem<128, 2>() < 226 
 // A list on the line of pages.
 struct Place {
     int list;                       // sequence, or sequence x token with a selection
-    uint32_t np;                    // its pages
+    uint32_t np;                    // its pages, rounded up to whole pieces where units are
     uint32_t base;                  // the line's position of its first page
 };
 
@@ -137,8 +138,35 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
         if (blockIdx.x == 0 && tid == 0) atomicOr(a.L.status, kStatusList);
         sum = 0;
     }
-    const uint32_t total = static_cast<uint32_t>(sum);
-    const uint32_t chunk = max(static_cast<uint32_t>(kPieceMin), (total + gridDim.x - 1) / gridDim.x);
+    uint32_t total = static_cast<uint32_t>(sum);
+    const uint32_t even = max(static_cast<uint32_t>(kPieceMin), (total + gridDim.x - 1) / gridDim.x);
+    // Pieces that end with their units spare the CTAs a second start and join: taken
+    // when the least piece with which the grid covers units one by one is at most
+    // kStraddle pages longer than even shares (8 lists of 256 pages on 152 CTAs: 15
+    // against 18 us).  The line then holds every unit rounded up to whole pieces.
+    uint32_t chunk = even;
+    bool whole_pieces = false;
+    if (n_lists <= 32 || a.sel) {
+        auto count = [&](uint32_t c) -> uint32_t {        // pieces of c pages
+            if (a.sel) return static_cast<uint32_t>(min(static_cast<uint64_t>(n_lists) * mult * ((a.n_sel + c - 1) / c), uint64_t(0x7fffffff)));
+            return __reduce_add_sync(0xffffffffu, (np_lane + c - 1) / c) * mult;
+        };
+        uint32_t n = count(even);
+        if (n > gridDim.x && count(even + kStraddle) <= gridDim.x) {
+            uint32_t lo = even + 1, hi = even + kStraddle;
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (count(mid) <= gridDim.x) hi = mid;
+                else lo = mid + 1;
+            }
+            chunk = hi;
+            n = count(chunk);
+        }
+        whole_pieces = n <= gridDim.x;
+        if (whole_pieces) total = n * chunk;
+    }
+    // a list's units on the line
+    auto padded = [&](uint32_t np) { return whole_pieces ? (np + chunk - 1) / chunk * chunk : np; };
     const uint32_t pos0 = blockIdx.x * chunk, pos_end = min(total, pos0 + chunk);
 
     // lists without a page: their rows are written here
@@ -158,13 +186,13 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
 
     Place at = {0, 0, 0};
     if (a.sel) {
-        at.np = a.n_sel;
+        at.np = padded(a.n_sel);
         at.list = static_cast<int>(pos0 / (at.np * mult));
         at.base = at.list * (at.np * mult);
     } else {
         uint32_t before = 0;
         for (int c0 = 0; c0 < n_lists; c0 += 32) {
-            const uint32_t n = c0 == 0 ? np_lane : c0 + lane < n_lists ? pages_of(a, c0 + lane) : 0u;
+            const uint32_t n = padded(c0 == 0 ? np_lane : c0 + lane < n_lists ? pages_of(a, c0 + lane) : 0u);
             uint32_t inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -186,20 +214,24 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     // The units of the piece in turn, for both roles: pages [pg0, pg1) of one unit.
     struct Unit {
         uint32_t u_in, unit0;                       // its number within the list; the line's position of its page 0
-        int pg0, pg1, kh, rg, seq;
+        uint32_t next;                              // the line's position behind what of it is in the piece
+        int np, pg0, pg1, kh, rg, seq;              // np: its pages
         int64_t tok0;                               // token of its row 0
     };
     auto unit_at = [&](uint32_t pos) {
         while (pos >= at.base + at.np * mult) {     // the next list with pages
             at.base += at.np * mult;
             ++at.list;
-            at.np = pages_of(a, at.list);
+            at.np = padded(pages_of(a, at.list));
         }
         Unit x;
         x.u_in = (pos - at.base) / at.np;
         x.unit0 = at.base + x.u_in * at.np;
         x.pg0 = static_cast<int>(pos - x.unit0);
-        x.pg1 = static_cast<int>(min(at.np, pos_end - x.unit0));
+        const uint32_t to = min(at.np, pos_end - x.unit0);
+        x.next = x.unit0 + to;
+        x.np = static_cast<int>(pages_of(a, at.list));
+        x.pg1 = min(static_cast<int>(to), x.np);
         x.kh = static_cast<int>(x.u_in / a.row_groups);
         x.rg = static_cast<int>(x.u_in - x.kh * a.row_groups);
         x.seq = a.sel ? at.list / a.nq : at.list;
@@ -284,7 +316,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 n_put += n;
                 ok = __all_sync(0xffffffffu, ok);
             }
-            pos = x.unit0 + x.pg1;
+            pos = x.next;
         }
         if (!ok && lane == 0) {
             // copies in flight land before the CTA ends (bounded)
@@ -563,7 +595,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
             }
         };
         // ---- the warps' results together, eight columns at a time ---------------
-        const bool whole = x.pg0 == 0 && x.pg1 == static_cast<int>(at.np);
+        const bool whole = x.pg0 == 0 && x.pg1 == x.np;
         const int64_t slot_out = 2 * static_cast<int64_t>(blockIdx.x) + (pos == pos0 ? 0 : 1);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
@@ -647,7 +679,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 if (tid == 0) a.counters[u] = 0;
             }
         }
-        pos = x.unit0 + x.pg1;
+        pos = x.next;
     }
 }
 
