@@ -47,8 +47,8 @@ constexpr int kMmaWarp = kSoftWarps + kProdWarps;   // S; the next warp O; two m
 constexpr int kPfThreads = (kMmaWarp + 4) * 32;
 // Registers of a thread by role: 16 warps launch with 128 each, the softmax groups
 // take what the others can spare (spilled, they would go to an L1 of 20 KB:
-// 396 us against PFTIME at 512 tokens over 32768 keys).
-constexpr int kRegSoft = 176, kRegProd = 104, kRegMma = 56;
+// such loads had been most of the waiting).
+constexpr int kRegSoft = 176, kRegProd = 112, kRegMma = 48;
 static_assert(2 * kRegSoft + kRegProd + kRegMma <= 4 * 128, "no more than the launch has");
 static_assert(kRegSoft >= 128 && kRegProd <= 128 && kRegMma <= 128, "the first is an increase, the others decreases");
 template <int N>
@@ -66,6 +66,13 @@ constexpr int kPlanHere = 256;                  // plan entries that the prefill
 constexpr int kPlanSmem = 1024;                 // plan entries kept in shared memory
 constexpr float kPfShift = 8.f, kPfGrow = 5.f, kPfScaleGrow = 2.f;
 constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a wait gives up (tens of ms at least)
+// The tensor core rounds its sums toward zero.  A tile's 16 additions (both parts of
+// the weights) shrink O by 2.4e-7 on average and blur it by 1.4e-7, in
+// proportion to the tiles (measured against 64 bits for 3 to 128 tiles): fp32
+// results take at most kExactTiles at a time, put together in fp32, and the
+// average loss is given back.
+constexpr int kExactTiles = 8;
+constexpr float kLoss = 2.4e-7f;
 constexpr float kNoScale = -100.f;              // log2 d_v - r of a zero scale (fp16 0, while l stays right)
 
 template <int D>
@@ -169,17 +176,24 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, in
 struct Unit {
     int s, kh, pr;
     uint32_t unit0;                             // the line's position of its tile 0
-    int t0, t1, n;                              // its tiles [t0, t1) are this CTA's, of n
+    int n;                                      // its tiles
+    int p0, p1;                                 // [p0, p1) of them are this CTA's part
+    int t0, t1, sub;                            // [t0, t1) of the part are at hand, sub tiles at a time
 };
 struct Walk {
     const uint32_t *plan;                       // shared or global memory
     int np, S, Hk;
+    int most;                                   // tiles at a time
     uint32_t end;                               // of the piece
 
     __device__ void cut(Unit &x, uint32_t pos) const
     {
-        x.t0 = static_cast<int>(pos - x.unit0);
-        x.t1 = static_cast<int>(min(static_cast<uint32_t>(x.n), end - x.unit0));
+        x.p0 = static_cast<int>(pos - x.unit0);
+        x.p1 = static_cast<int>(min(static_cast<uint32_t>(x.n), end - x.unit0));
+        const int len = x.p1 - x.p0, k = (len + most - 1) / most;
+        x.sub = (len + k - 1) / k;
+        x.t0 = x.p0;
+        x.t1 = x.p0 + x.sub;
     }
     __device__ int tiles(const Unit &x) const
     {
@@ -214,7 +228,12 @@ struct Walk {
     }
     __device__ bool next(Unit &x) const         // false at the end of the piece
     {
-        const uint32_t pos = x.unit0 + x.t1;
+        if (x.t1 < x.p1) {                      // the part goes on
+            x.t0 = x.t1;
+            x.t1 = min(x.p1, x.t0 + x.sub);
+            return true;
+        }
+        const uint32_t pos = x.unit0 + x.p1;
         if (pos >= end) return false;
         do {
             if (++x.pr == np) {
@@ -281,7 +300,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     start();
     const int np = pa.n_pairs;
     const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
-    Walk walk{pa.plan, np, a.L.S, a.L.Hk, 0};
+    Walk walk{pa.plan, np, a.L.S, a.L.Hk, HILO ? kExactTiles : INT32_MAX / 2, 0};
     uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
     if (n_entries <= kPlanHere) {               // few entries: every CTA counts them itself
         for (int e = warp; e < n_entries; e += kPfThreads / 32) {
@@ -442,7 +461,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             Unit x = walk.first(pos0);
             do {
                 const bool two = two_tiles(x);
-                ok = all(wait(PB_QFULL, units0++ & 1)) && (!two || all(wait(PB_QFULL + 1, units1++ & 1)));
+                // (a part that goes on keeps its queries)
+                if (x.t0 == x.p0) ok = all(wait(PB_QFULL, units0++ & 1)) && (!two || all(wait(PB_QFULL + 1, units1++ & 1)));
 #pragma unroll 1
                 for (int tl = x.t0; ok && tl < x.t1; ++tl, ++j) {
                     const int b = static_cast<int>(j & 1);
@@ -577,8 +597,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
         bool more = any;
 #pragma unroll 1
         for (int u = 0; more; u ^= 1) {
-            meet();
             const Unit &x = s_unit[warp][u];
+            meet();
             const bool tile_on = active(x);
             const int n = x.t1 - x.t0;
             float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
@@ -716,19 +736,36 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                     s_unit[warp][u ^ 1] = y;
                 }
                 more = __shfl_sync(0xffffffffu, again, 0) != 0;
-                if (more && active(s_unit[warp][u ^ 1])) put_q(row_index(s_unit[warp][u ^ 1]));
+                __syncwarp();
+                const Unit &y = s_unit[warp][u ^ 1];
+                if (more && y.t0 == y.p0 && active(y)) put_q(row_index(y));
             }
             if (!tile_on) continue;
             const int64_t out = row_index(x);
-            const bool whole = n == x.n;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x.unit0 + x.t0 == pos0 ? 0 : 1);
+            const bool whole = x.p0 == 0 && x.p1 == x.n && x.t1 == x.p1;      // the result, not a piece
+            const bool joins = x.t0 > x.p0;                                   // an earlier stretch of the part is in the slot
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x.unit0 + x.p0 == pos0 ? 0 : 1);
             // ---------------- O / l, lse: result or piece ------------------------------
             bool have = wait(PB_PDONE + g, (tiles - 1) & 1) && !*reinterpret_cast<volatile int *>(&s_abort);
             have = __all_sync(0xffffffffu, have);
             if (have) tc::tc_fence_after();
             const bool empty = !have || !(l_run > 0.f);
-            const float inv = empty ? 0.f : fast_exp2(r_ref == -INFINITY ? 0.f : r_ref) / l_run;
-            const float lse2 = empty ? -INFINITY : m_ref - kPfShift + log2f(l_run);
+            float inv = empty ? 0.f : fast_exp2(r_ref == -INFINITY ? 0.f : r_ref) / l_run;
+            float lse2 = empty ? -INFINITY : m_ref - kPfShift + log2f(l_run);
+            float *const ml = a.part_ml + (slot * 2 + g) * kPM + m;
+            float w_old = 0.f;                  // weight of the stretches before
+            if (HILO) {
+                inv *= 1.f + kLoss * n;
+                if (joins && out >= 0) {
+                    const float z = __ldcg(ml), top = fmaxf(z, lse2);
+                    if (top != -INFINITY) {
+                        const float e_old = fast_exp2(z - top), e_new = fast_exp2(lse2 - top);
+                        w_old = e_old / (e_old + e_new);
+                        inv *= e_new / (e_old + e_new);
+                        lse2 = top + log2f(e_old + e_new);
+                    }
+                }
+            }
             // 16 columns of the warp's rows through shared memory, so that four lanes
             // write 64 (fp16: 32) bytes of a row
             float *stage = reinterpret_cast<float *>(sm + SM::kStage) + warp * 32 * SM::kStageLd;
@@ -750,9 +787,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rl = i * 8 + (lane >> 2), col = c * 16 + (lane & 3) * 4;
-                    const float4 v = *reinterpret_cast<const float4 *>(stage + rl * SM::kStageLd + (lane & 3) * 4);
+                    float4 v = *reinterpret_cast<const float4 *>(stage + rl * SM::kStageLd + (lane & 3) * 4);
                     const int64_t r = __shfl_sync(0xffffffffu, out, rl);
+                    const float w = HILO ? __shfl_sync(0xffffffffu, w_old, rl) : 0.f;
                     if (r < 0) continue;
+                    if (HILO && joins) {        // (the same thread wrote it)
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((slot * 2 + g) * kPM + (warp & 3) * 32 + rl) * D + col));
+                        v.x = fmaf(w, y.x, v.x);
+                        v.y = fmaf(w, y.y, v.y);
+                        v.z = fmaf(w, y.z, v.z);
+                        v.w = fmaf(w, y.w, v.w);
+                    }
                     if (!whole)
                         *reinterpret_cast<float4 *>(a.part_o + ((slot * 2 + g) * kPM + (warp & 3) * 32 + rl) * D + col) = v;
                     else if (pa.out_f16)
@@ -765,7 +810,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             }
             if (out >= 0) {
                 if (whole) a.lse[out] = lse2 * 0.6931471805599453f;
-                else a.part_ml[(slot * 2 + g) * kPM + m] = lse2;
+                else *ml = lse2;
             }
             tc::tc_fence_before();              // O_g is read before W_g of the next unit is announced
         }

@@ -135,6 +135,8 @@ PREFILL = [
     ([700, 20], 33, 16, 1, 128, False), ([2000], 70, 40, 8, 64, True), ([5000, 129], 64, 8, 4, 128, True),
     ([40], 100, 6, 2, 128, True), ([260] * 9, 72, 4, 1, 64, False), ([70, 0, 131] * 100, 34, 1, 1, 64, True),
     ([65] * 1100, 33, 1, 1, 64, False),
+    # units of more tiles than fp32 results take at a time, one or less of them a CTA
+    ([1300, 2500] + [1300] * 38, 33, 4, 4, 64, True), ([1400] * 20, 33, 8, 8, 128, False),
 ]
 
 
