@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     // against 18 us).  The line then holds every unit rounded up to whole pieces.
     uint32_t chunk = even;
     bool whole_pieces = false;
-    if (n_lists <= 32 || a.sel) {
+    if (sum != 0 && (n_lists <= 32 || a.sel)) {
         auto count = [&](uint32_t c) -> uint32_t {        // pieces of c pages
             if (a.sel) return static_cast<uint32_t>(min(static_cast<uint64_t>(n_lists) * mult * ((a.n_sel + c - 1) / c), uint64_t(0x7fffffff)));
             return __reduce_add_sync(0xffffffffu, (np_lane + c - 1) / c) * mult;
@@ -581,10 +581,10 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 }
                 if (final) {
                     const int64_t r = out_row(row);
-                    const float v = Lw > 0.f ? O / Lw : 0.f;
+                    const float v = Lw == 0.f ? 0.f : O / Lw;
                     if (F16) static_cast<__half *>(a.o)[r * D + d] = __float2half_rn(v);
                     else static_cast<float *>(a.o)[r * D + d] = v;
-                    if (d == 0) a.lse[r] = Lw > 0.f ? (M - kShift + log2f(Lw)) * 0.6931471805599453f : -INFINITY;
+                    if (d == 0) a.lse[r] = Lw == 0.f ? -INFINITY : (M - kShift + log2f(Lw)) * 0.6931471805599453f;
                 } else {
                     a.part_o[(slot * (8 * NC) + j * 8 + c) * D + d] = O;
                     if (d == 0) {
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
                 if (g == 0) {
-                    s_ml[warp][2 * t + e][0] = m_ref[j][e];
+                    s_ml[warp][2 * t + e][0] = y == y ? m_ref[j][e] : INFINITY;   // (a NaN stays one in every sum)
                     s_ml[warp][2 * t + e][1] = y;
                 }
 #pragma unroll
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnArgs a, float *mass
                 const float2 x = __ldcg(reinterpret_cast<const float2 *>(pl + (t * a.G + g) * a.page_ld) + i);
                 sum += z == -INFINITY ? 0.f : fast_exp2(x.x - z) + fast_exp2(x.y - z);
             }
-            if (sum > 0.f) atomicAdd(out + blk, sum);
+            if (sum != 0.f) atomicAdd(out + blk, sum);
         }
         __syncthreads();
     }

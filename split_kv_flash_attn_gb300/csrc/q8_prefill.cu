@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             bool have = wait(PB_PDONE + g, (tiles - 1) & 1) && !*reinterpret_cast<volatile int *>(&s_abort);
             have = __all_sync(0xffffffffu, have);
             if (have) tc::tc_fence_after();
-            const bool empty = !have || !(l_run > 0.f);
+            const bool empty = !have || l_run == 0.f;
             float inv = empty ? 0.f : fast_exp2(r_ref == -INFINITY ? 0.f : r_ref) / l_run;
             float lse2 = empty ? -INFINITY : m_ref - kPfShift + log2f(l_run);
             float *const ml = a.part_ml + (slot * 2 + g) * kPM + m;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                 inv *= 1.f + kLoss * n;
                 if (joins && out >= 0) {
                     const float z = __ldcg(ml), top = fmaxf(z, lse2);
-                    if (top != -INFINITY) {
+                    if (z != -INFINITY || lse2 != -INFINITY) {
                         const float e_old = fast_exp2(z - top), e_new = fast_exp2(lse2 - top);
                         w_old = e_old / (e_old + e_new);
                         inv *= e_new / (e_old + e_new);
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa
     for (int i = 0; i < kMergeRows; ++i) {
         const int row = pr * 2 * kPM + rr[i];
         if (row >= a.rows || rr[i] >= 2 * kPM) continue;
-        const float q = W[i] > 0.f ? 1.f / W[i] : 0.f;
+        const float q = W[i] == 0.f ? 0.f : 1.f / W[i];
         const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
         if (pa.out_f16)
             *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + lane * 4) =
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa
         else
             *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + lane * 4) =
                 make_float4(v[i][0] * q, v[i][1] * q, v[i][2] * q, v[i][3] * q);
-        if (lane == 0) a.lse[r] = W[i] > 0.f ? (M[i] + log2f(W[i])) * 0.6931471805599453f : -INFINITY;
+        if (lane == 0) a.lse[r] = W[i] == 0.f ? -INFINITY : (M[i] + log2f(W[i])) * 0.6931471805599453f;
     }
 }
 

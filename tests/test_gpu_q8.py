@@ -247,6 +247,45 @@ def test_attention_over_a_selection(h, lens, nq, H, Hk, D, n):
     assert h.status() == 0
 
 
+@pytest.mark.parametrize("nq,lens", [(1, [700, 0, 40]), (3, [3000, 64, 65]), (70, [700, 5, 130]), (70, [1300] * 40)])
+@pytest.mark.parametrize("f16", [False, True])
+def test_a_query_with_nan_gives_nan_in_its_own_row(h, nq, lens, f16):
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(nq)
+    c = u.Cache(rng, lens, 2, 128)
+    pool, ids, kv_len = c.on_gpu()
+    q = _dev(_q(rng, len(lens), nq, 8, 128))
+    pos = _dev(_causal(c, nq)) if nq > 1 else None
+    o_type = torch.float16 if f16 else None
+    o, lse = skv.q8_attn(h, pool, q, ids, kv_len, q_pos=pos, o_dtype=o_type)
+    q[0, nq // 2, 5, 17] = float("nan")
+    q[2, nq - 1, 0, 3] = float("nan")
+    oo, ll = skv.q8_attn(h, pool, q, ids, kv_len, q_pos=pos, o_dtype=o_type)
+    bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    bad[0, nq // 2, 5] = bad[2, nq - 1, 0] = True
+    assert ll[bad].isnan().all() and oo[bad].isnan().all()
+    assert torch.equal(ll[~bad], lse[~bad]) and torch.equal(oo[~bad], o[~bad])
+    assert h.status() == 0
+
+
+def test_fp32_results_over_long_lists(h):
+    """Values of one sign, where every truncated addition loses the same way: 2^-18 of
+    the largest value (u.check's bound where scores are small) over 128 tiles."""
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(62)
+    c = u.Cache(rng, [16384] * 5, 8, 64)
+    c.v = rng.integers(64, 128, c.v.shape).astype(np.int8)
+    c.ks[:] = 1e-4
+    c.vs[:] = 0.01
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 5, 33, 8, 64)
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len)
+    ref = list(u.attention(c, q))
+    u.check(o, lse, ref)
+    assert h.status() == 0
+
+
 # --------------------------------------------------------------- the selection
 
 @pytest.mark.parametrize("lens,nq,H,Hk,D,n,first,last,causal", [
