@@ -464,7 +464,8 @@ int skv_bcache_pool(const skv_bcache *c, const void **k_pages, const void **v_pa
  * beyond the list is cut to it and sets the same bit; a negative one is 0.  Entries
  * behind a sequence's last token are not read by attention and selection.
  * One page may stand in several lists as long as no append writes it.
- * A token the page does not hold yet may keep any bytes.
+ * A token the page does not hold yet may keep any bytes.  Scales are finite
+ * numbers of either sign.
  *
  * The calls below take their sizes from skv_shape (S, nq, H, Hk, D, scale);
  * its k_type, v_type and row strides are not looked at.  D is 64 or 128.  They

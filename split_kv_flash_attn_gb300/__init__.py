@@ -21,6 +21,7 @@ streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -423,6 +424,17 @@ def _q8_stream(h, stream, device):
     return _stream(stream)
 
 
+def _on_stream(stream, device):
+    """Context in which a call's results are allocated: they belong to the stream
+    it runs on, so that memory freed on another one is not written early."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 _raw_stream_fn = None
 
 
@@ -486,7 +498,8 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, scale)
     st = _q8_stream(h, stream, dev)
     if o is None:
-        o = torch.empty_like(q, dtype=torch.float32 if o_dtype is None else o_dtype)
+        with _on_stream(stream, dev):
+            o = torch.empty_like(q, dtype=torch.float32 if o_dtype is None else o_dtype)
     else:
         _need("o", o, o.dtype, q.shape, dev)
     if o.dtype is torch.float32:
@@ -498,7 +511,8 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     if o_dtype is not None and o.dtype is not o_dtype:
         raise SplitKVError(1, f"o is {o.dtype}, o_dtype {o_dtype}")
     if lse is None:
-        lse = torch.empty((S, nq, H), dtype=torch.float32, device=q.device)
+        with _on_stream(stream, dev):
+            lse = torch.empty((S, nq, H), dtype=torch.float32, device=q.device)
     else:
         _need("lse", lse, torch.float32, (S, nq, H), dev)
     n_sel, sel_ptr, mass_ptr = 0, None, None
@@ -527,7 +541,8 @@ def q8_select(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, n_sel, n_first=1,
     st = _q8_stream(h, stream, pool.device)
     n_sel = int(n_sel)
     if sel is None:
-        sel = torch.empty((S, nq, Hk, max(0, n_sel)), dtype=torch.int32, device=q.device)
+        with _on_stream(stream, pool.device):
+            sel = torch.empty((S, nq, Hk, max(0, n_sel)), dtype=torch.int32, device=q.device)
     else:
         _need("sel", sel, torch.int32, (S, nq, Hk, n_sel), pool.device)
     h.check(_lib.lib().skv_q8_select(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
@@ -544,8 +559,9 @@ def q8_evict(h: Handle, page_ids, mass, kv_len, *, n_keep, n_first=1, n_last=1, 
     S, Hk, cap = _q8_lists(page_ids, kv_len, dev)
     st = _q8_stream(h, stream, dev)
     _need("mass", mass, torch.float32, (S, Hk, cap), dev)
-    ids_out, freed = torch.empty_like(page_ids), torch.empty_like(page_ids)
-    mass_out, len_out = torch.empty_like(mass), torch.empty_like(kv_len)
+    with _on_stream(stream, dev):
+        ids_out, freed = torch.empty_like(page_ids), torch.empty_like(page_ids)
+        mass_out, len_out = torch.empty_like(mass), torch.empty_like(kv_len)
     h.check(_lib.lib().skv_q8_evict(h.ptr, S, Hk, cap, page_ids.data_ptr(), mass.data_ptr(), kv_len.data_ptr(),
                                     int(n_keep), int(n_first), int(n_last), ids_out.data_ptr(), mass_out.data_ptr(),
                                     len_out.data_ptr(), freed.data_ptr(), st))

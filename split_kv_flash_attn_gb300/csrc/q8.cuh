@@ -166,10 +166,13 @@ struct SelectArgs {
     const float *k_scale;
     const __half *q;
     const int32_t *q_pos;
-    int nq, H, G;
+    int nq, H, G;                  // nq: tokens of this launch
+    int nq_ld, tok0;               // as in AttnArgs
     int n_sel, n_first, n_last;
     uint32_t *keys;                // scratch [S][nq][Hk][cap]
     int32_t *sel;
+
+    __host__ __device__ int64_t token(int s, int t) const { return static_cast<int64_t>(s) * nq_ld + tok0 + t; }
 };
 int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st);
 int launch_evict(skv_handle *h, const Lists &L, const float *mass, int n_keep, int n_first, int n_last,

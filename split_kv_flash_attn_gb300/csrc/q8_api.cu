@@ -1,6 +1,7 @@
 // q8_api.cu -- host side of the calls over 8-bit pages: checks, scratch and the
 // choice of kernel.
 #include <algorithm>
+#include <cmath>
 
 #include "q8.cuh"
 
@@ -28,8 +29,9 @@ struct OnDevice {
 // 67.9 us at 32 rows and 92.8 / 68 at 48.  Over short contexts decode stays ahead
 // for longer (2000 keys of one sequence: 18.6 / 26.4 us at 96 rows), but by less.
 constexpr int kTcRows = 33;
-// Scratch for the pages' log sums of one launch.
-constexpr int64_t kMassScratch = int64_t(256) << 20;
+// Scratch for the pages' log sums or the selection's keys of one launch (one token's
+// at least).
+constexpr int64_t kPageScratch = int64_t(256) << 20;
 
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
@@ -62,6 +64,7 @@ static int check_query(skv_handle *h, const skv_q8_pool *pool, const skv_shape *
     if (sh->nq < 1 || sh->H < 1 || sh->Hk < 1 || sh->S < 1 || sh->H % sh->Hk)
         return fail(h, SKV_EINVAL, "bad shape S=%d nq=%d H=%d Hk=%d", sh->S, sh->nq, sh->H, sh->Hk);
     if (sh->D != pool->D) return fail(h, SKV_EINVAL, "head dim %d over pages of head dim %d", sh->D, pool->D);
+    if (!std::isfinite(sh->scale)) return fail(h, SKV_EINVAL, "scale is not finite");
     if (!q) return fail(h, SKV_EINVAL, "q is NULL");
     if (misaligned(q, 16)) return fail(h, SKV_EUNSUPPORTED, "q must be 16-byte aligned");
     if (static_cast<int64_t>(sh->S) * sh->nq > INT32_MAX || static_cast<int64_t>(sh->nq) * (sh->H / sh->Hk) > INT32_MAX)
@@ -143,7 +146,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     // kernel 8 or 16.
     const bool tc = !sel && static_cast<int64_t>(shape->nq) * a.G >= kTcRows;
     // Tokens of one launch: as many as the kernels' counters have units for, and as
-    // keep the pages' log sums within kMassScratch (at least one).
+    // keep the pages' log sums within kPageScratch (at least one).
     const int64_t heads = static_cast<int64_t>(shape->S) * shape->Hk;
     constexpr int64_t max_units = kMaxUnits - 1;          // (a grid's y)
     int64_t nq_max = shape->nq;
@@ -158,7 +161,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
         const int64_t pairs = std::min<int64_t>(INT32_MAX, (int64_t(1) << 31) / (heads * ((pages_per_list + 1) / 2)));
         nq_max = std::min(nq_max, pairs * unit_rows / a.G);
     }
-    if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kMassScratch / (heads * a.G * per_list * 8)));
+    if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kPageScratch / (heads * a.G * per_list * 8)));
     if (nq_max < 1)
         return fail(h, SKV_EUNSUPPORTED, "S*Hk = %lld lists of %lld pages with %d query heads each are too many for one launch",
                     (long long)heads, (long long)pages_per_list, a.G);
@@ -220,16 +223,23 @@ int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape
     a.k_scale = pool->k_scale;
     a.q = static_cast<const __half *>(q);
     a.q_pos = q_pos;
-    a.nq = shape->nq;
+    a.nq_ld = shape->nq;
     a.H = shape->H;
     a.G = shape->H / shape->Hk;
     a.n_sel = n_sel;
     a.n_first = n_first;
     a.n_last = n_last;
     a.sel = sel;
-    if ((rc = ensure_workspace(h, static_cast<size_t>(rows) * pages_per_list * sizeof(uint32_t), st))) return rc;
+    const int64_t per_token = static_cast<int64_t>(shape->S) * shape->Hk * pages_per_list * sizeof(uint32_t);
+    const int nq_max = static_cast<int>(std::min<int64_t>(shape->nq, std::max<int64_t>(1, kPageScratch / per_token)));
+    if ((rc = ensure_workspace(h, static_cast<size_t>(per_token) * nq_max, st))) return rc;
     a.keys = static_cast<uint32_t *>(h->workspace);
-    return launch_select(h, a, shape->D, st);
+    for (int t = 0; t < shape->nq; t += nq_max) {
+        a.tok0 = t;
+        a.nq = std::min(nq_max, shape->nq - t);
+        if ((rc = launch_select(h, a, shape->D, st))) return rc;
+    }
+    return SKV_OK;
 }
 
 int skv_q8_evict(skv_handle *h, int32_t S, int32_t Hk, int64_t pages_per_list, const int32_t *page_ids,

@@ -18,6 +18,8 @@
 //
 // Bound: a token's append is two dependent reads (length, page id) and one
 // write deep, the prompt's by its bytes (x read once, codes written once).
+#include <algorithm>
+
 #include "q8.cuh"
 
 namespace skv {
@@ -33,6 +35,7 @@ struct AppendArgs {
     const void *x[2];              // [S][n_max][Hk][D]
     const int32_t *n_new;
     int n_max;
+    int64_t page0;                 // of the pages that a list's tokens touch, the launch's first
 };
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(X) == 2 ? 4 : 3) append
     const int64_t len = max(0, __ldg(a.L.kv_len + s));
     const int n = min(a.n_max, a.n_new ? max(0, __ldg(a.n_new + s)) : a.n_max);
     if (n == 0) return;
-    const int64_t blk = len / kPage + (blockIdx.y >> 1);
+    const int64_t blk = len / kPage + a.page0 + (blockIdx.y >> 1);
     const int64_t p0 = blk * kPage;                  // token of the page's row 0
     if (p0 >= len + n) return;
     const int r_lo = static_cast<int>(max(int64_t(0), len - p0));            // first row written
@@ -318,15 +321,19 @@ int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_
     a.n_max = n_max;
     // a run of n tokens touches at most ceil((n + 63) / 64) pages
     const int64_t blocks = (static_cast<int64_t>(n_max) + 2 * kPage - 2) / kPage;
-    const dim3 grid(L.Hk, static_cast<unsigned>(2 * blocks), L.S);
-    cudaError_t e;
-    if (x_type == SKV_F32)
-        e = pool.D == 128 ? launch(append_kernel<128, float>, grid, kAppendThreads, 0, st, a)
-                          : launch(append_kernel<64, float>, grid, kAppendThreads, 0, st, a);
-    else
-        e = pool.D == 128 ? launch(append_kernel<128, __half>, grid, kAppendThreads, 0, st, a)
-                          : launch(append_kernel<64, __half>, grid, kAppendThreads, 0, st, a);
-    return cuda_fail(h, e, "8-bit append launch");
+    constexpr int64_t most = 65535 / 2;              // (a grid's y)
+    for (a.page0 = 0; a.page0 < blocks; a.page0 += most) {
+        const dim3 grid(L.Hk, static_cast<unsigned>(2 * std::min(most, blocks - a.page0)), L.S);
+        cudaError_t e;
+        if (x_type == SKV_F32)
+            e = pool.D == 128 ? launch(append_kernel<128, float>, grid, kAppendThreads, 0, st, a)
+                              : launch(append_kernel<64, float>, grid, kAppendThreads, 0, st, a);
+        else
+            e = pool.D == 128 ? launch(append_kernel<128, __half>, grid, kAppendThreads, 0, st, a)
+                              : launch(append_kernel<64, __half>, grid, kAppendThreads, 0, st, a);
+        if (e != cudaSuccess) return cuda_fail(h, e, "8-bit append launch");
+    }
+    return SKV_OK;
 }
 
 }  // namespace q8

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                 raw[e] = make_uint2(0, 0);
                 if (c < cols) {
                     const int tok = t0 + c / nh, head = kh * a.G + h0 + c % nh;
-                    const __half *qp = a.q + ((static_cast<int64_t>(s) * a.nq + tok) * a.H + head) * D + lane * N;
+                    const __half *qp = a.q + (a.token(s, tok) * a.H + head) * D + lane * N;
                     if constexpr (N == 4) raw[e] = __ldg(reinterpret_cast<const uint2 *>(qp));
                     else raw[e].x = __ldg(reinterpret_cast<const uint32_t *>(qp));
                 }
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                 // pages that hold a key the token sees
                 int64_t seen = len;
                 if (a.q_pos)
-                    seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + static_cast<int64_t>(s) * a.nq + t0 + tid)) + 1));
+                    seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + a.token(s, t0 + tid))) + 1));
                 s_nb[tid] = static_cast<int>((seen + kPage - 1) / kPage);
             }
 #pragma unroll
@@ -405,13 +405,14 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a)
     start();
     __shared__ PickScratch<THREADS> sc;
     const int64_t row = blockIdx.x;
-    const int64_t tok = row / a.L.Hk;
-    const int s = static_cast<int>(tok / a.nq);
+    const int64_t st = row / a.L.Hk;
+    const int s = static_cast<int>(st / a.nq);
+    const int64_t tok = a.token(s, static_cast<int>(st % a.nq));
     int64_t seen = list_len(a.L, s);
     if (a.q_pos) seen = max(int64_t(0), min(seen, static_cast<int64_t>(__ldg(a.q_pos + tok)) + 1));
     const int n = static_cast<int>((seen + kPage - 1) / kPage);
     const uint32_t *src = a.keys + row * a.L.cap;
-    int32_t *out = a.sel + row * a.n_sel;
+    int32_t *out = a.sel + (tok * a.L.Hk + row % a.L.Hk) * a.n_sel;
     Keys<THREADS, KPT> keys(n, src);
     if constexpr (KPT > 0) keys.fill([&](int i) { return __ldcg(src + i); });
     // no more pages than places: all candidates; else the keys above the n-th and the

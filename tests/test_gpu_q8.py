@@ -77,6 +77,34 @@ def test_append_special_values_and_ragged_counts(h):
     assert h.status() == 0
 
 
+def test_append_of_more_pages_than_one_grid_has(h):
+    """The tokens of one call, and of two that part at a page's border: the same bytes."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    n, cut, D = 2097152 + 300, 64 * 20000, 64
+    cap = n // u.PAGE + 2
+    x = torch.randn((2, 1, n, 1, D), device="cuda", dtype=torch.float16)
+    ids = torch.randperm(cap, device="cuda").to(torch.int32).view(1, 1, cap)
+    pools = []
+    for parts in ([(0, n)], [(0, cut), (cut, n)]):
+        pool = skv.Q8Pool.empty(cap, D)
+        for t in (pool.k, pool.v, pool.k_scale, pool.v_scale, pool.k_min, pool.k_max):
+            t.zero_()
+        for a, b in parts:
+            skv.q8_append(h, pool, x[0, :, a:b].contiguous(), x[1, :, a:b].contiguous(), ids,
+                          torch.tensor([a], dtype=torch.int32, device="cuda"))
+        pools.append(pool)
+    for name in ("k", "v", "k_scale", "v_scale", "k_min", "k_max"):
+        assert torch.equal(getattr(pools[0], name), getattr(pools[1], name)), name
+    page = int(ids[0, 0, (n - 1) // u.PAGE])
+    want = x[0, 0, (n - 1) // u.PAGE * u.PAGE:, 0].float()
+    rows = want.shape[0]
+    # half a step of the scale, and fp32 products
+    assert ((pools[0].k[page, :rows].float() * pools[0].k_scale[page] - want).abs().max()
+            <= pools[0].k_scale[page] * 0.5001)
+    assert h.status() == 0
+
+
 def test_append_without_a_page_is_reported(h):
     import split_kv_flash_attn_gb300 as skv
     rng = np.random.default_rng(6)
@@ -286,6 +314,32 @@ def test_fp32_results_over_long_lists(h):
     assert h.status() == 0
 
 
+@pytest.mark.parametrize("G,nq,sel", [(2, 600, False), (1, 30, False), (2, 600, True)])
+def test_weights_in_several_launches(h, G, nq, sel):
+    """Lists so long that the pages' log sums of all tokens exceed the scratch of one
+    launch: results, weights and log sums as of one."""
+    import split_kv_flash_attn_gb300 as skv
+    import torch
+    rng = np.random.default_rng(G + nq)
+    cap = 65536 if nq > 30 else 1 << 21
+    c = u.Cache(rng, [400], 1, 64, cap=cap)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 1, nq, G, 64)
+    pos = rng.integers(-5, 450, (1, nq)).astype(np.int32)
+    n_sel = 60000                                     # (with the padding)
+    s = None
+    if sel:
+        s = np.full((1, nq, 1, n_sel), -1, np.int32)
+        s[..., 1], s[..., -1] = 2, 0
+    mass = torch.zeros((1, 1, cap), device="cuda")
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(pos), mass=mass, sel=None if s is None else _dev(s))
+    ref = u.attention(c, q, q_pos=pos, sel=s)
+    u.check(o, lse, ref)
+    tol = (ref[3] / (2 * ref[5]) + 2.0 ** -20) * nq * G
+    assert np.abs(mass.double().cpu().numpy() - ref[2]).max() <= tol
+    assert h.status() == 0
+
+
 # --------------------------------------------------------------- the selection
 
 @pytest.mark.parametrize("lens,nq,H,Hk,D,n,first,last,causal", [
@@ -310,6 +364,25 @@ def test_selection(h, lens, nq, H, Hk, D, n, first, last, causal):
                         q_pos=None if q_pos is None else _dev(q_pos))
     want = u.select(c, q, n, first, last, q_pos)
     assert np.array_equal(got.cpu().numpy(), want)
+    assert h.status() == 0
+
+
+def test_selection_of_many_tokens_in_long_lists(h):
+    """More keys than the scratch of one launch holds: the tokens go in several."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(9)
+    S, nq, H, D, cap = 2, 700, 2, 64, 65536
+    c = u.Cache(rng, [700, 333], 1, D, cap=cap)
+    pool, ids, kv_len = c.on_gpu()
+    q = _dev(_q(rng, S, nq, H, D))
+    pos = _dev(rng.integers(-5, 800, (S, nq)).astype(np.int32))
+    got = skv.q8_select(h, pool, q, ids, kv_len, n_sel=4, q_pos=pos)
+    for t in (0, 255, 511, 512, 513, 699):            # token by token, the same
+        one = skv.q8_select(h, pool, q[:, t:t + 1].contiguous(), ids, kv_len, n_sel=4, q_pos=pos[:, t:t + 1].contiguous())
+        assert torch.equal(got[:, t:t + 1], one), t
+    want = u.select(c, q[:, -3:].cpu().numpy(), 4, 1, 1, pos[:, -3:].cpu().numpy())
+    assert np.array_equal(got[:, -3:].cpu().numpy(), want)
     assert h.status() == 0
 
 
@@ -531,6 +604,38 @@ def test_runs_on_the_stream_it_is_given(h):
         o, lse = skv.q8_attn(h, pool, zero, ids, kv_len)
     s.synchronize()
     u.check(o, lse, u.attention(c, q))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_belong_to_the_stream_of_the_call(h, raw):
+    """Memory freed on the current stream, on which work with it is still queued, is
+    not what a call on another stream writes its results to."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(24)
+    c = u.Cache(rng, [640], 2, 128)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 1, 1, 8, 128)
+    qd = _dev(q)
+    mass = torch.rand((1, 2, c.cap), device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    big = torch.zeros(64 << 20, device="cuda")
+    old = [torch.empty(1024 * k, device="cuda") for k in (1, 2, 4) for _ in range(4)]
+    for _ in range(20):
+        big.add_(1.0)
+    for x in old:
+        x.fill_(7.0)                                  # behind big's additions
+    del old, x
+    st = s.cuda_stream if raw else s
+    sel = skv.q8_select(h, pool, qd, ids, kv_len, n_sel=4, stream=st)
+    o, lse = skv.q8_attn(h, pool, qd, ids, kv_len, stream=st)
+    kept = skv.q8_evict(h, ids, mass, kv_len, n_keep=6, stream=st)
+    torch.cuda.synchronize()
+    assert np.array_equal(sel.cpu().numpy(), u.select(c, q, 4, 1, 1))
+    u.check(o, lse, u.attention(c, q))
+    for a, b in zip(kept, u.evict(c.ids, mass.cpu().numpy(), c.lens, 6, 1, 1)):
+        assert np.array_equal(a.cpu().numpy(), b)
 
 
 def test_offsets_beyond_32_bits(h):

@@ -72,7 +72,8 @@ def test_append_of_nothing_is_fine(lib, hnd):
 
 
 @pytest.mark.parametrize("kw,rc", [(dict(S=0), 1), (dict(nq=0), 1), (dict(H=9), 1), (dict(Hk=0), 1), (dict(D=64), 1),
-                                   (dict(S=65536), 2), (dict(nq=2 ** 30, S=4), 2)])
+                                   (dict(S=65536), 2), (dict(nq=2 ** 30, S=4), 2),
+                                   (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1)])
 def test_bad_shapes(lib, hnd, kw, rc):
     sh = _shape(**kw)
     assert lib.skv_q8_attn(hnd, _pool(), sh, A, A, 4, A, None, None, 0, None, 3, A, A, None) == rc
