@@ -21,7 +21,6 @@ streams.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -425,10 +424,8 @@ def _q8_stream(h, stream, device):
 
 
 def _on_stream(stream, device):
-    """Context in which a call's results are allocated: they belong to the stream
-    it runs on, so that memory freed on another one is not written early."""
-    if stream is None:
-        return contextlib.nullcontext()
+    """Context in which the results of a call on a given stream are allocated: they
+    belong to that stream, so that memory freed on another one is not written early."""
     torch = _torch()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
@@ -448,8 +445,7 @@ def _raw_stream():
     return _raw_stream_fn
 
 
-def _q8_lists(page_ids, kv_len, device):
-    torch = _torch()
+def _q8_lists(torch, page_ids, kv_len, device):
     shape = page_ids.shape
     if len(shape) != 3:
         raise SplitKVError(1, f"page_ids: want int32 [S, Hk, pages_per_list], got {list(shape)}")
@@ -458,23 +454,24 @@ def _q8_lists(page_ids, kv_len, device):
     return shape
 
 
-def _q8_query(pool, q, page_ids, kv_len, q_pos, scale):
-    torch = _torch()
-    S, Hk, cap = _q8_lists(page_ids, kv_len, pool.device)
-    if q.dim() != 4:
-        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(q.shape)}")
-    _, nq, H, _ = q.shape
-    _need("q", q, torch.float16, (S, nq, H, pool.D), pool.device)
+def _q8_query(torch, pool, q, page_ids, kv_len, q_pos, scale):
+    dev, D = pool.device, pool.D
+    S, Hk, cap = _q8_lists(torch, page_ids, kv_len, dev)
+    shape = q.shape
+    if len(shape) != 4:
+        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(shape)}")
+    _, nq, H, _ = shape
+    _need("q", q, torch.float16, (S, nq, H, D), dev)
     if q_pos is not None:
-        _need("q_pos", q_pos, torch.int32, (S, nq), pool.device)
-    return SkvShape(S, nq, H, Hk, pool.D, pool.scale if scale is None else float(scale), 0, 0, 0, 0), S, nq, H, Hk, cap
+        _need("q_pos", q_pos, torch.int32, (S, nq), dev)
+    return SkvShape(S, nq, H, Hk, D, pool.scale if scale is None else float(scale), 0, 0, 0, 0), S, nq, H, Hk, cap
 
 
 def q8_append(h: Handle, pool: Q8Pool, k_new, v_new, page_ids, kv_len, *, n_new=None, stream=None):
     """skv_q8_append: write k_new, v_new (fp32 or fp16 [S, n, Hk, D]) as tokens
     kv_len[s] .. of each sequence; n_new int32 [S]: how many of the n rows."""
     torch = _torch()
-    S, Hk, cap = _q8_lists(page_ids, kv_len, pool.device)
+    S, Hk, cap = _q8_lists(torch, page_ids, kv_len, pool.device)
     st = _q8_stream(h, stream, pool.device)
     if k_new.dim() != 4 or k_new.dtype not in (torch.float32, torch.float16):
         raise SplitKVError(1, f"k_new: want fp32 or fp16 [S, n, Hk, D], got {k_new.dtype} {list(k_new.shape)}")
@@ -495,11 +492,16 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     o_dtype (or a given o) is torch.float16."""
     torch = _torch()
     dev = pool.device
-    sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, scale)
+    sh, S, nq, H, Hk, cap = _q8_query(torch, pool, q, page_ids, kv_len, q_pos, scale)
     st = _q8_stream(h, stream, dev)
     if o is None:
-        with _on_stream(stream, dev):
-            o = torch.empty_like(q, dtype=torch.float32 if o_dtype is None else o_dtype)
+        if o_dtype is None:
+            o_dtype = torch.float32
+        if stream is None:
+            o = torch.empty_like(q, dtype=o_dtype)
+        else:
+            with _on_stream(stream, dev):
+                o = torch.empty_like(q, dtype=o_dtype)
     else:
         _need("o", o, o.dtype, q.shape, dev)
     if o.dtype is torch.float32:
@@ -511,8 +513,11 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     if o_dtype is not None and o.dtype is not o_dtype:
         raise SplitKVError(1, f"o is {o.dtype}, o_dtype {o_dtype}")
     if lse is None:
-        with _on_stream(stream, dev):
+        if stream is None:
             lse = torch.empty((S, nq, H), dtype=torch.float32, device=q.device)
+        else:
+            with _on_stream(stream, dev):
+                lse = torch.empty((S, nq, H), dtype=torch.float32, device=q.device)
     else:
         _need("lse", lse, torch.float32, (S, nq, H), dev)
     n_sel, sel_ptr, mass_ptr = 0, None, None
@@ -523,7 +528,7 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     if mass is not None:
         _need("mass", mass, torch.float32, (S, Hk, cap), dev)
         mass_ptr = mass.data_ptr()
-    rc = _lib.lib().skv_q8_attn(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
+    rc = _lib.lib().skv_q8_attn(h._h, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
                                 kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(), sel_ptr, n_sel,
                                 mass_ptr, o_type, o.data_ptr(), lse.data_ptr(), st)
     if rc:
@@ -537,17 +542,23 @@ def q8_select(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, n_sel, n_first=1,
     -1 padded) of the pages with the largest score bounds for each query and
     KV head, the first n_first and last n_last among them."""
     torch = _torch()
-    sh, S, nq, H, Hk, cap = _q8_query(pool, q, page_ids, kv_len, q_pos, None)
+    sh, S, nq, H, Hk, cap = _q8_query(torch, pool, q, page_ids, kv_len, q_pos, None)
     st = _q8_stream(h, stream, pool.device)
     n_sel = int(n_sel)
     if sel is None:
-        with _on_stream(stream, pool.device):
-            sel = torch.empty((S, nq, Hk, max(0, n_sel)), dtype=torch.int32, device=q.device)
+        shape = (S, nq, Hk, max(0, n_sel))
+        if stream is None:
+            sel = torch.empty(shape, dtype=torch.int32, device=q.device)
+        else:
+            with _on_stream(stream, pool.device):
+                sel = torch.empty(shape, dtype=torch.int32, device=q.device)
     else:
         _need("sel", sel, torch.int32, (S, nq, Hk, n_sel), pool.device)
-    h.check(_lib.lib().skv_q8_select(h.ptr, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
-                                     kv_len.data_ptr(), _ptr(q_pos), n_sel, int(n_first), int(n_last),
-                                     sel.data_ptr(), st))
+    rc = _lib.lib().skv_q8_select(h._h, pool._ref, ctypes.byref(sh), q.data_ptr(), page_ids.data_ptr(), cap,
+                                  kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(), n_sel, int(n_first),
+                                  int(n_last), sel.data_ptr(), st)
+    if rc:
+        h.check(rc)
     return sel
 
 
@@ -556,12 +567,17 @@ def q8_evict(h: Handle, page_ids, mass, kv_len, *, n_keep, n_first=1, n_last=1, 
     n_last, the others of largest mass): (page_ids, mass, kv_len, freed)."""
     torch = _torch()
     dev = page_ids.get_device()
-    S, Hk, cap = _q8_lists(page_ids, kv_len, dev)
+    S, Hk, cap = _q8_lists(torch, page_ids, kv_len, dev)
     st = _q8_stream(h, stream, dev)
     _need("mass", mass, torch.float32, (S, Hk, cap), dev)
-    with _on_stream(stream, dev):
-        ids_out, freed = torch.empty_like(page_ids), torch.empty_like(page_ids)
-        mass_out, len_out = torch.empty_like(mass), torch.empty_like(kv_len)
+    def results():
+        return (torch.empty_like(page_ids), torch.empty_like(mass), torch.empty_like(kv_len),
+                torch.empty_like(page_ids))
+    if stream is None:
+        ids_out, mass_out, len_out, freed = results()
+    else:
+        with _on_stream(stream, dev):
+            ids_out, mass_out, len_out, freed = results()
     h.check(_lib.lib().skv_q8_evict(h.ptr, S, Hk, cap, page_ids.data_ptr(), mass.data_ptr(), kv_len.data_ptr(),
                                     int(n_keep), int(n_first), int(n_last), ids_out.data_ptr(), mass_out.data_ptr(),
                                     len_out.data_ptr(), freed.data_ptr(), st))
