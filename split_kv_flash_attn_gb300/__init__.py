@@ -456,12 +456,18 @@ def _q8_lists(torch, page_ids, kv_len, device):
 
 def _q8_query(torch, pool, q, page_ids, kv_len, q_pos, scale):
     dev, D = pool.device, pool.D
-    S, Hk, cap = _q8_lists(torch, page_ids, kv_len, dev)
-    shape = q.shape
-    if len(shape) != 4:
-        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(shape)}")
+    lists, shape = page_ids.shape, q.shape
+    # all checks in one expression; what fails is found again below, with its message
+    if not (len(lists) == 3 and len(shape) == 4 and page_ids.dtype is torch.int32 and kv_len.dtype is torch.int32
+            and q.dtype is torch.float16 and kv_len.shape == lists[:1] and shape[0] == lists[0] and shape[3] == D
+            and page_ids.get_device() == dev and kv_len.get_device() == dev and q.get_device() == dev
+            and page_ids.is_contiguous() and kv_len.is_contiguous() and q.is_contiguous()):
+        _q8_lists(torch, page_ids, kv_len, dev)
+        if len(shape) != 4:
+            raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(shape)}")
+        _need("q", q, torch.float16, (lists[0], shape[1], shape[2], D), dev)
+    S, Hk, cap = lists
     _, nq, H, _ = shape
-    _need("q", q, torch.float16, (S, nq, H, D), dev)
     if q_pos is not None:
         _need("q_pos", q_pos, torch.int32, (S, nq), dev)
     return SkvShape(S, nq, H, Hk, D, pool.scale if scale is None else float(scale), 0, 0, 0, 0), S, nq, H, Hk, cap

@@ -175,7 +175,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     // two partials for each CTA's piece
     const size_t po = round256(static_cast<size_t>(2) * grid * unit_rows * D * sizeof(float));
     const size_t pm = round256(static_cast<size_t>(2) * grid * unit_rows * 2 * sizeof(float));
-    const size_t pp = tc ? round256((static_cast<size_t>(shape->S) * a.row_groups + 1) * sizeof(uint32_t)) : 0;
+    const size_t pp = tc ? round256((static_cast<size_t>(shape->S) * a.row_groups + 2) * sizeof(uint32_t)) : 0;
     const size_t pl = mass ? static_cast<size_t>(heads) * a.nq * a.G * per_list * (tc ? 4 : 8) : 0;
     if ((rc = ensure_workspace(h, po + pm + pp + pl, st))) return rc;
     uint8_t *ws = static_cast<uint8_t *>(h->workspace);

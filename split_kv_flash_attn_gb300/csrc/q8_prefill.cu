@@ -25,7 +25,8 @@
 //
 // Work split.  All key tiles of all (sequence, KV head, tile pair) units form one
 // line (its prefix sums are taken from the lengths and query positions on the
-// device, by a one-CTA kernel where they are many), cut into one equal piece for each CTA; units that several
+// device, by a one-CTA kernel where they are many), cut into one piece for each CTA:
+// equal ones, or slightly longer ones that end with their units.  Units that several
 // pieces share are merged by a kernel of a warp a row, in piece order (by the last
 // CTA of each unit that took 60 to 100 us).
 //
@@ -62,6 +63,7 @@ __device__ __forceinline__ void fewer_regs()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr uint32_t kPieceTiles = 3;                // fewest key tiles of a piece: each costs set-up and merge
+constexpr int kStraddleTiles = 3;               // tiles that a second start and result of a CTA cost
 constexpr int kPlanHere = 256;                  // plan entries that the prefill kernel counts itself
 constexpr int kPlanSmem = 1024;                 // plan entries kept in shared memory
 constexpr float kPfShift = 8.f, kPfGrow = 5.f, kPfScaleGrow = 2.f;
@@ -69,9 +71,9 @@ constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a w
 // The tensor core rounds its sums toward zero.  A tile's 16 additions (both parts of
 // the weights) shrink O by 2.4e-7 on average and blur it by 1.4e-7, in
 // proportion to the tiles (measured against 64 bits for 3 to 128 tiles): fp32
-// results take at most kExactTiles at a time, put together in fp32, and the
+// results take about kExactTiles at a time, put together in fp32, and the
 // average loss is given back.
-constexpr int kExactTiles = 8;
+constexpr int kExactTiles = 8, kExactMore = 2;    // (up to that many more rather than another stretch)
 constexpr float kLoss = 2.4e-7f;
 constexpr float kNoScale = -100.f;              // log2 d_v - r of a zero scale (fp16 0, while l stays right)
 
@@ -85,7 +87,8 @@ struct PfSmem {
     static constexpr int kStage = kV + 2 * kTile;               // results on their way out: 32 rows of 16 for each softmax warp
     static constexpr int kStageLd = 20;                         // (floats a row: free of bank conflicts)
     static constexpr int kPlan = kStage + kSoftWarps * 32 * kStageLd * 4;
-    static constexpr int kTotal = kPlan + (kPlanSmem + 1) * 4 + 1024;   // + alignment slack
+    static constexpr int kTiles = kPlan + (kPlanSmem + 2) * 4;          // tiles of each entry, where they are counted here
+    static constexpr int kTotal = kTiles + kPlanHere * 4 + 1024;        // + alignment slack
 };
 static_assert(PfSmem<128>::kTotal <= 226 * 1024, "shared memory per CTA");
 
@@ -101,7 +104,8 @@ enum { PB_KFULL = 0, PB_KEMPTY = 2, PB_VFULL = 4, PB_VEMPTY = 6, PB_QFULL = 8, P
 
 struct PrefillArgs {
     AttnArgs a;
-    uint32_t *plan;                             // [S * n_pairs + 1] tiles before each (sequence, pair)
+    uint32_t *plan;                             // [S * n_pairs + 1] the line's length before each (sequence, pair) of one
+                                                // head, then the tiles of a piece
     int n_pairs;
     int out_f16;
 };
@@ -139,7 +143,7 @@ __device__ __forceinline__ void check_lengths(const AttnArgs &a, int t, int n)
 }
 
 // The plan of many entries: prefix sums of their tiles.
-__global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, int n_pairs, uint32_t *plan)
+__global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, int n_pairs, uint32_t *plan, int ctas)
 {
     start();
     __shared__ uint32_t s_sum[32];
@@ -169,7 +173,10 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnArgs a, in
         plan[e] = before;
         before += x;
     }
-    if (tid == 1023) plan[n] = before;
+    if (tid == 1023) {
+        plan[n] = before;
+        plan[n + 1] = piece_tiles(before * a.L.Hk, ctas);
+    }
 }
 
 // The units of a CTA's piece of the line in turn, as every role walks them.
@@ -185,12 +192,23 @@ struct Walk {
     int np, S, Hk;
     int most;                                   // tiles at a time
     uint32_t end;                               // of the piece
+    uint32_t whole;                             // tiles of a piece where pieces end with their units, else 0
+    const uint32_t *of;                         // with whole: the entries' tiles (the line holds them rounded up to pieces)
 
     __device__ void cut(Unit &x, uint32_t pos) const
     {
-        x.p0 = static_cast<int>(pos - x.unit0);
-        x.p1 = static_cast<int>(min(static_cast<uint32_t>(x.n), end - x.unit0));
-        const int len = x.p1 - x.p0, k = (len + most - 1) / most;
+        if (whole) {                            // the unit's tiles in as many equal parts as it has pieces
+            const uint32_t T = of[x.s * np + x.pr];   // (below 2^24, and k and i below 2^8)
+            const uint32_t k = x.n / whole, i = (pos - x.unit0) / whole;
+            x.n = static_cast<int>(T);
+            x.p0 = static_cast<int>(i * T / k);
+            x.p1 = static_cast<int>((i + 1) * T / k);
+            x.unit0 = pos - x.p0;
+        } else {
+            x.p0 = static_cast<int>(pos - x.unit0);
+            x.p1 = static_cast<int>(min(static_cast<uint32_t>(x.n), end - x.unit0));
+        }
+        const int len = x.p1 - x.p0, k = max(1, (len + most - 1 - kExactMore) / most);
         x.sub = (len + k - 1) / k;
         x.t0 = x.p0;
         x.t1 = x.p0 + x.sub;
@@ -234,7 +252,7 @@ struct Walk {
             return true;
         }
         const uint32_t pos = x.unit0 + x.p1;
-        if (pos >= end) return false;
+        if (whole || pos >= end) return false;
         do {
             if (++x.pr == np) {
                 x.pr = 0;
@@ -267,7 +285,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     __shared__ alignas(8) uint64_t s_bar[PB_COUNT];
     __shared__ Meta s_meta[4][2];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_whole;
     __shared__ Unit s_unit[kSoftWarps][2];      // the softmax warps' units: kept out of their registers
     const uint32_t bar0 = smem_addr(s_bar);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -300,28 +318,47 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     start();
     const int np = pa.n_pairs;
     const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
-    Walk walk{pa.plan, np, a.L.S, a.L.Hk, HILO ? kExactTiles : INT32_MAX / 2, 0};
-    uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan);
+    uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan), *s_tiles = reinterpret_cast<uint32_t *>(sm + SM::kTiles);
+    Walk walk{pa.plan, np, a.L.S, a.L.Hk, HILO ? kExactTiles : INT32_MAX / 2, 0, 0, s_tiles};
     if (n_entries <= kPlanHere) {               // few entries: every CTA counts them itself
         for (int e = warp; e < n_entries; e += kPfThreads / 32) {
             const uint32_t x = entry_tiles(a, np, e);
-            if (lane == 0) s_plan[e] = x;
+            if (lane == 0) s_tiles[e] = x;
         }
         if (blockIdx.x == 0) check_lengths(a, tid, kPfThreads);
         walk.plan = s_plan;
     } else if (n_entries <= kPlanSmem) {
-        for (int i = tid; i <= n_entries; i += kPfThreads) s_plan[i] = __ldcg(pa.plan + i);
+        for (int i = tid; i <= n_entries + 1; i += kPfThreads) s_plan[i] = __ldcg(pa.plan + i);
         walk.plan = s_plan;
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
-    if (n_entries <= kPlanHere) {               // their prefix sums; the merge reads CTA 0's
+    if (n_entries <= kPlanHere) {               // pieces and prefix sums; the merge reads CTA 0's
         if (warp == 0) {
+            // Pieces that end with their units spare the CTAs a second start and result:
+            // taken when the least piece with which the grid covers units one by one is
+            // at most kStraddleTiles longer than even shares (64 tokens of eight ragged
+            // sequences over up to 4096 keys, fp32: 48 us, against 56).
+            uint32_t sum = 0, n[kStraddleTiles + 1] = {};
+            for (int e = lane; e < n_entries; e += 32) sum += s_tiles[e];
+            const uint32_t even = piece_tiles(__reduce_add_sync(0xffffffffu, sum) * a.L.Hk, gridDim.x);
+            for (int e = lane; e < n_entries; e += 32)
+#pragma unroll
+                for (int i = 0; i <= kStraddleTiles; ++i) n[i] += (s_tiles[e] + even + i - 1) / (even + i);
+            uint32_t chunk = even;
+            bool fits = false;
+#pragma unroll
+            for (int i = kStraddleTiles; i >= 0; --i)
+                if (__reduce_add_sync(0xffffffffu, n[i]) * a.L.Hk <= gridDim.x) {
+                    chunk = even + i;
+                    fits = true;
+                }
             uint32_t before = 0;
             for (int b = 0; b < n_entries; b += 32) {
-                const uint32_t x = b + lane < n_entries ? s_plan[b + lane] : 0u;
+                uint32_t x = b + lane < n_entries ? s_tiles[b + lane] : 0u;
+                if (fits) x = (x + chunk - 1) / chunk * chunk;
                 uint32_t inc = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -331,15 +368,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                 if (b + lane < n_entries) s_plan[b + lane] = before + inc - x;
                 before += __shfl_sync(0xffffffffu, inc, 31);
             }
-            if (lane == 0) s_plan[n_entries] = before;
+            if (lane == 0) {
+                s_plan[n_entries] = before;
+                s_plan[n_entries + 1] = chunk;
+                s_whole = fits;
+            }
         }
         __syncthreads();
+        if (s_whole) walk.whole = s_plan[n_entries + 1];
         if (blockIdx.x == 0)
-            for (int i = tid; i <= n_entries; i += kPfThreads) pa.plan[i] = s_plan[i];
+            for (int i = tid; i <= n_entries + 1; i += kPfThreads) pa.plan[i] = s_plan[i];
     }
 
     const uint32_t total = walk.plan[n_entries] * a.L.Hk;
-    const uint32_t chunk = piece_tiles(total, gridDim.x);
+    const uint32_t chunk = walk.plan[n_entries + 1];
     const uint32_t pos0 = min(total, blockIdx.x * chunk);
     walk.end = min(total, pos0 + chunk);
     const bool any = pos0 < walk.end;
@@ -578,7 +620,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             constexpr int LPR = D / 8;
             const int c = lane % LPR;
             uint8_t *qt = sm + SM::kQ + g * SM::kTile + (c >> 3) * SM::kHalf;
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < LPR; ++i) {
                 const int rl = i * (32 / LPR) + lane / LPR;         // row of the warp
                 const int64_t r = __shfl_sync(0xffffffffu, index, rl);
@@ -827,7 +869,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
 // lanes a row, kMergeRows rows a thread.
 constexpr int kMergeRows = 4;
 template <int D>
-__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa, int pieces)
+__global__ void __launch_bounds__(256, 2) prefill_merge_kernel(const PrefillArgs pa)
 {
     start();
     const AttnArgs &a = pa.a;
@@ -836,11 +878,10 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs pa
     const int unit = blockIdx.y, list = unit / np, pr = unit - list * np;
     const int s = list / a.L.Hk, kh = list - s * a.L.Hk;
     const int64_t e0 = static_cast<int64_t>(s) * np;
-    const uint32_t total = __ldcg(pa.plan + static_cast<int64_t>(a.L.S) * np) * a.L.Hk;
+    const uint32_t chunk = __ldcg(pa.plan + static_cast<int64_t>(a.L.S) * np + 1);
     const uint32_t p0 = __ldcg(pa.plan + e0), pe = __ldcg(pa.plan + e0 + pr), pe1 = __ldcg(pa.plan + e0 + pr + 1);
     const uint32_t T = __ldcg(pa.plan + e0 + np) - p0;
     if (pe1 == pe) return;
-    const uint32_t chunk = piece_tiles(total, pieces);
     const uint32_t unit0 = p0 * a.L.Hk + kh * T + (pe - p0);
     const uint32_t c_lo = unit0 / chunk, c_hi = (unit0 + (pe1 - pe) - 1) / chunk;
     if (c_lo == c_hi) return;
@@ -937,7 +978,7 @@ static int launch_one(skv_handle *h, const PrefillArgs &pa, int grid, cudaStream
     if (l != cudaSuccess) return cuda_fail(h, l, "8-bit prefill launch");
     const int units = pa.a.L.S * pa.a.L.Hk * pa.n_pairs;
     const int rows = std::min(2 * kPM, pa.a.rows);
-    return cuda_fail(h, launch(prefill_merge_kernel<D>, dim3((rows * (D / 4) + 256 * kMergeRows - 1) / (256 * kMergeRows), units), 256, 0, st, pa, grid),
+    return cuda_fail(h, launch(prefill_merge_kernel<D>, dim3((rows * (D / 4) + 256 * kMergeRows - 1) / (256 * kMergeRows), units), 256, 0, st, pa),
                      "8-bit prefill merge launch");
 }
 
@@ -945,7 +986,7 @@ int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, uint32_t *
                    cudaStream_t st)
 {
     if (static_cast<int64_t>(a.L.S) * n_pairs > kPlanHere) {
-        const cudaError_t e = launch(prefill_plan_kernel, dim3(1), 1024, 0, st, a, n_pairs, plan);
+        const cudaError_t e = launch(prefill_plan_kernel, dim3(1), 1024, 0, st, a, n_pairs, plan, grid);
         if (e != cudaSuccess) return cuda_fail(h, e, "8-bit prefill plan launch");
     }
     const PrefillArgs pa{a, plan, n_pairs, f16};
