@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                     if (blk >= 0 && blk * kPage < lim) m.id = max(-1, checked_page(a.L, __ldg(ids + blk)));
                     m.blk = static_cast<int>(blk);
                     if (m.id >= 0) {
-                        m.ks = __ldg(a.k_scale + m.id) * a.scale_log2;
+                        m.ks = __ldg(a.k_scale + m.id);
                         m.vs = __ldg(a.v_scale + m.id);
                     }
                 }
@@ -289,14 +289,30 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 const Meta cur = nxt;
                 if (first + 32 < x.pg1) nxt = load_meta(first + 32);
                 const int n = min(32, x.pg1 - first);
+                // the CTA's first pages go out before their scales are there; they are
+                // announced below
+                const int early = n_put == 0 ? min(n, NS) : 0;
+                for (int i = 0; i < early; ++i) {
+                    const int id = __shfl_sync(0xffffffffu, cur.id, i);
+                    if (id >= 0 && lane == 0) {
+                        const uint32_t dst = smem_addr(ring + i * 2 * BYTES), full = bar0 + 8 * i;
+                        tc::mbar_expect_tx_only(full, 2 * BYTES);
+                        tc::tma_load_3d(dst, &map_k, 0, 0, id, full);
+                        tc::tma_load_3d(dst + BYTES, &map_v, 0, 0, id, full);
+                    }
+                }
                 // (64 entries: those of the 32 pages before are still in use, at
                 // most NS of them not taken yet)
-                if (lane < n) s_meta[(n_put + lane) % 64] = cur;
+                if (lane < n) s_meta[(n_put + lane) % 64] = Meta{cur.id, cur.blk, cur.ks * a.scale_log2, cur.vs};
                 __syncwarp();
                 if (lane == 0) {
                     for (int i = 0; i < n; ++i) {
                         const uint32_t m = n_put + i, slot = m % NS, turn = m / NS;
                         const uint32_t full = bar0 + 8 * slot, empty = bar0 + 8 * (NS + slot);
+                        if (i < early) {
+                            tc::mbar_arrive(full);
+                            continue;
+                        }
                         if (turn > 0 && !wait(empty, (turn - 1) & 1)) {
                             ok = false;
                             n_put = m - n;          // (+ n below)
