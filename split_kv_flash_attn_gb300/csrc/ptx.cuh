@@ -104,6 +104,21 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1)
         : "+f"(d0), "+f"(d1)
         : "f"(a0), "f"(a1));
 }
+// d += a * b, two at a time.
+__device__ __forceinline__ void fma2_to(float &d0, float &d1, float a0, float a1, float b)
+{
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 d, {%0, %1};\n"
+        " fma.rn.f32x2 d, a, b, d;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1), "f"(b));
+}
+// Three-operand extremes; a NaN yields to the others.
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float d;
+    asm("min.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;

@@ -189,46 +189,58 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(X) == 2 ? 4 : 3) append
         hi[e] = -127.f;
     }
     if (plain) {
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = r0 + i * RPP;
-        if (r < r_lo || r >= r_hi) continue;
-        // t + 1.5 2^23 rounds t to an integer, whose low byte is the sum's
+        // v / d' + 1.5 2^23 rounds to an integer, whose low byte is the sum's
         constexpr float kMagic = 12582912.f;
-        float v[8], c[8];
-        uint32_t q[8];
-        in[i].values(v);
-        float off = 0.f;
+        float c[2][8];                                                      // of two rows; NaN: none
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = v[e] * rd;
-            const float m = t + kMagic;
-            q[e] = __float_as_uint(m);
-            c[e] = m - kMagic;
-            off = fmaxf(off, fabsf(t - c[e]));
-        }
-        if (!(off < 0.5f - 0x1p-13f)) {
-            // next to a half-integer h, the sign of x - h d' decides (one rounding,
-            // so the sign is exact; d' is not tiny)
+        for (int i = 0; i < PASSES; ++i) {
+            const int r = r0 + i * RPP;
+            float(&ci)[8] = c[i & 1];
+            if (r >= r_lo && r < r_hi) {
+                float v[8], side[8];
+                uint32_t q[8];
+                in[i].values(v);
+                float off = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float side = v[e] * rd - c[e];
-                const float rem = __fmaf_rn(-(c[e] + copysignf(0.5f, side)), d1, v[e]) * copysignf(1.f, side);
-                if (rem > 0.f || (rem == 0.f && fabsf(side) > 0.25f && (q[e] & 1u))) {
-                    c[e] += copysignf(1.f, side);
-                    q[e] = __float_as_uint(c[e] + kMagic);
+                for (int e = 0; e < 8; e += 2) {
+                    float m0, m1;
+                    fma2(m0, m1, v[e], v[e + 1], rd, kMagic);
+                    q[e] = __float_as_uint(m0);
+                    q[e + 1] = __float_as_uint(m1);
+                    add2(m0, m1, -kMagic, -kMagic);
+                    ci[e] = m0;
+                    ci[e + 1] = m1;
+                    side[e] = -m0;
+                    side[e + 1] = -m1;
+                    fma2_to(side[e], side[e + 1], v[e], v[e + 1], rd);
+                    off = max3(off, fabsf(side[e]), fabsf(side[e + 1]));
+                }
+                if (!(off < 0.5f - 0x1p-13f)) {
+                    // next to a half-integer h, the sign of x - h d' decides (one rounding,
+                    // so the sign is exact; d' is not tiny)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float rem = __fmaf_rn(-(ci[e] + copysignf(0.5f, side[e])), d1, v[e]) * copysignf(1.f, side[e]);
+                        if (rem > 0.f || (rem == 0.f && fabsf(side[e]) > 0.25f && (q[e] & 1u))) {
+                            ci[e] += copysignf(1.f, side[e]);
+                            q[e] = __float_as_uint(ci[e] + kMagic);
+                        }
+                    }
+                }
+                *reinterpret_cast<uint2 *>(page + r * D + c8) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ci[e] = __uint_as_float(0x7fffffffu);
+            }
+            if ((i & 1) && which == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    lo[e] = min3(lo[e], c[0][e], c[1][e]);
+                    hi[e] = max3(hi[e], c[0][e], c[1][e]);
                 }
             }
         }
-        *reinterpret_cast<uint2 *>(page + r * D + c8) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
-        if (which == 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                lo[e] = fminf(lo[e], c[e]);
-                hi[e] = fmaxf(hi[e], c[e]);
-            }
-        }
-    }
+        static_assert(PASSES % 2 == 0, "rows in pairs");
     } else {
         // the values once more, one by one
         for (int r = r0; r < r_hi; r += RPP) {
