@@ -110,7 +110,7 @@ __device__ __forceinline__ uint32_t recode4(const int8_t *lut, uint32_t w)
 }
 
 template <int D, typename X>
-__global__ void __launch_bounds__(kAppendThreads, sizeof(X) == 2 ? 4 : 3) append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a)
 {
     constexpr int TPR = D / 8;                       // threads a row
     constexpr int RPP = kAppendThreads / TPR;        // rows a pass
