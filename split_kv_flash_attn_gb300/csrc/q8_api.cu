@@ -25,9 +25,10 @@ struct OnDevice {
 // Query rows of a KV head from which the tensor-core kernel serves: it computes 256
 // rows whatever is there, the decode kernel passes over the keys again for each 16.
 // Eight KV heads of D = 128, decode against tensor cores: 32768 keys of one sequence
-// 39.5 / 53 us at 32 rows and 49.8 / 53 at 48; 8000 keys of eight sequences 65.8 /
-// 67.9 us at 32 rows and 92.8 / 68 at 48.  Over short contexts decode stays ahead
-// for longer (2000 keys of one sequence: 18.6 / 26.4 us at 96 rows), but by less.
+// 39.7 / 43.6 us at 32 rows and 49.7 / 43.6 at 48 with fp16 results (fp32: 44 / 59 and
+// 57 / 59); 8000 keys of eight sequences 66 / 65 us at 32 rows and 93 / 65 at 48
+// (fp32: 75 / 107 and 106 / 107; 190 / 107 at 96).  Over short contexts decode stays
+// ahead for longer, but by less (2000 keys of one sequence, fp32, 96 rows: 20 / 23 us).
 constexpr int kTcRows = 33;
 // Scratch for the pages' log sums or the selection's keys of one launch (one token's
 // at least).

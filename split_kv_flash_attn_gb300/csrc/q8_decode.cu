@@ -18,8 +18,9 @@
 // together by the last CTA to finish with it, in piece order (so results do not
 // depend on timing).  (Equal pieces end up to 15 % apart, as some SMs see less
 // bandwidth; short pieces handed out at the end cost more than that: each begins
-// with a chain of look-ups and ends with a join, 72 against 64 us.)  Lengths are read on the device: a call costs its keys, not
-// its lists' capacity, and ragged batches stay balanced.
+// with a chain of look-ups and ends with a join, 72 against 64 us.)  Lengths are read
+// on the device: a call costs its keys, not its lists' capacity, and ragged batches
+// stay balanced.
 //
 // A CTA is one warp that fetches and W that compute.  The first walks the CTA's
 // pages, looks their ids and scales up 32 at a time and keeps a ring of pages (K
@@ -37,8 +38,10 @@
 // Keys are the M side of S = K Q^T and channels that of O^T = V^T P^T, so
 // the eight query columns of a product carry a KV head's query heads.
 //
-// Bound: the pages' bytes at long lengths (see the table in the design notes);
-// launch, plan and merge at short ones.
+// Bound: the pages' bytes at long lengths (one sequence over 1048576 keys, eight KV
+// heads of D = 128: 323 us, 6.65 TB/s; eight sequences of up to 32768: 61 us, 5.2 TB/s,
+// DRAM reads 316 MB, which is the pages); launch, look-ups and joins at short ones
+// (256 keys: 5.9 us).
 #include "q8.cuh"
 
 namespace skv {
@@ -49,9 +52,9 @@ constexpr float kGrow = 4.f;        // ... and their reference moves when a scor
 constexpr int kStep = 32;           // keys a warp takes at a time
 constexpr uint32_t kStraddle = 8;   // pages that a second start and join of a CTA cost
 
-// Computing warps and ring slots.  One column group: 8 sequences x 32768 keys take
-// 64 us with 11 and 11, 65 with 7 and 7 or 8 and 8, 70 with 6 and 12; two groups
-// need the registers of 7 warps.
+// Computing warps and ring slots.  One column group: eight sequences of up to 32768
+// keys take 61 us with 11 and 11, 63 with 7 and 7 or 8 and 8, 68 with 6 and 12 (one
+// of 1048576: 323, 334, 340 and 367); two groups need the registers of 7 warps.
 __host__ __device__ constexpr int warps_of(int nc) { return nc == 1 ? 11 : 7; }
 __host__ __device__ constexpr int slots_of(int nc) { return nc == 1 ? 11 : 7; }
 template <int D, int NC>

@@ -18,9 +18,10 @@
 // prefix sums over the warps' equal shares.  Ties at the n-th key go to the lowest
 // indices.
 //
-// Bound: the scores by latency (lengths, ids, extremes and queries are read one
-// after the other, 2D + 8 bytes a page and head in all); the choice by its
-// counting rounds, each one pass over registers and one barrier, three or four until
+// Bound (select and attend over 16 of 128 pages: 18 us, of which 9 here; 512 of 4096
+// pages of 16 lists: 53 and 19): the scores by latency (lengths, ids, extremes and
+// queries are read one after the other, 2D + 8 bytes a page and head in all); the
+// choice by its counting rounds, each one pass over registers and one barrier, three or four until
 // few keys are left to each warp alone (without that 12 rounds: 13.4 against 10.3 us
 // for 64 lists of 2048 pages).
 #include <algorithm>
@@ -455,7 +456,8 @@ __device__ void in_order(const Keys<THREADS, KPT> &keys, uint32_t T, PickScratch
 }
 
 // Threads and keys a thread for lists of up to `cap` pages: few threads meet sooner
-// and count in registers (4096 pages: 14 us with 1024 threads over shared memory).
+// and count in registers (choosing from 4096 pages took 14 us with 1024 threads over
+// shared memory, 11 so).
 template <typename F>
 auto for_cap(int64_t cap, F f)
 {
