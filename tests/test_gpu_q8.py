@@ -564,6 +564,90 @@ def test_graph_replays_follow_the_inputs(h):
     hh.close()
 
 
+def test_a_captured_prompt_step(h):
+    """Append, attention of many rows in fp32 and fp16, weights and eviction in one graph,
+    replayed on other tokens and lengths."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(25)
+    hh = skv.Handle(0)
+    Hk, H, D, n = 2, 8, 128, 70
+    c = u.Cache(rng, [300, 1100], Hk, D, extra=n)
+    pool, ids, kv_len = c.on_gpu()
+    after = kv_len + n
+    x = torch.zeros((2, 2, n, Hk, D), dtype=torch.float16, device="cuda")
+    q = torch.zeros((2, n, H, D), dtype=torch.float16, device="cuda")
+    pos = torch.zeros((2, n), dtype=torch.int32, device="cuda")
+    mass = torch.zeros((2, Hk, c.cap), device="cuda")
+
+    def step():
+        skv.q8_append(hh, pool, x[0], x[1], ids, kv_len)
+        a = skv.q8_attn(hh, pool, q, ids, after, q_pos=pos, mass=mass)
+        b = skv.q8_attn(hh, pool, q, ids, after, q_pos=pos, o_dtype=torch.float16)
+        return a + b + skv.q8_evict(hh, ids, mass, after, n_keep=6, n_first=1, n_last=2)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for lens in ([300, 1100], [0, 63], [129, 640]):
+        c.lens[:] = lens
+        kv_len.copy_(_dev(c.lens))
+        xx = rng.standard_normal((2, 2, n, Hk, D)).astype(np.float16)
+        x.copy_(_dev(xx))
+        c.k, c.v, c.ks, c.vs = (t.cpu().numpy().copy() for t in (pool.k, pool.v, pool.k_scale, pool.v_scale))
+        u.append(c, xx[0], xx[1])
+        c.lens += n
+        after.copy_(_dev(c.lens))
+        qq, pp = _q(rng, 2, n, H, D), _causal(c, n)
+        q.copy_(_dev(qq))
+        pos.copy_(_dev(pp))
+        mass.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(pool.k.cpu().numpy(), c.k) and np.array_equal(pool.v_scale.cpu().numpy(), c.vs)
+        ref = u.attention(c, qq, q_pos=pp)
+        u.check(out[0], out[1], ref)
+        u.check(out[2], out[3], ref, f16=True)
+        for a, b in zip(out[4:], u.evict(c.ids, mass.cpu().numpy(), c.lens, 6, 1, 2)):
+            assert np.array_equal(a.cpu().numpy(), b)
+    assert hh.status() == 0
+    hh.close()
+
+
+def test_two_handles_on_two_streams_at_once(h):
+    """Calls that overlap on the GPU, each with its handle: the results of one after the other."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(26)
+    hh = skv.Handle(0)
+    jobs = []
+    for hd, lens, nq in ((h, [9000, 4000, 1], 1), (hh, [3000, 7000], 70)):
+        c = u.Cache(rng, lens, 4, 128)
+        pool, ids, kv_len = c.on_gpu()
+        q, pos = _dev(_q(rng, len(lens), nq, 16, 128)), _dev(_causal(c, nq))
+
+        def job(hd=hd, pool=pool, ids=ids, kv_len=kv_len, q=q, pos=pos):
+            sel = skv.q8_select(hd, pool, q, ids, kv_len, n_sel=9, q_pos=pos)
+            return (sel, *skv.q8_attn(hd, pool, q, ids, kv_len, q_pos=pos),
+                    *skv.q8_attn(hd, pool, q, ids, kv_len, q_pos=pos, sel=sel))
+        jobs.append((job, torch.cuda.Stream()))
+    want = [job() for job, _ in jobs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (job, st) in enumerate(jobs):
+            with torch.cuda.stream(st):
+                got[i].append(job())
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, r))
+    assert h.status() == 0 and hh.status() == 0
+    hh.close()
+
+
 def test_capture_does_not_grow_scratch():
     import torch
     import split_kv_flash_attn_gb300 as skv
