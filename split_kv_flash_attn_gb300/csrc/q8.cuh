@@ -170,6 +170,7 @@ struct SelectArgs {
     int nq_ld, tok0;               // as in AttnArgs
     int n_sel, n_first, n_last;
     uint32_t *keys;                // scratch [S][nq][Hk][cap]
+    int *counters;                 // arrivals, zero between launches
     int32_t *sel;
 
     __host__ __device__ int64_t token(int s, int t) const { return static_cast<int64_t>(s) * nq_ld + tok0 + t; }

@@ -235,6 +235,7 @@ int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape
     const int nq_max = static_cast<int>(std::min<int64_t>(shape->nq, std::max<int64_t>(1, kPageScratch / per_token)));
     if ((rc = ensure_workspace(h, static_cast<size_t>(per_token) * nq_max, st))) return rc;
     a.keys = static_cast<uint32_t *>(h->workspace);
+    a.counters = h->counters;
     for (int t = 0; t < shape->nq; t += nq_max) {
         a.tok0 = t;
         a.nq = std::min(nq_max, shape->nq - t);

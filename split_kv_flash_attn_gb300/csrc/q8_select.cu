@@ -13,7 +13,8 @@
 // head, 8 columns at a time.
 //
 // The choice.  Scores become 32-bit keys whose order as unsigned numbers is the
-// scores' order; one CTA for each list finds the n-th largest key two bits at a
+// scores' order; one CTA for each list (a kernel of its own, or the last to score a
+// page of it) finds the n-th largest key two bits at a
 // time, counting keys in registers, and writes the picked indices in order by
 // prefix sums over the warps' equal shares.  Ties at the n-th key go to the lowest
 // indices.
@@ -75,179 +76,6 @@ struct Extremes {
             }
     }
 };
-
-// Grid: x pieces of a list's pages, `tg` tokens at a time dealt to `parts` CTAs, y KV
-// heads, z sequences.  The warps of a CTA take groups of 16 of its pages in turn, a
-// group's bytes a turn ahead.
-template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArgs a, int tg, int parts)
-{
-    constexpr int KS = D / 16, CH = D / 64;
-    __shared__ uint2 s_q[kScoreCols / 8][KS][32];         // coded queries in fragment order
-    __shared__ float s_dq[kScoreCols];
-    __shared__ int s_nb[kScoreCols];
-    __shared__ float s_f[kScoreWarps][16][kScoreCols + 1];
-    start();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int kh = blockIdx.y, s = blockIdx.z;
-    const int64_t len = list_len(a.L, s);
-    const int64_t nb = (len + kPage - 1) / kPage;
-    const int piece = blockIdx.x / parts, part = blockIdx.x - piece * parts;
-    const int64_t groups = (nb + 15) / 16, stride = static_cast<int64_t>(gridDim.x / parts) * kScoreWarps;
-    const int64_t group0 = static_cast<int64_t>(piece) * kScoreWarps + warp;
-    if (static_cast<int64_t>(piece) * kScoreWarps >= groups) return;
-    const int32_t *ids = a.L.ids + (static_cast<int64_t>(s) * a.L.Hk + kh) * a.L.cap;
-
-    // tokens in rounds whose columns fit; a token of more query heads than that
-    // takes several rounds
-    const int hg = min(a.G, kScoreCols);                  // heads a round
-    for (int t0 = part * tg; t0 < a.nq; t0 += parts * tg) {
-        const int nt = min(tg, a.nq - t0);
-        for (int h0 = 0; h0 < a.G; h0 += hg) {
-            const int nh = min(hg, a.G - h0);
-            const int cols = nt * nh, ncg = (cols + 7) / 8;
-            Extremes<D> nxt;
-            nxt.ids_of(a, ids, group0 * 16, group0 < groups ? nb : 0, g);
-            __syncthreads();                              // the last round's columns are read
-            // coded queries: a warp takes up to eight columns, their values requested together
-            constexpr int N = D / 32, CPW = kScoreCols / kScoreWarps;
-            uint2 raw[CPW];
-#pragma unroll
-            for (int e = 0; e < CPW; ++e) {
-                const int c = warp + e * kScoreWarps;
-                raw[e] = make_uint2(0, 0);
-                if (c < cols) {
-                    const int tok = t0 + c / nh, head = kh * a.G + h0 + c % nh;
-                    const __half *qp = a.q + (a.token(s, tok) * a.H + head) * D + lane * N;
-                    if constexpr (N == 4) raw[e] = __ldg(reinterpret_cast<const uint2 *>(qp));
-                    else raw[e].x = __ldg(reinterpret_cast<const uint32_t *>(qp));
-                }
-            }
-            if (tid < nt) {
-                // pages that hold a key the token sees
-                int64_t seen = len;
-                if (a.q_pos)
-                    seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + a.token(s, t0 + tid))) + 1));
-                s_nb[tid] = static_cast<int>((seen + kPage - 1) / kPage);
-            }
-#pragma unroll
-            for (int e = 0; e < CPW; ++e) {
-                const int c = warp + e * kScoreWarps;
-                if (c >= ncg * 8) break;
-                float v[N];
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const uint32_t w = i == 0 ? raw[e].x : raw[e].y;
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-                    v[i] = f.x;
-                    v[i + 1] = f.y;
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float m = fabsf(v[i]);
-                    top = fmaxf(top, m <= 65504.f ? m : 0.f);
-                }
-                // (magnitudes: their order is that of their bits)
-                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-                const float dq = over_127(top);
-                if (lane == 0) s_dq[c] = dq;
-                // the integer nearest v / dq: by the approximate reciprocal unless that
-                // comes within 2^-13 of a half-integer (its error is below 2^-14)
-                float rd;
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(dq));
-                bool sure = dq > 0.f;
-                float r[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float x = v[i] * rd;
-                    r[i] = rintf(x);
-                    sure = sure && fabsf(x - r[i]) < 0.5f - 0x1p-13f;
-                }
-                if (!sure) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) r[i] = dq > 0.f ? static_cast<float>(nearest_code(v[i], dq)) : 0.f;
-                }
-                __half hc[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) hc[i] = __float2half_rn(r[i]);
-                // channel d of column c: chunk d/64, t = d/16 % 4, word d/4 % 4, place d % 4
-                const int d = lane * N;
-                __half *dst = reinterpret_cast<__half *>(&s_q[c >> 3][(d >> 6) * 4 + ((d >> 2) & 3)][(c & 7) * 4 + ((d >> 4) & 3)]) + (d & 3);
-#pragma unroll
-                for (int i = 0; i < N; ++i) dst[i] = hc[i];
-            }
-            nxt.load(a, t);
-            __syncthreads();
-            for (int64_t gr = group0; gr < groups; gr += stride) {
-                const Extremes<D> cur = nxt;
-                // lane l finishes page l % 16
-                const int id0 = __shfl_sync(0xffffffffu, cur.id[0], (lane & 7) * 4);
-                const int id1 = __shfl_sync(0xffffffffu, cur.id[1], (lane & 7) * 4);
-                const int page_id = (lane & 8) ? id1 : id0;
-                const float page_scale = page_id >= 0 ? __ldg(a.k_scale + page_id) : 0.f;
-                if (gr + stride < groups) {
-                    nxt.ids_of(a, ids, (gr + stride) * 16, nb, g);
-                    nxt.load(a, t);
-                }
-                float acc[kScoreCols / 8][4];
-#pragma unroll
-                for (int j = 0; j < kScoreCols / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint4 &lo = cur.x[part][0][c], &hi = cur.x[part][1][c];
-                            const uint32_t x = (w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w) ^ 0x80808080u;
-                            const uint32_t y = (w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w) ^ 0x80808080u;
-                            const uint32_t a0 = codes_lo(x), a1 = codes_lo(y), a2 = codes_hi(x), a3 = codes_hi(y);
-                            const __half2 z = __half2half2(__ushort_as_half(0));
-#pragma unroll
-                            for (int j = 0; j < kScoreCols / 8; ++j) {
-                                if (j >= ncg) break;
-                                uint2 q = s_q[j][c * 4 + w][lane];
-                                __half2 q0 = *reinterpret_cast<__half2 *>(&q.x), q1 = *reinterpret_cast<__half2 *>(&q.y);
-                                q0 = part == 0 ? __hmax2(q0, z) : __hmin2(q0, z);
-                                q1 = part == 0 ? __hmax2(q1, z) : __hmin2(q1, z);
-                                mma_16816(acc[j], a0, a1, a2, a3, *reinterpret_cast<uint32_t *>(&q0),
-                                          *reinterpret_cast<uint32_t *>(&q1));
-                            }
-                        }
-#pragma unroll
-                for (int j = 0; j < kScoreCols / 8; ++j) {
-                    if (j >= ncg) break;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = j * 8 + 2 * t + (e & 1);
-                        s_f[warp][g + 8 * (e >> 1)][c] = __fmul_rn(acc[j][e], s_dq[c]);
-                    }
-                }
-                __syncwarp();
-                // (page, token): the largest of its heads
-                for (int x = lane; x < 16 * nt; x += 32) {
-                    const int b = x & 15, tok = x >> 4;   // b = lane & 15: the lane's own page
-                    float m = -INFINITY;
-                    for (int i = 0; i < nh; ++i) m = fmaxf(m, s_f[warp][b][tok * nh + i]);
-                    const int64_t blk = gr * 16 + b;
-                    if (blk >= nb) continue;
-                    const int64_t row = (static_cast<int64_t>(s) * a.nq + t0 + tok) * a.L.Hk + kh;
-                    uint32_t *out = a.keys + row * a.L.cap + blk;
-                    const int nbq = s_nb[tok];
-                    uint32_t key = kNever;
-                    if (page_id >= 0 && blk < nbq) {
-                        key = blk < a.n_first || blk >= nbq - a.n_last ? kAlways : order_key(__fmul_rn(m, page_scale));
-                        if (h0 > 0) key = page_scale >= 0.f ? max(key, *out) : min(key, *out);
-                    }
-                    *out = key;
-                }
-                __syncwarp();
-            }
-        }
-    }
-}
 
 // ---------------------------------------------------------------- the choice
 
@@ -467,7 +295,29 @@ auto for_cap(int64_t cap, F f)
     return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 0>());
 }
 
-// One CTA a row (sequence, token, KV head).
+// The choice for one row (sequence, token, KV head) of n candidate pages.
+template <int THREADS, int KPT>
+__device__ void pick_row(const uint32_t *src, int n, int n_sel, int32_t *out, PickScratch<THREADS> &sc)
+{
+    Keys<THREADS, KPT> keys(n, src);
+    if constexpr (KPT > 0) keys.fill([&](int i) { return __ldcg(src + i); });
+    // no more pages than places: all candidates; else the keys above the n-th and the
+    // first ties with it
+    const uint32_t T = n > n_sel ? threshold(keys, n_sel, sc) : kNever;
+    int need = 0, picked = 0;
+    in_order(
+        keys, T, sc,
+        [&](int above, int, int) {
+            need = T == kNever ? 0 : n_sel - above;
+            picked = above + need;
+        },
+        [&](int i, uint32_t k, int above, int ties, int) {
+            if (k > T || (k == T && ties < need)) out[above + min(ties, need)] = i;
+        });
+    for (int i = picked + threadIdx.x; i < n_sel; i += THREADS) out[i] = -1;
+}
+
+// One CTA a row.
 template <int THREADS, int KPT>
 __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a)
 {
@@ -479,25 +329,198 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(const SelectArgs a)
     const int64_t tok = a.token(s, static_cast<int>(st % a.nq));
     int64_t seen = list_len(a.L, s);
     if (a.q_pos) seen = max(int64_t(0), min(seen, static_cast<int64_t>(__ldg(a.q_pos + tok)) + 1));
-    const int n = static_cast<int>((seen + kPage - 1) / kPage);
-    const uint32_t *src = a.keys + row * a.L.cap;
-    int32_t *out = a.sel + (tok * a.L.Hk + row % a.L.Hk) * a.n_sel;
-    Keys<THREADS, KPT> keys(n, src);
-    if constexpr (KPT > 0) keys.fill([&](int i) { return __ldcg(src + i); });
-    // no more pages than places: all candidates; else the keys above the n-th and the
-    // first ties with it
-    const uint32_t T = n > a.n_sel ? threshold(keys, a.n_sel, sc) : kNever;
-    int need = 0, picked = 0;
-    in_order(
-        keys, T, sc,
-        [&](int above, int, int) {
-            need = T == kNever ? 0 : a.n_sel - above;
-            picked = above + need;
-        },
-        [&](int i, uint32_t k, int above, int ties, int) {
-            if (k > T || (k == T && ties < need)) out[above + min(ties, need)] = i;
-        });
-    for (int i = picked + threadIdx.x; i < a.n_sel; i += THREADS) out[i] = -1;
+    pick_row<THREADS, KPT>(a.keys + row * a.L.cap, static_cast<int>((seen + kPage - 1) / kPage), a.n_sel,
+                           a.sel + (tok * a.L.Hk + row % a.L.Hk) * a.n_sel, sc);
+}
+
+// ------------------------------------------------------- the bounds of all pages
+
+// Grid: x pieces of a list's pages, `tg` tokens at a time dealt to `parts` CTAs, y KV
+// heads, z sequences.  The warps of a CTA take groups of 16 of its pages in turn, a
+// group's bytes a turn ahead.  KPT > 0 (one token a sequence, lists of up to KPT pages a
+// thread): the last CTA of a list makes its choice.
+template <int D, int KPT>
+__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArgs a, int tg, int parts)
+{
+    constexpr int KS = D / 16, CH = D / 64;
+    __shared__ uint2 s_q[kScoreCols / 8][KS][32];         // coded queries in fragment order
+    __shared__ float s_dq[kScoreCols];
+    __shared__ int s_nb[kScoreCols];
+    __shared__ float s_f[kScoreWarps][16][kScoreCols + 1];
+    start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int kh = blockIdx.y, s = blockIdx.z;
+    const int64_t len = list_len(a.L, s);
+    const int64_t nb = (len + kPage - 1) / kPage;
+    const int piece = blockIdx.x / parts, part = blockIdx.x - piece * parts;
+    const int64_t groups = (nb + 15) / 16, stride = static_cast<int64_t>(gridDim.x / parts) * kScoreWarps;
+    const int64_t group0 = static_cast<int64_t>(piece) * kScoreWarps + warp;
+    if (static_cast<int64_t>(piece) * kScoreWarps >= groups && (KPT == 0 || piece > 0)) return;
+    const int32_t *ids = a.L.ids + (static_cast<int64_t>(s) * a.L.Hk + kh) * a.L.cap;
+
+    // tokens in rounds whose columns fit; a token of more query heads than that
+    // takes several rounds
+    const int hg = min(a.G, kScoreCols);                  // heads a round
+    for (int t0 = part * tg; t0 < a.nq; t0 += parts * tg) {
+        const int nt = min(tg, a.nq - t0);
+        for (int h0 = 0; h0 < a.G; h0 += hg) {
+            const int nh = min(hg, a.G - h0);
+            const int cols = nt * nh, ncg = (cols + 7) / 8;
+            Extremes<D> nxt;
+            nxt.ids_of(a, ids, group0 * 16, group0 < groups ? nb : 0, g);
+            __syncthreads();                              // the last round's columns are read
+            // coded queries: a warp takes up to eight columns, their values requested together
+            constexpr int N = D / 32, CPW = kScoreCols / kScoreWarps;
+            uint2 raw[CPW];
+#pragma unroll
+            for (int e = 0; e < CPW; ++e) {
+                const int c = warp + e * kScoreWarps;
+                raw[e] = make_uint2(0, 0);
+                if (c < cols) {
+                    const int tok = t0 + c / nh, head = kh * a.G + h0 + c % nh;
+                    const __half *qp = a.q + (a.token(s, tok) * a.H + head) * D + lane * N;
+                    if constexpr (N == 4) raw[e] = __ldg(reinterpret_cast<const uint2 *>(qp));
+                    else raw[e].x = __ldg(reinterpret_cast<const uint32_t *>(qp));
+                }
+            }
+            if (tid < nt) {
+                // pages that hold a key the token sees
+                int64_t seen = len;
+                if (a.q_pos)
+                    seen = max(int64_t(0), min(len, static_cast<int64_t>(__ldg(a.q_pos + a.token(s, t0 + tid))) + 1));
+                s_nb[tid] = static_cast<int>((seen + kPage - 1) / kPage);
+            }
+#pragma unroll
+            for (int e = 0; e < CPW; ++e) {
+                const int c = warp + e * kScoreWarps;
+                if (c >= ncg * 8) break;
+                float v[N];
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const uint32_t w = i == 0 ? raw[e].x : raw[e].y;
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                    v[i] = f.x;
+                    v[i + 1] = f.y;
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float m = fabsf(v[i]);
+                    top = fmaxf(top, m <= 65504.f ? m : 0.f);
+                }
+                // (magnitudes: their order is that of their bits)
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                const float dq = over_127(top);
+                if (lane == 0) s_dq[c] = dq;
+                // the integer nearest v / dq: by the approximate reciprocal unless that
+                // comes within 2^-13 of a half-integer (its error is below 2^-14)
+                float rd;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(dq));
+                bool sure = dq > 0.f;
+                float r[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float x = v[i] * rd;
+                    r[i] = rintf(x);
+                    sure = sure && fabsf(x - r[i]) < 0.5f - 0x1p-13f;
+                }
+                if (!sure) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) r[i] = dq > 0.f ? static_cast<float>(nearest_code(v[i], dq)) : 0.f;
+                }
+                __half hc[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) hc[i] = __float2half_rn(r[i]);
+                // channel d of column c: chunk d/64, t = d/16 % 4, word d/4 % 4, place d % 4
+                const int d = lane * N;
+                __half *dst = reinterpret_cast<__half *>(&s_q[c >> 3][(d >> 6) * 4 + ((d >> 2) & 3)][(c & 7) * 4 + ((d >> 4) & 3)]) + (d & 3);
+#pragma unroll
+                for (int i = 0; i < N; ++i) dst[i] = hc[i];
+            }
+            nxt.load(a, t);
+            __syncthreads();
+            for (int64_t gr = group0; gr < groups; gr += stride) {
+                const Extremes<D> cur = nxt;
+                // lane l finishes page l % 16
+                const int id0 = __shfl_sync(0xffffffffu, cur.id[0], (lane & 7) * 4);
+                const int id1 = __shfl_sync(0xffffffffu, cur.id[1], (lane & 7) * 4);
+                const int page_id = (lane & 8) ? id1 : id0;
+                const float page_scale = page_id >= 0 ? __ldg(a.k_scale + page_id) : 0.f;
+                if (gr + stride < groups) {
+                    nxt.ids_of(a, ids, (gr + stride) * 16, nb, g);
+                    nxt.load(a, t);
+                }
+                float acc[kScoreCols / 8][4];
+#pragma unroll
+                for (int j = 0; j < kScoreCols / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint4 &lo = cur.x[part][0][c], &hi = cur.x[part][1][c];
+                            const uint32_t x = (w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w) ^ 0x80808080u;
+                            const uint32_t y = (w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w) ^ 0x80808080u;
+                            const uint32_t a0 = codes_lo(x), a1 = codes_lo(y), a2 = codes_hi(x), a3 = codes_hi(y);
+                            const __half2 z = __half2half2(__ushort_as_half(0));
+#pragma unroll
+                            for (int j = 0; j < kScoreCols / 8; ++j) {
+                                if (j >= ncg) break;
+                                uint2 q = s_q[j][c * 4 + w][lane];
+                                __half2 q0 = *reinterpret_cast<__half2 *>(&q.x), q1 = *reinterpret_cast<__half2 *>(&q.y);
+                                q0 = part == 0 ? __hmax2(q0, z) : __hmin2(q0, z);
+                                q1 = part == 0 ? __hmax2(q1, z) : __hmin2(q1, z);
+                                mma_16816(acc[j], a0, a1, a2, a3, *reinterpret_cast<uint32_t *>(&q0),
+                                          *reinterpret_cast<uint32_t *>(&q1));
+                            }
+                        }
+#pragma unroll
+                for (int j = 0; j < kScoreCols / 8; ++j) {
+                    if (j >= ncg) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = j * 8 + 2 * t + (e & 1);
+                        s_f[warp][g + 8 * (e >> 1)][c] = __fmul_rn(acc[j][e], s_dq[c]);
+                    }
+                }
+                __syncwarp();
+                // (page, token): the largest of its heads
+                for (int x = lane; x < 16 * nt; x += 32) {
+                    const int b = x & 15, tok = x >> 4;   // b = lane & 15: the lane's own page
+                    float m = -INFINITY;
+                    for (int i = 0; i < nh; ++i) m = fmaxf(m, s_f[warp][b][tok * nh + i]);
+                    const int64_t blk = gr * 16 + b;
+                    if (blk >= nb) continue;
+                    const int64_t row = (static_cast<int64_t>(s) * a.nq + t0 + tok) * a.L.Hk + kh;
+                    uint32_t *out = a.keys + row * a.L.cap + blk;
+                    const int nbq = s_nb[tok];
+                    uint32_t key = kNever;
+                    if (page_id >= 0 && blk < nbq) {
+                        key = blk < a.n_first || blk >= nbq - a.n_last ? kAlways : order_key(__fmul_rn(m, page_scale));
+                        if (h0 > 0) key = page_scale >= 0.f ? max(key, *out) : min(key, *out);
+                    }
+                    *out = key;
+                }
+                __syncwarp();
+            }
+        }
+    }
+    if constexpr (KPT > 0) {
+        constexpr int kThreads = kScoreWarps * 32;
+        static_assert(sizeof(PickScratch<kThreads>) <= sizeof(s_f), "in the place of the scores");
+        const int list = s * a.L.Hk + kh;
+        const int pieces = static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(gridDim.x), (groups + kScoreWarps - 1) / kScoreWarps)));
+        __threadfence();
+        __syncthreads();
+        if (!__syncthreads_or(tid == 0 && atomicAdd(a.counters + list, 1) == pieces - 1)) return;
+        if (tid == 0) a.counters[list] = 0;
+        __threadfence();
+        pick_row<kThreads, KPT>(a.keys + static_cast<int64_t>(list) * a.L.cap, s_nb[0], a.n_sel,
+                                a.sel + (a.token(s, 0) * a.L.Hk + kh) * a.n_sel,
+                                *reinterpret_cast<PickScratch<kThreads> *>(&s_f));
+    }
 }
 
 int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
@@ -514,9 +537,17 @@ int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
     tg = std::min(tg, static_cast<int>((a.nq + deal - 1) / deal));
     const int parts = static_cast<int>(std::min<int64_t>(deal, (a.nq + tg - 1) / tg));
     const dim3 grid(static_cast<unsigned>(pieces * parts), a.L.Hk, a.L.S);
-    cudaError_t e = D == 128 ? launch(score_kernel<128>, grid, kScoreWarps * 32, 0, st, a, tg, parts)
-                             : launch(score_kernel<64>, grid, kScoreWarps * 32, 0, st, a, tg, parts);
+    // One token a sequence and short lists: the choice by the last CTA of a list's scores.
+    // As fast on the GPU (16 of 128 pages, with the attention: 18.6 against 18.4 us), and
+    // one launch less on the host (25 against 30 us a step).  By one CTA of 256 threads
+    // longer lists take longer (512 of 4096 pages: 67 against 53 us).
+    constexpr int kFused = 4;
+    const bool fused = a.nq == 1 && a.L.cap <= kFused * kScoreWarps * 32 && lists <= kMaxUnits;
+    const auto kernel = D == 128 ? (fused ? score_kernel<128, kFused> : score_kernel<128, 0>)
+                                 : (fused ? score_kernel<64, kFused> : score_kernel<64, 0>);
+    cudaError_t e = launch(kernel, grid, kScoreWarps * 32, 0, st, a, tg, parts);
     if (e != cudaSuccess) return cuda_fail(h, e, "page score launch");
+    if (fused) return SKV_OK;
     const dim3 rows(static_cast<unsigned>(static_cast<int64_t>(a.L.S) * a.nq * a.L.Hk));
     e = for_cap(a.L.cap, [&](auto threads, auto kpt) {
         return launch(pick_kernel<threads.value, kpt.value>, rows, threads.value, 0, st, a);

@@ -346,7 +346,10 @@ def test_weights_in_several_launches(h, G, nq, sel):
     ([1000], 1, 4, 1, 128, 4, 1, 1, False), ([5000, 64, 0, 1], 1, 8, 2, 64, 16, 0, 0, False),
     ([777, 2500], 3, 10, 2, 128, 7, 2, 2, True), ([300], 20, 4, 4, 64, 3, 1, 2, True),
     ([4096], 1, 80, 1, 64, 10, 0, 1, False), ([64 * 2000], 1, 2, 1, 64, 300, 1, 1, False), ([64 * 7000 - 3], 1, 1, 1, 64, 77, 0, 1, False),
-    ([64 * 17000], 1, 1, 1, 64, 2000, 1, 2, False), ([130], 2, 8, 8, 128, 8, 1, 1, True), ([9000], 1, 2, 2, 128, 1, 0, 1, False)])
+    ([64 * 17000], 1, 1, 1, 64, 2000, 1, 2, False), ([130], 2, 8, 8, 128, 8, 1, 1, True), ([9000], 1, 2, 2, 128, 1, 0, 1, False),
+    # lists at the border of what the last CTA of the scores chooses from, one of them empty, and more heads than it takes at once
+    ([64 * 4092, 0, 64 * 3000 - 1], 1, 4, 2, 128, 500, 1, 1, False), ([64 * 4095], 1, 1, 1, 64, 4000, 0, 1, False),
+    ([64 * 900, 5], 1, 130, 1, 64, 20, 0, 0, True)])
 def test_selection(h, lens, nq, H, Hk, D, n, first, last, causal):
     import split_kv_flash_attn_gb300 as skv
     rng = np.random.default_rng(sum(lens) + n)
