@@ -1,8 +1,8 @@
 // q8_append.cu -- writing tokens into 8-bit pages.
 //
 // One CTA for each (page touched, K or V, KV head, sequence).  It holds the
-// page's new values in registers (at most 64 rows of D: 8 values of up to 4
-// rows a thread), takes their largest magnitude, d' = max(d, fp32(amax/127)),
+// page's new values in registers (at most 64 rows of D: 8 values of 4 or 8 rows
+// a thread), takes their largest magnitude, d' = max(d, fp32(amax/127)),
 // and writes the codes nearest x/d' and, for K, the channels' smallest and
 // largest codes.  Only when d' > d and the page holds earlier tokens are those
 // read and recoded, through a table of the 255 codes (one fp64 division each:
@@ -17,10 +17,10 @@
 // with a 4096-token prompt.
 //
 // Bound: a token's append is two dependent reads (length, page id) and one write deep
-// (4.1 us for 32 sequences); a prompt's is bound by its instructions, close to 20
-// of a warp for 32 values (two prompts of 4096 tokens, eight heads of D = 128: 15.4 us from
-// fp16, 3.3 TB/s, and 17.2 from fp32, 4.9 TB/s; x read once, codes written once).
-// Four CTAs a SM: three or two took 18.7 and 23 us from fp32.
+// (4.0 us for 32 sequences); a prompt's is bound by its instructions, close to 20
+// of a warp for 32 values (two prompts of 4096 tokens, eight heads of D = 128: 14.7 us from
+// fp16, 3.5 TB/s, and 16.9 from fp32, 5.0 TB/s; x read once, codes written once).
+// 1024 threads a SM: three quarters and half of that took 18.7 and 23 us from fp32.
 #include <algorithm>
 
 #include "q8.cuh"
@@ -28,7 +28,10 @@
 namespace skv {
 namespace q8 {
 
-constexpr int kAppendThreads = 256;
+// Threads of a CTA.  The same bytes as four prompts of 4096 tokens with D = 64 took 21.5
+// us (fp16) and 22.8 (fp32) with 256 threads, 14.7 and 15.9 with 128; with D = 128 fp16
+// rows 15.5 with 256 and 14.7 with 128, fp32 rows 16.9 and 27.5 (64 registers of rows).
+__host__ __device__ constexpr int append_threads(int D, bool f16) { return f16 ? 128 : 2 * D; }
 
 struct AppendArgs {
     Lists L;
@@ -113,14 +116,15 @@ __device__ __forceinline__ uint32_t recode4(const int8_t *lut, uint32_t w)
 }
 
 template <int D, typename X>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(append_threads(D, sizeof(X) == 2), 1024 / append_threads(D, sizeof(X) == 2)) append_kernel(const AppendArgs a)
 {
+    constexpr int kThreads = append_threads(D, sizeof(X) == 2);
     constexpr int TPR = D / 8;                       // threads a row
-    constexpr int RPP = kAppendThreads / TPR;        // rows a pass
+    constexpr int RPP = kThreads / TPR;        // rows a pass
     constexpr int PASSES = kPage / RPP;
-    __shared__ float s_max[kAppendThreads / 32];
+    __shared__ float s_max[kThreads / 32];
     __shared__ int8_t s_lut[256];
-    __shared__ uint32_t s_lo[kAppendThreads / 32][TPR][2], s_hi[kAppendThreads / 32][TPR][2];
+    __shared__ uint32_t s_lo[kThreads / 32][TPR][2], s_hi[kThreads / 32][TPR][2];
     start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // (heads side by side: their rows of a token are neighbours in memory)
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
     if (lane == 0) s_max[warp] = amax;
     const bool any_odd = __syncthreads_or(odd);
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
     const float d1 = fmaxf(d0, over_127(amax));
     const bool recode = r_lo > 0 && d1 != d0;
     const bool plain = !any_odd && d1 >= 0x1p-100f;                         // every value finite, d' not tiny
@@ -262,11 +266,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
         }
     }
     if (recode) {
-        const int c = static_cast<int8_t>(tid);
-        double t = d1 > 0.f ? rint(static_cast<double>(c) * static_cast<double>(d0) / static_cast<double>(d1)) : 0.0;
-        s_lut[tid] = static_cast<int8_t>(fmin(fmax(t, -127.0), 127.0));
+        for (int i = tid; i < 256; i += kThreads) {
+            const int c = static_cast<int8_t>(i);
+            const double t = d1 > 0.f ? rint(static_cast<double>(c) * static_cast<double>(d0) / static_cast<double>(d1)) : 0.0;
+            s_lut[i] = static_cast<int8_t>(fmin(fmax(t, -127.0), 127.0));
+        }
         __syncthreads();
-        for (int i = tid; i < r_lo * TPR; i += kAppendThreads) {
+        for (int i = tid; i < r_lo * TPR; i += kThreads) {
             const uint2 w = *reinterpret_cast<const uint2 *>(page + i * 8);
             *reinterpret_cast<uint2 *>(page + i * 8) = make_uint2(recode4(s_lut, w.x), recode4(s_lut, w.y));
         }
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendA
         const int c = tid >> 1, e = tid & 1;
         uint32_t l = s_lo[0][c][e], m = s_hi[0][c][e];
 #pragma unroll
-        for (int w = 1; w < kAppendThreads / 32; ++w) {
+        for (int w = 1; w < kThreads / 32; ++w) {
             l = __vmins4(l, s_lo[w][c][e]);
             m = __vmaxs4(m, s_hi[w][c][e]);
         }
@@ -340,12 +346,13 @@ int launch_append(skv_handle *h, const skv_q8_pool &pool, const Lists &L, int n_
     for (a.page0 = 0; a.page0 < blocks; a.page0 += most) {
         const dim3 grid(L.Hk, static_cast<unsigned>(2 * std::min(most, blocks - a.page0)), L.S);
         cudaError_t e;
+        const int threads = append_threads(pool.D, x_type == SKV_F16);
         if (x_type == SKV_F32)
-            e = pool.D == 128 ? launch(append_kernel<128, float>, grid, kAppendThreads, 0, st, a)
-                              : launch(append_kernel<64, float>, grid, kAppendThreads, 0, st, a);
+            e = pool.D == 128 ? launch(append_kernel<128, float>, grid, threads, 0, st, a)
+                              : launch(append_kernel<64, float>, grid, threads, 0, st, a);
         else
-            e = pool.D == 128 ? launch(append_kernel<128, __half>, grid, kAppendThreads, 0, st, a)
-                              : launch(append_kernel<64, __half>, grid, kAppendThreads, 0, st, a);
+            e = pool.D == 128 ? launch(append_kernel<128, __half>, grid, threads, 0, st, a)
+                              : launch(append_kernel<64, __half>, grid, threads, 0, st, a);
         if (e != cudaSuccess) return cuda_fail(h, e, "8-bit append launch");
     }
     return SKV_OK;
