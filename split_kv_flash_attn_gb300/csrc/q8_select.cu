@@ -20,11 +20,11 @@
 // indices.
 //
 // Bound (select and attend over 16 of 128 pages: 18 us, of which 9 here; 512 of 4096
-// pages of 16 lists: 53 and 19): the scores by latency (lengths, ids, extremes and
+// pages of 16 lists: 52 and 18): the scores by latency (lengths, ids, extremes and
 // queries are read one after the other, 2D + 8 bytes a page and head in all); the
 // choice by its counting rounds, each one pass over registers and one barrier, three or four until
-// few keys are left to each warp alone (without that 12 rounds: 13.4 against 10.3 us
-// for 64 lists of 2048 pages).
+// few keys are left to each warp alone (cutting 64 lists of up to 2048 pages to 512 took
+// 13.4 us with 12 rounds, 10.3 so, and 9.0 since a warp ends a round at its last key).
 #include <algorithm>
 #include <type_traits>
 
@@ -101,8 +101,10 @@ struct Keys {
         const int lane = threadIdx.x & 31;
         if constexpr (KPT > 0) {
 #pragma unroll
-            for (int e = 0; e < KPT; ++e)
-                if (lo + 32 * e < hi) f(lo + 32 * e + lane, k[e], lo + 32 * e + lane < hi);
+            for (int e = 0; e < KPT; ++e) {
+                if (lo + 32 * e >= hi) break;
+                f(lo + 32 * e + lane, k[e], lo + 32 * e + lane < hi);
+            }
         } else {
             for (int i = lo; i < hi; i += 32) f(i + lane, i + lane < hi ? at[i + lane] : 0u, i + lane < hi);
         }
@@ -540,7 +542,7 @@ int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
     // One token a sequence and short lists: the choice by the last CTA of a list's scores.
     // As fast on the GPU (16 of 128 pages, with the attention: 18.6 against 18.4 us), and
     // one launch less on the host (25 against 30 us a step).  By one CTA of 256 threads
-    // longer lists take longer (512 of 4096 pages: 67 against 53 us).
+    // longer lists take longer (512 of 4096 pages: 67 us with the attention, 52 by a kernel of 512 threads).
     constexpr int kFused = 4;
     const bool fused = a.nq == 1 && a.L.cap <= kFused * kScoreWarps * 32 && lists <= kMaxUnits;
     const auto kernel = D == 128 ? (fused ? score_kernel<128, kFused> : score_kernel<128, 0>)
