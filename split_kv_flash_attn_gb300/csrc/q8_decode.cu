@@ -39,9 +39,9 @@
 // the eight query columns of a product carry a KV head's query heads.
 //
 // Bound: the pages' bytes at long lengths (one sequence over 1048576 keys, eight KV
-// heads of D = 128: 323 us, 6.65 TB/s; eight sequences of up to 32768: 61 us, 5.2 TB/s,
+// heads of D = 128: 320 us, 6.7 TB/s; eight sequences of up to 32768: 61 us, 5.2 TB/s,
 // DRAM reads 316 MB, which is the pages); launch, look-ups and joins at short ones
-// (256 keys: 5.9 us).
+// (256 keys: 5.6 us).
 #include "q8.cuh"
 
 namespace skv {
@@ -54,7 +54,7 @@ constexpr uint32_t kStraddle = 8;   // pages that a second start and join of a C
 
 // Computing warps and ring slots.  One column group: eight sequences of up to 32768
 // keys take 61 us with 11 and 11, 63 with 7 and 7 or 8 and 8, 68 with 6 and 12 (one
-// of 1048576: 323, 334, 340 and 367); two groups need the registers of 7 warps.
+// of 1048576: 320, 334, 340 and 367); two groups need the registers of 7 warps.
 __host__ __device__ constexpr int warps_of(int nc) { return nc == 1 ? 11 : 7; }
 __host__ __device__ constexpr int slots_of(int nc) { return nc == 1 ? 11 : 7; }
 template <int D, int NC>
@@ -114,6 +114,10 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_lists = a.sel ? a.L.S * a.nq : a.L.S;
     const uint32_t mult = a.L.Hk * a.row_groups;    // units per list
+    if (tid == kConsumers) {
+        tc::prefetch_tmap(&map_k);
+        tc::prefetch_tmap(&map_v);
+    }
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < 2 * NS; ++i) tc::mbar_init(bar0 + 8 * i, i < NS ? 1 : 2);
@@ -292,16 +296,16 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 const Meta cur = nxt;
                 if (first + 32 < x.pg1) nxt = load_meta(first + 32);
                 const int n = min(32, x.pg1 - first);
-                // the CTA's first pages go out before their scales are there; they are
-                // announced below
+                // the CTA's first pages go out before their scales are there, K and V by
+                // neighbouring lanes (one lane took 60 ns a copy); they are announced below
                 const int early = n_put == 0 ? min(n, NS) : 0;
-                for (int i = 0; i < early; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, cur.id, i);
-                    if (id >= 0 && lane == 0) {
-                        const uint32_t dst = smem_addr(ring + i * 2 * BYTES), full = bar0 + 8 * i;
-                        tc::mbar_expect_tx_only(full, 2 * BYTES);
-                        tc::tma_load_3d(dst, &map_k, 0, 0, id, full);
-                        tc::tma_load_3d(dst + BYTES, &map_v, 0, 0, id, full);
+                if (early) {                        // lanes 2i and 2i + 1: K and V of page i
+                    static_assert(2 * NS <= 32, "a lane for each copy");
+                    const int id = __shfl_sync(0xffffffffu, cur.id, lane >> 1);
+                    if (lane < 2 * early && id >= 0) {
+                        const uint32_t full = bar0 + 8 * (lane >> 1);
+                        if ((lane & 1) == 0) tc::mbar_expect_tx_only(full, 2 * BYTES);
+                        tc::tma_load_3d(smem_addr(ring + lane * BYTES), (lane & 1) ? &map_v : &map_k, 0, 0, id, full);
                     }
                 }
                 // (64 entries: those of the 32 pages before are still in use, at
