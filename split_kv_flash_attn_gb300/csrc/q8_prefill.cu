@@ -870,15 +870,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     }
 }
 
-// Rows of units that several CTAs share: their pieces together, in order.  D / 4
-// lanes a row, kMergeRows rows a thread.
+// Rows of units that several CTAs share: their pieces together.  D / 4 lanes a row,
+// kMergeRows rows a thread.  DEEP = false: all pieces in order; true: every warp of a CTA
+// the same rows and batches of four pieces in turn, then the warps' sums in order.
 constexpr int kMergeRows = 4;
-template <int D>
+template <int D, bool DEEP>
 __global__ void __launch_bounds__(256, 2) prefill_merge_kernel(const PrefillArgs pa)
 {
     start();
     const AttnArgs &a = pa.a;
-    constexpr int LPR = D / 4, RPP = 256 / LPR;
+    constexpr int LPR = D / 4, RPP = (DEEP ? 32 : 256) / LPR;
+    constexpr int kWarps = 8;
     const int np = pa.n_pairs;
     const int unit = blockIdx.y, list = unit / np, pr = unit - list * np;
     const int s = list / a.L.Hk, kh = list - s * a.L.Hk;
@@ -895,13 +897,13 @@ __global__ void __launch_bounds__(256, 2) prefill_merge_kernel(const PrefillArgs
     int rr[kMergeRows];                         // rows of the unit
 #pragma unroll
     for (int i = 0; i < kMergeRows; ++i) {
-        rr[i] = (blockIdx.x * kMergeRows + i) * RPP + threadIdx.x / LPR;
+        rr[i] = (blockIdx.x * kMergeRows + i) * RPP + (DEEP ? threadIdx.x & 31 : threadIdx.x) / LPR;
         M[i] = -INFINITY;
         W[i] = v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
     }
     // pieces four at a time, all their loads before any use
 #pragma unroll 1
-    for (uint32_t c0 = c_lo; c0 <= c_hi; c0 += 4) {
+    for (uint32_t c0 = c_lo + (DEEP ? threadIdx.x / 32 * 4 : 0); c0 <= c_hi; c0 += DEEP ? kWarps * 4 : 4) {
         float z[kMergeRows][4];
         float4 y[kMergeRows][4];
 #pragma unroll
@@ -930,19 +932,52 @@ __global__ void __launch_bounds__(256, 2) prefill_merge_kernel(const PrefillArgs
                 v[i][3] = fmaf(v[i][3], bo, bn * y[i][e].w);
             }
     }
-#pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
-        const int row = pr * 2 * kPM + rr[i];
-        if (row >= a.rows || rr[i] >= 2 * kPM) continue;
-        const float q = W[i] == 0.f ? 0.f : 1.f / W[i];
+    auto write = [&](int r_unit, float Mr, float Wr, const float (&vr)[4]) {
+        const int row = pr * 2 * kPM + r_unit;
+        if (row >= a.rows || r_unit >= 2 * kPM) return;
+        const float q = Wr == 0.f ? 0.f : 1.f / Wr;
         const int64_t r = a.token(s, row / a.G) * a.H + kh * a.G + row % a.G;
         if (pa.out_f16)
             *reinterpret_cast<uint2 *>(static_cast<__half *>(a.o) + r * D + lane * 4) =
-                make_uint2(pack_half2(v[i][0] * q, v[i][1] * q), pack_half2(v[i][2] * q, v[i][3] * q));
+                make_uint2(pack_half2(vr[0] * q, vr[1] * q), pack_half2(vr[2] * q, vr[3] * q));
         else
             *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + r * D + lane * 4) =
-                make_float4(v[i][0] * q, v[i][1] * q, v[i][2] * q, v[i][3] * q);
-        if (lane == 0) a.lse[r] = W[i] == 0.f ? -INFINITY : (M[i] + log2f(W[i])) * 0.6931471805599453f;
+                make_float4(vr[0] * q, vr[1] * q, vr[2] * q, vr[3] * q);
+        if (lane == 0) a.lse[r] = Wr == 0.f ? -INFINITY : (Mr + log2f(Wr)) * 0.6931471805599453f;
+    };
+    if constexpr (!DEEP) {
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) write(rr[i], M[i], W[i], v[i]);
+    } else {
+        constexpr int kRows = kMergeRows * RPP; // of the CTA
+        __shared__ float s_m[kWarps][kRows], s_w[kWarps][kRows];
+        __shared__ float4 s_v[kWarps][kRows][LPR];
+        const int warp = threadIdx.x / 32, sub = (threadIdx.x & 31) / LPR;
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+            if (lane == 0) {
+                s_m[warp][i * RPP + sub] = M[i];
+                s_w[warp][i * RPP + sub] = W[i];
+            }
+            s_v[warp][i * RPP + sub][lane] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        }
+        __syncthreads();
+        const int rl = threadIdx.x / LPR;
+        if (rl >= kRows) return;
+        float Mr = -INFINITY, Wr = 0.f, vr[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) Mr = fmaxf(Mr, s_m[w][rl]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float b = s_m[w][rl] == -INFINITY ? 0.f : fast_exp2(s_m[w][rl] - Mr);
+            const float4 y = s_v[w][rl][lane];
+            Wr = fmaf(s_w[w][rl], b, Wr);
+            vr[0] = fmaf(y.x, b, vr[0]);
+            vr[1] = fmaf(y.y, b, vr[1]);
+            vr[2] = fmaf(y.z, b, vr[2]);
+            vr[3] = fmaf(y.w, b, vr[3]);
+        }
+        write(blockIdx.x * kRows + rl, Mr, Wr, vr);
     }
 }
 
@@ -983,8 +1018,14 @@ static int launch_one(skv_handle *h, const PrefillArgs &pa, int grid, cudaStream
     if (l != cudaSuccess) return cuda_fail(h, l, "8-bit prefill launch");
     const int units = pa.a.L.S * pa.a.L.Hk * pa.n_pairs;
     const int rows = std::min(2 * kPM, pa.a.rows);
-    return cuda_fail(h, launch(prefill_merge_kernel<D>, dim3((rows * (D / 4) + 256 * kMergeRows - 1) / (256 * kMergeRows), units), 256, 0, st, pa),
-                     "8-bit prefill merge launch");
+    // Pieces of a unit, flat against deep: one unit of 108 rows and 140669 keys (138 pieces)
+    // 61 / 34 us the call, four over 100000 keys (38) 61 / 53, eight over 32768 (19)
+    // 48.4 / 49.1, sixteen (10) 73 / 80.
+    const bool deep = grid > 24 * units;
+    const int per_cta = (deep ? 32 : 256) * kMergeRows;
+    const dim3 ctas((rows * (D / 4) + per_cta - 1) / per_cta, units);
+    return cuda_fail(h, deep ? launch(prefill_merge_kernel<D, true>, ctas, 256, 0, st, pa)
+                             : launch(prefill_merge_kernel<D, false>, ctas, 256, 0, st, pa), "8-bit prefill merge launch");
 }
 
 int launch_prefill(skv_handle *h, const AttnArgs &a, int D, bool f16, uint32_t *plan, int n_pairs, float *mass, int grid,

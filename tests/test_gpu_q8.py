@@ -165,6 +165,8 @@ PREFILL = [
     ([65] * 1100, 33, 1, 1, 64, False),
     # units of more tiles than fp32 results take at a time, one or less of them a CTA
     ([1300, 2500] + [1300] * 38, 33, 4, 4, 64, True), ([1400] * 20, 33, 8, 8, 128, False),
+    # few units of many pieces
+    ([30000], 34, 3, 1, 128, True), ([17000, 0, 9000], 40, 2, 1, 64, True),
 ]
 
 
