@@ -312,32 +312,29 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 // most NS of them not taken yet)
                 if (lane < n) s_meta[(n_put + lane) % 64] = Meta{cur.id, cur.blk, cur.ks * a.scale_log2, cur.vs};
                 __syncwarp();
-                if (lane == 0) {
-                    for (int i = 0; i < n; ++i) {
-                        const uint32_t m = n_put + i, slot = m % NS, turn = m / NS;
-                        const uint32_t full = bar0 + 8 * slot, empty = bar0 + 8 * (NS + slot);
-                        if (i < early) {
-                            tc::mbar_arrive(full);
-                            continue;
-                        }
-                        if (turn > 0 && !wait(empty, (turn - 1) & 1)) {
-                            ok = false;
-                            n_put = m - n;          // (+ n below)
-                            break;
-                        }
+                // two pages at a time, a lane for each copy (by one lane the pages of D = 64
+                // took 300 ns each, more than their bytes)
+                int done = 0;
+                for (; done < n; done += 2) {
+                    const int i = done + (lane >> 1);
+                    const bool mine = lane < 4 && i < n;
+                    const uint32_t m = n_put + i, slot = m % NS, turn = m / NS;
+                    const uint32_t full = bar0 + 8 * slot, empty = bar0 + 8 * (NS + slot);
+                    ok = __all_sync(0xffffffffu, !mine || turn == 0 || wait(empty, (turn - 1) & 1));
+                    if (!ok) break;
+                    if (mine) {
                         const int id = s_meta[m % 64].id;
-                        if (id >= 0) {
-                            const uint32_t dst = smem_addr(ring + slot * 2 * BYTES);
-                            tc::mbar_expect_tx(full, 2 * BYTES);
-                            tc::tma_load_3d(dst, &map_k, 0, 0, id, full);
-                            tc::tma_load_3d(dst + BYTES, &map_v, 0, 0, id, full);
-                        } else {
-                            tc::mbar_arrive(full);
+                        const bool copy = id >= 0 && i >= early;
+                        if ((lane & 1) == 0) {
+                            if (copy) tc::mbar_expect_tx(full, 2 * BYTES);
+                            else tc::mbar_arrive(full);
                         }
+                        if (copy)
+                            tc::tma_load_3d(smem_addr(ring + (2 * slot + (lane & 1)) * BYTES), (lane & 1) ? &map_v : &map_k, 0, 0, id, full);
                     }
+                    __syncwarp();
                 }
-                n_put += n;
-                ok = __all_sync(0xffffffffu, ok);
+                n_put += min(done, n);
             }
             pos = x.next;
         }
