@@ -39,9 +39,9 @@
 // the eight query columns of a product carry a KV head's query heads.
 //
 // Bound: the pages' bytes at long lengths (one sequence over 1048576 keys, eight KV
-// heads of D = 128: 320 us, 6.7 TB/s; eight sequences of up to 32768: 61 us, 5.2 TB/s,
+// heads of D = 128: 316 us, 6.8 TB/s; eight sequences of up to 32768: 60 us, 5.3 TB/s,
 // DRAM reads 316 MB, which is the pages); launch, look-ups and joins at short ones
-// (256 keys: 5.6 us).
+// (256 keys: 5.7 us).
 #include "q8.cuh"
 
 namespace skv {
@@ -52,16 +52,19 @@ constexpr float kGrow = 4.f;        // ... and their reference moves when a scor
 constexpr int kStep = 32;           // keys a warp takes at a time
 constexpr uint32_t kStraddle = 8;   // pages that a second start and join of a CTA cost
 
-// Computing warps and ring slots.  One column group: eight sequences of up to 32768
-// keys take 61 us with 11 and 11, 63 with 7 and 7 or 8 and 8, 68 with 6 and 12 (one
-// of 1048576: 320, 334, 340 and 367); two groups need the registers of 7 warps.
-__host__ __device__ constexpr int warps_of(int nc) { return nc == 1 ? 11 : 7; }
-__host__ __device__ constexpr int slots_of(int nc) { return nc == 1 ? 11 : 7; }
+// Computing warps and as many ring slots.  One column group, D = 128: eight sequences of
+// up to 32768 keys take 60 us with 11 and 11, 63 with 7 and 7 or 8 and 8, 68 with 6 and
+// 12 (one of 1048576: 316, 334, 340 and 367); D = 64: 38.5 us with 15, 44 with 11.  Two
+// groups need the registers of 7 warps with D = 128; with D = 64 (four tokens of
+// eight sequences over 16000 keys) 47.8 us with 10, 51.7 with 7.
+__host__ __device__ constexpr int warps_of(int D, int nc) { return nc == 1 ? (D == 64 ? 15 : 11) : (D == 64 ? 10 : 7); }
+// Pages that the fetching warp requests at a time: a ring of 7 would stand still.
+__host__ __device__ constexpr int batch_of(int D, int nc) { return nc == 2 && D == 128 ? 2 : 4; }
 template <int D, int NC>
 __host__ __device__ constexpr int decode_smem()
 {
-    return 1024 + slots_of(NC) * 2 * kPage * D               // the ring, aligned for the swizzle
-           + warps_of(NC) * 8 * (D + 4) * 4                  // the warps' results
+    return 1024 + warps_of(D, NC) * 2 * kPage * D               // the ring, aligned for the swizzle
+           + warps_of(D, NC) * 8 * (D + 4) * 4                  // the warps' results
            + NC * (D / 16) * 32 * 8;                         // query fragments
 }
 static_assert(decode_smem<128, 1>() < 226 * 1024 && decode_smem<128, 2>() < 226 * 1024, "shared memory per CTA");
@@ -85,7 +88,7 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i)
 }
 
 template <int D, int NC, bool HILO, bool F16>
-__global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
+__global__ void __launch_bounds__(warps_of(D, NC) * 32 + 32, 1)
     decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a)
 {
     constexpr int KS = D / 16;                      // k-steps of S
@@ -93,10 +96,11 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
     constexpr int MT = D / 16;                      // m-tiles of O^T
     constexpr int VW = D / 32;                      // words of a value row per thread
     constexpr int LDO = D + 4;
-    constexpr int W = warps_of(NC);                 // computing warps; the last warp fetches
+    constexpr int W = warps_of(D, NC);                 // computing warps; the last warp fetches
     constexpr int kConsumers = W * 32, kThreads = kConsumers + 32;
-    constexpr int NS = slots_of(NC);
+    constexpr int NS = warps_of(D, NC);
     static_assert(2 * NS % W == 0, "the same warps own a slot's halves at every turn");
+    constexpr int kBatch = batch_of(D, NC);
     constexpr int BYTES = kPage * D;                // of a slot's K or V
     struct Meta {
         int id, blk;
@@ -312,12 +316,12 @@ __global__ void __launch_bounds__(warps_of(NC) * 32 + 32, 1)
                 // most NS of them not taken yet)
                 if (lane < n) s_meta[(n_put + lane) % 64] = Meta{cur.id, cur.blk, cur.ks * a.scale_log2, cur.vs};
                 __syncwarp();
-                // two pages at a time, a lane for each copy (by one lane the pages of D = 64
-                // took 300 ns each, more than their bytes)
+                // kBatch pages at a time, a lane for each copy (by one lane a page took 300 ns,
+                // D = 64 more than its bytes: 50 us where two at a time take 44 and four 41)
                 int done = 0;
-                for (; done < n; done += 2) {
+                for (; done < n; done += kBatch) {
                     const int i = done + (lane >> 1);
-                    const bool mine = lane < 4 && i < n;
+                    const bool mine = lane < 2 * kBatch && i < n;
                     const uint32_t m = n_put + i, slot = m % NS, turn = m / NS;
                     const uint32_t full = bar0 + 8 * slot, empty = bar0 + 8 * (NS + slot);
                     ok = __all_sync(0xffffffffu, !mine || turn == 0 || wait(empty, (turn - 1) & 1));
@@ -777,10 +781,10 @@ static int launch_one(skv_handle *h, const CUtensorMap &mk, const CUtensorMap &m
     static KernelAttrCache cache;
     constexpr int smem = decode_smem<D, NC>();
     const cudaError_t e = kernel_smem_optin(cache, reinterpret_cast<const void *>(decode_kernel<D, NC, HILO, F16>), smem,
-                                            warps_of(NC) * 32 + 32, nullptr);
+                                            warps_of(D, NC) * 32 + 32, nullptr);
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(8-bit decode)");
     if (h->prof_before) cudaEventRecord(h->prof_before, st);
-    const cudaError_t l = launch(decode_kernel<D, NC, HILO, F16>, dim3(grid), warps_of(NC) * 32 + 32, smem, st, mk, mv, a);
+    const cudaError_t l = launch(decode_kernel<D, NC, HILO, F16>, dim3(grid), warps_of(D, NC) * 32 + 32, smem, st, mk, mv, a);
     if (h->prof_after) cudaEventRecord(h->prof_after, st);
     return cuda_fail(h, l, "8-bit decode launch");
 }
