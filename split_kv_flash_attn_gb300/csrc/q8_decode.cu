@@ -415,7 +415,10 @@ __global__ void __launch_bounds__(warps_of(D, NC) * 32 + 32, 1)
         for (uint32_t n = n_taken + (warp + W - n_taken % W) % W; n < n_end; n += W) {
             const uint32_t m = n >> 1, slot = m % NS;   // (units begin at even n)
             const int p = x.pg0 + static_cast<int>((n - n_taken) >> 1), h = n & 1;
-            const bool there = wait(bar0 + 8 * slot, (m / NS) & 1);
+            // (the warp goes one way: what follows are its products and shuffles)
+            const uint32_t full = bar0 + 8 * slot, turn = (m / NS) & 1;
+            bool there = __all_sync(0xffffffffu, tc::mbar_try_wait(full, turn));
+            if (!there) there = __all_sync(0xffffffffu, wait(full, turn));
             const Meta meta = s_meta[m % 64];
             if (!there || meta.id < 0) {
                 if (a.page_lse && lane < 8 * NC && row0 + lane < a.rows) page_lse(row0 + lane)[2 * p + h] = -INFINITY;
