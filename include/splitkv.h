@@ -505,7 +505,8 @@ int skv_q8_append(skv_handle *h, const skv_q8_pool *pool, int32_t S, int32_t Hk,
  * NULL: token t sees key j iff j <= q_pos[s][t] (and j < kv_len[s]).  sel NULL:
  * every page of the list.  sel int32 [S][nq][Hk][n_sel]: only the pages with
  * these indices in the list, chosen for each query and KV head (entries below
- * 0 or behind the last token are skipped; an index given twice counts twice).
+ * 0 or behind the last token are skipped; an index given twice counts twice;
+ * n_sel < 2^30).
  * mass NULL, or fp32 [S][Hk][pages_per_list]: for every page that is read, the
  * attention probabilities of its keys, summed over the tokens and the query
  * heads of the KV head, are added to it (in an order that does not change from
@@ -527,7 +528,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
  *           fp32(dq * sum_d max(cq_d * k_min_d, cq_d * k_max_d)),
  * dq = fp32(max|q| / 127) and cq_d the integer nearest q_d / dq, both
  * products rounded to fp32: an upper bound of the coded query's scores over
- * the page.  n_first + n_last <= n_sel. */
+ * the page.  n_first + n_last <= n_sel < 2^30. */
 int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,
                   const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
                   int32_t n_sel, int32_t n_first, int32_t n_last, int32_t *sel, void *stream);

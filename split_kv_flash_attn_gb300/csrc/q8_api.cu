@@ -33,6 +33,9 @@ constexpr int kTcRows = 33;
 // Scratch for the pages' log sums or the selection's keys of one launch (one token's
 // at least).
 constexpr int64_t kPageScratch = int64_t(256) << 20;
+// Entries of a selection: the kernels index them, and the log sums of their halves,
+// in 32 bits.
+constexpr int32_t kMaxSel = 1 << 30;
 
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
@@ -119,6 +122,7 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
         (rc = check_lists(h, shape->S, shape->Hk, page_ids, pages_per_list, kv_len)))
         return rc;
     if (sel && n_sel < 1) return fail(h, SKV_EINVAL, "n_sel = %d", n_sel);
+    if (sel && n_sel >= kMaxSel) return fail(h, SKV_EUNSUPPORTED, "n_sel = %d (below 2^30 is supported)", n_sel);
     if (o_type != SKV_F32 && o_type != SKV_F16) return fail(h, SKV_EINVAL, "o_type is SKV_F32 or SKV_F16");
     if (!o || !lse) return fail(h, SKV_EINVAL, "o or lse is NULL");
     if (misaligned(o, 16) || misaligned(lse, 4)) return fail(h, SKV_EUNSUPPORTED, "o must be 16-byte aligned");
@@ -212,6 +216,7 @@ int skv_q8_select(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape
         return rc;
     if (n_sel < 1 || n_first < 0 || n_last < 0 || static_cast<int64_t>(n_first) + n_last > n_sel)
         return fail(h, SKV_EINVAL, "n_sel = %d with n_first = %d, n_last = %d", n_sel, n_first, n_last);
+    if (n_sel >= kMaxSel) return fail(h, SKV_EUNSUPPORTED, "n_sel = %d (below 2^30 is supported)", n_sel);
     if (!sel) return fail(h, SKV_EINVAL, "sel is NULL");
     const int64_t rows = static_cast<int64_t>(shape->S) * shape->nq * shape->Hk;
     if (rows > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "S*nq*Hk exceeds 2^31 - 1");
