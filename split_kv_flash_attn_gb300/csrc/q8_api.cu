@@ -166,10 +166,11 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
         const int64_t pairs = std::min<int64_t>(INT32_MAX, (int64_t(1) << 31) / (heads * ((pages_per_list + 1) / 2)));
         nq_max = std::min(nq_max, pairs * unit_rows / a.G);
     }
-    if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kPageScratch / (heads * a.G * per_list * 8)));
     if (nq_max < 1)
         return fail(h, SKV_EUNSUPPORTED, "S*Hk = %lld lists of %lld pages with %d query heads each are too many for one launch",
                     (long long)heads, (long long)pages_per_list, a.G);
+    // (a token's units fit a launch: heads * G is below 2^24 here, and the product below 2^57)
+    if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kPageScratch / (heads * a.G * per_list * 8)));
     a.nq = static_cast<int>(nq_max);
     a.rows = sel ? rows1 : a.nq * a.G;
     a.row_groups = static_cast<int>((a.rows + unit_rows - 1) / unit_rows);
