@@ -519,6 +519,13 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
                 const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
                 const int32_t *sel, int32_t n_sel, float *mass, int32_t o_type, void *o, float *lse, void *stream);
 
+/* Tokens that one launch of skv_q8_attn takes for calls of this shape (n_sel 0: over
+ * whole lists; mass: whether page weights are asked for); a call of more tokens
+ * takes several launches.  Bounded by units (65535), by page visits (units x pages of
+ * the list or entries of the selection, below 2^32) and by scratch.
+ * SKV_EUNSUPPORTED: a single token is too much, and the call refuses it.  Needs no GPU. */
+int skv_plan_q8_tokens(const skv_shape *shape, int64_t pages_per_list, int32_t n_sel, int32_t mass, int32_t *tokens);
+
 /* Pick n_sel pages for every query and KV head: sel int32 [S][nq][Hk][n_sel]
  * receives list indices in ascending order, padded with -1.  Candidates are
  * the pages that hold a key the token sees and are present.  Those among the

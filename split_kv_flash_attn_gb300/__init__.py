@@ -28,7 +28,7 @@ from . import _lib
 from ._lib import F16, F32, Q4_0, Q8_0, Q8_PAGE, SkvQ8Pool, SkvShape
 
 __all__ = ["Handle", "SplitKVError", "F16", "Q8_0", "Q4_0", "attn_partial", "attn_combine", "attn_window_tail",
-           "attn_paged", "BlockCache", "kv_dequant_q8_0", "kv_dequant_q4_0", "gather_rows", "kv_append", "plan_splits", "plan_prefill_splits",
+           "attn_paged", "BlockCache", "kv_dequant_q8_0", "kv_dequant_q4_0", "gather_rows", "kv_append", "plan_splits", "plan_prefill_splits", "plan_q8_tokens",
            "segment_bytes", "Q8_PAGE", "Q8Pool", "q8_append", "q8_attn", "q8_select", "q8_evict"]
 
 
@@ -540,6 +540,16 @@ def q8_attn(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, scale=None, q_pos=N
     if rc:
         h.check(rc)
     return o, lse
+
+
+def plan_q8_tokens(S, nq, H, Hk, pages_per_list, *, n_sel=0, mass=False):
+    """skv_plan_q8_tokens: the tokens that one launch of q8_attn takes for calls of
+    this shape (n_sel 0: over whole lists).  Needs no GPU."""
+    sh, n = SkvShape(int(S), int(nq), int(H), int(Hk), 128, 1.0, 0, 0, 0, 0), ctypes.c_int32()
+    rc = _lib.lib().skv_plan_q8_tokens(ctypes.byref(sh), int(pages_per_list), int(n_sel), int(bool(mass)), ctypes.byref(n))
+    if rc != 0:
+        raise SplitKVError(rc, "skv_plan_q8_tokens rejected its arguments")
+    return n.value
 
 
 def q8_select(h: Handle, pool: Q8Pool, q, page_ids, kv_len, *, n_sel, n_first=1, n_last=1, q_pos=None, sel=None,

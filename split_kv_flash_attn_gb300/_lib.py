@@ -27,7 +27,7 @@ EXPORTS = [
     "skv_bcache_append", "skv_bcache_attn", "skv_bcache_stats", "skv_bcache_check", "skv_bcache_pool",
     "skv_bcache_create_ring", "skv_bcache_ring_restore", "skv_bcache_ring_attn",
     "skv_attn_partial_static", "skv_plan_window", "skv_plan_tail_tile", "skv_selftest_wait_timeout",
-    "skv_q8_append", "skv_q8_attn", "skv_q8_select", "skv_q8_evict",
+    "skv_q8_append", "skv_q8_attn", "skv_q8_select", "skv_q8_evict", "skv_plan_q8_tokens",
 ]
 
 
@@ -92,6 +92,7 @@ def _declare(lib):
         "skv_bcache_check": ([P, ctypes.POINTER(I32)], ctypes.c_int),
         "skv_q8_append": ([P, QP, I32, I32, I32, I32, P, P, P, I64, P, P, P], ctypes.c_int),
         "skv_q8_attn": ([P, QP, SH, P, P, I64, P, P, P, I32, P, I32, P, P, P], ctypes.c_int),
+        "skv_plan_q8_tokens": ([SH, I64, I32, I32, ctypes.POINTER(I32)], ctypes.c_int),
         "skv_q8_select": ([P, QP, SH, P, P, I64, P, P, I32, I32, I32, P, P], ctypes.c_int),
         "skv_q8_evict": ([P, I32, I32, I64, P, P, P, I32, I32, I32, P, P, P, P, P], ctypes.c_int),
         "skv_bcache_pool": ([P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(I64), ctypes.POINTER(P)],

@@ -33,6 +33,10 @@ constexpr int kTcRows = 33;
 // Scratch for the pages' log sums or the selection's keys of one launch (one token's
 // at least).
 constexpr int64_t kPageScratch = int64_t(256) << 20;
+// Pages that the units of a decode launch pass by: positions on their line, and those with
+// the units rounded up to whole pieces (a CTA's fraction of a page and 8 pages more for each
+// CTA), are counted in 32 bits.
+constexpr int64_t kMaxVisits = 0xffff0000ll;
 // Entries of a selection: the kernels index them, and the log sums of their halves,
 // in 32 bits.
 constexpr int32_t kMaxSel = 1 << 30;
@@ -80,6 +84,41 @@ static Lists lists_of(skv_handle *h, int64_t n_pages, int32_t S, int32_t Hk, con
                       const int32_t *kv_len)
 {
     return Lists{ids, kv_len, cap, n_pages, S, Hk, h->status};
+}
+
+// How a call is served: which kernel, rows of its units (the tensor-core kernel takes 256
+// at a time, the decode kernel 8 or 16), and the tokens of one launch: as many as the
+// kernels' counters have units for, as keep their lines of pages or key tiles within
+// 32 bits, and as keep the pages' log sums within kPageScratch (but one at least).
+struct AttnSplit {
+    bool tc;
+    int nc;
+    int64_t unit_rows;
+    int64_t tokens;                // 0: not even one
+};
+
+static AttnSplit attn_split(const skv_shape &sh, int64_t cap, int32_t n_sel, bool mass)
+{
+    const bool sel = n_sel > 0;
+    const int64_t heads = static_cast<int64_t>(sh.S) * sh.Hk, G = sh.H / sh.Hk;
+    constexpr int64_t max_units = kMaxUnits - 1;          // (a grid's y)
+    AttnSplit x;
+    x.tc = !sel && sh.nq * G >= kTcRows;
+    x.nc = (sel ? G : sh.nq * G) <= 8 ? 1 : 2;
+    x.unit_rows = x.tc ? 256 : 8 * x.nc;
+    const int64_t groups = (G + x.unit_rows - 1) / x.unit_rows;   // units of a token's rows
+    x.tokens = std::min<int64_t>(sh.nq, sel ? max_units / (heads * groups) : (max_units / heads) * x.unit_rows / G);
+    if (x.tokens < 1) return x;
+    // (a token's units fit a launch: heads * G is below 2^24 from here on)
+    if (sel) {
+        x.tokens = std::min(x.tokens, kMaxVisits / (heads * groups * n_sel));
+    } else {
+        const int64_t line = x.tc ? (int64_t(1) << 31) / (heads * ((cap + 1) / 2)) : kMaxVisits / (heads * cap);
+        x.tokens = std::min(x.tokens, std::min<int64_t>(INT32_MAX, line) * x.unit_rows / G);
+    }
+    if (x.tokens >= 1 && mass)
+        x.tokens = std::min(x.tokens, std::max<int64_t>(1, kPageScratch / (heads * G * (sel ? n_sel : cap) * 8)));
+    return x;
 }
 
 static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -147,32 +186,17 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
     a.lse = lse;
     a.counters = h->counters;
     const bool f16 = o_type == SKV_F16;
-    // Rows of a KV head: the tensor-core kernel takes 256 at a time, the decode
-    // kernel 8 or 16.
-    const bool tc = !sel && static_cast<int64_t>(shape->nq) * a.G >= kTcRows;
-    // Tokens of one launch: as many as the kernels' counters have units for, and as
-    // keep the pages' log sums within kPageScratch (at least one).
     const int64_t heads = static_cast<int64_t>(shape->S) * shape->Hk;
-    constexpr int64_t max_units = kMaxUnits - 1;          // (a grid's y)
-    int64_t nq_max = shape->nq;
-    const int rows1 = sel ? a.G : 0;                      // rows of a unit that do not grow with the tokens
-    const int nc = (sel ? a.G : static_cast<int64_t>(shape->nq) * a.G) <= 8 ? 1 : 2;
-    const int64_t unit_rows = tc ? 256 : 8 * nc;
-    if (sel) nq_max = std::min(nq_max, max_units / std::max<int64_t>(1, heads * ((a.G + unit_rows - 1) / unit_rows)));
-    else nq_max = std::min(nq_max, (max_units / heads) * unit_rows / a.G);
     const int64_t per_list = sel ? n_sel : pages_per_list;
-    if (tc) {
-        // the tensor-core kernel counts key tiles of a launch in 32 bits
-        const int64_t pairs = std::min<int64_t>(INT32_MAX, (int64_t(1) << 31) / (heads * ((pages_per_list + 1) / 2)));
-        nq_max = std::min(nq_max, pairs * unit_rows / a.G);
-    }
+    const AttnSplit split = attn_split(*shape, pages_per_list, a.n_sel, mass != nullptr);
+    const bool tc = split.tc;
+    const int nc = split.nc;
+    const int64_t unit_rows = split.unit_rows, nq_max = split.tokens;
     if (nq_max < 1)
         return fail(h, SKV_EUNSUPPORTED, "S*Hk = %lld lists of %lld pages with %d query heads each are too many for one launch",
-                    (long long)heads, (long long)pages_per_list, a.G);
-    // (a token's units fit a launch: heads * G is below 2^24 here, and the product below 2^57)
-    if (mass) nq_max = std::min(nq_max, std::max<int64_t>(1, kPageScratch / (heads * a.G * per_list * 8)));
+                    (long long)heads, (long long)per_list, a.G);
     a.nq = static_cast<int>(nq_max);
-    a.rows = sel ? rows1 : a.nq * a.G;
+    a.rows = sel ? a.G : a.nq * a.G;
     a.row_groups = static_cast<int>((a.rows + unit_rows - 1) / unit_rows);
     const int64_t units = (sel ? heads * a.nq : heads) * a.row_groups;
     // one CTA a SM, but no more than pieces of kPieceMin pages
@@ -202,6 +226,18 @@ int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, 
         }
         if (rc) return rc;
     }
+    return SKV_OK;
+}
+
+int skv_plan_q8_tokens(const skv_shape *shape, int64_t pages_per_list, int32_t n_sel, int32_t mass, int32_t *tokens)
+{
+    if (!shape || !tokens || shape->S < 1 || shape->S > 65535 || shape->nq < 1 || shape->Hk < 1 || shape->Hk > 65535 ||
+        shape->H < shape->Hk || shape->H % shape->Hk || pages_per_list < 1 || pages_per_list > INT32_MAX / kPage || n_sel < 0 ||
+        n_sel >= kMaxSel || static_cast<int64_t>(shape->nq) * (shape->H / shape->Hk) > INT32_MAX)
+        return SKV_EINVAL;
+    const int64_t n = attn_split(*shape, pages_per_list, n_sel, mass != 0).tokens;
+    if (n < 1) return SKV_EUNSUPPORTED;
+    *tokens = static_cast<int32_t>(n);
     return SKV_OK;
 }
 

@@ -130,10 +130,10 @@ __global__ void __launch_bounds__(warps_of(D, NC) * 32 + 32, 1)
     start();
 
     // ---- the plan: total pages, this CTA's piece, the list that it starts in --
-    uint64_t sum = 0;
+    uint32_t sum = 0;                               // (the host gives a launch no more than kMaxVisits)
     uint32_t np_lane = 0;                           // pages of list `lane`
     if (a.sel) {
-        sum = static_cast<uint64_t>(n_lists) * a.n_sel;
+        sum = static_cast<uint32_t>(n_lists) * a.n_sel;
     } else {
         for (int i = lane; i < n_lists; i += 32) {
             const uint32_t n = pages_of(a, i);
@@ -145,11 +145,7 @@ __global__ void __launch_bounds__(warps_of(D, NC) * 32 + 32, 1)
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     sum *= mult;
-    if (sum > (1u << 30)) {                         // (16 TB of pages: lengths that are none)
-        if (blockIdx.x == 0 && tid == 0) atomicOr(a.L.status, kStatusList);
-        sum = 0;
-    }
-    uint32_t total = static_cast<uint32_t>(sum);
+    uint32_t total = sum;
     const uint32_t even = max(static_cast<uint32_t>(kPieceMin), (total + gridDim.x - 1) / gridDim.x);
     // Pieces that end with their units spare the CTAs a second start and join: taken
     // when the least piece with which the grid covers units one by one is at most
