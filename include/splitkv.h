@@ -488,9 +488,10 @@ typedef struct skv_q8_pool {
  * n_new[s] when n_new is given, at most n_max; negative counts as 0).  k_new,
  * v_new: x_type (SKV_F32 or SKV_F16) [S][n_max][Hk][D], 16-byte aligned; kv_len
  * itself is left to the caller.  For each page touched
- *   d' = max(d, fp32(amax / 127)), amax = largest finite magnitude written,
+ *   d' = max(|d|, fp32(amax / 127)), amax = largest finite magnitude written,
  * d = its present scale when it holds earlier tokens (below kv_len[s]), else 0;
- * earlier codes c become the integer nearest c*d/d' when d' > d, new codes are
+ * earlier codes c become the integer nearest c*d/d' when d' is another number than
+ * d (larger, or d negative: appends leave no negative scale), new codes are
  * the integer nearest x/d' within [-127, 127] (ties to even, decided by the
  * exact quotient; d' = 0 gives codes 0; NaN gives 0, an infinity +-127), and the
  * smallest and largest K codes follow.  Nothing else of the page changes, so

@@ -2,9 +2,9 @@
 //
 // One CTA for each (page touched, K or V, KV head, sequence).  It holds the
 // page's new values in registers (at most 64 rows of D: 8 values of 4 or 8 rows
-// a thread), takes their largest magnitude, d' = max(d, fp32(amax/127)),
+// a thread), takes their largest magnitude, d' = max(|d|, fp32(amax/127)),
 // and writes the codes nearest x/d' and, for K, the channels' smallest and
-// largest codes.  Only when d' > d and the page holds earlier tokens are those
+// largest codes.  Only when d' is not d and the page holds earlier tokens are those
 // read and recoded, through a table of the 255 codes (one fp64 division each:
 // c*d has 31 significant bits, so c*d/d' cannot be rounded onto a half-integer
 // that it is not); rounding is monotone, so the old extremes recode like codes.
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(append_threads(D, sizeof(X) == 2), 1024 / appe
     const bool any_odd = __syncthreads_or(odd);
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
-    const float d1 = fmaxf(d0, over_127(amax));
+    const float d1 = fmaxf(fabsf(d0), over_127(amax));                      // (a negative scale leaves with its codes turned)
     const bool recode = r_lo > 0 && d1 != d0;
     const bool plain = !any_odd && d1 >= 0x1p-100f;                         // every value finite, d' not tiny
     int8_t *page = codes + id * (kPage * D);

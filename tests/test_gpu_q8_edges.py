@@ -4,6 +4,7 @@ beyond their lists, and the borders between the forms of the choice."""
 import numpy as np
 import pytest
 
+import q8_rows as r
 import q8_util as u
 
 pytestmark = pytest.mark.gpu
@@ -24,6 +25,38 @@ def _dev(a):
 
 def _q(rng, S, nq, H, D):
     return rng.standard_normal((S, nq, H, D)).astype(np.float16)
+
+
+# ------------------------------------------------------- scales of either sign
+
+def _signed(rng, lens, Hk, D, extra):
+    c = u.Cache(rng, lens, Hk, D, extra=extra)
+    c.ks *= rng.choice([-1, 1], c.n_pages).astype(np.float32)
+    c.vs *= rng.choice([-1, 1], c.n_pages).astype(np.float32)
+    return c
+
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("D,Hk,n,lens,size", [
+    # rows that grow the scale, that do not, and that are zeros
+    (128, 2, 3, [10, 63, 1, 64], 30.0), (64, 3, 20, [5, 40, 127], 0.01), (128, 1, 7, [33, 2], 0.0), (64, 2, 70, [61, 0, 100], 1.0)])
+def test_append_to_pages_of_a_negative_scale(h, D, Hk, n, lens, size, f16):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(D + n)
+    c = _signed(rng, lens, Hk, D, n)
+    pool, ids, kv_len = c.on_gpu()
+    held = c.k[c.ids[0, 0, 0], 0].astype(np.float64) * float(c.ks[c.ids[0, 0, 0]])
+    x = (rng.standard_normal((2, len(lens), n, Hk, D)) * size).astype(np.float16 if f16 else np.float32)
+    for _ in range(2):                                # again: the same bytes
+        skv.q8_append(h, pool, _dev(x[0]), _dev(x[1]), ids, kv_len)
+        r.append(c, x[0], x[1])
+        for name, want in (("k", c.k), ("v", c.v), ("k_scale", c.ks), ("v_scale", c.vs)):
+            got = getattr(pool, name).cpu().numpy()
+            assert np.array_equal(got, want), f"{name} differs in {np.count_nonzero(got != want)} places"
+    # what was held is still there, to half a step of the new scale
+    p = c.ids[0, 0, 0]
+    assert np.abs(c.k[p, 0] * float(c.ks[p]) - held).max() <= 0.5001 * c.ks[p]
+    assert h.status() == 0
 
 
 # ------------------------------------------------------- very many page visits
