@@ -7,7 +7,8 @@
 // largest codes.  Only when d' is not d and the page holds earlier tokens are those
 // read and recoded, through a table of the 255 codes (one fp64 division each:
 // c*d has 31 significant bits, so c*d/d' cannot be rounded onto a half-integer
-// that it is not); rounding is monotone, so the old extremes recode like codes.
+// that it is not); rounding is monotone, so the old extremes recode like codes
+// (d negative: the smallest becomes the largest).
 //
 // A code is rint(t), t = x (1/d') with an approximate reciprocal, when t is further
 // than 2^-13 from every half-integer: t is off by less than 2^-21.4 * 128 = 2^-14.4
@@ -314,8 +315,9 @@ __global__ void __launch_bounds__(append_threads(D, sizeof(X) == 2), 1024 / appe
         if (r_lo > 0) {
             uint32_t ol = *pl, om = *pm;
             if (recode) {
-                ol = recode4(s_lut, ol);
-                om = recode4(s_lut, om);
+                const uint32_t rl = recode4(s_lut, ol), rm = recode4(s_lut, om);
+                ol = __vmins4(rl, rm);              // (a negative d exchanges the two)
+                om = __vmaxs4(rl, rm);
             }
             l = __vmins4(l, ol);
             m = __vmaxs4(m, om);

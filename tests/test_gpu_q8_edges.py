@@ -59,6 +59,28 @@ def test_append_to_pages_of_a_negative_scale(h, D, Hk, n, lens, size, f16):
     assert h.status() == 0
 
 
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("D,Hk,n,lens,size", [(128, 2, 3, [10, 63, 1, 64], 30.0), (64, 3, 20, [5, 40, 127], 0.01), (128, 1, 70, [33, 2], 1.0)])
+def test_extremes_of_pages_of_a_negative_scale(h, D, Hk, n, lens, size, f16):
+    """Recoding with a negative factor exchanges the smallest and the largest codes."""
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(D + n + 1)
+    c = _signed(rng, lens, Hk, D, n)
+    pool, ids, kv_len = c.on_gpu()
+    x = (rng.standard_normal((2, len(lens), n, Hk, D)) * size).astype(np.float16 if f16 else np.float32)
+    skv.q8_append(h, pool, _dev(x[0]), _dev(x[1]), ids, kv_len)
+    r.append(c, x[0], x[1])
+    assert np.array_equal(pool.k_min.cpu().numpy(), c.lo) and np.array_equal(pool.k_max.cpu().numpy(), c.hi)
+    # and a selection of the pages written, whose scales are positive now
+    c.lens += n
+    c.ks = np.abs(c.ks)
+    pool.k_scale.abs_()
+    q = _q(rng, len(lens), 1, 4 * Hk, D)
+    got = skv.q8_select(h, pool, _dev(q), ids, kv_len + n, n_sel=2, n_first=0, n_last=0)
+    assert np.array_equal(got.cpu().numpy(), u.select(c, q, 2, 0, 0))
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- very many page visits
 
 def test_selections_of_more_visits_than_2_to_the_30(h):
