@@ -532,8 +532,9 @@ int skv_plan_q8_tokens(const skv_shape *shape, int64_t pages_per_list, int32_t n
  * the pages that hold a key the token sees and are present.  Those among the
  * list's first n_first pages and among the last n_last that hold a visible key
  * are always picked; the others by the largest bound, ties to the lowest index:
- *   bound = k_scale * max over the KV head's query heads of
- *           fp32(dq * sum_d max(cq_d * k_min_d, cq_d * k_max_d)),
+ *   bound = |k_scale| * max over the KV head's query heads of
+ *           fp32(dq * sum_d max(cq_d * x_d, cq_d * y_d)),
+ * x, y = k_min, k_max, or -k_min, -k_max where k_scale < 0;
  * dq = fp32(max|q| / 127) and cq_d the integer nearest q_d / dq, both
  * products rounded to fp32: an upper bound of the coded query's scores over
  * the page.  n_first + n_last <= n_sel < 2^30. */

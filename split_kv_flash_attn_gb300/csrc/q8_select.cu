@@ -4,8 +4,10 @@
 //
 // The bound.  A page keeps the smallest and largest K code of each channel,
 // so sum_d max(cq_d min_d, cq_d max_d) bounds the product of the coded query with
-// every key of the page.  It is cq+ . max + cq- . min, the positive and the
-// negative part of the query against the two extremes: one product of length
+// every key of the page (where its scale is negative, sum_d max(-cq_d min_d, -cq_d max_d) the
+// negated product).  It is cq+ . max + cq- . min, the positive and the
+// negative part of the query against the two extremes, which change places (and the
+// sign) for a negative scale: one product of length
 // 2D of whole numbers of at most 127, whose sums stay below 2^21, so the tensor
 // cores' fp32 sums are exact and the picks do not depend on the order of
 // anything.  A warp takes 16 pages (the M side; bytes straight from global
@@ -55,6 +57,7 @@ struct Extremes {
     static constexpr int CH = D / 64;
     uint4 x[2][2][CH];
     int id[2];
+    float scale[2];
 
     __device__ void ids_of(const SelectArgs &a, const int32_t *ids, int64_t first, int64_t nb, int g)
     {
@@ -67,12 +70,28 @@ struct Extremes {
     __device__ void load(const SelectArgs &a, int t)
     {
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr)
+        for (int rr = 0; rr < 2; ++rr) {
+            scale[rr] = id[rr] >= 0 ? __ldg(a.k_scale + id[rr]) : 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int64_t off = static_cast<int64_t>(max(id[rr], 0)) * D + 64 * c + 16 * t;
                 x[0][rr][c] = id[rr] >= 0 ? ld_stream16(a.k_max + off) : make_uint4(0, 0, 0, 0);
                 x[1][rr][c] = id[rr] >= 0 ? ld_stream16(a.k_min + off) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    // Where a scale is negative, the two change places.
+    __device__ void turn()
+    {
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr)
+            if (scale[rr] < 0.f) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint4 y = x[0][rr][c];
+                    x[0][rr][c] = x[1][rr][c];
+                    x[1][rr][c] = y;
+                }
             }
     }
 };
@@ -443,12 +462,15 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
             nxt.load(a, t);
             __syncthreads();
             for (int64_t gr = group0; gr < groups; gr += stride) {
-                const Extremes<D> cur = nxt;
+                Extremes<D> cur = nxt;
                 // lane l finishes page l % 16
                 const int id0 = __shfl_sync(0xffffffffu, cur.id[0], (lane & 7) * 4);
                 const int id1 = __shfl_sync(0xffffffffu, cur.id[1], (lane & 7) * 4);
+                const float ks0 = __shfl_sync(0xffffffffu, cur.scale[0], (lane & 7) * 4);
+                const float ks1 = __shfl_sync(0xffffffffu, cur.scale[1], (lane & 7) * 4);
                 const int page_id = (lane & 8) ? id1 : id0;
-                const float page_scale = page_id >= 0 ? __ldg(a.k_scale + page_id) : 0.f;
+                const float page_scale = (lane & 8) ? ks1 : ks0;
+                if (__any_sync(0xffffffffu, page_scale < 0.f)) cur.turn();
                 if (gr + stride < groups) {
                     nxt.ids_of(a, ids, (gr + stride) * 16, nb, g);
                     nxt.load(a, t);
@@ -484,7 +506,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int c = j * 8 + 2 * t + (e & 1);
-                        s_f[warp][g + 8 * (e >> 1)][c] = __fmul_rn(acc[j][e], s_dq[c]);
+                        s_f[warp][g + 8 * (e >> 1)][c] = __fmul_rn(acc[j][e], cur.scale[e >> 1] < 0.f ? -s_dq[c] : s_dq[c]);
                     }
                 }
                 __syncwarp();
@@ -500,8 +522,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
                     const int nbq = s_nb[tok];
                     uint32_t key = kNever;
                     if (page_id >= 0 && blk < nbq) {
-                        key = blk < a.n_first || blk >= nbq - a.n_last ? kAlways : order_key(__fmul_rn(m, page_scale));
-                        if (h0 > 0) key = page_scale >= 0.f ? max(key, *out) : min(key, *out);
+                        key = blk < a.n_first || blk >= nbq - a.n_last ? kAlways : order_key(__fmul_rn(m, fabsf(page_scale)));
+                        if (h0 > 0) key = max(key, *out);
                     }
                     *out = key;
                 }

@@ -81,6 +81,38 @@ def test_extremes_of_pages_of_a_negative_scale(h, D, Hk, n, lens, size, f16):
     assert h.status() == 0
 
 
+@pytest.mark.parametrize("lens,nq,H,Hk,D,n", [([3000, 700], 1, 8, 2, 128, 6), ([64 * 1500], 1, 4, 1, 64, 100), ([2000], 5, 12, 2, 64, 4),
+                                              ([64 * 300], 1, 150, 1, 128, 20), ([64 * 40, 0], 1, 1, 1, 64, 7)])
+def test_selection_over_scales_of_either_sign(h, lens, nq, H, Hk, D, n):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(sum(lens) + D)
+    c = _signed(rng, lens, Hk, D, 0)
+    c.ks[c.ids[0, 0, 5]] = 0.0
+    c.ks[c.ids[0, 0, 6]] = -0.0
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, len(lens), nq, H, D)
+    q_pos = (c.lens[:, None] - nq + np.arange(nq)[None]).astype(np.int32) if nq > 1 else None
+    got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=n, n_first=0, n_last=0, q_pos=None if q_pos is None else _dev(q_pos))
+    assert np.array_equal(got.cpu().numpy(), r.select(c, q, n, 0, 0, q_pos))
+    assert h.status() == 0
+
+
+def test_the_bound_of_a_negative_scale_is_one(h):
+    """The page of the best key under the coded query is picked when every other page's bound is lower."""
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(3)
+    c = u.Cache(rng, [64 * 40], 1, 128)
+    c.k //= 8
+    c.ks[:] = -0.03
+    q = _q(rng, 1, 1, 1, 128)
+    cq = u.code(q[0, 0, 0], np.float32(np.abs(q).astype(np.float64).max() / 127)).astype(int)
+    c.k[c.ids[0, 0, 17], 9] = np.clip(-cq, -127, 127)    # one key along the query, its codes against it
+    c.extremes()
+    pool, ids, kv_len = c.on_gpu()
+    got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=1, n_first=0, n_last=0).cpu().numpy()
+    assert got.tolist() == [[[[17]]]]
+
+
 # ------------------------------------------------------- very many page visits
 
 def test_selections_of_more_visits_than_2_to_the_30(h):
