@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectArg
     const int g = lane >> 2, t = lane & 3;
     const int kh = blockIdx.y, s = blockIdx.z;
     const int64_t len = list_len(a.L, s);
+    if (blockIdx.x == 0 && kh == 0 && tid == 0 && len < max(0, __ldg(a.L.kv_len + s))) atomicOr(a.L.status, kStatusList);
     const int64_t nb = (len + kPage - 1) / kPage;
     const int piece = blockIdx.x / parts, part = blockIdx.x - piece * parts;
     const int64_t groups = (nb + 15) / 16, stride = static_cast<int64_t>(gridDim.x / parts) * kScoreWarps;

@@ -113,6 +113,25 @@ def test_the_bound_of_a_negative_scale_is_one(h):
     assert got.tolist() == [[[[17]]]]
 
 
+# ------------------------------------------------------- lengths beyond their lists
+
+@pytest.mark.parametrize("nq,cap", [(1, 4), (3, 4), (1, 1500)])
+def test_selection_reports_a_length_beyond_its_list(h, nq, cap):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(12)
+    c = u.Cache(rng, [cap * u.PAGE, 100], 2, 64, cap=cap)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 2, nq, 4, 64)
+    kv_len[0] += 1                                    # cut to the list
+    got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=2)
+    assert np.array_equal(got.cpu().numpy(), u.select(c, q, 2, 1, 1))
+    with pytest.raises(skv.SplitKVError, match="0x4"):
+        h.status()
+    kv_len[0] -= 1
+    skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=2)
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- very many page visits
 
 def test_selections_of_more_visits_than_2_to_the_30(h):
