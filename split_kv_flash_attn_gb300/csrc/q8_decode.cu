@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(warps_of(D, NC) * 32 + 32, 1)
     uint32_t np_lane = 0;                           // pages of list `lane`
     if (a.sel) {
         sum = static_cast<uint32_t>(n_lists) * a.n_sel;
+        if (blockIdx.x == 0)
+            for (int i = tid; i < a.L.S; i += kThreads)
+                if (list_len(a.L, i) < max(0, a.L.kv_len[i])) atomicOr(a.L.status, kStatusList);
     } else {
         for (int i = lane; i < n_lists; i += 32) {
             const uint32_t n = pages_of(a, i);

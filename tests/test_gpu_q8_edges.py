@@ -132,6 +132,24 @@ def test_selection_reports_a_length_beyond_its_list(h, nq, cap):
     assert h.status() == 0
 
 
+@pytest.mark.parametrize("S,nq", [(2, 1), (2, 3), (40, 1)])
+def test_attention_over_a_selection_reports_a_length_beyond_its_list(h, S, nq):
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(13)
+    c = u.Cache(rng, [4 * u.PAGE] * S, 2, 64, cap=4)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, S, nq, 4, 64)
+    sel = rng.integers(-1, 6, (S, nq, 2, 3)).astype(np.int32)
+    kv_len[S - 1] += 1
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, sel=_dev(sel))
+    u.check(o, lse, u.attention(c, q, sel=sel))
+    with pytest.raises(skv.SplitKVError, match="0x4"):
+        h.status()
+    kv_len[S - 1] -= 1
+    skv.q8_attn(h, pool, _dev(q), ids, kv_len, sel=_dev(sel))
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- very many page visits
 
 def test_selections_of_more_visits_than_2_to_the_30(h):
