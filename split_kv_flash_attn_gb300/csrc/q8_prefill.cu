@@ -670,13 +670,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                     // what does not depend on the scores first: the pages' factors and reference
                     __all_sync(0xffffffffu, wait(PB_META + static_cast<int>(j & 3), (j >> 2) & 1));
                     const Meta mt0 = s_meta[j & 3][0], mt1 = s_meta[j & 3][1];
-                    const float r_old = r_ref;
-                    const float lv_max = fmaxf(mt0.lv, mt1.lv);             // (-inf where there is no page)
-                    if (lv_max > r_ref + kPfScaleGrow) r_ref = ceilf(lv_max);
-                    const float dl0 = mt0.lv == -INFINITY ? kNoScale : fmaxf(mt0.lv - r_ref, kNoScale);
-                    const float dl1 = mt1.lv == -INFINITY ? kNoScale : fmaxf(mt1.lv - r_ref, kNoScale);
-                    const float un0 = fast_exp2(-dl0), un1 = fast_exp2(-dl1);
                     const int lim0 = mt0.on ? lim : 0, lim1 = mt1.on ? lim - kPage : 0;
+                    // (-inf where there is no page, or none that the row sees: a page it does not
+                    // see must not push its own values out of fp16)
+                    const float lv0 = lim0 > 0 ? mt0.lv : -INFINITY, lv1 = lim1 > 0 ? mt1.lv : -INFINITY;
+                    const float r_old = r_ref;
+                    const float lv_max = fmaxf(lv0, lv1);
+                    if (lv_max > r_ref + kPfScaleGrow) r_ref = ceilf(lv_max);
+                    const float dl0 = lv0 == -INFINITY ? kNoScale : fmaxf(lv0 - r_ref, kNoScale);
+                    const float dl1 = lv1 == -INFINITY ? kNoScale : fmaxf(lv1 - r_ref, kNoScale);
+                    const float un0 = fast_exp2(-dl0), un1 = fast_exp2(-dl1);
                     const bool masked = __any_sync(0xffffffffu, lim0 < kPage || lim1 < kPage);
                     __all_sync(0xffffffffu, wait(PB_SFULL + g, tiles & 1));
                     tc::tc_fence_after();

@@ -1,4 +1,7 @@
-"""More references of the calls over 8-bit pages, in 64 bits: scales of either sign."""
+"""More references of the calls over 8-bit pages, in 64 bits: scales of either
+sign, and attention with a bound for each row from what that row sees."""
+import math
+
 import numpy as np
 
 from q8_util import PAGE, code, visible
@@ -52,3 +55,54 @@ def select(c, q, n_sel, n_first, n_last, q_pos=None):
                 pick = sorted(b for _, _, b in sorted(rank)[:n_sel])
                 out[s, t, k, :len(pick)] = pick
     return out
+
+
+def attention(c, q, *, q_pos=None, sel=None):
+    """(o, lse, tol_o, tol_lse, vmax) in 64 bits, the last three for each row: as in q8_util.attention, with
+    the largest |v| and the largest sum |q_d k_d| of the keys that the row sees itself."""
+    S, nq, H, D = q.shape
+    Hk, G = c.Hk, H // c.Hk
+    o = np.zeros((S, nq, H, D))
+    lse = np.full((S, nq, H), -np.inf)
+    tol, vmax = np.zeros((S, nq, H)), np.zeros((S, nq, H))
+    for s in range(S):
+        for k in range(Hk):
+            for t in range(nq):
+                m = visible(c, s, t, q_pos)
+                blocks = range(-(-m // PAGE)) if sel is None else [b for b in map(int, sel[s, t, k]) if 0 <= b and b * PAGE < m]
+                kk, vv = [], []
+                for b in blocks:
+                    p, n = int(c.ids[s, k, b]), min(PAGE, m - b * PAGE)
+                    if 0 <= p < c.n_pages:
+                        kk.append(c.k[p, :n].astype(np.float64) * float(c.ks[p]))
+                        vv.append(c.v[p, :n].astype(np.float64) * float(c.vs[p]))
+                if not kk:
+                    continue
+                kk, vv = np.concatenate(kk), np.concatenate(vv)
+                rows = slice(k * G, (k + 1) * G)
+                x = q[s, t, rows].astype(np.float64)
+                w = x @ kk.T / math.sqrt(D)
+                top = w.max(1, keepdims=True)
+                e = np.exp(w - top)
+                z = e.sum(1, keepdims=True)
+                o[s, t, rows] = e / z @ vv
+                lse[s, t, rows] = (top + np.log(z))[:, 0]
+                tol[s, t, rows] = (D + 4) * 2.0 ** -23 * (np.abs(x) @ np.abs(kk).T).max(1) / math.sqrt(D) + 2.0 ** -19
+                vmax[s, t, rows] = np.abs(vv).max()
+    return o, lse, 2 * tol * vmax, tol + 2.0 ** -22 * np.where(np.isfinite(lse), np.abs(lse), 0), vmax
+
+
+def check(o, lse, ref, *, f16=False):
+    """Every row within its own bound.  fp16: the result's rounding and one of each weight, half a step
+    (2^-11) of each, and half a step of the smallest numbers (2^-25)."""
+    ro, rl, tol_o, tol_l, vmax = ref
+    assert str(o.dtype) == ("torch.float16" if f16 else "torch.float32")
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(lse), np.isneginf(rl)) and np.all(o[np.isneginf(rl)] == 0)
+    if f16:
+        tol_o = tol_o + 2.0 ** -11 * (np.abs(ro).max(-1) + vmax) + 2.0 ** -25
+    off = np.abs(o - ro).max(-1) - tol_o
+    at = np.unravel_index(off.argmax(), off.shape)
+    assert off[at] <= 0, f"row {at}: max|do| = {off[at] + tol_o[at]:.3e} > {tol_o[at]:.3e}"
+    on = np.isfinite(rl)
+    assert np.all(np.abs(lse[on] - rl[on]) <= tol_l[on])

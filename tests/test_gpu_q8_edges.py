@@ -113,6 +113,29 @@ def test_the_bound_of_a_negative_scale_is_one(h):
     assert got.tolist() == [[[[17]]]]
 
 
+# ------------------------------------------------ values that a row does not see
+
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("D,nq,H,Hk", [(128, 90, 4, 2), (64, 300, 1, 1), (128, 3, 8, 2)])
+def test_a_far_value_scale_behind_a_row_s_limit(h, D, nq, H, Hk, f16):
+    """Tokens that see the first page of a tile, whose other page holds values 2^30 as large: each row
+    within what its own keys give (fp16: as half a step of its own weights and results)."""
+    import split_kv_flash_attn_gb300 as skv
+    import torch
+    rng = np.random.default_rng(D + nq)
+    c = u.Cache(rng, [640, 200], Hk, D)
+    near, far = c.ids[:, :, 0:10:2], c.ids[:, :, 1:10:2]
+    c.vs[near[near >= 0]] *= np.float32(2.0 ** (-15 if not f16 else -3))
+    c.vs[far[far >= 0]] *= np.float32(2.0 ** (15 if not f16 else 27))
+    q_pos = rng.integers(0, 640, (2, nq)).astype(np.int32)
+    q_pos[:, : nq if f16 else nq // 2] = rng.integers(0, 64, (2, nq if f16 else nq // 2))   # (far values are beyond fp16)
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 2, nq, H, D)
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(q_pos), o_dtype=torch.float16 if f16 else None)
+    r.check(o, lse, r.attention(c, q, q_pos=q_pos), f16=f16)
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- lengths beyond their lists
 
 @pytest.mark.parametrize("nq,cap", [(1, 4), (3, 4), (1, 1500)])
