@@ -73,13 +73,20 @@ constexpr int kPlanHere = 256;                  // plan entries that the prefill
 constexpr int kPlanSmem = 1024;                 // plan entries kept in shared memory
 constexpr float kPfShift = 8.f, kPfGrow = 5.f, kPfScaleGrow = 2.f;
 constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a wait gives up (tens of ms at least)
-// The tensor core rounds its sums toward zero.  A tile's 16 additions (both parts of
-// the weights) shrink O by 2.4e-7 on average and blur it by 1.4e-7, in
-// proportion to the tiles (measured against 64 bits for 3 to 128 tiles): fp32
-// results take about kExactTiles at a time, put together in fp32, and the
-// average loss is given back.
+// The tensor core rounds its sums toward zero, so O loses with every addition, in proportion
+// to the tiles (rows of like weights over values of one sign 5e-7 a tile with both parts
+// of the weights): fp32 results take about kExactTiles at a time, put together in fp32.
+// What a stretch loses is given back by taking the row's sum of weights the same way:
+// each product's 16 keys added to w_cut toward zero, once for the first parts and once more
+// for the second (kLowPart of the first), and O multiplied by the true sum over it.
+// Weights of zero then count for nothing (a fixed share for each tile made a row of one key
+// 2.4e-6 too large).  Ten tiles of like weights, relative to the results: values of one sign
+// 3.0e-6 too small without, 5e-7 off with it; of both signs 2.1e-6 and 1.2e-6; few keys
+// that decide the row, values of one sign 6e-6 and 4e-6.  Time: 48.8 -> 49.5 us (64 tokens of
+// eight ragged sequences of up to 4096 keys); stretches of at most six tiles without it
+// 61 us and 1.5e-6 to 4e-6, of four 73 us and 1.2e-6 to 3.2e-6.
 constexpr int kExactTiles = 8, kExactMore = 2;    // (up to that many more rather than another stretch)
-constexpr float kLoss = 2.4e-7f;
+constexpr float kLowPart = 0x1p-12f;
 constexpr float kNoScale = -100.f;              // log2 d_v - r of a zero scale (fp16 0, while l stays right)
 
 template <int D>
@@ -649,6 +656,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             const bool tile_on = active(x);
             const int n = x.t1 - x.t0;
             float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
+            float w_sum = 0.f, w_cut = 0.f;     // of the weights in O: their sum, and one as the tensor core takes it
             if (tile_on) {
                 const int row = (2 * x.pr + g) * kPM + m;
                 const int len = static_cast<int>(list_len(a.L, x.s));
@@ -729,6 +737,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                     // what rounding left 16 further on): the second page's, which are in
                     // registers, then the first's; each half is announced by itself.
                     float lq[2][4];
+                    if (HILO) w_cut *= alpha_o;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int c = i ^ 2;
@@ -738,13 +747,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                         float(&l4)[4] = lq[c >> 1];
                         if ((c & 1) == 0) l4[0] = l4[1] = l4[2] = l4[3] = 0.f;
                         uint32_t hi[16], lo[16];
+                        float s16[2];                   // of a product's 16 keys
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float w0, w1;
                             fma2(w0, w1, __uint_as_float(xc[e]), __uint_as_float(xc[e + 1]), ks, of);
                             w0 = fast_exp2(w0);
                             w1 = fast_exp2(w1);
-                            add2(l4[e & 2], l4[(e & 2) + 1], w0, w1);
+                            if (HILO) {
+                                if ((e & 15) == 0) s16[0] = s16[1] = 0.f;
+                                add2(s16[0], s16[1], w0, w1);
+                                if ((e & 15) == 14) {
+                                    const float h = s16[0] + s16[1];
+                                    l4[e >> 4] += h;
+                                    w_cut = __fmaf_rz(kLowPart, h, __fadd_rz(w_cut, h));
+                                }
+                            } else {
+                                add2(l4[e & 2], l4[(e & 2) + 1], w0, w1);
+                            }
                             hi[e >> 1] = pack_half2(w0, w1);
                             if (HILO) {
                                 const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e >> 1]));
@@ -763,8 +783,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     tc::mbar_arrive(bar(PB_PFULL + g));
-                    const float ls0 = ((lq[0][0] + lq[0][1]) + (lq[0][2] + lq[0][3])) * un0;
-                    const float ls1 = ((lq[1][0] + lq[1][1]) + (lq[1][2] + lq[1][3])) * un1;
+                    const float ws0 = (lq[0][0] + lq[0][1]) + (lq[0][2] + lq[0][3]);
+                    const float ws1 = (lq[1][0] + lq[1][1]) + (lq[1][2] + lq[1][3]);
+                    const float ls0 = ws0 * un0, ls1 = ws1 * un1;
+                    if (HILO) w_sum = w_sum * alpha_o + (ws0 + ws1);
                     if (pl) {
                         if (pages > 0) pl[0] = ls0 > 0.f ? ref - kPfShift + log2f(ls0) : -INFINITY;
                         if (pages > 1) pl[a.rows] = ls1 > 0.f ? ref - kPfShift + log2f(ls1) : -INFINITY;
@@ -805,7 +827,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             float *const ml = a.part_ml + (slot * 2 + g) * kPM + m;
             float w_old = 0.f;                  // weight of the stretches before
             if (HILO) {
-                inv *= 1.f + kLoss * n;
+                if (w_cut > 0.f) inv *= w_sum * (1.f + kLowPart) / w_cut;
                 if (joins && out >= 0) {
                     const float z = __ldcg(ml), top = fmaxf(z, lse2);
                     if (z != -INFINITY || lse2 != -INFINITY) {

@@ -136,6 +136,58 @@ def test_a_far_value_scale_behind_a_row_s_limit(h, D, nq, H, Hk, f16):
     assert h.status() == 0
 
 
+# ------------------------------------------------------- rows that one key decides
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("masked", [True, False])
+def test_fp32_rows_of_one_key(h, D, masked):
+    """Rows of one visible key (or of one key whose score leaves the others nothing) in units of
+    1 to 10 tiles of 128 keys, one unit a CTA: o is that key's value.
+
+    Relative bound.  The weight in two fp16 parts 2^-22; the truncated sum of their products, and of
+    the weights, 2^-23 each; the value's scale through log2 (one step of a number below 8, times ln 2:
+    2^-21.5) and 2^x (2^-22), their difference's rounding (2^-23); seven more fp32 roundings of 2^-24:
+    in all 2^-19.3, so 2^-19."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(D)
+    Hk = 8
+    S = max(1, torch.cuda.get_device_properties(0).multi_processor_count // Hk)
+    for tiles in (1, 4, 8, 10):
+        n = 128 * tiles
+        c = u.Cache(rng, [n] * S, Hk, D)
+        c.ks[:] = 0.05
+        key = rng.integers(0, n, S)
+        q = np.zeros((S, 40, Hk, D), np.float16)
+        q_pos = np.full((S, 40), n - 1, np.int32)
+        if masked:
+            key[:] = 0
+            q_pos[:, :39] = 0
+        else:
+            for s in range(S):
+                # the key along the query, all others at least 80 lower: 2^-115 of its weight
+                sg = rng.choice([-1, 1], D)
+                q[s] = (sg * 10).astype(np.float16)
+                for k in range(Hk):
+                    c.k[c.ids[s, k, key[s] // 64], key[s] % 64] = 127 * sg
+        c.extremes()
+        pool, ids, kv_len = c.on_gpu()
+        o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=_dev(q_pos))
+        o = o.double().cpu().numpy()
+        for s in range(S):
+            for k in range(Hk):
+                p = c.ids[s, k, key[s] // 64]
+                want = c.v[p, key[s] % 64].astype(np.float64) * float(c.vs[p])
+                if not masked:
+                    w = np.concatenate([c.k[c.ids[s, k, b]] for b in range(n // 64)]).astype(np.float64) @ q[s, 0, k].astype(np.float64)
+                    w *= float(c.ks[p]) / np.sqrt(D)
+                    w = np.sort(w)
+                    assert w[-1] - w[-2] > 80
+                off = np.abs(o[s, :39, k] - want).max() / np.abs(want).max()
+                assert off <= 2.0 ** -19, f"{tiles} tiles, sequence {s}, head {k}: off by {off:.2e}"
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- lengths beyond their lists
 
 @pytest.mark.parametrize("nq,cap", [(1, 4), (3, 4), (1, 1500)])
