@@ -87,6 +87,12 @@ constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a w
 // 61 us and 1.5e-6 to 4e-6, of four 73 us and 1.2e-6 to 3.2e-6.
 constexpr int kExactTiles = 8, kExactMore = 2;    // (up to that many more rather than another stretch)
 constexpr float kLowPart = 0x1p-12f;
+// fp16 results (single weights, nothing given back) take more: values of one sign lose 1.6e-6
+// of the whole sum a tile, which over lists of 1048576 keys in one stretch made results
+// 6.7e-3 too small (262144 keys: 1.7e-3); at kLongTiles it is 9e-5, a fifth of half a
+// step of fp16.  512 tokens of eight sequences over 65536 keys 3.25 -> 3.37 ms (64
+// tiles: 3.50 ms, 4e-5); CTAs of fewer tiles, as for one sequence over 32768, as before.
+constexpr int kLongTiles = 128;
 constexpr float kNoScale = -100.f;              // log2 d_v - r of a zero scale (fp16 0, while l stays right)
 
 template <int D>
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
     const int np = pa.n_pairs;
     const int64_t n_entries = static_cast<int64_t>(a.L.S) * np;
     uint32_t *s_plan = reinterpret_cast<uint32_t *>(sm + SM::kPlan), *s_tiles = reinterpret_cast<uint32_t *>(sm + SM::kTiles);
-    Walk walk{pa.plan, np, a.L.S, a.L.Hk, HILO ? kExactTiles : INT32_MAX / 2, 0, 0, s_tiles};
+    Walk walk{pa.plan, np, a.L.S, a.L.Hk, HILO ? kExactTiles : kLongTiles, 0, 0, s_tiles};
     if (n_entries <= kPlanHere) {               // few entries: every CTA counts them itself
         for (int e = warp; e < n_entries; e += kPfThreads / 32) {
             const uint32_t x = entry_tiles(a, np, e);
@@ -826,16 +832,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
             float lse2 = empty ? -INFINITY : m_ref - kPfShift + log2f(l_run);
             float *const ml = a.part_ml + (slot * 2 + g) * kPM + m;
             float w_old = 0.f;                  // weight of the stretches before
-            if (HILO) {
-                if (w_cut > 0.f) inv *= w_sum * (1.f + kLowPart) / w_cut;
-                if (joins && out >= 0) {
-                    const float z = __ldcg(ml), top = fmaxf(z, lse2);
-                    if (z != -INFINITY || lse2 != -INFINITY) {
-                        const float e_old = fast_exp2(z - top), e_new = fast_exp2(lse2 - top);
-                        w_old = e_old / (e_old + e_new);
-                        inv *= e_new / (e_old + e_new);
-                        lse2 = top + log2f(e_old + e_new);
-                    }
+            if (HILO && w_cut > 0.f) inv *= w_sum * (1.f + kLowPart) / w_cut;
+            if (joins && out >= 0) {
+                const float z = __ldcg(ml), top = fmaxf(z, lse2);
+                if (z != -INFINITY || lse2 != -INFINITY) {
+                    const float e_old = fast_exp2(z - top), e_new = fast_exp2(lse2 - top);
+                    w_old = e_old / (e_old + e_new);
+                    inv *= e_new / (e_old + e_new);
+                    lse2 = top + log2f(e_old + e_new);
                 }
             }
             // 16 columns of the warp's rows through shared memory, so that four lanes
@@ -861,9 +865,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const PrefillArg
                     const int rl = i * 8 + (lane >> 2), col = c * 16 + (lane & 3) * 4;
                     float4 v = *reinterpret_cast<const float4 *>(stage + rl * SM::kStageLd + (lane & 3) * 4);
                     const int64_t r = __shfl_sync(0xffffffffu, out, rl);
-                    const float w = HILO ? __shfl_sync(0xffffffffu, w_old, rl) : 0.f;
+                    const float w = __shfl_sync(0xffffffffu, w_old, rl);
                     if (r < 0) continue;
-                    if (HILO && joins) {        // (the same thread wrote it)
+                    if (joins) {                // (the same thread wrote it)
                         const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((slot * 2 + g) * kPM + (warp & 3) * 32 + rl) * D + col));
                         v.x = fmaf(w, y.x, v.x);
                         v.y = fmaf(w, y.y, v.y);

@@ -244,3 +244,33 @@ def test_selections_of_more_visits_than_2_to_the_30(h):
     assert h.status() == 0
     want = np.broadcast_to(np.array([b for _, b in few], np.int32), (1, nq, 1, 3))
     u.check(o, lse, u.attention(c, q, sel=want))
+
+
+# ------------------------------------------------------- fp16 results over long lists
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp16_results_over_long_lists(h, D):
+    """Values of one sign over 524288 keys, a unit for every SM: the tensor core's truncated sums must
+    not show beside the roundings to fp16 of the weights and of the result, half a step (2^-11) each."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    n, Hk, nq = 1 << 19, 8, 64
+    S = max(1, torch.cuda.get_device_properties(0).multi_processor_count // Hk)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    k = torch.randint(-60, 61, (n // 64, 64, D), device="cuda", generator=g, dtype=torch.int8)
+    v = torch.randint(1, 128, (n // 64, 64, D), device="cuda", generator=g, dtype=torch.int8)
+    ks, vs = (torch.full((n // 64,), x, device="cuda") for x in (0.02, 0.01))
+    pool = skv.Q8Pool(k, v, ks, vs, k.amin(1), k.amax(1))
+    ids = torch.arange(n // 64, device="cuda", dtype=torch.int32).expand(S, Hk, -1).contiguous()   # (one list for all)
+    q = torch.randn((S, nq, Hk, D), device="cuda", generator=g).half()
+    o, _ = skv.q8_attn(h, pool, q, ids, torch.full((S,), n, dtype=torch.int32, device="cuda"), o_dtype=torch.float16)
+    assert h.status() == 0
+    kk = k.view(n, D).double() * float(ks[0])
+    for s in (0, S - 1):
+        x = q[s, ::16].reshape(-1, D).double()
+        want = torch.softmax(x @ kk.T * D ** -0.5, -1) @ (v.view(n, D).double() * float(vs[0]))
+        off = ((o[s, ::16].reshape(-1, D).double() - want).abs() / want).max().item()
+        # scores, as in q8_util: 2 (D + 4) 2^-23 A and 2^-18
+        A = ((x.abs() @ kk[:8192].abs().T).max() * D ** -0.5).item()
+        assert off <= 2.0 ** -10 + 2 * (D + 4) * 2.0 ** -23 * A + 2.0 ** -18
