@@ -1,6 +1,7 @@
 """The calls over 8-bit pages at their edges, against definitions in 64 bits: scales of
-either sign, rows beside pages that they do not see, rows that one key decides, lengths
-beyond their lists, and the borders between the forms of the choice."""
+either sign and far apart, rows beside pages that they do not see, rows that one key decides,
+very long lists and selections, lengths beyond their lists, and the borders between the forms
+of the choice."""
 import numpy as np
 import pytest
 
@@ -188,6 +189,36 @@ def test_fp32_rows_of_one_key(h, D, masked):
     assert h.status() == 0
 
 
+# ------------------------------------------------------- fp16 results over long lists
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp16_results_over_long_lists(h, D):
+    """Values of one sign over 524288 keys, a unit for every SM: the tensor core's truncated sums must
+    not show beside the roundings to fp16 of the weights and of the result, half a step (2^-11) each."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    n, Hk, nq = 1 << 19, 8, 64
+    S = max(1, torch.cuda.get_device_properties(0).multi_processor_count // Hk)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    k = torch.randint(-60, 61, (n // 64, 64, D), device="cuda", generator=g, dtype=torch.int8)
+    v = torch.randint(1, 128, (n // 64, 64, D), device="cuda", generator=g, dtype=torch.int8)
+    ks, vs = (torch.full((n // 64,), x, device="cuda") for x in (0.02, 0.01))
+    pool = skv.Q8Pool(k, v, ks, vs, k.amin(1), k.amax(1))
+    ids = torch.arange(n // 64, device="cuda", dtype=torch.int32).expand(S, Hk, -1).contiguous()   # (one list for all)
+    q = torch.randn((S, nq, Hk, D), device="cuda", generator=g).half()
+    o, _ = skv.q8_attn(h, pool, q, ids, torch.full((S,), n, dtype=torch.int32, device="cuda"), o_dtype=torch.float16)
+    assert h.status() == 0
+    kk = k.view(n, D).double() * float(ks[0])
+    for s in (0, S - 1):
+        x = q[s, ::16].reshape(-1, D).double()
+        want = torch.softmax(x @ kk.T * D ** -0.5, -1) @ (v.view(n, D).double() * float(vs[0]))
+        off = ((o[s, ::16].reshape(-1, D).double() - want).abs() / want).max().item()
+        # scores, as in q8_util: 2 (D + 4) 2^-23 A and 2^-18
+        A = ((x.abs() @ kk[:8192].abs().T).max() * D ** -0.5).item()
+        assert off <= 2.0 ** -10 + 2 * (D + 4) * 2.0 ** -23 * A + 2.0 ** -18
+
+
 # ------------------------------------------------------- lengths beyond their lists
 
 @pytest.mark.parametrize("nq,cap", [(1, 4), (3, 4), (1, 1500)])
@@ -246,31 +277,21 @@ def test_selections_of_more_visits_than_2_to_the_30(h):
     u.check(o, lse, u.attention(c, q, sel=want))
 
 
-# ------------------------------------------------------- fp16 results over long lists
+# ------------------------------------------------------- the borders of the choice
 
-@pytest.mark.parametrize("D", [64, 128])
-def test_fp16_results_over_long_lists(h, D):
-    """Values of one sign over 524288 keys, a unit for every SM: the tensor core's truncated sums must
-    not show beside the roundings to fp16 of the weights and of the result, half a step (2^-11) each."""
-    import torch
+@pytest.mark.parametrize("cap", [1024, 1025, 6144, 6145, 16384, 16385])
+@pytest.mark.parametrize("full", [True, False])
+def test_selection_at_the_borders_of_its_forms(h, cap, full):
+    """Lists of as many pages as one form of the choice holds and of one more, filled to the last
+    page or not, beside an empty one."""
     import split_kv_flash_attn_gb300 as skv
-    n, Hk, nq = 1 << 19, 8, 64
-    S = max(1, torch.cuda.get_device_properties(0).multi_processor_count // Hk)
-    g = torch.Generator(device="cuda")
-    g.manual_seed(D)
-    k = torch.randint(-60, 61, (n // 64, 64, D), device="cuda", generator=g, dtype=torch.int8)
-    v = torch.randint(1, 128, (n // 64, 64, D), device="cuda", generator=g, dtype=torch.int8)
-    ks, vs = (torch.full((n // 64,), x, device="cuda") for x in (0.02, 0.01))
-    pool = skv.Q8Pool(k, v, ks, vs, k.amin(1), k.amax(1))
-    ids = torch.arange(n // 64, device="cuda", dtype=torch.int32).expand(S, Hk, -1).contiguous()   # (one list for all)
-    q = torch.randn((S, nq, Hk, D), device="cuda", generator=g).half()
-    o, _ = skv.q8_attn(h, pool, q, ids, torch.full((S,), n, dtype=torch.int32, device="cuda"), o_dtype=torch.float16)
+    rng = np.random.default_rng(cap)
+    n = cap * u.PAGE - (0 if full else 65)
+    c = u.Cache(rng, [n, 0], 1, 64, cap=cap)
+    pool, ids, kv_len = c.on_gpu()
+    assert ids.shape[2] == cap
+    q = _q(rng, 2, 1, 2, 64)
+    for n_sel in (1, 100, cap - 1):
+        got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=n_sel, n_first=0, n_last=1)
+        assert np.array_equal(got.cpu().numpy(), u.select(c, q, n_sel, 0, 1))
     assert h.status() == 0
-    kk = k.view(n, D).double() * float(ks[0])
-    for s in (0, S - 1):
-        x = q[s, ::16].reshape(-1, D).double()
-        want = torch.softmax(x @ kk.T * D ** -0.5, -1) @ (v.view(n, D).double() * float(vs[0]))
-        off = ((o[s, ::16].reshape(-1, D).double() - want).abs() / want).max().item()
-        # scores, as in q8_util: 2 (D + 4) 2^-23 A and 2^-18
-        A = ((x.abs() @ kk[:8192].abs().T).max() * D ** -0.5).item()
-        assert off <= 2.0 ** -10 + 2 * (D + 4) * 2.0 ** -23 * A + 2.0 ** -18
