@@ -137,6 +137,38 @@ def test_a_far_value_scale_behind_a_row_s_limit(h, D, nq, H, Hk, f16):
     assert h.status() == 0
 
 
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("nq,causal", [(1, False), (3, True), (40, False), (40, True)])
+def test_far_scales_row_by_row(h, nq, causal, f16):
+    """Lists whose value scales lie up to 2^40 apart, absent pages, zero and negative scales: every row
+    within its own bound (a bound over all rows would pass zeros for the smaller ones)."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(nq + causal)
+    c = u.Cache(rng, [700, 640, 128, 300], 2, 128)
+    c.ids[0, 0, 3] = -1
+    c.ids[0, 1, 0] = -5
+    c.ids[2, 1, :2] = -1
+    for s in range(4):
+        for k in range(2):
+            p = c.ids[s, k][c.ids[s, k] >= 0]
+            c.vs[p] *= np.float32(2.0 ** (-12 if f16 else -40) * rng.random()) * rng.choice([-1, 1], len(p)).astype(np.float32)
+            if k:                                     # and far from one another within a list
+                c.vs[p] *= (2.0 ** rng.integers(-4 if f16 else -30, 10, len(p))).astype(np.float32)
+    c.vs[c.ids[1, 0, 1]] = 0.0
+    c.ks[c.ids[1, 1, 4]] = 0.0
+    c.ks[c.ids[0, 0, 1]] *= -1
+    pool, ids, kv_len = c.on_gpu()
+    q = _q(rng, 4, nq, 8, 128)
+    q_pos = (c.lens[:, None] - nq + np.arange(nq)[None]).astype(np.int32) if causal else None
+    if causal:
+        q_pos[:, ::2] = rng.integers(0, 700, q_pos[:, ::2].shape)
+    o, lse = skv.q8_attn(h, pool, _dev(q), ids, kv_len, q_pos=None if q_pos is None else _dev(q_pos),
+                         o_dtype=torch.float16 if f16 else None)
+    r.check(o, lse, r.attention(c, q, q_pos=q_pos), f16=f16)
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- rows that one key decides
 
 @pytest.mark.parametrize("D", [64, 128])
