@@ -461,7 +461,7 @@ int skv_bcache_pool(const skv_bcache *c, const void **k_pages, const void **v_pa
  * (all heads of a sequence hold the same number).  A negative page id is
  * absent: nothing is read and its keys do not exist.  A page id outside the
  * pool reads as absent and sets bit 2 of the device status word; a kv_len
- * beyond the list is cut to it and sets the same bit; a negative one is 0.  Entries
+ * beyond the list is cut to it and sets the same bit (an append has no page for such tokens: bit 1); a negative one is 0.  Entries
  * behind a sequence's last token are not read by attention and selection.
  * One page may stand in several lists as long as no append writes it.
  * A token the page does not hold yet may keep any bytes.  Scales are finite
@@ -512,10 +512,18 @@ int skv_q8_append(skv_handle *h, const skv_q8_pool *pool, int32_t S, int32_t Hk,
  * attention probabilities of its keys, summed over the tokens and the query
  * heads of the KV head, are added to it (in an order that does not change from
  * run to run).  o: o_type [S][nq][H][D] (SKV_F32 or SKV_F16), lse fp32
- * [S][nq][H]; a row that sees no key gets o = 0, lse = -inf.  fp32 results are
- * good to about 1e-6 (probabilities enter the value product in two fp16
- * parts) and can be merged with those of other partitions
- * (skv_attn_combine). */
+ * [S][nq][H]; a row that sees no key gets o = 0, lse = -inf.  Both can be merged with
+ * those of other partitions when o is fp32 (skv_attn_combine).
+ *
+ * Precision, relative to the largest |value| that the row sees, beside what its fp32
+ * scores leave.  SKV_F32: about 1e-6 (probabilities enter the value product in two
+ * fp16 parts), up to 5e-6 for rows that few keys decide when a KV head has more than 32
+ * rows (tokens x query heads; with sel, query heads).  SKV_F16: with up to 8 rows the fp32 result,
+ * rounded; with more a probability enters as one fp16 number, off by up to half a
+ * step (2^-11) like the result itself, so that errors are about 1.4 times those of the
+ * result's rounding (512 tokens over 32768 keys: 2.9e-4 of the result in the 2-norm where rounding alone
+ * leaves 2.1e-4).  Who wants more asks for SKV_F32.  A key with less than 2^-32 of the
+ * row's largest probability counts in lse, but may not in o. */
 int skv_q8_attn(skv_handle *h, const skv_q8_pool *pool, const skv_shape *shape, const void *q,
                 const int32_t *page_ids, int64_t pages_per_list, const int32_t *kv_len, const int32_t *q_pos,
                 const int32_t *sel, int32_t n_sel, float *mass, int32_t o_type, void *o, float *lse, void *stream);

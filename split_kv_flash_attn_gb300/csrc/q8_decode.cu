@@ -796,7 +796,10 @@ static int launch_d(skv_handle *h, const CUtensorMap &mk, const CUtensorMap &mv,
                     int nc, cudaStream_t st)
 {
     // One column group always takes both parts of the weights (its products are
-    // a small part of a page's time); two of them only when o is fp32.
+    // a small part of a page's time); two of them only when o is fp32.  For fp16 results the
+    // second part would cost 7 to 13 % (four tokens of eight sequences over 16000 keys, D = 128:
+    // 68.1 -> 75.1 us, D = 64: 46.1 -> 49.3; eight tokens over 32768: 39.5 -> 44.6) to take away an
+    // error as large as the result's own rounding.
     if (nc == 1)
         return f16 ? launch_one<D, 1, true, true>(h, mk, mv, a, grid, st)
                    : launch_one<D, 1, true, false>(h, mk, mv, a, grid, st);

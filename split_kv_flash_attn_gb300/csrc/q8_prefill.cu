@@ -10,7 +10,10 @@
 // m the row's reference (an integer, moved when a score passes it by 2^5), r the
 // pages' (moved when a scale passes it by 2^2), both by exact powers of two.
 // w stays below 2^15 and goes into the product as one fp16 number for fp16
-// results, as two (itself rounded, and what that left) for fp32 ones.
+// results, as two (itself rounded, and what that left) for fp32 ones.  One is off by up to
+// 2^-11 as the result's own rounding is, and both together by 1.4 times that rounding: 512 tokens over
+// 32768 keys 2.9e-4 of the result in the 2-norm, with two parts 2.1e-4 (the rounding
+// alone) at 291 us instead of 229.
 //
 // A CTA owns two 128-row query tiles of one KV head at a time (rows = tokens x
 // the head's query heads), so each decoded tile serves both:

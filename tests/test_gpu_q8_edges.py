@@ -327,3 +327,37 @@ def test_selection_at_the_borders_of_its_forms(h, cap, full):
         got = skv.q8_select(h, pool, _dev(q), ids, kv_len, n_sel=n_sel, n_first=0, n_last=1)
         assert np.array_equal(got.cpu().numpy(), u.select(c, q, n_sel, 0, 1))
     assert h.status() == 0
+
+
+# ------------------------------------------------------- results in fp16
+
+@pytest.mark.parametrize("lens,nq,H,Hk,D,sel", [([1000, 3, 517], 1, 16, 2, 128, False), ([5000], 2, 4, 1, 64, False), ([3000, 640], 5, 8, 1, 128, True)])
+def test_fp16_results_of_up_to_eight_rows_are_the_fp32_ones_rounded(h, lens, nq, H, Hk, D, sel):
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(nq + H)
+    c = u.Cache(rng, lens, Hk, D)
+    pool, ids, kv_len = c.on_gpu()
+    q = _dev(_q(rng, len(lens), nq, H, D))
+    s = _dev(rng.integers(-1, 12, (len(lens), nq, Hk, 9)).astype(np.int32)) if sel else None
+    o, lse = skv.q8_attn(h, pool, q, ids, kv_len, sel=s)
+    oo, ll = skv.q8_attn(h, pool, q, ids, kv_len, sel=s, o_dtype=torch.float16)
+    assert torch.equal(oo, o.half()) and torch.equal(ll, lse)
+
+
+@pytest.mark.parametrize("lens,nq,H,Hk,D", [([4000, 900], 3, 8, 2, 128), ([4000], 200, 4, 2, 128), ([2500, 77], 60, 2, 1, 64)])
+def test_fp16_results_of_more_rows(h, lens, nq, H, Hk, D):
+    """One fp16 number a weight and one a result, half a step (2^-11) of each: no further from the fp32
+    result than 2^-11 (sum p |v| + |o|), and 2^-17 for what the two differ by before."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(nq)
+    c = u.Cache(rng, lens, Hk, D)
+    pool, ids, kv_len = c.on_gpu()
+    q = _dev(_q(rng, len(lens), nq, H, D))
+    o, _ = skv.q8_attn(h, pool, q, ids, kv_len)
+    oo, _ = skv.q8_attn(h, pool, q, ids, kv_len, o_dtype=torch.float16)
+    pool.v.copy_(pool.v.abs())
+    size, _ = skv.q8_attn(h, pool, q, ids, kv_len)    # sum p |v| (the scales are positive)
+    vmax = 127 * float(c.vs.max())
+    assert ((oo.double() - o.double()).abs() <= 2.0 ** -11 * (size.double() + o.double().abs()) + 2.0 ** -17 * vmax).all()
