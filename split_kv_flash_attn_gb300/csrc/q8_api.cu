@@ -25,10 +25,12 @@ struct OnDevice {
 // Query rows of a KV head from which the tensor-core kernel serves: it computes 256
 // rows whatever is there, the decode kernel passes over the keys again for each 16.
 // Eight KV heads of D = 128, decode against tensor cores: 32768 keys of one sequence
-// 39.7 / 43.6 us at 32 rows and 49.7 / 43.6 at 48 with fp16 results (fp32: 44 / 59 and
-// 57 / 59); 8000 keys of eight sequences 66 / 65 us at 32 rows and 93 / 65 at 48
-// (fp32: 75 / 107 and 106 / 107; 190 / 107 at 96).  Over short contexts decode stays
-// ahead for longer, but by less (2000 keys of one sequence, fp32, 96 rows: 20 / 23 us).
+// 39.9 / 44.2 us at 32 rows and 49.8 / 44.0 at 36 with fp16 results (fp32: 44.4 / 60.5,
+// 57.3 / 60.3, and 74.5 / 60.4 at 64); 8000 keys of eight sequences 66.5 / 65.5 us at 32 rows
+// and 91.5 / 65.7 at 36 (fp32: 75 / 109, 104 / 108 and 132 / 108 at 64).  So the border is
+// fp16's; fp32 results of 33 to 48 rows lose 2 to 5 % by it.  Over short contexts it costs
+// both types a few us up to 128 rows (2000 keys of one sequence: 16.2 / 20.6 us at 36 rows and
+// 20.8 / 21.0 at 128, fp32 16.7 / 22.6 and 22.1 / 22.9): lengths are not known to the host.
 constexpr int kTcRows = 33;
 // Scratch for the pages' log sums or the selection's keys of one launch (one token's
 // at least).

@@ -39,9 +39,10 @@
 // the eight query columns of a product carry a KV head's query heads.
 //
 // Bound: the pages' bytes at long lengths (one sequence over 1048576 keys, eight KV
-// heads of D = 128: 316 us, 6.8 TB/s; eight sequences of up to 32768: 60 us, 5.3 TB/s,
+// heads of D = 128: 321 us, 6.7 TB/s; eight sequences of up to 32768: 60.8 us, 5.2 TB/s,
 // DRAM reads 316 MB, which is the pages); launch, look-ups and joins at short ones
-// (256 keys: 5.7 us).
+// (256 keys: 5.7 us); fetching and decoding the pages once for each 16 rows from 17 on
+// (8 sequences of 16000 keys: 68 us with 16 rows a KV head, 110 with 32).
 #include "q8.cuh"
 
 namespace skv {
@@ -53,8 +54,9 @@ constexpr int kStep = 32;           // keys a warp takes at a time
 constexpr uint32_t kStraddle = 8;   // pages that a second start and join of a CTA cost
 
 // Computing warps and as many ring slots.  One column group, D = 128: eight sequences of
-// up to 32768 keys take 60 us with 11 and 11, 63 with 7 and 7 or 8 and 8, 68 with 6 and
-// 12 (one of 1048576: 316, 334, 340 and 367); D = 64: 38.5 us with 15, 44 with 11.  Two
+// up to 32768 keys took 60 us with 11 and 11, 63 with 7 and 7 or 8 and 8, 68 with 6 and
+// 12 (one of 1048576: 316, 334, 340 and 367; before the warps voted on their waits, which
+// costs 1 %); D = 64: 38.5 us with 15, 44 with 11.  Two
 // groups need the registers of 7 warps with D = 128; with D = 64 (four tokens of
 // eight sequences over 16000 keys) 47.8 us with 10, 51.7 with 7.
 __host__ __device__ constexpr int warps_of(int D, int nc) { return nc == 1 ? (D == 64 ? 15 : 11) : (D == 64 ? 10 : 7); }

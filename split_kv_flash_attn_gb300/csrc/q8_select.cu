@@ -21,8 +21,8 @@
 // prefix sums over the warps' equal shares.  Ties at the n-th key go to the lowest
 // indices.
 //
-// Bound (select and attend over 16 of 128 pages: 18 us, of which 9 here; 512 of 4096
-// pages of 16 lists: 52 and 18): the scores by latency (lengths, ids, extremes and
+// Bound (select and attend over 16 of 128 pages: 18.5 us, of which 9 here; 512 of 4096
+// pages of 16 lists: 53 and 18): the scores by latency (lengths, ids, extremes and
 // queries are read one after the other, 2D + 8 bytes a page and head in all); the
 // choice by its counting rounds, each one pass over registers and one barrier, three or four until
 // few keys are left to each warp alone (cutting 64 lists of up to 2048 pages to 512 took
@@ -564,7 +564,8 @@ int launch_select(skv_handle *h, const SelectArgs &a, int D, cudaStream_t st)
     const dim3 grid(static_cast<unsigned>(pieces * parts), a.L.Hk, a.L.S);
     // One token a sequence and short lists: the choice by the last CTA of a list's scores.
     // As fast on the GPU (16 of 128 pages, with the attention: 18.6 against 18.4 us), and
-    // one launch less on the host (25 against 30 us a step).  By one CTA of 256 threads
+    // one launch less on the host (25 against 30 us a step on one box; 27 to 38 us as fused
+    // over several).  By one CTA of 256 threads
     // longer lists take longer (512 of 4096 pages: 67 us with the attention, 52 by a kernel of 512 threads).
     constexpr int kFused = 4;
     const bool fused = a.nq == 1 && a.L.cap <= kFused * kScoreWarps * 32 && lists <= kMaxUnits;
