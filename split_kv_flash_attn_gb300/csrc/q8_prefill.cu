@@ -86,8 +86,8 @@ constexpr uint32_t kSpins = 1u << 20;           // polls of a barrier before a w
 // 2.4e-6 too large).  Ten tiles of like weights, relative to the results: values of one sign
 // 3.0e-6 too small without, 5e-7 off with it; of both signs 2.1e-6 and 1.2e-6; few keys
 // that decide the row, values of one sign 6e-6 and 4e-6.  Time: 48.8 -> 49.5 us (64 tokens of
-// eight ragged sequences of up to 4096 keys); stretches of at most six tiles without it
-// 61 us and 1.5e-6 to 4e-6, of four 73 us and 1.2e-6 to 3.2e-6.
+// eight ragged sequences of up to 4096 keys); stretches of at most seven tiles without
+// it 61 us and 1.5e-6 to 4e-6, of five 73 us and 1.2e-6 to 3.2e-6.
 constexpr int kExactTiles = 8, kExactMore = 2;    // (up to that many more rather than another stretch)
 constexpr float kLowPart = 0x1p-12f;
 // fp16 results (single weights, nothing given back) take more: values of one sign lose 1.6e-6

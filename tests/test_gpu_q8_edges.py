@@ -251,6 +251,39 @@ def test_fp16_results_over_long_lists(h, D):
         assert off <= 2.0 ** -10 + 2 * (D + 4) * 2.0 ** -23 * A + 2.0 ** -18
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp16_results_of_long_pieces_across_units(h, D):
+    """160 units of 80 to 330 tiles, more than there are SMs, so that pieces of over 128 tiles begin and end
+    within units: fp16 results, log sums and weights beside the fp32 call's."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    rng = np.random.default_rng(D)
+    S, Hk, H, nq, n_pages = 20, 8, 16, 40, 700
+    lens = rng.integers(10000, 42000, S).astype(np.int32)
+    cap = int(-(-lens.max() // 64))
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()   # noqa: E731
+    k = rng.integers(-60, 61, (n_pages, 64, D)).astype(np.int8)
+    v = rng.integers(1, 128, (n_pages, 64, D)).astype(np.int8)
+    pool = skv.Q8Pool(dev(k), dev(v), dev(rng.uniform(0.01, 0.03, n_pages).astype(np.float32)),
+                      dev(rng.uniform(0.005, 0.02, n_pages).astype(np.float32)), dev(k.min(1)), dev(k.max(1)))
+    ids = rng.integers(-1, n_pages, (S, Hk, cap)).astype(np.int32)     # (pages in several lists, some absent)
+    q = _dev(_q(rng, S, nq, H, D))
+    pos = _dev((lens[:, None] - nq + np.arange(nq)[None]).astype(np.int32))
+    res = []
+    for t in (torch.float32, torch.float16):
+        mass = torch.zeros((S, Hk, cap), device="cuda")
+        res.append((*skv.q8_attn(h, pool, q, dev(ids), dev(lens), q_pos=pos, mass=mass, o_dtype=t), mass))
+    (o, lse, mass), (oo, ll, mm) = res
+    # values of one sign, so sum p |v| = |o|: half a step for the weights and one for the result
+    assert ((oo.double() - o.double()).abs() <= 2.0 ** -10 * o.double().abs() + 2.0 ** -17 * 127 * 0.02).all()
+    # the same scores, summed in other stretches: 2^-22 of the log sums, 2^-20 for their sums
+    assert ((ll - lse).abs() <= 2.0 ** -22 * lse.abs() + 2.0 ** -20).all()
+    assert ((mm - mass).abs() <= 2.0 ** -16 * mass + 2.0 ** -20).all()
+    one = skv.q8_attn(h, pool, q[7:8].contiguous(), dev(ids[7:8]), dev(lens[7:8]), q_pos=pos[7:8].contiguous())[0]
+    assert ((one - o[7:8]).abs() <= 2.0 ** -17 * 127 * 0.02).all()
+    assert h.status() == 0
+
+
 # ------------------------------------------------------- lengths beyond their lists
 
 @pytest.mark.parametrize("nq,cap", [(1, 4), (3, 4), (1, 1500)])
