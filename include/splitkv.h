@@ -562,6 +562,124 @@ int skv_q8_evict(skv_handle *h, int32_t S, int32_t Hk, int64_t pages_per_list, c
                  const float *mass, const int32_t *kv_len, int32_t n_keep, int32_t n_first, int32_t n_last,
                  int32_t *page_ids_out, float *mass_out, int32_t *kv_len_out, int32_t *freed_out, void *stream);
 
+/* ---- queries and keys before attention: norm and rotation -------------------
+ *
+ * Rows x of D values (one head of one token) become
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ * and then pairs of y turn by an angle that the token's positions give:
+ *   pair i < rot_dims/2: (a, b) = (y[i], y[i + rot_dims/2]), or (y[2i], y[2i+1]) when interleaved,
+ *   theta = pos[axis[i]][token] * freq[i],
+ *   a' = factor * (a cos theta - b sin theta),  b' = factor * (a sin theta + b cos theta);
+ * values from rot_dims on pass.  Everything is computed in fp32 and rounded once; an
+ * angle is reduced exactly in whole turns (64-bit fixed point of freq / 2 pi), so
+ * that far positions lose nothing.
+ *
+ * x_type, o_type: SKV_F32, SKV_F16 or SKV_BF16.  Token t's heads stand side by side,
+ * [heads][D], `stride` elements after token t-1's: q, k and v may be parts of one
+ * packed projection.  Bases and strides are multiples of 16 bytes.  D is 64 or 128;
+ * rot_dims is even and at most D, and a multiple of 16 unless interleaved.
+ * pos int32 [n_axes][n]; a token whose position on the first axis is negative is
+ * padding: its rows are not read, its results are zeros, and no cache row is
+ * written for it.  axis NULL: every pair turns with axis 0; entries are in
+ * [0, n_axes) (others count as 0).  weights fp32 [D]; freq fp32, axis int32
+ * [rot_dims/2]; all 4-byte aligned device memory.
+ * q or k may be left out (H or Hk 0).  The calls run on the handle's device,
+ * whichever is current. */
+#define SKV_BF16 4           /* element type of rows here */
+
+typedef struct skv_rope_spec {
+    int32_t D;
+    int32_t rot_dims;
+    int32_t interleaved;
+    int32_t n_axes;          /* 1 .. 8                                           */
+    const float *freq;       /* angle of a pair per position, non-negative       */
+    const int32_t *axis;     /* or NULL                                          */
+    float factor;            /* on cos and sin, usually 1                        */
+    float eps;
+} skv_rope_spec;
+
+/* q [n][H][D] -> q_out [n][H][D], k [n][Hk][D] -> k_out [n][Hk][D] (contiguous,
+ * o_type SKV_F32, SKV_F16 or SKV_BF16, not overlapping the inputs). */
+int skv_rope(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32_t H, int32_t Hk, int32_t x_type,
+             const void *q, int64_t q_stride, const void *k, int64_t k_stride, const float *q_weight,
+             const float *k_weight, const int32_t *pos, int32_t o_type, void *q_out, void *k_out, void *stream);
+
+/* Where rows go: a cache of two regions as for skv_kv_append. */
+typedef struct skv_cache_dst {
+    int32_t type;            /* SKV_F16 / SKV_Q8_0 / SKV_Q4_0                    */
+    int64_t row_bytes;
+    void *dst0;
+    int64_t n_rows0;
+    void *dst1;
+    int64_t n_rows1;
+} skv_cache_dst;
+
+/* skv_rope for serving: q goes to q_out (fp16, as attention takes it), k (turned)
+ * and v (as it is) straight into cache rows; what is stored is what
+ * skv_kv_append stores for the same fp32 rows.  positions int32 [n]: the cache
+ * position of each token (negative: nothing is written; one beyond the cache sets
+ * bit 1 of the device status word); pos are the positions of the rotation. */
+int skv_rope_append(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32_t H, int32_t Hk, int32_t x_type,
+                    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *q_weight, const float *k_weight, const int32_t *pos,
+                    const int32_t *positions, void *q_out, const skv_cache_dst *k_dst, const skv_cache_dst *v_dst,
+                    void *stream);
+
+/* Gradients of skv_rope: dq_out, dk_out (g_type, contiguous [n][H][D], [n][Hk][D])
+ * are those of its results; dq, dk (x_type, strides as above) receive those of q
+ * and k, and dq_weight, dk_weight (fp32 [D]; NULL where the weight is) those of
+ * the weights, summed over tokens and heads in an order that does not change from
+ * run to run.  q and k are read only where a weight is given.  Padding tokens get
+ * zeros and add nothing. */
+int skv_rope_backward(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32_t H, int32_t Hk, int32_t x_type,
+                      const void *q, int64_t q_stride, const void *k, int64_t k_stride, const float *q_weight,
+                      const float *k_weight, const int32_t *pos, int32_t g_type, const void *dq_out,
+                      const void *dk_out, void *dq, int64_t dq_stride, void *dk, int64_t dk_stride,
+                      float *dq_weight, float *dk_weight, void *stream);
+
+/* ---- gradients of attention ---------------------------------------------------
+ *
+ * Gradients of skv_attn_partial over fp16 rows for q, k and v, given o and lse
+ * (what the forward call gave), d_o = the gradient of o, and d_lse = the gradient
+ * of lse (NULL: none).  The probabilities are computed again:
+ *   p = exp(scale * q.k - lse) where the token sees the key, else 0,
+ *   delta = d_o.o - d_lse,  ds = p * (d_o.v - delta),
+ *   dv = sum p * d_o,  dk = scale * sum ds * q,  dq = scale * sum ds * k.
+ * Over one partition of several, give the merged o and lse with their gradients:
+ * dk and dv are then the partition's, and the partitions' dq add up.  So the combine
+ * needs no gradient of its own.
+ *
+ * The arguments up to key_pos0 and kv_begin, kv_end mean what they mean to
+ * skv_attn_partial; shape->k_type and v_type are SKV_F16, there is no additive
+ * mask.  o, lse fp32; d_o: do_type (SKV_F16 or SKV_F32), contiguous like o.
+ * Results, of g_type (SKV_F32 or SKV_F16):
+ *   dq [S][nq][H][D];
+ *   dk, dv [kv_end - kv_begin][Hk][D] over a dense range, summed over the
+ *   sequences, which share it;  with kv_rows [S][kv_end - kv_begin][Hk][D], entry
+ *   by entry of the lists (zeros for padding): a row that stands in several lists
+ *   gets its gradient as the sum of their entries, which is left to the caller.
+ * dq, or dk and dv together, may be NULL: that part is not computed.  A row with
+ * lse = -inf sees no key: its dq is zero, its q and d_o are not looked at.  Keys
+ * that no token sees are not looked at either and get zeros.  Every result is
+ * written whole; results do not change from run to run.
+ *
+ * Precision.  Products take fp16 operands and add in fp32: p, ds and an fp32 d_o enter
+ * them rounded to fp16 (half a step is 2^-11 of the value), scaled by powers of two
+ * so that neither long rows nor small gradients leave its range.  The scale of ds
+ * goes by the largest |d_o| and |v| that a key tile (for dk) or the query row (for
+ * dq) meets: tokens whose gradients are more than about 2^-20 of the largest one that
+ * meets the same 128 keys lose bits in dk (for fp32 d_o in dv too).
+ * A NaN or an infinity in a row of q, d_o, k or v that is seen spreads over the
+ * results of the 128 rows or keys that are computed with it.
+ *
+ * Limits: D 64 or 128; q, d_o, o, results 16-byte aligned, k, v and their row
+ * strides too; S*nq and kv_end below 2^31 - 256. */
+int skv_attn_backward(skv_handle *h, const skv_shape *shape, const void *q, const void *k, const void *v,
+                      const int32_t *q_pos, int64_t key_pos0, const int32_t *kv_rows, int64_t kv_rows_ld,
+                      int32_t kv_rows_per_head, int64_t kv_begin, int64_t kv_end, const float *o, const float *lse,
+                      int32_t do_type, const void *d_o, const float *d_lse, int32_t g_type, void *dq, void *dk,
+                      void *dv, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

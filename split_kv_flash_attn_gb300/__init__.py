@@ -18,6 +18,12 @@ streams.
     sel = q8_select(h, pool, q, page_ids, kv_len, n_sel=64)      # the pages of the largest score bounds ...
     o, lse = q8_attn(h, pool, q, page_ids, kv_len, sel=sel)      # ... and attention over those alone
     page_ids, mass, kv_len, freed = q8_evict(h, page_ids, mass, kv_len, n_keep=512)
+
+    spec = Rope(D, freq)                                         # rotation (and norm) of queries and keys
+    q = rope_append(h, spec, x_q, x_k, x_v, pos, rows, K, V)     # q as attention takes it; k, v into cache rows
+    q, k = rope(h, spec, x_q, x_k, pos, q_weight=wq, k_weight=wk)
+    dq, dk, dv = attn_backward(h, q, k, v, o, lse, d_o, Hk=8, q_pos=pos)
+    dx_q, dx_k, dwq, dwk = rope_backward(h, spec, dq, dk, pos, q=x_q, k=x_k, q_weight=wq, k_weight=wk)
 """
 from __future__ import annotations
 
@@ -25,11 +31,12 @@ import ctypes
 import math
 
 from . import _lib
-from ._lib import F16, F32, Q4_0, Q8_0, Q8_PAGE, SkvQ8Pool, SkvShape
+from ._lib import BF16, F16, F32, Q4_0, Q8_0, Q8_PAGE, SkvCacheDst, SkvQ8Pool, SkvRopeSpec, SkvShape
 
 __all__ = ["Handle", "SplitKVError", "F16", "Q8_0", "Q4_0", "attn_partial", "attn_combine", "attn_window_tail",
            "attn_paged", "BlockCache", "kv_dequant_q8_0", "kv_dequant_q4_0", "gather_rows", "kv_append", "plan_splits", "plan_prefill_splits", "plan_q8_tokens",
-           "segment_bytes", "Q8_PAGE", "Q8Pool", "q8_append", "q8_attn", "q8_select", "q8_evict"]
+           "segment_bytes", "Q8_PAGE", "Q8Pool", "q8_append", "q8_attn", "q8_select", "q8_evict",
+           "Rope", "rope", "rope_append", "rope_backward", "attn_backward"]
 
 
 class SplitKVError(RuntimeError):
@@ -598,3 +605,294 @@ def q8_evict(h: Handle, page_ids, mass, kv_len, *, n_keep, n_first=1, n_last=1, 
                                     int(n_keep), int(n_first), int(n_last), ids_out.data_ptr(), mass_out.data_ptr(),
                                     len_out.data_ptr(), freed.data_ptr(), st))
     return ids_out, mass_out, len_out, freed
+
+
+class Rope:
+    """How rows turn (see include/splitkv.h): freq fp32 [rot_dims/2] (device), the
+    angle of each pair per position; axis int32 [rot_dims/2]: the axis of pos that a
+    pair turns with (None: the first); interleaved: pairs (2i, 2i+1) instead of
+    (i, i + rot_dims/2); factor: on cos and sin; eps: of the norm.  The tensors stay
+    the caller's; the spec keeps references to them."""
+
+    def __init__(self, D, freq, *, axis=None, interleaved=False, factor=1.0, eps=1e-6, n_axes=None):
+        torch = _torch()
+        if freq.dim() != 1:
+            raise SplitKVError(1, f"freq: want fp32 [rot_dims/2], got {list(freq.shape)}")
+        half, self.device = int(freq.shape[0]), freq.get_device()
+        _need("freq", freq, torch.float32, (half,), self.device)
+        if axis is not None:
+            _need("axis", axis, torch.int32, (half,), self.device)
+            if n_axes is None:
+                n_axes = int(axis.max().item()) + 1 if half else 1
+        self.D, self.rot_dims, self.n_axes, self.freq, self.axis = int(D), 2 * half, int(n_axes or 1), freq, axis
+        self._c = SkvRopeSpec(self.D, 2 * half, int(bool(interleaved)), self.n_axes, freq.data_ptr(), _ptr(axis),
+                              float(factor), float(eps))
+        self._ref = ctypes.byref(self._c)
+
+
+_row_types = None
+
+
+def _row_type(name, x):
+    global _row_types
+    if _row_types is None:
+        torch = _torch()
+        _row_types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    t = _row_types.get(x if not hasattr(x, "dtype") else x.dtype)
+    if t is None:
+        raise SplitKVError(1, f"{name}: fp32, fp16 or bf16 is wanted, got {x if not hasattr(x, 'dtype') else x.dtype}")
+    return t
+
+
+def _token_rows(name, x, lead, D, dtype, device):
+    """Heads and token stride of rows [*lead, heads, D] whose heads stand side by side and whose tokens a fixed
+    stride apart (a part of a packed projection, say)."""
+    shape, stride, k = x.shape, x.stride(), len(lead)
+    ok = (len(shape) == k + 2 and shape[:k] == lead and shape[-1] == D and x.dtype is dtype and x.get_device() == device
+          and (stride[-1] == 1 and (stride[-2] == D or shape[-2] == 1) or x.numel() == 0))
+    step, want = 0, None
+    if ok:
+        for i in range(k - 1, -1, -1):
+            if shape[i] > 1:
+                if want is None:
+                    step = stride[i]
+                    want = step * shape[i]
+                elif stride[i] != want:
+                    ok = x.numel() == 0
+                    break
+                else:
+                    want *= shape[i]
+    if not ok:
+        raise SplitKVError(1, f"{name}: want {dtype} [{', '.join(map(str, lead))}, heads, {D}] on device {device} with heads side by side "
+                              f"and tokens a fixed stride apart, got {x.dtype} {list(shape)} of strides {list(stride)} on {x.device}")
+    return int(shape[-2]), int(step) if step else int(shape[-2]) * D
+
+
+def _tokens(lead):
+    n = 1
+    for m in lead:
+        n *= int(m)
+    return n
+
+
+def _positions(spec, pos, n):
+    torch = _torch()
+    if pos.dtype is not torch.int32 or pos.get_device() != spec.device or not pos.is_contiguous() or pos.numel() != n * spec.n_axes:
+        raise SplitKVError(1, f"pos: want contiguous int32 of {spec.n_axes} x {n} positions on device {spec.device}, "
+                              f"got {pos.dtype} {list(pos.shape)} on {pos.device}")
+    return pos.data_ptr()
+
+
+def _weights(spec, *pairs):
+    torch = _torch()
+    for name, w in pairs:
+        if w is not None:
+            _need(name, w, torch.float32, (spec.D,), spec.device)
+
+
+def _new(shape, dtype, like, stream, device):
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _on_stream(stream, device):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _rope_inputs(h, spec, q, k, pos, stream):
+    """(device, stream, leading shape, tokens, H, q stride, Hk, k stride, row type, pointer of pos)"""
+    some = q if q is not None else k
+    if some is None:
+        raise SplitKVError(1, "q or k is wanted")
+    lead, dev = tuple(some.shape[:-2]), spec.device
+    st = _q8_stream(h, stream, dev)
+    xt = _row_type("q" if q is not None else "k", some)
+    H, qs = _token_rows("q", q, lead, spec.D, some.dtype, dev) if q is not None else (0, 0)
+    Hk, ks = _token_rows("k", k, lead, spec.D, some.dtype, dev) if k is not None else (0, 0)
+    n = _tokens(lead)
+    return st, lead, n, H, qs, Hk, ks, xt, _positions(spec, pos, n)
+
+
+def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dtype=None, q_out=None, k_out=None,
+         stream=None):
+    """skv_rope: norm (where a weight fp32 [D] is given) and rotation of q [..., H, D] and k [..., Hk, D]
+    (fp32, fp16 or bf16; either may be None); pos int32 [n_axes, ...] (without the axis for one).
+    Results are fp16 unless o_dtype (or a given q_out, k_out) says otherwise."""
+    torch = _torch()
+    st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(h, spec, q, k, pos, stream)
+    _weights(spec, ("q_weight", q_weight), ("k_weight", k_weight))
+    if o_dtype is None:
+        o_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else torch.float16
+    ot = _row_type("o_dtype", o_dtype)
+    outs = []
+    for name, x, heads, out in (("q_out", q, H, q_out), ("k_out", k, Hk, k_out)):
+        if x is None:
+            out = None
+        elif out is None:
+            out = _new((*lead, heads, spec.D), o_dtype, x, stream, spec.device)
+        else:
+            _need(name, out, o_dtype, (*lead, heads, spec.D), spec.device)
+        outs.append(out)
+    rc = _lib.lib().skv_rope(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
+                             pp, ot, _ptr(outs[0]), _ptr(outs[1]), st)
+    if rc:
+        h.check(rc)
+    return outs[0], outs[1]
+
+
+def _cache_dst(name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes):
+    if type_ not in (F16, Q8_0, Q4_0):
+        raise SplitKVError(1, f"{name}: unknown element type {type_}")
+    if row_bytes is None:
+        row_bytes = Hk * segment_bytes(type_, D)
+    if n_rows0 is None:
+        n_rows0 = 0 if dst0 is None else dst0.numel() * dst0.element_size() // row_bytes
+    if n_rows1 is None:
+        n_rows1 = 0 if dst1 is None else dst1.numel() * dst1.element_size() // row_bytes
+    return SkvCacheDst(int(type_), int(row_bytes), _ptr(dst0), int(n_rows0), _ptr(dst1), int(n_rows1))
+
+
+def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, k_dst1=None, v_dst1=None, *,
+                q_weight=None, k_weight=None, k_type=F16, v_type=F16, n_rows0=None, n_rows1=None, k_row_bytes=None,
+                v_row_bytes=None, q_out=None, stream=None):
+    """skv_rope_append: norm and rotation of q [..., H, D] and k [..., Hk, D]; q is returned as fp16 rows, k and
+    v [..., Hk, D] go to the cache rows `positions` (int32 [...]) of two-region caches as for kv_append."""
+    torch = _torch()
+    if k is None or v is None:
+        raise SplitKVError(1, "k and v are wanted")
+    st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(h, spec, q, k, pos, stream)
+    Hv, vs = _token_rows("v", v, lead, spec.D, k.dtype, spec.device)
+    if Hv != Hk:
+        raise SplitKVError(1, f"v has {Hv} heads, k {Hk}")
+    _weights(spec, ("q_weight", q_weight), ("k_weight", k_weight))
+    if positions.dtype is not torch.int32 or positions.get_device() != spec.device or positions.numel() != n or not positions.is_contiguous():
+        raise SplitKVError(1, f"positions: want contiguous int32 of {n} positions on device {spec.device}")
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = _new((*lead, H, spec.D), torch.float16, q, stream, spec.device)
+    else:
+        _need("q_out", q_out, torch.float16, (*lead, H, spec.D), spec.device)
+    kd = _cache_dst("k_type", k_type, Hk, spec.D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes)
+    vd = _cache_dst("v_type", v_type, Hk, spec.D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes)
+    rc = _lib.lib().skv_rope_append(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                    _ptr(q_weight), _ptr(k_weight), pp, positions.data_ptr(), _ptr(q_out),
+                                    ctypes.byref(kd), ctypes.byref(vd), st)
+    if rc:
+        h.check(rc)
+    return q_out
+
+
+def rope_backward(h: Handle, spec: Rope, dq_out, dk_out, pos, *, q=None, k=None, q_weight=None, k_weight=None,
+                  x_dtype=None, dq=None, dk=None, stream=None):
+    """skv_rope_backward: (dq, dk, dq_weight, dk_weight) from the gradients of rope's results.  q, k: rope's
+    inputs, wanted where a weight is given; the gradients have their type, or x_dtype (the results' gradients'
+    type by default).  dq, dk may be given (rows of a packed gradient, say)."""
+    torch = _torch()
+    some = dq_out if dq_out is not None else dk_out
+    if some is None:
+        raise SplitKVError(1, "dq_out or dk_out is wanted")
+    lead, dev, D = tuple(some.shape[:-2]), spec.device, spec.D
+    st = _q8_stream(h, stream, dev)
+    gt = _row_type("dq_out" if dq_out is not None else "dk_out", some)
+    n = _tokens(lead)
+    pp = _positions(spec, pos, n)
+    _weights(spec, ("q_weight", q_weight), ("k_weight", k_weight))
+    if x_dtype is None:
+        x_dtype = next((x.dtype for x in (q, k, dq, dk) if x is not None), some.dtype)
+    xt = _row_type("x_dtype", x_dtype)
+    heads, xs, strides, outs, out_strides, dws = [], [], [], [], [], []
+    for name, g, x, w, out in (("q", dq_out, q, q_weight, dq), ("k", dk_out, k, k_weight, dk)):
+        if g is None:
+            if w is not None:
+                raise SplitKVError(1, f"{name}_weight without d{name}_out")
+            heads.append(0), xs.append(None), strides.append(0), outs.append(None), out_strides.append(0), dws.append(None)
+            continue
+        if g.dim() != len(lead) + 2:
+            raise SplitKVError(1, f"d{name}_out: want [..., heads, {D}], got {list(g.shape)}")
+        hd = int(g.shape[-2])
+        _need(f"d{name}_out", g, some.dtype, (*lead, hd, D), dev)
+        stride = 0
+        if w is not None:
+            if x is None:
+                raise SplitKVError(1, f"{name} is wanted with its weight")
+            xh, stride = _token_rows(name, x, lead, D, x_dtype, dev)
+            if xh != hd:
+                raise SplitKVError(1, f"{name} has {xh} heads, d{name}_out {hd}")
+        if out is None:
+            out = _new((*lead, hd, D), x_dtype, g, stream, dev)
+        oh, ostride = _token_rows(f"d{name}", out, lead, D, x_dtype, dev)
+        if oh != hd:
+            raise SplitKVError(1, f"d{name} has {oh} heads, d{name}_out {hd}")
+        heads.append(hd), xs.append(x if w is not None else None), strides.append(stride), outs.append(out)
+        out_strides.append(ostride)
+        dws.append(None if w is None else _new((D,), torch.float32, g, stream, dev))
+    rc = _lib.lib().skv_rope_backward(h._h, spec._ref, n, heads[0], heads[1], xt, _ptr(xs[0]), strides[0], _ptr(xs[1]),
+                                      strides[1], _ptr(q_weight), _ptr(k_weight), pp, gt, _ptr(dq_out), _ptr(dk_out),
+                                      _ptr(outs[0]), out_strides[0], _ptr(outs[1]), out_strides[1], _ptr(dws[0]),
+                                      _ptr(dws[1]), st)
+    if rc:
+        h.check(rc)
+    return outs[0], outs[1], dws[0], dws[1]
+
+
+def attn_backward(h: Handle, q, k, v, o, lse, d_o, *, Hk, scale=None, kv_begin=0, kv_end=None, kv_rows=None,
+                  kv_rows_per_head=False, q_pos=None, key_pos0=0, k_row_bytes=None, v_row_bytes=None, d_lse=None,
+                  need_dq=True, need_dkv=True, g_dtype=None, dq=None, dk=None, dv=None, stream=None):
+    """skv_attn_backward: (dq, dk, dv) of attn_partial over fp16 rows, from its o, lse and their gradients d_o (fp16
+    or fp32) and d_lse.  Results are fp32 unless g_dtype (or a given result) is torch.float16; need_dq=False or
+    need_dkv=False leaves a part out (None)."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(q.shape)}")
+    dev = q.get_device()
+    S, nq, H, D = (int(x) for x in q.shape)
+    st = _q8_stream(h, stream, dev)
+    _need("q", q, torch.float16, (S, nq, H, D), dev)
+    _need("o", o, torch.float32, (S, nq, H, D), dev)
+    _need("lse", lse, torch.float32, (S, nq, H), dev)
+    if d_o.dtype not in (torch.float16, torch.float32):
+        raise SplitKVError(1, f"d_o: fp16 or fp32 is wanted, got {d_o.dtype}")
+    _need("d_o", d_o, d_o.dtype, (S, nq, H, D), dev)
+    if d_lse is not None:
+        _need("d_lse", d_lse, torch.float32, (S, nq, H), dev)
+    if q_pos is not None:
+        _need("q_pos", q_pos, torch.int32, (S, nq), dev)
+    for name, x in (("k", k), ("v", v)):
+        if x.dtype is not torch.float16 or x.get_device() != dev:
+            raise SplitKVError(1, f"{name}: want fp16 rows on device {dev}, got {x.dtype} on {x.device}")
+        if not x.is_contiguous() and (k_row_bytes if name == "k" else v_row_bytes) is None:
+            raise SplitKVError(1, f"{name}: rows that are not contiguous need {name}_row_bytes")
+    Hk, per_head = int(Hk), bool(kv_rows_per_head)
+    rows_ld = 0
+    if kv_rows is not None:
+        rows_ld = int(kv_rows.shape[-1])
+        _need("kv_rows", kv_rows, torch.int32, (S, Hk, rows_ld) if per_head else (S, rows_ld), dev)
+    if kv_end is None:
+        kv_end = rows_ld if kv_rows is not None else int(k.shape[0])
+    kv_begin, kv_end = int(kv_begin), int(kv_end)
+    n = max(0, kv_end - kv_begin)
+    if kv_rows is None and (kv_end > k.shape[0] or kv_end > v.shape[0]):
+        raise SplitKVError(1, f"kv_end {kv_end} lies beyond k's {k.shape[0]} or v's {v.shape[0]} rows")
+    sh = _shape(q, Hk, F16, F16, k_row_bytes, v_row_bytes, scale)
+    if g_dtype is None:
+        g_dtype = next((x.dtype for x in (dq, dk, dv) if x is not None), torch.float32)
+    if g_dtype not in (torch.float16, torch.float32):
+        raise SplitKVError(1, f"g_dtype: fp32 or fp16 is wanted, got {g_dtype}")
+    kv_shape = (n, Hk, D) if kv_rows is None else (S, n, Hk, D)
+    outs = []
+    for name, x, shape, need in (("dq", dq, (S, nq, H, D), need_dq), ("dk", dk, kv_shape, need_dkv), ("dv", dv, kv_shape, need_dkv)):
+        if not need:
+            x = None
+        elif x is None:
+            x = _new(shape, g_dtype, q, stream, dev)
+        else:
+            _need(name, x, g_dtype, shape, dev)
+        outs.append(x)
+    rc = _lib.lib().skv_attn_backward(h._h, ctypes.byref(sh), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_pos),
+                                      int(key_pos0), _ptr(kv_rows), rows_ld, int(per_head), kv_begin, kv_end,
+                                      o.data_ptr(), lse.data_ptr(), F16 if d_o.dtype is torch.float16 else F32,
+                                      d_o.data_ptr(), _ptr(d_lse), F16 if g_dtype is torch.float16 else F32,
+                                      _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), st)
+    if rc:
+        h.check(rc)
+    return outs[0], outs[1], outs[2]

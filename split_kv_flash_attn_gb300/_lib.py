@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(PKG, "libsplitkv.so")
 SKV_OK = 0
 STATUS = {0: "SKV_OK", 1: "SKV_EINVAL", 2: "SKV_EUNSUPPORTED", 3: "SKV_ENOTPINNED", 4: "SKV_ENOMEM",
           5: "SKV_ECAPTURE", 6: "SKV_ECUDA", 7: "SKV_ETIMEOUT", 8: "SKV_EDEVICE"}
-F16, Q8_0, Q4_0, F32 = 0, 1, 2, 3
+F16, Q8_0, Q4_0, F32, BF16 = 0, 1, 2, 3, 4
 Q8_PAGE = 64
 
 # Every entry point that include/splitkv.h declares.
@@ -28,6 +28,7 @@ EXPORTS = [
     "skv_bcache_create_ring", "skv_bcache_ring_restore", "skv_bcache_ring_attn",
     "skv_attn_partial_static", "skv_plan_window", "skv_plan_tail_tile", "skv_selftest_wait_timeout",
     "skv_q8_append", "skv_q8_attn", "skv_q8_select", "skv_q8_evict", "skv_plan_q8_tokens",
+    "skv_rope", "skv_rope_append", "skv_rope_backward", "skv_attn_backward",
 ]
 
 
@@ -49,10 +50,22 @@ class SkvQ8Pool(ctypes.Structure):
                 ("k_max", ctypes.c_void_p)]
 
 
+class SkvRopeSpec(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int32), ("rot_dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("factor", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class SkvCacheDst(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("row_bytes", ctypes.c_int64), ("dst0", ctypes.c_void_p),
+                ("n_rows0", ctypes.c_int64), ("dst1", ctypes.c_void_p), ("n_rows1", ctypes.c_int64)]
+
+
 def _declare(lib):
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     SH = ctypes.POINTER(SkvShape)
     QP = ctypes.POINTER(SkvQ8Pool)
+    RP, CP = ctypes.POINTER(SkvRopeSpec), ctypes.POINTER(SkvCacheDst)
     sig = {
         "skv_create": ([ctypes.c_int, ctypes.POINTER(P)], ctypes.c_int),
         "skv_destroy": ([P], ctypes.c_int),
@@ -95,6 +108,12 @@ def _declare(lib):
         "skv_plan_q8_tokens": ([SH, I64, I32, I32, ctypes.POINTER(I32)], ctypes.c_int),
         "skv_q8_select": ([P, QP, SH, P, P, I64, P, P, I32, I32, I32, P, P], ctypes.c_int),
         "skv_q8_evict": ([P, I32, I32, I64, P, P, P, I32, I32, I32, P, P, P, P, P], ctypes.c_int),
+        "skv_rope": ([P, RP, I64, I32, I32, I32, P, I64, P, I64, P, P, P, I32, P, P, P], ctypes.c_int),
+        "skv_rope_append": ([P, RP, I64, I32, I32, I32, P, I64, P, I64, P, I64, P, P, P, P, P, CP, CP, P], ctypes.c_int),
+        "skv_rope_backward": ([P, RP, I64, I32, I32, I32, P, I64, P, I64, P, P, P, I32, P, P, P, I64, P, I64, P, P, P],
+                              ctypes.c_int),
+        "skv_attn_backward": ([P, SH, P, P, P, P, I64, P, I64, I32, I64, I64, P, P, I32, P, P, I32, P, P, P, P],
+                              ctypes.c_int),
         "skv_bcache_pool": ([P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(I64), ctypes.POINTER(P)],
                             ctypes.c_int),
     }

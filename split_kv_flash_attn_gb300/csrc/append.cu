@@ -35,40 +35,9 @@
 //    scale comes from the IEEE division.
 // The stored bytes are therefore those of the plain fp32 rule, bit for bit.
 #include "internal.h"
+#include "kv_encode.cuh"
 
 namespace skv {
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// fp16(fl(amax / qmax)) without a division unless the product could round
-// to another fp16 value (see the header).
-__device__ __forceinline__ __half block_scale(float amax, float qmax, float inv_qmax)
-{
-    const float s0 = __fmul_rn(amax, inv_qmax);
-    const __half h = __float2half_rn(s0);
-    const __half lo = __float2half_rn(__fmul_rn(s0, 1.f - 0x1p-20f));
-    const __half hi = __float2half_rn(__fmul_rn(s0, 1.f + 0x1p-20f));
-    if (__half_as_ushort(lo) == __half_as_ushort(h) && __half_as_ushort(hi) == __half_as_ushort(h)) return h;
-    return __float2half_rn(__fdiv_rn(amax, qmax));
-}
-
-// 1/d to within 2^-22 (relative), one instruction; d is a normal fp32 value.
-__device__ __forceinline__ float rcp_approx(float d)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-    return r;
-}
-
-// Bytes 0 of four words, in order, as one word.
-__device__ __forceinline__ uint32_t low_bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-}
 
 // Each warp takes kItemsPerWarp consecutive (row, head) items: it loads all of
 // their values first, then converts and stores, so a warp keeps several loads
@@ -165,11 +134,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_quant_kernel(const f
     constexpr int STEPS = kItemsPerWarp / IPS;
     static_assert(STEPS * IPS == kItemsPerWarp, "items per warp");
     constexpr int BLK = T == SKV_Q8_0 ? 34 : 18;
-    constexpr float QMAX = T == SKV_Q8_0 ? 127.f : 7.f;
-    constexpr float INV_QMAX = 1.f / QMAX;
     const int lane = threadIdx.x & 31;
     const int l = lane % LPI;                                     // lane within its item
-    const int b = l >> 2, j0 = (l & 3) * 8;                       // block, first value of the lane
+    const int b = l >> 2;                                         // block of the lane
     const int64_t total = static_cast<int64_t>(n) * Hk;
     const int64_t first =
         (static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5)) * kItemsPerWarp;
@@ -211,43 +178,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_quant_kernel(const f
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
         // every lane takes part in the block's shuffles; only valid items store
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[s][i]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const __half d16 = block_scale(amax, QMAX, INV_QMAX);
-        const float d = __half2float(d16);
-        const float rd = d > 0.f ? rcp_approx(d) : 0.f;           // d = 0: every code 0
-        int q[8];
-        float off = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t0 = __fmul_rn(v[s][i], rd);
-            const float r0 = rintf(t0);
-            off = fmaxf(off, fabsf(t0 - r0));
-            q[i] = static_cast<int>(r0);
-        }
-        if (off >= 0.5f - 0x1p-13f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __float2int_rn(__fdiv_rn(v[s][i], d));
-        }
-        if (d < 0x1p-14f) {
-            constexpr int QLO = T == SKV_Q8_0 ? -127 : -8, QHI = T == SKV_Q8_0 ? 127 : 7;   // codes -127..127, 0..15
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = max(QLO, min(QHI, q[i]));
-        }
-        uint32_t c[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = static_cast<uint32_t>(T == SKV_Q8_0 ? q[i] : q[i] + 8);
-        uint32_t w0 = low_bytes4(c[0], c[1], c[2], c[3]), w1 = low_bytes4(c[4], c[5], c[6], c[7]);
-        if (T == SKV_Q4_0) {
-            // byte j holds value j (low nibble) and value j + 16 (high nibble):
-            // the lane two further on holds values j0 + 16 ..
-            const uint32_t h0 = __shfl_down_sync(0xffffffffu, w0, 2), h1 = __shfl_down_sync(0xffffffffu, w1, 2);
-            w0 |= h0 << 4;
-            w1 |= h1 << 4;
-        }
+        __half d16;
+        uint32_t w0, w1;
+        encode8<T>(v[s], d16, w0, w1);
         const int64_t ps = p[s];
         if (ps < 0) continue;                                     // beyond the items, or not written
         const int h = hd[s];
@@ -257,20 +190,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_quant_kernel(const f
         }
         uint8_t *row = ps < n_rows0 ? dst0 + ps * row_bytes : dst1 + (ps - n_rows0) * row_bytes;
         uint8_t *blk = row + static_cast<int64_t>(h) * (DD / 32) * BLK + b * BLK;   // 2-byte aligned
-        if (T == SKV_Q8_0 || j0 < 16) {
-            uint16_t *dst = reinterpret_cast<uint16_t *>(blk + 2 + j0);
-            dst[0] = static_cast<uint16_t>(w0);
-            dst[1] = static_cast<uint16_t>(w0 >> 16);
-            dst[2] = static_cast<uint16_t>(w1);
-            dst[3] = static_cast<uint16_t>(w1 >> 16);
-        }
-        if (j0 == 0) *reinterpret_cast<__half *>(blk) = d16;
+        store8<T>(blk, l, d16, w0, w1);
     }
 }
 
 // A device-accessible address for a destination region: device memory as is,
 // page-locked host memory through its mapped device address.
-static int device_address(skv_handle *h, void *p, uint8_t **out)
+int device_address(skv_handle *h, void *p, uint8_t **out)
 {
     *out = nullptr;
     if (!p) return SKV_OK;

@@ -1,0 +1,230 @@
+// bwd_api.cu -- host side of skv_attn_backward: checks, geometry, scratch, launches.
+#include <string.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "bwd.cuh"
+
+namespace skv {
+namespace bwd {
+
+static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+static size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Fixed cost of a CTA of the two kernels, in tiles of 128 x 128 (about 1.2 us each): tensor
+// memory, barriers, row statistics, pipeline fill, result.
+constexpr int kOverheadTiles = 4;
+
+// Tokens x heads of a query tile: the fewest tiles, then the fewest heads (a tile of
+// one head has consecutive tokens, which see about the same keys).
+static void choose_tiles(Geo &g)
+{
+    int64_t best = INT64_MAX;
+    for (int gb = 1; gb <= std::min(g.G, kTile); ++gb) {
+        const int64_t tb = std::min<int64_t>(kTile / gb, g.T);
+        const int64_t tiles = (g.T + tb - 1) / tb * ((g.G + gb - 1) / gb);
+        if (tiles < best) {
+            best = tiles;
+            g.Gb = gb;
+            g.Tb = static_cast<int>(tb);
+        }
+    }
+    g.TT = static_cast<int>(std::min<int64_t>((g.T + g.Tb - 1) / g.Tb, INT32_MAX));
+    g.GG = (g.G + g.Gb - 1) / g.Gb;
+    g.QT = static_cast<int>(std::min<int64_t>(best, INT32_MAX));
+}
+
+// 5-D map over [groups][T][Hk][G][D] fp16 rows: a box is 64 values x Gb heads x Tb tokens.
+static int map_q(skv_handle *h, CUtensorMap *map, const void *base, const Geo &g)
+{
+    tc::EncodeTiledFn fn = tc::encode_fn();
+    if (!fn) return fail(h, SKV_ECUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t d = static_cast<cuuint64_t>(g.D);
+    cuuint64_t dims[5] = {d, static_cast<cuuint64_t>(g.G), static_cast<cuuint64_t>(g.Hk), static_cast<cuuint64_t>(g.T),
+                          static_cast<cuuint64_t>(g.groups)};
+    cuuint64_t strides[4] = {2 * d, 2 * d * g.G, 2 * d * g.H, g.groups > 1 ? 2 * d * g.H * g.T : 2 * d * g.H};
+    cuuint32_t box[5] = {64, static_cast<cuuint32_t>(g.Gb), 1, static_cast<cuuint32_t>(g.Tb), 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(h, SKV_EUNSUPPORTED, "tensor map encoding failed (%d)", static_cast<int>(r));
+    return SKV_OK;
+}
+
+// 3-D map over [groups][n][Hk * D] fp16 rows: a box is 64 values x 128 keys.
+static int map_k(skv_handle *h, CUtensorMap *map, const void *base, const Geo &g, int64_t row_bytes)
+{
+    tc::EncodeTiledFn fn = tc::encode_fn();
+    if (!fn) return fail(h, SKV_ECUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.Hk) * g.D, static_cast<cuuint64_t>(g.n), static_cast<cuuint64_t>(g.groups)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes * (g.groups > 1 ? g.n : 1))};
+    cuuint32_t box[3] = {64, kTile, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(h, SKV_EUNSUPPORTED, "tensor map encoding failed (%d)", static_cast<int>(r));
+    return SKV_OK;
+}
+
+static int check(skv_handle *h, const skv_shape *sh, const void *q, const void *k, const void *v, const int32_t *q_pos,
+                 const int32_t *kv_rows, int64_t kv_rows_ld, int64_t kv_begin, int64_t kv_end, const float *o, const float *lse,
+                 int32_t do_type, const void *d_o, const float *d_lse, int32_t g_type, void *dq, void *dk, void *dv)
+{
+    if (!sh) return fail(h, SKV_EINVAL, "shape is NULL");
+    if (sh->S < 1 || sh->nq < 1 || sh->H < 1 || sh->Hk < 1 || sh->H % sh->Hk)
+        return fail(h, SKV_EINVAL, "bad shape S=%d nq=%d H=%d Hk=%d", sh->S, sh->nq, sh->H, sh->Hk);
+    if (sh->D != 64 && sh->D != 128) return fail(h, SKV_EUNSUPPORTED, "head dim %d (supported: 64, 128)", sh->D);
+    if (sh->k_type != SKV_F16 || sh->v_type != SKV_F16) return fail(h, SKV_EUNSUPPORTED, "gradients are of fp16 rows");
+    if (!std::isfinite(sh->scale)) return fail(h, SKV_EINVAL, "scale is not finite");
+    if (kv_begin < 0 || kv_end < kv_begin)
+        return fail(h, SKV_EINVAL, "bad key range [%lld, %lld)", (long long)kv_begin, (long long)kv_end);
+    if (kv_rows && kv_rows_ld < kv_end) return fail(h, SKV_EINVAL, "kv_rows_ld smaller than kv_end");
+    if (static_cast<int64_t>(sh->S) * sh->nq > INT32_MAX - 256 || kv_end > INT32_MAX - 256)
+        return fail(h, SKV_EUNSUPPORTED, "S*nq or kv_end exceeds 2^31 - 256");
+    if (!q || !k || !v || !o || !lse || !d_o) return fail(h, SKV_EINVAL, "NULL pointer");
+    if (!dk != !dv) return fail(h, SKV_EINVAL, "dk and dv go together");
+    if (do_type != SKV_F16 && do_type != SKV_F32) return fail(h, SKV_EINVAL, "d_o: type %d (fp16 or fp32 is wanted)", do_type);
+    if (g_type != SKV_F16 && g_type != SKV_F32) return fail(h, SKV_EINVAL, "results: type %d (fp16 or fp32 is wanted)", g_type);
+    const int64_t seg = static_cast<int64_t>(sh->Hk) * sh->D * 2;
+    if (sh->k_row_bytes < seg || sh->v_row_bytes < seg) return fail(h, SKV_EINVAL, "row stride smaller than Hk head segments");
+    if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) || misaligned(d_o, 16) ||
+        misaligned(dq, 16) || misaligned(dk, 16) || misaligned(dv, 16) || sh->k_row_bytes % 16 || sh->v_row_bytes % 16)
+        return fail(h, SKV_EUNSUPPORTED, "q, k, v, o, d_o, results and row strides must be multiples of 16 bytes");
+    if (misaligned(lse, 4) || misaligned(d_lse, 4) || misaligned(q_pos, 4) || misaligned(kv_rows, 4))
+        return fail(h, SKV_EUNSUPPORTED, "lse, d_lse, q_pos and kv_rows must be 4-byte aligned");
+    // strides of a tensor map are below 2^40
+    if (sh->k_row_bytes >= int64_t(1) << 39 || sh->v_row_bytes >= int64_t(1) << 39)
+        return fail(h, SKV_EUNSUPPORTED, "row stride exceeds 2^39 bytes");
+    return SKV_OK;
+}
+
+}  // namespace bwd
+}  // namespace skv
+
+using namespace skv;
+
+extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const void *q, const void *k, const void *v,
+                                 const int32_t *q_pos, int64_t key_pos0, const int32_t *kv_rows, int64_t kv_rows_ld,
+                                 int32_t kv_rows_per_head, int64_t kv_begin, int64_t kv_end, const float *o,
+                                 const float *lse, int32_t do_type, const void *d_o, const float *d_lse, int32_t g_type,
+                                 void *dq, void *dk, void *dv, void *stream)
+{
+    using namespace bwd;
+    if (!h) return SKV_EINVAL;
+    h->err[0] = 0;
+    int rc = check(h, shape, q, k, v, q_pos, kv_rows, kv_rows_ld, kv_begin, kv_end, o, lse, do_type, d_o, d_lse, g_type, dq, dk, dv);
+    if (rc) return rc;
+    if (!dq && !dk) return SKV_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Geo g{};
+    g.groups = kv_rows ? shape->S : 1;
+    g.T = kv_rows ? shape->nq : static_cast<int64_t>(shape->S) * shape->nq;
+    g.Hk = shape->Hk;
+    g.H = shape->H;
+    g.G = shape->H / shape->Hk;
+    g.D = shape->D;
+    g.n = kv_end - kv_begin;
+    g.KT = static_cast<int>((g.n + kTile - 1) / kTile);
+    choose_tiles(g);
+    const int64_t units = static_cast<int64_t>(g.groups) * g.Hk;
+    if (g.QT > kMaxQTiles) return fail(h, SKV_EUNSUPPORTED, "%d query tiles of a KV head (at most %d)", g.QT, kMaxQTiles);
+    if (units * (g.KT + static_cast<int64_t>(g.QT)) > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many tiles for one launch");
+    if (g.groups > 1 && (2 * static_cast<int64_t>(g.H) * g.D * g.T >= int64_t(1) << 39 ||
+                         2 * static_cast<int64_t>(g.Hk) * g.D * g.n >= int64_t(1) << 39))
+        return fail(h, SKV_EUNSUPPORTED, "a sequence's rows exceed 2^39 bytes");
+    OnDevice on(h->device);
+    const size_t gs = g_type == SKV_F32 ? 4 : 2;
+    const int64_t q_vals = static_cast<int64_t>(g.groups) * g.T * g.H * g.D, k_vals = static_cast<int64_t>(g.groups) * g.n * g.Hk * g.D;
+    if (g.n == 0) {
+        if (dq) return cuda_fail(h, cudaMemsetAsync(dq, 0, static_cast<size_t>(q_vals) * gs, st), "clearing dq");
+        return SKV_OK;
+    }
+    // Pieces of a unit's tiles for grids that would leave SMs idle.
+    int64_t len = 0;
+    int32_t kv_pieces = 1, q_pieces = 1;
+    if (dk && (rc = plan_splits_cost(static_cast<int64_t>(g.QT) * kTile, units * g.KT, h->sm_count, 1, kTile, 0, kOverheadTiles, &len, &kv_pieces)))
+        return fail(h, rc, "piece planning failed");
+    if (dq && (rc = plan_splits_cost(g.n, units * g.QT, h->sm_count, 1, kTile, 0, kOverheadTiles, &len, &q_pieces)))
+        return fail(h, rc, "piece planning failed");
+    if (kv_pieces > 65535 || q_pieces > 65535) return fail(h, SKV_EUNSUPPORTED, "too many pieces");
+    const bool kv_slot = dk && (kv_pieces > 1 || g.QT > kStretch), q_slot = dq && (q_pieces > 1 || g.KT > kStretch);
+
+    // Scratch: row statistics, tile sums, exponents of the keys, rows gathered or converted, fp32 sums.
+    size_t need = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = need;
+        need += up(bytes);
+        return at;
+    };
+    const size_t q_tiles = static_cast<size_t>(units) * g.QT, k_tiles = static_cast<size_t>(units) * g.KT;
+    const size_t at_info = take(q_tiles * kInfoRows * kTile * 4);
+    const size_t at_sum = take(q_tiles * sizeof(TileSum));
+    const size_t at_ew = take(k_tiles * kTile);
+    const size_t at_do = take(do_type == SKV_F32 ? static_cast<size_t>(q_vals) * 2 : 0);
+    const size_t at_k = take(kv_rows ? static_cast<size_t>(k_vals) * 2 : 0);
+    const size_t at_v = take(kv_rows ? static_cast<size_t>(k_vals) * 2 : 0);
+    const size_t at_kv = take(kv_slot ? static_cast<size_t>(k_vals) * 2 * kv_pieces * 4 : 0);
+    const size_t at_q = take(q_slot ? static_cast<size_t>(q_vals) * q_pieces * 4 : 0);
+    if ((rc = ensure_workspace(h, need, st))) return rc;
+    uint8_t *ws = static_cast<uint8_t *>(h->workspace);
+
+    PrepArgs p{};
+    p.g = g;
+    p.d_o = d_o;
+    p.o = o;
+    p.lse = lse;
+    p.d_lse = d_lse;
+    p.q_pos = q_pos;
+    p.pos0 = key_pos0 + kv_begin;
+    p.doh = reinterpret_cast<__half *>(ws + at_do);
+    p.info = reinterpret_cast<float *>(ws + at_info);
+    p.sum = reinterpret_cast<TileSum *>(ws + at_sum);
+    p.k = static_cast<const uint8_t *>(k) + (kv_rows ? 0 : kv_begin * shape->k_row_bytes);
+    p.v = static_cast<const uint8_t *>(v) + (kv_rows ? 0 : kv_begin * shape->v_row_bytes);
+    p.k_row_bytes = shape->k_row_bytes;
+    p.v_row_bytes = shape->v_row_bytes;
+    p.rows = kv_rows ? kv_rows + kv_begin : nullptr;
+    p.rows_ld = kv_rows_ld;
+    p.rows_per_head = kv_rows_per_head ? 1 : 0;
+    p.kg = reinterpret_cast<__half *>(ws + at_k);
+    p.vg = reinterpret_cast<__half *>(ws + at_v);
+    p.ew = reinterpret_cast<int8_t *>(ws + at_ew);
+
+    const int64_t packed = static_cast<int64_t>(g.Hk) * g.D * 2;
+    CUtensorMap mq, mo, mk, mv;
+    rc = map_q(h, &mq, q, g);
+    if (!rc) rc = map_q(h, &mo, do_type == SKV_F32 ? static_cast<const void *>(p.doh) : d_o, g);
+    if (!rc) rc = map_k(h, &mk, kv_rows ? static_cast<const void *>(p.kg) : p.k, g, kv_rows ? packed : shape->k_row_bytes);
+    if (!rc) rc = map_k(h, &mv, kv_rows ? static_cast<const void *>(p.vg) : p.v, g, kv_rows ? packed : shape->v_row_bytes);
+    if (rc) return rc;
+    if ((rc = launch_prep(h, p, do_type, st))) return rc;
+
+    MainArgs a{};
+    a.g = g;
+    a.scale = shape->scale;
+    a.info = p.info;
+    a.sum = p.sum;
+    a.ew = p.ew;
+    a.g_type = g_type;
+    a.status = h->status;
+    if (dk) {
+        a.pieces = kv_pieces;
+        a.slot = kv_slot ? reinterpret_cast<float *>(ws + at_kv) : nullptr;
+        a.out0 = dk;
+        a.out1 = dv;
+        if ((rc = launch_kv(h, mq, mo, mk, mv, a, st))) return rc;
+        if (kv_pieces > 1 && (rc = launch_join(h, a.slot, kv_pieces, k_vals, 2, g_type, dk, dv, st))) return rc;
+    }
+    if (dq) {
+        a.pieces = q_pieces;
+        a.slot = q_slot ? reinterpret_cast<float *>(ws + at_q) : nullptr;
+        a.out0 = dq;
+        a.out1 = nullptr;
+        if ((rc = launch_q(h, mq, mo, mk, mv, a, st))) return rc;
+        if (q_pieces > 1 && (rc = launch_join(h, a.slot, q_pieces, q_vals, 1, g_type, dq, nullptr, st))) return rc;
+    }
+    return SKV_OK;
+}

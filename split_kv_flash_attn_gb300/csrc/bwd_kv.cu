@@ -1,0 +1,545 @@
+// bwd_kv.cu -- dk and dv: a CTA owns 128 keys of a KV head (TMEM lanes) and walks over
+// the query tiles that see one of them.
+//
+//   S^T  = K Q^T        [128 keys x 128 rows]   dP^T = V dO^T
+//   P^T  = 2^(S c - L)  over S in tensor memory, dS^T = P^T (dP^T sigma - D) over dP
+//   dV  += P^T dO       dK  += dS^T Q           (A from tensor memory)
+// Q and dO tiles are each the K-major B operand of one product and the MN-major one of the
+// other: one TMA load serves both.  Tensor memory is full: S, dP, dV, dK of 128 columns
+// (D = 64: two of 64).  So S and dP have one buffer each, and the tensor core turns
+// from one to the other: while the compute warps form P(j) it runs dK(j-1), dP(j), and
+// while they form dS(j) it runs dV(j), S(j+1).
+//
+// Warps: 0-7 compute (two threads a key, 64 rows of the tile each), 8 TMA, 9 issues S and
+// dV, 10 issues dP and dK (each pair in one thread, whose products run in order: the
+// buffers need no further wait), 11 looks each tile over when it has landed: it folds the powers of two
+// into L and D, tells whether the tile needs a mask, and clears rows of
+// tokens that see nothing, whatever they hold.
+//
+// Every mbarrier wait is bounded, as in the prefill kernel.
+#include <string.h>
+
+#include "bwd.cuh"
+
+namespace skv {
+namespace bwd {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kCompute = 256;
+constexpr int kStages = 2;
+constexpr int kHalf = kTile * 128;                           // a 64-column block of a tile
+
+template <int D>
+struct Lay {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kTileBytes;
+    static constexpr int kOffQ = 2 * kTileBytes;
+    static constexpr int kOffO = kOffQ + kStages * kTileBytes;
+    static constexpr int kOffInfo = kOffO + kStages * kTileBytes;
+    static constexpr int kOffBits = kOffInfo + kStages * kInfoBytes;      // bitmap of visited query tiles
+    static constexpr int kOffBar = kOffBits + kMaxQTiles / 8;
+    static constexpr int kBytes = kOffBar + 256 + 1024;                   // + alignment
+};
+static_assert(Lay<128>::kBytes <= 226 * 1024, "shared memory per CTA");
+
+enum { B_KV, B_QLAND, B_QFULL = B_QLAND + kStages, B_QEMPTY = B_QFULL + kStages, B_OLAND = B_QEMPTY + kStages,
+       B_OFULL = B_OLAND + kStages, B_OEMPTY = B_OFULL + kStages, B_S = B_OEMPTY + kStages, B_P, B_DP, B_DS, B_ACCV,
+       B_ACCK, B_COUNT };
+static_assert(B_COUNT * 8 <= 256, "barrier area");
+
+// Tensor memory columns.
+constexpr int kColS = 0, kColP = 128, kColV = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    splitkv_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
+                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const MainArgs a)
+{
+    using L = Lay<D>;
+    constexpr int kColK = kColV + D;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_addr(sm);
+    auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_count, s_lim, s_eN, s_eD, s_c, s_ew;
+    __shared__ int s_need[kStages];
+    __shared__ int s_list[kStretch];
+    uint32_t *bits = reinterpret_cast<uint32_t *>(sm + L::kOffBits);
+
+    const Geo &g = a.g;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // key tile slowest: under causal positions the first keys have the most rows
+    const int heads = g.Hk * g.groups;
+    const int kt = blockIdx.x / heads, gh = blockIdx.x - kt * heads;
+    const int group = gh / g.Hk, hk = gh - group * g.Hk;
+    const int piece = blockIdx.y;
+    const int64_t j0 = static_cast<int64_t>(kt) * kTile;
+    const int64_t tile0 = static_cast<int64_t>(gh) * g.QT;
+    const int box_rows = g.Gb * g.Tb;
+
+    if (tid == 0) {
+        s_abort = 0;
+        s_count = 0;
+        s_lim = 0;
+        s_eN = s_eD = kNoExp;
+        s_c = -1000;
+        s_ew = -100;
+    }
+    if (warp == 0) {
+        tc::tmem_alloc<512>(smem_addr(&s_tmem));
+        tc::tmem_relinquish();
+    }
+    if (tid == kCompute) {
+        tc::mbar_init(bar(B_KV), 1);
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(bar(B_QLAND + i), 1);
+            tc::mbar_init(bar(B_QFULL + i), 32);
+            tc::mbar_init(bar(B_QEMPTY + i), 1);
+            tc::mbar_init(bar(B_OLAND + i), 1);
+            tc::mbar_init(bar(B_OFULL + i), 32);
+            tc::mbar_init(bar(B_OEMPTY + i), 2);             // dP and dV of the tile
+        }
+        tc::mbar_init(bar(B_S), 1);
+        tc::mbar_init(bar(B_P), kCompute);
+        tc::mbar_init(bar(B_DP), 1);
+        tc::mbar_init(bar(B_DS), kCompute);
+        tc::mbar_init(bar(B_ACCV), 1);
+        tc::mbar_init(bar(B_ACCK), 1);
+        tc::fence_barrier_init();
+        tc::prefetch_tmap(&tq);
+        tc::prefetch_tmap(&to);
+    }
+    __syncthreads();
+    // ---- the query tiles that see one of these keys, and their sizes ----
+    {
+        int n = 0, lim = 0, eN = kNoExp, eD = kNoExp, c = -1000;
+        for (int b = 0; b < g.QT; b += kThreads) {
+            const int i = b + tid;
+            int4 s = make_int4(0, 0, 0, 0);
+            if (i < g.QT) s = __ldg(reinterpret_cast<const int4 *>(a.sum + tile0 + i));
+            const bool seen = i < g.QT && s.x > j0;
+            const uint32_t w = __ballot_sync(0xffffffffu, seen);
+            if (lane == 0 && b + warp * 32 < g.QT) bits[(b >> 5) + warp] = w;
+            if (seen) {
+                ++n;
+                lim = max(lim, s.x);
+                eN = max(eN, s.y);
+                eD = max(eD, s.z);
+                c = max(c, s.w);
+            }
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        lim = __reduce_max_sync(0xffffffffu, lim);
+        eN = __reduce_max_sync(0xffffffffu, eN);
+        eD = __reduce_max_sync(0xffffffffu, eD);
+        c = __reduce_max_sync(0xffffffffu, c);
+        if (lane == 0) {
+            atomicAdd(&s_count, n);
+            atomicMax(&s_lim, lim);
+            atomicMax(&s_eN, eN);
+            atomicMax(&s_eD, eD);
+            atomicMax(&s_c, c);
+        }
+        // rows that no TMA box writes
+        for (int i = tid; i < (kTile - box_rows) * (D / 8) * 2 * kStages; i += kThreads) {
+            const int per = (kTile - box_rows) * (D / 8);
+            const int buf = i / per, x = i - buf * per, r = box_rows + x / (D / 8), ch = x % (D / 8);
+            *reinterpret_cast<uint4 *>(sm + L::kOffQ + buf * L::kTileBytes + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async_smem();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int key_lane = (warp & 3) * 32 + lane;             // compute threads: their key
+    const int64_t key = j0 + key_lane;
+    bool there = false;
+    if (warp < 8) {
+        const int e = a.ew[(static_cast<int64_t>(gh) * g.KT + kt) * kTile + key_lane];
+        there = key < min(g.n, static_cast<int64_t>(s_lim)) && e != kAbsent;
+        if (there && warp < 4) atomicMax(&s_ew, e);
+    }
+    const int any = __syncthreads_or(there);
+    const int cmax = s_c > -1000 ? s_c : 0;
+    // 2^E bounds |d_o.v - delta| of these rows and keys
+    const int E = max(max(s_eN + s_ew, s_eD) + 1, cmax - 100);
+    const int sig_e = max(-100, min(100, cmax - E));
+    const float sigma = pow2(sig_e);
+    const int count = any ? s_count : 0;
+    const int o_lo = static_cast<int>(static_cast<int64_t>(count) * piece / a.pieces);
+    const int o_hi = static_cast<int>(static_cast<int64_t>(count) * (piece + 1) / a.pieces);
+
+    auto wait = [&](int b, uint32_t parity) -> bool {
+        if (tc::mbar_try_wait(bar(b), parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&s_abort)) return false;
+        if (bounded_wait(bar(b), parity, a.status)) return true;
+        s_abort = 1;
+        atomicOr(a.status, 1);
+        return false;
+    };
+
+    constexpr int NC = D / 2;                                // result columns of a compute thread
+    const int hf = warp >> 2;
+    const int64_t out_at = ((group * g.n + key) * g.Hk + hk) * D + hf * NC;
+    const int64_t out_all = static_cast<int64_t>(g.groups) * g.n * g.Hk * D;
+    float *slot_v = a.slot ? a.slot + (static_cast<int64_t>(piece) * 2 + 1) * out_all + out_at : nullptr;
+    float *slot_k = a.slot ? a.slot + static_cast<int64_t>(piece) * 2 * out_all + out_at : nullptr;
+
+    if (o_lo >= o_hi && warp < 8 && key < g.n) {             // nobody sees these keys
+        float z[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) z[i] = 0.f;
+        if (a.pieces > 1) {
+            store_row<NC>(slot_k, 0, SKV_F32, z);
+            store_row<NC>(slot_v, 0, SKV_F32, z);
+        } else {
+            store_row<NC>(a.out0, out_at, a.g_type, z);
+            store_row<NC>(a.out1, out_at, a.g_type, z);
+        }
+    }
+
+    int it0 = 0, stretch = 0;
+    for (int o = o_lo; o < o_hi; o += kStretch, ++stretch) {
+        const int nt = min(kStretch, o_hi - o);
+        if (warp == 0) {                                     // the tiles of ordinals o .. o + nt - 1
+            int before = 0;
+            const int words = (g.QT + 31) >> 5;
+            for (int w0 = 0; w0 < words && before < o + nt; w0 += 32) {
+                uint32_t w = w0 + lane < words ? bits[w0 + lane] : 0;
+                int pre = __popc(w);
+                const int mine = pre;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, pre, d);
+                    if (lane >= d) pre += x;
+                }
+                const int all = __shfl_sync(0xffffffffu, pre, 31);
+                int ord = before + pre - mine;
+                while (w) {
+                    const int b = __ffs(w) - 1;
+                    w &= w - 1;
+                    if (ord >= o && ord < o + nt) s_list[ord - o] = (w0 + lane) * 32 + b;
+                    ++ord;
+                }
+                before += all;
+            }
+        }
+        __syncthreads();
+
+        if (warp == 8) {
+            // ---------------- TMA ----------------------------------------
+            if (lane == 0) {
+                if (stretch == 0) {
+                    tc::mbar_expect_tx(bar(B_KV), 2 * L::kTileBytes);
+                    for (int b = 0; b < D / 64; ++b) {
+                        tc::tma_load_3d(sbase + L::kOffK + b * kHalf, &tk, hk * D + 64 * b, static_cast<int>(j0), group, bar(B_KV));
+                        tc::tma_load_3d(sbase + L::kOffV + b * kHalf, &tv, hk * D + 64 * b, static_cast<int>(j0), group, bar(B_KV));
+                    }
+                }
+                const uint32_t box = static_cast<uint32_t>(box_rows) * D * 2;
+                int q_out = 0, o_out = 0;                    // loads issued in this stretch
+                for (int i = 0; i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
+                    const int qt = s_list[i];
+                    const QTile t = q_tile(g, group, hk, qt);
+                    if (it >= kStages && !wait(B_QEMPTY + st, ph ^ 1)) break;
+                    tc::mbar_expect_tx(bar(B_QLAND + st), box + kInfoBytes);
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_5d(sbase + L::kOffQ + st * L::kTileBytes + b * kHalf, &tq, 64 * b, t.g0, hk,
+                                        static_cast<int>(t.t0), group, bar(B_QLAND + st));
+                    tc::bulk_load(sbase + L::kOffInfo + st * kInfoBytes, a.info + (tile0 + qt) * (kInfoRows * kTile), kInfoBytes,
+                                  bar(B_QLAND + st));
+                    ++q_out;
+                    if (it >= kStages && !wait(B_OEMPTY + st, ph ^ 1)) break;
+                    tc::mbar_expect_tx(bar(B_OLAND + st), box);
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_5d(sbase + L::kOffO + st * L::kTileBytes + b * kHalf, &to, 64 * b, t.g0, hk,
+                                        static_cast<int>(t.t0), group, bar(B_OLAND + st));
+                    ++o_out;
+                }
+                if (*reinterpret_cast<volatile int *>(&s_abort)) {
+                    // every load must land before the CTA exits
+                    tc::mbar_wait(bar(B_KV), 0, nullptr, 100000000ull);
+                    for (int i = max(0, q_out - kStages); i < q_out; ++i)
+                        tc::mbar_wait(bar(B_QLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
+                    for (int i = max(0, o_out - kStages); i < o_out; ++i)
+                        tc::mbar_wait(bar(B_OLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
+                }
+            }
+        } else if (warp == 9) {
+            // ---------------- S and dV ------------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
+                constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
+                const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, 16, 1024);
+                const uint64_t dq0 = tc::smem_desc(sbase + L::kOffQ, 16, 1024);
+                const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, kHalf, 1024);
+                int done = -1;                               // tile of this thread's last commit on B_S
+                auto issue_s = [&](int it) {
+                    const int st = it & (kStages - 1);
+                    if (!wait(B_QFULL + st, (it / kStages) & 1)) return false;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        tc::mma_f16_ss(tmem + kColS, tc::desc_add(dk0, off), tc::desc_add(dq0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                    }
+                    tc::mma_commit(bar(B_S));
+                    done = it;
+                    return true;
+                };
+                bool ok = wait(B_KV, 0) && issue_s(it0);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1);
+                    ok = wait(B_P, it & 1) && wait(B_OFULL + st, (it / kStages) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        tc::mma_f16_ts(tmem + kColV, tmem + kColS + (kk & 3) * 8 + (kk >> 2) * 64,
+                                       tc::desc_add(do0, st * L::kTileBytes + kk * 2048), kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(bar(B_OEMPTY + st));
+                    if (i + 1 < nt) ok = issue_s(it + 1);
+                    else tc::mma_commit(bar(B_ACCV));
+                }
+                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0) {
+                    tc::mma_commit(bar(B_ACCV));
+                    tc::mbar_wait(bar(B_ACCV), stretch & 1, nullptr, 100000000ull);
+                }
+            }
+        } else if (warp == 10) {
+            // ---------------- dP and dK -----------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
+                constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
+                const uint64_t dv0 = tc::smem_desc(sbase + L::kOffV, 16, 1024);
+                const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, 16, 1024);
+                const uint64_t dq0 = tc::smem_desc(sbase + L::kOffQ, kHalf, 1024);
+                int done = -1;
+                auto issue_p = [&](int it) {
+                    const int st = it & (kStages - 1);
+                    if (!wait(B_OFULL + st, (it / kStages) & 1)) return false;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        tc::mma_f16_ss(tmem + kColP, tc::desc_add(dv0, off), tc::desc_add(do0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                    }
+                    tc::mma_commit(bar(B_DP));
+                    tc::mma_commit(bar(B_OEMPTY + st));
+                    done = it;
+                    return true;
+                };
+                bool ok = wait(B_KV, 0) && issue_p(it0);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1);
+                    ok = wait(B_DS, it & 1) && wait(B_QFULL + st, (it / kStages) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        tc::mma_f16_ts(tmem + kColK, tmem + kColP + (kk & 3) * 8 + (kk >> 2) * 64,
+                                       tc::desc_add(dq0, st * L::kTileBytes + kk * 2048), kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(bar(B_QEMPTY + st));
+                    if (i + 1 < nt) ok = issue_p(it + 1);
+                    else tc::mma_commit(bar(B_ACCK));
+                }
+                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0) {
+                    tc::mma_commit(bar(B_ACCK));
+                    tc::mbar_wait(bar(B_ACCK), stretch & 1, nullptr, 100000000ull);
+                }
+            }
+        } else if (warp == 11) {
+            // ---------------- each tile as it has landed --------------------
+            for (int i = 0; i < nt; ++i) {
+                const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
+                bool ok = wait(B_QLAND + st, ph);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                float *info = reinterpret_cast<float *>(sm + L::kOffInfo + st * kInfoBytes);
+                float4 l4 = reinterpret_cast<float4 *>(info)[lane];
+                float4 d4 = reinterpret_cast<float4 *>(info + kTile)[lane];
+                const int4 c4 = reinterpret_cast<int4 *>(info + 2 * kTile)[lane];
+                const int4 m4 = reinterpret_cast<int4 *>(info + 3 * kTile)[lane];
+                l4.x += static_cast<float>(cmax - c4.x);
+                l4.y += static_cast<float>(cmax - c4.y);
+                l4.z += static_cast<float>(cmax - c4.z);
+                l4.w += static_cast<float>(cmax - c4.w);
+                d4.x *= sigma;
+                d4.y *= sigma;
+                d4.z *= sigma;
+                d4.w *= sigma;
+                reinterpret_cast<float4 *>(info)[lane] = l4;
+                reinterpret_cast<float4 *>(info + kTile)[lane] = d4;
+                auto cuts = [&](int m) { return m > 0 && m < j0 + kTile; };
+                const bool need = __any_sync(0xffffffffu, cuts(m4.x) || cuts(m4.y) || cuts(m4.z) || cuts(m4.w));
+                if (lane == 0) s_need[st] = need;
+                const uint32_t nib = (m4.x < 0) | (m4.y < 0) << 1 | (m4.z < 0) << 2 | (m4.w < 0) << 3;
+                const bool dirty = __any_sync(0xffffffffu, nib != 0);
+                auto clear = [&](int off) {
+                    for (int s = 0; s < 32; ++s) {
+                        uint32_t w = __shfl_sync(0xffffffffu, nib, s);
+                        while (w) {
+                            const int r = 4 * s + __ffs(w) - 1;
+                            w &= w - 1;
+                            if (lane < D / 8)
+                                *reinterpret_cast<uint4 *>(sm + off + st * L::kTileBytes + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                };
+                if (dirty) clear(L::kOffQ);
+                tc::mbar_arrive(bar(B_QFULL + st));
+                ok = wait(B_OLAND + st, ph);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (dirty) clear(L::kOffO);
+                tc::mbar_arrive(bar(B_OFULL + st));
+            }
+        } else {
+            // ---------------- P and dS --------------------------------------
+            const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            const float c1 = a.scale * 1.4426950408889634f;
+            for (int i = 0; i < nt; ++i) {
+                const int it = it0 + i, st = it & (kStages - 1);
+                const float *info = reinterpret_cast<const float *>(sm + L::kOffInfo + st * kInfoBytes) + hf * 64;
+                bool ok = wait(B_QFULL + st, (it / kStages) & 1);
+                ok = ok && wait(B_S, it & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+                const bool need = s_need[st] != 0;
+                float p[64];
+                {
+                    uint32_t r[2][32];
+                    tc::tmem_ld32(lane_base + kColS + hf * 64, r[0]);
+                    tc::tmem_ld32(lane_base + kColS + hf * 64 + 32, r[1]);
+                    tc::tmem_wait_ld(r[0]);
+                    tc::tmem_wait_ld(r[1]);
+                    uint32_t ph[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        const float4 l4 = *reinterpret_cast<const float4 *>(info + c);
+                        p[c] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][c & 31]), c1, -l4.x));
+                        p[c + 1] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][(c & 31) + 1]), c1, -l4.y));
+                        p[c + 2] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][(c & 31) + 2]), c1, -l4.z));
+                        p[c + 3] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][(c & 31) + 3]), c1, -l4.w));
+                    }
+                    if (need) {
+                        const int4 *lim = reinterpret_cast<const int4 *>(info + 3 * kTile);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const int4 m = lim[c >> 2];
+                            if (key >= m.x) p[c] = 0.f;
+                            if (key >= m.y) p[c + 1] = 0.f;
+                            if (key >= m.z) p[c + 2] = 0.f;
+                            if (key >= m.w) p[c + 3] = 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) ph[c] = pack_half2(p[2 * c], p[2 * c + 1]);
+                    tc::tmem_st32u(lane_base + kColS + hf * 64, ph);
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(bar(B_P));
+                ok = wait(B_DP, it & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+                uint32_t dh[32];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[32];
+                    tc::tmem_ld32(lane_base + kColP + hf * 64 + 32 * u, r);
+                    tc::tmem_wait_ld(r);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 d4 = *reinterpret_cast<const float4 *>(info + kTile + 32 * u + c);
+                        const float x0 = p[32 * u + c] * fmaf(__uint_as_float(r[c]), sigma, -d4.x);
+                        const float x1 = p[32 * u + c + 1] * fmaf(__uint_as_float(r[c + 1]), sigma, -d4.y);
+                        const float x2 = p[32 * u + c + 2] * fmaf(__uint_as_float(r[c + 2]), sigma, -d4.z);
+                        const float x3 = p[32 * u + c + 3] * fmaf(__uint_as_float(r[c + 3]), sigma, -d4.w);
+                        dh[16 * u + c / 2] = pack_half2(x0, x1);
+                        dh[16 * u + c / 2 + 1] = pack_half2(x2, x3);
+                    }
+                }
+                tc::tmem_st32u(lane_base + kColP + hf * 64, dh);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(bar(B_DS));
+            }
+            // ---------------- sums of this stretch ------------------------------
+            bool ok = !*reinterpret_cast<volatile int *>(&s_abort);
+            ok = ok && wait(B_ACCV, stretch & 1);
+            ok = ok && wait(B_ACCK, stretch & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc::tc_fence_after();
+                const bool last = o + kStretch >= o_hi;
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {    // dk, dv
+                    const Pow2 f(which ? 1.f : a.scale, which ? cmax - kPShift : cmax - sig_e - kPShift);
+                    float *slot = which ? slot_v : slot_k;
+                    float v[NC];
+#pragma unroll
+                    for (int u = 0; u < NC / 32; ++u) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(lane_base + (which ? kColV : kColK) + hf * NC + 32 * u, r);
+                        tc::tmem_wait_ld(r);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[32 * u + c] = there ? f(__uint_as_float(r[c])) : 0.f;
+                    }
+                    if (key < g.n) {
+                        if (stretch > 0) add_row<NC>(slot, v);
+                        if (last && a.pieces == 1) store_row<NC>(which ? a.out1 : a.out0, out_at, a.g_type, v);
+                        else store_row<NC>(slot, 0, SKV_F32, v);
+                    }
+                }
+                tc::tc_fence_before();
+            }
+        }
+        __syncwarp();
+        __syncthreads();
+        if (s_abort) break;
+        it0 += nt;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc<512>(tmem);
+    }
+}
+
+template <int D>
+KernelAttrCache &attr_cache()
+{
+    static KernelAttrCache c;
+    return c;
+}
+
+template <int D>
+int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
+             const MainArgs &a, cudaStream_t st)
+{
+    cudaError_t e = kernel_smem_optin(attr_cache<D>(), reinterpret_cast<const void *>(splitkv_bwd_kv_kernel<D>), Lay<D>::kBytes,
+                                      kThreads, nullptr);
+    if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(dk/dv)");
+    const dim3 grid(static_cast<unsigned>(a.g.KT * a.g.Hk * a.g.groups), static_cast<unsigned>(a.pieces));
+    splitkv_bwd_kv_kernel<D><<<grid, kThreads, Lay<D>::kBytes, st>>>(mq, mo, mk, mv, a);
+    return cuda_fail(h, cudaGetLastError(), "dk/dv kernel launch");
+}
+
+}  // namespace
+
+int launch_kv(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
+              const MainArgs &a, cudaStream_t st)
+{
+    return a.g.D == 64 ? launch_t<64>(h, mq, mo, mk, mv, a, st) : launch_t<128>(h, mq, mo, mk, mv, a, st);
+}
+
+}  // namespace bwd
+}  // namespace skv

@@ -1,0 +1,411 @@
+// bwd_q.cu -- dq: a CTA owns a query tile (TMEM lanes) and walks over the key tiles that it
+// sees.
+//
+//   S = Q K^T   dP = dO V^T   [128 rows x 128 keys]
+//   dS = 2^(S c - L) (dP sigma - D)   over S in tensor memory
+//   dQ += dS K                        (A from tensor memory)
+// K serves S as the K-major and dQ as the MN-major B operand: one TMA load for both.
+// Tensor memory: two S buffers, dP, dQ.  While the compute warps are at tile j, the tensor
+// core runs S(j+1), dQ(j-1) and, once dP(j) has been loaded, dP(j+1).
+//
+// Warps: 0-7 compute (two threads a row, 64 keys of the tile each; a row's L, D, sigma
+// and limit are registers), 8 TMA, 9 issues S and dP, 10 issues dQ, 11 looks each K tile
+// over: absent keys of lists, and rows behind the last key that any row sees, which
+// hold anything, are cleared.
+#include <string.h>
+
+#include "bwd.cuh"
+
+namespace skv {
+namespace bwd {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kCompute = 256;
+constexpr int kStages = 2;
+constexpr int kHalf = kTile * 128;
+
+template <int D>
+struct Lay {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffO = kTileBytes;
+    static constexpr int kOffK = 2 * kTileBytes;
+    static constexpr int kOffV = kOffK + kStages * kTileBytes;
+    static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+    static constexpr int kBytes = kOffBar + 256 + 1024;
+};
+static_assert(Lay<128>::kBytes <= 226 * 1024, "shared memory per CTA");
+
+enum { B_QO, B_KLAND, B_KFULL = B_KLAND + kStages, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
+       B_VEMPTY = B_VFULL + kStages, B_S = B_VEMPTY + kStages, B_DS = B_S + 2, B_DQ = B_DS + 2, B_DP = B_DQ + 2, B_DPFREE,
+       B_ACC, B_COUNT };
+static_assert(B_COUNT * 8 <= 256, "barrier area");
+
+constexpr int kColS = 0, kColP = 256, kColQ = 384;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    splitkv_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
+                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const MainArgs a)
+{
+    using L = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_addr(sm);
+    auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_ew, s_last;
+    __shared__ uint32_t s_here[kStages][4];                  // keys of a tile that are there
+
+    const Geo &g = a.g;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the last tokens first: under causal positions they see the most keys
+    const int heads = g.Hk * g.groups * g.GG;
+    const int ti = g.TT - 1 - blockIdx.x / heads, rest = blockIdx.x % heads;
+    const int gi = rest % g.GG, gh = rest / g.GG;
+    const int group = gh / g.Hk, hk = gh - group * g.Hk;
+    const int qt = gi * g.TT + ti;
+    const int64_t tile = static_cast<int64_t>(gh) * g.QT + qt;
+    const QTile t = q_tile(g, group, hk, qt);
+    const int box_rows = g.Gb * g.Tb;
+    const int lim_tile = a.sum[tile].lim_max;
+
+    if (tid == 0) {
+        s_abort = 0;
+        s_ew = -100;
+        s_last = -1;
+    }
+    if (warp == 0) {
+        tc::tmem_alloc<512>(smem_addr(&s_tmem));
+        tc::tmem_relinquish();
+    }
+    if (tid == kCompute) {
+        tc::mbar_init(bar(B_QO), 1);
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(bar(B_KLAND + i), 1);
+            tc::mbar_init(bar(B_KFULL + i), 32);
+            tc::mbar_init(bar(B_KEMPTY + i), 1);
+            tc::mbar_init(bar(B_VFULL + i), 1);
+            tc::mbar_init(bar(B_VEMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(B_S + i), 1);
+            tc::mbar_init(bar(B_DS + i), kCompute);
+            tc::mbar_init(bar(B_DQ + i), 1);
+        }
+        tc::mbar_init(bar(B_DP), 1);
+        tc::mbar_init(bar(B_DPFREE), kCompute);
+        tc::mbar_init(bar(B_ACC), 1);
+        tc::fence_barrier_init();
+        tc::prefetch_tmap(&tk);
+        tc::prefetch_tmap(&tv);
+    }
+    __syncthreads();
+    // ---- the largest |v| of the keys that the tile sees, and the last key that is there ----
+    {
+        const int4 *ew = reinterpret_cast<const int4 *>(a.ew + static_cast<int64_t>(gh) * g.KT * kTile);
+        int top = -100, last = -1;
+        for (int i = tid; i < (lim_tile + 15) / 16; i += kThreads) {
+            const int4 x = __ldg(ew + i);
+            const int w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int b = 0; b < 16; ++b) {
+                const int e = static_cast<int8_t>(w[b >> 2] >> (8 * (b & 3)));
+                if (e != kAbsent && 16 * i + b < lim_tile) {
+                    top = max(top, e);
+                    last = 16 * i + b;
+                }
+            }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        last = __reduce_max_sync(0xffffffffu, last);
+        if (lane == 0) {
+            atomicMax(&s_ew, top);
+            atomicMax(&s_last, last);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int n_all = (s_last + kTile) / kTile;              // key tiles up to the last key
+    const int j_lo = static_cast<int>(static_cast<int64_t>(n_all) * blockIdx.y / a.pieces);
+    const int j_hi = static_cast<int>(static_cast<int64_t>(n_all) * (blockIdx.y + 1) / a.pieces);
+
+    auto wait = [&](int b, uint32_t parity) -> bool {
+        if (tc::mbar_try_wait(bar(b), parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&s_abort)) return false;
+        if (bounded_wait(bar(b), parity, a.status)) return true;
+        s_abort = 1;
+        atomicOr(a.status, 1);
+        return false;
+    };
+
+    // ---- a compute thread's row ----
+    constexpr int NC = D / 2;
+    const int m = (warp & 3) * 32 + lane, hf = warp >> 2;
+    float row_L = INFINITY, row_D = 0.f, sigma = 1.f;
+    int lim = 0, out_e = 0;
+    int64_t row = -1;
+    if (warp < 8) {
+        const float *info = a.info + tile * (kInfoRows * kTile) + m;
+        row_L = info[0];
+        lim = max(0, __float_as_int(info[3 * kTile]));
+        const int c = __float_as_int(info[2 * kTile]), ex = __float_as_int(info[4 * kTile]);
+        const int e = max(-100, min(100, max((ex >> 16) + s_ew, static_cast<int>(static_cast<int16_t>(ex & 0xffff))) + 1));
+        sigma = pow2(-e);
+        row_D = info[kTile] * sigma;
+        out_e = e + c - kPShift;
+        row = q_row(g, t, m);
+    }
+    const int64_t out_all = static_cast<int64_t>(g.groups) * g.T * g.H * D;
+    const int64_t out_at = row * D + hf * NC;
+    float *slot = a.slot ? a.slot + static_cast<int64_t>(blockIdx.y) * out_all + out_at : nullptr;
+
+    if (j_lo >= j_hi && row >= 0) {                          // no keys
+        float z[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) z[i] = 0.f;
+        if (a.pieces > 1) store_row<NC>(slot, 0, SKV_F32, z);
+        else store_row<NC>(a.out0, out_at, a.g_type, z);
+    }
+
+    int it0 = 0, stretch = 0;
+    for (int j = j_lo; j < j_hi; j += kStretch, ++stretch) {
+        const int nt = min(kStretch, j_hi - j);
+        if (warp == 8) {
+            // ---------------- TMA ----------------------------------------
+            if (lane == 0) {
+                if (stretch == 0) {
+                    tc::mbar_expect_tx(bar(B_QO), 2u * box_rows * D * 2);
+                    for (int b = 0; b < D / 64; ++b) {
+                        tc::tma_load_5d(sbase + L::kOffQ + b * kHalf, &tq, 64 * b, t.g0, hk, static_cast<int>(t.t0), group, bar(B_QO));
+                        tc::tma_load_5d(sbase + L::kOffO + b * kHalf, &to, 64 * b, t.g0, hk, static_cast<int>(t.t0), group, bar(B_QO));
+                    }
+                }
+                int k_out = 0, v_out = 0;
+                for (int i = 0; i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
+                    const int y = (j + i) * kTile;
+                    if (it >= kStages && !wait(B_KEMPTY + st, ph ^ 1)) break;
+                    tc::mbar_expect_tx(bar(B_KLAND + st), L::kTileBytes);
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_3d(sbase + L::kOffK + st * L::kTileBytes + b * kHalf, &tk, hk * D + 64 * b, y, group, bar(B_KLAND + st));
+                    ++k_out;
+                    if (it >= kStages && !wait(B_VEMPTY + st, ph ^ 1)) break;
+                    tc::mbar_expect_tx(bar(B_VFULL + st), L::kTileBytes);
+                    for (int b = 0; b < D / 64; ++b)
+                        tc::tma_load_3d(sbase + L::kOffV + st * L::kTileBytes + b * kHalf, &tv, hk * D + 64 * b, y, group, bar(B_VFULL + st));
+                    ++v_out;
+                }
+                if (*reinterpret_cast<volatile int *>(&s_abort)) {
+                    tc::mbar_wait(bar(B_QO), 0, nullptr, 100000000ull);
+                    for (int i = max(0, k_out - kStages); i < k_out; ++i)
+                        tc::mbar_wait(bar(B_KLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
+                    for (int i = max(0, v_out - kStages); i < v_out; ++i)
+                        tc::mbar_wait(bar(B_VFULL + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
+                }
+            }
+        } else if (warp == 9) {
+            // ---------------- S and dP ------------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
+                const uint64_t dq0 = tc::smem_desc(sbase + L::kOffQ, 16, 1024);
+                const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, 16, 1024);
+                const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, 16, 1024);
+                const uint64_t dv0 = tc::smem_desc(sbase + L::kOffV, 16, 1024);
+                int done = -1;
+                bool ok = wait(B_QO, 0);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1), sb = it & 1;
+                    ok = wait(B_KFULL + st, (it / kStages) & 1);
+                    // the buffer's last dS has been read
+                    ok = ok && (it < 2 || wait(B_DQ + sb, ((it >> 1) - 1) & 1));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        tc::mma_f16_ss(tmem + kColS + sb * kTile, tc::desc_add(dq0, off), tc::desc_add(dk0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                    }
+                    tc::mma_commit(bar(B_S + sb));
+                    ok = wait(B_VFULL + st, (it / kStages) & 1) && (it < 1 || wait(B_DPFREE, (it - 1) & 1));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        tc::mma_f16_ss(tmem + kColP, tc::desc_add(do0, off), tc::desc_add(dv0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                    }
+                    tc::mma_commit(bar(B_DP));
+                    tc::mma_commit(bar(B_VEMPTY + st));
+                    done = it;
+                }
+                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
+                    tc::mbar_wait(bar(B_DP), done & 1, nullptr, 100000000ull);
+            }
+        } else if (warp == 10) {
+            // ---------------- dQ --------------------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kIdescQ = tc::idesc_f16(kTile, D, true);
+                const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, kHalf, 1024);
+                int done = -1;
+                for (int i = 0; i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1), sb = it & 1;
+                    if (!wait(B_DS + sb, (it >> 1) & 1) || !wait(B_KFULL + st, (it / kStages) & 1)) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        tc::mma_f16_ts(tmem + kColQ, tmem + kColS + sb * kTile + (kk & 3) * 8 + (kk >> 2) * 64,
+                                       tc::desc_add(dk0, st * L::kTileBytes + kk * 2048), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(bar(B_KEMPTY + st));
+                    tc::mma_commit(bar(B_DQ + sb));
+                    if (i + 1 == nt) tc::mma_commit(bar(B_ACC));
+                    done = it;
+                }
+                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
+                    tc::mbar_wait(bar(B_DQ + (done & 1)), (done >> 1) & 1, nullptr, 100000000ull);
+            }
+        } else if (warp == 11) {
+            // ---------------- each K tile as it has landed -------------------
+            const int8_t *ew = a.ew + static_cast<int64_t>(gh) * g.KT * kTile;
+            for (int i = 0; i < nt; ++i) {
+                const int it = it0 + i, st = it & (kStages - 1);
+                const int jt = (j + i) * kTile;
+                const uint32_t e4 = *reinterpret_cast<const uint32_t *>(ew + jt + 4 * lane);
+                uint32_t w = 0;                              // this lane's four keys
+#pragma unroll
+                for (int b = 0; b < 4; ++b) w |= (((e4 >> (8 * b)) & 255u) != 128u ? 1u : 0u) << b;
+                w <<= 4 * (lane & 7);
+                w |= __shfl_xor_sync(0xffffffffu, w, 1);
+                w |= __shfl_xor_sync(0xffffffffu, w, 2);
+                w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                bool ok = wait(B_KLAND + st, (it / kStages) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if ((lane & 7) == 0) s_here[st][lane >> 3] = w;
+                if (jt + kTile > lim_tile) {                 // rows that no token of the tile sees
+                    for (int x = lane; x < (jt + kTile - lim_tile) * (D / 8); x += 32) {
+                        const int r = lim_tile - jt + x / (D / 8), ch = x % (D / 8);
+                        *reinterpret_cast<uint4 *>(sm + L::kOffK + st * L::kTileBytes + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_proxy_async_smem();
+                }
+                tc::mbar_arrive(bar(B_KFULL + st));
+            }
+        } else {
+            // ---------------- dS --------------------------------------------
+            const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            const float c1 = a.scale * 1.4426950408889634f;
+            for (int i = 0; i < nt; ++i) {
+                const int it = it0 + i, st = it & (kStages - 1), sb = it & 1;
+                const uint32_t cs = lane_base + kColS + sb * kTile + hf * 64;
+                bool ok = wait(B_KFULL + st, (it / kStages) & 1);
+                const uint32_t h0 = s_here[st][hf * 2], h1 = s_here[st][hf * 2 + 1];
+                const int left = lim - (j + i) * kTile - hf * 64;        // columns of this half that the row sees
+                ok = ok && wait(B_S + sb, (it >> 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+                float p[64];
+                {
+                    uint32_t r[2][32];
+                    tc::tmem_ld32(cs, r[0]);
+                    tc::tmem_ld32(cs + 32, r[1]);
+                    tc::tmem_wait_ld(r[0]);
+                    tc::tmem_wait_ld(r[1]);
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) p[c] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][c & 31]), c1, -row_L));
+                }
+                ok = wait(B_DP, it & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+                uint32_t r[2][32];
+                tc::tmem_ld32(lane_base + kColP + hf * 64, r[0]);
+                tc::tmem_ld32(lane_base + kColP + hf * 64 + 32, r[1]);
+                tc::tmem_wait_ld(r[0]);
+                tc::tmem_wait_ld(r[1]);
+                tc::tc_fence_before();
+                tc::mbar_arrive(bar(B_DPFREE));
+#pragma unroll
+                for (int c = 0; c < 64; ++c) p[c] *= fmaf(__uint_as_float(r[c >> 5][c & 31]), sigma, -row_D);
+                if (__any_sync(0xffffffffu, left < 64 || (h0 & h1) != 0xffffffffu)) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= left || !(((c < 32 ? h0 : h1) >> (c & 31)) & 1u)) p[c] = 0.f;
+                }
+                uint32_t dh[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) dh[c] = pack_half2(p[2 * c], p[2 * c + 1]);
+                tc::tmem_st32u(cs, dh);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(bar(B_DS + sb));
+            }
+            // ---------------- the sum of this stretch ----------------------------
+            bool ok = !*reinterpret_cast<volatile int *>(&s_abort);
+            ok = ok && wait(B_ACC, stretch & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc::tc_fence_after();
+                const Pow2 f(a.scale, out_e);
+                float v[NC];
+#pragma unroll
+                for (int u = 0; u < NC / 32; ++u) {
+                    uint32_t r[32];
+                    tc::tmem_ld32(lane_base + kColQ + hf * NC + 32 * u, r);
+                    tc::tmem_wait_ld(r);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[32 * u + c] = lim > 0 ? f(__uint_as_float(r[c])) : 0.f;
+                }
+                if (row >= 0) {
+                    if (stretch > 0) add_row<NC>(slot, v);
+                    if (j + kStretch >= j_hi && a.pieces == 1) store_row<NC>(a.out0, out_at, a.g_type, v);
+                    else store_row<NC>(slot, 0, SKV_F32, v);
+                }
+                tc::tc_fence_before();
+            }
+        }
+        __syncwarp();
+        __syncthreads();
+        tc::tc_fence_after();
+        if (s_abort) break;
+        it0 += nt;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc<512>(tmem);
+    }
+}
+
+template <int D>
+KernelAttrCache &attr_cache()
+{
+    static KernelAttrCache c;
+    return c;
+}
+
+template <int D>
+int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
+             const MainArgs &a, cudaStream_t st)
+{
+    cudaError_t e = kernel_smem_optin(attr_cache<D>(), reinterpret_cast<const void *>(splitkv_bwd_q_kernel<D>), Lay<D>::kBytes,
+                                      kThreads, nullptr);
+    if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(dq)");
+    const dim3 grid(static_cast<unsigned>(a.g.QT * a.g.Hk * a.g.groups), static_cast<unsigned>(a.pieces));
+    splitkv_bwd_q_kernel<D><<<grid, kThreads, Lay<D>::kBytes, st>>>(mq, mo, mk, mv, a);
+    return cuda_fail(h, cudaGetLastError(), "dq kernel launch");
+}
+
+}  // namespace
+
+int launch_q(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
+             const MainArgs &a, cudaStream_t st)
+{
+    return a.g.D == 64 ? launch_t<64>(h, mq, mo, mk, mv, a, st) : launch_t<128>(h, mq, mo, mk, mv, a, st);
+}
+
+}  // namespace bwd
+}  // namespace skv

@@ -52,6 +52,20 @@ int ensure_ring(skv_handle *h, size_t bytes_per_slot, int n_slots, cudaStream_t 
 
 int64_t segment_bytes(int type, int D);
 
+// Makes the handle's device current for a call.
+struct OnDevice {
+    int prev = -1;
+    bool moved = false;
+    explicit OnDevice(int want)
+    {
+        if (cudaGetDevice(&prev) == cudaSuccess && prev != want) moved = cudaSetDevice(want) == cudaSuccess;
+    }
+    ~OnDevice()
+    {
+        if (moved) cudaSetDevice(prev);
+    }
+};
+
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) takes effect in the current
 // device's context only, so a kernel's opt-in (and the occupancy it gives) is
 // recorded per device.  One cache per kernel instance; host threads share it
@@ -224,6 +238,10 @@ constexpr int kFusedSplitPages = 8;
 int attn_paged_fused(skv_handle *h, const skv_shape *shape, const void *q, const void *k_pages, const void *v_pages,
                      const int32_t *page_ids, int32_t pages_per_list, float *o, float *lse, cudaStream_t st,
                      const DecodeArgs &fuse);
+
+// A device-accessible address for a destination region: device memory as is,
+// page-locked host memory through its mapped device address (append.cu).
+int device_address(skv_handle *h, void *p, uint8_t **out);
 
 int launch_dequant(int type, const void *blocks, int64_t n_values, float *out, cudaStream_t st);
 int launch_gather(const void *src, int64_t row_bytes, const int32_t *rows, int64_t n, void *dst,

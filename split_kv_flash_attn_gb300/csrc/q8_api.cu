@@ -8,20 +8,6 @@
 namespace skv {
 namespace q8 {
 
-// Makes the handle's device current for a call.
-struct OnDevice {
-    int prev = -1;
-    bool moved = false;
-    explicit OnDevice(int want)
-    {
-        if (cudaGetDevice(&prev) == cudaSuccess && prev != want) moved = cudaSetDevice(want) == cudaSuccess;
-    }
-    ~OnDevice()
-    {
-        if (moved) cudaSetDevice(prev);
-    }
-};
-
 // Query rows of a KV head from which the tensor-core kernel serves: it computes 256
 // rows whatever is there, the decode kernel passes over the keys again for each 16.
 // Eight KV heads of D = 128, decode against tensor cores: 32768 keys of one sequence
