@@ -627,20 +627,21 @@ class Rope:
         self.D, self.rot_dims, self.n_axes, self.freq, self.axis = int(D), 2 * half, int(n_axes or 1), freq, axis
         self._c = SkvRopeSpec(self.D, 2 * half, int(bool(interleaved)), self.n_axes, freq.data_ptr(), _ptr(axis),
                               float(factor), float(eps))
+        self._d = (self.D,)
         self._ref = ctypes.byref(self._c)
 
 
 _row_types = None
 
 
-def _row_type(name, x):
+def _row_type(name, dtype):
     global _row_types
     if _row_types is None:
         torch = _torch()
         _row_types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    t = _row_types.get(x if not hasattr(x, "dtype") else x.dtype)
+    t = _row_types.get(dtype)
     if t is None:
-        raise SplitKVError(1, f"{name}: fp32, fp16 or bf16 is wanted, got {x if not hasattr(x, 'dtype') else x.dtype}")
+        raise SplitKVError(1, f"{name}: fp32, fp16 or bf16 is wanted, got {dtype}")
     return t
 
 
@@ -648,7 +649,10 @@ def _token_rows(name, x, lead, D, dtype, device):
     """Heads and token stride of rows [*lead, heads, D] whose heads stand side by side and whose tokens a fixed
     stride apart (a part of a packed projection, say)."""
     shape, stride, k = x.shape, x.stride(), len(lead)
-    ok = (len(shape) == k + 2 and shape[:k] == lead and shape[-1] == D and x.dtype is dtype and x.get_device() == device
+    ok = x.dtype is dtype and x.get_device() == device
+    if k == 1 and ok and len(shape) == 3 and shape[0] == lead[0] and shape[2] == D and stride[2] == 1 and stride[1] == D:
+        return shape[1], stride[0]                            # the usual case, without the loop
+    ok = (ok and len(shape) == k + 2 and shape[:k] == lead and shape[-1] == D
           and (stride[-1] == 1 and (stride[-2] == D or shape[-2] == 1) or x.numel() == 0))
     step, want = 0, None
     if ok:
@@ -671,45 +675,44 @@ def _token_rows(name, x, lead, D, dtype, device):
 def _tokens(lead):
     n = 1
     for m in lead:
-        n *= int(m)
+        n *= m
     return n
 
 
-def _positions(spec, pos, n):
-    torch = _torch()
-    if pos.dtype is not torch.int32 or pos.get_device() != spec.device or not pos.is_contiguous() or pos.numel() != n * spec.n_axes:
-        raise SplitKVError(1, f"pos: want contiguous int32 of {spec.n_axes} x {n} positions on device {spec.device}, "
+def _positions(torch, name, pos, want, device):
+    if pos.dtype is not torch.int32 or pos.get_device() != device or not pos.is_contiguous() or pos.numel() != want:
+        raise SplitKVError(1, f"{name}: want contiguous int32 of {want} positions on device {device}, "
                               f"got {pos.dtype} {list(pos.shape)} on {pos.device}")
     return pos.data_ptr()
 
 
-def _weights(spec, *pairs):
-    torch = _torch()
-    for name, w in pairs:
-        if w is not None:
-            _need(name, w, torch.float32, (spec.D,), spec.device)
+def _weight(torch, name, w, spec):
+    if w is None:
+        return None
+    if w.dtype is not torch.float32 or w.shape != spec._d or w.get_device() != spec.device or not w.is_contiguous():
+        _need(name, w, torch.float32, spec._d, spec.device)
+    return w.data_ptr()
 
 
-def _new(shape, dtype, like, stream, device):
-    torch = _torch()
+def _new(torch, shape, dtype, like, stream, device):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with _on_stream(stream, device):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _rope_inputs(h, spec, q, k, pos, stream):
-    """(device, stream, leading shape, tokens, H, q stride, Hk, k stride, row type, pointer of pos)"""
-    some = q if q is not None else k
+def _rope_inputs(torch, h, spec, q, k, pos, stream):
+    """stream, leading shape, tokens, H, q stride, Hk, k stride, row type, pointer of pos"""
+    some = k if k is not None else q
     if some is None:
         raise SplitKVError(1, "q or k is wanted")
-    lead, dev = tuple(some.shape[:-2]), spec.device
+    lead, dev, D, dtype = some.shape[:-2], spec.device, spec.D, some.dtype
     st = _q8_stream(h, stream, dev)
-    xt = _row_type("q" if q is not None else "k", some)
-    H, qs = _token_rows("q", q, lead, spec.D, some.dtype, dev) if q is not None else (0, 0)
-    Hk, ks = _token_rows("k", k, lead, spec.D, some.dtype, dev) if k is not None else (0, 0)
-    n = _tokens(lead)
-    return st, lead, n, H, qs, Hk, ks, xt, _positions(spec, pos, n)
+    xt = _row_type("q" if some is q else "k", dtype)
+    H, qs = _token_rows("q", q, lead, D, dtype, dev) if q is not None else (0, 0)
+    Hk, ks = _token_rows("k", k, lead, D, dtype, dev) if k is not None else (0, 0)
+    n = lead[0] if len(lead) == 1 else _tokens(lead)
+    return st, lead, n, H, qs, Hk, ks, xt, _positions(torch, "pos", pos, n * spec.n_axes, dev)
 
 
 def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dtype=None, q_out=None, k_out=None,
@@ -718,25 +721,28 @@ def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dt
     (fp32, fp16 or bf16; either may be None); pos int32 [n_axes, ...] (without the axis for one).
     Results are fp16 unless o_dtype (or a given q_out, k_out) says otherwise."""
     torch = _torch()
-    st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(h, spec, q, k, pos, stream)
-    _weights(spec, ("q_weight", q_weight), ("k_weight", k_weight))
+    st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(torch, h, spec, q, k, pos, stream)
+    wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
     if o_dtype is None:
         o_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else torch.float16
-    ot = _row_type("o_dtype", o_dtype)
-    outs = []
-    for name, x, heads, out in (("q_out", q, H, q_out), ("k_out", k, Hk, k_out)):
-        if x is None:
-            out = None
-        elif out is None:
-            out = _new((*lead, heads, spec.D), o_dtype, x, stream, spec.device)
-        else:
-            _need(name, out, o_dtype, (*lead, heads, spec.D), spec.device)
-        outs.append(out)
-    rc = _lib.lib().skv_rope(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
-                             pp, ot, _ptr(outs[0]), _ptr(outs[1]), st)
+    ot, D = _row_type("o_dtype", o_dtype), spec.D
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = _new(torch, (*lead, H, D), o_dtype, q, stream, spec.device)
+    else:
+        _need("q_out", q_out, o_dtype, (*lead, H, D), spec.device)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = _new(torch, (*lead, Hk, D), o_dtype, k, stream, spec.device)
+    else:
+        _need("k_out", k_out, o_dtype, (*lead, Hk, D), spec.device)
+    rc = _lib.lib().skv_rope(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, _ptr(k), ks, wq, wk, pp, ot, _ptr(q_out),
+                             _ptr(k_out), st)
     if rc:
         h.check(rc)
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
 def _cache_dst(name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes):
@@ -745,10 +751,11 @@ def _cache_dst(name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes):
     if row_bytes is None:
         row_bytes = Hk * segment_bytes(type_, D)
     if n_rows0 is None:
-        n_rows0 = 0 if dst0 is None else dst0.numel() * dst0.element_size() // row_bytes
+        n_rows0 = 0 if dst0 is None else dst0.numel() * dst0.element_size() // max(1, row_bytes)
     if n_rows1 is None:
-        n_rows1 = 0 if dst1 is None else dst1.numel() * dst1.element_size() // row_bytes
-    return SkvCacheDst(int(type_), int(row_bytes), _ptr(dst0), int(n_rows0), _ptr(dst1), int(n_rows1))
+        n_rows1 = 0 if dst1 is None else dst1.numel() * dst1.element_size() // max(1, row_bytes)
+    return SkvCacheDst(type_, row_bytes, None if dst0 is None else dst0.data_ptr(), n_rows0,
+                       None if dst1 is None else dst1.data_ptr(), n_rows1)
 
 
 def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, k_dst1=None, v_dst1=None, *,
@@ -759,24 +766,23 @@ def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, 
     torch = _torch()
     if k is None or v is None:
         raise SplitKVError(1, "k and v are wanted")
-    st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(h, spec, q, k, pos, stream)
-    Hv, vs = _token_rows("v", v, lead, spec.D, k.dtype, spec.device)
+    st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(torch, h, spec, q, k, pos, stream)
+    D, dev = spec.D, spec.device
+    Hv, vs = _token_rows("v", v, lead, D, k.dtype, dev)
     if Hv != Hk:
         raise SplitKVError(1, f"v has {Hv} heads, k {Hk}")
-    _weights(spec, ("q_weight", q_weight), ("k_weight", k_weight))
-    if positions.dtype is not torch.int32 or positions.get_device() != spec.device or positions.numel() != n or not positions.is_contiguous():
-        raise SplitKVError(1, f"positions: want contiguous int32 of {n} positions on device {spec.device}")
+    wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
+    at = _positions(torch, "positions", positions, n, dev)
     if q is None:
         q_out = None
     elif q_out is None:
-        q_out = _new((*lead, H, spec.D), torch.float16, q, stream, spec.device)
+        q_out = _new(torch, (*lead, H, D), torch.float16, q, stream, dev)
     else:
-        _need("q_out", q_out, torch.float16, (*lead, H, spec.D), spec.device)
-    kd = _cache_dst("k_type", k_type, Hk, spec.D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes)
-    vd = _cache_dst("v_type", v_type, Hk, spec.D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes)
+        _need("q_out", q_out, torch.float16, (*lead, H, D), dev)
+    kd = _cache_dst("k_type", k_type, Hk, D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes)
+    vd = _cache_dst("v_type", v_type, Hk, D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes)
     rc = _lib.lib().skv_rope_append(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                                    _ptr(q_weight), _ptr(k_weight), pp, positions.data_ptr(), _ptr(q_out),
-                                    ctypes.byref(kd), ctypes.byref(vd), st)
+                                    wq, wk, pp, at, _ptr(q_out), ctypes.byref(kd), ctypes.byref(vd), st)
     if rc:
         h.check(rc)
     return q_out
@@ -791,26 +797,29 @@ def rope_backward(h: Handle, spec: Rope, dq_out, dk_out, pos, *, q=None, k=None,
     some = dq_out if dq_out is not None else dk_out
     if some is None:
         raise SplitKVError(1, "dq_out or dk_out is wanted")
-    lead, dev, D = tuple(some.shape[:-2]), spec.device, spec.D
+    lead, dev, D = some.shape[:-2], spec.device, spec.D
     st = _q8_stream(h, stream, dev)
-    gt = _row_type("dq_out" if dq_out is not None else "dk_out", some)
-    n = _tokens(lead)
-    pp = _positions(spec, pos, n)
-    _weights(spec, ("q_weight", q_weight), ("k_weight", k_weight))
+    g_dtype = some.dtype
+    gt = _row_type("dq_out" if some is dq_out else "dk_out", g_dtype)
+    n = lead[0] if len(lead) == 1 else _tokens(lead)
+    pp = _positions(torch, "pos", pos, n * spec.n_axes, dev)
+    wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
     if x_dtype is None:
-        x_dtype = next((x.dtype for x in (q, k, dq, dk) if x is not None), some.dtype)
+        x_dtype = next((x.dtype for x in (q, k, dq, dk) if x is not None), g_dtype)
     xt = _row_type("x_dtype", x_dtype)
-    heads, xs, strides, outs, out_strides, dws = [], [], [], [], [], []
-    for name, g, x, w, out in (("q", dq_out, q, q_weight, dq), ("k", dk_out, k, k_weight, dk)):
+
+    def side(name, g, x, w, out):
+        """heads, pointer and stride of x, of the gradient, the gradient and that of the weight"""
         if g is None:
             if w is not None:
                 raise SplitKVError(1, f"{name}_weight without d{name}_out")
-            heads.append(0), xs.append(None), strides.append(0), outs.append(None), out_strides.append(0), dws.append(None)
-            continue
-        if g.dim() != len(lead) + 2:
-            raise SplitKVError(1, f"d{name}_out: want [..., heads, {D}], got {list(g.shape)}")
-        hd = int(g.shape[-2])
-        _need(f"d{name}_out", g, some.dtype, (*lead, hd, D), dev)
+            return 0, None, 0, None, 0, None
+        shape = g.shape
+        if len(shape) != len(lead) + 2:
+            raise SplitKVError(1, f"d{name}_out: want [..., heads, {D}], got {list(shape)}")
+        hd = shape[-2]
+        _need(f"d{name}_out", g, g_dtype, (*lead, hd, D), dev)
+        ptr = dw = None
         stride = 0
         if w is not None:
             if x is None:
@@ -818,21 +827,21 @@ def rope_backward(h: Handle, spec: Rope, dq_out, dk_out, pos, *, q=None, k=None,
             xh, stride = _token_rows(name, x, lead, D, x_dtype, dev)
             if xh != hd:
                 raise SplitKVError(1, f"{name} has {xh} heads, d{name}_out {hd}")
+            ptr, dw = x.data_ptr(), _new(torch, spec._d, torch.float32, g, stream, dev)
         if out is None:
-            out = _new((*lead, hd, D), x_dtype, g, stream, dev)
+            return hd, ptr, stride, _new(torch, shape, x_dtype, g, stream, dev), hd * D, dw
         oh, ostride = _token_rows(f"d{name}", out, lead, D, x_dtype, dev)
         if oh != hd:
             raise SplitKVError(1, f"d{name} has {oh} heads, d{name}_out {hd}")
-        heads.append(hd), xs.append(x if w is not None else None), strides.append(stride), outs.append(out)
-        out_strides.append(ostride)
-        dws.append(None if w is None else _new((D,), torch.float32, g, stream, dev))
-    rc = _lib.lib().skv_rope_backward(h._h, spec._ref, n, heads[0], heads[1], xt, _ptr(xs[0]), strides[0], _ptr(xs[1]),
-                                      strides[1], _ptr(q_weight), _ptr(k_weight), pp, gt, _ptr(dq_out), _ptr(dk_out),
-                                      _ptr(outs[0]), out_strides[0], _ptr(outs[1]), out_strides[1], _ptr(dws[0]),
-                                      _ptr(dws[1]), st)
+        return hd, ptr, stride, out, ostride, dw
+
+    H, qp, qs, dq, dqs, dwq = side("q", dq_out, q, q_weight, dq)
+    Hk, kp, ks, dk, dks, dwk = side("k", dk_out, k, k_weight, dk)
+    rc = _lib.lib().skv_rope_backward(h._h, spec._ref, n, H, Hk, xt, qp, qs, kp, ks, wq, wk, pp, gt, _ptr(dq_out),
+                                      _ptr(dk_out), _ptr(dq), dqs, _ptr(dk), dks, _ptr(dwq), _ptr(dwk), st)
     if rc:
         h.check(rc)
-    return outs[0], outs[1], dws[0], dws[1]
+    return dq, dk, dwq, dwk
 
 
 def attn_backward(h: Handle, q, k, v, o, lse, d_o, *, Hk, scale=None, kv_begin=0, kv_end=None, kv_rows=None,
@@ -842,57 +851,63 @@ def attn_backward(h: Handle, q, k, v, o, lse, d_o, *, Hk, scale=None, kv_begin=0
     or fp32) and d_lse.  Results are fp32 unless g_dtype (or a given result) is torch.float16; need_dq=False or
     need_dkv=False leaves a part out (None)."""
     torch = _torch()
-    if q.dim() != 4:
-        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(q.shape)}")
-    dev = q.get_device()
-    S, nq, H, D = (int(x) for x in q.shape)
+    shape, dev, f16, f32 = q.shape, q.get_device(), torch.float16, torch.float32
+    if len(shape) != 4:
+        raise SplitKVError(1, f"q: want fp16 [S, nq, H, D], got {list(shape)}")
+    S, nq, H, D = shape
     st = _q8_stream(h, stream, dev)
-    _need("q", q, torch.float16, (S, nq, H, D), dev)
-    _need("o", o, torch.float32, (S, nq, H, D), dev)
-    _need("lse", lse, torch.float32, (S, nq, H), dev)
-    if d_o.dtype not in (torch.float16, torch.float32):
-        raise SplitKVError(1, f"d_o: fp16 or fp32 is wanted, got {d_o.dtype}")
-    _need("d_o", d_o, d_o.dtype, (S, nq, H, D), dev)
+    d_type, rows3 = d_o.dtype, shape[:3]
+    # all checks in one expression; what fails is found again below, with its message
+    if not (q.dtype is f16 and o.dtype is f32 and lse.dtype is f32 and (d_type is f16 or d_type is f32) and k.dtype is f16
+            and v.dtype is f16 and o.shape == shape and d_o.shape == shape and lse.shape == rows3 and o.get_device() == dev
+            and lse.get_device() == dev and d_o.get_device() == dev and k.get_device() == dev and v.get_device() == dev
+            and q.is_contiguous() and o.is_contiguous() and lse.is_contiguous() and d_o.is_contiguous()
+            and (k_row_bytes is not None or k.is_contiguous()) and (v_row_bytes is not None or v.is_contiguous())):
+        if d_type not in (f16, f32):
+            raise SplitKVError(1, f"d_o: fp16 or fp32 is wanted, got {d_type}")
+        for name, x, t, want in (("q", q, f16, shape), ("o", o, f32, shape), ("lse", lse, f32, rows3), ("d_o", d_o, d_type, shape)):
+            _need(name, x, t, want, dev)
+        for name, x in (("k", k), ("v", v)):
+            if x.dtype is not f16 or x.get_device() != dev:
+                raise SplitKVError(1, f"{name}: want fp16 rows on device {dev}, got {x.dtype} on {x.device}")
+        raise SplitKVError(1, "k or v: rows that are not contiguous need k_row_bytes and v_row_bytes")
     if d_lse is not None:
-        _need("d_lse", d_lse, torch.float32, (S, nq, H), dev)
+        _need("d_lse", d_lse, f32, rows3, dev)
     if q_pos is not None:
         _need("q_pos", q_pos, torch.int32, (S, nq), dev)
-    for name, x in (("k", k), ("v", v)):
-        if x.dtype is not torch.float16 or x.get_device() != dev:
-            raise SplitKVError(1, f"{name}: want fp16 rows on device {dev}, got {x.dtype} on {x.device}")
-        if not x.is_contiguous() and (k_row_bytes if name == "k" else v_row_bytes) is None:
-            raise SplitKVError(1, f"{name}: rows that are not contiguous need {name}_row_bytes")
-    Hk, per_head = int(Hk), bool(kv_rows_per_head)
-    rows_ld = 0
+    Hk, per_head, rows_ld = int(Hk), bool(kv_rows_per_head), 0
     if kv_rows is not None:
-        rows_ld = int(kv_rows.shape[-1])
+        rows_ld = kv_rows.shape[-1]
         _need("kv_rows", kv_rows, torch.int32, (S, Hk, rows_ld) if per_head else (S, rows_ld), dev)
     if kv_end is None:
-        kv_end = rows_ld if kv_rows is not None else int(k.shape[0])
+        kv_end = rows_ld if kv_rows is not None else k.shape[0]
     kv_begin, kv_end = int(kv_begin), int(kv_end)
     n = max(0, kv_end - kv_begin)
     if kv_rows is None and (kv_end > k.shape[0] or kv_end > v.shape[0]):
         raise SplitKVError(1, f"kv_end {kv_end} lies beyond k's {k.shape[0]} or v's {v.shape[0]} rows")
-    sh = _shape(q, Hk, F16, F16, k_row_bytes, v_row_bytes, scale)
+    row = Hk * 2 * D
+    sh = SkvShape(S, nq, H, Hk, D, 1.0 / math.sqrt(D) if scale is None else float(scale), F16, F16,
+                  row if k_row_bytes is None else int(k_row_bytes), row if v_row_bytes is None else int(v_row_bytes))
     if g_dtype is None:
-        g_dtype = next((x.dtype for x in (dq, dk, dv) if x is not None), torch.float32)
-    if g_dtype not in (torch.float16, torch.float32):
+        g_dtype = next((x.dtype for x in (dq, dk, dv) if x is not None), f32)
+    if g_dtype is not f16 and g_dtype is not f32:
         raise SplitKVError(1, f"g_dtype: fp32 or fp16 is wanted, got {g_dtype}")
     kv_shape = (n, Hk, D) if kv_rows is None else (S, n, Hk, D)
-    outs = []
-    for name, x, shape, need in (("dq", dq, (S, nq, H, D), need_dq), ("dk", dk, kv_shape, need_dkv), ("dv", dv, kv_shape, need_dkv)):
+
+    def result(name, x, want, need):
         if not need:
-            x = None
-        elif x is None:
-            x = _new(shape, g_dtype, q, stream, dev)
-        else:
-            _need(name, x, g_dtype, shape, dev)
-        outs.append(x)
+            return None
+        if x is None:
+            return _new(torch, want, g_dtype, q, stream, dev)
+        _need(name, x, g_dtype, want, dev)
+        return x
+
+    outs = (result("dq", dq, shape, need_dq), result("dk", dk, kv_shape, need_dkv), result("dv", dv, kv_shape, need_dkv))
     rc = _lib.lib().skv_attn_backward(h._h, ctypes.byref(sh), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_pos),
                                       int(key_pos0), _ptr(kv_rows), rows_ld, int(per_head), kv_begin, kv_end,
-                                      o.data_ptr(), lse.data_ptr(), F16 if d_o.dtype is torch.float16 else F32,
-                                      d_o.data_ptr(), _ptr(d_lse), F16 if g_dtype is torch.float16 else F32,
+                                      o.data_ptr(), lse.data_ptr(), F16 if d_type is f16 else F32,
+                                      d_o.data_ptr(), _ptr(d_lse), F16 if g_dtype is f16 else F32,
                                       _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), st)
     if rc:
         h.check(rc)
-    return outs[0], outs[1], outs[2]
+    return outs

@@ -10,139 +10,155 @@ namespace bwd {
 
 constexpr int kPrepThreads = 256;
 
-__device__ __forceinline__ float warp_sum(float x)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-__device__ __forceinline__ float warp_max(float x)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
-
-// A query tile: a warp takes a row at a time, D/32 values a lane, four rows in flight.
+// A query tile.  First the sums of its rows, D/8 lanes a row, eight values a lane, all
+// loads of a thread's rows before their sums; then a thread for each row.
 template <int D, bool F32DO>
 __device__ void prep_rows(const PrepArgs &a, int64_t tile)
 {
-    constexpr int V = D / 32, U = 4;
+    constexpr int LPR = D / 8, RPP = kPrepThreads / LPR, IT = kTile / RPP;   // rows of a pass, passes: 8 or 4
+    constexpr int U = 4;                                                    // passes in flight
     const Geo &g = a.g;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, l = tid % LPR;
     const int qt = static_cast<int>(tile % g.QT);
-    const int64_t gh = tile / g.QT;
-    const QTile t = q_tile(g, static_cast<int>(gh / g.Hk), static_cast<int>(gh % g.Hk), qt);
-    float *info = a.info + tile * (kInfoRows * kTile);
-    int lim_max = 0, mN = kNoExp, mD = kNoExp, mC = -1000;
-    for (int r0 = warp * (kTile / 8); r0 < (warp + 1) * (kTile / 8); r0 += U) {
+    const int gh = static_cast<int>(tile / g.QT);
+    const QTile t = q_tile(g, gh / g.Hk, gh % g.Hk, qt);
+    __shared__ float s_dot[kTile], s_n2[kTile];
+    __shared__ int s_c[kTile];
+#pragma unroll
+    for (int i0 = 0; i0 < IT; i0 += U) {
+        uint4 xr[U][F32DO ? 2 : 1];
+        float4 y[U][2];
         int64_t row[U];
-        float x[U][V], y[U][V], lse[U], dl[U];
-        int32_t pos[U];
+        bool live[U];
+        float dl[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            row[u] = q_row(g, t, r0 + u);
+            row[u] = q_row(g, t, (i0 + u) * RPP + tid / LPR);
             const int64_t rr = row[u] < 0 ? 0 : row[u];
-            const int64_t at = rr * D + lane * V;
+            const int64_t at = rr * D + 8 * l;
             if constexpr (F32DO) {
-                if constexpr (V == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.d_o) + at);
-                    x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
-                } else {
-                    const float2 f = *reinterpret_cast<const float2 *>(static_cast<const float *>(a.d_o) + at);
-                    x[u][0] = f.x; x[u][1] = f.y;
-                }
+                const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.d_o) + at);
+                xr[u][0] = __ldg(p);
+                xr[u][1] = __ldg(p + 1);
+                dl[u] = a.d_lse ? a.d_lse[rr] : 0.f;
             } else {
-                const __half *p = static_cast<const __half *>(a.d_o) + at;
-#pragma unroll
-                for (int i = 0; i < V; i += 2) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(p + i));
-                    x[u][i] = f.x;
-                    x[u][i + 1] = f.y;
-                }
+                xr[u][0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(a.d_o) + at));
             }
-            if constexpr (V == 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(a.o + at);
-                y[u][0] = f.x; y[u][1] = f.y; y[u][2] = f.z; y[u][3] = f.w;
-            } else {
-                const float2 f = *reinterpret_cast<const float2 *>(a.o + at);
-                y[u][0] = f.x; y[u][1] = f.y;
-            }
-            lse[u] = a.lse[rr];
-            dl[u] = a.d_lse ? a.d_lse[rr] : 0.f;
-            pos[u] = a.q_pos ? a.q_pos[rr / g.H] : 0;
+            const float4 *o = reinterpret_cast<const float4 *>(a.o + at);
+            y[u][0] = __ldg(o);
+            y[u][1] = __ldg(o + 1);
+            if (F32DO) live[u] = row[u] >= 0 && a.lse[rr] != -INFINITY;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u;
-            int64_t lim = g.n;
-            if (a.q_pos) lim = min(g.n, max(static_cast<int64_t>(0), static_cast<int64_t>(pos[u]) - a.pos0 + 1));
-            const bool dead = row[u] >= 0 && lse[u] == -INFINITY;
-            const bool live = row[u] >= 0 && !dead;
+            const int r = (i0 + u) * RPP + tid / LPR;
+            float x[8];
             int c = 0;
             if constexpr (F32DO) {
+                const uint32_t w[8] = {xr[u][0].x, xr[u][0].y, xr[u][0].z, xr[u][0].w, xr[u][1].x, xr[u][1].y, xr[u][1].z, xr[u][1].w};
                 float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(x[u][i]));
-                m = warp_max(m);
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = live[u] ? __uint_as_float(w[i]) : 0.f;
+                    m = fmaxf(m, fabsf(x[i]));
+                }
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 // the row's largest value at 2^13 .. 2^14; a d_lse far beyond it keeps delta' in range
                 c = max(exp_of(m) - 14, exp_of(fabsf(dl[u])) - 40);
                 c = max(-120, min(115, c));
                 const float f = pow2(-c / 2), f2 = pow2(-c - (-c / 2));
+                uint32_t h[4];
 #pragma unroll
-                for (int i = 0; i < V; ++i) x[u][i] = __half2float(__float2half_rn(x[u][i] * f * f2));
-                if (!live) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) x[u][i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 hh = __floats2half2_rn(x[2 * i] * f * f2, x[2 * i + 1] * f * f2);
+                    h[i] = *reinterpret_cast<const uint32_t *>(&hh);
+                    const float2 v = __half22float2(hh);
+                    x[2 * i] = v.x;
+                    x[2 * i + 1] = v.y;
                 }
-                if (row[u] >= 0) {
-                    __half *p = a.doh + row[u] * D + lane * V;
+                if (row[u] >= 0)
+                    *reinterpret_cast<uint4 *>(a.doh + row[u] * D + 8 * l) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                const uint32_t w[4] = {xr[u][0].x, xr[u][0].y, xr[u][0].z, xr[u][0].w};
 #pragma unroll
-                    for (int i = 0; i < V; i += 2)
-                        *reinterpret_cast<__half2 *>(p + i) = __floats2half2_rn(x[u][i], x[u][i + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                    x[2 * i] = v.x;
+                    x[2 * i + 1] = v.y;
                 }
-                dl[u] = dl[u] * f * f2;
             }
+            const float yy[8] = {y[u][0].x, y[u][0].y, y[u][0].z, y[u][0].w, y[u][1].x, y[u][1].y, y[u][1].z, y[u][1].w};
             float dot = 0.f, n2 = 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                dot = fmaf(x[u][i], y[u][i], dot);
-                n2 = fmaf(x[u][i], x[u][i], n2);
+            for (int i = 0; i < 8; ++i) {
+                dot = fmaf(x[i], yy[i], dot);
+                n2 = fmaf(x[i], x[i], n2);
             }
-            dot = warp_sum(dot);
-            n2 = warp_sum(n2);
-            const float delta = dot - dl[u];
-            const int eN = max(kNoExp, min(60, exp_of_norm2(n2))), eD = exp_of(fabsf(delta));
-            if (lane == 0) {
-                // rows that see nothing get p' = 0 through L, and lim -1 where their q and d_o exist
-                const bool sees = live && lim > 0;
-                info[r] = sees ? lse[u] * 1.4426950408889634f - static_cast<float>(kPShift) : INFINITY;
-                info[kTile + r] = sees ? delta : 0.f;
-                info[2 * kTile + r] = __int_as_float(sees ? c : 0);
-                info[3 * kTile + r] = __int_as_float(sees ? static_cast<int>(lim) : row[u] >= 0 ? -1 : 0);
-                info[4 * kTile + r] = __int_as_float(sees ? (eN << 16) | (eD & 0xffff) : (kNoExp << 16) | (kNoExp & 0xffff));
+#pragma unroll
+            for (int o = LPR / 2; o; o >>= 1) {
+                dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                n2 += __shfl_xor_sync(0xffffffffu, n2, o);
             }
-            if (live && lim > 0) {
-                lim_max = max(lim_max, static_cast<int>(lim));
-                if (eN > kNoExp) mN = max(mN, eN + c);
-                if (eD > kNoExp) mD = max(mD, eD + c);
-                if (eN > kNoExp || eD > kNoExp) mC = max(mC, c);
+            if (l == 0) {
+                s_dot[r] = dot;
+                s_n2[r] = n2;
+                if (F32DO) s_c[r] = c;
             }
         }
     }
-    __shared__ int s_red[8][4];
-    if (lane == 0) {
-        s_red[warp][0] = lim_max;
-        s_red[warp][1] = mN;
-        s_red[warp][2] = mD;
-        s_red[warp][3] = mC;
+    // this thread's row
+    int lim_max = 0, mN = kNoExp, mD = kNoExp, mC = -1000;
+    int64_t row = -1, lim = 0;
+    float lse = 0.f, dl = 0.f;
+    if (tid < kTile) {
+        row = q_row(g, t, tid);
+        const int64_t rr = row < 0 ? 0 : row;
+        lse = a.lse[rr];
+        dl = a.d_lse ? a.d_lse[rr] : 0.f;
+        lim = g.n;
+        if (a.q_pos) {
+            const int64_t tok = row < 0 ? 0 : t.group * g.T + t.t0 + tid / g.Gb;
+            lim = min(g.n, max(static_cast<int64_t>(0), static_cast<int64_t>(a.q_pos[tok]) - a.pos0 + 1));
+        }
     }
     __syncthreads();
-    if (threadIdx.x < 4) {
-        int x = s_red[0][threadIdx.x];
-        for (int w = 1; w < 8; ++w) x = max(x, s_red[w][threadIdx.x]);
-        reinterpret_cast<int *>(a.sum + tile)[threadIdx.x] = x;
+    if (tid < kTile) {
+        float *info = a.info + tile * (kInfoRows * kTile) + tid;
+        const int c = F32DO ? s_c[tid] : 0;
+        const float delta = s_dot[tid] - dl * pow2(-c / 2) * pow2(-c - (-c / 2));
+        const int eN = max(kNoExp, min(60, exp_of_norm2(s_n2[tid]))), eD = exp_of(fabsf(delta));
+        // rows that see nothing get p' = 0 through L, and lim -1 where their q and d_o exist
+        const bool sees = row >= 0 && lse != -INFINITY && lim > 0;
+        info[0] = sees ? lse * 1.4426950408889634f - static_cast<float>(kPShift) : INFINITY;
+        info[kTile] = sees ? delta : 0.f;
+        info[2 * kTile] = __int_as_float(sees ? c : 0);
+        info[3 * kTile] = __int_as_float(sees ? static_cast<int>(lim) : row >= 0 ? -1 : 0);
+        info[4 * kTile] = __int_as_float(sees ? (eN << 16) | (eD & 0xffff) : (kNoExp << 16) | (kNoExp & 0xffff));
+        if (sees) {
+            lim_max = static_cast<int>(lim);
+            if (eN > kNoExp) mN = eN + c;
+            if (eD > kNoExp) mD = eD + c;
+            if (eN > kNoExp || eD > kNoExp) mC = c;
+        }
     }
+    __shared__ int s_red[4][4];
+    if (tid < kTile) {
+        lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+        mN = __reduce_max_sync(0xffffffffu, mN);
+        mD = __reduce_max_sync(0xffffffffu, mD);
+        mC = __reduce_max_sync(0xffffffffu, mC);
+        if ((tid & 31) == 0) {
+            s_red[tid >> 5][0] = lim_max;
+            s_red[tid >> 5][1] = mN;
+            s_red[tid >> 5][2] = mD;
+            s_red[tid >> 5][3] = mC;
+        }
+    }
+    __syncthreads();
+    if (tid < 4)
+        reinterpret_cast<int *>(a.sum + tile)[tid] =
+            max(max(s_red[0][tid], s_red[1][tid]), max(s_red[2][tid], s_red[3][tid]));
 }
 
 // A key tile: D/8 lanes a key, eight values a lane.

@@ -1,10 +1,16 @@
 // rope.cu -- norm and rotation of query and key rows, the same with the keys and
 // values written into cache rows, and the gradients.
 //
-// A row is one head of one token, D values; D/8 neighbouring lanes hold it, eight
-// consecutive values each (one 16-byte load of fp16), so a row's sums are
-// three or four shuffles and the partner of value i in split halves, i + R/2, is eight
-// values of another lane of the row (R/2 is a multiple of 8 there).
+// A row is one head of one token, D values; D/8 neighbouring lanes hold it, a lane two groups of
+// four consecutive values chosen so that both values of a pair are its own: in split halves
+// groups l and R/8 + l.  So a row costs no exchange but the sum of its squares, and since a
+// normed row is 1/rms times the row times weights, the weights go into the angles' factors.
+//
+// The rows of all tokens stand in one line: a token's query rows, key rows and value rows, cut into
+// batches of 2 KB.  Each warp takes an equal run of batches and keeps a token's angles in registers for
+// all rows of one kind.  It asks for a batch while it computes the one before (across tokens
+// too); the gradients, which read twice as much for a row, keep three batches in flight
+// into the warp's own shared memory.
 //
 // Angles.  theta = pos * freq in whole turns is pos * (freq / 2 pi), of which only the
 // fraction counts.  freq = m 2^e with a 24-bit m, so its turns per position are the
@@ -12,9 +18,15 @@
 // 2^-64 turns, off by less than freq / 2 units.  The product with pos wraps modulo
 // one turn by itself, in integers, and stays exact to 2^-33 turns for
 // every 32-bit position.  Its quadrant is taken off and sincospif gives the rest.
-// A CTA takes a run of rows, token after token, and computes the angles of its
-// tokens once (an fp64 product and cosine for each pair would cost more than the
-// rows: this GPU's fp64 rate is a hundredth of its fp32 rate).
+// (An fp64 product and cosine for each pair would cost more than the rows: this
+// GPU's fp64 rate is a hundredth of its fp32 rate.)  A lane computes two pairs of the token's
+// and shuffles bring it those of its values.
+//
+// Bound by latency and instructions rather than by memory: sixteen warps an SM, a batch's chain of
+// sums and a root in each.  8192 tokens of 32 + 8 heads of 128, fp16, normed (168 MB): 32 us;
+// batches of half the size 36, three CTAs an SM (80 registers, spilled) 36, the ring of the
+// gradients 35, a row's values consecutive in a lane and partners by shuffles 75.  Its gradients
+// (252 MB): 49 us and 3 for the weights' sums; batches in registers 60, a token a warp 83.
 #include "internal.h"
 #include "kv_encode.cuh"
 
@@ -22,8 +34,10 @@ namespace skv {
 namespace rope {
 
 constexpr int kThreads = 256;
-// Rows of a thread, all loaded before any is computed.
-constexpr int kIter = 4;
+// Shared memory of a warp for the gradients' batches in flight.
+constexpr int kRing = 8192;
+// CTAs resident on an SM (registers).
+constexpr int kCtas = 2;
 
 struct Side {                 // queries, or keys
     const void *x;            // rows [n][heads][D], `stride` elements a token
@@ -39,7 +53,7 @@ struct Dst {                  // cache region pair
     int64_t row_bytes;
     uint8_t *d0, *d1;
     int64_t n0, n1;
-    int vec16;                // 16-byte stores are aligned (fp16 rows)
+    int vec8;                 // 8-byte stores are aligned (fp16 rows)
 };
 
 struct Args {
@@ -56,7 +70,8 @@ struct Args {
     const int32_t *positions;
     Dst kd, vd;
     int *status;
-    int64_t chunks;
+    int bq, bk, bv;           // batches of a token's queries, keys and values
+    int64_t batches;          // of all tokens
     float *dw;                // backward: partial weight gradients [grid][2][D]
 };
 
@@ -78,10 +93,10 @@ __device__ __forceinline__ uint64_t turns_of(float freq)
     return (bits >> 31) ? 0 - t : t;
 }
 
-// factor * (cos, sin) of pos * freq.
-__device__ __forceinline__ float2 cos_sin(int32_t pos, float freq, float factor)
+// factor * (cos, sin) of pos positions, `turns` each.
+__device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t turns, float factor)
 {
-    const uint64_t phase = turns_of(freq) * static_cast<uint64_t>(static_cast<int64_t>(pos)) + 0x80000000ull;
+    const uint64_t phase = turns * static_cast<uint64_t>(static_cast<int64_t>(pos)) + 0x80000000ull;
     const int32_t ph = static_cast<int32_t>(phase >> 32);                     // 2^-32 turns
     const int32_t quad = static_cast<int32_t>(static_cast<uint32_t>(ph) + 0x20000000u) >> 30;
     const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>(ph) - (static_cast<uint32_t>(quad) << 30));
@@ -101,57 +116,76 @@ __device__ __forceinline__ float2 cos_sin(int32_t pos, float freq, float factor)
     return make_float2(c, s);
 }
 
-// Eight values of a type as loaded, and as fp32.
+constexpr int elem(int type) { return type == SKV_F32 ? 4 : 2; }
+// A lane's two groups of four values as loaded, and as fp32.
 template <int XT>
 struct Raw {
-    uint4 a[XT == SKV_F32 ? 2 : 1];
+    uint32_t w[2 * elem(XT)];
 };
 template <int XT>
-__device__ __forceinline__ Raw<XT> load8(const void *p, int64_t at)
+__device__ __forceinline__ Raw<XT> zero_rows()
 {
     Raw<XT> r;
-    if constexpr (XT == SKV_F32) {
-        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at);
-        r.a[0] = __ldg(s);
-        r.a[1] = __ldg(s + 1);
-    } else {
-        r.a[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at));
-    }
+#pragma unroll
+    for (int i = 0; i < 2 * elem(XT); ++i) r.w[i] = 0;
     return r;
 }
 template <int XT>
-__device__ __forceinline__ Raw<XT> zero8()
+__device__ __forceinline__ Raw<XT> load_rows(const void *x, int64_t at, int a, int b)
 {
     Raw<XT> r;
-    r.a[0] = make_uint4(0, 0, 0, 0);
-    if constexpr (XT == SKV_F32) r.a[1] = r.a[0];
+    if constexpr (XT == SKV_F32) {
+        const float *p = static_cast<const float *>(x) + at;
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + a)), v = __ldg(reinterpret_cast<const uint4 *>(p + b));
+        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+        r.w[4] = v.x; r.w[5] = v.y; r.w[6] = v.z; r.w[7] = v.w;
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(x) + at;
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p + a)), v = __ldg(reinterpret_cast<const uint2 *>(p + b));
+        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = v.x; r.w[3] = v.y;
+    }
     return r;
 }
 template <int XT>
 __device__ __forceinline__ void to_f32(const Raw<XT> &r, float (&v)[8])
 {
-    const uint32_t w[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
-    if constexpr (XT == SKV_F32) {
-        const uint32_t u[4] = {r.a[1].x, r.a[1].y, r.a[1].z, r.a[1].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = __uint_as_float(w[i]);
-            v[4 + i] = __uint_as_float(u[i]);
-        }
-    } else if constexpr (XT == SKV_F16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    for (int i = 0; i < 2 * elem(XT); ++i) {
+        if constexpr (XT == SKV_F32) {
+            v[i] = __uint_as_float(r.w[i]);
+        } else if constexpr (XT == SKV_F16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
             v[2 * i] = f.x;
             v[2 * i + 1] = f.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
         }
     }
+}
+// Copy a row of D values to shared memory, 16 bytes at a time, neighbouring lanes side by side (zeros
+// unless `in`).
+template <int XT, int LPR>
+__device__ __forceinline__ void copy_row(uint32_t dst, const void *x, int64_t at, int l, bool in)
+{
+    const uint8_t *src = static_cast<const uint8_t *>(x) + at * elem(XT);
+#pragma unroll
+    for (int k = 0; k < elem(XT) / 2; ++k) cp_async16(dst + (k * LPR + l) * 16, src + (k * LPR + l) * 16, in ? 16 : 0);
+}
+// A lane's two groups of a row in shared memory.
+template <int XT>
+__device__ __forceinline__ void read_row(const uint8_t *row, int a, int b, float (&v)[8])
+{
+    Raw<XT> r;
+    if constexpr (XT == SKV_F32) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(row + 4 * a), y = *reinterpret_cast<const uint4 *>(row + 4 * b);
+        r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+        r.w[4] = y.x; r.w[5] = y.y; r.w[6] = y.z; r.w[7] = y.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(row + 2 * a), y = *reinterpret_cast<const uint2 *>(row + 2 * b);
+        r.w[0] = x.x; r.w[1] = x.y; r.w[2] = y.x; r.w[3] = y.y;
+    }
+    to_f32<XT>(r, v);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -159,50 +193,157 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ void store_as(int type, void *p, int64_t at, const float (&v)[8])
+// A lane's two groups as rows of a type.
+__device__ __forceinline__ void store_as(int type, void *out, int64_t at, int a, int b, const float (&v)[8])
 {
     if (type == SKV_F32) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if (type == SKV_F16) {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
-            make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+        float *p = static_cast<float *>(out) + at;
+        *reinterpret_cast<float4 *>(p + a) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + b) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        uint16_t *p = static_cast<uint16_t *>(out) + at;
+        uint2 x, y;
+        if (type == SKV_F16) {
+            x = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+            y = make_uint2(pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+        } else {
+            x = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            y = make_uint2(pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        }
+        *reinterpret_cast<uint2 *>(p + a) = x;
+        *reinterpret_cast<uint2 *>(p + b) = y;
     }
 }
 
-// The run of rows [first, first + rows) that a CTA takes, its tokens' angles in `tab`
-// [token][half], for tokens from `t0` on.
-struct Chunk {
-    int64_t t0;
-    int head0, heads, rows;
-};
-template <int D>
-constexpr int kRows = kThreads / (D / 8) * kIter;
-
-template <int D>
-__device__ __forceinline__ Chunk chunk_of(const Args &a, int64_t c)
+// Two fp32 operations in one instruction; the values stand in pairs of registers.
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1)
 {
-    Chunk k;
-    k.heads = a.H + a.Hk + a.Hv;
-    const int64_t first = c * kRows<D>;
-    k.t0 = first / k.heads;
-    k.head0 = static_cast<int>(first - k.t0 * k.heads);
-    const int64_t left = a.n * k.heads - first;
-    k.rows = left < kRows<D> ? static_cast<int>(left) : kRows<D>;
-    return k;
+    const float2 d = __fmul2_rn(make_float2(a0, a1), make_float2(b0, b1));
+    d0 = d.x;
+    d1 = d.y;
 }
-__device__ __forceinline__ void angles(const Args &a, const Chunk &k, float2 *tab)
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1)
 {
-    const int tokens = (k.head0 + k.rows - 1) / k.heads + 1;
-    for (int i = threadIdx.x; i < tokens * a.half; i += kThreads) {
-        const int t = i / a.half, p = i - t * a.half;
-        int ax = a.axis ? __ldg(a.axis + p) : 0;
-        if (static_cast<unsigned>(ax) >= static_cast<unsigned>(a.n_axes)) ax = 0;
-        tab[i] = cos_sin(__ldg(a.pos + ax * a.n + k.t0 + t), __ldg(a.freq + p), a.factor);
+    const float2 d = __ffma2_rn(make_float2(a0, a1), make_float2(b0, b1), make_float2(c0, c1));
+    d0 = d.x;
+    d1 = d.y;
+}
+template <typename F>
+__device__ __forceinline__ void pairs(F f)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) f(i);
+}
+
+// The groups of lane l: their first values.
+struct Groups {
+    int a, b;
+};
+template <int LPR, bool INTER>
+__device__ __forceinline__ Groups groups_of(int half, int l)
+{
+    if (INTER) return Groups{8 * l, 8 * l + 4};
+    const int hl = half >> 2;                              // lanes of a half; the others hold what passes
+    return l < hl ? Groups{4 * l, half + 4 * l} : Groups{8 * l, 8 * l + 4};
+}
+
+// What a lane needs of its token's angles: its values turn as
+//   y = c v + s partner(v),
+// partner: the other value of its pair; `in`: pairs that turn (of four, the first ones; the others
+// have c = 1 or the weight).  back: the angles' negatives.
+struct Turn {
+    float c[8], s[8];
+    int in;
+};
+struct Pairs {
+    float2 p[2];                                           // (cos, sin) of pairs 2 lane, 2 lane + 1
+};
+// The lane's pairs: turns a position, and the axis of their positions.
+struct Lane {
+    uint64_t turns[2];
+    int axis[2];                                           // -1: no such pair
+};
+__device__ __forceinline__ Lane lane_of(const Args &a)
+{
+    Lane r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int p = 2 * (threadIdx.x & 31) + i;
+        r.turns[i] = 0;
+        r.axis[i] = -1;
+        if (p < a.half) {
+            int ax = a.axis ? __ldg(a.axis + p) : 0;
+            if (static_cast<unsigned>(ax) >= static_cast<unsigned>(a.n_axes)) ax = 0;
+            r.axis[i] = ax;
+            r.turns[i] = turns_of(__ldg(a.freq + p));
+        }
+    }
+    return r;
+}
+// A token's positions for the lane's pairs, its first axis' one, and its cache row.
+struct Token {
+    int32_t pos[2], first, at;
+};
+__device__ __forceinline__ Token token_of(const Args &a, const Lane &ln, int t)
+{
+    Token r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.pos[i] = ln.axis[i] >= 0 ? __ldg(a.pos + ln.axis[i] * a.n + t) : 0;
+    r.first = __ldg(a.pos + t);
+    r.at = a.positions ? __ldg(a.positions + t) : -1;
+    return r;
+}
+__device__ __forceinline__ Pairs pairs_of(const Args &a, const Lane &ln, const Token &tk)
+{
+    Pairs r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.p[i] = cos_sin(tk.pos[i], ln.turns[i], a.factor);
+    return r;
+}
+// A place in the line of batches.
+struct Place {
+    int t, b;
+    __device__ __forceinline__ void step(int per)
+    {
+        if (++b == per) {
+            b = 0;
+            ++t;
+        }
+    }
+};
+
+// (All lanes of the warp take part.)
+template <bool BACK, bool INTER>
+__device__ __forceinline__ Turn turn_of(const Args &a, const Pairs &pr, int l)
+{
+    Turn r;
+    r.in = min(4, max(0, a.half - 4 * l));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                          // pair 4l + i
+        float c = __shfl_sync(0xffffffffu, pr.p[i & 1].x, 2 * l + (i >> 1));
+        float s = __shfl_sync(0xffffffffu, pr.p[i & 1].y, 2 * l + (i >> 1));
+        if (i >= r.in) c = 1.f;
+        if (BACK) s = -s;
+        r.c[INTER ? 2 * i : i] = r.c[INTER ? 2 * i + 1 : 4 + i] = c;
+        r.s[INTER ? 2 * i : i] = -s;
+        r.s[INTER ? 2 * i + 1 : 4 + i] = s;
+    }
+    return r;
+}
+template <bool INTER>
+__device__ __forceinline__ constexpr int partner(int i) { return INTER ? i ^ 1 : i ^ 4; }
+
+// c v + s partner(v)
+template <bool INTER>
+__device__ __forceinline__ void turn(const Turn &t, const float (&v)[8], float (&y)[8])
+{
+    pairs([&](int i) { mul2(y[i], y[i + 1], v[i], v[i + 1], t.c[i], t.c[i + 1]); });
+    if (t.in == 4) {
+        pairs([&](int i) { fma2(y[i], y[i + 1], v[partner<INTER>(i)], v[partner<INTER>(i + 1)], t.s[i], t.s[i + 1], y[i], y[i + 1]); });
+    } else if (INTER) {                                    // (split halves turn whole lanes)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < t.in) fma2(y[2 * i], y[2 * i + 1], v[2 * i + 1], v[2 * i], t.s[2 * i], t.s[2 * i + 1], y[2 * i], y[2 * i + 1]);
     }
 }
 
@@ -214,57 +355,46 @@ __device__ __forceinline__ float row_sum(float s)
     return s;
 }
 
-// Turn a row's values (lane l of its LPR lanes) by its token's angles; back: by
-// their negatives.  All lanes of the warp take part.
-template <int LPR, bool BACK>
-__device__ __forceinline__ void turn(const Args &a, const float2 *tab, int l, float (&v)[8])
+__device__ __forceinline__ void load_weight(const float *w, const Groups &gr, float (&v)[8])
 {
-    if (a.inter) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(w + gr.a)), y = __ldg(reinterpret_cast<const float4 *>(w + gr.b));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+}
+// The weight enters the angles' factors: the value's own with c, its partner's with s.
+template <bool INTER>
+__device__ __forceinline__ void weigh(Turn &t, const float *w, const Groups &gr)
+{
+    float wv[8];
+    load_weight(w, gr, wv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = 4 * l + i;
-            if (p < a.half) {
-                const float2 cs = tab[p];
-                const float sn = BACK ? -cs.y : cs.y;
-                const float x = v[2 * i], y = v[2 * i + 1];
-                v[2 * i] = x * cs.x - y * sn;
-                v[2 * i + 1] = x * sn + y * cs.x;
-            }
-        }
-    } else {
-        const int hl = a.half >> 3;                        // lanes of a half
-        const int lane = threadIdx.x & 31;
-        const bool lower = l < hl, in = l < 2 * hl;
-        const int src = lower ? lane + hl : in ? lane - hl : lane;
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, v[i], src);
-        if (in) {
-            const float4 *cs = reinterpret_cast<const float4 *>(tab + 8 * (lower ? l : l - hl));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 c = cs[i];                    // (cos, sin) of two pairs
-                const bool neg = BACK ? !lower : lower;    // lower: a cos - b sin, upper: b cos + a sin
-                v[2 * i] = v[2 * i] * c.x + (neg ? -c.y : c.y) * o[2 * i];
-                v[2 * i + 1] = v[2 * i + 1] * c.z + (neg ? -c.w : c.w) * o[2 * i + 1];
-            }
-        }
+    for (int i = 0; i < 8; ++i) {
+        t.c[i] *= wv[i];
+        t.s[i] *= wv[partner<INTER>(i)];
     }
 }
 
-__device__ __forceinline__ void load_weight(const float *w, int l, float (&v)[8])
+// A lane's groups into the cache row at position p (negative: none).  Blocks of quantised rows want
+// eight consecutive values of a lane: `stage` (the warp's, 32 x 8 floats) puts them in
+// order where the groups are not.  All lanes of the warp take part.
+template <int LPR, bool ORDERED>
+__device__ __forceinline__ void put_cache(const Dst &d, int64_t p, int head, int l, const Groups &gr, float (&v)[8], float *stage,
+                                          int *status)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ldg(w + 8 * l + i);
-}
-
-// One row's part into its cache row; p: its position, or negative.
-__device__ __forceinline__ void put_cache(const Dst &d, int D, int64_t p, int head, int l, const float (&v)[8], int *status)
-{
-    const bool quant = d.type != SKV_F16;
+    constexpr int D = LPR * 8;
     __half d16;
     uint32_t w0 = 0, w1 = 0;
-    if (quant) {                                           // the whole warp takes part
+    if (d.type != SKV_F16) {
+        if (!ORDERED) {
+            float *row = stage + ((threadIdx.x & 31) / LPR) * D;
+            __syncwarp();
+            *reinterpret_cast<float4 *>(row + gr.a) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(row + gr.b) = make_float4(v[4], v[5], v[6], v[7]);
+            __syncwarp();
+            const float4 x = reinterpret_cast<const float4 *>(row)[2 * l], y = reinterpret_cast<const float4 *>(row)[2 * l + 1];
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        }
         if (d.type == SKV_Q8_0) encode8<SKV_Q8_0>(v, d16, w0, w1);
         else encode8<SKV_Q4_0>(v, d16, w0, w1);
     }
@@ -274,215 +404,274 @@ __device__ __forceinline__ void put_cache(const Dst &d, int D, int64_t p, int he
         return;
     }
     uint8_t *row = p < d.n0 ? d.d0 + p * d.row_bytes : d.d1 + (p - d.n0) * d.row_bytes;
-    if (quant) {
+    if (d.type != SKV_F16) {
         const int blk = d.type == SKV_Q8_0 ? 34 : 18;
         uint8_t *b = row + (static_cast<int64_t>(head) * (D / 32) + (l >> 2)) * blk;
         if (d.type == SKV_Q8_0) store8<SKV_Q8_0>(b, l, d16, w0, w1);
         else store8<SKV_Q4_0>(b, l, d16, w0, w1);
         return;
     }
-    uint8_t *o = row + (static_cast<int64_t>(head) * D + 8 * l) * 2;
-    const uint32_t h[4] = {pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7])};
-    if (d.vec16) {
-        *reinterpret_cast<uint4 *>(o) = make_uint4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(o)[i] = h[i];   // rows are 4-byte aligned
+    uint8_t *o = row + static_cast<int64_t>(head) * D * 2;
+    const uint2 x = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3])), y = make_uint2(pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+    if (d.vec8) {
+        *reinterpret_cast<uint2 *>(o + 2 * gr.a) = x;
+        *reinterpret_cast<uint2 *>(o + 2 * gr.b) = y;
+    } else {                                               // rows are 4-byte aligned
+        uint32_t *q = reinterpret_cast<uint32_t *>(o + 2 * gr.a), *r = reinterpret_cast<uint32_t *>(o + 2 * gr.b);
+        q[0] = x.x;
+        q[1] = x.y;
+        r[0] = y.x;
+        r[1] = y.y;
     }
 }
 
-template <int XT, int D, bool CACHE>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Args a)
+// Rows of a thread in a batch, by the bytes of an element that it loads.
+constexpr int iter_of(int bytes) { return bytes <= 2 ? 4 : bytes <= 4 ? 2 : 1; }
+
+template <int XT, int D, bool CACHE, bool INTER>
+__global__ void __launch_bounds__(kThreads, kCtas) rope_kernel(const Args a)
 {
-    constexpr int LPR = D / 8, RPI = kThreads / LPR;
-    extern __shared__ float4 smem4[];
-    float2 *tab = reinterpret_cast<float2 *>(smem4);
-    const Chunk ck = chunk_of<D>(a, blockIdx.x);
-    const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
-    Raw<XT> raw[kIter];
-    int tok[kIter], head[kIter];                           // token after t0 and head, or head -1
-    int32_t at[kIter], p0[kIter];
+    constexpr int LPR = D / 8, RPW = 32 / LPR;             // lanes of a row, rows of a warp at a time
+    constexpr int IT = iter_of(elem(XT)), RB = RPW * IT;   // rows of a batch
+    __shared__ __align__(16) float s_stage[CACHE && !INTER ? kThreads / 32 : 1][CACHE && !INTER ? 256 : 1];
+    const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const int64_t w0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t lo = a.batches / warps * w0 + min(w0, a.batches % warps);
+    int left = static_cast<int>(a.batches / warps) + (w0 < a.batches % warps);
+    if (!left) return;                                     // (whole warps)
+    const int per = a.bq + a.bk + a.bv;
+    const Groups turned = groups_of<LPR, INTER>(a.half, l), plain{8 * l, 8 * l + 4};
+    Place next{static_cast<int>(lo / per), static_cast<int>(lo % per)};
+    Raw<XT> asked[IT];
+    auto ask = [&]() {
+        const int seg = next.b < a.bq ? 0 : !CACHE || next.b < a.bq + a.bk ? 1 : 2;
+        const int h0 = (seg == 0 ? next.b : seg == 1 ? next.b - a.bq : next.b - a.bq - a.bk) * RB + g, heads = seg == 0 ? a.H : a.Hk;
+        const void *x = seg == 0 ? a.q.x : seg == 1 ? a.k.x : a.v;
+        const int64_t x0 = static_cast<int64_t>(next.t) * (seg == 0 ? a.q.stride : seg == 1 ? a.k.stride : a.v_stride);
+        const Groups gr = CACHE && seg == 2 ? plain : turned;
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-        const int r = it * RPI + g;
-        raw[it] = zero8<XT>();
-        tok[it] = 0;
-        head[it] = -1;
-        at[it] = -1;
-        p0[it] = -1;
-        if (r < ck.rows) {
-            const int x = ck.head0 + r;
-            tok[it] = x / ck.heads;
-            const int hd = x - tok[it] * ck.heads;
-            head[it] = hd;
-            const int64_t t = ck.t0 + tok[it];
-            if (hd < a.H) raw[it] = load8<XT>(a.q.x, t * a.q.stride + hd * D + 8 * l);
-            else if (hd < a.H + a.Hk) raw[it] = load8<XT>(a.k.x, t * a.k.stride + (hd - a.H) * D + 8 * l);
-            else raw[it] = load8<XT>(a.v, t * a.v_stride + (hd - a.H - a.Hk) * D + 8 * l);
-            p0[it] = __ldg(a.pos + t);
-            if (CACHE && hd >= a.H) at[it] = __ldg(a.positions + t);
+        for (int it = 0; it < IT; ++it) {
+            asked[it] = zero_rows<XT>();
+            if (h0 + it * RPW < heads) asked[it] = load_rows<XT>(x, x0 + (h0 + it * RPW) * D, gr.a, gr.b);
         }
-    }
-    angles(a, ck, tab);
-    __syncthreads();
+    };
+    ask();
+    const Lane ln = lane_of(a);
+    Token coming = token_of(a, ln, next.t);
+    Pairs pr;
+    Turn tr;
+    bool pad = false;
+    int at = -1, seg_last = -1;
+    int t_last = -1;
+#pragma unroll 1
+    for (; left; --left) {
+        const Place p = next;
+        Raw<XT> raw[IT];
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-        float v[8];
-        const int hd = head[it];
-        const bool isq = hd < a.H, isk = !isq && hd < a.H + a.Hk;
-        to_f32<XT>(p0[it] < 0 ? zero8<XT>() : raw[it], v); // a padding token's rows are zeros
-        if (a.q.w || a.k.w) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-            ss = row_sum<LPR>(ss);
-            const float *w = hd < 0 ? nullptr : isq ? a.q.w : isk ? a.k.w : nullptr;
-            if (w) {
-                const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-                float wv[8];
-                load_weight(w, l, wv);
-                // padding stays zero whatever eps is
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = p0[it] < 0 ? 0.f : v[i] * rs * wv[i];
+        for (int it = 0; it < IT; ++it) raw[it] = asked[it];
+        next.step(per);
+        if (left > 1) ask();
+        const int seg = p.b < a.bq ? 0 : !CACHE || p.b < a.bq + a.bk ? 1 : 2;
+        const float *w = seg == 0 ? a.q.w : seg == 1 ? a.k.w : nullptr;
+        if (p.t != t_last) {
+            pad = coming.first < 0;                        // a padding token's results are zeros
+            at = pad ? -1 : coming.at;
+            pr = pairs_of(a, ln, coming);
+            if (p.t + 1 < a.n) coming = token_of(a, ln, p.t + 1);
+        }
+        if (p.t != t_last || seg != seg_last) {
+            if (!CACHE || seg < 2) {
+                tr = turn_of<false, INTER>(a, pr, l);
+                if (w) weigh<INTER>(tr, w, turned);
             }
+            t_last = p.t;
+            seg_last = seg;
         }
-        float y[8];
+        const int h0 = (seg == 0 ? p.b : seg == 1 ? p.b - a.bq : p.b - a.bq - a.bk) * RB, heads = seg == 0 ? a.H : a.Hk;
+        const int64_t o0 = static_cast<int64_t>(p.t) * heads * D;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = v[i];
-        turn<LPR, false>(a, tab + tok[it] * a.half, l, y);
-        if (!isq && !isk) {                                // values do not turn
+        for (int it = 0; it < IT; ++it) {
+            if (h0 + it * RPW >= heads) break;
+            const int hd = h0 + it * RPW + g;
+            float v[8];
+            to_f32<XT>(raw[it], v);
+            if (!CACHE || seg < 2) {
+                float y[8];
+                turn<INTER>(tr, v, y);
+                if (w) {
+                    float s0, s1;
+                    mul2(s0, s1, v[0], v[1], v[0], v[1]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = v[i];
-        }
-        if (p0[it] < 0) {
+                    for (int i = 2; i < 8; i += 2) fma2(s0, s1, v[i], v[i + 1], v[i], v[i + 1], s0, s1);
+                    const float rs = rsqrtf(row_sum<LPR>(s0 + s1) * (1.f / D) + a.eps);
+                    pairs([&](int i) { mul2(v[i], v[i + 1], y[i], y[i + 1], rs, rs); });
+                } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 0.f;
-        }
-        const int64_t t = ck.t0 + tok[it];
-        if (hd >= 0 && isq) store_as(CACHE ? SKV_F16 : a.o_type, a.q.out, (t * a.H + hd) * D + 8 * l, y);
-        if constexpr (CACHE) {
-            const int64_t p = p0[it] < 0 ? -1 : at[it];
-            if (__any_sync(0xffffffffu, isk)) put_cache(a.kd, D, isk ? p : -1, hd - a.H, l, y, a.status);
-            const bool isv = hd >= a.H + a.Hk;
-            if (__any_sync(0xffffffffu, isv)) put_cache(a.vd, D, isv ? p : -1, hd - a.H - a.Hk, l, y, a.status);
-        } else {
-            if (isk) store_as(a.o_type, a.k.out, (t * a.Hk + hd - a.H) * D + 8 * l, y);
+                    for (int i = 0; i < 8; ++i) v[i] = y[i];
+                }
+            }
+            if (pad) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            }
+            if constexpr (CACHE) {
+                if (seg == 2) put_cache<LPR, true>(a.vd, hd < heads ? at : -1, hd, l, plain, v, nullptr, a.status);
+                else if (seg == 1) put_cache<LPR, INTER>(a.kd, hd < heads ? at : -1, hd, l, turned, v, s_stage[INTER ? 0 : threadIdx.x >> 5], a.status);
+                else if (hd < heads) store_as(SKV_F16, a.q.out, o0 + hd * D, turned.a, turned.b, v);
+            } else {
+                if (hd < heads) store_as(a.o_type, seg == 0 ? a.q.out : a.k.out, o0 + hd * D, turned.a, turned.b, v);
+            }
         }
     }
 }
 
 // Gradients.  With a norm, each thread also sums its eight columns of the weights'
-// gradients over its rows; a CTA takes chunks in turn (a fixed deal), adds up its
-// threads' sums at the end and leaves them in its own slot of dw.
-template <int GT, int XT, int D, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_back_kernel(const Args a)
+// gradients over its rows; a CTA adds up its threads' sums at the end and leaves them in its own
+// slot of dw.
+template <int GT, int XT, int D, bool NORM, bool INTER>
+__global__ void __launch_bounds__(kThreads, kCtas) rope_back_kernel(const Args a)
 {
-    constexpr int LPR = D / 8, RPI = kThreads / LPR;
-    extern __shared__ float4 smem4[];
-    float2 *tab = reinterpret_cast<float2 *>(smem4);
-    const int l = threadIdx.x % LPR, g = threadIdx.x / LPR;
-    float sq[8], sk[8];
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int IT = iter_of(elem(GT) + (NORM ? elem(XT) : 0)), RB = RPW * IT;
+    constexpr int ROWG = D * elem(GT), ROWX = NORM ? D * elem(XT) : 0;
+    constexpr int BATCH = RB * (ROWG + ROWX), DEPTH = kRing / BATCH;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t *ring = smem + (threadIdx.x >> 5) * kRing;
+    const uint32_t ring_s = smem_addr(ring);
+    const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const int64_t w0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t lo = a.batches / warps * w0 + min(w0, a.batches % warps);
+    int left = static_cast<int>(a.batches / warps) + (w0 < a.batches % warps);
+    const Groups gr = groups_of<LPR, INTER>(a.half, l);
+    float sum[2][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq[i] = sk[i] = 0.f;
-    for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-        const Chunk ck = chunk_of<D>(a, c);
-        Raw<XT> raw[NORM ? kIter : 1];
-        Raw<GT> grad[kIter];
-        int tok[kIter], head[kIter];
-        int32_t p0[kIter];
-#pragma unroll
-        for (int it = 0; it < kIter; ++it) {
-            const int r = it * RPI + g;
-            if (NORM) raw[it] = zero8<XT>();
-            grad[it] = zero8<GT>();
-            tok[it] = 0;
-            head[it] = -1;
-            p0[it] = -1;
-            if (r < ck.rows) {
-                const int x = ck.head0 + r;
-                tok[it] = x / ck.heads;
-                const int hd = x - tok[it] * ck.heads;
-                head[it] = hd;
-                const int64_t t = ck.t0 + tok[it];
-                const Side &s = hd < a.H ? a.q : a.k;
-                const int hh = hd < a.H ? hd : hd - a.H, hs = hd < a.H ? a.H : a.Hk;
-                grad[it] = load8<GT>(s.g, (t * hs + hh) * D + 8 * l);
-                if (NORM && s.w) raw[it] = load8<XT>(s.x, t * s.stride + hh * D + 8 * l);
-                p0[it] = __ldg(a.pos + t);
-            }
-        }
-        angles(a, ck, tab);
-        __syncthreads();
-#pragma unroll
-        for (int it = 0; it < kIter; ++it) {
-            const int hd = head[it];
-            const bool isq = hd < a.H, pad = p0[it] < 0;
-            float y[8];
-            to_f32<GT>(pad ? zero8<GT>() : grad[it], y);
-            turn<LPR, true>(a, tab + tok[it] * a.half, l, y);
-            if (NORM) {
-                const float *w = hd < 0 ? nullptr : isq ? a.q.w : a.k.w;
-                float x[8];
-                to_f32<XT>(pad ? zero8<XT>() : raw[it], x);
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-                ss = row_sum<LPR>(ss);
-                const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-                float u[8], m = 0.f;
-                float wv[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) wv[i] = 1.f;
-                if (w) load_weight(w, l, wv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= rs;
-                    u[i] = y[i] * wv[i];
-                    m = fmaf(u[i], x[i], m);
-                }
-                m = row_sum<LPR>(m) * (1.f / D);
-                if (w && !pad) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float s = y[i] * x[i];
-                        if (isq) sq[i] += s;
-                        else sk[i] += s;
-                        y[i] = rs * (u[i] - x[i] * m);
-                    }
-                }
-            }
-            if (pad) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = 0.f;
-            }
-            if (hd >= 0) {
+    for (int i = 0; i < 8; ++i) sum[0][i] = sum[1][i] = 0.f;
+    if (left) {
+        const int per = a.bq + a.bk;
+        Place next{static_cast<int>(lo / per), static_cast<int>(lo % per)};
+        Place p = next;
+        int asks = left, slot = 0, filled = 0;
+        auto ask = [&]() {
+            if (asks > 0) {
+                --asks;
+                const bool isq = next.b < a.bq;
                 const Side &s = isq ? a.q : a.k;
-                const int64_t t = ck.t0 + tok[it];
-                store_as(XT, s.out, t * s.out_stride + (isq ? hd : hd - a.H) * D + 8 * l, y);
+                const int h0 = (isq ? next.b : next.b - a.bq) * RB + g, heads = isq ? a.H : a.Hk;
+                const int64_t g0 = static_cast<int64_t>(next.t) * heads * D, x0 = next.t * s.stride;
+                const uint32_t dst = ring_s + filled * BATCH;
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    const bool in = h0 + it * RPW < heads;
+                    const int hd = in ? h0 + it * RPW : 0;
+                    copy_row<GT, LPR>(dst + (it * RPW + g) * ROWG, s.g, g0 + hd * D, l, in);
+                    if (NORM && s.w) copy_row<XT, LPR>(dst + RB * ROWG + (it * RPW + g) * ROWX, s.x, x0 + hd * D, l, in);
+                }
+                next.step(per);
+                filled = filled + 1 == DEPTH ? 0 : filled + 1;
             }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH - 1; ++i) ask();
+        const Lane ln = lane_of(a);
+        Token coming = token_of(a, ln, p.t);
+        Pairs pr;
+        Turn tr;
+        float wv[8];
+        bool pad = false;
+        int t_last = -1;
+        int seg_last = -1;
+#pragma unroll 1
+        for (; left; --left) {
+            __syncwarp();
+            ask();
+            const bool isq = p.b < a.bq;
+            const Side &s = isq ? a.q : a.k;
+            const bool norm = NORM && s.w;
+            if (p.t != t_last) {
+                pad = coming.first < 0;
+                pr = pairs_of(a, ln, coming);
+                if (p.t + 1 < a.n) coming = token_of(a, ln, p.t + 1);
+            }
+            if (p.t != t_last || isq != seg_last) {
+                tr = turn_of<true, INTER>(a, pr, l);
+                if (norm) load_weight(s.w, gr, wv);
+                t_last = p.t;
+                seg_last = isq;
+            }
+            cp_async_wait<DEPTH - 1>();
+            __syncwarp();
+            const int h0 = (isq ? p.b : p.b - a.bq) * RB, heads = isq ? a.H : a.Hk;
+            const int64_t o0 = p.t * s.out_stride;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                if (h0 + it * RPW >= heads) break;
+                const int hd = h0 + it * RPW + g;
+                float y[8], v[8];
+                read_row<GT>(ring + slot * BATCH + (it * RPW + g) * ROWG, gr.a, gr.b, y);
+                turn<INTER>(tr, y, v);
+                if (norm) {
+                    float x[8], u[8], s0, s1, m0, m1;
+                    read_row<XT>(ring + slot * BATCH + RB * ROWG + (it * RPW + g) * ROWX, gr.a, gr.b, x);
+                    pairs([&](int i) { mul2(u[i], u[i + 1], v[i], v[i + 1], wv[i], wv[i + 1]); });
+                    mul2(s0, s1, x[0], x[1], x[0], x[1]);
+                    mul2(m0, m1, u[0], u[1], x[0], x[1]);
+#pragma unroll
+                    for (int i = 2; i < 8; i += 2) {
+                        fma2(s0, s1, x[i], x[i + 1], x[i], x[i + 1], s0, s1);
+                        fma2(m0, m1, u[i], u[i + 1], x[i], x[i + 1], m0, m1);
+                    }
+                    float ss = s0 + s1, ux = m0 + m1;
+#pragma unroll
+                    for (int d = LPR / 2; d; d >>= 1) {
+                        ss += __shfl_xor_sync(0xffffffffu, ss, d);
+                        ux += __shfl_xor_sync(0xffffffffu, ux, d);
+                    }
+                    const float rs = rsqrtf(ss * (1.f / D) + a.eps);
+                    pairs([&](int i) { mul2(x[i], x[i + 1], x[i], x[i + 1], rs, rs); });
+                    if (!pad && hd < heads) {              // (rows that are none are zeros, but eps may be 0)
+                        if (isq) pairs([&](int i) { fma2(sum[0][i], sum[0][i + 1], v[i], v[i + 1], x[i], x[i + 1], sum[0][i], sum[0][i + 1]); });
+                        else pairs([&](int i) { fma2(sum[1][i], sum[1][i + 1], v[i], v[i + 1], x[i], x[i + 1], sum[1][i], sum[1][i + 1]); });
+                    }
+                    // u - (x rs) mean(u x rs)
+                    const float k = -(ux * rs) * (1.f / D);
+                    pairs([&](int i) { fma2(u[i], u[i + 1], x[i], x[i + 1], k, k, u[i], u[i + 1]); });
+                    pairs([&](int i) { mul2(v[i], v[i + 1], u[i], u[i + 1], rs, rs); });
+                }
+                if (pad) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                }
+                if (hd < heads) store_as(XT, s.out, o0 + hd * D, gr.a, gr.b, v);
+            }
+            slot = slot + 1 == DEPTH ? 0 : slot + 1;
+            p.step(per);
         }
-        __syncthreads();                                   // the table is used again
     }
     if constexpr (NORM) {
-        float *red = reinterpret_cast<float *>(smem4);     // [warp][2][D]
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        __syncthreads();                                   // the rings are free
+        float(*red)[2][D] = reinterpret_cast<float(*)[2][D]>(smem);
+        const int warp = threadIdx.x >> 5;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
 #pragma unroll
             for (int o = LPR; o < 32; o <<= 1) {
-                sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], o);
-                sk[i] += __shfl_xor_sync(0xffffffffu, sk[i], o);
+                sum[0][i] += __shfl_xor_sync(0xffffffffu, sum[0][i], o);
+                sum[1][i] += __shfl_xor_sync(0xffffffffu, sum[1][i], o);
             }
             if (lane < LPR) {
-                red[(warp * 2) * D + 8 * l + i] = sq[i];
-                red[(warp * 2 + 1) * D + 8 * l + i] = sk[i];
+                const int at = i < 4 ? gr.a + i : gr.b + i - 4;
+                red[warp][0][at] = sum[0][i];
+                red[warp][1][at] = sum[1][i];
             }
         }
         __syncthreads();
         if (threadIdx.x < 2 * D) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) s += red[w * 2 * D + threadIdx.x];
+            for (int w = 0; w < kThreads / 32; ++w) s += red[w][threadIdx.x / D][threadIdx.x % D];
             a.dw[static_cast<int64_t>(blockIdx.x) * 2 * D + threadIdx.x] = s;
         }
     }
@@ -508,7 +697,6 @@ __global__ void __launch_bounds__(1024) rope_weight_kernel(const float *dw, int 
     }
 }
 
-static int elem_size(int type) { return type == SKV_F32 ? 4 : 2; }
 static bool row_type(int t) { return t == SKV_F32 || t == SKV_F16 || t == SKV_BF16; }
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
@@ -518,8 +706,8 @@ static int check(skv_handle *h, const skv_rope_spec *s, int64_t n, int32_t H, in
     if (s->D != 64 && s->D != 128) return fail(h, SKV_EUNSUPPORTED, "head dim %d (supported: 64, 128)", s->D);
     if (s->rot_dims < 0 || s->rot_dims > s->D || s->rot_dims % 2)
         return fail(h, SKV_EINVAL, "rot_dims %d: even and at most D is wanted", s->rot_dims);
-    if (!s->interleaved && s->rot_dims % 16)
-        return fail(h, SKV_EUNSUPPORTED, "rot_dims %d: a multiple of 16 is wanted for split halves", s->rot_dims);
+    if (!s->interleaved && s->rot_dims % 8)
+        return fail(h, SKV_EUNSUPPORTED, "rot_dims %d: a multiple of 8 is wanted for split halves", s->rot_dims);
     if (s->n_axes < 1 || s->n_axes > 8) return fail(h, SKV_EINVAL, "n_axes %d: 1 to 8", s->n_axes);
     if (s->rot_dims && !s->freq) return fail(h, SKV_EINVAL, "freq is NULL");
     if (n < 0 || n > INT32_MAX || H < 0 || Hk < 0 || H > 65535 || Hk > 65535)
@@ -536,7 +724,7 @@ static int check_rows(skv_handle *h, const char *name, const void *p, int64_t st
     if (!p) return fail(h, SKV_EINVAL, "%s is NULL", name);
     if (n > 1 && (stride < static_cast<int64_t>(heads) * D || stride > (int64_t(1) << 40)))
         return fail(h, SKV_EINVAL, "%s: stride %lld holds no %d heads of %d", name, (long long)stride, heads, D);
-    if (misaligned(p, 16) || (n > 1 && stride * elem_size(type) % 16))
+    if (misaligned(p, 16) || (n > 1 && stride * elem(type) % 16))
         return fail(h, SKV_EUNSUPPORTED, "%s: base and stride must be multiples of 16 bytes", name);
     return SKV_OK;
 }
@@ -559,11 +747,11 @@ static int check_dst(skv_handle *h, const char *name, const skv_cache_dst *c, in
     d->row_bytes = c->row_bytes;
     d->n0 = c->n_rows0;
     d->n1 = c->n_rows1;
-    d->vec16 = c->row_bytes % 16 == 0 && !misaligned(d->d0, 16) && !misaligned(d->d1, 16);
+    d->vec8 = c->row_bytes % 8 == 0 && !misaligned(d->d0, 8) && !misaligned(d->d1, 8);
     return SKV_OK;
 }
 
-static Args base_args(skv_handle *h, const skv_rope_spec *s, int64_t n, int H, int Hk, int Hv, const int32_t *pos)
+static Args base_args(skv_handle *h, const skv_rope_spec *s, int64_t n, int H, int Hk, int Hv, const int32_t *pos, int bytes)
 {
     Args a{};
     a.n = n;
@@ -579,34 +767,74 @@ static Args base_args(skv_handle *h, const skv_rope_spec *s, int64_t n, int H, i
     a.factor = s->factor;
     a.eps = s->eps;
     a.status = h->status;
-    const int64_t rows = n * (H + Hk + Hv), per = kThreads / (s->D / 8) * kIter;
-    a.chunks = (rows + per - 1) / per;
+    // rows of a batch, as the kernels have them
+    const int rb = 256 / s->D * iter_of(bytes);
+    a.bq = (H + rb - 1) / rb;
+    a.bk = (Hk + rb - 1) / rb;
+    a.bv = (Hv + rb - 1) / rb;
+    a.batches = n * (a.bq + a.bk + a.bv);                  // below 2^47; a warp's share below 2^31 (2^36 / resident warps: memory ends before)
     return a;
 }
-// Shared memory of a chunk's angles: at most its rows' tokens.
-static int table_bytes(const Args &a, int D)
+// CTAs for the line of batches: as many as are resident, or a warp for each batch.
+static unsigned grid_of(skv_handle *h, const Args &a, int ctas)
 {
-    const int rows = kThreads / (D / 8) * kIter, heads = a.H + a.Hk + a.Hv;
-    const int tokens = heads == 1 ? rows : (rows - 2) / heads + 2;
-    return tokens * a.half * static_cast<int>(sizeof(float2));
+    const int64_t most = static_cast<int64_t>(ctas) * h->sm_count, need = (a.batches + kThreads / 32 - 1) / (kThreads / 32);
+    return static_cast<unsigned>(need < most ? need : most);
 }
 
+template <int XT, int D, bool CACHE, bool INTER>
+static cudaError_t launch_t(const Args &a, unsigned grid, cudaStream_t st)
+{
+    rope_kernel<XT, D, CACHE, INTER><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <int XT, bool CACHE>
+static cudaError_t launch_x(const Args &a, int D, unsigned grid, cudaStream_t st)
+{
+    if (D == 64) return a.inter ? launch_t<XT, 64, CACHE, true>(a, grid, st) : launch_t<XT, 64, CACHE, false>(a, grid, st);
+    return a.inter ? launch_t<XT, 128, CACHE, true>(a, grid, st) : launch_t<XT, 128, CACHE, false>(a, grid, st);
+}
 template <bool CACHE>
 static int launch(skv_handle *h, const Args &a, int x_type, int D, cudaStream_t st)
 {
-    if (a.chunks > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many rows for one launch");
-    const int smem = table_bytes(a, D);
-    const dim3 grid(static_cast<unsigned>(a.chunks));
-#define SKV_ROPE(T)                                                        \
-    do {                                                                   \
-        if (D == 64) rope_kernel<T, 64, CACHE><<<grid, kThreads, smem, st>>>(a); \
-        else rope_kernel<T, 128, CACHE><<<grid, kThreads, smem, st>>>(a);  \
-    } while (0)
-    if (x_type == SKV_F32) SKV_ROPE(SKV_F32);
-    else if (x_type == SKV_F16) SKV_ROPE(SKV_F16);
-    else SKV_ROPE(SKV_BF16);
-#undef SKV_ROPE
-    return cuda_fail(h, cudaGetLastError(), "rope launch");
+    const unsigned grid = grid_of(h, a, kCtas);
+    cudaError_t e;
+    if (x_type == SKV_F32) e = launch_x<SKV_F32, CACHE>(a, D, grid, st);
+    else if (x_type == SKV_F16) e = launch_x<SKV_F16, CACHE>(a, D, grid, st);
+    else e = launch_x<SKV_BF16, CACHE>(a, D, grid, st);
+    return cuda_fail(h, e, "rope launch");
+}
+
+template <int GT, int XT, int D, bool NORM, bool INTER>
+static cudaError_t launch_back_t(const Args &a, unsigned grid, cudaStream_t st)
+{
+    static KernelAttrCache attr;
+    constexpr int smem = kThreads / 32 * kRing;
+    const cudaError_t e = kernel_smem_optin(attr, reinterpret_cast<const void *>(rope_back_kernel<GT, XT, D, NORM, INTER>), smem, kThreads, nullptr);
+    if (e == cudaSuccess) rope_back_kernel<GT, XT, D, NORM, INTER><<<grid, kThreads, smem, st>>>(a);
+    return e;
+}
+template <int GT, int XT, int D>
+static cudaError_t launch_back_d(const Args &a, bool norm, unsigned grid, cudaStream_t st)
+{
+    if (norm) return a.inter ? launch_back_t<GT, XT, D, true, true>(a, grid, st) : launch_back_t<GT, XT, D, true, false>(a, grid, st);
+    return a.inter ? launch_back_t<GT, XT, D, false, true>(a, grid, st) : launch_back_t<GT, XT, D, false, false>(a, grid, st);
+}
+template <int GT>
+static cudaError_t launch_back_g(const Args &a, int x_type, int D, bool norm, unsigned grid, cudaStream_t st)
+{
+    if (x_type == SKV_F32) return D == 64 ? launch_back_d<GT, SKV_F32, 64>(a, norm, grid, st) : launch_back_d<GT, SKV_F32, 128>(a, norm, grid, st);
+    if (x_type == SKV_F16) return D == 64 ? launch_back_d<GT, SKV_F16, 64>(a, norm, grid, st) : launch_back_d<GT, SKV_F16, 128>(a, norm, grid, st);
+    return D == 64 ? launch_back_d<GT, SKV_BF16, 64>(a, norm, grid, st) : launch_back_d<GT, SKV_BF16, 128>(a, norm, grid, st);
+}
+static int launch_back(skv_handle *h, const Args &a, int g_type, int x_type, int D, bool norm, unsigned grid, cudaStream_t st)
+{
+    cudaError_t e;
+    if (g_type == SKV_F32) e = launch_back_g<SKV_F32>(a, x_type, D, norm, grid, st);
+    else if (g_type == SKV_F16) e = launch_back_g<SKV_F16>(a, x_type, D, norm, grid, st);
+    else e = launch_back_g<SKV_BF16>(a, x_type, D, norm, grid, st);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return cuda_fail(h, e, "rope gradient launch");
 }
 
 }  // namespace rope
@@ -629,11 +857,11 @@ extern "C" int skv_rope(skv_handle *h, const skv_rope_spec *spec, int64_t n, int
     if (!rc) rc = rope::check_rows(h, "q_out", q_out, static_cast<int64_t>(H) * D, H, D, o_type, n);
     if (!rc) rc = rope::check_rows(h, "k_out", k_out, static_cast<int64_t>(Hk) * D, Hk, D, o_type, n);
     if (rc) return rc;
-    if (rope::misaligned(q_weight, 4) || rope::misaligned(k_weight, 4))
-        return fail(h, SKV_EUNSUPPORTED, "weights must be 4-byte aligned");
+    if (rope::misaligned(q_weight, 16) || rope::misaligned(k_weight, 16))
+        return fail(h, SKV_EUNSUPPORTED, "weights must be 16-byte aligned");
     if (n == 0 || H + Hk == 0) return SKV_OK;
     OnDevice on(h->device);
-    rope::Args a = rope::base_args(h, spec, n, H, Hk, 0, pos);
+    rope::Args a = rope::base_args(h, spec, n, H, Hk, 0, pos, rope::elem(x_type));
     a.q = rope::Side{q, q_stride, q_weight, q_out, 0, nullptr};
     a.k = rope::Side{k, k_stride, k_weight, k_out, 0, nullptr};
     a.o_type = o_type;
@@ -658,10 +886,10 @@ extern "C" int skv_rope_append(skv_handle *h, const skv_rope_spec *spec, int64_t
     if (!rc) rc = rope::check_rows(h, "q_out", q_out, static_cast<int64_t>(H) * D, H, D, SKV_F16, n);
     if (rc) return rc;
     if (n > 0 && !positions) return fail(h, SKV_EINVAL, "positions is NULL");
-    if (rope::misaligned(positions, 4) || rope::misaligned(q_weight, 4) || rope::misaligned(k_weight, 4))
-        return fail(h, SKV_EUNSUPPORTED, "positions and weights must be 4-byte aligned");
+    if (rope::misaligned(positions, 4) || rope::misaligned(q_weight, 16) || rope::misaligned(k_weight, 16))
+        return fail(h, SKV_EUNSUPPORTED, "positions must be 4-byte and weights 16-byte aligned");
     OnDevice on(h->device);
-    rope::Args a = rope::base_args(h, spec, n, H, Hk, Hk, pos);
+    rope::Args a = rope::base_args(h, spec, n, H, Hk, Hk, pos, rope::elem(x_type));
     rc = rope::check_dst(h, "k_dst", k_dst, Hk, D, &a.kd);
     if (!rc) rc = rope::check_dst(h, "v_dst", v_dst, Hk, D, &a.vd);
     if (rc || n == 0) return rc;
@@ -695,51 +923,20 @@ extern "C" int skv_rope_backward(skv_handle *h, const skv_rope_spec *spec, int64
     if (rc) return rc;
     if (!q_weight != !dq_weight || !k_weight != !dk_weight)
         return fail(h, SKV_EINVAL, "a weight and its gradient go together");
-    if (rope::misaligned(q_weight, 4) || rope::misaligned(k_weight, 4) || rope::misaligned(dq_weight, 4) ||
+    if (rope::misaligned(q_weight, 16) || rope::misaligned(k_weight, 16) || rope::misaligned(dq_weight, 4) ||
         rope::misaligned(dk_weight, 4))
-        return fail(h, SKV_EUNSUPPORTED, "weights must be 4-byte aligned");
+        return fail(h, SKV_EUNSUPPORTED, "weights must be 16-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     OnDevice on(h->device);
-    rope::Args a = rope::base_args(h, spec, n, H, Hk, 0, pos);
+    rope::Args a = rope::base_args(h, spec, n, H, Hk, 0, pos, rope::elem(g_type) + (norm ? rope::elem(x_type) : 0));
     a.q = rope::Side{q, q_stride, q_weight, dq, dq_stride, dq_out};
     a.k = rope::Side{k, k_stride, k_weight, dk, dk_stride, dk_out};
-    if (!norm && a.chunks == 0) return SKV_OK;
-    if (a.chunks > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many rows for one launch");
-    // with weights: as many CTAs as are resident at once, each with a slot of sums
-    const int64_t most = norm ? 4 * static_cast<int64_t>(h->sm_count) : INT32_MAX;
-    const unsigned grid = static_cast<unsigned>(a.chunks < most ? a.chunks : most);
+    const unsigned grid = rope::grid_of(h, a, rope::kCtas);
     if (norm && grid) {
         if ((rc = ensure_workspace(h, static_cast<size_t>(grid) * 2 * D * sizeof(float), st))) return rc;
         a.dw = static_cast<float *>(h->workspace);
     }
-    int smem = rope::table_bytes(a, D);
-    if (norm && smem < rope::kThreads / 32 * 2 * D * 4) smem = rope::kThreads / 32 * 2 * D * 4;
-    if (grid) {
-#define SKV_BACK(G, X, N)                                                                           \
-    do {                                                                                            \
-        if (D == 64) rope::rope_back_kernel<G, X, 64, N><<<grid, rope::kThreads, smem, st>>>(a);    \
-        else rope::rope_back_kernel<G, X, 128, N><<<grid, rope::kThreads, smem, st>>>(a);           \
-    } while (0)
-#define SKV_BACK_N(G, X)              \
-    do {                              \
-        if (norm) SKV_BACK(G, X, true); \
-        else SKV_BACK(G, X, false);   \
-    } while (0)
-#define SKV_BACK_X(G)                                             \
-    do {                                                          \
-        if (x_type == SKV_F32) SKV_BACK_N(G, SKV_F32);            \
-        else if (x_type == SKV_F16) SKV_BACK_N(G, SKV_F16);       \
-        else SKV_BACK_N(G, SKV_BF16);                             \
-    } while (0)
-        if (g_type == SKV_F32) SKV_BACK_X(SKV_F32);
-        else if (g_type == SKV_F16) SKV_BACK_X(SKV_F16);
-        else SKV_BACK_X(SKV_BF16);
-#undef SKV_BACK_X
-#undef SKV_BACK_N
-#undef SKV_BACK
-        rc = cuda_fail(h, cudaGetLastError(), "rope gradient launch");
-        if (rc) return rc;
-    }
+    if (grid && (rc = rope::launch_back(h, a, g_type, x_type, D, norm, grid, st))) return rc;
     if (norm) {
         rope::rope_weight_kernel<<<2 * D / 32, 1024, 0, st>>>(a.dw, static_cast<int>(grid), D, dq_weight, dk_weight);
         rc = cuda_fail(h, cudaGetLastError(), "rope weight launch");
