@@ -10,10 +10,12 @@
 // from one to the other: while the compute warps form P(j) it runs dK(j-1), dP(j), and
 // while they form dS(j) it runs dV(j), S(j+1).
 //
-// Warps: 0-7 compute (two threads a key, 64 rows of the tile each), 8 TMA, 9 issues S and
-// dV, 10 issues dP and dK (each pair in one thread, whose products run in order: the
-// buffers need no further wait), 11 looks each tile over when it has landed: it folds the powers of two
-// into L and D, tells whether the tile needs a mask, and clears rows of
+// Warps: 0-7 compute (two threads a key, 64 rows of the tile each), 8 TMA, 9 issues the
+// products in the order dV(j), S(j+1), dK(j), dP(j+1) (one thread: they run in order, so the
+// buffers need no further wait, and S(j+1), which the compute warps wait for, never
+// stands behind dP; a thread each for dV, S and dK, dP measured 15 % slower),
+// 10 looks each tile over when it has landed: it folds the powers of two
+// into -L and -D, tells whether the tile needs a mask, and clears rows of
 // tokens that see nothing, whatever they hold.
 //
 // Every mbarrier wait is bounded, as in the prefill kernel.
@@ -25,7 +27,7 @@ namespace skv {
 namespace bwd {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 352;
 constexpr int kCompute = 256;
 constexpr int kStages = 2;
 constexpr int kHalf = kTile * 128;                           // a 64-column block of a tile
@@ -45,8 +47,7 @@ struct Lay {
 static_assert(Lay<128>::kBytes <= 226 * 1024, "shared memory per CTA");
 
 enum { B_KV, B_QLAND, B_QFULL = B_QLAND + kStages, B_QEMPTY = B_QFULL + kStages, B_OLAND = B_QEMPTY + kStages,
-       B_OFULL = B_OLAND + kStages, B_OEMPTY = B_OFULL + kStages, B_S = B_OEMPTY + kStages, B_P, B_DP, B_DS, B_ACCV,
-       B_ACCK, B_COUNT };
+       B_OFULL = B_OLAND + kStages, B_OEMPTY = B_OFULL + kStages, B_S = B_OEMPTY + kStages, B_P, B_DP, B_DS, B_ACC, B_COUNT };
 static_assert(B_COUNT * 8 <= 256, "barrier area");
 
 // Tensor memory columns.
@@ -100,14 +101,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(bar(B_QEMPTY + i), 1);
             tc::mbar_init(bar(B_OLAND + i), 1);
             tc::mbar_init(bar(B_OFULL + i), 32);
-            tc::mbar_init(bar(B_OEMPTY + i), 2);             // dP and dV of the tile
+            tc::mbar_init(bar(B_OEMPTY + i), 1);
         }
         tc::mbar_init(bar(B_S), 1);
         tc::mbar_init(bar(B_P), kCompute);
         tc::mbar_init(bar(B_DP), 1);
         tc::mbar_init(bar(B_DS), kCompute);
-        tc::mbar_init(bar(B_ACCV), 1);
-        tc::mbar_init(bar(B_ACCK), 1);
+        tc::mbar_init(bar(B_ACC), 1);
         tc::fence_barrier_init();
         tc::prefetch_tmap(&tq);
         tc::prefetch_tmap(&to);
@@ -272,89 +272,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 9) {
-            // ---------------- S and dV ------------------------------------
+            // ---------------- products ------------------------------------
             if (lane == 0) {
                 constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
                 constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
-                const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, 16, 1024);
-                const uint64_t dq0 = tc::smem_desc(sbase + L::kOffQ, 16, 1024);
-                const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, kHalf, 1024);
-                int done = -1;                               // tile of this thread's last commit on B_S
-                auto issue_s = [&](int it) {
+                const uint64_t dk = tc::smem_desc(sbase + L::kOffK, 16, 1024), dv = tc::smem_desc(sbase + L::kOffV, 16, 1024);
+                // Q and dO as K-major operands (S, dP) and as MN-major ones (dK, dV)
+                const uint64_t dq_k = tc::smem_desc(sbase + L::kOffQ, 16, 1024), dq_n = tc::smem_desc(sbase + L::kOffQ, kHalf, 1024);
+                const uint64_t do_k = tc::smem_desc(sbase + L::kOffO, 16, 1024), do_n = tc::smem_desc(sbase + L::kOffO, kHalf, 1024);
+                bool out = false;                            // something was issued
+                auto scores = [&](int it, int full, int col, uint64_t da, uint64_t db, int done) {
                     const int st = it & (kStages - 1);
-                    if (!wait(B_QFULL + st, (it / kStages) & 1)) return false;
+                    if (!wait(full + st, (it / kStages) & 1)) return false;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColS, tc::desc_add(dk0, off), tc::desc_add(dq0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss(tmem + col, tc::desc_add(da, off), tc::desc_add(db, st * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(B_S));
-                    done = it;
+                    tc::mma_commit(bar(done));
+                    out = true;
                     return true;
                 };
-                bool ok = wait(B_KV, 0) && issue_s(it0);
-                for (int i = 0; ok && i < nt; ++i) {
-                    const int it = it0 + i, st = it & (kStages - 1);
-                    ok = wait(B_P, it & 1) && wait(B_OFULL + st, (it / kStages) & 1);
-                    if (!ok) break;
+                auto sums = [&](int it, int ready, int col, int from, uint64_t db, bool first, int empty) {
+                    const int st = it & (kStages - 1);
+                    if (!wait(ready, it & 1)) return false;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(tmem + kColV, tmem + kColS + (kk & 3) * 8 + (kk >> 2) * 64,
-                                       tc::desc_add(do0, st * L::kTileBytes + kk * 2048), kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(bar(B_OEMPTY + st));
-                    if (i + 1 < nt) ok = issue_s(it + 1);
-                    else tc::mma_commit(bar(B_ACCV));
+                        tc::mma_f16_ts(tmem + col, tmem + from + (kk & 3) * 8 + (kk >> 2) * 64,
+                                       tc::desc_add(db, st * L::kTileBytes + kk * 2048), kIdescV, (!first || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(bar(empty + st));
+                    return true;
+                };
+                bool ok = wait(B_KV, 0) && scores(it0, B_QFULL, kColS, dk, dq_k, B_S) && scores(it0, B_OFULL, kColP, dv, do_k, B_DP);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int it = it0 + i;
+                    ok = sums(it, B_P, kColV, kColS, do_n, i == 0, B_OEMPTY);
+                    if (ok && i + 1 < nt) ok = scores(it + 1, B_QFULL, kColS, dk, dq_k, B_S);
+                    ok = ok && sums(it, B_DS, kColK, kColP, dq_n, i == 0, B_QEMPTY);
+                    if (ok && i + 1 < nt) ok = scores(it + 1, B_OFULL, kColP, dv, do_k, B_DP);
                 }
-                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0) {
-                    tc::mma_commit(bar(B_ACCV));
-                    tc::mbar_wait(bar(B_ACCV), stretch & 1, nullptr, 100000000ull);
+                if (out) {
+                    tc::mma_commit(bar(B_ACC));
+                    if (!ok) tc::mbar_wait(bar(B_ACC), stretch & 1, nullptr, 100000000ull);   // nothing runs on when the CTA leaves
                 }
             }
         } else if (warp == 10) {
-            // ---------------- dP and dK -----------------------------------
-            if (lane == 0) {
-                constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
-                constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
-                const uint64_t dv0 = tc::smem_desc(sbase + L::kOffV, 16, 1024);
-                const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, 16, 1024);
-                const uint64_t dq0 = tc::smem_desc(sbase + L::kOffQ, kHalf, 1024);
-                int done = -1;
-                auto issue_p = [&](int it) {
-                    const int st = it & (kStages - 1);
-                    if (!wait(B_OFULL + st, (it / kStages) & 1)) return false;
-                    tc::tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColP, tc::desc_add(dv0, off), tc::desc_add(do0, st * L::kTileBytes + off), kIdescS, kk > 0);
-                    }
-                    tc::mma_commit(bar(B_DP));
-                    tc::mma_commit(bar(B_OEMPTY + st));
-                    done = it;
-                    return true;
-                };
-                bool ok = wait(B_KV, 0) && issue_p(it0);
-                for (int i = 0; ok && i < nt; ++i) {
-                    const int it = it0 + i, st = it & (kStages - 1);
-                    ok = wait(B_DS, it & 1) && wait(B_QFULL + st, (it / kStages) & 1);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(tmem + kColK, tmem + kColP + (kk & 3) * 8 + (kk >> 2) * 64,
-                                       tc::desc_add(dq0, st * L::kTileBytes + kk * 2048), kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(bar(B_QEMPTY + st));
-                    if (i + 1 < nt) ok = issue_p(it + 1);
-                    else tc::mma_commit(bar(B_ACCK));
-                }
-                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0) {
-                    tc::mma_commit(bar(B_ACCK));
-                    tc::mbar_wait(bar(B_ACCK), stretch & 1, nullptr, 100000000ull);
-                }
-            }
-        } else if (warp == 11) {
             // ---------------- each tile as it has landed --------------------
             for (int i = 0; i < nt; ++i) {
                 const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
@@ -365,14 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float4 d4 = reinterpret_cast<float4 *>(info + kTile)[lane];
                 const int4 c4 = reinterpret_cast<int4 *>(info + 2 * kTile)[lane];
                 const int4 m4 = reinterpret_cast<int4 *>(info + 3 * kTile)[lane];
-                l4.x += static_cast<float>(cmax - c4.x);
-                l4.y += static_cast<float>(cmax - c4.y);
-                l4.z += static_cast<float>(cmax - c4.z);
-                l4.w += static_cast<float>(cmax - c4.w);
-                d4.x *= sigma;
-                d4.y *= sigma;
-                d4.z *= sigma;
-                d4.w *= sigma;
+                l4.x = -(l4.x + static_cast<float>(cmax - c4.x));
+                l4.y = -(l4.y + static_cast<float>(cmax - c4.y));
+                l4.z = -(l4.z + static_cast<float>(cmax - c4.z));
+                l4.w = -(l4.w + static_cast<float>(cmax - c4.w));
+                d4.x *= -sigma;
+                d4.y *= -sigma;
+                d4.z *= -sigma;
+                d4.w *= -sigma;
                 reinterpret_cast<float4 *>(info)[lane] = l4;
                 reinterpret_cast<float4 *>(info + kTile)[lane] = d4;
                 auto cuts = [&](int m) { return m > 0 && m < j0 + kTile; };
@@ -422,11 +386,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t ph[32];
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4 *>(info + c);
-                        p[c] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][c & 31]), c1, -l4.x));
-                        p[c + 1] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][(c & 31) + 1]), c1, -l4.y));
-                        p[c + 2] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][(c & 31) + 2]), c1, -l4.z));
-                        p[c + 3] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][(c & 31) + 3]), c1, -l4.w));
+                        const float4 l4 = *reinterpret_cast<const float4 *>(info + c);   // -L
+                        const uint32_t *x = &r[c >> 5][c & 31];
+                        const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(c1, c1), make_float2(l4.x, l4.y));
+                        const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(c1, c1), make_float2(l4.z, l4.w));
+                        p[c] = fast_exp2(a.x);
+                        p[c + 1] = fast_exp2(a.y);
+                        p[c + 2] = fast_exp2(b.x);
+                        p[c + 3] = fast_exp2(b.y);
                     }
                     if (need) {
                         const int4 *lim = reinterpret_cast<const int4 *>(info + 3 * kTile);
@@ -457,13 +424,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_wait_ld(r);
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
-                        const float4 d4 = *reinterpret_cast<const float4 *>(info + kTile + 32 * u + c);
-                        const float x0 = p[32 * u + c] * fmaf(__uint_as_float(r[c]), sigma, -d4.x);
-                        const float x1 = p[32 * u + c + 1] * fmaf(__uint_as_float(r[c + 1]), sigma, -d4.y);
-                        const float x2 = p[32 * u + c + 2] * fmaf(__uint_as_float(r[c + 2]), sigma, -d4.z);
-                        const float x3 = p[32 * u + c + 3] * fmaf(__uint_as_float(r[c + 3]), sigma, -d4.w);
-                        dh[16 * u + c / 2] = pack_half2(x0, x1);
-                        dh[16 * u + c / 2 + 1] = pack_half2(x2, x3);
+                        const float4 d4 = *reinterpret_cast<const float4 *>(info + kTile + 32 * u + c);   // -D
+                        const float2 sg = make_float2(sigma, sigma);
+                        const float *pp = &p[32 * u + c];
+                        float2 a = __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sg, make_float2(d4.x, d4.y));
+                        float2 b = __ffma2_rn(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sg, make_float2(d4.z, d4.w));
+                        a = __fmul2_rn(a, make_float2(pp[0], pp[1]));
+                        b = __fmul2_rn(b, make_float2(pp[2], pp[3]));
+                        dh[16 * u + c / 2] = pack_half2(a.x, a.y);
+                        dh[16 * u + c / 2 + 1] = pack_half2(b.x, b.y);
                     }
                 }
                 tc::tmem_st32u(lane_base + kColP + hf * 64, dh);
@@ -473,8 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---------------- sums of this stretch ------------------------------
             bool ok = !*reinterpret_cast<volatile int *>(&s_abort);
-            ok = ok && wait(B_ACCV, stretch & 1);
-            ok = ok && wait(B_ACCK, stretch & 1);
+            ok = ok && wait(B_ACC, stretch & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc::tc_fence_after();

@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kCompute = 256;
-constexpr int kStages = 2;
+constexpr int kK = 3, kV = 2;                               // K and V tiles in shared memory
 constexpr int kHalf = kTile * 128;
 
 template <int D>
@@ -31,14 +31,14 @@ struct Lay {
     static constexpr int kOffQ = 0;
     static constexpr int kOffO = kTileBytes;
     static constexpr int kOffK = 2 * kTileBytes;
-    static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+    static constexpr int kOffV = kOffK + kK * kTileBytes;
+    static constexpr int kOffBar = kOffV + kV * kTileBytes;
     static constexpr int kBytes = kOffBar + 256 + 1024;
 };
-static_assert(Lay<128>::kBytes <= 226 * 1024, "shared memory per CTA");
+static_assert(Lay<128>::kBytes <= 227 * 1024 - 128, "shared memory per CTA");
 
-enum { B_QO, B_KLAND, B_KFULL = B_KLAND + kStages, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
-       B_VEMPTY = B_VFULL + kStages, B_S = B_VEMPTY + kStages, B_DS = B_S + 2, B_DQ = B_DS + 2, B_DP = B_DQ + 2, B_DPFREE,
+enum { B_QO, B_KLAND, B_KFULL = B_KLAND + kK, B_KEMPTY = B_KFULL + kK, B_VFULL = B_KEMPTY + kK,
+       B_VEMPTY = B_VFULL + kV, B_S = B_VEMPTY + kV, B_DS = B_S + 2, B_DQ = B_DS + 2, B_DP = B_DQ + 2, B_DPFREE,
        B_ACC, B_COUNT };
 static_assert(B_COUNT * 8 <= 256, "barrier area");
 
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_ew, s_last;
-    __shared__ uint32_t s_here[kStages][4];                  // keys of a tile that are there
+    __shared__ uint32_t s_here[kK][4];                  // keys of a tile that are there
 
     const Geo &g = a.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -82,10 +82,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == kCompute) {
         tc::mbar_init(bar(B_QO), 1);
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kK; ++i) {
             tc::mbar_init(bar(B_KLAND + i), 1);
             tc::mbar_init(bar(B_KFULL + i), 32);
             tc::mbar_init(bar(B_KEMPTY + i), 1);
+        }
+        for (int i = 0; i < kV; ++i) {
             tc::mbar_init(bar(B_VFULL + i), 1);
             tc::mbar_init(bar(B_VEMPTY + i), 1);
         }
@@ -186,25 +188,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 int k_out = 0, v_out = 0;
                 for (int i = 0; i < nt; ++i) {
-                    const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
+                    const int it = it0 + i, ks = it % kK, vs = it % kV;
                     const int y = (j + i) * kTile;
-                    if (it >= kStages && !wait(B_KEMPTY + st, ph ^ 1)) break;
-                    tc::mbar_expect_tx(bar(B_KLAND + st), L::kTileBytes);
+                    if (it >= kK && !wait(B_KEMPTY + ks, (it / kK - 1) & 1)) break;
+                    tc::mbar_expect_tx(bar(B_KLAND + ks), L::kTileBytes);
                     for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_3d(sbase + L::kOffK + st * L::kTileBytes + b * kHalf, &tk, hk * D + 64 * b, y, group, bar(B_KLAND + st));
+                        tc::tma_load_3d(sbase + L::kOffK + ks * L::kTileBytes + b * kHalf, &tk, hk * D + 64 * b, y, group, bar(B_KLAND + ks));
                     ++k_out;
-                    if (it >= kStages && !wait(B_VEMPTY + st, ph ^ 1)) break;
-                    tc::mbar_expect_tx(bar(B_VFULL + st), L::kTileBytes);
+                    if (it >= kV && !wait(B_VEMPTY + vs, (it / kV - 1) & 1)) break;
+                    tc::mbar_expect_tx(bar(B_VFULL + vs), L::kTileBytes);
                     for (int b = 0; b < D / 64; ++b)
-                        tc::tma_load_3d(sbase + L::kOffV + st * L::kTileBytes + b * kHalf, &tv, hk * D + 64 * b, y, group, bar(B_VFULL + st));
+                        tc::tma_load_3d(sbase + L::kOffV + vs * L::kTileBytes + b * kHalf, &tv, hk * D + 64 * b, y, group, bar(B_VFULL + vs));
                     ++v_out;
                 }
                 if (*reinterpret_cast<volatile int *>(&s_abort)) {
                     tc::mbar_wait(bar(B_QO), 0, nullptr, 100000000ull);
-                    for (int i = max(0, k_out - kStages); i < k_out; ++i)
-                        tc::mbar_wait(bar(B_KLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
-                    for (int i = max(0, v_out - kStages); i < v_out; ++i)
-                        tc::mbar_wait(bar(B_VFULL + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
+                    for (int i = max(0, k_out - kK); i < k_out; ++i)
+                        tc::mbar_wait(bar(B_KLAND + (it0 + i) % kK), ((it0 + i) / kK) & 1, nullptr, 100000000ull);
+                    for (int i = max(0, v_out - kV); i < v_out; ++i)
+                        tc::mbar_wait(bar(B_VFULL + (it0 + i) % kV), ((it0 + i) / kV) & 1, nullptr, 100000000ull);
                 }
             }
         } else if (warp == 9) {
@@ -218,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int done = -1;
                 bool ok = wait(B_QO, 0);
                 for (int i = 0; ok && i < nt; ++i) {
-                    const int it = it0 + i, st = it & (kStages - 1), sb = it & 1;
-                    ok = wait(B_KFULL + st, (it / kStages) & 1);
+                    const int it = it0 + i, ks = it % kK, vs = it % kV, sb = it & 1;
+                    ok = wait(B_KFULL + ks, (it / kK) & 1);
                     // the buffer's last dS has been read
                     ok = ok && (it < 2 || wait(B_DQ + sb, ((it >> 1) - 1) & 1));
                     if (!ok) break;
@@ -227,19 +229,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColS + sb * kTile, tc::desc_add(dq0, off), tc::desc_add(dk0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss(tmem + kColS + sb * kTile, tc::desc_add(dq0, off), tc::desc_add(dk0, ks * L::kTileBytes + off), kIdescS, kk > 0);
                     }
                     tc::mma_commit(bar(B_S + sb));
-                    ok = wait(B_VFULL + st, (it / kStages) & 1) && (it < 1 || wait(B_DPFREE, (it - 1) & 1));
+                    ok = wait(B_VFULL + vs, (it / kV) & 1) && (it < 1 || wait(B_DPFREE, (it - 1) & 1));
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColP, tc::desc_add(do0, off), tc::desc_add(dv0, st * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss(tmem + kColP, tc::desc_add(do0, off), tc::desc_add(dv0, vs * L::kTileBytes + off), kIdescS, kk > 0);
                     }
                     tc::mma_commit(bar(B_DP));
-                    tc::mma_commit(bar(B_VEMPTY + st));
+                    tc::mma_commit(bar(B_VEMPTY + vs));
                     done = it;
                 }
                 if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
@@ -252,14 +254,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, kHalf, 1024);
                 int done = -1;
                 for (int i = 0; i < nt; ++i) {
-                    const int it = it0 + i, st = it & (kStages - 1), sb = it & 1;
-                    if (!wait(B_DS + sb, (it >> 1) & 1) || !wait(B_KFULL + st, (it / kStages) & 1)) break;
+                    const int it = it0 + i, ks = it % kK, sb = it & 1;
+                    if (!wait(B_DS + sb, (it >> 1) & 1) || !wait(B_KFULL + ks, (it / kK) & 1)) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         tc::mma_f16_ts(tmem + kColQ, tmem + kColS + sb * kTile + (kk & 3) * 8 + (kk >> 2) * 64,
-                                       tc::desc_add(dk0, st * L::kTileBytes + kk * 2048), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(bar(B_KEMPTY + st));
+                                       tc::desc_add(dk0, ks * L::kTileBytes + kk * 2048), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(bar(B_KEMPTY + ks));
                     tc::mma_commit(bar(B_DQ + sb));
                     if (i + 1 == nt) tc::mma_commit(bar(B_ACC));
                     done = it;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- each K tile as it has landed -------------------
             const int8_t *ew = a.ew + static_cast<int64_t>(gh) * g.KT * kTile;
             for (int i = 0; i < nt; ++i) {
-                const int it = it0 + i, st = it & (kStages - 1);
+                const int it = it0 + i, st = it % kK;
                 const int jt = (j + i) * kTile;
                 const uint32_t e4 = *reinterpret_cast<const uint32_t *>(ew + jt + 4 * lane);
                 uint32_t w = 0;                              // this lane's four keys
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w |= __shfl_xor_sync(0xffffffffu, w, 1);
                 w |= __shfl_xor_sync(0xffffffffu, w, 2);
                 w |= __shfl_xor_sync(0xffffffffu, w, 4);
-                bool ok = wait(B_KLAND + st, (it / kStages) & 1);
+                bool ok = wait(B_KLAND + st, (it / kK) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 if ((lane & 7) == 0) s_here[st][lane >> 3] = w;
                 if (jt + kTile > lim_tile) {                 // rows that no token of the tile sees
@@ -299,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             const float c1 = a.scale * 1.4426950408889634f;
             for (int i = 0; i < nt; ++i) {
-                const int it = it0 + i, st = it & (kStages - 1), sb = it & 1;
+                const int it = it0 + i, st = it % kK, sb = it & 1;
                 const uint32_t cs = lane_base + kColS + sb * kTile + hf * 64;
-                bool ok = wait(B_KFULL + st, (it / kStages) & 1);
+                bool ok = wait(B_KFULL + st, (it / kK) & 1);
                 const uint32_t h0 = s_here[st][hf * 2], h1 = s_here[st][hf * 2 + 1];
                 const int left = lim - (j + i) * kTile - hf * 64;        // columns of this half that the row sees
                 ok = ok && wait(B_S + sb, (it >> 1) & 1);
@@ -315,7 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_wait_ld(r[0]);
                     tc::tmem_wait_ld(r[1]);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) p[c] = fast_exp2(fmaf(__uint_as_float(r[c >> 5][c & 31]), c1, -row_L));
+                    for (int c = 0; c < 64; c += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c >> 5][c & 31]), __uint_as_float(r[c >> 5][(c & 31) + 1])),
+                                                    make_float2(c1, c1), make_float2(-row_L, -row_L));
+                        p[c] = fast_exp2(x.x);
+                        p[c + 1] = fast_exp2(x.y);
+                    }
                 }
                 ok = wait(B_DP, it & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -328,7 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tc_fence_before();
                 tc::mbar_arrive(bar(B_DPFREE));
 #pragma unroll
-                for (int c = 0; c < 64; ++c) p[c] *= fmaf(__uint_as_float(r[c >> 5][c & 31]), sigma, -row_D);
+                for (int c = 0; c < 64; c += 2) {
+                    float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c >> 5][c & 31]), __uint_as_float(r[c >> 5][(c & 31) + 1])),
+                                          make_float2(sigma, sigma), make_float2(-row_D, -row_D));
+                    x = __fmul2_rn(x, make_float2(p[c], p[c + 1]));
+                    p[c] = x.x;
+                    p[c + 1] = x.y;
+                }
                 if (__any_sync(0xffffffffu, left < 64 || (h0 & h1) != 0xffffffffu)) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
