@@ -366,49 +366,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // ---------------- P and dS --------------------------------------
+            // A thread holds, of each eight columns (rows of the tile) of its half, two columns of four keys: L and D
+            // then come in 16 loads of two values, of which a warp's threads read four different ones.  (A key a
+            // thread, each of its 64 columns' values read by the whole warp, took 1370 clocks of shared memory's time
+            // for a tile, beside the products' 2050.)
             const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            const float c1 = a.scale * 1.4426950408889634f;
+            const float2 c1 = make_float2(a.scale * 1.4426950408889634f, a.scale * 1.4426950408889634f);
+            const float2 sg = make_float2(sigma, sigma);
+            const int64_t key4 = j0 + (warp & 3) * 32 + (lane >> 2);      // its first key; the others 8, 16, 24 on
             for (int i = 0; i < nt; ++i) {
                 const int it = it0 + i, st = it & (kStages - 1);
-                const float *info = reinterpret_cast<const float *>(sm + L::kOffInfo + st * kInfoBytes) + hf * 64;
+                const float *info = reinterpret_cast<const float *>(sm + L::kOffInfo + st * kInfoBytes) + hf * 64 + 2 * (lane & 3);
                 bool ok = wait(B_QFULL + st, (it / kStages) & 1);
                 ok = ok && wait(B_S, it & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
                 const bool need = s_need[st] != 0;
-                float p[64];
+                float p[64];                                 // [16 lanes][group of 8 columns][key, key + 8][two columns]
                 {
                     uint32_t r[2][32];
-                    tc::tmem_ld32(lane_base + kColS + hf * 64, r[0]);
-                    tc::tmem_ld32(lane_base + kColS + hf * 64 + 32, r[1]);
+                    tc::tmem_ld16x64(lane_base + kColS + hf * 64, r[0]);
+                    tc::tmem_ld16x64(lane_base + (16u << 16) + kColS + hf * 64, r[1]);
                     tc::tmem_wait_ld(r[0]);
                     tc::tmem_wait_ld(r[1]);
-                    uint32_t ph[32];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4 *>(info + c);   // -L
-                        const uint32_t *x = &r[c >> 5][c & 31];
-                        const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(c1, c1), make_float2(l4.x, l4.y));
-                        const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(c1, c1), make_float2(l4.z, l4.w));
-                        p[c] = fast_exp2(a.x);
-                        p[c + 1] = fast_exp2(a.y);
-                        p[c + 2] = fast_exp2(b.x);
-                        p[c + 3] = fast_exp2(b.y);
+                    for (int g8 = 0; g8 < 8; ++g8) {
+                        const float2 l2 = *reinterpret_cast<const float2 *>(info + 8 * g8);   // -L
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const uint32_t *x = &r[u >> 1][4 * g8 + 2 * (u & 1)];
+                            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c1, l2);
+                            float *pp = &p[(u >> 1) * 32 + 4 * g8 + 2 * (u & 1)];
+                            pp[0] = fast_exp2(e.x);
+                            pp[1] = fast_exp2(e.y);
+                        }
                     }
                     if (need) {
-                        const int4 *lim = reinterpret_cast<const int4 *>(info + 3 * kTile);
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            const int4 m = lim[c >> 2];
-                            if (key >= m.x) p[c] = 0.f;
-                            if (key >= m.y) p[c + 1] = 0.f;
-                            if (key >= m.z) p[c + 2] = 0.f;
-                            if (key >= m.w) p[c + 3] = 0.f;
+                        for (int g8 = 0; g8 < 8; ++g8) {
+                            const int2 m = *reinterpret_cast<const int2 *>(info + 3 * kTile + 8 * g8);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                float *pp = &p[(u >> 1) * 32 + 4 * g8 + 2 * (u & 1)];
+                                if (key4 + 8 * u >= m.x) pp[0] = 0.f;
+                                if (key4 + 8 * u >= m.y) pp[1] = 0.f;
+                            }
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) ph[c] = pack_half2(p[2 * c], p[2 * c + 1]);
-                    tc::tmem_st32u(lane_base + kColS + hf * 64, ph);
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t ph[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) ph[c] = pack_half2(p[32 * u + 2 * c], p[32 * u + 2 * c + 1]);
+                        tc::tmem_st16x32(lane_base + (static_cast<uint32_t>(16 * u) << 16) + kColS + hf * 64, ph);
+                    }
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
@@ -416,26 +427,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(B_DP, it & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
-                uint32_t dh[32];
+                float2 d2[8];                                // -D
+#pragma unroll
+                for (int g8 = 0; g8 < 8; ++g8) d2[g8] = *reinterpret_cast<const float2 *>(info + kTile + 8 * g8);
+                uint32_t dh[2][16];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t r[32];
-                    tc::tmem_ld32(lane_base + kColP + hf * 64 + 32 * u, r);
+                    tc::tmem_ld16x64(lane_base + (static_cast<uint32_t>(16 * u) << 16) + kColP + hf * 64, r);
                     tc::tmem_wait_ld(r);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 d4 = *reinterpret_cast<const float4 *>(info + kTile + 32 * u + c);   // -D
-                        const float2 sg = make_float2(sigma, sigma);
-                        const float *pp = &p[32 * u + c];
-                        float2 a = __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sg, make_float2(d4.x, d4.y));
-                        float2 b = __ffma2_rn(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sg, make_float2(d4.z, d4.w));
-                        a = __fmul2_rn(a, make_float2(pp[0], pp[1]));
-                        b = __fmul2_rn(b, make_float2(pp[2], pp[3]));
-                        dh[16 * u + c / 2] = pack_half2(a.x, a.y);
-                        dh[16 * u + c / 2 + 1] = pack_half2(b.x, b.y);
+                    for (int c = 0; c < 16; ++c) {           // group c / 2, key + 8 (c % 2)
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sg, d2[c >> 1]);
+                        x = __fmul2_rn(x, make_float2(p[32 * u + 2 * c], p[32 * u + 2 * c + 1]));
+                        dh[u][c] = pack_half2(x.x, x.y);
                     }
                 }
-                tc::tmem_st32u(lane_base + kColP + hf * 64, dh);
+                tc::tmem_st16x32(lane_base + kColP + hf * 64, dh[0]);
+                tc::tmem_st16x32(lane_base + (16u << 16) + kColP + hf * 64, dh[1]);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 tc::mbar_arrive(bar(B_DS));
