@@ -3,9 +3,9 @@
 // With p = exp(scale q.k - lse), delta = d_o.o - d_lse and ds = p (d_o.v - delta),
 //   dv = sum_q p d_o,  dk = scale sum_q ds q,  dq = scale sum_k ds k.
 //
-// Three launches: prepare (row statistics; gathered rows of lists), dk and dv (a CTA
-// owns 128 keys of a KV head and walks over the query tiles that see one of them),
-// dq (a CTA owns a query tile and walks over its keys).  S and d_o.v are
+// Two launches: prepare (row statistics; gathered rows of lists), and one of CTAs for
+// dk and dv (each owns 128 keys of a KV head and walks over the query tiles that see one of
+// them) and of CTAs for dq (each owns a query tile and walks over its keys).  S and d_o.v are
 // computed in both: 7 products instead of 5, but no sum of dq crosses CTAs.
 // Adding it up in memory instead would move 4 bytes for every key tile, query row and
 // channel, 64 KB for each 128 x 128 tile that takes about 1.3 us: 7.5 TB/s of
@@ -32,6 +32,8 @@ namespace skv {
 namespace bwd {
 
 constexpr int kTile = 128;               // rows of a query tile, keys of a key tile
+constexpr int kThreads = 384;            // of the gradient kernels: eight compute warps and four others
+constexpr int kCompute = 256;
 constexpr int kPShift = 15;              // p' = 2^15 p
 // Tiles after which an accumulator is added to fp32 memory.  The tensor core cuts its
 // sums off instead of rounding them, and loses about 2^-24 of a sum's size for
@@ -192,10 +194,9 @@ __device__ __forceinline__ void add_row(const float *p, float (&v)[NC])
 int launch_prep(skv_handle *h, const PrepArgs &a, int do_type, cudaStream_t st);
 int launch_join(skv_handle *h, const float *slot, int pieces, int64_t n, int outs, int g_type, void *out0, void *out1,
                 cudaStream_t st);
-int launch_kv(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-              const MainArgs &a, cudaStream_t st);
-int launch_q(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-             const MainArgs &a, cudaStream_t st);
+// One launch of both: kv_args.out0 or q_args.out0 NULL leaves a part out.
+int launch_main(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
+                const MainArgs &kv_args, const MainArgs &q_args, cudaStream_t st);
 
 }  // namespace bwd
 }  // namespace skv

@@ -12,9 +12,32 @@ namespace bwd {
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Fixed cost of a CTA of the two kernels, in tiles of 128 x 128 (about 1.2 us each): tensor
+// Fixed cost of a CTA, in tiles of 128 x 128 (1.8 us for dk and dv, 1.2 for dq): tensor
 // memory, barriers, row statistics, pipeline fill, result.
 constexpr int kOverheadTiles = 4;
+
+// Pieces of a unit's `tiles` tiles.  Units that all take them run in whole waves of SMs; under
+// positions (`some`) they may take half of them on average, first the ones that take most, and only
+// the largest one and the sum count: the mean of both costs decides.  Pieces are added up by a
+// further launch: a few us, and `unit_bytes` of each unit once more for each piece (1 MB takes about a
+// tenth of a tile's time over all SMs).
+static int pieces_of(int64_t tiles, int64_t units, int sms, bool some, int64_t unit_bytes)
+{
+    double best = 0;
+    int pieces = 1;
+    for (int64_t p = 1; p <= std::min<int64_t>(tiles, 64) && units * (p - 1) < 8 * static_cast<int64_t>(sms); ++p) {
+        const double per = static_cast<double>((tiles + p - 1) / p + kOverheadTiles);
+        const double waves = static_cast<double>((units * p + sms - 1) / sms) * per;
+        const double share = std::max(per, units * (0.5 * tiles + p * kOverheadTiles) / sms);
+        double cost = some ? 0.5 * (waves + share) : waves;
+        if (p > 1) cost += 2 + 1e-7 * static_cast<double>(unit_bytes) * units * (p + 0.5);
+        if (p == 1 || cost < best) {
+            best = cost;
+            pieces = static_cast<int>(p);
+        }
+    }
+    return pieces;
+}
 
 // Tokens x heads of a query tile: the fewest tiles, then the fewest heads (a tile of
 // one head has consecutive tokens, which see about the same keys).
@@ -143,13 +166,8 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
         return SKV_OK;
     }
     // Pieces of a unit's tiles for grids that would leave SMs idle.
-    int64_t len = 0;
-    int32_t kv_pieces = 1, q_pieces = 1;
-    if (dk && (rc = plan_splits_cost(static_cast<int64_t>(g.QT) * kTile, units * g.KT, h->sm_count, 1, kTile, 0, kOverheadTiles, &len, &kv_pieces)))
-        return fail(h, rc, "piece planning failed");
-    if (dq && (rc = plan_splits_cost(g.n, units * g.QT, h->sm_count, 1, kTile, 0, kOverheadTiles, &len, &q_pieces)))
-        return fail(h, rc, "piece planning failed");
-    if (kv_pieces > 65535 || q_pieces > 65535) return fail(h, SKV_EUNSUPPORTED, "too many pieces");
+    const int kv_pieces = dk ? pieces_of(g.QT, units * g.KT, h->sm_count, q_pos != nullptr, 2 * kTile * g.D * 4) : 1;
+    const int q_pieces = dq ? pieces_of(g.KT, units * g.QT, h->sm_count, q_pos != nullptr, kTile * g.D * 4) : 1;
     const bool kv_slot = dk && (kv_pieces > 1 || g.QT > kStretch), q_slot = dq && (q_pieces > 1 || g.KT > kStretch);
 
     // Scratch: row statistics, tile sums, exponents of the keys, rows gathered or converted, fp32 sums.
@@ -210,21 +228,16 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
     a.ew = p.ew;
     a.g_type = g_type;
     a.status = h->status;
-    if (dk) {
-        a.pieces = kv_pieces;
-        a.slot = kv_slot ? reinterpret_cast<float *>(ws + at_kv) : nullptr;
-        a.out0 = dk;
-        a.out1 = dv;
-        if ((rc = launch_kv(h, mq, mo, mk, mv, a, st))) return rc;
-        if (kv_pieces > 1 && (rc = launch_join(h, a.slot, kv_pieces, k_vals, 2, g_type, dk, dv, st))) return rc;
-    }
-    if (dq) {
-        a.pieces = q_pieces;
-        a.slot = q_slot ? reinterpret_cast<float *>(ws + at_q) : nullptr;
-        a.out0 = dq;
-        a.out1 = nullptr;
-        if ((rc = launch_q(h, mq, mo, mk, mv, a, st))) return rc;
-        if (q_pieces > 1 && (rc = launch_join(h, a.slot, q_pieces, q_vals, 1, g_type, dq, nullptr, st))) return rc;
-    }
+    MainArgs b = a;
+    a.pieces = kv_pieces;
+    a.slot = kv_slot ? reinterpret_cast<float *>(ws + at_kv) : nullptr;
+    a.out0 = dk;
+    a.out1 = dv;
+    b.pieces = q_pieces;
+    b.slot = q_slot ? reinterpret_cast<float *>(ws + at_q) : nullptr;
+    b.out0 = dq;
+    if ((rc = launch_main(h, mq, mo, mk, mv, a, b, st))) return rc;
+    if (kv_pieces > 1 && (rc = launch_join(h, a.slot, kv_pieces, k_vals, 2, g_type, dk, dv, st))) return rc;
+    if (q_pieces > 1 && (rc = launch_join(h, b.slot, q_pieces, q_vals, 1, g_type, dq, nullptr, st))) return rc;
     return SKV_OK;
 }

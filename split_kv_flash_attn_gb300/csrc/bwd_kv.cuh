@@ -1,4 +1,4 @@
-// bwd_kv.cu -- dk and dv: a CTA owns 128 keys of a KV head (TMEM lanes) and walks over
+// bwd_kv.cuh -- dk and dv: a CTA owns 128 keys of a KV head (TMEM lanes) and walks over
 // the query tiles that see one of them.
 //
 //   S^T  = K Q^T        [128 keys x 128 rows]   dP^T = V dO^T
@@ -10,25 +10,24 @@
 // from one to the other: while the compute warps form P(j) it runs dK(j-1), dP(j), and
 // while they form dS(j) it runs dV(j), S(j+1).
 //
-// Warps: 0-7 compute (two threads a key, 64 rows of the tile each), 8 TMA, 9 issues the
-// products in the order dV(j), S(j+1), dK(j), dP(j+1) (one thread: they run in order, so the
-// buffers need no further wait, and S(j+1), which the compute warps wait for, never
-// stands behind dP; a thread each for dV, S and dK, dP measured 15 % slower),
-// 10 looks each tile over when it has landed: it folds the powers of two
+// Warps: 0-7 compute (two threads a key, 64 rows of the tile each), 8 TMA, 9 issues dV(j) and
+// S(j+1), 10 dK(j) and dP(j+1), in turns, so that S(j+1), which the compute warps wait
+// for, does not stand behind dP; a thread's products run in order, so that their buffers
+// need no further wait.  The turn passes before a thread's last two products go out, and
+// its waits for operands fall into the other's turn.  (16384 tokens of 8 heads: no turns
+// 937 us, one thread for all four 867.)  11 looks each tile over when it has landed: it folds the powers of two
 // into -L and -D, tells whether the tile needs a mask, and clears rows of
 // tokens that see nothing, whatever they hold.
 //
 // Every mbarrier wait is bounded, as in the prefill kernel.
-#include <string.h>
+#pragma once
 
 #include "bwd.cuh"
 
 namespace skv {
 namespace bwd {
-namespace {
+namespace kv {
 
-constexpr int kThreads = 352;
-constexpr int kCompute = 256;
 constexpr int kStages = 2;
 constexpr int kHalf = kTile * 128;                           // a 64-column block of a tile
 
@@ -47,20 +46,19 @@ struct Lay {
 static_assert(Lay<128>::kBytes <= 226 * 1024, "shared memory per CTA");
 
 enum { B_KV, B_QLAND, B_QFULL = B_QLAND + kStages, B_QEMPTY = B_QFULL + kStages, B_OLAND = B_QEMPTY + kStages,
-       B_OFULL = B_OLAND + kStages, B_OEMPTY = B_OFULL + kStages, B_S = B_OEMPTY + kStages, B_P, B_DP, B_DS, B_ACC, B_COUNT };
+       B_OFULL = B_OLAND + kStages, B_OEMPTY = B_OFULL + kStages, B_S = B_OEMPTY + kStages, B_P, B_DP, B_DS, B_TURN,
+       B_ACC = B_TURN + 2, B_COUNT = B_ACC + 2 };
 static_assert(B_COUNT * 8 <= 256, "barrier area");
 
 // Tensor memory columns.
 constexpr int kColS = 0, kColP = 128, kColV = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    splitkv_bwd_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
-                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const MainArgs a)
+__device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to, const CUtensorMap &tk, const CUtensorMap &tv,
+                                    const MainArgs &a, int unit, int piece, uint8_t *smem_raw)
 {
     using L = Lay<D>;
     constexpr int kColK = kColV + D;
-    extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(sm);
     auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
@@ -74,9 +72,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // key tile slowest: under causal positions the first keys have the most rows
     const int heads = g.Hk * g.groups;
-    const int kt = blockIdx.x / heads, gh = blockIdx.x - kt * heads;
+    const int kt = unit / heads, gh = unit - kt * heads;
     const int group = gh / g.Hk, hk = gh - group * g.Hk;
-    const int piece = blockIdx.y;
     const int64_t j0 = static_cast<int64_t>(kt) * kTile;
     const int64_t tile0 = static_cast<int64_t>(gh) * g.QT;
     const int box_rows = g.Gb * g.Tb;
@@ -101,17 +98,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(bar(B_QEMPTY + i), 1);
             tc::mbar_init(bar(B_OLAND + i), 1);
             tc::mbar_init(bar(B_OFULL + i), 32);
-            tc::mbar_init(bar(B_OEMPTY + i), 1);
+            tc::mbar_init(bar(B_OEMPTY + i), 2);             // dP and dV of the tile
         }
         tc::mbar_init(bar(B_S), 1);
         tc::mbar_init(bar(B_P), kCompute);
         tc::mbar_init(bar(B_DP), 1);
         tc::mbar_init(bar(B_DS), kCompute);
-        tc::mbar_init(bar(B_ACC), 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(B_TURN + i), 1);
+            tc::mbar_init(bar(B_ACC + i), 1);
+        }
         tc::fence_barrier_init();
+        // the keys' tiles, while the query tiles are looked through
+        tc::mbar_expect_tx(bar(B_KV), 2 * L::kTileBytes);
+        for (int b = 0; b < D / 64; ++b) {
+            tc::tma_load_3d(sbase + L::kOffK + b * kHalf, &tk, hk * D + 64 * b, static_cast<int>(j0), group, bar(B_KV));
+            tc::tma_load_3d(sbase + L::kOffV + b * kHalf, &tv, hk * D + 64 * b, static_cast<int>(j0), group, bar(B_KV));
+        }
         tc::prefetch_tmap(&tq);
         tc::prefetch_tmap(&to);
     }
+    const int key_lane = (warp & 3) * 32 + lane;             // compute threads: their key
+    const int64_t key = j0 + key_lane;
+    const int key_exp = warp < 8 ? a.ew[(static_cast<int64_t>(gh) * g.KT + kt) * kTile + key_lane] : kAbsent;
     __syncthreads();
     // ---- the query tiles that see one of these keys, and their sizes ----
     {
@@ -156,14 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int key_lane = (warp & 3) * 32 + lane;             // compute threads: their key
-    const int64_t key = j0 + key_lane;
-    bool there = false;
-    if (warp < 8) {
-        const int e = a.ew[(static_cast<int64_t>(gh) * g.KT + kt) * kTile + key_lane];
-        there = key < min(g.n, static_cast<int64_t>(s_lim)) && e != kAbsent;
-        if (there && warp < 4) atomicMax(&s_ew, e);
-    }
+    const bool there = key < min(g.n, static_cast<int64_t>(s_lim)) && key_exp != kAbsent;
+    if (there && warp < 4) atomicMax(&s_ew, key_exp);
     const int any = __syncthreads_or(there);
     const int cmax = s_c > -1000 ? s_c : 0;
     // 2^E bounds |d_o.v - delta| of these rows and keys
@@ -190,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *slot_v = a.slot ? a.slot + (static_cast<int64_t>(piece) * 2 + 1) * out_all + out_at : nullptr;
     float *slot_k = a.slot ? a.slot + static_cast<int64_t>(piece) * 2 * out_all + out_at : nullptr;
 
+    if (o_lo >= o_hi && tid == kCompute) wait(B_KV, 0);      // the loads land before the CTA leaves
     if (o_lo >= o_hi && warp < 8 && key < g.n) {             // nobody sees these keys
         float z[NC];
 #pragma unroll
@@ -234,13 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 8) {
             // ---------------- TMA ----------------------------------------
             if (lane == 0) {
-                if (stretch == 0) {
-                    tc::mbar_expect_tx(bar(B_KV), 2 * L::kTileBytes);
-                    for (int b = 0; b < D / 64; ++b) {
-                        tc::tma_load_3d(sbase + L::kOffK + b * kHalf, &tk, hk * D + 64 * b, static_cast<int>(j0), group, bar(B_KV));
-                        tc::tma_load_3d(sbase + L::kOffV + b * kHalf, &tv, hk * D + 64 * b, static_cast<int>(j0), group, bar(B_KV));
-                    }
-                }
                 const uint32_t box = static_cast<uint32_t>(box_rows) * D * 2;
                 int q_out = 0, o_out = 0;                    // loads issued in this stretch
                 for (int i = 0; i < nt; ++i) {
@@ -271,54 +268,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::mbar_wait(bar(B_OLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
                 }
             }
-        } else if (warp == 9) {
-            // ---------------- products ------------------------------------
+        } else if (warp == 9 || warp == 10) {
+            // ---------------- products: dV(j), S(j+1), and dK(j), dP(j+1) ----
             if (lane == 0) {
+                const bool second = warp == 10;
                 constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
                 constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
-                const uint64_t dk = tc::smem_desc(sbase + L::kOffK, 16, 1024), dv = tc::smem_desc(sbase + L::kOffV, 16, 1024);
-                // Q and dO as K-major operands (S, dP) and as MN-major ones (dK, dV)
-                const uint64_t dq_k = tc::smem_desc(sbase + L::kOffQ, 16, 1024), dq_n = tc::smem_desc(sbase + L::kOffQ, kHalf, 1024);
-                const uint64_t do_k = tc::smem_desc(sbase + L::kOffO, 16, 1024), do_n = tc::smem_desc(sbase + L::kOffO, kHalf, 1024);
+                // S = K Q^T or dP = V dO^T (both operands K-major); dV = P^T dO or dK = dS^T Q (B MN-major)
+                const uint64_t da = tc::smem_desc(sbase + (second ? L::kOffV : L::kOffK), 16, 1024);
+                const uint64_t db = tc::smem_desc(sbase + (second ? L::kOffO : L::kOffQ), 16, 1024);
+                const uint64_t dn = tc::smem_desc(sbase + (second ? L::kOffQ : L::kOffO), kHalf, 1024);
+                const uint32_t col = tmem + (second ? kColP : kColS), acc = tmem + (second ? kColK : kColV);
+                const int b_in = second ? B_OFULL : B_QFULL, b_in2 = second ? B_QFULL : B_OFULL;
+                const int b_out = second ? B_DP : B_S, b_ready = second ? B_DS : B_P;
+                const int b_mine = second ? B_TURN : B_TURN + 1, b_other = second ? B_TURN + 1 : B_TURN;
                 bool out = false;                            // something was issued
-                auto scores = [&](int it, int full, int col, uint64_t da, uint64_t db, int done) {
+                auto scores = [&](int it, bool pass) {
                     const int st = it & (kStages - 1);
-                    if (!wait(full + st, (it / kStages) & 1)) return false;
+                    if (!wait(b_in + st, (it / kStages) & 1)) return false;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + col, tc::desc_add(da, off), tc::desc_add(db, st * L::kTileBytes + off), kIdescS, kk > 0);
+                        if (pass && kk == D / 16 - 2) tc::mbar_arrive(bar(b_other));   // ahead of the end of its wait
+                        tc::mma_f16_ss(col, tc::desc_add(da, off), tc::desc_add(db, st * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(done));
+                    tc::mma_commit(bar(b_out));
+                    if (second) tc::mma_commit(bar(B_OEMPTY + st));
                     out = true;
                     return true;
                 };
-                auto sums = [&](int it, int ready, int col, int from, uint64_t db, bool first, int empty) {
-                    const int st = it & (kStages - 1);
-                    if (!wait(ready, it & 1)) return false;
+                bool ok = wait(B_KV, 0) && scores(it0, second);   // (the first dV goes first)
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int it = it0 + i, st = it & (kStages - 1);
+                    ok = wait(b_ready, it & 1) && wait(b_in2 + st, (it / kStages) & 1) && wait(b_mine, it & 1);
+                    if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(tmem + col, tmem + from + (kk & 3) * 8 + (kk >> 2) * 64,
-                                       tc::desc_add(db, st * L::kTileBytes + kk * 2048), kIdescV, (!first || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(bar(empty + st));
-                    return true;
-                };
-                bool ok = wait(B_KV, 0) && scores(it0, B_QFULL, kColS, dk, dq_k, B_S) && scores(it0, B_OFULL, kColP, dv, do_k, B_DP);
-                for (int i = 0; ok && i < nt; ++i) {
-                    const int it = it0 + i;
-                    ok = sums(it, B_P, kColV, kColS, do_n, i == 0, B_OEMPTY);
-                    if (ok && i + 1 < nt) ok = scores(it + 1, B_QFULL, kColS, dk, dq_k, B_S);
-                    ok = ok && sums(it, B_DS, kColK, kColP, dq_n, i == 0, B_QEMPTY);
-                    if (ok && i + 1 < nt) ok = scores(it + 1, B_OFULL, kColP, dv, do_k, B_DP);
+                        tc::mma_f16_ts(acc, col + (kk & 3) * 8 + (kk >> 2) * 64, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
+                                       kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(bar((second ? B_QEMPTY : B_OEMPTY) + st));
+                    if (i + 1 < nt) ok = scores(it + 1, true);
+                    else if (!second) tc::mbar_arrive(bar(b_other));
                 }
                 if (out) {
-                    tc::mma_commit(bar(B_ACC));
-                    if (!ok) tc::mbar_wait(bar(B_ACC), stretch & 1, nullptr, 100000000ull);   // nothing runs on when the CTA leaves
+                    const int b_acc = second ? B_ACC + 1 : B_ACC;
+                    tc::mma_commit(bar(b_acc));
+                    if (!ok) tc::mbar_wait(bar(b_acc), stretch & 1, nullptr, 100000000ull);   // nothing runs on when the CTA leaves
                 }
             }
-        } else if (warp == 10) {
+        } else if (warp == 11) {
             // ---------------- each tile as it has landed --------------------
             for (int i = 0; i < nt; ++i) {
                 const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- sums of this stretch ------------------------------
             bool ok = !*reinterpret_cast<volatile int *>(&s_abort);
             ok = ok && wait(B_ACC, stretch & 1);
+            ok = ok && wait(B_ACC + 1, stretch & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc::tc_fence_after();
@@ -491,32 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
-KernelAttrCache &attr_cache()
-{
-    static KernelAttrCache c;
-    return c;
-}
-
-template <int D>
-int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-             const MainArgs &a, cudaStream_t st)
-{
-    cudaError_t e = kernel_smem_optin(attr_cache<D>(), reinterpret_cast<const void *>(splitkv_bwd_kv_kernel<D>), Lay<D>::kBytes,
-                                      kThreads, nullptr);
-    if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(dk/dv)");
-    const dim3 grid(static_cast<unsigned>(a.g.KT * a.g.Hk * a.g.groups), static_cast<unsigned>(a.pieces));
-    splitkv_bwd_kv_kernel<D><<<grid, kThreads, Lay<D>::kBytes, st>>>(mq, mo, mk, mv, a);
-    return cuda_fail(h, cudaGetLastError(), "dk/dv kernel launch");
-}
-
-}  // namespace
-
-int launch_kv(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-              const MainArgs &a, cudaStream_t st)
-{
-    return a.g.D == 64 ? launch_t<64>(h, mq, mo, mk, mv, a, st) : launch_t<128>(h, mq, mo, mk, mv, a, st);
-}
-
+}  // namespace kv
 }  // namespace bwd
 }  // namespace skv

@@ -1,4 +1,4 @@
-// bwd_q.cu -- dq: a CTA owns a query tile (TMEM lanes) and walks over the key tiles that it
+// bwd_q.cuh -- dq: a CTA owns a query tile (TMEM lanes) and walks over the key tiles that it
 // sees.
 //
 //   S = Q K^T   dP = dO V^T   [128 rows x 128 keys]
@@ -12,16 +12,14 @@
 // and limit are registers), 8 TMA, 9 issues S and dP, 10 issues dQ, 11 looks each K tile
 // over: absent keys of lists, and rows behind the last key that any row sees, which
 // hold anything, are cleared.
-#include <string.h>
+#pragma once
 
 #include "bwd.cuh"
 
 namespace skv {
 namespace bwd {
-namespace {
+namespace q {
 
-constexpr int kThreads = 384;
-constexpr int kCompute = 256;
 constexpr int kK = 3, kV = 2;                               // K and V tiles in shared memory
 constexpr int kHalf = kTile * 128;
 
@@ -45,12 +43,10 @@ static_assert(B_COUNT * 8 <= 256, "barrier area");
 constexpr int kColS = 0, kColP = 256, kColQ = 384;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    splitkv_bwd_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
-                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const MainArgs a)
+__device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to, const CUtensorMap &tk, const CUtensorMap &tv,
+                                    const MainArgs &a, int unit, int piece, uint8_t *smem_raw)
 {
     using L = Lay<D>;
-    extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(sm);
     auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
@@ -62,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // the last tokens first: under causal positions they see the most keys
     const int heads = g.Hk * g.groups * g.GG;
-    const int ti = g.TT - 1 - blockIdx.x / heads, rest = blockIdx.x % heads;
+    const int ti = g.TT - 1 - unit / heads, rest = unit % heads;
     const int gi = rest % g.GG, gh = rest / g.GG;
     const int group = gh / g.Hk, hk = gh - group * g.Hk;
     const int qt = gi * g.TT + ti;
@@ -100,6 +96,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_init(bar(B_DPFREE), kCompute);
         tc::mbar_init(bar(B_ACC), 1);
         tc::fence_barrier_init();
+        // the rows, while the keys' exponents are looked through
+        tc::mbar_expect_tx(bar(B_QO), 2u * box_rows * D * 2);
+        for (int b = 0; b < D / 64; ++b) {
+            tc::tma_load_5d(sbase + L::kOffQ + b * kHalf, &tq, 64 * b, t.g0, hk, static_cast<int>(t.t0), group, bar(B_QO));
+            tc::tma_load_5d(sbase + L::kOffO + b * kHalf, &to, 64 * b, t.g0, hk, static_cast<int>(t.t0), group, bar(B_QO));
+        }
         tc::prefetch_tmap(&tk);
         tc::prefetch_tmap(&tv);
     }
@@ -132,8 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int n_all = (s_last + kTile) / kTile;              // key tiles up to the last key
-    const int j_lo = static_cast<int>(static_cast<int64_t>(n_all) * blockIdx.y / a.pieces);
-    const int j_hi = static_cast<int>(static_cast<int64_t>(n_all) * (blockIdx.y + 1) / a.pieces);
+    const int j_lo = static_cast<int>(static_cast<int64_t>(n_all) * piece / a.pieces);
+    const int j_hi = static_cast<int>(static_cast<int64_t>(n_all) * (piece + 1) / a.pieces);
 
     auto wait = [&](int b, uint32_t parity) -> bool {
         if (tc::mbar_try_wait(bar(b), parity)) return true;
@@ -163,8 +165,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int64_t out_all = static_cast<int64_t>(g.groups) * g.T * g.H * D;
     const int64_t out_at = row * D + hf * NC;
-    float *slot = a.slot ? a.slot + static_cast<int64_t>(blockIdx.y) * out_all + out_at : nullptr;
+    float *slot = a.slot ? a.slot + static_cast<int64_t>(piece) * out_all + out_at : nullptr;
 
+    if (j_lo >= j_hi && tid == kCompute) wait(B_QO, 0);      // the loads land before the CTA leaves
     if (j_lo >= j_hi && row >= 0) {                          // no keys
         float z[NC];
 #pragma unroll
@@ -179,13 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 8) {
             // ---------------- TMA ----------------------------------------
             if (lane == 0) {
-                if (stretch == 0) {
-                    tc::mbar_expect_tx(bar(B_QO), 2u * box_rows * D * 2);
-                    for (int b = 0; b < D / 64; ++b) {
-                        tc::tma_load_5d(sbase + L::kOffQ + b * kHalf, &tq, 64 * b, t.g0, hk, static_cast<int>(t.t0), group, bar(B_QO));
-                        tc::tma_load_5d(sbase + L::kOffO + b * kHalf, &to, 64 * b, t.g0, hk, static_cast<int>(t.t0), group, bar(B_QO));
-                    }
-                }
                 int k_out = 0, v_out = 0;
                 for (int i = 0; i < nt; ++i) {
                     const int it = it0 + i, ks = it % kK, vs = it % kV;
@@ -393,32 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
-KernelAttrCache &attr_cache()
-{
-    static KernelAttrCache c;
-    return c;
-}
-
-template <int D>
-int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-             const MainArgs &a, cudaStream_t st)
-{
-    cudaError_t e = kernel_smem_optin(attr_cache<D>(), reinterpret_cast<const void *>(splitkv_bwd_q_kernel<D>), Lay<D>::kBytes,
-                                      kThreads, nullptr);
-    if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(dq)");
-    const dim3 grid(static_cast<unsigned>(a.g.QT * a.g.Hk * a.g.groups), static_cast<unsigned>(a.pieces));
-    splitkv_bwd_q_kernel<D><<<grid, kThreads, Lay<D>::kBytes, st>>>(mq, mo, mk, mv, a);
-    return cuda_fail(h, cudaGetLastError(), "dq kernel launch");
-}
-
-}  // namespace
-
-int launch_q(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-             const MainArgs &a, cudaStream_t st)
-{
-    return a.g.D == 64 ? launch_t<64>(h, mq, mo, mk, mv, a, st) : launch_t<128>(h, mq, mo, mk, mv, a, st);
-}
-
+}  // namespace q
 }  // namespace bwd
 }  // namespace skv
