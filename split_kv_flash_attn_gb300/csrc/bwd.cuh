@@ -196,7 +196,7 @@ int launch_join(skv_handle *h, const float *slot, int pieces, int64_t n, int out
                 cudaStream_t st);
 // One launch of both: kv_args.out0 or q_args.out0 NULL leaves a part out.
 int launch_main(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-                const MainArgs &kv_args, const MainArgs &q_args, cudaStream_t st);
+                const MainArgs &kv_args, const MainArgs &q_args, bool q_first, cudaStream_t st);
 
 }  // namespace bwd
 }  // namespace skv

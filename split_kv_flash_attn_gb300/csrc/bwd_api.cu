@@ -12,31 +12,47 @@ namespace bwd {
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Fixed cost of a CTA, in tiles of 128 x 128 (1.8 us for dk and dv, 1.2 for dq): tensor
-// memory, barriers, row statistics, pipeline fill, result.
-constexpr int kOverheadTiles = 4;
+// Costs in tiles of 128 x 128 of dq (1.2 us): a tile of dk and dv, a CTA's fixed part (tensor memory,
+// barriers, row statistics, pipeline fill, result), the launch that adds up pieces.
+constexpr double kKvTile = 1.5, kFixed = 4, kJoin = 2.5;
+// fp32 bytes that the adding up moves in a tile's time.
+constexpr double kJoinBytes = 7e6;
 
-// Pieces of a unit's `tiles` tiles.  Units that all take them run in whole waves of SMs; under
-// positions (`some`) they may take half of them on average, first the ones that take most, and only
-// the largest one and the sum count: the mean of both costs decides.  Pieces are added up by a
-// further launch: a few us, and `unit_bytes` of each unit once more for each piece (1 MB takes about a
-// tenth of a tile's time over all SMs).
-static int pieces_of(int64_t tiles, int64_t units, int sms, bool some, int64_t unit_bytes)
+// The CTAs of one launch: those of the kind whose CTAs take longer go out first, the others fill the
+// SMs.  So the launch ends when the longest CTA does, or when all SMs' work is done and about half a CTA of
+// the second kind later; a unit's tiles are cut into pieces (their sums added up by a further launch)
+// where that ends sooner.  16384 tokens, causal: no pieces, where whole waves of each kind by itself
+// wanted four; 512 tokens over 32768 keys: dq's 128 CTAs of 256 tiles first, dk and dv's 2048 of 16 after
+// them, where dq after them wanted seven pieces.
+struct Plan {
+    int kv_pieces, q_pieces;
+    bool q_first;
+};
+static Plan plan_of(const Geo &g, int64_t units, int sms, bool kv, bool q, bool some)
 {
-    double best = 0;
-    int pieces = 1;
-    for (int64_t p = 1; p <= std::min<int64_t>(tiles, 64) && units * (p - 1) < 8 * static_cast<int64_t>(sms); ++p) {
-        const double per = static_cast<double>((tiles + p - 1) / p + kOverheadTiles);
-        const double waves = static_cast<double>((units * p + sms - 1) / sms) * per;
-        const double share = std::max(per, units * (0.5 * tiles + p * kOverheadTiles) / sms);
-        double cost = some ? 0.5 * (waves + share) : waves;
-        if (p > 1) cost += 2 + 1e-7 * static_cast<double>(unit_bytes) * units * (p + 0.5);
-        if (p == 1 || cost < best) {
-            best = cost;
-            pieces = static_cast<int>(p);
+    static const int steps[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
+    const double share = some ? 0.75 : 1.0;                // positions: tiles seen, between half and all of them
+    const double kv_bytes = 8.0 * units * g.KT * kTile * g.D, q_bytes = 4.0 * units * g.QT * kTile * g.D;
+    Plan best{1, 1, false};
+    double least = -1;
+    for (int pk : steps) {
+        if (pk > 1 && (!kv || pk > g.QT)) break;
+        for (int pq : steps) {
+            if (pq > 1 && (!q || pq > g.KT)) break;
+            const double kv_one = kv ? kKvTile * ((g.QT + pk - 1) / pk) + kFixed : 0, q_one = q ? (g.KT + pq - 1) / pq + kFixed : 0;
+            const double kv_all = kv ? units * g.KT * (kKvTile * share * g.QT + kFixed * pk) : 0;
+            const double q_all = q ? units * g.QT * (share * g.KT + kFixed * pq) : 0;
+            const double last = !kv ? q_one : !q ? kv_one : std::min(kv_one, q_one);
+            double cost = std::max(std::max(kv_one, q_one), (kv_all + q_all) / sms + 0.5 * last);
+            if (pk > 1) cost += kJoin + kv_bytes * (pk + 0.5) / kJoinBytes;
+            if (pq > 1) cost += kJoin + q_bytes * (pq + 0.5) / kJoinBytes;
+            if (least < 0 || cost < least - 1e-9) {
+                least = cost;
+                best = Plan{pk, pq, q_one > kv_one};
+            }
         }
     }
-    return pieces;
+    return best;
 }
 
 // Tokens x heads of a query tile: the fewest tiles, then the fewest heads (a tile of
@@ -166,8 +182,8 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
         return SKV_OK;
     }
     // Pieces of a unit's tiles for grids that would leave SMs idle.
-    const int kv_pieces = dk ? pieces_of(g.QT, units * g.KT, h->sm_count, q_pos != nullptr, 2 * kTile * g.D * 4) : 1;
-    const int q_pieces = dq ? pieces_of(g.KT, units * g.QT, h->sm_count, q_pos != nullptr, kTile * g.D * 4) : 1;
+    const Plan plan = plan_of(g, units, h->sm_count, dk != nullptr, dq != nullptr, q_pos != nullptr);
+    const int kv_pieces = plan.kv_pieces, q_pieces = plan.q_pieces;
     const bool kv_slot = dk && (kv_pieces > 1 || g.QT > kStretch), q_slot = dq && (q_pieces > 1 || g.KT > kStretch);
 
     // Scratch: row statistics, tile sums, exponents of the keys, rows gathered or converted, fp32 sums.
@@ -236,7 +252,7 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
     b.pieces = q_pieces;
     b.slot = q_slot ? reinterpret_cast<float *>(ws + at_q) : nullptr;
     b.out0 = dq;
-    if ((rc = launch_main(h, mq, mo, mk, mv, a, b, st))) return rc;
+    if ((rc = launch_main(h, mq, mo, mk, mv, a, b, plan.q_first, st))) return rc;
     if (kv_pieces > 1 && (rc = launch_join(h, a.slot, kv_pieces, k_vals, 2, g_type, dk, dv, st))) return rc;
     if (q_pieces > 1 && (rc = launch_join(h, b.slot, q_pieces, q_vals, 1, g_type, dq, nullptr, st))) return rc;
     return SKV_OK;

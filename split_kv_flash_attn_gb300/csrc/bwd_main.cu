@@ -1,5 +1,6 @@
-// bwd_main.cu -- the launch of the gradient kernels: the CTAs of dk and dv, then those of dq, which
-// need nothing of the others and fill the SMs as those run out of work.
+// bwd_main.cu -- the launch of the gradient kernels: the CTAs of dk and dv and those of dq, which
+// need nothing of each other; the kind that goes out second fills the SMs as the first
+// runs out of work.
 #include "bwd_kv.cuh"
 #include "bwd_q.cuh"
 
@@ -10,22 +11,24 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     splitkv_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
                        const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                       const __grid_constant__ MainArgs kv_args, const __grid_constant__ MainArgs q_args, int kv_ctas)
+                       const __grid_constant__ MainArgs kv_args, const __grid_constant__ MainArgs q_args, int kv_ctas, int q_first)
 {
     extern __shared__ uint8_t smem_raw[];
-    const int b = blockIdx.x;
-    if (b < kv_ctas) {
+    const int q_ctas = gridDim.x - kv_ctas, first = q_first ? q_ctas : kv_ctas;
+    const bool second = blockIdx.x >= first;
+    const int b = second ? blockIdx.x - first : blockIdx.x;
+    if (second != (q_first != 0)) {
+        const int units = q_ctas / q_args.pieces;
+        q::run<D>(tq, to, tk, tv, q_args, b % units, b / units, smem_raw);
+    } else {
         const int units = kv_ctas / kv_args.pieces;
         kv::run<D>(tq, to, tk, tv, kv_args, b % units, b / units, smem_raw);
-    } else {
-        const int units = (gridDim.x - kv_ctas) / q_args.pieces;
-        q::run<D>(tq, to, tk, tv, q_args, (b - kv_ctas) % units, (b - kv_ctas) / units, smem_raw);
     }
 }
 
 template <int D>
 static int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-                    const MainArgs &kv_args, const MainArgs &q_args, cudaStream_t st)
+                    const MainArgs &kv_args, const MainArgs &q_args, bool q_first, cudaStream_t st)
 {
     static KernelAttrCache attr;
     constexpr int smem = kv::Lay<D>::kBytes > q::Lay<D>::kBytes ? kv::Lay<D>::kBytes : q::Lay<D>::kBytes;
@@ -36,15 +39,15 @@ static int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo,
     const int64_t q_ctas = q_args.out0 ? units * q_args.g.QT * q_args.pieces : 0;
     if (kv_ctas + q_ctas > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many tiles for one launch");
     splitkv_bwd_kernel<D><<<static_cast<unsigned>(kv_ctas + q_ctas), kThreads, smem, st>>>(mq, mo, mk, mv, kv_args, q_args,
-                                                                                           static_cast<int>(kv_ctas));
+                                                                                           static_cast<int>(kv_ctas), q_first);
     return cuda_fail(h, cudaGetLastError(), "gradient kernel launch");
 }
 
 int launch_main(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-                const MainArgs &kv_args, const MainArgs &q_args, cudaStream_t st)
+                const MainArgs &kv_args, const MainArgs &q_args, bool q_first, cudaStream_t st)
 {
-    return kv_args.g.D == 64 ? launch_t<64>(h, mq, mo, mk, mv, kv_args, q_args, st)
-                             : launch_t<128>(h, mq, mo, mk, mv, kv_args, q_args, st);
+    return kv_args.g.D == 64 ? launch_t<64>(h, mq, mo, mk, mv, kv_args, q_args, q_first, st)
+                             : launch_t<128>(h, mq, mo, mk, mv, kv_args, q_args, q_first, st);
 }
 
 }  // namespace bwd
