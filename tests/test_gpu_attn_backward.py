@@ -339,3 +339,58 @@ def test_against_differences(skv, h):
         # fp16 operands: 2^-11 of each product, of random sign; 1e-3 of the gradient's and direction's norms is far above
         room = 1e-3 * float(grads[i].double().norm() * way.norm())
         assert abs(slope - got) <= room, (i, slope, got, room)
+
+
+@pytest.mark.parametrize("lists", [False, True])
+def test_rows_far_into_a_cache(skv, h, lists):
+    """Keys whose offsets pass 32 bits: the end of a cache of a little over 4 GiB, as a range and by lists."""
+    import torch
+    S, nq, n, H, Hk, D = 1, 40, 200, 2, 1, 128
+    rows = (1 << 32) // 256 + 300
+    q, k, v, d_o = _inputs(S, nq, n, H, Hk, D, seed=21)
+    K = torch.full((rows, Hk, D), math.nan, dtype=torch.float16, device="cuda")
+    V = torch.full((rows, Hk, D), math.nan, dtype=torch.float16, device="cuda")
+    K[rows - n:], V[rows - n:] = k, v
+    see = torch.ones((1, nq, n), dtype=torch.bool, device="cuda")
+    o, lse = _forward(q, k[None], v[None], see)
+    want, bound = _want(q, k[None], v[None], see, o, lse, d_o)
+    if lists:
+        at = torch.arange(rows - n, rows, device="cuda", dtype=torch.int32).view(1, n)
+        got = skv.attn_backward(h, q, K, V, o, lse, d_o, Hk=Hk, kv_rows=at)
+    else:
+        got = skv.attn_backward(h, q, K, V, o, lse, d_o, Hk=Hk, kv_begin=rows - n)
+    assert h.status() == 0
+    _check3(got, want, bound, "far")
+
+
+def test_a_set_status_bit_does_not_disturb(skv):
+    """Bits that other calls leave in the status word (an append beyond its cache) do not end a gradient's waits."""
+    import torch
+    h = skv.Handle(0)
+    q, k, v, d_o = _inputs(1, 300, 500, 4, 2, 128, seed=22)
+    o, lse = skv.attn_partial(h, q, k, v, Hk=2)
+    ref = skv.attn_backward(h, q, k, v, o, lse, d_o, Hk=2)
+    assert h.status() == 0
+    skv.kv_append(h, torch.zeros((1, 2, 128), device="cuda"), torch.tensor([600], dtype=torch.int32, device="cuda"), k.clone())
+    got = skv.attn_backward(h, q, k, v, o, lse, d_o, Hk=2)
+    with pytest.raises(skv.SplitKVError) as e:
+        h.status()
+    assert e.value.status == 8
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+    h.close()
+
+
+def test_many_heads_and_sequences(skv, h):
+    """More KV heads times sequences than fit a wave, lists of other lengths than the tokens, one token each."""
+    import torch
+    S, nq, n, H, Hk, D = 9, 1, 333, 80, 40, 64
+    q, k, v, d_o = _inputs(S, nq, n, H, Hk, D, seed=23, shared=False)
+    lists = torch.arange(S * n, device="cuda", dtype=torch.int32).view(S, n)
+    see = torch.ones((S, nq, n), dtype=torch.bool, device="cuda")
+    kk, vv = k.view(S, n, Hk, D), v.view(S, n, Hk, D)
+    o, lse = _forward(q, kk, vv, see)
+    want, bound = _want(q, kk, vv, see, o, lse, d_o)
+    got = skv.attn_backward(h, q, k, v, o, lse, d_o, Hk=Hk, kv_rows=lists)
+    assert h.status() == 0
+    _check3(got, want, bound, "many")

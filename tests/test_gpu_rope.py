@@ -325,3 +325,35 @@ def rope_forward_grad(x, w, pos, freq):
     th = (pos.double().view(-1, 1) * freq.double()).unsqueeze(1)
     a, b = y.chunk(2, -1)
     return torch.cat((a * th.cos() - b * th.sin(), a * th.sin() + b * th.cos()), -1)
+
+
+def test_rows_far_into_a_cache_and_a_projection(skv, h):
+    """Cache rows and token strides whose offsets pass 32 bits."""
+    import torch
+    from tests.grad_util import check
+    H, Hk, D, n = 2, 1, 128, 5
+    rows = (1 << 32) // 256 + 100                                # 4 GiB of fp16 rows and a little
+    K = torch.zeros((rows, Hk, D), dtype=torch.float16, device="cuda")
+    V = torch.zeros((rows, Hk, D), dtype=torch.float16, device="cuda")
+    stride = (1 << 30) + 64                                      # elements; the last token starts beyond 2^32
+    flat = torch.empty(4 * stride + 4 * D, dtype=torch.float16, device="cuda")
+    x = flat.as_strided((n, H + 2 * Hk, D), (stride, D, 1))
+    g = _gen(3)
+    x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).view(1, n)
+    freq = (10000.0 ** (-torch.arange(64, device="cuda", dtype=torch.float64) / 64)).float()
+    at = (rows - 1 - 2 * torch.arange(n, device="cuda")).to(torch.int32)
+    spec = skv.Rope(D, freq)
+    q = skv.rope_append(h, spec, x[:, :H], x[:, H:H + 1], x[:, H + 1:], pos, at, K, V)
+    assert h.status() == 0
+    zero = torch.zeros(64, dtype=torch.int32, device="cuda")
+    for a, b in ((x[:, :H], q), (x[:, H:H + 1], K[at.long()])):
+        want, bound = _turn_bound(a, None, pos, freq, zero, False, 1.0)
+        check(b, want, bound, "far")
+    assert torch.equal(V[at.long()], x[:, H + 1:])
+    assert int((K.view(rows, -1) != 0).any(1).sum()) == n
+    dq = skv.rope_backward(h, spec, q, None, pos, dq=x[:, :H])[0]
+    assert dq.data_ptr() == x.data_ptr()
+    # turned there and back: two roundings of fp16 and what they pass through a turn
+    back = skv.rope_backward(h, spec, q, None, pos, x_dtype=torch.float32)[0]
+    assert torch.equal(back.half(), dq)
