@@ -32,8 +32,12 @@ namespace skv {
 namespace bwd {
 
 constexpr int kTile = 128;               // rows of a query tile, keys of a key tile
-constexpr int kThreads = 384;            // of the gradient kernels: eight compute warps and four others
-constexpr int kCompute = 256;
+// Threads of the gradient kernels: sixteen compute warps and four others (96 registers).  A thread's
+// chain of tensor-memory loads, exponentials and stores is mostly latency: four warps for each
+// quarter of an SM where two left it idle.
+constexpr int kThreads = 640, kCompute = 512;
+constexpr int kParts = kCompute / 128;   // compute threads that share a lane of tensor memory: columns of a tile in as many parts
+constexpr int kCols = kTile / kParts;    // columns of a thread
 constexpr int kPShift = 15;              // p' = 2^15 p
 // Tiles after which an accumulator is added to fp32 memory.  The tensor core cuts its
 // sums off instead of rounding them, and loses about 2^-24 of a sum's size for
@@ -161,7 +165,7 @@ __device__ __forceinline__ int64_t q_row(const Geo &g, const QTile &t, int r)
     return (t.group * g.T + tok) * g.H + static_cast<int64_t>(t.hk) * g.G + gg;
 }
 
-// Half a row of results: NC values at `out` elements, as g_type.
+// Part of a row of results: NC values at `at`, as g_type.
 template <int NC>
 __device__ __forceinline__ void store_row(void *base, int64_t at, int g_type, const float (&v)[NC])
 {
@@ -189,6 +193,23 @@ __device__ __forceinline__ void add_row(const float *p, float (&v)[NC])
         v[i + 2] += x.z;
         v[i + 3] += x.w;
     }
+}
+
+// NC (32 or 16) columns of this thread's lane.
+template <int NC>
+__device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[NC])
+{
+    static_assert(NC == 32 || NC == 16, "columns of a thread");
+    uint32_t r[NC];
+    if constexpr (NC == 32) {
+        tc::tmem_ld32(taddr, r);
+        tc::tmem_wait_ld(r);
+    } else {
+        tc::tmem_ld16(taddr, r);
+        tc::tmem_wait_ld16(r);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 int launch_prep(skv_handle *h, const PrepArgs &a, int do_type, cudaStream_t st);

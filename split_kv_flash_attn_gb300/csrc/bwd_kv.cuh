@@ -10,12 +10,12 @@
 // from one to the other: while the compute warps form P(j) it runs dK(j-1), dP(j), and
 // while they form dS(j) it runs dV(j), S(j+1).
 //
-// Warps: 0-7 compute (two threads a key, 64 rows of the tile each), 8 TMA, 9 issues dV(j) and
-// S(j+1), 10 dK(j) and dP(j+1), in turns, so that S(j+1), which the compute warps wait
+// Warps: 0-15 compute (32 rows of the tile and 32 keys each), 16 TMA, 17 issues dV(j) and
+// S(j+1), 18 dK(j) and dP(j+1), in turns, so that S(j+1), which the compute warps wait
 // for, does not stand behind dP; a thread's products run in order, so that their buffers
 // need no further wait.  The turn passes before a thread's last two products go out, and
 // its waits for operands fall into the other's turn.  (16384 tokens of 8 heads: no turns
-// 937 us, one thread for all four 867.)  11 looks each tile over when it has landed: it folds the powers of two
+// 937 us, one thread for all four 867.)  19 looks each tile over when it has landed: it folds the powers of two
 // into -L and -D, tells whether the tile needs a mask, and clears rows of
 // tokens that see nothing, whatever they hold.
 //
@@ -40,7 +40,8 @@ struct Lay {
     static constexpr int kOffO = kOffQ + kStages * kTileBytes;
     static constexpr int kOffInfo = kOffO + kStages * kTileBytes;
     static constexpr int kOffBits = kOffInfo + kStages * kInfoBytes;      // bitmap of visited query tiles
-    static constexpr int kOffBar = kOffBits + kMaxQTiles / 8;
+    static constexpr int kOffList = kOffBits + kMaxQTiles / 8;
+    static constexpr int kOffBar = kOffList + kStretch * 4;
     static constexpr int kBytes = kOffBar + 256 + 1024;                   // + alignment
 };
 static_assert(Lay<128>::kBytes <= 226 * 1024, "shared memory per CTA");
@@ -65,8 +66,8 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_count, s_lim, s_eN, s_eD, s_c, s_ew;
     __shared__ int s_need[kStages];
-    __shared__ int s_list[kStretch];
     uint32_t *bits = reinterpret_cast<uint32_t *>(sm + L::kOffBits);
+    int *s_list = reinterpret_cast<int *>(sm + L::kOffList);       // a stretch's query tiles
 
     const Geo &g = a.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -120,7 +121,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
     }
     const int key_lane = (warp & 3) * 32 + lane;             // compute threads: their key
     const int64_t key = j0 + key_lane;
-    const int key_exp = warp < 8 ? a.ew[(static_cast<int64_t>(gh) * g.KT + kt) * kTile + key_lane] : kAbsent;
+    const int key_exp = warp < kCompute / 32 ? a.ew[(static_cast<int64_t>(gh) * g.KT + kt) * kTile + key_lane] : kAbsent;
     __syncthreads();
     // ---- the query tiles that see one of these keys, and their sizes ----
     {
@@ -186,24 +187,25 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
         return false;
     };
 
-    constexpr int NC = D / 2;                                // result columns of a compute thread
-    const int hf = warp >> 2;
-    const int64_t out_at = ((group * g.n + key) * g.Hk + hk) * D + hf * NC;
-    const int64_t out_all = static_cast<int64_t>(g.groups) * g.n * g.Hk * D;
-    float *slot_v = a.slot ? a.slot + (static_cast<int64_t>(piece) * 2 + 1) * out_all + out_at : nullptr;
-    float *slot_k = a.slot ? a.slot + static_cast<int64_t>(piece) * 2 * out_all + out_at : nullptr;
+    constexpr int NC = D / kParts;                           // result columns of a compute thread
+    const int part = warp >> 2;                              // its part of a tile's rows, and of the results' columns
+    // (where this thread's results go; worked out where they are stored: registers are short in between)
+    auto out_at = [&]() { return ((group * g.n + key) * g.Hk + hk) * D + part * NC; };
+    auto slot_of = [&](int which) {                          // dk's fp32 sums, then dv's
+        return a.slot + (static_cast<int64_t>(piece) * 2 + which) * (static_cast<int64_t>(g.groups) * g.n * g.Hk * D) + out_at();
+    };
 
     if (o_lo >= o_hi && tid == kCompute) wait(B_KV, 0);      // the loads land before the CTA leaves
-    if (o_lo >= o_hi && warp < 8 && key < g.n) {             // nobody sees these keys
+    if (o_lo >= o_hi && warp < kCompute / 32 && key < g.n) {             // nobody sees these keys
         float z[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) z[i] = 0.f;
         if (a.pieces > 1) {
-            store_row<NC>(slot_k, 0, SKV_F32, z);
-            store_row<NC>(slot_v, 0, SKV_F32, z);
+            store_row<NC>(slot_of(0), 0, SKV_F32, z);
+            store_row<NC>(slot_of(1), 0, SKV_F32, z);
         } else {
-            store_row<NC>(a.out0, out_at, a.g_type, z);
-            store_row<NC>(a.out1, out_at, a.g_type, z);
+            store_row<NC>(a.out0, out_at(), a.g_type, z);
+            store_row<NC>(a.out1, out_at(), a.g_type, z);
         }
     }
 
@@ -235,7 +237,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
         }
         __syncthreads();
 
-        if (warp == 8) {
+        if (warp == kCompute / 32) {
             // ---------------- TMA ----------------------------------------
             if (lane == 0) {
                 const uint32_t box = static_cast<uint32_t>(box_rows) * D * 2;
@@ -268,10 +270,10 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                         tc::mbar_wait(bar(B_OLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
                 }
             }
-        } else if (warp == 9 || warp == 10) {
+        } else if (warp == kCompute / 32 + 1 || warp == kCompute / 32 + 2) {
             // ---------------- products: dV(j), S(j+1), and dK(j), dP(j+1) ----
             if (lane == 0) {
-                const bool second = warp == 10;
+                const bool second = warp == kCompute / 32 + 2;
                 constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
                 constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
                 // S = K Q^T or dP = V dO^T (both operands K-major); dV = P^T dO or dK = dS^T Q (B MN-major)
@@ -306,7 +308,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(acc, col + (kk & 3) * 8 + (kk >> 2) * 64, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
+                        tc::mma_f16_ts(acc, col + (kk & 1) * 8 + (kk >> 1) * kCols, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
                                        kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
                     tc::mma_commit(bar((second ? B_QEMPTY : B_OEMPTY) + st));
                     if (i + 1 < nt) ok = scores(it + 1, true);
@@ -318,7 +320,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     if (!ok) tc::mbar_wait(bar(b_acc), stretch & 1, nullptr, 100000000ull);   // nothing runs on when the CTA leaves
                 }
             }
-        } else if (warp == 11) {
+        } else if (warp == kCompute / 32 + 3) {
             // ---------------- each tile as it has landed --------------------
             for (int i = 0; i < nt; ++i) {
                 const int it = it0 + i, st = it & (kStages - 1), ph = (it / kStages) & 1;
@@ -366,59 +368,61 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             }
         } else {
             // ---------------- P and dS --------------------------------------
-            // A thread holds, of each eight columns (rows of the tile) of its half, two columns of four keys: L and D
-            // then come in 16 loads of two values, of which a warp's threads read four different ones.  (A key a
-            // thread, each of its 64 columns' values read by the whole warp, took 1370 clocks of shared memory's time
+            // A thread holds, of each eight columns (rows of the tile) of its part, two columns of four keys: L and D
+            // then come in 8 loads of two values, of which a warp's threads read four different ones.  (A key a
+            // thread, each of its columns' values read by the whole warp, took 1370 clocks of shared memory's time
             // for a tile, beside the products' 2050.)
             const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            const uint32_t ts = lane_base + kColS + part * kCols, tp = lane_base + kColP + part * kCols;
             const float2 c1 = make_float2(a.scale * 1.4426950408889634f, a.scale * 1.4426950408889634f);
             const float2 sg = make_float2(sigma, sigma);
-            const int64_t key4 = j0 + (warp & 3) * 32 + (lane >> 2);      // its first key; the others 8, 16, 24 on
+            const int key4 = (warp & 3) * 32 + (lane >> 2);  // its first key in the tile; the others 8, 16, 24 on
+            constexpr int G8 = kCols / 8;                    // groups of eight columns
             for (int i = 0; i < nt; ++i) {
                 const int it = it0 + i, st = it & (kStages - 1);
-                const float *info = reinterpret_cast<const float *>(sm + L::kOffInfo + st * kInfoBytes) + hf * 64 + 2 * (lane & 3);
+                const float *info = reinterpret_cast<const float *>(sm + L::kOffInfo + st * kInfoBytes) + part * kCols + 2 * (lane & 3);
                 bool ok = wait(B_QFULL + st, (it / kStages) & 1);
                 ok = ok && wait(B_S, it & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
-                const bool need = s_need[st] != 0;
-                float p[64];                                 // [16 lanes][group of 8 columns][key, key + 8][two columns]
+                float p[2 * 4 * G8];                         // [16 lanes][group][key, key + 8][two columns]
                 {
-                    uint32_t r[2][32];
-                    tc::tmem_ld16x64(lane_base + kColS + hf * 64, r[0]);
-                    tc::tmem_ld16x64(lane_base + (16u << 16) + kColS + hf * 64, r[1]);
-                    tc::tmem_wait_ld(r[0]);
-                    tc::tmem_wait_ld(r[1]);
+                    uint32_t r[2][4 * G8];
+                    tc::tmem_ld16x32(ts, r[0]);
+                    tc::tmem_ld16x32(ts + (16u << 16), r[1]);
+                    const bool need = s_need[st] != 0;
+                    tc::tmem_wait_ld16(r[0]);
+                    tc::tmem_wait_ld16(r[1]);
 #pragma unroll
-                    for (int g8 = 0; g8 < 8; ++g8) {
+                    for (int g8 = 0; g8 < G8; ++g8) {
                         const float2 l2 = *reinterpret_cast<const float2 *>(info + 8 * g8);   // -L
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             const uint32_t *x = &r[u >> 1][4 * g8 + 2 * (u & 1)];
                             const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c1, l2);
-                            float *pp = &p[(u >> 1) * 32 + 4 * g8 + 2 * (u & 1)];
+                            float *pp = &p[(u >> 1) * 4 * G8 + 4 * g8 + 2 * (u & 1)];
                             pp[0] = fast_exp2(e.x);
                             pp[1] = fast_exp2(e.y);
                         }
                     }
                     if (need) {
 #pragma unroll
-                        for (int g8 = 0; g8 < 8; ++g8) {
+                        for (int g8 = 0; g8 < G8; ++g8) {
                             const int2 m = *reinterpret_cast<const int2 *>(info + 3 * kTile + 8 * g8);
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
-                                float *pp = &p[(u >> 1) * 32 + 4 * g8 + 2 * (u & 1)];
-                                if (key4 + 8 * u >= m.x) pp[0] = 0.f;
-                                if (key4 + 8 * u >= m.y) pp[1] = 0.f;
+                                float *pp = &p[(u >> 1) * 4 * G8 + 4 * g8 + 2 * (u & 1)];
+                                if (j0 + key4 + 8 * u >= m.x) pp[0] = 0.f;
+                                if (j0 + key4 + 8 * u >= m.y) pp[1] = 0.f;
                             }
                         }
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        uint32_t ph[16];
+                        uint32_t ph[2 * G8];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) ph[c] = pack_half2(p[32 * u + 2 * c], p[32 * u + 2 * c + 1]);
-                        tc::tmem_st16x32(lane_base + (static_cast<uint32_t>(16 * u) << 16) + kColS + hf * 64, ph);
+                        for (int c = 0; c < 2 * G8; ++c) ph[c] = pack_half2(p[4 * G8 * u + 2 * c], p[4 * G8 * u + 2 * c + 1]);
+                        tc::tmem_st16x16(ts + (static_cast<uint32_t>(16 * u) << 16), ph);
                     }
                 }
                 tc::tmem_wait_st();
@@ -427,24 +431,25 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 ok = wait(B_DP, it & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
-                float2 d2[8];                                // -D
+                uint32_t r[2][4 * G8];
+                tc::tmem_ld16x32(tp, r[0]);
+                tc::tmem_ld16x32(tp + (16u << 16), r[1]);
+                float2 d2[G8];                               // -D
 #pragma unroll
-                for (int g8 = 0; g8 < 8; ++g8) d2[g8] = *reinterpret_cast<const float2 *>(info + kTile + 8 * g8);
-                uint32_t dh[2][16];
+                for (int g8 = 0; g8 < G8; ++g8) d2[g8] = *reinterpret_cast<const float2 *>(info + kTile + 8 * g8);
+                tc::tmem_wait_ld16(r[0]);
+                tc::tmem_wait_ld16(r[1]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    uint32_t r[32];
-                    tc::tmem_ld16x64(lane_base + (static_cast<uint32_t>(16 * u) << 16) + kColP + hf * 64, r);
-                    tc::tmem_wait_ld(r);
+                    uint32_t dh[2 * G8];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {           // group c / 2, key + 8 (c % 2)
-                        float2 x = __ffma2_rn(make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sg, d2[c >> 1]);
-                        x = __fmul2_rn(x, make_float2(p[32 * u + 2 * c], p[32 * u + 2 * c + 1]));
-                        dh[u][c] = pack_half2(x.x, x.y);
+                    for (int c = 0; c < 2 * G8; ++c) {       // group c / 2, key + 8 (c % 2)
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(r[u][2 * c]), __uint_as_float(r[u][2 * c + 1])), sg, d2[c >> 1]);
+                        x = __fmul2_rn(x, make_float2(p[4 * G8 * u + 2 * c], p[4 * G8 * u + 2 * c + 1]));
+                        dh[c] = pack_half2(x.x, x.y);
                     }
+                    tc::tmem_st16x16(tp + (static_cast<uint32_t>(16 * u) << 16), dh);
                 }
-                tc::tmem_st16x32(lane_base + kColP + hf * 64, dh[0]);
-                tc::tmem_st16x32(lane_base + (16u << 16) + kColP + hf * 64, dh[1]);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 tc::mbar_arrive(bar(B_DS));
@@ -460,20 +465,14 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {    // dk, dv
                     const Pow2 f(which ? 1.f : a.scale, which ? cmax - kPShift : cmax - sig_e - kPShift);
-                    float *slot = which ? slot_v : slot_k;
                     float v[NC];
+                    load_cols<NC>(lane_base + (which ? kColV : kColK) + part * NC, v);
 #pragma unroll
-                    for (int u = 0; u < NC / 32; ++u) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(lane_base + (which ? kColV : kColK) + hf * NC + 32 * u, r);
-                        tc::tmem_wait_ld(r);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[32 * u + c] = there ? f(__uint_as_float(r[c])) : 0.f;
-                    }
+                    for (int c = 0; c < NC; ++c) v[c] = there ? f(v[c]) : 0.f;
                     if (key < g.n) {
-                        if (stretch > 0) add_row<NC>(slot, v);
-                        if (last && a.pieces == 1) store_row<NC>(which ? a.out1 : a.out0, out_at, a.g_type, v);
-                        else store_row<NC>(slot, 0, SKV_F32, v);
+                        if (stretch > 0) add_row<NC>(slot_of(which), v);
+                        if (last && a.pieces == 1) store_row<NC>(which ? a.out1 : a.out0, out_at(), a.g_type, v);
+                        else store_row<NC>(slot_of(which), 0, SKV_F32, v);
                     }
                 }
                 tc::tc_fence_before();

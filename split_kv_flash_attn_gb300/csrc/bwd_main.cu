@@ -31,6 +31,8 @@ static int launch_t(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo,
                     const MainArgs &kv_args, const MainArgs &q_args, bool q_first, cudaStream_t st)
 {
     static KernelAttrCache attr;
+    constexpr int kStatic = 1792;                          // at most, of both: 1.7 KB as built
+    static_assert(q::Lay<128>::kBytes + kStatic <= 227 * 1024 && kv::Lay<128>::kBytes + kStatic <= 227 * 1024, "shared memory per CTA");
     constexpr int smem = kv::Lay<D>::kBytes > q::Lay<D>::kBytes ? kv::Lay<D>::kBytes : q::Lay<D>::kBytes;
     const cudaError_t e = kernel_smem_optin(attr, reinterpret_cast<const void *>(splitkv_bwd_kernel<D>), smem, kThreads, nullptr);
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaFuncSetAttribute(gradients)");

@@ -2,14 +2,22 @@
 // sees.
 //
 //   S = Q K^T   dP = dO V^T   [128 rows x 128 keys]
-//   dS = 2^(S c - L) (dP sigma - D)   over S in tensor memory
+//   dS = 2^(S c - L) (dP sigma - D)   over dP in tensor memory
 //   dQ += dS K                        (A from tensor memory)
 // K serves S as the K-major and dQ as the MN-major B operand: one TMA load for both.
-// Tensor memory: two S buffers, dP, dQ.  While the compute warps are at tile j, the tensor
-// core runs S(j+1), dQ(j-1) and, once dP(j) has been loaded, dP(j+1).
+// Tensor memory: S, two dP buffers, dQ.  S(j+1) goes out as soon as S(j) has been loaded, dP(j+1) once
+// dQ(j-1) has read the dS that stood in its buffer: both are there before the compute warps
+// have done tile j.  (Two S buffers with dS over them and one dP: S(j+1) then waits for dQ(j-1) behind
+// dP(j), 1140 us for 16384 x 16384 of 8 heads.)
 //
-// Warps: 0-7 compute (two threads a row, 64 keys of the tile each; a row's L, D, sigma
-// and limit are registers), 8 TMA, 9 issues S and dP, 10 issues dQ, 11 looks each K tile
+// What rounding dS to fp16 takes from a row's terms, eps_k, would come out as sum_k eps_k K_k.  Keys of a
+// head have much in common (a mean that all scores share and the softmax ignores), so the sum of
+// a row's eps is kept in fp32 and times the mean of the CTA's first keys given back: any
+// vector would do, and what all keys share drops out of the error.  (Keys of N(0, 1) plus half as much in
+// common: dq's error 3.2e-4 -> 2.9e-4 of its norm, 2.1e-4 of which is its own rounding.)
+//
+// Warps: 0-15 compute (four threads a row, 32 keys of the tile each; a row's L, D, sigma
+// and limit are registers), 16 TMA, 17 issues S and dP, 18 issues dQ, 19 looks each K tile
 // over: absent keys of lists, and rows behind the last key that any row sees, which
 // hold anything, are cleared.
 #pragma once
@@ -36,11 +44,11 @@ struct Lay {
 static_assert(Lay<128>::kBytes <= 227 * 1024 - 128, "shared memory per CTA");
 
 enum { B_QO, B_KLAND, B_KFULL = B_KLAND + kK, B_KEMPTY = B_KFULL + kK, B_VFULL = B_KEMPTY + kK,
-       B_VEMPTY = B_VFULL + kV, B_S = B_VEMPTY + kV, B_DS = B_S + 2, B_DQ = B_DS + 2, B_DP = B_DQ + 2, B_DPFREE,
+       B_VEMPTY = B_VFULL + kV, B_DP = B_VEMPTY + kV, B_DS = B_DP + 2, B_DQ = B_DS + 2, B_S = B_DQ + 2, B_SFREE,
        B_ACC, B_COUNT };
 static_assert(B_COUNT * 8 <= 256, "barrier area");
 
-constexpr int kColS = 0, kColP = 256, kColQ = 384;
+constexpr int kColS = 0, kColP = 128, kColQ = 384;
 
 template <int D>
 __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to, const CUtensorMap &tk, const CUtensorMap &tv,
@@ -52,7 +60,9 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
     auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_ew, s_last;
-    __shared__ uint32_t s_here[kK][4];                  // keys of a tile that are there
+    __shared__ float s_mean[D];                              // mean of the first keys
+    __shared__ float s_sum[2][kTile];                        // its parts; what rounding took from dS, by halves
+    __shared__ uint32_t s_here[kK][4];                       // keys of a tile that are there
 
     const Geo &g = a.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -88,12 +98,12 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             tc::mbar_init(bar(B_VEMPTY + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar(B_S + i), 1);
+            tc::mbar_init(bar(B_DP + i), 1);
             tc::mbar_init(bar(B_DS + i), kCompute);
             tc::mbar_init(bar(B_DQ + i), 1);
         }
-        tc::mbar_init(bar(B_DP), 1);
-        tc::mbar_init(bar(B_DPFREE), kCompute);
+        tc::mbar_init(bar(B_S), 1);
+        tc::mbar_init(bar(B_SFREE), kCompute);
         tc::mbar_init(bar(B_ACC), 1);
         tc::fence_barrier_init();
         // the rows, while the keys' exponents are looked through
@@ -147,12 +157,11 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
     };
 
     // ---- a compute thread's row ----
-    constexpr int NC = D / 2;
-    const int m = (warp & 3) * 32 + lane, hf = warp >> 2;
+    constexpr int NC = D / kParts;
+    const int m = (warp & 3) * 32 + lane, part = warp >> 2;
     float row_L = INFINITY, row_D = 0.f, sigma = 1.f;
     int lim = 0, out_e = 0;
-    int64_t row = -1;
-    if (warp < 8) {
+    if (warp < kCompute / 32) {
         const float *info = a.info + tile * (kInfoRows * kTile) + m;
         row_L = info[0];
         lim = max(0, __float_as_int(info[3 * kTile]));
@@ -161,25 +170,28 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
         sigma = pow2(-e);
         row_D = info[kTile] * sigma;
         out_e = e + c - kPShift;
-        row = q_row(g, t, m);
     }
-    const int64_t out_all = static_cast<int64_t>(g.groups) * g.T * g.H * D;
-    const int64_t out_at = row * D + hf * NC;
-    float *slot = a.slot ? a.slot + static_cast<int64_t>(piece) * out_all + out_at : nullptr;
+    // (where this thread's result goes; worked out where it is stored)
+    auto slot_of = [&](int64_t row) {
+        return a.slot + piece * (static_cast<int64_t>(g.groups) * g.T * g.H * D) + row * D + part * NC;
+    };
 
     if (j_lo >= j_hi && tid == kCompute) wait(B_QO, 0);      // the loads land before the CTA leaves
-    if (j_lo >= j_hi && row >= 0) {                          // no keys
+    if (j_lo >= j_hi && warp < kCompute / 32) {                          // no keys
+        const int64_t row = q_row(g, t, m);
         float z[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) z[i] = 0.f;
-        if (a.pieces > 1) store_row<NC>(slot, 0, SKV_F32, z);
-        else store_row<NC>(a.out0, out_at, a.g_type, z);
+        if (row >= 0) {
+            if (a.pieces > 1) store_row<NC>(slot_of(row), 0, SKV_F32, z);
+            else store_row<NC>(a.out0, row * D + part * NC, a.g_type, z);
+        }
     }
 
     int it0 = 0, stretch = 0;
     for (int j = j_lo; j < j_hi; j += kStretch, ++stretch) {
         const int nt = min(kStretch, j_hi - j);
-        if (warp == 8) {
+        if (warp == kCompute / 32) {
             // ---------------- TMA ----------------------------------------
             if (lane == 0) {
                 int k_out = 0, v_out = 0;
@@ -205,7 +217,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                         tc::mbar_wait(bar(B_VFULL + (it0 + i) % kV), ((it0 + i) / kV) & 1, nullptr, 100000000ull);
                 }
             }
-        } else if (warp == 9) {
+        } else if (warp == kCompute / 32 + 1) {
             // ---------------- S and dP ------------------------------------
             if (lane == 0) {
                 constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
@@ -218,32 +230,32 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 for (int i = 0; ok && i < nt; ++i) {
                     const int it = it0 + i, ks = it % kK, vs = it % kV, sb = it & 1;
                     ok = wait(B_KFULL + ks, (it / kK) & 1);
-                    // the buffer's last dS has been read
-                    ok = ok && (it < 2 || wait(B_DQ + sb, ((it >> 1) - 1) & 1));
+                    ok = ok && (it < 1 || wait(B_SFREE, (it - 1) & 1));
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColS + sb * kTile, tc::desc_add(dq0, off), tc::desc_add(dk0, ks * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss(tmem + kColS, tc::desc_add(dq0, off), tc::desc_add(dk0, ks * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(B_S + sb));
-                    ok = wait(B_VFULL + vs, (it / kV) & 1) && (it < 1 || wait(B_DPFREE, (it - 1) & 1));
+                    tc::mma_commit(bar(B_S));
+                    // (the buffer's last dS has been read)
+                    ok = wait(B_VFULL + vs, (it / kV) & 1) && (it < 2 || wait(B_DQ + sb, ((it >> 1) - 1) & 1));
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColP, tc::desc_add(do0, off), tc::desc_add(dv0, vs * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss(tmem + kColP + sb * kTile, tc::desc_add(do0, off), tc::desc_add(dv0, vs * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(B_DP));
+                    tc::mma_commit(bar(B_DP + sb));
                     tc::mma_commit(bar(B_VEMPTY + vs));
                     done = it;
                 }
                 if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
-                    tc::mbar_wait(bar(B_DP), done & 1, nullptr, 100000000ull);
+                    tc::mbar_wait(bar(B_DP + (done & 1)), (done >> 1) & 1, nullptr, 100000000ull);
             }
-        } else if (warp == 10) {
+        } else if (warp == kCompute / 32 + 2) {
             // ---------------- dQ --------------------------------------------
             if (lane == 0) {
                 constexpr uint32_t kIdescQ = tc::idesc_f16(kTile, D, true);
@@ -255,7 +267,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(tmem + kColQ, tmem + kColS + sb * kTile + (kk & 3) * 8 + (kk >> 2) * 64,
+                        tc::mma_f16_ts(tmem + kColQ, tmem + kColP + sb * kTile + (kk & 1) * 8 + (kk >> 1) * kCols,
                                        tc::desc_add(dk0, ks * L::kTileBytes + kk * 2048), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
                     tc::mma_commit(bar(B_KEMPTY + ks));
                     tc::mma_commit(bar(B_DQ + sb));
@@ -265,7 +277,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
                     tc::mbar_wait(bar(B_DQ + (done & 1)), (done >> 1) & 1, nullptr, 100000000ull);
             }
-        } else if (warp == 11) {
+        } else if (warp == kCompute / 32 + 3) {
             // ---------------- each K tile as it has landed -------------------
             const int8_t *ew = a.ew + static_cast<int64_t>(gh) * g.KT * kTile;
             for (int i = 0; i < nt; ++i) {
@@ -296,62 +308,102 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             // ---------------- dS --------------------------------------------
             const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             const float c1 = a.scale * 1.4426950408889634f;
-            for (int i = 0; i < nt; ++i) {
-                const int it = it0 + i, st = it % kK, sb = it & 1;
-                const uint32_t cs = lane_base + kColS + sb * kTile + hf * 64;
-                bool ok = wait(B_KFULL + st, (it / kK) & 1);
-                const uint32_t h0 = s_here[st][hf * 2], h1 = s_here[st][hf * 2 + 1];
-                const int left = lim - (j + i) * kTile - hf * 64;        // columns of this half that the row sees
-                ok = ok && wait(B_S + sb, (it >> 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc::tc_fence_after();
-                float p[64];
-                {
-                    uint32_t r[2][32];
-                    tc::tmem_ld32(cs, r[0]);
-                    tc::tmem_ld32(cs + 32, r[1]);
-                    tc::tmem_wait_ld(r[0]);
-                    tc::tmem_wait_ld(r[1]);
-#pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c >> 5][c & 31]), __uint_as_float(r[c >> 5][(c & 31) + 1])),
-                                                    make_float2(c1, c1), make_float2(-row_L, -row_L));
-                        p[c] = fast_exp2(x.x);
-                        p[c + 1] = fast_exp2(x.y);
+            auto compute_sync = [&]() { asm volatile("bar.sync 5, %0;\n" ::"n"(kCompute) : "memory"); };
+            if (stretch == 0) {
+                // the mean of the first tile's keys: the first 256 threads add up two channels of 32 or 16 rows,
+                // the upper half of them leaves its sums, the lower one adds its own
+                constexpr int PAIRS = D / 2, ROWS = kTile / (256 / PAIRS);
+                float *sum = &s_sum[0][0] + (tid & 127) * 2;
+                float2 m2 = make_float2(0.f, 0.f);
+                const bool ok = wait(B_KFULL, 0);
+                if (__all_sync(0xffffffffu, ok) && tid < 256) {
+                    const int pr = tid % PAIRS, r0 = tid / PAIRS * ROWS;
+                    const uint8_t *col = sm + L::kOffK + (pr >> 5) * kHalf + (pr & 3) * 4;
+                    for (int r = r0; r < r0 + ROWS; ++r) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(col + r * 128 + ((((pr & 31) >> 2) ^ (r & 7)) << 4)));
+                        m2.x += x.x;
+                        m2.y += x.y;
                     }
                 }
-                ok = wait(B_DP, it & 1);
+                if (tid >= 128 && tid < 256) {
+                    sum[0] = m2.x;
+                    sum[1] = m2.y;
+                }
+                compute_sync();
+                if (tid < 128) {
+                    sum[0] += m2.x;
+                    sum[1] += m2.y;
+                }
+                compute_sync();
+                if (tid < D) {
+                    float m1 = 0.f;
+                    for (int k = tid; k < 256; k += D) m1 += (&s_sum[0][0])[k];
+                    s_mean[tid] = m1 * (1.f / kTile);
+                }
+                compute_sync();
+            }
+            float2 eps2 = make_float2(0.f, 0.f);
+            for (int i = 0; i < nt; ++i) {
+                const int it = it0 + i, st = it % kK, sb = it & 1;
+                const uint32_t cs = lane_base + kColS + part * kCols, cp = lane_base + kColP + sb * kTile + part * kCols;
+                bool ok = wait(B_KFULL + st, (it / kK) & 1);
+                const uint32_t here = s_here[st][part];
+                const int left = lim - (j + i) * kTile - part * kCols;   // columns of this part that the row sees
+                ok = ok && wait(B_S, it & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
-                uint32_t r[2][32];
-                tc::tmem_ld32(lane_base + kColP + hf * 64, r[0]);
-                tc::tmem_ld32(lane_base + kColP + hf * 64 + 32, r[1]);
-                tc::tmem_wait_ld(r[0]);
-                tc::tmem_wait_ld(r[1]);
+                float p[kCols];
+                uint32_t r[kCols];
+                tc::tmem_ld32(cs, r);
+                tc::tmem_wait_ld(r);
                 tc::tc_fence_before();
-                tc::mbar_arrive(bar(B_DPFREE));
+                tc::mbar_arrive(bar(B_SFREE));
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c >> 5][c & 31]), __uint_as_float(r[c >> 5][(c & 31) + 1])),
-                                          make_float2(sigma, sigma), make_float2(-row_D, -row_D));
+                for (int c = 0; c < kCols; c += 2) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), make_float2(c1, c1),
+                                                make_float2(-row_L, -row_L));
+                    p[c] = fast_exp2(x.x);
+                    p[c + 1] = fast_exp2(x.y);
+                }
+                ok = wait(B_DP + sb, (it >> 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+                tc::tmem_ld32(cp, r);
+                tc::tmem_wait_ld(r);
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2) {
+                    float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), make_float2(sigma, sigma),
+                                          make_float2(-row_D, -row_D));
                     x = __fmul2_rn(x, make_float2(p[c], p[c + 1]));
                     p[c] = x.x;
                     p[c + 1] = x.y;
                 }
-                if (__any_sync(0xffffffffu, left < 64 || (h0 & h1) != 0xffffffffu)) {
+                if (__any_sync(0xffffffffu, left < kCols || here != 0xffffffffu)) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c >= left || !(((c < 32 ? h0 : h1) >> (c & 31)) & 1u)) p[c] = 0.f;
+                    for (int c = 0; c < kCols; ++c)
+                        if (c >= left || !((here >> c) & 1u)) p[c] = 0.f;
                 }
-                uint32_t dh[32];
+                uint32_t dh[kCols / 2];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) dh[c] = pack_half2(p[2 * c], p[2 * c + 1]);
-                tc::tmem_st32u(cs, dh);
+                for (int c = 0; c < kCols / 2; ++c) dh[c] = pack_half2(p[2 * c], p[2 * c + 1]);
+                tc::tmem_st16u(cp, dh);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 tc::mbar_arrive(bar(B_DS + sb));
+                // (while the products run)
+#pragma unroll
+                for (int c = 0; c < kCols / 2; ++c) {
+                    const __half2 h2 = *reinterpret_cast<const __half2 *>(&dh[c]);
+                    eps2 = __fadd2_rn(eps2, make_float2(sub_h(__low2half(h2), p[2 * c]), sub_h(__high2half(h2), p[2 * c + 1])));
+                }
             }
             // ---------------- the sum of this stretch ----------------------------
+            float eps = eps2.x + eps2.y;
+            if (part >= 2) s_sum[part - 2][m] = eps;
+            compute_sync();
+            if (part < 2) s_sum[part][m] += eps;
+            compute_sync();
+            eps = -(s_sum[0][m] + s_sum[1][m]);
             bool ok = !*reinterpret_cast<volatile int *>(&s_abort);
             ok = ok && wait(B_ACC, stretch & 1);
             ok = __all_sync(0xffffffffu, ok);
@@ -359,18 +411,14 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 tc::tc_fence_after();
                 const Pow2 f(a.scale, out_e);
                 float v[NC];
+                load_cols<NC>(lane_base + kColQ + part * NC, v);
 #pragma unroll
-                for (int u = 0; u < NC / 32; ++u) {
-                    uint32_t r[32];
-                    tc::tmem_ld32(lane_base + kColQ + hf * NC + 32 * u, r);
-                    tc::tmem_wait_ld(r);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[32 * u + c] = lim > 0 ? f(__uint_as_float(r[c])) : 0.f;
-                }
+                for (int c = 0; c < NC; ++c) v[c] = lim > 0 ? f(fmaf(eps, s_mean[part * NC + c], v[c])) : 0.f;
+                const int64_t row = q_row(g, t, m);
                 if (row >= 0) {
-                    if (stretch > 0) add_row<NC>(slot, v);
-                    if (j + kStretch >= j_hi && a.pieces == 1) store_row<NC>(a.out0, out_at, a.g_type, v);
-                    else store_row<NC>(slot, 0, SKV_F32, v);
+                    if (stretch > 0) add_row<NC>(slot_of(row), v);
+                    if (j + kStretch >= j_hi && a.pieces == 1) store_row<NC>(a.out0, row * D + part * NC, a.g_type, v);
+                    else store_row<NC>(slot_of(row), 0, SKV_F32, v);
                 }
                 tc::tc_fence_before();
             }

@@ -126,6 +126,14 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// a - c of an fp16 and an fp32 number, in fp32.
+__device__ __forceinline__ float sub_h(__half a, float c)
+{
+    float d;
+    asm volatile("sub.rn.f32.f16 %0, %1, %2;\n" : "=f"(d) : "h"(__half_as_ushort(a)), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;

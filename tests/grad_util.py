@@ -33,6 +33,9 @@ def attention_backward(q, k, v, see, scale, o, lse, d_o, d_lse=None):
           rounded to fp16 first: 2^-11 of each value, 2^-25 2^-13 of the row's largest below the normal range;
       ds: the fp16 number that enters the product: 2^-11, or 2^-25 of its scale 2^(e - 15), e at most 3 above the
           largest possible |dp - delta| (a row's own for dq, the call's largest one for dk);
+          What this takes from the terms of a row of dq is given back for the mean m of one tile's keys (of 128, those
+          behind the last one that the row's tile sees counted as zeros): sum eps_k K_k - (sum eps_k) m, so |eps_k| |K_k - m|
+          stands in the bound, with |m| at most the largest mean that the first keys of a tile have;
       sums over keys or rows: fp32, cut off every 16 terms within stretches of 16384: 2^-24 of the sum of magnitudes for
           each of at most 1024 steps.
     """
@@ -67,9 +70,12 @@ def attention_backward(q, k, v, see, scale, o, lse, d_o, d_lse=None):
             edp = da * (2.0 ** -19 + (H if f32do else 0.0)) + (top * 2.0 ** -38 * (vv.abs().sum(1) + oo.abs().sum(1, keepdim=True)) if f32do else 0.0)
             eds = ds.abs() * ep + p * edp
             size = torch.linalg.vector_norm(dd, dim=1, keepdim=True) * torch.linalg.vector_norm(vv, dim=1).max() + delta.abs()
+            tiles = torch.nn.functional.pad(kk, (0, 0, 0, -n % 128)).view(-1, 128, D).cumsum(1) / 128
+            mean = tiles.abs().amax((0, 1))
             sub_q, sub_k = size * 2.0 ** -40 * 8, size.max() * 2.0 ** -40 * 8
             dq[b, :, h] = ds @ kk * scale
             bq[b, :, h] = ((eds + ds.abs() * H + sub_q) * sb) @ kk.abs() * abs(scale) + ds.abs() @ kk.abs() * abs(scale) * steps
+            bq[b, :, h] += ((ds.abs() * H + sub_q) * sb).sum(1, keepdim=True) * mean * abs(scale)
             dk[b, :, h // G] += ds.t() @ qq * scale
             bk[b, :, h // G] += ((eds + ds.abs() * H + sub_k) * sb).t() @ qq.abs() * abs(scale) + ds.abs().t() @ qq.abs() * abs(scale) * steps
             dv[b, :, h // G] += p.t() @ dd
