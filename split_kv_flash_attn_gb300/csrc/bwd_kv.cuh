@@ -272,7 +272,8 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             }
         } else if (warp == kCompute / 32 + 1 || warp == kCompute / 32 + 2) {
             // ---------------- products: dV(j), S(j+1), and dK(j), dP(j+1) ----
-            if (lane == 0) {
+            {
+                const uint32_t one = tc::elect_one();        // the lane that issues; all of the warp waits
                 const bool second = warp == kCompute / 32 + 2;
                 constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
                 constexpr uint32_t kIdescV = tc::idesc_f16(kTile, D, true);
@@ -287,36 +288,37 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 bool out = false;                            // something was issued
                 auto scores = [&](int it, bool pass) {
                     const int st = it & (kStages - 1);
-                    if (!wait(b_in + st, (it / kStages) & 1)) return false;
+                    if (!__all_sync(0xffffffffu, wait(b_in + st, (it / kStages) & 1))) return false;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        if (pass && kk == D / 16 - 2) tc::mbar_arrive(bar(b_other));   // ahead of the end of its wait
-                        tc::mma_f16_ss(col, tc::desc_add(da, off), tc::desc_add(db, st * L::kTileBytes + off), kIdescS, kk > 0);
+                        if (pass && one && kk == D / 16 - 2) tc::mbar_arrive(bar(b_other));   // ahead of the end of its wait
+                        tc::mma_f16_ss_if(one, col, tc::desc_add(da, off), tc::desc_add(db, st * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(b_out));
-                    if (second) tc::mma_commit(bar(B_OEMPTY + st));
+                    tc::mma_commit_if(one, bar(b_out));
+                    if (second) tc::mma_commit_if(one, bar(B_OEMPTY + st));
                     out = true;
                     return true;
                 };
-                bool ok = wait(B_KV, 0) && scores(it0, second);   // (the first dV goes first)
+                bool ok = __all_sync(0xffffffffu, wait(B_KV, 0)) && scores(it0, second);   // (the first dV goes first)
                 for (int i = 0; ok && i < nt; ++i) {
                     const int it = it0 + i, st = it & (kStages - 1);
                     ok = wait(b_ready, it & 1) && wait(b_in2 + st, (it / kStages) & 1) && wait(b_mine, it & 1);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(acc, col + (kk & 1) * 8 + (kk >> 1) * kCols, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
+                        tc::mma_f16_ts_if(one, acc, col + (kk & 1) * 8 + (kk >> 1) * kCols, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
                                        kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(bar((second ? B_QEMPTY : B_OEMPTY) + st));
+                    tc::mma_commit_if(one, bar((second ? B_QEMPTY : B_OEMPTY) + st));
                     if (i + 1 < nt) ok = scores(it + 1, true);
-                    else if (!second) tc::mbar_arrive(bar(b_other));
+                    else if (!second && one) tc::mbar_arrive(bar(b_other));
                 }
                 if (out) {
                     const int b_acc = second ? B_ACC + 1 : B_ACC;
-                    tc::mma_commit(bar(b_acc));
+                    tc::mma_commit_if(one, bar(b_acc));
                     if (!ok) tc::mbar_wait(bar(b_acc), stretch & 1, nullptr, 100000000ull);   // nothing runs on when the CTA leaves
                 }
             }

@@ -219,37 +219,40 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             }
         } else if (warp == kCompute / 32 + 1) {
             // ---------------- S and dP ------------------------------------
-            if (lane == 0) {
+            {
+                const uint32_t one = tc::elect_one();        // the lane that issues; all of the warp waits
                 constexpr uint32_t kIdescS = tc::idesc_f16(kTile, kTile, false);
                 const uint64_t dq0 = tc::smem_desc(sbase + L::kOffQ, 16, 1024);
                 const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, 16, 1024);
                 const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, 16, 1024);
                 const uint64_t dv0 = tc::smem_desc(sbase + L::kOffV, 16, 1024);
                 int done = -1;
-                bool ok = wait(B_QO, 0);
+                bool ok = __all_sync(0xffffffffu, wait(B_QO, 0));
                 for (int i = 0; ok && i < nt; ++i) {
                     const int it = it0 + i, ks = it % kK, vs = it % kV, sb = it & 1;
                     ok = wait(B_KFULL + ks, (it / kK) & 1);
                     ok = ok && (it < 1 || wait(B_SFREE, (it - 1) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColS, tc::desc_add(dq0, off), tc::desc_add(dk0, ks * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss_if(one, tmem + kColS, tc::desc_add(dq0, off), tc::desc_add(dk0, ks * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(B_S));
+                    tc::mma_commit_if(one, bar(B_S));
                     // (the buffer's last dS has been read)
                     ok = wait(B_VFULL + vs, (it / kV) & 1) && (it < 2 || wait(B_DQ + sb, ((it >> 1) - 1) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColP + sb * kTile, tc::desc_add(do0, off), tc::desc_add(dv0, vs * L::kTileBytes + off), kIdescS, kk > 0);
+                        tc::mma_f16_ss_if(one, tmem + kColP + sb * kTile, tc::desc_add(do0, off), tc::desc_add(dv0, vs * L::kTileBytes + off), kIdescS, kk > 0);
                     }
-                    tc::mma_commit(bar(B_DP + sb));
-                    tc::mma_commit(bar(B_VEMPTY + vs));
+                    tc::mma_commit_if(one, bar(B_DP + sb));
+                    tc::mma_commit_if(one, bar(B_VEMPTY + vs));
                     done = it;
                 }
                 if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
@@ -257,21 +260,23 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             }
         } else if (warp == kCompute / 32 + 2) {
             // ---------------- dQ --------------------------------------------
-            if (lane == 0) {
+            {
+                const uint32_t one = tc::elect_one();        // the lane that issues; all of the warp waits
                 constexpr uint32_t kIdescQ = tc::idesc_f16(kTile, D, true);
                 const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, kHalf, 1024);
                 int done = -1;
                 for (int i = 0; i < nt; ++i) {
                     const int it = it0 + i, ks = it % kK, sb = it & 1;
-                    if (!wait(B_DS + sb, (it >> 1) & 1) || !wait(B_KFULL + ks, (it / kK) & 1)) break;
+                    const bool ok = wait(B_DS + sb, (it >> 1) & 1) && wait(B_KFULL + ks, (it / kK) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_f16_ts(tmem + kColQ, tmem + kColP + sb * kTile + (kk & 1) * 8 + (kk >> 1) * kCols,
+                        tc::mma_f16_ts_if(one, tmem + kColQ, tmem + kColP + sb * kTile + (kk & 1) * 8 + (kk >> 1) * kCols,
                                        tc::desc_add(dk0, ks * L::kTileBytes + kk * 2048), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(bar(B_KEMPTY + ks));
-                    tc::mma_commit(bar(B_DQ + sb));
-                    if (i + 1 == nt) tc::mma_commit(bar(B_ACC));
+                    tc::mma_commit_if(one, bar(B_KEMPTY + ks));
+                    tc::mma_commit_if(one, bar(B_DQ + sb));
+                    if (i + 1 == nt) tc::mma_commit_if(one, bar(B_ACC));
                     done = it;
                 }
                 if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
