@@ -304,7 +304,8 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 bool ok = __all_sync(0xffffffffu, wait(B_KV, 0)) && scores(it0, second);   // (the first dV goes first)
                 for (int i = 0; ok && i < nt; ++i) {
                     const int it = it0 + i, st = it & (kStages - 1);
-                    ok = wait(b_ready, it & 1) && wait(b_in2 + st, (it / kStages) & 1) && wait(b_mine, it & 1);
+                    // what is there early first: the compute warps' arrival is then the last wait before the products
+                    ok = wait(b_mine, it & 1) && wait(b_in2 + st, (it / kStages) & 1) && wait(b_ready, it & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::tc_fence_after();
