@@ -12,26 +12,31 @@ namespace bwd {
 static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Costs in tiles of 128 x 128 of dq (1.2 us): a tile of dk and dv, a CTA's fixed part (tensor memory,
+// Costs in tiles of 128 x 128 of dq (1.1 us): a tile of dk and dv, a CTA's fixed part (tensor memory,
 // barriers, row statistics, pipeline fill, result), the launch that adds up pieces.
-constexpr double kKvTile = 1.5, kFixed = 4, kJoin = 2.5;
+constexpr double kKvTile = 1.5, kFixed = 6, kJoin = 2.5;
 // fp32 bytes that the adding up moves in a tile's time.
-constexpr double kJoinBytes = 7e6;
+constexpr double kJoinBytes = 9e6;
 
 // The CTAs of one launch: those of the kind whose CTAs take longer go out first, the others fill the
 // SMs.  So the launch ends when the longest CTA does, or when all SMs' work is done and about half a CTA of
 // the second kind later; a unit's tiles are cut into pieces (their sums added up by a further launch)
-// where that ends sooner.  16384 tokens, causal: no pieces, where whole waves of each kind by itself
-// wanted four; 512 tokens over 32768 keys: dq's 128 CTAs of 256 tiles first, dk and dv's 2048 of 16 after
-// them, where dq after them wanted seven pieces.
+// where that ends sooner.  Positions are taken to be those of a causal mask whose last token sees
+// all keys (what they hold is known on the device only): the share of tiles seen.
+//   16384 tokens, causal, 8 heads on 2: no pieces 1233 us, dk and dv in two 1273; on one KV head (128 CTAs
+//   of up to 1024 tiles) none 1642, two 1265; 8192 tokens on 2 none 428, two 369.
+//   512 tokens over 32768 keys: dq's 128 CTAs of 256 tiles first, dk and dv's 2048 of 16 after them 749 us,
+//   the other way round 769.  128 tokens over 4096 keys: none 57, dq in two 63.
+// Of 32 shapes (1 to 16384 tokens) the plan took the best pieces or came within 6 % of them, but for 16384 tokens
+// that all see 16384 keys, 8 heads on 2: none 2913, dk and dv in six 2548.  There dq's CTAs, beside a second
+// wave of dk's and dv's long ones, slow these down by half; why was not found.
 struct Plan {
     int kv_pieces, q_pieces;
     bool q_first;
 };
-static Plan plan_of(const Geo &g, int64_t units, int sms, bool kv, bool q, bool some)
+static Plan plan_of(const Geo &g, int64_t units, int sms, bool kv, bool q, double share)
 {
     static const int steps[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
-    const double share = some ? 0.75 : 1.0;                // positions: tiles seen, between half and all of them
     const double kv_bytes = 8.0 * units * g.KT * kTile * g.D, q_bytes = 4.0 * units * g.QT * kTile * g.D;
     Plan best{1, 1, false};
     double least = -1;
@@ -182,7 +187,9 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
         return SKV_OK;
     }
     // Pieces of a unit's tiles for grids that would leave SMs idle.
-    const Plan plan = plan_of(g, units, h->sm_count, dk != nullptr, dq != nullptr, q_pos != nullptr);
+    const double nq = static_cast<double>(shape->nq), keys = static_cast<double>(g.n);
+    const double share = !q_pos ? 1.0 : nq <= keys ? 1.0 - 0.5 * nq / keys : 0.5 * keys / nq;
+    const Plan plan = plan_of(g, units, h->sm_count, dk != nullptr, dq != nullptr, share);
     const int kv_pieces = plan.kv_pieces, q_pieces = plan.q_pieces;
     const bool kv_slot = dk && (kv_pieces > 1 || g.QT > kStretch), q_slot = dq && (q_pieces > 1 || g.KT > kStretch);
 
