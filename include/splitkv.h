@@ -618,7 +618,9 @@ typedef struct skv_cache_dst {
  * and v (as it is) straight into cache rows; what is stored is what
  * skv_kv_append stores for the same fp32 rows.  positions int32 [n]: the cache
  * position of each token (negative: nothing is written; one beyond the cache sets
- * bit 1 of the device status word); pos are the positions of the rotation. */
+ * bit 1 of the device status word); pos are the positions of the rotation.  Each token has a
+ * cache row of its own: of two with one position the row may hold parts of both.  q_out and
+ * the cache do not overlap the inputs or each other. */
 int skv_rope_append(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32_t H, int32_t Hk, int32_t x_type,
                     const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                     int64_t v_stride, const float *q_weight, const float *k_weight, const int32_t *pos,
@@ -630,7 +632,7 @@ int skv_rope_append(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32_t
  * and k, and dq_weight, dk_weight (fp32 [D]; NULL where the weight is) those of
  * the weights, summed over tokens and heads in an order that does not change from
  * run to run.  q and k are read only where a weight is given.  Padding tokens get
- * zeros and add nothing. */
+ * zeros and add nothing.  Results do not overlap the inputs or each other. */
 int skv_rope_backward(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32_t H, int32_t Hk, int32_t x_type,
                       const void *q, int64_t q_stride, const void *k, int64_t k_stride, const float *q_weight,
                       const float *k_weight, const int32_t *pos, int32_t g_type, const void *dq_out,
@@ -661,14 +663,17 @@ int skv_rope_backward(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32
  * dq, or dk and dv together, may be NULL: that part is not computed.  A row with
  * lse = -inf sees no key: its dq is zero, its q and d_o are not looked at.  Keys
  * that no token sees are not looked at either and get zeros.  Every result is
- * written whole; results do not change from run to run.
+ * written whole and overlaps neither an input nor another result.  Results do not
+ * change from run to run (a part by itself may differ in its last bits from the same
+ * part with the other: the work may be cut otherwise).
  *
  * Precision.  Products take fp16 operands and add in fp32: p, ds and an fp32 d_o enter
  * them rounded to fp16 (half a step is 2^-11 of the value), scaled by powers of two
  * so that neither long rows nor small gradients leave its range.  The scale of ds
  * goes by the largest |d_o| and |v| that a key tile (for dk) or the query row (for
  * dq) meets: tokens whose gradients are more than about 2^-20 of the largest one that
- * meets the same 128 keys lose bits in dk (for fp32 d_o in dv too).
+ * meets the same 128 keys lose bits in dk (for fp32 d_o in dv too).  In dq, what rounding
+ * ds takes from the part that a row's keys have in common is given back.
  * A NaN or an infinity in a row of q, d_o, k or v that is seen spreads over the
  * results of the 128 rows or keys that are computed with it.
  *

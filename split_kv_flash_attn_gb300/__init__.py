@@ -880,12 +880,20 @@ def attn_backward(h: Handle, q, k, v, o, lse, d_o, *, Hk, scale=None, kv_begin=0
         rows_ld = kv_rows.shape[-1]
         _need("kv_rows", kv_rows, torch.int32, (S, Hk, rows_ld) if per_head else (S, rows_ld), dev)
     if kv_end is None:
+        if kv_rows is None and k.shape[0] != v.shape[0]:
+            raise SplitKVError(1, f"k has {k.shape[0]} rows, v {v.shape[0]}, and no kv_end says how many are wanted")
         kv_end = rows_ld if kv_rows is not None else k.shape[0]
     kv_begin, kv_end = int(kv_begin), int(kv_end)
     n = max(0, kv_end - kv_begin)
     if kv_rows is None and (kv_end > k.shape[0] or kv_end > v.shape[0]):
         raise SplitKVError(1, f"kv_end {kv_end} lies beyond k's {k.shape[0]} or v's {v.shape[0]} rows")
     row = Hk * 2 * D
+    if k_row_bytes is None and k.numel() != k.shape[0] * Hk * D or v_row_bytes is None and v.numel() != v.shape[0] * Hk * D:
+        raise SplitKVError(1, f"k {list(k.shape)} or v {list(v.shape)}: rows of {Hk} heads of {D} are wanted")
+    if kv_rows is None and n:
+        for name, x, step in (("k", k, k_row_bytes), ("v", v, v_row_bytes)):
+            if step is not None and (kv_end - 1) * step + row > x.untyped_storage().nbytes() - 2 * x.storage_offset():
+                raise SplitKVError(1, f"kv_end {kv_end} lies beyond {name}'s memory at {step} bytes a row")
     sh = SkvShape(S, nq, H, Hk, D, 1.0 / math.sqrt(D) if scale is None else float(scale), F16, F16,
                   row if k_row_bytes is None else int(k_row_bytes), row if v_row_bytes is None else int(v_row_bytes))
     if g_dtype is None:

@@ -182,3 +182,39 @@ def test_python_checks():
         skv._token_rows("q", y[:, :4, :4], (2, 4), 128, torch.float16, -1)
     with pytest.raises(skv.SplitKVError):
         skv._token_rows("q", y[:, :, ::2], (2, 5), 128, torch.float16, -1)
+
+
+def test_python_checks_of_gradients(monkeypatch):
+    """What k and v must hold for the heads and the range that the call names."""
+    import torch
+    import split_kv_flash_attn_gb300 as skv
+    from split_kv_flash_attn_gb300 import _lib
+
+    class Handle:
+        device, _h, ptr = -1, None, None
+
+        def check(self, rc):
+            assert rc == 0
+
+    class Lib:
+        def skv_attn_backward(self, *a):
+            return 0
+
+    monkeypatch.setattr(_lib, "lib", lambda: Lib())
+    q = torch.zeros((1, 4, 8, 64), dtype=torch.float16)
+    kv = torch.zeros((10, 2, 64), dtype=torch.float16)
+    o, lse = torch.zeros((1, 4, 8, 64)), torch.zeros((1, 4, 8))
+
+    def call(k=kv, v=kv, Hk=2, **kw):
+        return skv.attn_backward(Handle(), q, k, v, o, lse, q, Hk=Hk, stream=0, need_dq=False, need_dkv=False, **kw)
+
+    wide = torch.zeros((10, 6, 64), dtype=torch.float16)
+    rows = torch.zeros((1, 7), dtype=torch.int32)
+    call(), call(kv_begin=3, kv_end=9), call(kv_rows=rows), call(wide[:, :2], wide[:, 2:4], k_row_bytes=768, v_row_bytes=768)
+    call(wide[:, 4:], wide[:, 2:4], k_row_bytes=768, v_row_bytes=768)            # ends with the storage
+    bad = [dict(Hk=8), dict(Hk=1), dict(Hk=4, kv_rows=rows), dict(v=kv[:, :1].contiguous()), dict(k=kv[:8]), dict(kv_end=11),
+           dict(k=wide[:, :2]), dict(k_row_bytes=272), dict(v_row_bytes=512), dict(k=wide[:, 4:], k_row_bytes=784)]
+    for kw in bad:
+        with pytest.raises(skv.SplitKVError) as e:
+            call(**kw)
+        assert e.value.status == 1, kw
