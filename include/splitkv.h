@@ -579,8 +579,8 @@ int skv_q8_evict(skv_handle *h, int32_t S, int32_t Hk, int64_t pages_per_list, c
  * packed projection.  Bases and strides are multiples of 16 bytes.  D is 64 or 128;
  * rot_dims is even and at most D, and a multiple of 8 unless interleaved.
  * pos int32 [n_axes][n]; a token whose position on the first axis is negative is
- * padding: its rows are not read, its results are zeros, and no cache row is
- * written for it.  axis NULL: every pair turns with axis 0; entries are in
+ * padding: what its rows hold does not matter, its results are zeros, and no cache
+ * row is written for it.  axis NULL: every pair turns with axis 0; entries are in
  * [0, n_axes) (others count as 0).  weights fp32 [D], 16-byte aligned; freq fp32,
  * axis int32 [rot_dims/2]; all device memory.
  * q or k may be left out (H or Hk 0).  The calls run on the handle's device,

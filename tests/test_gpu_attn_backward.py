@@ -309,6 +309,30 @@ def test_empty_range(skv, h):
     assert (dq == 0).all() and dk.shape == dv.shape == (0, 1, 64)
 
 
+@pytest.mark.parametrize("nq,n,H,Hk,D,causal", [
+    (2048, 2048, 1, 1, 64, True),            # both kinds of CTAs cut into pieces
+    (1500, 1500, 1, 1, 128, False),
+    (2100, 6000, 16, 1, 64, False),          # pieces of dk and dv longer than a stretch of 128 tiles
+    (1100, 34000, 4, 2, 64, True),           # pieces of dq longer than one
+])
+@pytest.mark.parametrize("g16", [True, False])
+def test_pieces(skv, h, nq, n, H, Hk, D, causal, g16):
+    import torch
+    q, k, v, d_o = _inputs(1, nq, n, H, Hk, D, seed=31)
+    pos, see = None, torch.ones((1, nq, n), dtype=torch.bool, device="cuda")
+    if causal:
+        pos = (n - nq + torch.arange(nq, device="cuda")).to(torch.int32).view(1, nq)
+        see = torch.arange(n, device="cuda").view(1, 1, n) <= pos.view(1, nq, 1)
+    o, lse = _forward(q, k[None], v[None], see)
+    want, bound = _want(q, k[None], v[None], see, o, lse, d_o)
+    kw = dict(Hk=Hk, q_pos=pos, g_dtype=torch.float16 if g16 else torch.float32)
+    got = skv.attn_backward(h, q, k, v, o, lse, d_o, **kw)
+    assert h.status() == 0
+    _check3(got, want, bound, "pieces")
+    again = skv.attn_backward(h, q, k, v, o, lse, d_o, **kw)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
 def test_against_differences(skv, h):
     """sum(o * w) + sum(lse * u) of the forward call, moved along random directions of q, k and v (fp32 o and lse: a
     difference over a step of 2^-4 is good to the step's square and to the call's 1e-5)."""
