@@ -23,10 +23,11 @@
 // and shuffles bring it those of its values.
 //
 // Bound by latency and instructions rather than by memory: sixteen warps an SM, a batch's chain of
-// sums and a root in each.  8192 tokens of 32 + 8 heads of 128, fp16, normed (168 MB): 32 us;
-// batches of half the size 36, three CTAs an SM (80 registers, spilled) 36, the ring of the
+// sums and a root in each.  8192 tokens of 32 + 8 heads of 128, fp16, normed (168 MB): 30.4 us, 5.5 TB/s;
+// a pass of a batch's rows after the other 32, all four passes side by side (spilled) 31.6; then also batches
+// of half the size 36, three CTAs an SM (80 registers, spilled) 36, the ring of the
 // gradients 35, a row's values consecutive in a lane and partners by shuffles 75.  Its gradients
-// (252 MB): 49 us and 3 for the weights' sums; batches in registers 60, a token a warp 83.
+// (252 MB): 49 us and 3 for the weights' sums; passes side by side 48, batches in registers 60, a token a warp 83.
 #include "internal.h"
 #include "kv_encode.cuh"
 
@@ -490,37 +491,65 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_kernel(const Args a)
         }
         const int h0 = (seg == 0 ? p.b : seg == 1 ? p.b - a.bq : p.b - a.bq - a.bk) * RB, heads = seg == 0 ? a.H : a.Hk;
         const int64_t o0 = static_cast<int64_t>(p.t) * heads * D;
+        // Step by step for U rows, so that their chains run side by side (rows that are none are zeros).
+        constexpr int U = IT < 2 ? IT : 2;
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            if (h0 + it * RPW >= heads) break;
-            const int hd = h0 + it * RPW + g;
-            float v[8];
-            to_f32<XT>(raw[it], v);
+        for (int u0 = 0; u0 < IT; u0 += U) {
+            float y[U][8];
             if (!CACHE || seg < 2) {
-                float y[8];
-                turn<INTER>(tr, v, y);
-                if (w) {
-                    float s0, s1;
+                float ss[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float v[8], s0, s1;
+                    to_f32<XT>(raw[u0 + u], v);
+                    turn<INTER>(tr, v, y[u]);
                     mul2(s0, s1, v[0], v[1], v[0], v[1]);
 #pragma unroll
                     for (int i = 2; i < 8; i += 2) fma2(s0, s1, v[i], v[i + 1], v[i], v[i + 1], s0, s1);
-                    const float rs = rsqrtf(row_sum<LPR>(s0 + s1) * (1.f / D) + a.eps);
-                    pairs([&](int i) { mul2(v[i], v[i + 1], y[i], y[i + 1], rs, rs); });
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = y[i];
+                    ss[u] = s0 + s1;
                 }
+                if (w) {
+#pragma unroll
+                    for (int o = LPR / 2; o; o >>= 1) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const float rs = rsqrtf(ss[u] * (1.f / D) + a.eps);
+                        pairs([&](int i) { mul2(y[u][i], y[u][i + 1], y[u][i], y[u][i + 1], rs, rs); });
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) to_f32<XT>(raw[u0 + u], y[u]);
             }
             if (pad) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[u][i] = 0.f;
+                }
             }
-            if constexpr (CACHE) {
-                if (seg == 2) put_cache<LPR, true>(a.vd, hd < heads ? at : -1, hd, l, plain, v, nullptr, a.status);
-                else if (seg == 1) put_cache<LPR, INTER>(a.kd, hd < heads ? at : -1, hd, l, turned, v, s_stage[INTER ? 0 : threadIdx.x >> 5], a.status);
-                else if (hd < heads) store_as(SKV_F16, a.q.out, o0 + hd * D, turned.a, turned.b, v);
+            auto store = [&](auto put) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int hd = h0 + (u0 + u) * RPW + g;
+                    put(hd, hd < heads, y[u]);
+                }
+            };
+            if (CACHE && seg == 2) {
+                store([&](int hd, bool in, float (&v)[8]) { put_cache<LPR, true>(a.vd, in ? at : -1, hd, l, plain, v, nullptr, a.status); });
+            } else if (CACHE && seg == 1) {
+                store([&](int hd, bool in, float (&v)[8]) {
+                    put_cache<LPR, INTER>(a.kd, in ? at : -1, hd, l, turned, v, s_stage[INTER ? 0 : threadIdx.x >> 5], a.status);
+                });
             } else {
-                if (hd < heads) store_as(a.o_type, seg == 0 ? a.q.out : a.k.out, o0 + hd * D, turned.a, turned.b, v);
+                void *out = seg == 0 ? a.q.out : a.k.out;
+                const int type = CACHE ? SKV_F16 : a.o_type;
+                if (type == SKV_F32) store([&](int hd, bool in, float (&v)[8]) { if (in) store_as(SKV_F32, out, o0 + hd * D, turned.a, turned.b, v); });
+                else if (type == SKV_F16) store([&](int hd, bool in, float (&v)[8]) { if (in) store_as(SKV_F16, out, o0 + hd * D, turned.a, turned.b, v); });
+                else store([&](int hd, bool in, float (&v)[8]) { if (in) store_as(SKV_BF16, out, o0 + hd * D, turned.a, turned.b, v); });
             }
         }
     }
