@@ -647,14 +647,16 @@ def _row_type(name, dtype):
 
 def _token_rows(name, x, lead, D, dtype, device):
     """Heads and token stride of rows [*lead, heads, D] whose heads stand side by side and whose tokens a fixed
-    stride apart (a part of a packed projection, say)."""
+    stride apart (a part of a packed projection, say), which holds a token's heads: broadcast or overlapping tokens are
+    refused."""
     shape, stride, k = x.shape, x.stride(), len(lead)
     ok = x.dtype is dtype and x.get_device() == device
-    if k == 1 and ok and len(shape) == 3 and shape[0] == lead[0] and shape[2] == D and stride[2] == 1 and stride[1] == D:
+    if (k == 1 and ok and len(shape) == 3 and shape[0] == lead[0] and shape[2] == D and stride[2] == 1 and stride[1] == D
+            and (stride[0] >= shape[1] * D or shape[0] <= 1)):
         return shape[1], stride[0]                            # the usual case, without the loop
     ok = (ok and len(shape) == k + 2 and shape[:k] == lead and shape[-1] == D
           and (stride[-1] == 1 and (stride[-2] == D or shape[-2] == 1) or x.numel() == 0))
-    step, want = 0, None
+    step = want = None                                        # None: no dimension has more than one token
     if ok:
         for i in range(k - 1, -1, -1):
             if shape[i] > 1:
@@ -666,10 +668,12 @@ def _token_rows(name, x, lead, D, dtype, device):
                     break
                 else:
                     want *= shape[i]
+        if step is not None and step < shape[-2] * D and x.numel():
+            ok = False
     if not ok:
         raise SplitKVError(1, f"{name}: want {dtype} [{', '.join(map(str, lead))}, heads, {D}] on device {device} with heads side by side "
                               f"and tokens a fixed stride apart, got {x.dtype} {list(shape)} of strides {list(stride)} on {x.device}")
-    return int(shape[-2]), int(step) if step else int(shape[-2]) * D
+    return int(shape[-2]), int(shape[-2]) * D if step is None else int(step)
 
 
 def _tokens(lead):
