@@ -749,24 +749,54 @@ def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dt
     return q_out, k_out
 
 
-def _cache_dst(name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes):
+def _region_rows(name, x, half, need, row_bytes, n_rows, device):
+    """Rows of `need` bytes, row_bytes apart, that a cache region's tensor holds (or n_rows of them): contiguous memory, or
+    rows with that pitch (a part of a packed cache, say).  half: fp16 rows."""
+    dtype, size = x.dtype, x.element_size()
+    if dtype.is_floating_point and not (half and size == 2 and dtype is _torch().float16):
+        raise SplitKVError(1, f"{name}: want {'fp16 or ' if half else ''}bytes, got {dtype}")
+    at = x.get_device()
+    if at >= 0 and at != device:
+        raise SplitKVError(1, f"{name}: on device {at}, other tensors on {device}")
+    held = x.numel() * size
+    if row_bytes < need:
+        raise SplitKVError(1, f"{name}: a row stride of {row_bytes} bytes, a row has {need}")
+    if x.is_contiguous():
+        n = held // row_bytes or int(held >= need)            # (one row needs no padding behind it)
+    else:
+        row = x[0]
+        if x.stride(0) * size != row_bytes or not row.is_contiguous() or row.numel() * size < need:
+            raise SplitKVError(1, f"{name}: {list(x.shape)} of strides {list(x.stride())} is not contiguous and holds no rows "
+                                  f"{row_bytes} bytes apart (rows of another pitch want their row bytes)")
+        n = x.shape[0]
+    if n_rows is None:
+        return n
+    if n_rows > n and (n_rows - 1) * row_bytes + need > x.untyped_storage().nbytes() - size * x.storage_offset():
+        raise SplitKVError(1, f"{name}: {n_rows} rows lie beyond its memory at {row_bytes} bytes a row")
+    return n_rows
+
+
+def _cache_dst(name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes, device):
     if type_ not in (F16, Q8_0, Q4_0):
-        raise SplitKVError(1, f"{name}: unknown element type {type_}")
+        raise SplitKVError(1, f"{name}_type: unknown element type {type_}")
+    need = Hk * segment_bytes(type_, D)
     if row_bytes is None:
-        row_bytes = Hk * segment_bytes(type_, D)
-    if n_rows0 is None:
-        n_rows0 = 0 if dst0 is None else dst0.numel() * dst0.element_size() // max(1, row_bytes)
-    if n_rows1 is None:
-        n_rows1 = 0 if dst1 is None else dst1.numel() * dst1.element_size() // max(1, row_bytes)
-    return SkvCacheDst(type_, row_bytes, None if dst0 is None else dst0.data_ptr(), n_rows0,
-                       None if dst1 is None else dst1.data_ptr(), n_rows1)
+        row_bytes = need
+    if dst0 is not None:
+        n_rows0 = _region_rows(name + "_dst0", dst0, type_ == F16, need, row_bytes, n_rows0, device)
+    if dst1 is not None:
+        n_rows1 = _region_rows(name + "_dst1", dst1, type_ == F16, need, row_bytes, n_rows1, device)
+    return SkvCacheDst(type_, row_bytes, None if dst0 is None else dst0.data_ptr(), n_rows0 or 0,
+                       None if dst1 is None else dst1.data_ptr(), n_rows1 or 0)
 
 
 def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, k_dst1=None, v_dst1=None, *,
                 q_weight=None, k_weight=None, k_type=F16, v_type=F16, n_rows0=None, n_rows1=None, k_row_bytes=None,
                 v_row_bytes=None, q_out=None, stream=None):
     """skv_rope_append: norm and rotation of q [..., H, D] and k [..., Hk, D]; q is returned as fp16 rows, k and
-    v [..., Hk, D] go to the cache rows `positions` (int32 [...]) of two-region caches as for kv_append."""
+    v [..., Hk, D] go to the cache rows `positions` (int32 [...]) of two-region caches as for kv_append.  A region is a
+    contiguous tensor (fp16 rows or bytes), or one whose rows are k_row_bytes, v_row_bytes apart (a part of a packed
+    cache: its pitch), on the device or page-locked."""
     torch = _torch()
     if k is None or v is None:
         raise SplitKVError(1, "k and v are wanted")
@@ -783,8 +813,8 @@ def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, 
         q_out = _new(torch, (*lead, H, D), torch.float16, q, stream, dev)
     else:
         _need("q_out", q_out, torch.float16, (*lead, H, D), dev)
-    kd = _cache_dst("k_type", k_type, Hk, D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes)
-    vd = _cache_dst("v_type", v_type, Hk, D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes)
+    kd = _cache_dst("k", k_type, Hk, D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes, dev)
+    vd = _cache_dst("v", v_type, Hk, D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes, dev)
     rc = _lib.lib().skv_rope_append(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                                     wq, wk, pp, at, _ptr(q_out), ctypes.byref(kd), ctypes.byref(vd), st)
     if rc:

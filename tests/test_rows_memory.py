@@ -90,3 +90,84 @@ def test_token_strides_that_hold_their_heads():
     assert rows("q", x[:, :1], (5,), 128, F16, -1) == (1, 9 * 128)
     assert rows("q", x[:0], (0,), 128, F16, -1)[0] == 9
     assert rows("q", x[:, :0], (5,), 128, F16, -1)[0] == 0
+
+
+def _append(lib, Hk=2, D=64, n=3, **kw):
+    """rope_append of n tokens; the recorded cache regions (type, row bytes, address and rows of both) of k and v."""
+    x = torch.zeros((n, Hk, D), dtype=F16)
+    args = dict(k_dst0=None, v_dst0=None, stream=0)
+    args.update(kw)
+    at = torch.zeros((n,), dtype=I32)
+    skv.rope_append(Handle(), skv.Rope(D, torch.zeros(D // 2)), None, x, x, at, at, **args)
+    name, a = lib.calls[-1]
+    assert name == "skv_rope_append"
+    return [tuple(getattr(d._obj, f) for f in ("type", "row_bytes", "dst0", "n_rows0", "dst1", "n_rows1")) for d in (a[17], a[18])]
+
+
+def test_cache_regions_as_tensors_hold_them(lib):
+    Hk, D, row = 2, 64, 256
+    kv = torch.zeros((10, 2, Hk, D), dtype=F16)
+    K, V = kv[:, 0], kv[:, 1]
+    flat = torch.zeros(10 * row, dtype=U8)
+    # contiguous regions of any shape, their rows counted by bytes
+    k, v = _append(lib, k_dst0=flat, v_dst0=torch.zeros((7, Hk, D), dtype=F16), k_dst1=flat[:5 * row])
+    assert k == (skv.F16, row, flat.data_ptr(), 10, flat.data_ptr(), 5) and v[1] == row and v[3:] == (7, None, 0)
+    # parts of a packed cache, with their pitch: every row of them
+    k, v = _append(lib, k_dst0=K, v_dst0=V, k_row_bytes=2 * row, v_row_bytes=2 * row)
+    assert k == (skv.F16, 2 * row, K.data_ptr(), 10, None, 0) and v == (skv.F16, 2 * row, V.data_ptr(), 10, None, 0)
+    assert V.data_ptr() == K.data_ptr() + row
+    # every other row, one row, none
+    assert _append(lib, k_dst0=K[::2], v_dst0=V[:5], k_row_bytes=4 * row, v_row_bytes=2 * row)[0][3] == 5
+    assert _append(lib, k_dst0=K[:1], v_dst0=V[:0], k_row_bytes=2 * row, v_row_bytes=2 * row)[1][3] == 0
+    # an explicit count up to the memory's end, whose last row needs no padding behind it
+    assert _append(lib, k_dst0=K, v_dst0=V, k_row_bytes=2 * row, v_row_bytes=2 * row, n_rows0=10)[1][3] == 10
+    assert _append(lib, k_dst0=flat, v_dst0=flat, n_rows0=4)[0][3] == 4
+    q8, q4 = (torch.zeros((9, Hk * skv.segment_bytes(t, D)), dtype=U8) for t in (skv.Q8_0, skv.Q4_0))
+    k, v = _append(lib, k_dst0=q8, v_dst0=q4, k_type=skv.Q8_0, v_type=skv.Q4_0)
+    assert k[:2] == (skv.Q8_0, 136) and v[:2] == (skv.Q4_0, 72) and k[3] == v[3] == 9
+
+
+def test_cache_regions_that_would_be_written_wrongly_are_refused(lib):
+    Hk, D, row = 2, 64, 256
+    kv = torch.zeros((10, 2, Hk, D), dtype=F16)
+    K, V, good = kv[:, 0], kv[:, 1], torch.zeros((10, Hk, D), dtype=F16)
+    flat = torch.zeros(10 * row, dtype=U8)
+    bad = [
+        dict(k_dst0=K, v_dst0=good), dict(k_dst0=good, v_dst0=V),                    # a pitch that the call does not know of
+        dict(k_dst0=K, v_dst0=good, n_rows0=10),
+        dict(k_dst0=good, v_dst0=good, k_dst1=K), dict(k_dst0=good, v_dst0=good, v_dst1=V),
+        dict(k_dst0=K, v_dst0=good, k_row_bytes=row), dict(k_dst0=K, v_dst0=good, k_row_bytes=3 * row),      # another one than the tensor's
+        dict(k_dst0=good.transpose(0, 1), v_dst0=good, k_row_bytes=row), dict(k_dst0=good.transpose(1, 2), v_dst0=good, k_row_bytes=row),
+        dict(k_dst0=good[:, :, :32], v_dst0=good, k_row_bytes=row),
+        dict(k_dst0=K[:, :1], v_dst0=good, k_row_bytes=2 * row),                     # rows of fewer heads
+        dict(k_dst0=torch.zeros((1, Hk, D), dtype=F16).expand(10, Hk, D), v_dst0=good, k_row_bytes=row),     # one row for all
+        dict(k_dst0=torch.zeros((1, Hk, D), dtype=F16).expand(10, Hk, D), v_dst0=good, k_row_bytes=0),
+        dict(k_dst0=good, v_dst0=good, n_rows0=11), dict(k_dst0=flat, v_dst0=good, k_row_bytes=2 * row, n_rows0=6),    # more rows than memory
+        dict(k_dst0=K, v_dst0=V, k_row_bytes=2 * row, v_row_bytes=2 * row, n_rows0=11),
+        dict(k_dst0=good, v_dst0=good, k_dst1=good, n_rows1=11),
+        dict(k_dst0=good, v_dst0=good, k_row_bytes=128), dict(k_dst0=good, v_dst0=good, k_row_bytes=-row),   # rows that hold no Hk heads
+        dict(k_dst0=good.float(), v_dst0=good), dict(k_dst0=good, v_dst0=good.bfloat16()),                   # values of another type
+        dict(k_dst0=good, v_dst0=good, k_type=skv.Q8_0), dict(k_dst0=good, v_dst0=good, k_type=7),
+    ]
+    for kw in bad:
+        refused(_append, lib, **kw)
+    assert not lib.calls
+
+
+def test_cache_regions_on_another_device_are_refused(lib):
+    """A region is the handle's device's or (page-locked) host memory."""
+    class Far:
+        """A tensor of another device, as far as the check looks."""
+
+        def __init__(self, x):
+            self.x = x
+
+        def get_device(self):
+            return 5
+
+        def __getattr__(self, name):
+            return getattr(self.x, name)
+
+    good = torch.zeros((10, 2, 64), dtype=F16)
+    for kw in (dict(k_dst0=Far(good), v_dst0=good), dict(k_dst0=good, v_dst0=good, v_dst1=Far(good))):
+        assert "device" in refused(_append, lib, **kw)
