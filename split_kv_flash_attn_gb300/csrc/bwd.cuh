@@ -97,6 +97,9 @@ struct MainArgs {
     int *status;
 };
 
+// Limit of the waits for what is in flight when a CTA gives up.
+constexpr uint64_t kDrainNs = 100000000ull;
+
 // Wait for a phase of an mbarrier: gives up after two seconds, or when another wait of
 // the kernel has (bit 0 of the status word; other bits say other things).
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, const int *status)

@@ -25,7 +25,9 @@
 // S -> P -> dV, S and dP -> dS -> dK, dP: each half of it is about as long as the two products that run beside it.
 // Halves of a tile (products of 64 columns), which would shorten the links, took 8 % more.
 //
-// Every mbarrier wait is bounded, as in the prefill kernel.
+// Every mbarrier wait is bounded, as in the prefill kernel.  Whoever gives up, and when: at the end of a stretch all loads
+// asked for and all products issued are waited for before the CTA leaves, by waits that look at no status word; what they
+// wait for ends by itself.
 #pragma once
 
 #include "bwd.cuh"
@@ -71,7 +73,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
     auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_count, s_lim, s_eN, s_eD, s_c, s_ew;
-    __shared__ int s_need[kStages];
+    __shared__ int s_need[kStages], s_loads[2];
     uint32_t *bits = reinterpret_cast<uint32_t *>(sm + L::kOffBits);
     int *s_list = reinterpret_cast<int *>(sm + L::kOffList);       // a stretch's query tiles
 
@@ -201,7 +203,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
         return a.slot + (static_cast<int64_t>(piece) * 2 + which) * (static_cast<int64_t>(g.groups) * g.n * g.Hk * D) + out_at();
     };
 
-    if (o_lo >= o_hi && tid == kCompute) wait(B_KV, 0);      // the loads land before the CTA leaves
+    if (o_lo >= o_hi && tid == kCompute) tc::mbar_wait(bar(B_KV), 0, nullptr, kDrainNs);   // the loads land before the CTA leaves
     if (o_lo >= o_hi && warp < kCompute / 32 && key < g.n) {             // nobody sees these keys
         float z[NC];
 #pragma unroll
@@ -267,14 +269,8 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                                         static_cast<int>(t.t0), group, bar(B_OLAND + st));
                     ++o_out;
                 }
-                if (*reinterpret_cast<volatile int *>(&s_abort)) {
-                    // every load must land before the CTA exits
-                    tc::mbar_wait(bar(B_KV), 0, nullptr, 100000000ull);
-                    for (int i = max(0, q_out - kStages); i < q_out; ++i)
-                        tc::mbar_wait(bar(B_QLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
-                    for (int i = max(0, o_out - kStages); i < o_out; ++i)
-                        tc::mbar_wait(bar(B_OLAND + ((it0 + i) & (kStages - 1))), ((it0 + i) / kStages) & 1, nullptr, 100000000ull);
-                }
+                s_loads[0] = it0 + q_out;
+                s_loads[1] = it0 + o_out;
             }
         } else if (warp == kCompute / 32 + 1 || warp == kCompute / 32 + 2) {
             // ---------------- products: dV(j), S(j+1), and dK(j), dP(j+1) ----
@@ -291,7 +287,6 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 const int b_in = second ? B_OFULL : B_QFULL, b_in2 = second ? B_QFULL : B_OFULL;
                 const int b_out = second ? B_DP : B_S, b_ready = second ? B_DS : B_P;
                 const int b_mine = second ? B_TURN : B_TURN + 1, b_other = second ? B_TURN + 1 : B_TURN;
-                bool out = false;                            // something was issued
                 auto scores = [&](int it, bool pass) {
                     const int st = it & (kStages - 1);
                     if (!__all_sync(0xffffffffu, wait(b_in + st, (it / kStages) & 1))) return false;
@@ -304,7 +299,6 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     }
                     tc::mma_commit_if(one, bar(b_out));
                     if (second) tc::mma_commit_if(one, bar(B_OEMPTY + st));
-                    out = true;
                     return true;
                 };
                 bool ok = __all_sync(0xffffffffu, wait(B_KV, 0)) && scores(it0, second);   // (the first dV goes first)
@@ -323,11 +317,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     if (i + 1 < nt) ok = scores(it + 1, true);
                     else if (!second && one) tc::mbar_arrive(bar(b_other));
                 }
-                if (out) {
-                    const int b_acc = second ? B_ACC + 1 : B_ACC;
-                    tc::mma_commit_if(one, bar(b_acc));
-                    if (!ok) tc::mbar_wait(bar(b_acc), stretch & 1, nullptr, 100000000ull);   // nothing runs on when the CTA leaves
-                }
+                tc::mma_commit_if(one, bar(second ? B_ACC + 1 : B_ACC));
             }
         } else if (warp == kCompute / 32 + 3) {
             // ---------------- each tile as it has landed --------------------
@@ -488,8 +478,17 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             }
         }
         __syncwarp();
-        __syncthreads();
-        if (s_abort) break;
+        if (__syncthreads_or(s_abort)) {                     // (all of the CTA or none) nothing runs on when it leaves
+            if (tid == kCompute) {
+                tc::mbar_wait(bar(B_KV), 0, nullptr, kDrainNs);
+                for (int i = max(0, s_loads[0] - kStages); i < s_loads[0]; ++i)
+                    tc::mbar_wait(bar(B_QLAND + (i & (kStages - 1))), (i / kStages) & 1, nullptr, kDrainNs);
+                for (int i = max(0, s_loads[1] - kStages); i < s_loads[1]; ++i)
+                    tc::mbar_wait(bar(B_OLAND + (i & (kStages - 1))), (i / kStages) & 1, nullptr, kDrainNs);
+            }
+            if (tid == kCompute + 32 || tid == kCompute + 64) tc::mbar_wait(bar(B_ACC + (warp - kCompute / 32 - 1)), stretch & 1, nullptr, kDrainNs);
+            break;
+        }
         it0 += nt;
     }
     tc::tc_fence_before();

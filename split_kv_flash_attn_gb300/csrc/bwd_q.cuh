@@ -21,6 +21,8 @@
 // and limit are registers), 16 TMA, 17 issues S and dP, 18 issues dQ, 19 looks each K tile
 // over: absent keys of lists, and rows behind the last key that any row sees, which
 // hold anything, are cleared.
+//
+// Every wait is bounded; a CTA that gives up waits for its loads and products as bwd_kv.cuh says.
 #pragma once
 
 #include "bwd.cuh"
@@ -46,7 +48,7 @@ static_assert(Lay<128>::kBytes <= 227 * 1024 - 128, "shared memory per CTA");
 
 enum { B_QO, B_KLAND, B_KFULL = B_KLAND + kK, B_KEMPTY = B_KFULL + kK, B_VFULL = B_KEMPTY + kK,
        B_VEMPTY = B_VFULL + kV, B_DP = B_VEMPTY + kV, B_DS = B_DP + 2, B_DQ = B_DS + 2, B_S = B_DQ + 2, B_SFREE,
-       B_ACC, B_COUNT };
+       B_ACC, B_END, B_COUNT = B_END + 2 };
 static_assert(B_COUNT * 8 <= 256, "barrier area");
 
 constexpr int kColS = 0, kColP = 128, kColQ = 384;
@@ -60,7 +62,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
     const uint32_t sbase = smem_addr(sm);
     auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_ew, s_last;
+    __shared__ int s_abort, s_ew, s_last, s_loads[2];
     __shared__ float s_mean[D];                              // mean of the first keys
     __shared__ float s_sum[2][kTile];                        // its parts; what rounding took from dS, by halves
     __shared__ uint32_t s_here[kK][4];                       // keys of a tile that are there
@@ -106,6 +108,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
         tc::mbar_init(bar(B_S), 1);
         tc::mbar_init(bar(B_SFREE), kCompute);
         tc::mbar_init(bar(B_ACC), 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(bar(B_END + i), 1);   // used by a CTA that gives up
         tc::fence_barrier_init();
         // the rows, while the keys' exponents are looked through
         tc::mbar_expect_tx(bar(B_QO), 2u * box_rows * D * 2);
@@ -177,7 +180,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
         return a.slot + piece * (static_cast<int64_t>(g.groups) * g.T * g.H * D) + row * D + part * NC;
     };
 
-    if (j_lo >= j_hi && tid == kCompute) wait(B_QO, 0);      // the loads land before the CTA leaves
+    if (j_lo >= j_hi && tid == kCompute) tc::mbar_wait(bar(B_QO), 0, nullptr, kDrainNs);   // the loads land before the CTA leaves
     if (j_lo >= j_hi && warp < kCompute / 32) {                          // no keys
         const int64_t row = q_row(g, t, m);
         float z[NC];
@@ -210,13 +213,8 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                         tc::tma_load_3d(sbase + L::kOffV + vs * L::kTileBytes + b * kHalf, &tv, hk * D + 64 * b, y, group, bar(B_VFULL + vs));
                     ++v_out;
                 }
-                if (*reinterpret_cast<volatile int *>(&s_abort)) {
-                    tc::mbar_wait(bar(B_QO), 0, nullptr, 100000000ull);
-                    for (int i = max(0, k_out - kK); i < k_out; ++i)
-                        tc::mbar_wait(bar(B_KLAND + (it0 + i) % kK), ((it0 + i) / kK) & 1, nullptr, 100000000ull);
-                    for (int i = max(0, v_out - kV); i < v_out; ++i)
-                        tc::mbar_wait(bar(B_VFULL + (it0 + i) % kV), ((it0 + i) / kV) & 1, nullptr, 100000000ull);
-                }
+                s_loads[0] = it0 + k_out;
+                s_loads[1] = it0 + v_out;
             }
         } else if (warp == kCompute / 32 + 1) {
             // ---------------- S and dP ------------------------------------
@@ -227,7 +225,6 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 const uint64_t do0 = tc::smem_desc(sbase + L::kOffO, 16, 1024);
                 const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, 16, 1024);
                 const uint64_t dv0 = tc::smem_desc(sbase + L::kOffV, 16, 1024);
-                int done = -1;
                 bool ok = __all_sync(0xffffffffu, wait(B_QO, 0));
                 for (int i = 0; ok && i < nt; ++i) {
                     const int it = it0 + i, ks = it % kK, vs = it % kV, sb = it & 1;
@@ -254,10 +251,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     }
                     tc::mma_commit_if(one, bar(B_DP + sb));
                     tc::mma_commit_if(one, bar(B_VEMPTY + vs));
-                    done = it;
                 }
-                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
-                    tc::mbar_wait(bar(B_DP + (done & 1)), (done >> 1) & 1, nullptr, 100000000ull);
             }
         } else if (warp == kCompute / 32 + 2) {
             // ---------------- dQ --------------------------------------------
@@ -265,7 +259,6 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 const uint32_t one = tc::elect_one();        // the lane that issues; all of the warp waits
                 constexpr uint32_t kIdescQ = tc::idesc_f16(kTile, D, true);
                 const uint64_t dk0 = tc::smem_desc(sbase + L::kOffK, kHalf, 1024);
-                int done = -1;
                 for (int i = 0; i < nt; ++i) {
                     const int it = it0 + i, ks = it % kK, sb = it & 1;
                     const bool ok = wait(B_DS + sb, (it >> 1) & 1) && wait(B_KFULL + ks, (it / kK) & 1);
@@ -278,10 +271,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     tc::mma_commit_if(one, bar(B_KEMPTY + ks));
                     tc::mma_commit_if(one, bar(B_DQ + sb));
                     if (i + 1 == nt) tc::mma_commit_if(one, bar(B_ACC));
-                    done = it;
                 }
-                if (*reinterpret_cast<volatile int *>(&s_abort) && done >= 0)
-                    tc::mbar_wait(bar(B_DQ + (done & 1)), (done >> 1) & 1, nullptr, 100000000ull);
             }
         } else if (warp == kCompute / 32 + 3) {
             // ---------------- each K tile as it has landed -------------------
@@ -430,9 +420,21 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             }
         }
         __syncwarp();
-        __syncthreads();
+        const bool gave_up = __syncthreads_or(s_abort);      // all of the CTA or none
         tc::tc_fence_after();
-        if (s_abort) break;
+        if (gave_up) {                                       // nothing runs on when it leaves
+            if (tid == kCompute) {
+                tc::mbar_wait(bar(B_QO), 0, nullptr, kDrainNs);
+                for (int i = max(0, s_loads[0] - kK); i < s_loads[0]; ++i) tc::mbar_wait(bar(B_KLAND + i % kK), (i / kK) & 1, nullptr, kDrainNs);
+                for (int i = max(0, s_loads[1] - kV); i < s_loads[1]; ++i) tc::mbar_wait(bar(B_VFULL + i % kV), (i / kV) & 1, nullptr, kDrainNs);
+            }
+            if (warp == kCompute / 32 + 1 || warp == kCompute / 32 + 2) {
+                // (the thread that issued, the same one as there; its commit covers all its products)
+                tc::mma_commit_if(tc::elect_one(), bar(B_END + warp - kCompute / 32 - 1));
+                tc::mbar_wait(bar(B_END + warp - kCompute / 32 - 1), 0, nullptr, kDrainNs);
+            }
+            break;
+        }
         it0 += nt;
     }
     tc::tc_fence_before();
