@@ -51,9 +51,10 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 // Wait for the phase with the given parity to complete.  Gives up (returns
-// false) after `budget_ns` of wall-clock time, or as soon as *abort_flag is
-// non-zero (another CTA already gave up), so a broken pipeline cannot hold
-// the GPU.
+// false) after `budget_ns` of wall-clock time, or as soon as bit 0 of
+// *abort_flag is set (another CTA already gave up), so a broken pipeline cannot
+// hold the GPU.  The status word's other bits say other things (a row beyond its
+// cache, a bad page) and end no wait.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag,
                                           uint64_t budget_ns = 2000000000ull)
 {
@@ -61,7 +62,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
     for (uint32_t i = 0;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 255u) == 0) {
-            if (abort_flag && *abort_flag) return false;
+            if (abort_flag && (*abort_flag & 1)) return false;
             const uint64_t t = globaltimer_ns();
             if (i == 0) t0 = t;
             else if (t - t0 > budget_ns) return false;
