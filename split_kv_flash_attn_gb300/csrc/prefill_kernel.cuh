@@ -443,11 +443,9 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
                     tc::tma_load_2d(sbase + off + b * kTileBytes + kHalfTile, map, x + 64, y, bar(b_full + b));
                     ++issued;
                 }
-                if (*reinterpret_cast<volatile int *>(&s_abort)) {
-                    // drain: every issued load must land before the CTA exits
-                    for (int j = (issued > 2 ? issued - 2 : 0); j < issued; ++j)
-                        tc::mbar_wait(bar(b_full + (j & 1)), (j >> 1) & 1, nullptr, 100000000ull);
-                }
+                // every issued load lands before the CTA exits, whoever gives up, and when
+                for (int j = (issued > 2 ? issued - 2 : 0); j < issued; ++j)
+                    tc::mbar_wait(bar(b_full + (j & 1)), (j >> 1) & 1, nullptr, 100000000ull);
             }
         } else if constexpr (MODE == 2) {
             // ---------------- fp16 row lists: two K warps, two V warps -------
@@ -655,8 +653,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
         // PV MMAs, so that PV of one tile and S of a later one go out side by
         // side (a thread's issue of eight MMAs takes about as long as the
         // tensor core runs them).  MODE 1 and 2: one thread issues S of tile
-        // jj, then PV of tile jj-1.  Each issuer drains its own MMAs on abort:
-        // a commit covers every MMA its thread issued before it.
+        // jj, then PV of tile jj-1.  Each issuer waits for its own MMAs, since another
+        // warp may give up later: a commit covers every MMA its thread issued before it.
         if (lane == 0 && n_tiles > 0) {
             // operand descriptors of the first K and V slots; the rest are offsets
             const uint64_t dk0 = tc::smem_desc(sbase + kOffK, 16, 1024);
@@ -769,8 +767,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
                     }
                 }
             }
-            if (*reinterpret_cast<volatile int *>(&s_abort) && last_bar >= 0)
-                tc::mbar_wait(bar(last_bar), last_par, nullptr, 100000000ull);
+            if (last_bar >= 0) tc::mbar_wait(bar(last_bar), last_par, nullptr, 100000000ull);
         }
     } else {
         // ---------------- softmax warps (two threads per query row) -----------

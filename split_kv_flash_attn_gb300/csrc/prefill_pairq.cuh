@@ -267,10 +267,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     }
                 }
             }
-            if (*reinterpret_cast<volatile int *>(&s_abort)) {
-                // drain issued MMAs: the last commit covers every MMA issued before it
-                if (last_bar >= 0) tc::mbar_wait(bar(last_bar), last_par, nullptr, 100000000ull);
-            } else {
+            // issued MMAs, whoever gives up, and when: the last commit covers every MMA issued before it
+            if (last_bar >= 0) tc::mbar_wait(bar(last_bar), last_par, nullptr, 100000000ull);
+            if (!*reinterpret_cast<volatile int *>(&s_abort)) {
                 // no producer waits for the last commits on the stages' free
                 // barriers; they are awaited here, so that none is in flight at exit
                 wait(QB_KEMPTY, (n_tiles - 1) & 1);
