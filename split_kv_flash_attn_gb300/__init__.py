@@ -683,10 +683,16 @@ def _tokens(lead):
     return n
 
 
-def _positions(torch, name, pos, want, device):
-    if pos.dtype is not torch.int32 or pos.get_device() != device or not pos.is_contiguous() or pos.numel() != want:
-        raise SplitKVError(1, f"{name}: want contiguous int32 of {want} positions on device {device}, "
-                              f"got {pos.dtype} {list(pos.shape)} on {pos.device}")
+def _positions(name, pos, axes, lead, n, device):
+    """Pointer of positions of n tokens: int32 [axes, *lead] or [axes, n]; for one axis (axes 1, or 0: no axis of its own) also
+    without it."""
+    shape = pos.shape
+    rest = shape[1:] if axes and len(shape) and shape[0] == axes else None
+    if not (pos.dtype is _torch().int32 and pos.get_device() == device and pos.is_contiguous()
+            and (rest is not None and (rest == lead or rest == (n,)) or axes <= 1 and (shape == lead or shape == (n,)))):
+        want = ", ".join(map(str, (axes, *lead) if axes > 1 else lead))
+        raise SplitKVError(1, f"{name}: want contiguous int32 [{want}] (positions) on device {device}, got "
+                              f"{'' if pos.is_contiguous() else 'non-contiguous '}{pos.dtype} {list(shape)} on {pos.device}")
     return pos.data_ptr()
 
 
@@ -716,13 +722,14 @@ def _rope_inputs(torch, h, spec, q, k, pos, stream):
     H, qs = _token_rows("q", q, lead, D, dtype, dev) if q is not None else (0, 0)
     Hk, ks = _token_rows("k", k, lead, D, dtype, dev) if k is not None else (0, 0)
     n = lead[0] if len(lead) == 1 else _tokens(lead)
-    return st, lead, n, H, qs, Hk, ks, xt, _positions(torch, "pos", pos, n * spec.n_axes, dev)
+    return st, lead, n, H, qs, Hk, ks, xt, _positions("pos", pos, spec.n_axes, lead, n, dev)
 
 
 def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dtype=None, q_out=None, k_out=None,
          stream=None):
     """skv_rope: norm (where a weight fp32 [D] is given) and rotation of q [..., H, D] and k [..., Hk, D]
-    (fp32, fp16 or bf16; either may be None); pos int32 [n_axes, ...] (without the axis for one).
+    (fp32, fp16 or bf16; either may be None); pos int32 [n_axes, ...] or, tokens in one line, [n_axes, n] (without the
+    axis for one).
     Results are fp16 unless o_dtype (or a given q_out, k_out) says otherwise."""
     torch = _torch()
     st, lead, n, H, qs, Hk, ks, xt, pp = _rope_inputs(torch, h, spec, q, k, pos, stream)
@@ -806,7 +813,7 @@ def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, 
     if Hv != Hk:
         raise SplitKVError(1, f"v has {Hv} heads, k {Hk}")
     wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
-    at = _positions(torch, "positions", positions, n, dev)
+    at = _positions("positions", positions, 0, lead, n, dev)
     if q is None:
         q_out = None
     elif q_out is None:
@@ -836,7 +843,7 @@ def rope_backward(h: Handle, spec: Rope, dq_out, dk_out, pos, *, q=None, k=None,
     g_dtype = some.dtype
     gt = _row_type("dq_out" if some is dq_out else "dk_out", g_dtype)
     n = lead[0] if len(lead) == 1 else _tokens(lead)
-    pp = _positions(torch, "pos", pos, n * spec.n_axes, dev)
+    pp = _positions("pos", pos, spec.n_axes, lead, n, dev)
     wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
     if x_dtype is None:
         x_dtype = next((x.dtype for x in (q, k, dq, dk) if x is not None), g_dtype)

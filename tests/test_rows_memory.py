@@ -171,3 +171,33 @@ def test_cache_regions_on_another_device_are_refused(lib):
     good = torch.zeros((10, 2, 64), dtype=F16)
     for kw in (dict(k_dst0=Far(good), v_dst0=good), dict(k_dst0=good, v_dst0=good, v_dst1=Far(good))):
         assert "device" in refused(_append, lib, **kw)
+
+
+def test_positions_by_shape(lib):
+    """[n_axes, tokens], tokens as the rows have them or in one line, without the axis where there is one."""
+    x = torch.zeros((6, 4, 2, 64), dtype=F16)
+    y, f = torch.zeros_like(x), torch.zeros(32)
+    one, three = skv.Rope(64, f), skv.Rope(64, f, axis=torch.arange(32, dtype=I32) % 3)
+    K = torch.zeros((50, 2, 64), dtype=F16)
+
+    def calls(spec, pos, at=torch.zeros((6, 4), dtype=I32)):
+        return [lambda: skv.rope(Handle(), spec, x, x, pos, q_out=y, k_out=y, stream=0),
+                lambda: skv.rope_append(Handle(), spec, x, x, x, pos, at, K, K, q_out=y, stream=0),
+                lambda: skv.rope_backward(Handle(), spec, x, x, pos, dq=y, dk=y, stream=0)]
+
+    zeros = lambda *s: torch.zeros(s, dtype=I32)
+    for spec, shapes in ((one, [(6, 4), (24,), (1, 6, 4), (1, 24)]), (three, [(3, 6, 4), (3, 24)])):
+        for s in shapes:
+            for call in calls(spec, zeros(*s)):
+                call()
+    n = len(lib.calls)
+    for spec, shapes in ((one, [(4, 6), (24, 1), (6, 4, 1), (2, 12), (1, 4, 6), (6, 1, 4)]),
+                         (three, [(6, 4, 3), (24, 3), (72,), (3, 4, 6), (6, 3, 4), (1, 72), (3, 1, 24)])):
+        for s in shapes:
+            for call in calls(spec, zeros(*s)):
+                assert "positions" in refused(call)
+    # cache rows: tokens as the rows have them, or in one line
+    for s in ((4, 6), (1, 24), (1, 6, 4), (24, 1), (12, 2)):
+        assert "positions" in refused(calls(one, zeros(6, 4), zeros(*s))[1])
+    calls(one, zeros(6, 4), zeros(24))[1]()
+    assert len(lib.calls) == n + 1
