@@ -576,7 +576,8 @@ int skv_q8_evict(skv_handle *h, int32_t S, int32_t Hk, int64_t pages_per_list, c
  *
  * x_type, o_type: SKV_F32, SKV_F16 or SKV_BF16.  Token t's heads stand side by side,
  * [heads][D], `stride` elements after token t-1's: q, k and v may be parts of one
- * packed projection.  Bases and strides are multiples of 16 bytes.  D is 64 or 128;
+ * packed projection.  Bases and strides are multiples of 16 bytes, strides hold a token's
+ * heads.  n is below 2^31, H and Hk at most 65535.  D is 64 or 128;
  * rot_dims is even and at most D, and a multiple of 8 unless interleaved.
  * pos int32 [n_axes][n]; a token whose position on the first axis is negative is
  * padding: what its rows hold does not matter, its results are zeros, and no cache
@@ -667,18 +668,26 @@ int skv_rope_backward(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32
  * change from run to run (a part by itself may differ in its last bits from the same
  * part with the other: the work may be cut otherwise).
  *
- * Precision.  Products take fp16 operands and add in fp32: p, ds and an fp32 d_o enter
- * them rounded to fp16 (half a step is 2^-11 of the value), scaled by powers of two
- * so that neither long rows nor small gradients leave its range.  The scale of ds
- * goes by the largest |d_o| and |v| that a key tile (for dk) or the query row (for
- * dq) meets: tokens whose gradients are more than about 2^-20 of the largest one that
- * meets the same 128 keys lose bits in dk (for fp32 d_o in dv too).  In dq, what rounding
+ * Precision.  Products take fp16 operands and add in fp32, whatever the types of d_o and
+ * of the results: p, ds and an fp32 d_o enter them rounded to fp16 (half a step is 2^-11 of the
+ * value), so fp32 results are good to about 11 bits too.  Powers of two keep long rows
+ * and small gradients in fp16's range: ds is scaled by 2^15 over the largest |d_o||v| + |delta|
+ * that the query row (for dq) or a tile of 128 keys (for dk) meets.  Terms p (d_o.v - delta)
+ * that are smaller than about 2^-29 of that lose bits, and are off by at most 2^-40 of it.  So in
+ * dk a token whose gradients are much smaller than the largest that meets the same 128 keys
+ * loses bits: below about 2^-11 of it over 16384 keys of like weight (p = 2^-14; |d_o||v| is some
+ * 2^4 above what d_o.v comes to), below 2^-25 for a key that has all the weight.  For fp32 d_o
+ * the same holds of p in dv, by the rows' largest |d_o|: below 2^-15 and 2^-29.  In dq, what rounding
  * ds takes from the part that a row's keys have in common is given back.
  * A NaN or an infinity in a row of q, d_o, k or v that is seen spreads over the
  * results of the 128 rows or keys that are computed with it.
  *
  * Limits: D 64 or 128; q, d_o, o, results 16-byte aligned, k, v and their row
- * strides too; S*nq and kv_end below 2^31 - 256. */
+ * strides too; S*nq and kv_end below 2^31 - 256; of each KV head at most 32768 tiles of
+ * query rows (tokens, of one list or of all sequences over a dense range, times the query heads
+ * that share it; a tile has up to 128 rows: 2^22 of them where they fill it); tiles of queries
+ * and of 128 keys over all KV heads and lists together below 2^31; row strides, and the queries and keys of
+ * one list of several, below 2^39 bytes; |d_lse| beside an fp16 d_o below 2^96. */
 int skv_attn_backward(skv_handle *h, const skv_shape *shape, const void *q, const void *k, const void *v,
                       const int32_t *q_pos, int64_t key_pos0, const int32_t *kv_rows, int64_t kv_rows_ld,
                       int32_t kv_rows_per_head, int64_t kv_begin, int64_t kv_end, const float *o, const float *lse,

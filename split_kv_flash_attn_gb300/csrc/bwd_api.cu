@@ -174,7 +174,7 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
     g.KT = static_cast<int>((g.n + kTile - 1) / kTile);
     choose_tiles(g);
     const int64_t units = static_cast<int64_t>(g.groups) * g.Hk;
-    if (g.QT > kMaxQTiles) return fail(h, SKV_EUNSUPPORTED, "%d query tiles of a KV head (at most %d)", g.QT, kMaxQTiles);
+    if (g.QT > kMaxQTiles) return fail(h, SKV_EUNSUPPORTED, "%d tiles of query rows of a KV head (at most %d)", g.QT, kMaxQTiles);
     if (units * (g.KT + static_cast<int64_t>(g.QT)) > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many tiles for one launch");
     if (g.groups > 1 && (2 * static_cast<int64_t>(g.H) * g.D * g.T >= int64_t(1) << 39 ||
                          2 * static_cast<int64_t>(g.Hk) * g.D * g.n >= int64_t(1) << 39))
