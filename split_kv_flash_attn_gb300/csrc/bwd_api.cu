@@ -175,7 +175,8 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
     choose_tiles(g);
     const int64_t units = static_cast<int64_t>(g.groups) * g.Hk;
     if (g.QT > kMaxQTiles) return fail(h, SKV_EUNSUPPORTED, "%d tiles of query rows of a KV head (at most %d)", g.QT, kMaxQTiles);
-    if (units * (g.KT + static_cast<int64_t>(g.QT)) > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many tiles for one launch");
+    // (units first: the product of all stays within 64 bits, and so do the sizes below, of at most 128 rows a tile)
+    if (units > INT32_MAX || units * (g.KT + static_cast<int64_t>(g.QT)) > INT32_MAX) return fail(h, SKV_EUNSUPPORTED, "too many tiles for one launch");
     if (g.groups > 1 && (2 * static_cast<int64_t>(g.H) * g.D * g.T >= int64_t(1) << 39 ||
                          2 * static_cast<int64_t>(g.Hk) * g.D * g.n >= int64_t(1) << 39))
         return fail(h, SKV_EUNSUPPORTED, "a sequence's rows exceed 2^39 bytes");

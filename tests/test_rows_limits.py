@@ -48,6 +48,10 @@ ROWS = 1 << 22
     # all tiles
     (dict(nq=128, H=65536, Hk=65536, n=32768 * 128), "too many tiles"),
     (dict(lists=1, S=1 << 12, nq=1, H=1024, Hk=1024, n=512 * 128), "too many tiles"),
+    # ... whose number passes 64 bits, and whose heads alone do 31
+    (dict(lists=1, S=1 << 30, nq=1, H=1 << 30, Hk=1 << 30, D=64, n=1024), "too many tiles"),
+    (dict(lists=1, S=1 << 29, nq=1, H=1 << 30, Hk=1 << 30, D=64, n=31 * 128), "too many tiles"),
+    (dict(lists=1, S=1 << 16, nq=1, H=1 << 16, Hk=1 << 16, n=1), "too many tiles"),
     # bytes
     (dict(k_row_bytes=1 << 39), "2^39"), (dict(v_row_bytes=1 << 39), "2^39"),
     (dict(lists=1, S=2, nq=1 << 20, H=4096, Hk=4096, n=10), "2^39"),
