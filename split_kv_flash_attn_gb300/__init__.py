@@ -684,12 +684,11 @@ def _tokens(lead):
 
 
 def _positions(name, pos, axes, lead, n, device):
-    """Pointer of positions of n tokens: int32 [axes, *lead] or [axes, n]; for one axis (axes 1, or 0: no axis of its own) also
-    without it."""
+    """Pointer of positions of n tokens: int32 [axes, *lead] or [axes, n]; for one axis also without it."""
     shape = pos.shape
-    rest = shape[1:] if axes and len(shape) and shape[0] == axes else None
+    rest = shape[1:] if len(shape) and shape[0] == axes else None
     if not (pos.dtype is _torch().int32 and pos.get_device() == device and pos.is_contiguous()
-            and (rest is not None and (rest == lead or rest == (n,)) or axes <= 1 and (shape == lead or shape == (n,)))):
+            and (rest is not None and (rest == lead or rest == (n,)) or axes == 1 and (shape == lead or shape == (n,)))):
         want = ", ".join(map(str, (axes, *lead) if axes > 1 else lead))
         raise SplitKVError(1, f"{name}: want contiguous int32 [{want}] (positions) on device {device}, got "
                               f"{'' if pos.is_contiguous() else 'non-contiguous '}{pos.dtype} {list(shape)} on {pos.device}")
@@ -766,7 +765,7 @@ def _region_rows(name, x, half, need, row_bytes, n_rows, device):
     if at >= 0 and at != device:
         raise SplitKVError(1, f"{name}: on device {at}, other tensors on {device}")
     held = x.numel() * size
-    if row_bytes < need:
+    if row_bytes < max(1, need):
         raise SplitKVError(1, f"{name}: a row stride of {row_bytes} bytes, a row has {need}")
     if x.is_contiguous():
         n = held // row_bytes or int(held >= need)            # (one row needs no padding behind it)
@@ -813,7 +812,7 @@ def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, 
     if Hv != Hk:
         raise SplitKVError(1, f"v has {Hv} heads, k {Hk}")
     wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
-    at = _positions("positions", positions, 0, lead, n, dev)
+    at = _positions("positions", positions, 1, lead, n, dev)
     if q is None:
         q_out = None
     elif q_out is None:

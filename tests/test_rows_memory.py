@@ -196,8 +196,17 @@ def test_positions_by_shape(lib):
         for s in shapes:
             for call in calls(spec, zeros(*s)):
                 assert "positions" in refused(call)
-    # cache rows: tokens as the rows have them, or in one line
-    for s in ((4, 6), (1, 24), (1, 6, 4), (24, 1), (12, 2)):
-        assert "positions" in refused(calls(one, zeros(6, 4), zeros(*s))[1])
-    calls(one, zeros(6, 4), zeros(24))[1]()
-    assert len(lib.calls) == n + 1
+    # cache rows: as positions of one axis, whatever the rotation has
+    for spec, pos in ((one, zeros(6, 4)), (three, zeros(3, 24))):
+        for s in ((4, 6), (24, 1), (12, 2), (3, 24), (3, 6, 4)):
+            assert "positions" in refused(calls(spec, pos, zeros(*s))[1])
+        for s in ((6, 4), (24,), (1, 6, 4), (1, 24)):
+            calls(spec, pos, zeros(*s))[1]()
+    assert len(lib.calls) == n + 8
+
+
+def test_rows_of_no_heads(lib):
+    """No heads of k: refused, not divided by."""
+    K = torch.zeros((10, 2, 64), dtype=F16)
+    for kw in (dict(), dict(k_row_bytes=0, v_row_bytes=0)):
+        refused(_append, lib, Hk=0, k_dst0=K, v_dst0=K, **kw)
