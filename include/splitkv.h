@@ -670,15 +670,18 @@ int skv_rope_backward(skv_handle *h, const skv_rope_spec *spec, int64_t n, int32
  *
  * Precision.  Products take fp16 operands and add in fp32, whatever the types of d_o and
  * of the results: p, ds and an fp32 d_o enter them rounded to fp16 (half a step is 2^-11 of the
- * value), so fp32 results are good to about 11 bits too.  Powers of two keep long rows
+ * value), so fp32 results are good to about 11 bits too.  Small calls, of at most 2 tiles (128
+ * query rows x 128 keys of a KV head) for each SM, take p and ds in two fp16 parts (2^-22), and so does dq up
+ * to 8 tiles for each SM or where a KV head has one tile of query rows: an error of 2^-14 at most in the
+ * 2-norm before the results' own rounding.  Powers of two keep long rows
  * and small gradients in fp16's range: ds is scaled by 2^15 over the largest |d_o||v| + |delta|
  * that the query row (for dq) or a tile of 128 keys (for dk) meets.  Terms p (d_o.v - delta)
  * that are smaller than about 2^-29 of that lose bits, and are off by at most 2^-40 of it.  So in
  * dk a token whose gradients are much smaller than the largest that meets the same 128 keys
  * loses bits: below about 2^-11 of it over 16384 keys of like weight (p = 2^-14; |d_o||v| is some
  * 2^4 above what d_o.v comes to), below 2^-25 for a key that has all the weight.  For fp32 d_o
- * the same holds of p in dv, by the rows' largest |d_o|: below 2^-15 and 2^-29.  In dq, what rounding
- * ds takes from the part that a row's keys have in common is given back.
+ * the same holds of p in dv, by the rows' largest |d_o|: below 2^-15 and 2^-29.  In dq of one part, what rounding
+ * ds takes from what a row's keys have in common is given back.
  * A NaN or an infinity in a row of q, d_o, k or v that is seen spreads over the
  * results of the 128 rows or keys that are computed with it.
  *

@@ -890,7 +890,7 @@ def attn_backward(h: Handle, q, k, v, o, lse, d_o, *, Hk, scale=None, kv_begin=0
     """skv_attn_backward: (dq, dk, dv) of attn_partial over fp16 rows, from its o, lse and their gradients d_o (fp16
     or fp32) and d_lse.  Results are fp32 unless g_dtype (or a given result) is torch.float16; need_dq=False or
     need_dkv=False leaves a part out (None).  Products take fp16 operands whatever the types: results are good to about
-    11 bits in fp32 too (the header says what small gradients beside large ones lose)."""
+    11 bits in fp32 too, of small calls to about 14 (the header says which, and what small gradients beside large ones lose)."""
     torch = _torch()
     shape, dev, f16, f32 = q.shape, q.get_device(), torch.float16, torch.float32
     if len(shape) != 4:

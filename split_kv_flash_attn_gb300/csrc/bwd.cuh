@@ -22,6 +22,9 @@
 // for dq, the largest of the rows that a key tile meets for dk.  An fp32 d_o is
 // rounded to fp16 after a division by 2^c of its row (d_o' = d_o 2^-c); c then goes
 // into p' for dv: p' = 2^(15 + c - cmax) p.
+//
+// Two parts.  Small calls hold p' and ds' as high + low, each fp16: high stands in the first half of the columns that the
+// fp32 numbers had in tensor memory, low in the other half, and its product follows high's.
 #pragma once
 
 #include "internal.h"
@@ -38,6 +41,8 @@ constexpr int kTile = 128;               // rows of a query tile, keys of a key 
 constexpr int kThreads = 640, kCompute = 512;
 constexpr int kParts = kCompute / 128;   // compute threads that share a lane of tensor memory: columns of a tile in as many parts
 constexpr int kCols = kTile / kParts;    // columns of a thread
+constexpr int kLow = kCols / 2;          // where the low parts stand among a part's columns of tensor memory
+enum { kOnePart, kTwoOfDq, kTwoParts };  // how p and ds enter their products
 constexpr int kPShift = 15;              // p' = 2^15 p
 // Tiles after which an accumulator is added to fp32 memory.  The tensor core cuts its
 // sums off instead of rounding them, and loses about 2^-24 of a sum's size for
@@ -168,6 +173,13 @@ __device__ __forceinline__ int64_t q_row(const Geo &g, const QTile &t, int r)
     return (t.group * g.T + tok) * g.H + static_cast<int64_t>(t.hk) * g.G + gg;
 }
 
+// What two numbers in fp16 leave of them, in fp16.
+__device__ __forceinline__ uint32_t low_part(uint32_t high, float a, float b)
+{
+    const __half2 h2 = *reinterpret_cast<const __half2 *>(&high);
+    return pack_half2(-sub_h(__low2half(h2), a), -sub_h(__high2half(h2), b));
+}
+
 // Part of a row of results: NC values at `at`, as g_type.
 template <int NC>
 __device__ __forceinline__ void store_row(void *base, int64_t at, int g_type, const float (&v)[NC])
@@ -220,7 +232,7 @@ int launch_join(skv_handle *h, const float *slot, int pieces, int64_t n, int out
                 cudaStream_t st);
 // One launch of both: kv_args.out0 or q_args.out0 NULL leaves a part out.
 int launch_main(skv_handle *h, const CUtensorMap &mq, const CUtensorMap &mo, const CUtensorMap &mk, const CUtensorMap &mv,
-                const MainArgs &kv_args, const MainArgs &q_args, bool q_first, cudaStream_t st);
+                const MainArgs &kv_args, const MainArgs &q_args, bool q_first, int parts, cudaStream_t st);
 
 }  // namespace bwd
 }  // namespace skv

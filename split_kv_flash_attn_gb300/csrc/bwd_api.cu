@@ -15,6 +15,8 @@ static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 // Costs in tiles of 128 x 128 of dq (1.1 us): a tile of dk and dv, a CTA's fixed part (tensor memory,
 // barriers, row statistics, pipeline fill, result), the launch that adds up pieces.
 constexpr double kKvTile = 1.5, kFixed = 6, kJoin = 2.5;
+// Tiles of an SM up to which p and ds, or dq's ds alone, come in two fp16 parts.
+constexpr double kTwoTiles = 2, kTwoDqTiles = 8;
 // fp32 bytes that the adding up moves in a tile's time.
 constexpr double kJoinBytes = 9e6;
 
@@ -58,6 +60,20 @@ static Plan plan_of(const Geo &g, int64_t units, int sms, bool kv, bool q, doubl
         }
     }
     return best;
+}
+
+// p and ds as one fp16 number leave results an error like that of their own rounding to fp16: 3.0e-4 in the 2-norm where
+// that is 2.1e-4.  Over few rows or keys single roundings show: over 3.1e-4 in 3 % of 2086 shapes of up to 2e11 pairs x channels,
+// 4.1e-4 at most.  Two parts leave 2.1e-4.  Where an SM has few tiles, the CTAs' fixed parts hide what they cost:
+//   all in two: 26.6 us both ways (64 rows over 256 keys), 30.7 -> 34.8 (0.6 tiles an SM), 45 -> 47 (1.7); beyond, 50 -> 55 (3.4),
+//   67.6 -> 73.7 (6.7).  dq's ds in two: 49.2 -> 47.5 (2.5), 67.6 -> 64.5 (6.7), beyond 88 -> 98 (13.5), 166 -> 174 (27).
+// Where a KV head has one query tile, dq has few rows to even roundings out whatever the keys, and CTAs of dk and dv with
+// one tile each take the time: 398 -> 391 us (one token over 65536 keys).
+static int parts_of(const Geo &g, int64_t units, int sms)
+{
+    const double tiles = static_cast<double>(units) * g.QT * g.KT;
+    if (tiles <= kTwoTiles * sms) return kTwoParts;
+    return tiles <= kTwoDqTiles * sms || g.QT == 1 ? kTwoOfDq : kOnePart;
 }
 
 // Tokens x heads of a query tile: the fewest tiles, then the fewest heads (a tile of
@@ -191,6 +207,7 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
     const double nq = static_cast<double>(shape->nq), keys = static_cast<double>(g.n);
     const double share = !q_pos ? 1.0 : nq <= keys ? 1.0 - 0.5 * nq / keys : 0.5 * keys / nq;
     const Plan plan = plan_of(g, units, h->sm_count, dk != nullptr, dq != nullptr, share);
+    const int parts = parts_of(g, units, h->sm_count);
     const int kv_pieces = plan.kv_pieces, q_pieces = plan.q_pieces;
     const bool kv_slot = dk && (kv_pieces > 1 || g.QT > kStretch), q_slot = dq && (q_pieces > 1 || g.KT > kStretch);
 
@@ -260,7 +277,7 @@ extern "C" int skv_attn_backward(skv_handle *h, const skv_shape *shape, const vo
     b.pieces = q_pieces;
     b.slot = q_slot ? reinterpret_cast<float *>(ws + at_q) : nullptr;
     b.out0 = dq;
-    if ((rc = launch_main(h, mq, mo, mk, mv, a, b, plan.q_first, st))) return rc;
+    if ((rc = launch_main(h, mq, mo, mk, mv, a, b, plan.q_first, parts, st))) return rc;
     if (kv_pieces > 1 && (rc = launch_join(h, a.slot, kv_pieces, k_vals, 2, g_type, dk, dv, st))) return rc;
     if (q_pieces > 1 && (rc = launch_join(h, b.slot, q_pieces, q_vals, 1, g_type, dq, nullptr, st))) return rc;
     return SKV_OK;

@@ -62,7 +62,8 @@ static_assert(B_COUNT * 8 <= 256, "barrier area");
 // Tensor memory columns.
 constexpr int kColS = 0, kColP = 128, kColV = 256;
 
-template <int D>
+// TWO: p and ds in two fp16 parts each (bwd.cuh).
+template <int D, bool TWO>
 __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to, const CUtensorMap &tk, const CUtensorMap &tv,
                                     const MainArgs &a, int unit, int piece, uint8_t *smem_raw)
 {
@@ -313,6 +314,12 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         tc::mma_f16_ts_if(one, acc, col + (kk & 1) * 8 + (kk >> 1) * kCols, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
                                        kIdescV, (i > 0 || kk > 0) ? 1u : 0u);
+                    if constexpr (TWO) {
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            tc::mma_f16_ts_if(one, acc, col + kLow + (kk & 1) * 8 + (kk >> 1) * kCols, tc::desc_add(dn, st * L::kTileBytes + kk * 2048),
+                                           kIdescV, 1u);
+                    }
                     tc::mma_commit_if(one, bar((second ? B_QEMPTY : B_OEMPTY) + st));
                     if (i + 1 < nt) ok = scores(it + 1, true);
                     else if (!second && one) tc::mbar_arrive(bar(b_other));
@@ -422,6 +429,11 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
 #pragma unroll
                         for (int c = 0; c < 2 * G8; ++c) ph[c] = pack_half2(p[4 * G8 * u + 2 * c], p[4 * G8 * u + 2 * c + 1]);
                         tc::tmem_st16x16(ts + (static_cast<uint32_t>(16 * u) << 16), ph);
+                        if constexpr (TWO) {
+#pragma unroll
+                            for (int c = 0; c < 2 * G8; ++c) ph[c] = low_part(ph[c], p[4 * G8 * u + 2 * c], p[4 * G8 * u + 2 * c + 1]);
+                            tc::tmem_st16x16(ts + kLow + (static_cast<uint32_t>(16 * u) << 16), ph);
+                        }
                     }
                 }
                 tc::tmem_wait_st();
@@ -440,14 +452,16 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 tc::tmem_wait_ld16(r[1]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    uint32_t dh[2 * G8];
+                    uint32_t dh[2 * G8], dl[2 * G8];
 #pragma unroll
                     for (int c = 0; c < 2 * G8; ++c) {       // group c / 2, key + 8 (c % 2)
                         float2 x = __ffma2_rn(make_float2(__uint_as_float(r[u][2 * c]), __uint_as_float(r[u][2 * c + 1])), sg, d2[c >> 1]);
                         x = __fmul2_rn(x, make_float2(p[4 * G8 * u + 2 * c], p[4 * G8 * u + 2 * c + 1]));
                         dh[c] = pack_half2(x.x, x.y);
+                        if (TWO) dl[c] = low_part(dh[c], x.x, x.y);
                     }
                     tc::tmem_st16x16(tp + (static_cast<uint32_t>(16 * u) << 16), dh);
+                    if constexpr (TWO) tc::tmem_st16x16(tp + kLow + (static_cast<uint32_t>(16 * u) << 16), dl);
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();

@@ -53,7 +53,8 @@ static_assert(B_COUNT * 8 <= 256, "barrier area");
 
 constexpr int kColS = 0, kColP = 128, kColQ = 384;
 
-template <int D>
+// TWO: ds in two fp16 parts (bwd.cuh); nothing is given back then.
+template <int D, bool TWO>
 __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to, const CUtensorMap &tk, const CUtensorMap &tv,
                                     const MainArgs &a, int unit, int piece, uint8_t *smem_raw)
 {
@@ -268,6 +269,12 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         tc::mma_f16_ts_if(one, tmem + kColQ, tmem + kColP + sb * kTile + (kk & 1) * 8 + (kk >> 1) * kCols,
                                        tc::desc_add(dk0, ks * L::kTileBytes + kk * 2048), kIdescQ, (i > 0 || kk > 0) ? 1u : 0u);
+                    if constexpr (TWO) {
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            tc::mma_f16_ts_if(one, tmem + kColQ, tmem + kColP + sb * kTile + kLow + (kk & 1) * 8 + (kk >> 1) * kCols,
+                                           tc::desc_add(dk0, ks * L::kTileBytes + kk * 2048), kIdescQ, 1u);
+                    }
                     tc::mma_commit_if(one, bar(B_KEMPTY + ks));
                     tc::mma_commit_if(one, bar(B_DQ + sb));
                     if (i + 1 == nt) tc::mma_commit_if(one, bar(B_ACC));
@@ -305,7 +312,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
             const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             const float c1 = a.scale * 1.4426950408889634f;
             auto compute_sync = [&]() { asm volatile("bar.sync 5, %0;\n" ::"n"(kCompute) : "memory"); };
-            if (stretch == 0) {
+            if (!TWO && stretch == 0) {
                 // the mean of the first tile's keys: the first 256 threads add up two channels of 32 or 16 rows,
                 // the upper half of them leaves its sums, the lower one adds its own
                 constexpr int PAIRS = D / 2, ROWS = kTile / (256 / PAIRS);
@@ -383,23 +390,33 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
 #pragma unroll
                 for (int c = 0; c < kCols / 2; ++c) dh[c] = pack_half2(p[2 * c], p[2 * c + 1]);
                 tc::tmem_st16u(cp, dh);
+                if constexpr (TWO) {
+                    uint32_t dl[kCols / 2];
+#pragma unroll
+                    for (int c = 0; c < kCols / 2; ++c) dl[c] = low_part(dh[c], p[2 * c], p[2 * c + 1]);
+                    tc::tmem_st16u(cp + kLow, dl);
+                }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 tc::mbar_arrive(bar(B_DS + sb));
                 // (while the products run)
+                if constexpr (!TWO) {
 #pragma unroll
-                for (int c = 0; c < kCols / 2; ++c) {
-                    const __half2 h2 = *reinterpret_cast<const __half2 *>(&dh[c]);
-                    eps2 = __fadd2_rn(eps2, make_float2(sub_h(__low2half(h2), p[2 * c]), sub_h(__high2half(h2), p[2 * c + 1])));
+                    for (int c = 0; c < kCols / 2; ++c) {
+                        const __half2 h2 = *reinterpret_cast<const __half2 *>(&dh[c]);
+                        eps2 = __fadd2_rn(eps2, make_float2(sub_h(__low2half(h2), p[2 * c]), sub_h(__high2half(h2), p[2 * c + 1])));
+                    }
                 }
             }
             // ---------------- the sum of this stretch ----------------------------
             float eps = eps2.x + eps2.y;
-            if (part >= 2) s_sum[part - 2][m] = eps;
-            compute_sync();
-            if (part < 2) s_sum[part][m] += eps;
-            compute_sync();
-            eps = -(s_sum[0][m] + s_sum[1][m]);
+            if constexpr (!TWO) {
+                if (part >= 2) s_sum[part - 2][m] = eps;
+                compute_sync();
+                if (part < 2) s_sum[part][m] += eps;
+                compute_sync();
+                eps = -(s_sum[0][m] + s_sum[1][m]);
+            }
             bool ok = !*reinterpret_cast<volatile int *>(&s_abort);
             ok = ok && wait(B_ACC, stretch & 1);
             ok = __all_sync(0xffffffffu, ok);
@@ -409,7 +426,7 @@ __device__ __forceinline__ void run(const CUtensorMap &tq, const CUtensorMap &to
                 float v[NC];
                 load_cols<NC>(lane_base + kColQ + part * NC, v);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) v[c] = lim > 0 ? f(fmaf(eps, s_mean[part * NC + c], v[c])) : 0.f;
+                for (int c = 0; c < NC; ++c) v[c] = lim > 0 ? f(TWO ? v[c] : fmaf(eps, s_mean[part * NC + c], v[c])) : 0.f;
                 const int64_t row = q_row(g, t, m);
                 if (row >= 0) {
                     if (stretch > 0) add_row<NC>(slot_of(row), v);

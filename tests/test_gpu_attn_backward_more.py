@@ -137,3 +137,50 @@ def test_what_rounding_takes_from_common_keys_is_given_back(skv, h, D, common, n
     row = torch.linalg.vector_norm(ds, dim=1, keepdim=True) * rms * scale
     assert float((got - want).norm()) <= 4 * 2.0 ** -11 * float(row.norm())
     assert float((plain - want).norm()) > 4 * 2.0 ** -11 * float(row.norm())
+
+
+PARTS = [
+    # S, nq, n, H, Hk, D, causal, lists; what has two parts
+    (1, 64, 256, 4, 1, 64, True, False, "all"),
+    (1, 4, 21, 8, 2, 64, False, False, "all"),
+    (1, 30, 1126, 8, 8, 128, True, False, "all"),
+    (1, 300, 300, 4, 2, 128, True, False, "all"),
+    (3, 70, 150, 6, 2, 128, True, True, "all"),
+    (2, 500, 60, 5, 1, 64, False, True, "all"),
+    (1, 1, 1, 4, 4, 128, False, False, "all"),
+    (1, 512, 2048, 8, 2, 128, True, False, "dq"),         # 512 tiles
+    (3, 200, 520, 16, 4, 64, False, True, "dq"),          # 420 of lists
+    (1, 3, 30000, 8, 8, 128, True, False, "dq"),          # 1880 tiles, one of query rows for each KV head
+    (1, 16, 21000, 64, 8, 64, False, False, "dq"),        # 128 rows of it
+]
+
+
+@pytest.mark.parametrize("S,nq,n,H,Hk,D,causal,lists,parts", PARTS)
+def test_small_calls_hold_more_bits(skv, h, S, nq, n, H, Hk, D, causal, lists, parts):
+    """p and ds of two fp16 parts leave their fp32 errors: of p at most 2^-15 (scores' sums of 16 magnitudes 2^-23, 8 steps;
+    exponents below 64, 2^-22), of d_o.v - delta 2^-19 of some 10 times its size, in sums whose terms and errors are of
+    random sign: 2^-14 of a result's 2-norm (one part would leave 2^-12)."""
+    import torch
+    from tests.grad_util import attention_backward, attention_forward, check
+    g = _gen(n + nq)
+    q = torch.randn((S, nq, H, D), device="cuda", generator=g).half()
+    r = S * n if lists else n
+    k = (torch.randn((r, Hk, D), device="cuda", generator=g) + 0.5 * torch.randn((1, Hk, D), device="cuda", generator=g)).half()
+    v = torch.randn((r, Hk, D), device="cuda", generator=g).half()
+    d_o = (torch.randn((S, nq, H, D), device="cuda", generator=g) * 0.1).half()
+    rows = torch.arange(r, device="cuda", dtype=torch.int32).view(S, n) if lists else None
+    pos = (n - nq + torch.arange(nq, device="cuda")).repeat(S, 1).to(torch.int32) if causal else None
+    B, T = (S, nq) if lists else (1, S * nq)
+    see = torch.ones((B, T, n), dtype=torch.bool, device="cuda")
+    if causal:
+        see = torch.arange(n, device="cuda").view(1, 1, n) <= pos.view(B, T, 1)
+    q1, d1, k1, v1 = q.view(B, T, H, D), d_o.view(B, T, H, D), k.view(B, n, Hk, D), v.view(B, n, Hk, D)
+    o, lse = attention_forward(q1, k1, v1, see, D ** -0.5)
+    want, bound = attention_backward(q1, k1, v1, see, D ** -0.5, o, lse, d1)
+    got = skv.attn_backward(h, q, k, v, o.view(S, nq, H, D), lse.view(S, nq, H), d_o, Hk=Hk, q_pos=pos, kv_rows=rows)
+    assert h.status() == 0
+    for name, x, w, b in zip(("dq", "dk", "dv"), got, want, bound):
+        w, b = w.reshape(x.shape), b.reshape(x.shape)
+        check(x, w, b, name)
+        if (parts == "all" or name == "dq") and (n > 1 or name == "dv"):      # (one key: dq and dk are 0 but for delta's rounding)
+            assert float((x.double() - w).norm()) <= 2.0 ** -14 * float(w.norm()), name
