@@ -8,8 +8,10 @@
 // them) and of CTAs for dq (each owns a query tile and walks over its keys).  S and d_o.v are
 // computed in both: 7 products instead of 5, but no sum of dq crosses CTAs.
 // Adding it up in memory instead would move 4 bytes for every key tile, query row and
-// channel, 64 KB for each 128 x 128 tile that takes about 1.3 us: 7.5 TB/s of
-// reductions over 152 SMs, and in an order that changes from run to run.
+// channel: 64 KB for each 128 x 128 tile.  A tile of dk and dv takes 1.64 us for its four products; at that
+// rate five take about 2 us, and 152 SMs then add up 4.9 TB/s, half of that if two CTAs shared a
+// tile of dq.  Not built or timed: whether it would be faster than 7 products is open.  Its sums
+// would change from run to run unless CTAs took turns on a tile.
 //
 // A query tile is Tb tokens x Gb heads of a KV head's group, Tb * Gb <= 128 rows
 // (row = token * Gb + head), chosen for the fewest tiles.

@@ -13,7 +13,9 @@ static bool misaligned(const void *p, size_t n) { return reinterpret_cast<uintpt
 static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Costs in tiles of 128 x 128 of dq (1.1 us): a tile of dk and dv, a CTA's fixed part (tensor memory,
-// barriers, row statistics, pipeline fill, result), the launch that adds up pieces.
+// barriers, row statistics, pipeline fill, result), the launch that adds up pieces.  Measured with D = 128 and used for
+// D = 64 too, whose products are half as long but whose CTAs take nearly as much time (996 and 1230 us for 16384 causal
+// tokens, 8 heads on 2): pieces were not timed there.
 constexpr double kKvTile = 1.5, kFixed = 6, kJoin = 2.5;
 // Tiles of an SM up to which p and ds, or dq's ds alone, come in two fp16 parts.
 constexpr double kTwoTiles = 2, kTwoDqTiles = 8;
@@ -30,7 +32,7 @@ constexpr double kJoinBytes = 9e6;
 //   512 tokens over 32768 keys: dq's 128 CTAs of 256 tiles first, dk and dv's 2048 of 16 after them 749 us,
 //   the other way round 769.  128 tokens over 4096 keys: none 57, dq in two 63.
 // Of 32 shapes (1 to 16384 tokens) the plan took the best pieces or came within 6 % of them, but for 16384 tokens
-// that all see 16384 keys, 8 heads on 2: none 2913, dk and dv in six 2548.  There dq's CTAs, beside a second
+// that all see 16384 keys, 8 heads on 2: none 2850 to 2913, dk and dv in six 2548.  There dq's CTAs, beside a second
 // wave of dk's and dv's long ones, slow these down by half; why was not found.
 struct Plan {
     int kv_pieces, q_pieces;

@@ -23,7 +23,7 @@
 // and shuffles bring it those of its values.
 //
 // Bound by latency and instructions rather than by memory: sixteen warps an SM, a batch's chain of
-// sums and a root in each.  8192 tokens of 32 + 8 heads of 128, fp16, normed (168 MB): 30.4 us, 5.5 TB/s;
+// sums and a root in each.  8192 tokens of 32 + 8 heads of 128, fp16, normed (168 MB): 30.0 us, 5.6 TB/s;
 // a pass of a batch's rows after the other 32, all four passes side by side (spilled) 31.6; then also batches
 // of half the size 36, three CTAs an SM (80 registers, spilled) 36, the ring of the
 // gradients 35, a row's values consecutive in a lane and partners by shuffles 75.  Its gradients
