@@ -683,12 +683,11 @@ def _tokens(lead):
     return n
 
 
-def _positions(name, pos, axes, lead, n, device):
+def _positions(torch, name, pos, axes, lead, n, device):
     """Pointer of positions of n tokens: int32 [axes, *lead] or [axes, n]; for one axis also without it."""
     shape = pos.shape
-    rest = shape[1:] if len(shape) and shape[0] == axes else None
-    if not (pos.dtype is _torch().int32 and pos.get_device() == device and pos.is_contiguous()
-            and (rest is not None and (rest == lead or rest == (n,)) or axes == 1 and (shape == lead or shape == (n,)))):
+    if not ((shape == (axes, n) or axes == 1 and (shape == lead or shape == (n,)) or shape == (axes, *lead))
+            and pos.dtype is torch.int32 and pos.get_device() == device and pos.is_contiguous()):
         want = ", ".join(map(str, (axes, *lead) if axes > 1 else lead))
         raise SplitKVError(1, f"{name}: want contiguous int32 [{want}] (positions) on device {device}, got "
                               f"{'' if pos.is_contiguous() else 'non-contiguous '}{pos.dtype} {list(shape)} on {pos.device}")
@@ -721,7 +720,7 @@ def _rope_inputs(torch, h, spec, q, k, pos, stream):
     H, qs = _token_rows("q", q, lead, D, dtype, dev) if q is not None else (0, 0)
     Hk, ks = _token_rows("k", k, lead, D, dtype, dev) if k is not None else (0, 0)
     n = lead[0] if len(lead) == 1 else _tokens(lead)
-    return st, lead, n, H, qs, Hk, ks, xt, _positions("pos", pos, spec.n_axes, lead, n, dev)
+    return st, lead, n, H, qs, Hk, ks, xt, _positions(torch, "pos", pos, spec.n_axes, lead, n, dev)
 
 
 def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dtype=None, q_out=None, k_out=None,
@@ -755,45 +754,45 @@ def rope(h: Handle, spec: Rope, q, k, pos, *, q_weight=None, k_weight=None, o_dt
     return q_out, k_out
 
 
-def _region_rows(name, x, half, need, row_bytes, n_rows, device):
+def _region_rows(torch, name, x, half, need, row_bytes, n_rows, device):
     """Rows of `need` bytes, row_bytes apart, that a cache region's tensor holds (or n_rows of them): contiguous memory, or
     rows with that pitch (a part of a packed cache, say).  half: fp16 rows."""
-    dtype, size = x.dtype, x.element_size()
-    if dtype.is_floating_point and not (half and size == 2 and dtype is _torch().float16):
+    dtype = x.dtype
+    if dtype is not torch.uint8 and dtype.is_floating_point and not (half and dtype is torch.float16):
         raise SplitKVError(1, f"{name}: want {'fp16 or ' if half else ''}bytes, got {dtype}")
     at = x.get_device()
-    if at >= 0 and at != device:
+    if at != device and at >= 0:
         raise SplitKVError(1, f"{name}: on device {at}, other tensors on {device}")
-    held = x.numel() * size
-    if row_bytes < max(1, need):
+    if row_bytes < need or row_bytes < 1:
         raise SplitKVError(1, f"{name}: a row stride of {row_bytes} bytes, a row has {need}")
     if x.is_contiguous():
+        held = x.nbytes
         n = held // row_bytes or int(held >= need)            # (one row needs no padding behind it)
     else:
-        row = x[0]
+        row, size = x[0], x.element_size()
         if x.stride(0) * size != row_bytes or not row.is_contiguous() or row.numel() * size < need:
             raise SplitKVError(1, f"{name}: {list(x.shape)} of strides {list(x.stride())} is not contiguous and holds no rows "
                                   f"{row_bytes} bytes apart (rows of another pitch want their row bytes)")
         n = x.shape[0]
     if n_rows is None:
         return n
-    if n_rows > n and (n_rows - 1) * row_bytes + need > x.untyped_storage().nbytes() - size * x.storage_offset():
+    if n_rows > n and (n_rows - 1) * row_bytes + need > x.untyped_storage().nbytes() - x.element_size() * x.storage_offset():
         raise SplitKVError(1, f"{name}: {n_rows} rows lie beyond its memory at {row_bytes} bytes a row")
     return n_rows
 
 
-def _cache_dst(name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes, device):
+def _cache_dst(torch, name, type_, Hk, D, dst0, dst1, n_rows0, n_rows1, row_bytes, device):
     if type_ not in (F16, Q8_0, Q4_0):
         raise SplitKVError(1, f"{name}_type: unknown element type {type_}")
-    need = Hk * segment_bytes(type_, D)
+    half, p0, p1 = type_ == F16, None, None
+    need = Hk * 2 * D if half else Hk * segment_bytes(type_, D)
     if row_bytes is None:
         row_bytes = need
     if dst0 is not None:
-        n_rows0 = _region_rows(name + "_dst0", dst0, type_ == F16, need, row_bytes, n_rows0, device)
+        n_rows0, p0 = _region_rows(torch, name + "_dst0", dst0, half, need, row_bytes, n_rows0, device), dst0.data_ptr()
     if dst1 is not None:
-        n_rows1 = _region_rows(name + "_dst1", dst1, type_ == F16, need, row_bytes, n_rows1, device)
-    return SkvCacheDst(type_, row_bytes, None if dst0 is None else dst0.data_ptr(), n_rows0 or 0,
-                       None if dst1 is None else dst1.data_ptr(), n_rows1 or 0)
+        n_rows1, p1 = _region_rows(torch, name + "_dst1", dst1, half, need, row_bytes, n_rows1, device), dst1.data_ptr()
+    return SkvCacheDst(type_, row_bytes, p0, n_rows0 or 0, p1, n_rows1 or 0)
 
 
 def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, k_dst1=None, v_dst1=None, *,
@@ -812,15 +811,15 @@ def rope_append(h: Handle, spec: Rope, q, k, v, pos, positions, k_dst0, v_dst0, 
     if Hv != Hk:
         raise SplitKVError(1, f"v has {Hv} heads, k {Hk}")
     wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
-    at = _positions("positions", positions, 1, lead, n, dev)
+    at = _positions(torch, "positions", positions, 1, lead, n, dev)
     if q is None:
         q_out = None
     elif q_out is None:
         q_out = _new(torch, (*lead, H, D), torch.float16, q, stream, dev)
     else:
         _need("q_out", q_out, torch.float16, (*lead, H, D), dev)
-    kd = _cache_dst("k", k_type, Hk, D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes, dev)
-    vd = _cache_dst("v", v_type, Hk, D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes, dev)
+    kd = _cache_dst(torch, "k", k_type, Hk, D, k_dst0, k_dst1, n_rows0, n_rows1, k_row_bytes, dev)
+    vd = _cache_dst(torch, "v", v_type, Hk, D, v_dst0, v_dst1, n_rows0, n_rows1, v_row_bytes, dev)
     rc = _lib.lib().skv_rope_append(h._h, spec._ref, n, H, Hk, xt, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                                     wq, wk, pp, at, _ptr(q_out), ctypes.byref(kd), ctypes.byref(vd), st)
     if rc:
@@ -842,7 +841,7 @@ def rope_backward(h: Handle, spec: Rope, dq_out, dk_out, pos, *, q=None, k=None,
     g_dtype = some.dtype
     gt = _row_type("dq_out" if some is dq_out else "dk_out", g_dtype)
     n = lead[0] if len(lead) == 1 else _tokens(lead)
-    pp = _positions("pos", pos, spec.n_axes, lead, n, dev)
+    pp = _positions(torch, "pos", pos, spec.n_axes, lead, n, dev)
     wq, wk = _weight(torch, "q_weight", q_weight, spec), _weight(torch, "k_weight", k_weight, spec)
     if x_dtype is None:
         x_dtype = next((x.dtype for x in (q, k, dq, dk) if x is not None), g_dtype)
